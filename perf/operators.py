@@ -130,7 +130,7 @@ def prepare(case, seed):
         s["z" if case["kind"] == "norms_bwd" else "x"] = _randn(g, T, C, dtype=r, std=2.0)
         s["w_post"] = 1.0 + _randn(g, C, std=0.2)
         s["w_pre"] = 1.0 + _randn(g, C, std=0.2)
-        s["g"] = {"none": lambda: None, "channel": lambda: _randn(g, C), "token": lambda: _randn(g, T),
+        s["g"] = {"none": lambda: None, "channel": lambda: _randn(g, C), "token": lambda: _randn(g, T, 1),
                   "full": lambda: _randn(g, T, C, dtype=t)}[case["gate"]]()
         s["alpha"], s["beta"] = 1.0, 0.5
         if case["kind"] == "norms_bwd":
@@ -266,9 +266,7 @@ def _rstd(x):
 
 
 def _gate(s):
-    if s["g"] is None:
-        return 1.0
-    return s["g"].float()[:, None] if s["gate"] == "token" else s["g"].float()
+    return 1.0 if s["g"] is None else s["g"].float()
 
 
 def _norms(s):
@@ -293,7 +291,7 @@ def _norms_bwd(s):
     out = {"dy": dy.to(s["y"].dtype), "dres": (s["alpha"] * d).to(s["z"].dtype), "dw_post": dw_post}
     if s["gate"] != "none":
         dg = s["beta"] * d * p
-        out["dgate"] = (dg.sum(dim=0) if s["gate"] == "channel" else dg.sum(dim=1) if s["gate"] == "token"
+        out["dgate"] = (dg.sum(dim=0) if s["gate"] == "channel" else dg.sum(dim=1, keepdim=True) if s["gate"] == "token"
                         else dg.to(s["y"].dtype))
     out["dw_pre"] = dw_pre
     return out
@@ -369,7 +367,7 @@ def _exact_expert(s, e, rows):
 def _exact_join(s, y, x, w_post, gate, w_pre):
     p = y * torch.rsqrt(y.square().mean(1, keepdim=True) + EPS) * w_post
     if gate is not None:
-        p = p * (gate[:, None] if s["gate"] == "token" else gate)
+        p = p * gate
     z = s["alpha"] * x + s["beta"] * p
     return z, z * torch.rsqrt(z.square().mean(1, keepdim=True) + EPS) * w_pre
 
