@@ -16,12 +16,14 @@ import torch  # noqa: F401,E402
 _HERE = os.path.dirname(os.path.abspath(__file__))
 lib_path = os.path.join(_HERE, "libfp8z1.so")
 
-F32, BF16, E4M3 = 0, 1, 2
+F32, BF16, E4M3, F16 = 0, 1, 2, 3
 SCALE_AMAX, SCALE_POW2 = 0, 1
 SPLIT_BLOCK, SPLIT_PARAM = 0, 1
 STAT_PARTS = 4  # float64 partial sums of squares per slot
 NOALLOC_MAX_SLOTS = 262144  # largest table fp8z1_step_rowmajor_noalloc takes
 ALL_RANKS = -1
+ACT_SILU, ACT_GELU = 0, 1
+GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL = 0, 1, 2, 3
 
 BLOCK_ENTRY_DTYPE = np.dtype([
     ("param", "<i4"), ("expert", "<i4"), ("brow", "<u2"), ("bcol", "<u2"),
@@ -83,7 +85,21 @@ class State(C.Structure):
         return {f: getattr(self, f) for f, _ in self._fields_}
 
 
+class Ffn(C.Structure):
+    """The feed-forward block's sizes: T rows, E experts, widths D (x, y) and F (h, u, a)."""
+    _fields_ = [("T", C.c_int64), ("E", C.c_int64), ("D", C.c_int64), ("F", C.c_int64), ("dtype", C.c_int32),
+                ("act", C.c_int32)]
+
+
+class Norm(C.Structure):
+    """The norm join's sizes and settings."""
+    _fields_ = [("T", C.c_int64), ("C", C.c_int64), ("dtype", C.c_int32), ("res_dtype", C.c_int32),
+                ("gate", C.c_int32), ("eps", C.c_float), ("res_scale", C.c_float), ("block_scale", C.c_float),
+                ("weight_offset", C.c_float), ("reserved", C.c_int32)]
+
+
 assert C.sizeof(Block) == 16 and C.sizeof(State) == 64 and C.sizeof(Hparams) == 72
+assert C.sizeof(Ffn) == 40 and C.sizeof(Norm) == 48
 
 _vp = C.c_void_p
 _sig = {
@@ -108,6 +124,16 @@ _sig = {
     "fp8z1_state_write": (C.c_int, [_vp, C.POINTER(State), _vp]),
     "fp8z1_encode_e4m3": (C.c_int, [_vp, _vp, C.c_int64, _vp]),
     "fp8z1_dequantize": (C.c_int, [_vp, _vp, C.c_int64, C.c_int64, C.c_int64, C.c_int32, _vp, _vp]),
+    "fp8z1_ffn_up": (C.c_int, [C.POINTER(Ffn), *[_vp] * 10]),
+    "fp8z1_ffn_down": (C.c_int, [C.POINTER(Ffn), *[_vp] * 6]),
+    "fp8z1_ffn_down_bwd": (C.c_int, [C.POINTER(Ffn), *[_vp] * 10]),
+    "fp8z1_ffn_up_bwd": (C.c_int, [C.POINTER(Ffn), *[_vp] * 9]),
+    "fp8z1_ffn_wgrad_workspace_bytes": (C.c_int, [*[C.c_int64] * 4, C.POINTER(C.c_size_t)]),
+    "fp8z1_ffn_wgrad": (C.c_int, [*[C.c_int64] * 4, C.c_int32, _vp, _vp, _vp, C.c_int32, _vp, C.c_int32, _vp,
+                                  C.c_size_t, _vp]),
+    "fp8z1_norm_join": (C.c_int, [C.POINTER(Norm), *[_vp] * 8]),
+    "fp8z1_norm_join_bwd_workspace_bytes": (C.c_int, [C.POINTER(Norm), C.POINTER(C.c_size_t)]),
+    "fp8z1_norm_join_bwd": (C.c_int, [C.POINTER(Norm), *[_vp] * 13, C.c_size_t, _vp]),
     "fp8z1_probe_copy": (C.c_int, [_vp, _vp, C.c_int64, C.c_int64, _vp]),
     "fp8z1_probe_update_pattern": (C.c_int, [_vp, _vp, _vp, _vp, _vp, C.c_int64, C.c_int32, _vp]),
 }
@@ -224,7 +250,7 @@ def _held_params(table: Table):
 
 def _torch_dtype(code: int):
     import torch
-    return {F32: torch.float32, BF16: torch.bfloat16, E4M3: torch.uint8}[code]
+    return {F32: torch.float32, BF16: torch.bfloat16, E4M3: torch.uint8, F16: torch.float16}[code]
 
 
 def _check_param_list(table: Table, xs: Sequence, dtype: int, what: str, scales: bool = False) -> None:
@@ -364,6 +390,132 @@ def fp8z1_dequantize(codes, scales, shape, out_dtype: int, out, stream=None) -> 
           torch.float32 if out_dtype == F32 else torch.bfloat16)
     _check(lib.fp8z1_dequantize(_ptr(codes), _ptr(scales), e, r, c, out_dtype, _ptr(out), _stream(stream)),
            "fp8z1_dequantize")
+
+
+# ------------------------------------------------------------------ feed-forward block and norms
+
+def _need_rows(f: Ffn, what: str, **rows) -> None:
+    """Every given tensor holds T rows of its width, in the block's activation type."""
+    dt = _torch_dtype(f.dtype)
+    for name, (x, width) in rows.items():
+        if x is not None:
+            _need(x, f.T * width * 2, f"{what} {name}", dt)
+
+
+def _need_weights(f: Ffn, what: str, rows: int, cols: int, *weights) -> None:
+    for codes, scales in weights:
+        _need(codes, f.E * rows * cols, f"{what} codes", torch.uint8)
+        _need(scales, f.E * (-(-rows // 128)) * (-(-cols // 128)) * 4, f"{what} scales", torch.float32)
+
+
+def _need_offsets(offsets, n: int, what: str) -> None:
+    if offsets is not None:
+        _need(offsets, 4 * (n + 1), f"{what} offsets", torch.int32)
+
+
+def fp8z1_ffn_up(f: Ffn, x, gate_codes, gate_scales, up_codes, up_scales, offsets, h, u, a, stream=None) -> None:
+    """a = act(x Wg^T) * (x Wu^T); h and u keep the projections (both or neither None)."""
+    _need_rows(f, "ffn_up", x=(x, f.D), h=(h, f.F), u=(u, f.F), a=(a, f.F))
+    _need_weights(f, "ffn_up", f.F, f.D, (gate_codes, gate_scales), (up_codes, up_scales))
+    _need_offsets(offsets, f.E, "ffn_up")
+    _check(lib.fp8z1_ffn_up(C.byref(f), _ptr(x), _ptr(gate_codes), _ptr(gate_scales), _ptr(up_codes), _ptr(up_scales),
+                            _ptr(offsets), _ptr(h), _ptr(u), _ptr(a), _stream(stream)), "fp8z1_ffn_up")
+
+
+def fp8z1_ffn_down(f: Ffn, a, down_codes, down_scales, offsets, y, stream=None) -> None:
+    """y = a Wd^T."""
+    _need_rows(f, "ffn_down", a=(a, f.F), y=(y, f.D))
+    _need_weights(f, "ffn_down", f.D, f.F, (down_codes, down_scales))
+    _need_offsets(offsets, f.E, "ffn_down")
+    _check(lib.fp8z1_ffn_down(C.byref(f), _ptr(a), _ptr(down_codes), _ptr(down_scales), _ptr(offsets), _ptr(y),
+                              _stream(stream)), "fp8z1_ffn_down")
+
+
+def fp8z1_ffn_down_bwd(f: Ffn, dy, down_codes, down_scales, h, u, offsets, dh, du, a=None, stream=None) -> None:
+    """dh, du (and a again, unless None) from dy and the kept projections."""
+    _need_rows(f, "ffn_down_bwd", dy=(dy, f.D), h=(h, f.F), u=(u, f.F), dh=(dh, f.F), du=(du, f.F), a=(a, f.F))
+    _need_weights(f, "ffn_down_bwd", f.D, f.F, (down_codes, down_scales))
+    _need_offsets(offsets, f.E, "ffn_down_bwd")
+    _check(lib.fp8z1_ffn_down_bwd(C.byref(f), _ptr(dy), _ptr(down_codes), _ptr(down_scales), _ptr(h), _ptr(u),
+                                  _ptr(offsets), _ptr(dh), _ptr(du), _ptr(a), _stream(stream)), "fp8z1_ffn_down_bwd")
+
+
+def fp8z1_ffn_up_bwd(f: Ffn, dh, du, gate_codes, gate_scales, up_codes, up_scales, offsets, dx, stream=None) -> None:
+    """dx = dh Wg + du Wu."""
+    _need_rows(f, "ffn_up_bwd", dh=(dh, f.F), du=(du, f.F), dx=(dx, f.D))
+    _need_weights(f, "ffn_up_bwd", f.F, f.D, (gate_codes, gate_scales), (up_codes, up_scales))
+    _need_offsets(offsets, f.E, "ffn_up_bwd")
+    _check(lib.fp8z1_ffn_up_bwd(C.byref(f), _ptr(dh), _ptr(du), _ptr(gate_codes), _ptr(gate_scales), _ptr(up_codes),
+                                _ptr(up_scales), _ptr(offsets), _ptr(dx), _stream(stream)), "fp8z1_ffn_up_bwd")
+
+
+def fp8z1_ffn_wgrad_workspace_bytes(T: int, E: int, M: int, N: int) -> int:
+    n = C.c_size_t()
+    _check(lib.fp8z1_ffn_wgrad_workspace_bytes(T, E, M, N, C.byref(n)), "fp8z1_ffn_wgrad_workspace_bytes")
+    return n.value
+
+
+def fp8z1_ffn_wgrad(T: int, E: int, M: int, N: int, dtype: int, p, q, offsets, dw_dtype: int, dw,
+                    accumulate: bool = False, workspace=None, workspace_bytes: int = 0, stream=None) -> None:
+    """dw [E,M,N] = per expert p^T q (added to dw with accumulate)."""
+    if workspace is not None and not workspace_bytes and _is_tensor(workspace):
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    dt = _torch_dtype(dtype)
+    if p is not None:
+        _need(p, T * M * 2, "ffn_wgrad p", dt)
+    if q is not None:
+        _need(q, T * N * 2, "ffn_wgrad q", dt)
+    _need(dw, E * M * N * (4 if dw_dtype == F32 else 2), "ffn_wgrad dw", _torch_dtype(dw_dtype))
+    _need_offsets(offsets, E, "ffn_wgrad")
+    if workspace is not None:
+        _need(workspace, workspace_bytes, "ffn_wgrad workspace")
+    _check(lib.fp8z1_ffn_wgrad(T, E, M, N, dtype, _ptr(p), _ptr(q), _ptr(offsets), dw_dtype, _ptr(dw),
+                               int(bool(accumulate)), _ptr(workspace), workspace_bytes, _stream(stream)),
+           "fp8z1_ffn_wgrad")
+
+
+def _need_norm(f: Norm, what: str, act=(), res=(), weights=(), gates=()) -> None:
+    el = {F32: 4, BF16: 2, F16: 2}
+    for x in act:
+        if x is not None:
+            _need(x, f.T * f.C * el[f.dtype], what, _torch_dtype(f.dtype))
+    for x in res:
+        if x is not None:
+            _need(x, f.T * f.C * el[f.res_dtype], what, _torch_dtype(f.res_dtype))
+    for x in weights:
+        if x is not None:
+            _need(x, 4 * f.C, f"{what} weight", torch.float32)
+    for x in gates:
+        if x is not None:
+            n = {GATE_CHANNEL: f.C, GATE_TOKEN: f.T}.get(f.gate, f.T * f.C)
+            full = f.gate == GATE_FULL
+            _need(x, n * (el[f.dtype] if full else 4), f"{what} gate", _torch_dtype(f.dtype if full else F32))
+
+
+def fp8z1_norm_join(f: Norm, y, res, w_post, gate, w_pre, z, n, stream=None) -> None:
+    """z = res_scale res + block_scale gate norm(y), n = norm(z)."""
+    _need_norm(f, "norm_join", (y, n), (res, z), (w_post, w_pre), (gate,))
+    _check(lib.fp8z1_norm_join(C.byref(f), _ptr(y), _ptr(res), _ptr(w_post), _ptr(gate), _ptr(w_pre), _ptr(z), _ptr(n),
+                               _stream(stream)), "fp8z1_norm_join")
+
+
+def fp8z1_norm_join_bwd_workspace_bytes(f: Norm) -> int:
+    n = C.c_size_t()
+    _check(lib.fp8z1_norm_join_bwd_workspace_bytes(C.byref(f), C.byref(n)), "fp8z1_norm_join_bwd_workspace_bytes")
+    return n.value
+
+
+def fp8z1_norm_join_bwd(f: Norm, dz, dn, y, z, w_post, gate, w_pre, dy, dres, dw_post, dgate, dw_pre, workspace=None,
+                        workspace_bytes: int = 0, stream=None) -> None:
+    """The join's gradients; outputs that are None are not computed."""
+    if workspace is not None and not workspace_bytes and _is_tensor(workspace):
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    _need_norm(f, "norm_join_bwd", (dn, y, dy), (dz, z, dres), (w_post, w_pre, dw_post, dw_pre), (gate, dgate))
+    if workspace is not None:
+        _need(workspace, workspace_bytes, "norm_join_bwd workspace")
+    _check(lib.fp8z1_norm_join_bwd(C.byref(f), _ptr(dz), _ptr(dn), _ptr(y), _ptr(z), _ptr(w_post), _ptr(gate),
+                                   _ptr(w_pre), _ptr(dy), _ptr(dres), _ptr(dw_post), _ptr(dgate), _ptr(dw_pre),
+                                   _ptr(workspace), workspace_bytes, _stream(stream)), "fp8z1_norm_join_bwd")
 
 
 def fp8z1_probe_copy(src, dst, spread: int = 1, stream=None) -> None:

@@ -1,0 +1,121 @@
+// Matrix-core helpers of the feed-forward kernels: 16-bit element types, the
+// FP8 -> 16-bit widening of weight codes, the direct global -> LDS copy and the
+// transposing LDS reads of gfx950.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace fp8z1 {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef int i32x2 __attribute__((ext_vector_type(2)));
+
+// Operand layout of the two matrix instructions used (documented; both operands
+// alike): lane l of 32x32x16 holds row l % 32 at k = 8 * (l / 32) + 0..7 and gets
+// results (row 8 * (i / 4) + 4 * (l / 32) + i % 4, column l % 32), i = 0..15; lane l
+// of 16x16x32 holds row l % 16 at k = 8 * (l / 16) + 0..7 and gets results
+// (row 4 * (l / 16) + i, column l % 16), i = 0..3.  Any other assignment of k to
+// lanes gives the same sums as long as both operands use it.
+//
+// An E4M3 code has 4 significant bits and an exponent from -9 to 8, so both
+// 16-bit types hold it exactly: codes are widened without rounding and the block
+// scale multiplies the float32 partial sum.
+struct Bf16 {
+  typedef bf16x8 v8;
+  static __device__ __forceinline__ f32x16 mma32(v8 a, v8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ f32x4 mma16(v8 a, v8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  }
+  template <bool HI>
+  static __device__ __forceinline__ uint32_t widen2(int w) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HI));
+  }
+  static __device__ __forceinline__ float to_f32(uint16_t x) {
+    return __uint_as_float(static_cast<uint32_t>(x) << 16);
+  }
+  static __device__ __forceinline__ uint16_t from_f32(float x) {
+    return __builtin_bit_cast(uint16_t, static_cast<__bf16>(x));
+  }
+};
+
+struct F16 {
+  typedef f16x8 v8;
+  static __device__ __forceinline__ f32x16 mma32(v8 a, v8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ f32x4 mma16(v8 a, v8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+  }
+  template <bool HI>
+  static __device__ __forceinline__ uint32_t widen2(int w) {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, HI));
+  }
+  static __device__ __forceinline__ float to_f32(uint16_t x) {
+    return static_cast<float>(__builtin_bit_cast(_Float16, x));
+  }
+  static __device__ __forceinline__ uint16_t from_f32(float x) {
+    return __builtin_bit_cast(uint16_t, static_cast<_Float16>(x));
+  }
+};
+
+// 8 codes -> 8 elements
+template <class H>
+__device__ __forceinline__ typename H::v8 widen8(uint32_t lo, uint32_t hi) {
+  const uint4 r = make_uint4(H::template widen2<false>(lo), H::template widen2<true>(lo),
+                             H::template widen2<false>(hi), H::template widen2<true>(hi));
+  return __builtin_bit_cast(typename H::v8, r);
+}
+
+template <class H>
+__device__ __forceinline__ typename H::v8 as_v8(uint4 x) {
+  return __builtin_bit_cast(typename H::v8, x);
+}
+
+// 16 bytes at any alignment, one load (gfx950 runs in unaligned-access mode)
+typedef uint32_t v4u_a1_global_t __attribute__((ext_vector_type(4), aligned(1), address_space(1)));
+typedef uint32_t v4u_v_t __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ uint4 ld16(const uint8_t* p) {
+  const v4u_v_t r = *(const v4u_a1_global_t*)(p);
+  return make_uint4(r.x, r.y, r.z, r.w);
+}
+
+// The first `n` of 16 bytes, zeros after them (n may be <= 0 or >= 16); only those n
+// bytes are touched.
+__device__ __forceinline__ uint4 ld16_part(const uint8_t* p, int n) {
+  if (n >= 16) return ld16(p);
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    if (i < n) w[i / 4] |= static_cast<uint32_t>(p[i]) << (8 * (i % 4));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A wave's direct copy of 64 x 16 bytes from global memory (any 16-byte aligned
+// address per lane) to 1 KB of LDS: lane l's bytes land at dst + 16 l.
+__device__ __forceinline__ void copy16_to_lds(const uint8_t* src, uint8_t* dst) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(src),
+                                   (__attribute__((address_space(3))) void*)(dst), 16, 0, 0);
+}
+
+// Transposing reads, per group of 16 lanes.  16-bit: lane 4r + c names the 8 bytes
+// of row r, columns 4c..4c+3, and lane i receives column i of the four rows.
+// 8-bit: lane 2r + c names the 8 bytes of row r, columns 8c..8c+7, and lane i
+// receives column i of the eight rows.
+__device__ __forceinline__ i32x2 read_tr16(const uint8_t* p) {
+  return __builtin_bit_cast(
+      i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(p)));
+}
+__device__ __forceinline__ i32x2 read_tr8(const uint8_t* p) {
+  return __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) i32x2*)(p));
+}
+
+}  // namespace fp8z1

@@ -1,0 +1,543 @@
+// The join between two blocks of a residual network, in one pass over its rows:
+//   p = y rstd(y) (o + w_post)              norm after the block (or p = y)
+//   z = res_scale res + block_scale gate p  gate and residual scale
+//   n = z rstd(z) (o + w_pre)               norm before the next block
+// with rstd(x) = 1 / sqrt(mean(x^2) + eps), and its backward pass.  Everything between
+// the loads and the stores is float32; z is not rounded before it is normalized.
+//
+// A workgroup keeps a whole row in registers, 8 elements per thread and chunk, and walks
+// over rows with the weights held in registers, so each tensor is read or written
+// once and the weights once per workgroup.  The kernels are bound by HBM bandwidth.
+#include <hip/hip_runtime.h>
+
+#include "device_util.h"
+#include "mfma.h"
+
+namespace fp8z1 {
+namespace {
+
+struct NormArgs {
+  const void *y, *res, *gate;  // backward: res is the kept z
+  const float *w_post, *w_pre;
+  void *z, *n;  // forward outputs
+  // backward
+  const void *dz, *dn;
+  void *dy, *dres, *dgate;
+  float* part;  // [3][gridDim.x][C]: dw_post, dw_pre, dgate
+  int32_t T, C, gate_kind, want_post, want_pre, want_gate;
+  float eps, res_scale, block_scale, offset;
+};
+
+struct F32 {
+  static __device__ __forceinline__ float to_f32(float x) { return x; }
+  static __device__ __forceinline__ float from_f32(float x) { return x; }
+};
+template <class H>
+struct Elem {
+  typedef uint16_t type;
+};
+template <>
+struct Elem<F32> {
+  typedef float type;
+};
+
+// 8 elements of chunk `ch` of a row.  VEC: 8 consecutive ones by 16-byte accesses.
+// Otherwise (odd widths, unaligned rows) 8 elements a workgroup's width apart, so that
+// neighbouring threads still touch neighbouring elements.
+template <class H, bool VEC>
+__device__ __forceinline__ void load8(const void* row, int32_t C, int ch, float (&v)[8]) {
+  typedef typename Elem<H>::type E;
+  const E* p = static_cast<const E*>(row);
+  if (VEC) {
+    const int32_t c = (ch * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * 8;
+    if (c < C) {
+      E x[8];
+#pragma unroll
+      for (size_t i = 0; i < sizeof(x) / 16; ++i)
+        reinterpret_cast<uint4*>(x)[i] = reinterpret_cast<const uint4*>(p + c)[i];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = H::to_f32(x[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int32_t c = (ch * 8 + i) * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x);
+      v[i] = c < C ? H::to_f32(p[c]) : 0.0f;
+    }
+  }
+}
+
+template <class H, bool VEC>
+__device__ __forceinline__ void store8(void* row, int32_t C, int ch, const float (&v)[8]) {
+  typedef typename Elem<H>::type E;
+  E* p = static_cast<E*>(row);
+  if (VEC) {
+    const int32_t c = (ch * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * 8;
+    if (c < C) {
+      E x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = H::from_f32(v[i]);
+#pragma unroll
+      for (size_t i = 0; i < sizeof(x) / 16; ++i)
+        reinterpret_cast<uint4*>(p + c)[i] = reinterpret_cast<const uint4*>(x)[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int32_t c = (ch * 8 + i) * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x);
+      if (c < C) p[c] = H::from_f32(v[i]);
+    }
+  }
+}
+
+template <class H>
+__device__ __forceinline__ const void* row_of(const void* p, int64_t row, int32_t C) {
+  return static_cast<const typename Elem<H>::type*>(p) + row * C;
+}
+template <class H>
+__device__ __forceinline__ void* row_of(void* p, int64_t row, int32_t C) {
+  return static_cast<typename Elem<H>::type*>(p) + row * C;
+}
+
+// Sums of N values over the workgroup, in a fixed order; every thread gets them.  `lds`
+// holds 16 N floats; calls in a row use different ones, so one barrier each is enough
+// (a set is written again only after the next set's barrier).
+template <int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], float* lds) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor(v[i], o);
+  const int waves = blockDim.x >> 6, w = threadIdx.x >> 6;
+  if (waves == 1) return;
+  if ((threadIdx.x & 63) == 0)
+#pragma unroll
+    for (int i = 0; i < N; ++i) lds[w * N + i] = v[i];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = lds[i];
+  for (int k = 1; k < waves; ++k)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += lds[k * N + i];
+}
+
+__device__ __forceinline__ float rstd_of(float sum, int32_t C, float eps) {
+  return 1.0f / sqrtf(sum / static_cast<float>(C) + eps);
+}
+
+// o + w, or 1 where there is no weight
+template <bool VEC>
+__device__ __forceinline__ void load_weight(const float* w, int32_t C, int ch, float offset, float (&v)[8]) {
+  if (w) {
+    load8<F32, VEC>(w, C, ch, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += offset;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 1.0f;
+  }
+}
+
+// the gate's values of a row, times block_scale
+template <class H, bool VEC>
+__device__ __forceinline__ void load_gate(const NormArgs& a, int64_t row, int ch, float (&g)[8]) {
+  if (a.gate_kind == FP8Z1_GATE_CHANNEL) {
+    load8<F32, VEC>(a.gate, a.C, ch, g);
+  } else if (a.gate_kind == FP8Z1_GATE_FULL) {
+    load8<H, VEC>(row_of<H>(a.gate, row, a.C), a.C, ch, g);
+  } else {
+    const float x = a.gate_kind == FP8Z1_GATE_TOKEN ? static_cast<const float*>(a.gate)[row] : 1.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g[i] = x;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) g[i] *= a.block_scale;
+}
+
+template <class H, class R, bool VEC, int CH>
+__global__ __launch_bounds__(1024) void norm_join_kernel(NormArgs a) {
+  __shared__ float lds[2][16];
+  constexpr bool kHold = CH == 1;  // weights kept in registers over the rows
+  float wpost[CH][8], wpre[CH][8], gate[CH][8];
+#pragma unroll
+  for (int ch = 0; ch < CH; ++ch)
+    if (kHold) {
+      load_weight<VEC>(a.w_post, a.C, ch, a.offset, wpost[ch]);
+      load_weight<VEC>(a.w_pre, a.C, ch, a.offset, wpre[ch]);
+      if (a.gate_kind == FP8Z1_GATE_CHANNEL) load_gate<H, VEC>(a, 0, ch, gate[ch]);
+    }
+  for (int32_t row = blockIdx.x; row < a.T; row += gridDim.x) {
+    float y[CH][8], z[CH][8];
+    float sum[1] = {0.0f};
+#pragma unroll
+    for (int ch = 0; ch < CH; ++ch) {
+      if (a.y) load8<H, VEC>(row_of<H>(a.y, row, a.C), a.C, ch, y[ch]);
+      load8<R, VEC>(row_of<R>(a.res, row, a.C), a.C, ch, z[ch]);
+      if (!kHold) {
+        load_weight<VEC>(a.w_post, a.C, ch, a.offset, wpost[ch]);
+        load_weight<VEC>(a.w_pre, a.C, ch, a.offset, wpre[ch]);
+      }
+      if (a.y && (!kHold || a.gate_kind != FP8Z1_GATE_CHANNEL)) load_gate<H, VEC>(a, row, ch, gate[ch]);
+      if (a.y)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[0] = fmaf(y[ch][i], y[ch][i], sum[0]);
+    }
+    float r = 1.0f;
+    if (a.w_post) {
+      row_sums<1>(sum, lds[0]);
+      r = rstd_of(sum[0], a.C, a.eps);
+    }
+    sum[0] = 0.0f;
+#pragma unroll
+    for (int ch = 0; ch < CH; ++ch) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        z[ch][i] *= a.res_scale;
+        if (a.y) z[ch][i] = fmaf(gate[ch][i], y[ch][i] * r * wpost[ch][i], z[ch][i]);
+        sum[0] = fmaf(z[ch][i], z[ch][i], sum[0]);
+      }
+      if (a.z) store8<R, VEC>(row_of<R>(a.z, row, a.C), a.C, ch, z[ch]);
+    }
+    if (a.n) {
+      row_sums<1>(sum, lds[1]);
+      r = rstd_of(sum[0], a.C, a.eps);
+#pragma unroll
+      for (int ch = 0; ch < CH; ++ch) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[ch][i] = z[ch][i] * r * wpre[ch][i];
+        store8<H, VEC>(row_of<H>(a.n, row, a.C), a.C, ch, z[ch]);
+      }
+    }
+    if (!(a.w_post && a.n)) __syncthreads();  // only one of the two LDS sets is used per row
+  }
+}
+
+// Backward.  With v = dn (o + w_pre), z^ = z rstd(z):
+//   d    = dz + rstd(z) (v - z^ mean(v z^))        gradient at z
+//   dres = res_scale d,  dgate = block_scale d p,  dp = block_scale gate d
+//   dy   = rstd(y) (dp (o + w_post) - y^ mean(dp (o + w_post) y^))
+//   dw_pre = sum dn z^,  dw_post = sum dp y^,  and dgate summed over what it was broadcast to.
+// Two rounds of row sums; the sums over rows are kept per thread (each owns its
+// columns), written per workgroup and added in order by the kernel below, so no
+// atomics decide their order.
+template <class H, class R, bool VEC, int CH>
+__global__ __launch_bounds__(1024) void norm_join_bwd_kernel(NormArgs a) {
+  __shared__ float lds[2][48];
+  constexpr bool kHold = CH == 1;
+  float wpost[CH][8], wpre[CH][8], gate[CH][8], spost[CH][8], spre[CH][8], sgate[CH][8];
+#pragma unroll
+  for (int ch = 0; ch < CH; ++ch) {
+    if (kHold) {
+      load_weight<VEC>(a.w_post, a.C, ch, a.offset, wpost[ch]);
+      load_weight<VEC>(a.w_pre, a.C, ch, a.offset, wpre[ch]);
+      if (a.gate_kind == FP8Z1_GATE_CHANNEL) load_gate<H, VEC>(a, 0, ch, gate[ch]);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) spost[ch][i] = spre[ch][i] = sgate[ch][i] = 0.0f;
+  }
+  const float inv = 1.0f / static_cast<float>(a.C);
+  for (int32_t row = blockIdx.x; row < a.T; row += gridDim.x) {
+    float y[CH][8], z[CH][8], d[CH][8], dn[CH][8];
+    float s1[3] = {0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int ch = 0; ch < CH; ++ch) {
+      if (a.y) load8<H, VEC>(row_of<H>(a.y, row, a.C), a.C, ch, y[ch]);
+      if (a.dn) {
+        load8<H, VEC>(row_of<H>(a.dn, row, a.C), a.C, ch, dn[ch]);
+        load8<R, VEC>(row_of<R>(a.res, row, a.C), a.C, ch, z[ch]);
+      }
+      if (a.dz) {
+        load8<R, VEC>(row_of<R>(a.dz, row, a.C), a.C, ch, d[ch]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[ch][i] = 0.0f;
+      }
+      if (!kHold) {
+        load_weight<VEC>(a.w_post, a.C, ch, a.offset, wpost[ch]);
+        load_weight<VEC>(a.w_pre, a.C, ch, a.offset, wpre[ch]);
+      }
+      if (a.y && (!kHold || a.gate_kind != FP8Z1_GATE_CHANNEL)) load_gate<H, VEC>(a, row, ch, gate[ch]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (a.y) s1[0] = fmaf(y[ch][i], y[ch][i], s1[0]);
+        if (a.dn) {
+          s1[1] = fmaf(z[ch][i], z[ch][i], s1[1]);
+          s1[2] = fmaf(dn[ch][i] * wpre[ch][i], z[ch][i], s1[2]);
+        }
+      }
+    }
+    row_sums<3>(s1, lds[0]);
+    const float ry = a.w_post ? rstd_of(s1[0], a.C, a.eps) : 1.0f;
+    const float rz = rstd_of(s1[1], a.C, a.eps);
+    const float mz = s1[2] * rz * rz * inv;  // mean(v z^) rstd(z)
+    float s2[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int ch = 0; ch < CH; ++ch)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (a.dn) {
+          d[ch][i] = fmaf(rz, fmaf(-z[ch][i], mz, dn[ch][i] * wpre[ch][i]), d[ch][i]);
+          spre[ch][i] = fmaf(dn[ch][i], z[ch][i] * rz, spre[ch][i]);
+        }
+        if (a.y) {
+          y[ch][i] *= ry;                               // y^ (or y)
+          const float p = y[ch][i] * wpost[ch][i];
+          const float dp = gate[ch][i] * d[ch][i];
+          spost[ch][i] = fmaf(dp, y[ch][i], spost[ch][i]);
+          sgate[ch][i] = fmaf(d[ch][i], p, sgate[ch][i]);
+          s2[0] = fmaf(dp, p, s2[0]);
+          s2[1] = fmaf(d[ch][i], p, s2[1]);
+        }
+      }
+    row_sums<2>(s2, lds[1]);
+    const float my = s2[0] * inv;  // mean(dp (o + w_post) y^)
+#pragma unroll
+    for (int ch = 0; ch < CH; ++ch) {
+      if (a.y) {
+        float o[8];
+        if (a.gate_kind == FP8Z1_GATE_FULL && a.dgate) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] = a.block_scale * d[ch][i] * (y[ch][i] * wpost[ch][i]);
+          store8<H, VEC>(row_of<H>(a.dgate, row, a.C), a.C, ch, o);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          o[i] = gate[ch][i] * d[ch][i];
+          if (a.w_post) o[i] = ry * fmaf(-y[ch][i], my, o[i] * wpost[ch][i]);
+        }
+        if (a.dy) store8<H, VEC>(row_of<H>(a.dy, row, a.C), a.C, ch, o);
+      }
+      if (a.dres) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[ch][i] *= a.res_scale;
+        store8<R, VEC>(row_of<R>(a.dres, row, a.C), a.C, ch, d[ch]);
+      }
+    }
+    if (a.gate_kind == FP8Z1_GATE_TOKEN && a.dgate && threadIdx.x == 0)
+      static_cast<float*>(a.dgate)[row] = a.block_scale * s2[1];
+  }
+  const int64_t set = static_cast<int64_t>(gridDim.x) * a.C;
+#pragma unroll
+  for (int ch = 0; ch < CH; ++ch) {
+    if (a.want_post) store8<F32, VEC>(a.part + blockIdx.x * static_cast<int64_t>(a.C), a.C, ch, spost[ch]);
+    if (a.want_pre) store8<F32, VEC>(a.part + set + blockIdx.x * static_cast<int64_t>(a.C), a.C, ch, spre[ch]);
+    if (a.want_gate) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sgate[ch][i] *= a.block_scale;
+      store8<F32, VEC>(a.part + 2 * set + blockIdx.x * static_cast<int64_t>(a.C), a.C, ch, sgate[ch]);
+    }
+  }
+}
+
+// Column sums of the workgroups' partial sums (blockIdx.y: which gradient), in a fixed
+// order: 4 waves take every fourth workgroup's row, then their sums are added in order.
+__global__ __launch_bounds__(256) void norm_columns_kernel(const float* __restrict__ part, int32_t groups, int32_t C,
+                                                           float* o0, float* o1, float* o2) {
+  __shared__ float lds[4][64];
+  float* out = blockIdx.y == 0 ? o0 : blockIdx.y == 1 ? o1 : o2;
+  if (!out) return;
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int32_t c = static_cast<int32_t>(blockIdx.x) * 64 + lane;
+  const float* p = part + static_cast<int64_t>(blockIdx.y) * groups * C;
+  float v = 0.0f;
+  if (c < C)
+    for (int32_t g = w; g < groups; g += 4) v += p[static_cast<int64_t>(g) * C + c];
+  lds[w][lane] = v;
+  __syncthreads();
+  if (w == 0 && c < C) out[c] = lds[0][lane] + lds[1][lane] + lds[2][lane] + lds[3][lane];
+}
+
+constexpr int64_t kMaxC = FP8Z1_NORM_MAX_WIDTH;
+
+int threads_for(int64_t C) {
+  const int64_t per = C <= 8192 ? 8 : 16;  // elements a thread holds
+  return static_cast<int>((C + 64 * per - 1) / (64 * per) * 64);
+}
+
+// Workgroups: enough waves for the card (16 per compute unit), each walking over rows.
+int64_t groups_for(int64_t T, int64_t C, int waves_per_cu) {
+  const int64_t waves = threads_for(C) / 64;
+  const int64_t most = (256 * waves_per_cu + waves - 1) / waves;
+  return T < most ? T : most;
+}
+constexpr int kFwdWaves = 28, kBwdWaves = 14;
+
+bool misaligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
+
+int check_norm(const fp8z1_norm* f, const void* y, const float* w_post, const void* gate, const char* what) {
+  const std::string w(what);
+  if (!f) return set_error(FP8Z1_EINVAL, w + ": NULL description");
+  if (f->dtype != FP8Z1_BF16 && f->dtype != FP8Z1_F16 && f->dtype != FP8Z1_F32)
+    return set_error(FP8Z1_EINVAL, w + ": dtype must be FP8Z1_F32, FP8Z1_BF16 or FP8Z1_F16");
+  if (f->res_dtype != f->dtype && f->res_dtype != FP8Z1_F32)
+    return set_error(FP8Z1_EINVAL, w + ": res_dtype must be dtype or FP8Z1_F32");
+  if (f->gate < FP8Z1_GATE_NONE || f->gate > FP8Z1_GATE_FULL) return set_error(FP8Z1_EINVAL, w + ": unknown gate kind");
+  if (f->T < 0 || f->T > FP8Z1_FFN_MAX_ROWS) return set_error(FP8Z1_ESHAPE, w + ": T outside 0 .. 2^30");
+  if (f->C < 1 || f->C > kMaxC) return set_error(FP8Z1_ESHAPE, w + ": C outside 1 .. 16384");
+  if (!(f->eps >= 0.0f)) return set_error(FP8Z1_EINVAL, w + ": eps must be >= 0");
+  if (!y && f->T && (w_post || f->gate != FP8Z1_GATE_NONE))
+    return set_error(FP8Z1_EINVAL, w + ": a norm after the block or a gate needs y");
+  if ((f->gate != FP8Z1_GATE_NONE) != (gate != nullptr) && f->T)
+    return set_error(FP8Z1_EINVAL, w + ": gate pointer and gate kind disagree");
+  return FP8Z1_OK;
+}
+
+NormArgs base_args(const fp8z1_norm* f, const void* y, const void* res, const float* w_post, const void* gate,
+                   const float* w_pre) {
+  NormArgs a{};
+  a.y = y;
+  a.res = res;
+  a.gate = gate;
+  a.w_post = w_post;
+  a.w_pre = w_pre;
+  a.T = static_cast<int32_t>(f->T);
+  a.C = static_cast<int32_t>(f->C);
+  a.gate_kind = f->gate;
+  a.eps = f->eps;
+  a.res_scale = f->res_scale;
+  a.block_scale = f->block_scale;
+  a.offset = f->weight_offset;
+  return a;
+}
+
+template <class H, class R, bool BWD>
+void launch_typed(const NormArgs& a, bool vec, dim3 g, dim3 b, hipStream_t s) {
+  const bool one = a.C <= 8192;
+#define FP8Z1_NORM_GO(V, N)                                                        \
+  if (BWD)                                                                         \
+    hipLaunchKernelGGL((norm_join_bwd_kernel<H, R, V, N>), g, b, 0, s, a);         \
+  else                                                                             \
+    hipLaunchKernelGGL((norm_join_kernel<H, R, V, N>), g, b, 0, s, a)
+  if (vec && one) {
+    FP8Z1_NORM_GO(true, 1);
+  } else if (vec) {
+    FP8Z1_NORM_GO(true, 2);
+  } else if (one) {
+    FP8Z1_NORM_GO(false, 1);
+  } else {
+    FP8Z1_NORM_GO(false, 2);
+  }
+#undef FP8Z1_NORM_GO
+}
+
+template <bool BWD>
+void launch(const fp8z1_norm* f, const NormArgs& a, bool vec, int64_t groups, hipStream_t s) {
+  const dim3 g(static_cast<unsigned>(groups)), b(static_cast<unsigned>(threads_for(f->C)));
+  const bool wide = f->res_dtype == FP8Z1_F32;
+  if (f->dtype == FP8Z1_F32)
+    launch_typed<F32, F32, BWD>(a, vec, g, b, s);
+  else if (f->dtype == FP8Z1_BF16 && wide)
+    launch_typed<Bf16, F32, BWD>(a, vec, g, b, s);
+  else if (f->dtype == FP8Z1_BF16)
+    launch_typed<Bf16, Bf16, BWD>(a, vec, g, b, s);
+  else if (wide)
+    launch_typed<F16, F32, BWD>(a, vec, g, b, s);
+  else
+    launch_typed<F16, F16, BWD>(a, vec, g, b, s);
+}
+
+size_t elem_size(int32_t dtype) { return dtype == FP8Z1_F32 ? 4 : 2; }
+
+// Every pointer aligned to its elements (else an error), and whether 16-byte accesses fit.
+int check_alignment(const fp8z1_norm* f, std::initializer_list<const void*> act, std::initializer_list<const void*> res,
+                    std::initializer_list<const void*> f32, const void* gate_any, bool& vec, const char* what) {
+  vec = f->C % 8 == 0;
+  bool bad = false;
+  for (const void* p : act) bad |= misaligned(p, elem_size(f->dtype)), vec &= !misaligned(p, 16);
+  for (const void* p : res) bad |= misaligned(p, elem_size(f->res_dtype)), vec &= !misaligned(p, 16);
+  for (const void* p : f32) bad |= misaligned(p, 4), vec &= !misaligned(p, 16);
+  if (f->gate != FP8Z1_GATE_NONE) {
+    bad |= misaligned(gate_any, f->gate == FP8Z1_GATE_FULL ? elem_size(f->dtype) : 4);
+    vec &= f->gate == FP8Z1_GATE_TOKEN || !misaligned(gate_any, 16);
+  }
+  return bad ? set_error(FP8Z1_EINVAL, std::string(what) + ": misaligned argument") : FP8Z1_OK;
+}
+
+}  // namespace
+}  // namespace fp8z1
+
+using namespace fp8z1;
+
+extern "C" int fp8z1_norm_join(const fp8z1_norm* f, const void* y, const void* res, const float* w_post,
+                               const void* gate, const float* w_pre, void* z, void* n, void* stream) {
+  const char* what = "norm_join";
+  int rc = check_norm(f, y, w_post, gate, what);
+  if (rc) return rc;
+  if (f->T == 0) return FP8Z1_OK;
+  if (!res || (!z && !n)) return set_error(FP8Z1_EINVAL, "norm_join: NULL argument");
+  bool vec = false;
+  rc = check_alignment(f, {y, n}, {res, z}, {w_post, w_pre}, gate, vec, what);
+  if (rc) return rc;
+  NormArgs a = base_args(f, y, res, w_post, gate, w_pre);
+  a.z = z;
+  a.n = n;
+  launch<false>(f, a, vec, groups_for(f->T, f->C, kFwdWaves), static_cast<hipStream_t>(stream));
+  return check_hip(hipGetLastError(), "norm_join: launch");
+}
+
+extern "C" int fp8z1_norm_join_bwd_workspace_bytes(const fp8z1_norm* f, size_t* bytes) {
+  if (!bytes) return set_error(FP8Z1_EINVAL, "norm_join_bwd_workspace_bytes: NULL argument");
+  if (!f) return set_error(FP8Z1_EINVAL, "norm_join_bwd_workspace_bytes: NULL description");
+  if (f->T < 0 || f->T > FP8Z1_FFN_MAX_ROWS || f->C < 1 || f->C > kMaxC)
+    return set_error(FP8Z1_ESHAPE, "norm_join_bwd_workspace_bytes: T or C out of range");
+  *bytes = sizeof(float) * 3 * static_cast<size_t>(groups_for(f->T, f->C, kBwdWaves)) * static_cast<size_t>(f->C);
+  return FP8Z1_OK;
+}
+
+extern "C" int fp8z1_norm_join_bwd(const fp8z1_norm* f, const void* dz, const void* dn, const void* y, const void* z,
+                                   const float* w_post, const void* gate, const float* w_pre, void* dy, void* dres,
+                                   float* dw_post, void* dgate, float* dw_pre, void* workspace, size_t workspace_bytes,
+                                   void* stream) {
+  const char* what = "norm_join_bwd";
+  int rc = check_norm(f, y, w_post, gate, what);
+  if (rc) return rc;
+  if (f->T && !dz && !dn) return set_error(FP8Z1_EINVAL, "norm_join_bwd: dz and dn are both NULL");
+  if (f->T && dn && !z) return set_error(FP8Z1_EINVAL, "norm_join_bwd: dn needs z");
+  if (f->T && dy && !y) return set_error(FP8Z1_EINVAL, "norm_join_bwd: dy needs y");
+  if ((dw_post && !w_post) || (dw_pre && !w_pre)) return set_error(FP8Z1_EINVAL, "norm_join_bwd: gradient of no weight");
+  if (dgate && f->gate == FP8Z1_GATE_NONE) return set_error(FP8Z1_EINVAL, "norm_join_bwd: gradient of no gate");
+  bool vec = false;
+  rc = check_alignment(f, {y, dn, dy}, {z, dz, dres}, {w_post, w_pre, dw_post, dw_pre}, gate, vec, what);
+  if (!rc && dgate) {
+    bool v2 = false;
+    rc = check_alignment(f, {}, {}, {}, dgate, v2, what);
+    vec &= v2;
+  }
+  if (rc) return rc;
+  float* gate_cols = f->gate == FP8Z1_GATE_CHANNEL ? static_cast<float*>(dgate) : nullptr;
+  const bool sums = dw_post || dw_pre || gate_cols;
+  const int64_t groups = groups_for(f->T, f->C, kBwdWaves);
+  if (sums && f->T) {
+    size_t need = 0;
+    rc = fp8z1_norm_join_bwd_workspace_bytes(f, &need);
+    if (rc) return rc;
+    if (!workspace || workspace_bytes < need) return set_error(FP8Z1_EINVAL, "norm_join_bwd: workspace too small");
+    if (misaligned(workspace, 16)) return set_error(FP8Z1_EINVAL, "norm_join_bwd: misaligned workspace");
+  }
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (f->T) {
+    NormArgs a = base_args(f, y, z, w_post, gate, w_pre);
+    a.dz = dz;
+    a.dn = dn;
+    a.dy = dy;
+    a.dres = dres;
+    a.dgate = dgate;
+    a.part = static_cast<float*>(workspace);
+    a.want_post = dw_post != nullptr;
+    a.want_pre = dw_pre != nullptr;
+    a.want_gate = gate_cols != nullptr;
+    launch<true>(f, a, vec, groups, s);
+    rc = check_hip(hipGetLastError(), "norm_join_bwd: launch");
+    if (rc) return rc;
+  }
+  if (sums) {
+    hipLaunchKernelGGL(norm_columns_kernel, dim3(static_cast<unsigned>((f->C + 63) / 64), 3), dim3(256), 0, s,
+                       static_cast<const float*>(workspace), static_cast<int32_t>(groups), static_cast<int32_t>(f->C),
+                       dw_post, dw_pre, gate_cols);
+    rc = check_hip(hipGetLastError(), "norm_join_bwd: sums launch");
+  }
+  return rc;
+}

@@ -88,6 +88,7 @@ extern "C" {
 #define FP8Z1_F32 0
 #define FP8Z1_BF16 1
 #define FP8Z1_E4M3 2 /* OCP FP8 E4M3 codes, one byte each */
+#define FP8Z1_F16 3  /* IEEE binary16 (feed-forward block and norms only) */
 
 #define FP8Z1_BLOCK 128 /* block edge */
 #define FP8Z1_STAT_PARTS 4 /* float64 partial sums of squares per slot (one per 32 rows) */
@@ -305,6 +306,118 @@ int fp8z1_unfold(const fp8z1_table* table, const void* folded, int32_t dtype, co
  * stand for. */
 int fp8z1_dequantize(const uint8_t* codes, const float* scales, int64_t E, int64_t R, int64_t C, int32_t out_dtype,
                      void* out, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The feed-forward block that the sharded weights make up, and the norms around it.
+ *
+ * Weights are what fp8z1_unfold writes: row-major E4M3 codes [E, R, C] with one scale
+ * per 128x128 block, w = code * scale.  Per expert e the block is
+ *     h = x Wg^T,  u = x Wu^T,  a = act(h) * u,  y = a Wd^T
+ * with Wg, Wu [F, D] and Wd [D, F].  Rows (tokens) are sorted by expert: expert e
+ * has rows offsets[e] .. offsets[e+1]-1 (it may have none).  offsets is device memory,
+ * E + 1 int32, ascending from 0 to T, read when the kernels run; NULL stands for one
+ * expert with all rows.  Offsets outside [0, T] are clamped to it; rows that no
+ * expert covers are left unwritten.
+ *
+ * All activations and their gradients are contiguous rows of one 16-bit type, aligned to
+ * their element (16-byte aligned rows run faster), codes at any alignment.
+ * Products are summed in float32 on the matrix cores: codes are widened exactly and
+ * each block's scale multiplies the float32 partial sum of its 128 products, so
+ * the only roundings to 16 bits are those of the tensors that a call writes.
+ * Outputs must not overlap inputs.  T may be 0 (pointers to rows may then be NULL).
+ * No call allocates or waits; all of them may be captured into a HIP graph. */
+
+/* gated activation */
+#define FP8Z1_ACT_SILU 0 /* h / (1 + exp(-h)) */
+#define FP8Z1_ACT_GELU 1 /* 0.5 h (1 + tanh(sqrt(2/pi) (h + 0.044715 h^3))) */
+
+#define FP8Z1_FFN_MAX_ROWS (1 << 30)
+#define FP8Z1_FFN_MAX_WIDTH (1 << 20)
+#define FP8Z1_FFN_MAX_EXPERTS 65535
+
+typedef struct {
+  int64_t T; /* rows (tokens) */
+  int64_t E; /* experts */
+  int64_t D; /* width of x and y */
+  int64_t F; /* width of h, u and a */
+  int32_t dtype; /* FP8Z1_BF16 or FP8Z1_F16: type of all activations */
+  int32_t act;   /* FP8Z1_ACT_* */
+} fp8z1_ffn;
+
+/* a [T,F] = act(x Wg^T) * (x Wu^T) in one kernel; gate and up codes [E,F,D].  h and u
+ * [T,F] (both or neither NULL) keep the projections for the backward pass. */
+int fp8z1_ffn_up(const fp8z1_ffn* f, const void* x, const uint8_t* gate_codes, const float* gate_scales,
+                 const uint8_t* up_codes, const float* up_scales, const int32_t* offsets, void* h, void* u, void* a,
+                 void* stream);
+
+/* y [T,D] = a Wd^T; down codes [E,D,F]. */
+int fp8z1_ffn_down(const fp8z1_ffn* f, const void* a, const uint8_t* down_codes, const float* down_scales,
+                   const int32_t* offsets, void* y, void* stream);
+
+/* From dy [T,D] and the kept h, u: da = dy Wd (never written), dh = da * u * act'(h),
+ * du = da * act(h), and, unless a is NULL, a = act(h) * u again for the weight gradient. */
+int fp8z1_ffn_down_bwd(const fp8z1_ffn* f, const void* dy, const uint8_t* down_codes, const float* down_scales,
+                       const void* h, const void* u, const int32_t* offsets, void* dh, void* du, void* a,
+                       void* stream);
+
+/* dx [T,D] = dh Wg + du Wu, both products in one sum. */
+int fp8z1_ffn_up_bwd(const fp8z1_ffn* f, const void* dh, const void* du, const uint8_t* gate_codes,
+                     const float* gate_scales, const uint8_t* up_codes, const float* up_scales, const int32_t* offsets,
+                     void* dx, void* stream);
+
+/* Weight gradient dw [E,M,N] = per expert sum over its rows t of p[t,m] q[t,n], with p
+ * [T,M] and q [T,N] of `dtype` (FP8Z1_BF16 or FP8Z1_F16): dWg = (dh, x), dWu = (du, x),
+ * dWd = (dy, a).  dw_dtype FP8Z1_F32 (the gradients that fp8z1_fold and
+ * fp8z1_step_rowmajor read; with `accumulate` the products are added to dw) or
+ * FP8Z1_BF16.  An expert without rows gets zeros (or keeps its dw).
+ * Where the output is too small to fill the card the rows are split into partial sums in
+ * d_workspace, joined in a fixed order; with less than
+ * fp8z1_ffn_wgrad_workspace_bytes() bytes (or NULL) they are not split. */
+int fp8z1_ffn_wgrad_workspace_bytes(int64_t T, int64_t E, int64_t M, int64_t N, size_t* bytes);
+int fp8z1_ffn_wgrad(int64_t T, int64_t E, int64_t M, int64_t N, int32_t dtype, const void* p, const void* q,
+                    const int32_t* offsets, int32_t dw_dtype, void* dw, int32_t accumulate, void* d_workspace,
+                    size_t workspace_bytes, void* stream);
+
+/* gates of the join: the block's output is multiplied by */
+#define FP8Z1_GATE_NONE 0    /* nothing */
+#define FP8Z1_GATE_CHANNEL 1 /* float32 [C], the same for all rows */
+#define FP8Z1_GATE_TOKEN 2   /* float32 [T], the same for all channels */
+#define FP8Z1_GATE_FULL 3    /* [T,C] of dtype */
+
+#define FP8Z1_NORM_MAX_WIDTH 16384
+
+typedef struct {
+  int64_t T, C;
+  int32_t dtype;     /* y, n and a full gate: FP8Z1_BF16, FP8Z1_F16 or FP8Z1_F32 */
+  int32_t res_dtype; /* res and z: dtype or FP8Z1_F32 */
+  int32_t gate;      /* FP8Z1_GATE_* */
+  float eps;
+  float res_scale, block_scale;
+  float weight_offset; /* added to the norm weights (1 for weights kept around 0) */
+  int32_t reserved;
+} fp8z1_norm;
+
+/* The join between two blocks, in one pass over the rows:
+ *     p = y rstd(y) (weight_offset + w_post)     (p = y where w_post is NULL)
+ *     z = res_scale res + block_scale gate p     (z = res_scale res where y is NULL)
+ *     n = z rstd(z) (weight_offset + w_pre)      (factor 1 where w_pre is NULL)
+ * with rstd(x) = 1 / sqrt(mean(x^2) + eps) over the C values of a row.  Norm weights are
+ * float32 [C].  z or n may be NULL if it is not wanted.  All arithmetic is float32, and
+ * n is taken from z before z is rounded to res_dtype.  z may be res itself. */
+int fp8z1_norm_join(const fp8z1_norm* f, const void* y, const void* res, const float* w_post, const void* gate,
+                    const float* w_pre, void* z, void* n, void* stream);
+
+/* Its gradients, from dz (gradient at z, res_dtype) and dn (at n, dtype); one of them may be
+ * NULL (no such gradient).  y, w_post, gate, w_pre as in the forward call, z as it wrote
+ * it (not read if dn is NULL).  Outputs, each NULL if not wanted: dy [T,C] dtype, dres
+ * [T,C] res_dtype (may be dz itself), dw_post and dw_pre float32 [C], dgate of the gate's
+ * own shape and type.  dw_post, dw_pre and a channel gate's dgate need
+ * fp8z1_norm_join_bwd_workspace_bytes() bytes of device workspace (16-byte aligned). */
+int fp8z1_norm_join_bwd_workspace_bytes(const fp8z1_norm* f, size_t* bytes);
+int fp8z1_norm_join_bwd(const fp8z1_norm* f, const void* dz, const void* dn, const void* y, const void* z,
+                        const float* w_post, const void* gate, const float* w_pre, void* dy, void* dres,
+                        float* dw_post, void* dgate, float* dw_pre, void* d_workspace, size_t workspace_bytes,
+                        void* stream);
 
 /* Copy the device state to the host (synchronizes the stream) / from the host
  * (resume from a checkpoint). */
