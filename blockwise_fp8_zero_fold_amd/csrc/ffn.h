@@ -6,6 +6,11 @@
 
 namespace fp8z1 {
 
+template <int N>
+struct Int {
+  static constexpr int value = N;
+};
+
 enum FfnKind {
   kFfnUp = 0,       // a = act(x Wg^T) * (x Wu^T)
   kFfnDown = 1,     // y = a Wd^T
@@ -65,6 +70,7 @@ __device__ __forceinline__ bool find_tile(const int32_t* offsets, int32_t T, int
   } else {
     total = (T + ROWS - 1) / ROWS;
   }
+  total = __builtin_amdgcn_readfirstlane(total);
   const int64_t all = static_cast<int64_t>(total) * ncols;
   if (b >= all) return false;
   const int32_t g = static_cast<int32_t>(all), x = b % kXcds, per = g / kXcds, rem = g % kXcds;
@@ -101,6 +107,8 @@ __device__ __forceinline__ bool find_tile(const int32_t* offsets, int32_t T, int
   e = __builtin_amdgcn_readfirstlane(e);
   mt = __builtin_amdgcn_readfirstlane(mt);
   expert_rows(offsets, T, e, lo, hi);
+  lo = __builtin_amdgcn_readfirstlane(lo);
+  hi = __builtin_amdgcn_readfirstlane(hi);
   m0 = lo + mt * ROWS;
   return m0 < hi;
 }

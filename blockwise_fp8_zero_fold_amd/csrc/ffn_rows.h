@@ -1,0 +1,164 @@
+// Forward products for few rows per expert (serving): bound by the read of the weights.
+//
+// A workgroup takes 16 weight rows (of gate and up, or of down) of one expert and its WAVES
+// waves share k among them, a block of 128 (one scale) at a time in turn.  A wave reads
+// each of its weight rows' 128 bytes straight into registers, 32 bytes per lane, widens
+// them and multiplies by 16 TT rows of x on the matrix cores; the next block's bytes are
+// on their way meanwhile.  The waves' sums are added in order through LDS.
+#pragma once
+
+#include "ffn.h"
+
+namespace fp8z1 {
+namespace {
+
+template <class H, int KIND, int WAVES, int TT, bool ALIGNED>
+__global__ __launch_bounds__(WAVES * 64) void ffn_rows_kernel(FfnArgs p) {
+  constexpr bool kUp = KIND == kFfnUp;
+  constexpr int kM = kUp ? 2 : 1;  // matrices
+  typedef typename H::v8 v8;
+  __shared__ f32x4 sums[WAVES][kM * TT][64];
+  const int32_t e = blockIdx.y;
+  int32_t lo, hi;
+  expert_rows(p.offsets, p.T, e, lo, hi);
+  const int32_t N = p.N, K = p.K, n0 = static_cast<int32_t>(blockIdx.x) * 16;
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
+  const int32_t kb = (K + kB - 1) / kB, nb = (N + kB - 1) / kB;
+  const int64_t row = (static_cast<int64_t>(e) * N + min(n0 + r, N - 1)) * K + g * 32;
+  const uint8_t* const wt[2] = {p.w0 + row, kUp ? p.w1 + row : nullptr};
+  const int64_t sat = (static_cast<int64_t>(e) * nb + n0 / kB) * kb;
+  const float* const sc[2] = {p.s0 + sat, kUp ? p.s1 + sat : nullptr};
+
+  struct Block {
+    uint4 c[kM][2];
+    uint4 x[TT][4];
+    float s[kM];
+  };
+  for (int32_t t0 = lo; t0 < hi; t0 += 16 * TT) {
+    const uint8_t* xr[TT];
+#pragma unroll
+    for (int i = 0; i < TT; ++i) xr[i] = p.x0 + (static_cast<int64_t>(min(t0 + 16 * i + r, hi - 1)) * K + g * 32) * 2;
+    auto load = [&](int32_t q, Block& b) {
+      const int32_t left = K - q * kB - g * 32;  // of this lane's 32 k
+#pragma unroll
+      for (int m = 0; m < kM; ++m) {
+        b.s[m] = sc[m][q];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint8_t* src = wt[m] + q * kB + 16 * i;
+          if (ALIGNED)
+            b.c[m][i] = 16 * i < left ? *reinterpret_cast<const uint4*>(src) : make_uint4(0u, 0u, 0u, 0u);
+          else
+            b.c[m][i] = ld16_part(src, left - 16 * i);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < TT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint8_t* src = xr[t] + q * kB * 2 + 16 * i;
+          if (ALIGNED)
+            b.x[t][i] = 8 * i < left ? *reinterpret_cast<const uint4*>(src) : make_uint4(0u, 0u, 0u, 0u);
+          else
+            b.x[t][i] = ld16_part(src, 2 * left - 16 * i);
+        }
+    };
+    f32x4 acc[kM][TT];
+    const f32x4 zero = {};
+#pragma unroll
+    for (int m = 0; m < kM; ++m)
+#pragma unroll
+      for (int t = 0; t < TT; ++t) acc[m][t] = zero;
+    auto add = [&](const Block& b) {
+#pragma unroll
+      for (int m = 0; m < kM; ++m) {
+        f32x4 part[TT];
+#pragma unroll
+        for (int t = 0; t < TT; ++t) part[t] = zero;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 c = b.c[m][i / 2];
+          const v8 wv = i % 2 ? widen8<H>(c.z, c.w) : widen8<H>(c.x, c.y);
+#pragma unroll
+          for (int t = 0; t < TT; ++t) part[t] = H::mma16(wv, as_v8<H>(b.x[t][i]), part[t]);
+        }
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[m][t][i] = fmaf(b.s[m], part[t][i], acc[m][t][i]);
+      }
+    };
+    Block b0, b1;
+    if (w < kb) load(w, b0);
+    if (w + WAVES < kb) load(w + WAVES, b1);
+    for (int32_t q = w; q < kb; q += 2 * WAVES) {
+      add(b0);
+      if (q + 2 * WAVES < kb) load(q + 2 * WAVES, b0);
+      if (q + WAVES < kb) {
+        add(b1);
+        if (q + 3 * WAVES < kb) load(q + 3 * WAVES, b1);
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < kM; ++m)
+#pragma unroll
+      for (int t = 0; t < TT; ++t) sums[w][m * TT + t][lane] = acc[m][t];
+    __syncthreads();
+    if (w < TT) {
+      f32x4 v[kM];
+#pragma unroll
+      for (int m = 0; m < kM; ++m) {
+        v[m] = sums[0][m * TT + w][lane];
+        for (int k = 1; k < WAVES; ++k)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[m][i] += sums[k][m * TT + w][lane][i];
+      }
+      const int32_t t = t0 + 16 * w + r;
+      if (t < hi) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int32_t n = n0 + 4 * g + i;
+          if (n >= N) continue;
+          const int64_t at = static_cast<int64_t>(t) * N + n;
+          if (kUp) {
+            p.o0[at] = H::from_f32(act_value(p.act, v[0][i]) * v[kM - 1][i]);
+            if (p.o1) {
+              p.o1[at] = H::from_f32(v[0][i]);
+              p.o2[at] = H::from_f32(v[kM - 1][i]);
+            }
+          } else {
+            p.o0[at] = H::from_f32(v[0][i]);
+          }
+        }
+      }
+    }
+    __syncthreads();  // sums is written again for the next rows
+  }
+}
+
+template <class H, int KIND, int WAVES, int TT>
+void launch_rows_as(const FfnArgs& p, bool aligned, dim3 g, hipStream_t s) {
+  if (aligned)
+    hipLaunchKernelGGL((ffn_rows_kernel<H, KIND, WAVES, TT, true>), g, dim3(WAVES * 64), 0, s, p);
+  else
+    hipLaunchKernelGGL((ffn_rows_kernel<H, KIND, WAVES, TT, false>), g, dim3(WAVES * 64), 0, s, p);
+}
+
+// Few workgroups: 16 waves each, so that all of k is on its way at once; else 4.  Up to 16
+// rows per expert on average: one matrix tile of rows at a time; else two.
+template <class H, int KIND>
+void launch_rows(const FfnArgs& p, bool aligned, hipStream_t s) {
+  const dim3 g(static_cast<unsigned>((p.N + 15) / 16), static_cast<unsigned>(p.E));
+  const bool deep = static_cast<int64_t>(g.x) * g.y < 512, two = static_cast<int64_t>(p.T) > 8ll * p.E;
+  if (deep && two)
+    launch_rows_as<H, KIND, 16, 2>(p, aligned, g, s);
+  else if (deep)
+    launch_rows_as<H, KIND, 16, 1>(p, aligned, g, s);
+  else if (two)
+    launch_rows_as<H, KIND, 4, 2>(p, aligned, g, s);
+  else
+    launch_rows_as<H, KIND, 4, 1>(p, aligned, g, s);
+}
+
+}  // namespace
+}  // namespace fp8z1

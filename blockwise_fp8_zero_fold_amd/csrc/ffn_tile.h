@@ -1,0 +1,436 @@
+// The feed-forward block over blockwise-FP8 weights, tokens sorted by expert: both
+// projections with the gated activation, the down projection, and the backward pass
+// with respect to the activations.
+//
+// One tile kernel serves all four calls.  A workgroup of 4 waves computes 128 rows
+// (tokens of one expert) x 128 columns; each wave 64 x 64, as 2 x 2 matrix tiles of
+// 32 x 32.  The sum over k goes in blocks of 128, the blocks that one weight scale
+// covers:  acc += scale * sum_{k in block} x[m][k] * code[k][n],  the inner sum on the
+// matrix cores with the codes widened exactly, so no dequantized weight is rounded.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <initializer_list>
+
+#include "ffn.h"
+#include "ffn_rows.h"
+
+namespace fp8z1 {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kRows = 128;  // tile rows
+constexpr int kStep = 64;   // k per LDS stage
+constexpr int kABytes = kRows * kStep * 2;
+
+// Whether the block scales that a tile multiplies by are positive, finite and within a
+// factor 2^40 of each other.  Every wave looks at all of them, so all agree.
+__device__ __forceinline__ bool scales_close(const float* s, int32_t count, int32_t stride, float& lo, float& hi) {
+  bool ok = true;
+  for (int32_t i = threadIdx.x & 63; i < count; i += 64) {
+    const float x = s[static_cast<int64_t>(i) * stride];
+    ok = ok && x > 0.0f && x < 3e38f;
+    lo = fminf(lo, x);
+    hi = fmaxf(hi, x);
+  }
+  return ok;
+}
+
+// Chunk c of row r of an LDS tile sits at position c ^ swizzle(r) of the row.  LDS serves 256
+// bytes at a time: 16 lanes of a 16-byte read (16 rows of one chunk) or 32 lanes of a
+// transposing 8-byte read (8 rows of two neighbouring chunks), which the swizzle
+// spreads over all 16 places; with the lower 3 bits of the row alone half of the
+// LDS cycles were conflicts.
+__device__ __forceinline__ int swizzle_a(int r) { return (r >> 1) & 7; }  // rows of 128 bytes
+__device__ __forceinline__ int swizzle_b(int r) { return (r >> 2) & 3; }  // rows of 64 bytes
+template <int BYTES>
+__device__ __forceinline__ int swizzle_t(int r) {  // transposed reads, rows of 128 or 256 bytes
+  return BYTES == 256 ? (r & 7) << 1 : ((r >> 1) & 3) << 1;
+}
+
+// NT: 32-column tiles per wave (2 or 4).  DIRECT: rows and codes are 16-byte aligned, so a
+// stage goes from memory to LDS by direct copies; otherwise through registers, with
+// the bytes outside a row left out.
+//
+// The accumulator holds the sum in units of the current block's scale: between blocks
+// it is multiplied by scale_before / scale_now and the matrix cores add the next block's
+// code products right into it, so no second set of registers is needed for the partial
+// sums and a wave can own 64 x 128.  That product stays harmless while the tile's scales
+// are within 2^40 of each other; a tile with scales further apart sums each block apart
+// and adds scale * sum, in passes over half its columns.
+template <class H, int KIND, int NT, bool DIRECT>
+__global__ __launch_bounds__(kThreads, 2) void ffn_tile_kernel(FfnArgs p, int32_t ncols) {
+  constexpr bool kTrans = KIND == kFfnDownBwd || KIND == kFfnUpBwd;  // weights run along n
+  constexpr bool kUp = KIND == kFfnUp;
+  constexpr int kB2 = NT * 64;                  // weight rows (or columns) of a stage
+  constexpr int kCols = kUp ? kB2 / 2 : kB2;    // output columns of a tile
+  constexpr int kSeg = KIND == kFfnUpBwd ? 2 : 1;  // products added up
+  constexpr int kBBytes = kB2 * kStep;
+  constexpr int kBC = kBBytes / 16 / kThreads;  // 16-byte chunks per thread and stage: 2 or 4
+  constexpr int kBPer = kTrans ? kB2 / 16 : 4;  // chunks per row of B's stage
+  typedef typename H::v8 v8;
+  // two stages, as separate arrays: copies into one are then known not to touch the other
+  __shared__ __attribute__((aligned(16))) uint8_t sa0[kABytes];
+  __shared__ __attribute__((aligned(16))) uint8_t sb0[kBBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t sa1[kABytes];
+  __shared__ __attribute__((aligned(16))) uint8_t sb1[kBBytes];
+
+  int32_t e, lo, hi, m0, col;
+  if (!find_tile<kRows>(p.offsets, p.T, p.E, ncols, static_cast<int32_t>(blockIdx.x), e, lo, hi, m0, col)) return;
+  const int32_t n0 = col * kCols;
+  const int t = threadIdx.x, lane = t & 63, w = t >> 6, wm = w >> 1, wn = w & 1;
+  const int32_t N = p.N, K = p.K;
+  const int32_t nb = (N + kB - 1) / kB, kb = (K + kB - 1) / kB;
+
+  // This thread's 16-byte chunks of a stage, positions id = t + 256 j of the LDS tile.
+  // Their addresses are a base that is the same for the workgroup and moves with k,
+  // plus a 32-bit offset that stays; rows past the end repeat the last one.
+  uint32_t aoff[4], boff[kBC];
+  int32_t ac[4], bn[kBC], br[kBC];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int id = t + kThreads * j, r = id >> 3;
+    ac[j] = ((id & 7) ^ swizzle_a(r)) * 16;
+    aoff[j] = static_cast<uint32_t>(min(r, hi - 1 - m0)) * static_cast<uint32_t>(K) * 2 + ac[j];
+  }
+#pragma unroll
+  for (int j = 0; j < kBC; ++j) {
+    const int id = t + kThreads * j, r = id / kBPer;
+    if (kTrans) {
+      const int c = ((id % kBPer) ^ swizzle_t<kB2>(r)) * 16;
+      br[j] = r;
+      bn[j] = N - n0 - c;  // bytes of the chunk inside the row
+      // (direct copies: a chunk past the row, whose columns are not stored, is another's)
+      boff[j] = static_cast<uint32_t>(r) * static_cast<uint32_t>(N) + (DIRECT && bn[j] <= 0 ? 0 : c);
+    } else {
+      const int c = ((id & 3) ^ swizzle_b(r)) * 16;
+      br[j] = 0;
+      bn[j] = c;
+      boff[j] = static_cast<uint32_t>(min(kUp ? r % (kB2 / 2) : r, N - 1 - n0)) * static_cast<uint32_t>(K) + c;
+    }
+  }
+  const int64_t abase = static_cast<int64_t>(m0) * K * 2;
+  const int64_t bbase = static_cast<int64_t>(e) * N * K + (kTrans ? n0 : static_cast<int64_t>(n0) * K);
+
+  uint4 ra[4], rb[kBC];
+  // k0: first k of the stage within its product `seg`
+  auto fetch = [&](int seg, int32_t k0, uint8_t* sa, uint8_t* sb) {
+    const uint8_t* const x = (seg ? p.x1 : p.x0) + abase + 2 * static_cast<int64_t>(k0);
+    const int64_t kw = kTrans ? static_cast<int64_t>(k0) * N : k0;
+    const uint8_t* const wa = (seg ? p.w1 : p.w0) + bbase + kw;
+    const uint8_t* const wb = kUp ? p.w1 + bbase + kw : wa;  // upper half of the stage's rows
+    if (DIRECT) {  // k ends with a stage
+      const buffer_t xb = make_buffer(x, static_cast<int64_t>(p.T - m0) * K * 2 - 2 * static_cast<int64_t>(k0));
+      const int64_t left = static_cast<int64_t>(p.E) * N * K - bbase - kw;
+      const buffer_t ba = make_buffer(wa, left), bb = make_buffer(wb, left);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) copy16_to_lds(xb, aoff[j], sa + (w * 64 + kThreads * j) * 16);
+#pragma unroll
+      for (int j = 0; j < kBC; ++j)
+        copy16_to_lds(j < kBC / 2 ? ba : bb, boff[j], sb + (w * 64 + kThreads * j) * 16);
+      return;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) ra[j] = ld16_part(x + aoff[j], (K - k0) * 2 - ac[j]);
+#pragma unroll
+    for (int j = 0; j < kBC; ++j)
+      rb[j] = ld16_part((j < kBC / 2 ? wa : wb) + boff[j], kTrans ? (k0 + br[j] < K ? bn[j] : 0) : K - k0 - bn[j]);
+  };
+  auto put = [&](uint8_t* sa, uint8_t* sb) {
+    if (DIRECT) return;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(sa + (t + kThreads * j) * 16) = ra[j];
+#pragma unroll
+    for (int j = 0; j < kBC; ++j) *reinterpret_cast<uint4*>(sb + (t + kThreads * j) * 16) = rb[j];
+  };
+
+  const f32x16 zero = {};
+  const int half = lane >> 5, l32 = lane & 31, l16 = lane & 15, grp = lane >> 4;
+  // d[i][j - j0] += A tile i times B tile j, over one stage.  All LDS reads of the stage
+  // are issued before its matrix instructions, which then wait for them one by one.
+  auto compute = [&](const uint8_t* sa, const uint8_t* sb, auto& d, auto j0_, auto nj_) {
+    constexpr int j0 = decltype(j0_)::value, nj = decltype(nj_)::value;
+    uint4 a[4][2];
+    uint2 b[4][nj];
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = wm * 64 + i * 32 + l32;
+        // k of this lane: plain order where B is read transposed; otherwise the lane's
+        // 16 consecutive k of a 32-wide group, 8 per step, as B's 16-byte chunk holds them
+        const int c = kTrans ? ks * 2 + half : (ks >> 1) * 4 + half * 2 + (ks & 1);
+        a[ks][i] = *reinterpret_cast<const uint4*>(sa + r * 128 + ((c ^ swizzle_a(r)) << 4));
+      }
+#pragma unroll
+      for (int jj = 0; jj < nj; ++jj) {
+        const int j = j0 + jj;
+        if (kTrans) {
+          const int r = ks * 16 + (grp >> 1) * 8 + (l16 >> 1);
+          const int c = (wn * NT + j) * 2 + (grp & 1);
+          const i32x2 q = read_tr8(sb + r * kB2 + ((c ^ swizzle_t<kB2>(r)) << 4) + (l16 & 1) * 8);
+          b[ks][jj] = make_uint2(q.x, q.y);
+        } else if (ks % 2 == 0) {
+          // gate tiles first, then the up tiles of the same columns
+          const int r = kUp ? (j / (NT / 2)) * (kB2 / 2) + (wn * (NT / 2) + j % (NT / 2)) * 32 + l32
+                            : (wn * NT + j) * 32 + l32;
+          const int c = ks + half;
+          const uint4 q = *reinterpret_cast<const uint4*>(sb + r * 64 + ((c ^ swizzle_b(r)) << 4));
+          b[ks][jj] = make_uint2(q.x, q.y);
+          b[ks + 1][jj] = make_uint2(q.z, q.w);
+        }
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    v8 bw = widen8<H>(b[0][0].x, b[0][0].y);
+#pragma unroll
+    for (int s = 0; s < 4 * nj; ++s) {
+      const int ks = s / nj, jj = s % nj, sn = s + 1 < 4 * nj ? s + 1 : s;
+      const v8 bn = widen8<H>(b[sn / nj][sn % nj].x, b[sn / nj][sn % nj].y);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) d[i][jj] = H::mma32(as_v8<H>(a[ks][i]), bw, d[i][jj]);
+      bw = bn;
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  // the scales of this wave's columns: one per block of k (two matrices: one each)
+  const int32_t nblk = min((n0 + (kUp ? 0 : wn * NT * 32)) / kB, nb - 1);
+  const int32_t sstride = kTrans ? nb : 1;
+  const int64_t sat = kTrans ? static_cast<int64_t>(e) * kb * nb + nblk : (static_cast<int64_t>(e) * nb + nblk) * kb;
+  const float* const sp0 = p.s0 + sat;
+  const float* const sp1 = KIND == kFfnUpBwd || kUp ? p.s1 + sat : nullptr;
+  const int32_t blocks = kSeg * kb;  // scale blocks of k, each two stages
+  auto scale = [&](int32_t q, int which) {
+    const bool second = kSeg == 2 ? q >= kb : which == 1;
+    return (second ? sp1 : sp0)[static_cast<int64_t>(kSeg == 2 && second ? q - kb : q) * sstride];
+  };
+
+  // One pass over k; `block(q)` runs after the two stages of scale block q.
+  auto sweep = [&](auto& d, auto j0_, auto nj_, auto before, auto after) {
+    fetch(0, 0, sa0, sb0);
+    put(sa0, sb0);
+    for (int32_t q = 0; q < blocks; ++q) {
+      before(q);
+      __syncthreads();
+      const int32_t kn = (kSeg == 2 && q >= kb ? q - kb : q) * kB + kStep;
+      const bool both = kn < K;  // the last block may end with its first stage
+      if (both) fetch(kSeg == 2 && q >= kb ? 1 : 0, kn, sa1, sb1);
+      compute(sa0, sb0, d, j0_, nj_);
+      if (both) put(sa1, sb1);
+      __syncthreads();
+      const int32_t qn = q + 1;
+      if (qn < blocks) fetch(kSeg == 2 && qn >= kb ? 1 : 0, (kSeg == 2 && qn >= kb ? qn - kb : qn) * kB, sa0, sb0);
+      if (both) compute(sa1, sb1, d, j0_, nj_);
+      if (qn < blocks) put(sa0, sb0);
+      after(q);
+    }
+    __syncthreads();  // the stages are written again by the next pass
+  };
+
+  // results of tile column j (for kFfnUp: gate columns x, up columns v)
+  auto emit = [&](const f32x16& x, const f32x16& v, int i, int j) {
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const int32_t m = m0 + wm * 64 + i * 32 + (r >> 2) * 8 + half * 4 + (r & 3);
+      const int32_t n = n0 + (wn * (kUp ? NT / 2 : NT) + j) * 32 + l32;
+      if (m >= hi || n >= N) continue;
+      const int64_t at = static_cast<int64_t>(m) * N + n;
+      if (kUp) {
+        p.o0[at] = H::from_f32(act_value(p.act, x[r]) * v[r]);
+        if (p.o1) {
+          p.o1[at] = H::from_f32(x[r]);
+          p.o2[at] = H::from_f32(v[r]);
+        }
+      } else if (KIND == kFfnDownBwd) {
+        const float h = H::to_f32(p.h[at]), u = H::to_f32(p.u[at]);
+        float f, slope;
+        act_both(p.act, h, f, slope);
+        p.o0[at] = H::from_f32(x[r] * u * slope);
+        p.o1[at] = H::from_f32(x[r] * f);
+        if (p.o2) p.o2[at] = H::from_f32(f * u);
+      } else {
+        p.o0[at] = H::from_f32(x[r]);
+      }
+    }
+  };
+
+  // all waves decide alike: the barriers are shared
+  float slo = 3e38f, shi = 0.0f;
+  bool ok = true;
+#pragma unroll
+  for (int b = 0; b < (kCols + kB - 1) / kB; ++b) {
+    const int64_t off = static_cast<int64_t>(min(n0 / kB + b, nb - 1) - nblk) * (kTrans ? 1 : kb);
+    ok = scales_close(sp0 + off, kb, sstride, slo, shi) && ok;
+    if (kUp || kSeg == 2) ok = scales_close(sp1 + off, kb, sstride, slo, shi) && ok;
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    slo = fminf(slo, __shfl_xor(slo, o));
+    shi = fmaxf(shi, __shfl_xor(shi, o));
+  }
+  ok = __all(ok) && shi * 0x1p-40f <= slo;
+
+  if (ok) {
+    f32x16 acc[2][NT];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) acc[i][j] = zero;
+    float was[2] = {scale(0, 0), kUp ? scale(0, 1) : 1.0f};
+    sweep(
+        acc, Int<0>{}, Int<NT>{}, [&](int32_t) {},
+        [&](int32_t q) {
+          if (q + 1 == blocks) return;
+          float ratio[2];
+#pragma unroll
+          for (int k = 0; k < (kUp ? 2 : 1); ++k) {
+            const float now = scale(q + 1, k);
+            ratio[k] = was[k] / now;
+            was[k] = now;
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+              for (int r = 0; r < 16; ++r) acc[i][j][r] *= ratio[kUp && j >= NT / 2 ? 1 : 0];
+        });
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] *= was[kUp && j >= NT / 2 ? 1 : 0];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < (kUp ? NT / 2 : NT); ++j) emit(acc[i][j], acc[i][kUp ? j + NT / 2 : j], i, j);
+  } else {
+    auto pass = [&](auto j_) {
+      constexpr int j = decltype(j_)::value;
+      f32x16 sum[2][1], part[2][1], up[2][1];
+#pragma unroll
+      for (int k = 0; k < (kUp ? 2 : 1); ++k) {
+        auto& d = k ? up : sum;
+        d[0][0] = d[1][0] = zero;
+        auto add = [&](int32_t q) {
+          const float s = scale(q, k);
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) d[i][0][r] = fmaf(s, part[i][0][r], d[i][0][r]);
+        };
+        auto clear = [&](int32_t) { part[0][0] = part[1][0] = zero; };
+        if (k)
+          sweep(part, Int<kUp ? j + NT / 2 : j>{}, Int<1>{}, clear, add);
+        else
+          sweep(part, Int<j>{}, Int<1>{}, clear, add);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) emit(sum[i][0], up[i][0], i, j);
+    };
+    pass(Int<0>{});
+    if constexpr (!kUp || NT == 4) pass(Int<1>{});
+    if constexpr (!kUp && NT == 4) {
+      pass(Int<2>{});
+      pass(Int<3>{});
+    }
+  }
+}
+
+// The most row tiles that T rows in E runs can make: every run may end in a partial tile.
+int64_t most_row_tiles(int64_t T, int64_t E) { return T / kRows + (T < E ? T : E); }
+
+template <class H, int KIND, int NT>
+void launch_tiles(const FfnArgs& p, bool direct, dim3 g, int32_t ncols, hipStream_t s) {
+  if (direct)
+    hipLaunchKernelGGL((ffn_tile_kernel<H, KIND, NT, true>), g, dim3(kThreads), 0, s, p, ncols);
+  else
+    hipLaunchKernelGGL((ffn_tile_kernel<H, KIND, NT, false>), g, dim3(kThreads), 0, s, p, ncols);
+}
+
+bool misaligned(const void* p, size_t a);
+
+template <int KIND>
+int launch(const FfnArgs& p, int32_t dtype, hipStream_t s, const char* what) {
+  if (p.T == 0) return FP8Z1_OK;
+  constexpr bool kTrans = KIND == kFfnDownBwd || KIND == kFfnUpBwd;
+  const bool direct = !misaligned(p.x0, 16) && !misaligned(p.x1, 16) && !misaligned(p.w0, 16) &&
+                      !misaligned(p.w1, 16) && p.K % kStep == 0 && (!kTrans || p.N % 16 == 0);
+  // Few rows per expert: the weights' read is what counts
+  if constexpr (!kTrans)
+    if (static_cast<int64_t>(p.T) <= 32ll * p.E) {
+      const bool aligned = !misaligned(p.x0, 16) && !misaligned(p.w0, 16) && !misaligned(p.w1, 16) && p.K % 16 == 0;
+      if (dtype == FP8Z1_BF16)
+        launch_rows<Bf16, KIND>(p, aligned, s);
+      else
+        launch_rows<F16, KIND>(p, aligned, s);
+      return check_hip(hipGetLastError(), what);
+    }
+  const int64_t rows = most_row_tiles(p.T, p.E);
+  const int32_t per = KIND == kFfnUp ? 32 : 64;  // columns per NT
+  const bool wide = rows * ((p.N + 4 * per - 1) / (4 * per)) >= 512;
+  const int32_t cols = per * (wide ? 4 : 2), ncols = (p.N + cols - 1) / cols;
+  const int64_t grid = rows * ncols;
+  if (grid > 0x7fffffff) return set_error(FP8Z1_ESHAPE, std::string(what) + ": too many tiles");
+  const dim3 g(static_cast<unsigned>(grid));
+  if (dtype == FP8Z1_BF16 && wide)
+    launch_tiles<Bf16, KIND, 4>(p, direct, g, ncols, s);
+  else if (dtype == FP8Z1_BF16)
+    launch_tiles<Bf16, KIND, 2>(p, direct, g, ncols, s);
+  else if (wide)
+    launch_tiles<F16, KIND, 4>(p, direct, g, ncols, s);
+  else
+    launch_tiles<F16, KIND, 2>(p, direct, g, ncols, s);
+  return check_hip(hipGetLastError(), what);
+}
+
+bool misaligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
+
+int check_cfg(const fp8z1_ffn* f, const int32_t* offsets, const char* what) {
+  const std::string w(what);
+  if (!f) return set_error(FP8Z1_EINVAL, w + ": NULL description");
+  if (f->dtype != FP8Z1_BF16 && f->dtype != FP8Z1_F16)
+    return set_error(FP8Z1_EINVAL, w + ": dtype must be FP8Z1_BF16 or FP8Z1_F16");
+  if (f->act != FP8Z1_ACT_SILU && f->act != FP8Z1_ACT_GELU)
+    return set_error(FP8Z1_EINVAL, w + ": act must be FP8Z1_ACT_SILU or FP8Z1_ACT_GELU");
+  if (f->T < 0 || f->T > FP8Z1_FFN_MAX_ROWS) return set_error(FP8Z1_ESHAPE, w + ": T outside 0 .. 2^30");
+  if (f->E < 1 || f->E > FP8Z1_FFN_MAX_EXPERTS) return set_error(FP8Z1_ESHAPE, w + ": E outside 1 .. 65535");
+  if (f->D < 1 || f->D > FP8Z1_FFN_MAX_WIDTH || f->F < 1 || f->F > FP8Z1_FFN_MAX_WIDTH)
+    return set_error(FP8Z1_ESHAPE, w + ": D and F must be 1 .. 2^20");
+  if (!offsets && f->E != 1) return set_error(FP8Z1_EINVAL, w + ": offsets may be NULL for one expert only");
+  if (misaligned(offsets, 4)) return set_error(FP8Z1_EINVAL, w + ": misaligned offsets");
+  return FP8Z1_OK;
+}
+
+int check_rows(std::initializer_list<const void*> xs, const char* what) {
+  for (const void* x : xs) {
+    if (!x) return set_error(FP8Z1_EINVAL, std::string(what) + ": NULL argument");
+    if (misaligned(x, 2)) return set_error(FP8Z1_EINVAL, std::string(what) + ": misaligned rows");
+  }
+  return FP8Z1_OK;
+}
+
+int check_weights(const uint8_t* codes, const float* scales, const char* what) {
+  if (!codes || !scales) return set_error(FP8Z1_EINVAL, std::string(what) + ": NULL weights");
+  if (misaligned(scales, 4)) return set_error(FP8Z1_EINVAL, std::string(what) + ": misaligned scales");
+  return FP8Z1_OK;
+}
+
+FfnArgs base_args(const fp8z1_ffn* f, const int32_t* offsets, bool n_is_f) {
+  FfnArgs p{};
+  p.offsets = offsets;
+  p.T = static_cast<int32_t>(f->T);
+  p.E = static_cast<int32_t>(f->E);
+  p.N = static_cast<int32_t>(n_is_f ? f->F : f->D);
+  p.K = static_cast<int32_t>(n_is_f ? f->D : f->F);
+  p.act = f->act;
+  return p;
+}
+
+const uint8_t* bytes(const void* p) { return static_cast<const uint8_t*>(p); }
+
+}  // namespace
+}  // namespace fp8z1

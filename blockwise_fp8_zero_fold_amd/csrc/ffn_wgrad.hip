@@ -53,7 +53,7 @@ __global__ __launch_bounds__(kThreads, 2) void ffn_wgrad_kernel(WgradArgs g) {
   int32_t pn[4], qn[4], row[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const int ch = t + kThreads * j, r = ch >> 4, c = ((ch & 15) ^ ((r & 3) << 1)) * 8;
+    const int ch = t + kThreads * j, r = ch >> 4, c = ((ch & 15) ^ ((r & 3) << 2)) * 8;
     row[j] = r;
     poff[j] = (static_cast<int64_t>(lo + r) * g.M + m0 + c) * 2;
     qoff[j] = (static_cast<int64_t>(lo + r) * g.N + n0 + c) * 2;
@@ -81,7 +81,7 @@ __global__ __launch_bounds__(kThreads, 2) void ffn_wgrad_kernel(WgradArgs g) {
   auto operand = [&](const uint8_t* s, int col0, int ks) {
     const int r = ks * 16 + (grp >> 1) * 8 + (l16 >> 2);
     const int c = col0 / 8 + (grp & 1) * 2 + ((l16 & 3) >> 1);
-    const uint8_t* at = s + r * 256 + ((c ^ ((r & 3) << 1)) << 4) + (l16 & 1) * 8;
+    const uint8_t* at = s + r * 256 + ((c ^ ((r & 3) << 2)) << 4) + (l16 & 1) * 8;
     const i32x2 a = read_tr16(at), b = read_tr16(at + 4 * 256);
     return as_v8<H>(make_uint4(a.x, a.y, b.x, b.y));
   };

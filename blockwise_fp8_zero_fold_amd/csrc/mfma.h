@@ -99,11 +99,18 @@ __device__ __forceinline__ uint4 ld16_part(const uint8_t* p, int n) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// A wave's direct copy of 64 x 16 bytes from global memory (any 16-byte aligned
-// address per lane) to 1 KB of LDS: lane l's bytes land at dst + 16 l.
-__device__ __forceinline__ void copy16_to_lds(const uint8_t* src, uint8_t* dst) {
-  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(src),
-                                   (__attribute__((address_space(3))) void*)(dst), 16, 0, 0);
+// A wave's direct copy of 64 x 16 bytes from global memory to 1 KB of LDS: lane l's bytes,
+// at `off` bytes (16-byte aligned, its own for each lane) behind the buffer's base,
+// land at dst + 16 l.  The buffer is `size` bytes long at most; base and size are the
+// same for the wave, so the only vector register that an address takes is the offset.
+typedef __amdgpu_buffer_rsrc_t buffer_t;
+__device__ __forceinline__ buffer_t make_buffer(const uint8_t* base, int64_t size) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0,
+                                           static_cast<int>(size < 0x7fffffff ? size : 0x7fffffff), 0x00027000);
+}
+__device__ __forceinline__ void copy16_to_lds(buffer_t b, uint32_t off, uint8_t* dst) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (__attribute__((address_space(3))) void*)(dst), 16,
+                                           static_cast<int>(off), 0, 0, 0);
 }
 
 // Transposing reads, per group of 16 lanes.  16-bit: lane 4r + c names the 8 bytes
