@@ -124,10 +124,11 @@ _sig = {
     "fp8z1_state_write": (C.c_int, [_vp, C.POINTER(State), _vp]),
     "fp8z1_encode_e4m3": (C.c_int, [_vp, _vp, C.c_int64, _vp]),
     "fp8z1_dequantize": (C.c_int, [_vp, _vp, C.c_int64, C.c_int64, C.c_int64, C.c_int32, _vp, _vp]),
-    "fp8z1_ffn_up": (C.c_int, [C.POINTER(Ffn), *[_vp] * 10]),
-    "fp8z1_ffn_down": (C.c_int, [C.POINTER(Ffn), *[_vp] * 6]),
-    "fp8z1_ffn_down_bwd": (C.c_int, [C.POINTER(Ffn), *[_vp] * 10]),
-    "fp8z1_ffn_up_bwd": (C.c_int, [C.POINTER(Ffn), *[_vp] * 9]),
+    "fp8z1_ffn_workspace_bytes": (C.c_int, [C.POINTER(Ffn), C.POINTER(C.c_size_t)]),
+    "fp8z1_ffn_up": (C.c_int, [C.POINTER(Ffn), *[_vp] * 10, C.c_size_t, _vp]),
+    "fp8z1_ffn_down": (C.c_int, [C.POINTER(Ffn), *[_vp] * 6, C.c_size_t, _vp]),
+    "fp8z1_ffn_down_bwd": (C.c_int, [C.POINTER(Ffn), *[_vp] * 10, C.c_size_t, _vp]),
+    "fp8z1_ffn_up_bwd": (C.c_int, [C.POINTER(Ffn), *[_vp] * 9, C.c_size_t, _vp]),
     "fp8z1_ffn_wgrad_workspace_bytes": (C.c_int, [*[C.c_int64] * 4, C.POINTER(C.c_size_t)]),
     "fp8z1_ffn_wgrad": (C.c_int, [*[C.c_int64] * 4, C.c_int32, _vp, _vp, _vp, C.c_int32, _vp, C.c_int32, _vp,
                                   C.c_size_t, _vp]),
@@ -165,6 +166,12 @@ def _stream(stream) -> Optional[int]:
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _current_stream(device: int) -> int:
+    """torch's current stream of a device, as an address (without building a Stream object, which
+    takes 3 us of a small call)."""
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 def _ptr_list(xs: Sequence) -> C.Array:
@@ -413,40 +420,67 @@ def _need_offsets(offsets, n: int, what: str) -> None:
         _need(offsets, 4 * (n + 1), f"{what} offsets", torch.int32)
 
 
-def fp8z1_ffn_up(f: Ffn, x, gate_codes, gate_scales, up_codes, up_scales, offsets, h, u, a, stream=None) -> None:
+def fp8z1_ffn_workspace_bytes(f: Ffn) -> int:
+    n = C.c_size_t()
+    _check(lib.fp8z1_ffn_workspace_bytes(C.byref(f), C.byref(n)), "fp8z1_ffn_workspace_bytes")
+    return n.value
+
+
+def _workspace(workspace, workspace_bytes: int, what: str) -> int:
+    """The workspace's size: as given (a tensor must hold it), or a tensor's own."""
+    if workspace is None:
+        return 0
+    if not workspace_bytes and _is_tensor(workspace):
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    _need(workspace, workspace_bytes, f"{what} workspace")
+    return workspace_bytes
+
+
+def fp8z1_ffn_up(f: Ffn, x, gate_codes, gate_scales, up_codes, up_scales, offsets, h, u, a, workspace=None,
+                 workspace_bytes: int = 0, stream=None) -> None:
     """a = act(x Wg^T) * (x Wu^T); h and u keep the projections (both or neither None)."""
+    workspace_bytes = _workspace(workspace, workspace_bytes, "ffn_up")
     _need_rows(f, "ffn_up", x=(x, f.D), h=(h, f.F), u=(u, f.F), a=(a, f.F))
     _need_weights(f, "ffn_up", f.F, f.D, (gate_codes, gate_scales), (up_codes, up_scales))
     _need_offsets(offsets, f.E, "ffn_up")
     _check(lib.fp8z1_ffn_up(C.byref(f), _ptr(x), _ptr(gate_codes), _ptr(gate_scales), _ptr(up_codes), _ptr(up_scales),
-                            _ptr(offsets), _ptr(h), _ptr(u), _ptr(a), _stream(stream)), "fp8z1_ffn_up")
+                            _ptr(offsets), _ptr(h), _ptr(u), _ptr(a), _ptr(workspace), workspace_bytes, _stream(stream)),
+           "fp8z1_ffn_up")
 
 
-def fp8z1_ffn_down(f: Ffn, a, down_codes, down_scales, offsets, y, stream=None) -> None:
+def fp8z1_ffn_down(f: Ffn, a, down_codes, down_scales, offsets, y, workspace=None, workspace_bytes: int = 0,
+                   stream=None) -> None:
     """y = a Wd^T."""
+    workspace_bytes = _workspace(workspace, workspace_bytes, "ffn_down")
     _need_rows(f, "ffn_down", a=(a, f.F), y=(y, f.D))
     _need_weights(f, "ffn_down", f.D, f.F, (down_codes, down_scales))
     _need_offsets(offsets, f.E, "ffn_down")
     _check(lib.fp8z1_ffn_down(C.byref(f), _ptr(a), _ptr(down_codes), _ptr(down_scales), _ptr(offsets), _ptr(y),
-                              _stream(stream)), "fp8z1_ffn_down")
+                              _ptr(workspace), workspace_bytes, _stream(stream)), "fp8z1_ffn_down")
 
 
-def fp8z1_ffn_down_bwd(f: Ffn, dy, down_codes, down_scales, h, u, offsets, dh, du, a=None, stream=None) -> None:
+def fp8z1_ffn_down_bwd(f: Ffn, dy, down_codes, down_scales, h, u, offsets, dh, du, a=None, workspace=None,
+                       workspace_bytes: int = 0, stream=None) -> None:
     """dh, du (and a again, unless None) from dy and the kept projections."""
+    workspace_bytes = _workspace(workspace, workspace_bytes, "ffn_down_bwd")
     _need_rows(f, "ffn_down_bwd", dy=(dy, f.D), h=(h, f.F), u=(u, f.F), dh=(dh, f.F), du=(du, f.F), a=(a, f.F))
     _need_weights(f, "ffn_down_bwd", f.D, f.F, (down_codes, down_scales))
     _need_offsets(offsets, f.E, "ffn_down_bwd")
     _check(lib.fp8z1_ffn_down_bwd(C.byref(f), _ptr(dy), _ptr(down_codes), _ptr(down_scales), _ptr(h), _ptr(u),
-                                  _ptr(offsets), _ptr(dh), _ptr(du), _ptr(a), _stream(stream)), "fp8z1_ffn_down_bwd")
+                                  _ptr(offsets), _ptr(dh), _ptr(du), _ptr(a), _ptr(workspace), workspace_bytes,
+                                  _stream(stream)), "fp8z1_ffn_down_bwd")
 
 
-def fp8z1_ffn_up_bwd(f: Ffn, dh, du, gate_codes, gate_scales, up_codes, up_scales, offsets, dx, stream=None) -> None:
+def fp8z1_ffn_up_bwd(f: Ffn, dh, du, gate_codes, gate_scales, up_codes, up_scales, offsets, dx, workspace=None,
+                     workspace_bytes: int = 0, stream=None) -> None:
     """dx = dh Wg + du Wu."""
+    workspace_bytes = _workspace(workspace, workspace_bytes, "ffn_up_bwd")
     _need_rows(f, "ffn_up_bwd", dh=(dh, f.F), du=(du, f.F), dx=(dx, f.D))
     _need_weights(f, "ffn_up_bwd", f.F, f.D, (gate_codes, gate_scales), (up_codes, up_scales))
     _need_offsets(offsets, f.E, "ffn_up_bwd")
     _check(lib.fp8z1_ffn_up_bwd(C.byref(f), _ptr(dh), _ptr(du), _ptr(gate_codes), _ptr(gate_scales), _ptr(up_codes),
-                                _ptr(up_scales), _ptr(offsets), _ptr(dx), _stream(stream)), "fp8z1_ffn_up_bwd")
+                                _ptr(up_scales), _ptr(offsets), _ptr(dx), _ptr(workspace), workspace_bytes,
+                                _stream(stream)), "fp8z1_ffn_up_bwd")
 
 
 def fp8z1_ffn_wgrad_workspace_bytes(T: int, E: int, M: int, N: int) -> int:
@@ -458,8 +492,7 @@ def fp8z1_ffn_wgrad_workspace_bytes(T: int, E: int, M: int, N: int) -> int:
 def fp8z1_ffn_wgrad(T: int, E: int, M: int, N: int, dtype: int, p, q, offsets, dw_dtype: int, dw,
                     accumulate: bool = False, workspace=None, workspace_bytes: int = 0, stream=None) -> None:
     """dw [E,M,N] = per expert p^T q (added to dw with accumulate)."""
-    if workspace is not None and not workspace_bytes and _is_tensor(workspace):
-        workspace_bytes = workspace.numel() * workspace.element_size()
+    workspace_bytes = _workspace(workspace, workspace_bytes, "ffn_wgrad")
     dt = _torch_dtype(dtype)
     if p is not None:
         _need(p, T * M * 2, "ffn_wgrad p", dt)
@@ -467,8 +500,6 @@ def fp8z1_ffn_wgrad(T: int, E: int, M: int, N: int, dtype: int, p, q, offsets, d
         _need(q, T * N * 2, "ffn_wgrad q", dt)
     _need(dw, E * M * N * (4 if dw_dtype == F32 else 2), "ffn_wgrad dw", _torch_dtype(dw_dtype))
     _need_offsets(offsets, E, "ffn_wgrad")
-    if workspace is not None:
-        _need(workspace, workspace_bytes, "ffn_wgrad workspace")
     _check(lib.fp8z1_ffn_wgrad(T, E, M, N, dtype, _ptr(p), _ptr(q), _ptr(offsets), dw_dtype, _ptr(dw),
                                int(bool(accumulate)), _ptr(workspace), workspace_bytes, _stream(stream)),
            "fp8z1_ffn_wgrad")
@@ -508,11 +539,8 @@ def fp8z1_norm_join_bwd_workspace_bytes(f: Norm) -> int:
 def fp8z1_norm_join_bwd(f: Norm, dz, dn, y, z, w_post, gate, w_pre, dy, dres, dw_post, dgate, dw_pre, workspace=None,
                         workspace_bytes: int = 0, stream=None) -> None:
     """The join's gradients; outputs that are None are not computed."""
-    if workspace is not None and not workspace_bytes and _is_tensor(workspace):
-        workspace_bytes = workspace.numel() * workspace.element_size()
+    workspace_bytes = _workspace(workspace, workspace_bytes, "norm_join_bwd")
     _need_norm(f, "norm_join_bwd", (dn, y, dy), (dz, z, dres), (w_post, w_pre, dw_post, dw_pre), (gate, dgate))
-    if workspace is not None:
-        _need(workspace, workspace_bytes, "norm_join_bwd workspace")
     _check(lib.fp8z1_norm_join_bwd(C.byref(f), _ptr(dz), _ptr(dn), _ptr(y), _ptr(z), _ptr(w_post), _ptr(gate),
                                    _ptr(w_pre), _ptr(dy), _ptr(dres), _ptr(dw_post), _ptr(dgate), _ptr(dw_pre),
                                    _ptr(workspace), workspace_bytes, _stream(stream)), "fp8z1_norm_join_bwd")

@@ -28,73 +28,82 @@ Weight = Tuple[torch.Tensor, torch.Tensor]
 
 _ACT = {"silu": L.ACT_SILU, "gelu": L.ACT_GELU}
 _CODE = {torch.float32: L.F32, torch.bfloat16: L.BF16, torch.float16: L.F16}
+_HALF = (torch.bfloat16, torch.float16)
 
 
 def _fail(msg: str):
     raise L.Fp8z1Error(msg)
 
 
-def _code(x: torch.Tensor, what: str, allowed=(torch.bfloat16, torch.float16)) -> int:
-    if x.dtype not in allowed:
-        _fail(f"{what}: dtype {x.dtype}, expected one of {', '.join(map(str, allowed))}")
-    return _CODE[x.dtype]
+def _device(x: torch.Tensor, what: str) -> int:
+    """The current device's index; the library launches there, on torch's current stream."""
+    dev = x.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        _fail(f"{what}: tensors must be on the current device, not {x.device}")
+    return dev
 
 
-def _same_device(first: torch.Tensor, *xs) -> None:
-    """All on the current device: the library launches there, on torch's current stream."""
-    if not first.is_cuda or first.device.index != torch.cuda.current_device():
-        _fail(f"tensors must be on the current device, not {first.device}")
-    for x in xs:
-        if x is not None and x.device != first.device:
-            _fail(f"tensors on {first.device} and {x.device}")
+def _check(x: torch.Tensor, dev: int, dtype: torch.dtype, shape: Sequence[int], what: str) -> int:
+    """The address of a contiguous tensor of this type and shape on this device."""
+    if x.shape != shape:
+        _fail(f"{what}: shape {tuple(x.shape)}, expected {tuple(shape)}")
+    if x.dtype != dtype:
+        _fail(f"{what}: dtype {x.dtype}, expected {dtype}")
+    if x.get_device() != dev or not x.is_contiguous():
+        _fail(f"{what}: must be a contiguous tensor on device {dev}")
+    return x.data_ptr()
 
 
-def _rows(x: torch.Tensor, width: int, T: int, what: str) -> None:
-    if tuple(x.shape) != (T, width):
-        _fail(f"{what}: shape {tuple(x.shape)}, expected {(T, width)}")
+def _weight(w: Weight, dev: int, e: int, r: int, c: int, what: str) -> Tuple[int, int]:
+    return (_check(w[0], dev, torch.uint8, (e, r, c), what),
+            _check(w[1], dev, torch.float32, (e, -(-r // 128), -(-c // 128)), what))
 
 
-def _weight(w: Weight, shape: Sequence[int], what: str) -> None:
-    codes, scales = w
-    e, r, c = shape
-    if tuple(codes.shape) != (e, r, c):
-        _fail(f"{what}: codes {tuple(codes.shape)}, expected {(e, r, c)}")
-    if tuple(scales.shape) != (e, -(-r // 128), -(-c // 128)):
-        _fail(f"{what}: scales {tuple(scales.shape)}, expected {(e, -(-r // 128), -(-c // 128))}")
-
-
-def _offsets(offsets: Optional[torch.Tensor], E: int) -> None:
+def _offsets(offsets: Optional[torch.Tensor], dev: int, E: int, what: str) -> Optional[int]:
     if offsets is None:
         if E != 1:
-            _fail(f"{E} experts need offsets")
-    elif tuple(offsets.shape) != (E + 1,):
-        _fail(f"offsets: shape {tuple(offsets.shape)}, expected {(E + 1,)}")
+            _fail(f"{what}: {E} experts need offsets")
+        return None
+    return _check(offsets, dev, torch.int32, (E + 1,), f"{what} offsets")
 
 
-def _ffn(x: torch.Tensor, w_gate: Weight, w_up: Weight, w_down: Weight, offsets, act: str, what: str) -> L.Ffn:
+def _ffn(x: torch.Tensor, w_gate: Weight, act: str, what: str):
+    """Device, sizes and their description for the calls; x [T, D], gate codes [E, F, D]."""
     if x.dim() != 2 or w_gate[0].dim() != 3:
         _fail(f"{what}: rows must be [T, D] and codes [E, F, D]")
+    if x.dtype not in _HALF:
+        _fail(f"{what}: dtype {x.dtype}, expected torch.bfloat16 or torch.float16")
     if act not in _ACT:
         _fail(f"{what}: act {act!r}, expected one of {', '.join(_ACT)}")
     T, D = x.shape
-    E, F = w_gate[0].shape[:2]
-    _weight(w_gate, (E, F, D), f"{what} gate")
-    _weight(w_up, (E, F, D), f"{what} up")
-    _weight(w_down, (E, D, F), f"{what} down")
-    _offsets(offsets, E)
-    _same_device(x, *w_gate, *w_up, *w_down, offsets)
-    return L.Ffn(T, E, D, F, _code(x, what), _ACT[act])
+    E, F, _ = w_gate[0].shape
+    return _device(x, what), T, D, E, F, L.Ffn(T, E, D, F, _CODE[x.dtype], _ACT[act])
+
+
+def _empty(like: torch.Tensor, *shape: int) -> torch.Tensor:
+    return like.new_empty(shape)
+
+
+def _scratch(like: torch.Tensor, nbytes: int) -> Optional[torch.Tensor]:
+    return like.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
 
 
 def ffn_forward(x: torch.Tensor, w_gate: Weight, w_up: Weight, w_down: Weight,
                 offsets: Optional[torch.Tensor] = None, act: str = "silu", save: bool = False):
     """y [T,D] = (act(x Wg^T) * (x Wu^T)) Wd^T.  Returns (y, (h, u, a)) with ``save``, else (y, None)."""
-    f = _ffn(x, w_gate, w_up, w_down, offsets, act, "ffn_forward")
-    a = x.new_empty(f.T, f.F)
-    h, u = (torch.empty_like(a), torch.empty_like(a)) if save else (None, None)
-    y = torch.empty_like(x, memory_format=torch.contiguous_format)
-    L.fp8z1_ffn_up(f, x, *w_gate, *w_up, offsets, h, u, a)
-    L.fp8z1_ffn_down(f, a, *w_down, offsets, y)
+    what = "ffn_forward"
+    dev, T, D, E, F, f = _ffn(x, w_gate, act, what)
+    px = _check(x, dev, x.dtype, (T, D), what)
+    gate, up, down = (_weight(w_gate, dev, E, F, D, "ffn_forward gate"), _weight(w_up, dev, E, F, D, "ffn_forward up"),
+                      _weight(w_down, dev, E, D, F, "ffn_forward down"))
+    off = _offsets(offsets, dev, E, what)
+    a, y = _empty(x, T, F), _empty(x, T, D)
+    h, u = (_empty(x, T, F), _empty(x, T, F)) if save else (None, None)
+    n = L.fp8z1_ffn_workspace_bytes(f)
+    ws = _scratch(x, n)
+    pw, pa, stream = L._ptr(ws), a.data_ptr(), L._current_stream(dev)
+    L._check(L.lib.fp8z1_ffn_up(f, px, *gate, *up, off, L._ptr(h), L._ptr(u), pa, pw, n, stream), what)
+    L._check(L.lib.fp8z1_ffn_down(f, pa, *down, off, y.data_ptr(), pw, n, stream), what)
     return y, ((h, u, a) if save else None)
 
 
@@ -102,14 +111,19 @@ def ffn_backward_data(dy: torch.Tensor, h: torch.Tensor, u: torch.Tensor, w_gate
                       w_down: Weight, offsets: Optional[torch.Tensor] = None, act: str = "silu"):
     """(dx, dh, du, a): the gradients at the block's input and its projections, and a again
     (what the weight gradients need)."""
-    f = _ffn(dy, w_gate, w_up, w_down, offsets, act, "ffn_backward_data")
-    _rows(h, f.F, f.T, "h")
-    _rows(u, f.F, f.T, "u")
-    _same_device(dy, h, u)
-    dh, du, a = (torch.empty_like(h, memory_format=torch.contiguous_format) for _ in range(3))
-    dx = torch.empty_like(dy, memory_format=torch.contiguous_format)
-    L.fp8z1_ffn_down_bwd(f, dy, *w_down, h, u, offsets, dh, du, a)
-    L.fp8z1_ffn_up_bwd(f, dh, du, *w_gate, *w_up, offsets, dx)
+    what = "ffn_backward_data"
+    dev, T, D, E, F, f = _ffn(dy, w_gate, act, what)
+    py = _check(dy, dev, dy.dtype, (T, D), what)
+    ph, pu = (_check(v, dev, dy.dtype, (T, F), f"{what} projections") for v in (h, u))
+    gate, up, down = (_weight(w_gate, dev, E, F, D, f"{what} gate"), _weight(w_up, dev, E, F, D, f"{what} up"),
+                      _weight(w_down, dev, E, D, F, f"{what} down"))
+    off = _offsets(offsets, dev, E, what)
+    dh, du, a, dx = _empty(dy, T, F), _empty(dy, T, F), _empty(dy, T, F), _empty(dy, T, D)
+    n = L.fp8z1_ffn_workspace_bytes(f)
+    ws = _scratch(dy, n)
+    pw, pdh, pdu, stream = L._ptr(ws), dh.data_ptr(), du.data_ptr(), L._current_stream(dev)
+    L._check(L.lib.fp8z1_ffn_down_bwd(f, py, *down, ph, pu, off, pdh, pdu, a.data_ptr(), pw, n, stream), what)
+    L._check(L.lib.fp8z1_ffn_up_bwd(f, pdh, pdu, *gate, *up, off, dx.data_ptr(), pw, n, stream), what)
     return dx, dh, du, a
 
 
@@ -117,23 +131,23 @@ def ffn_weight_gradient(p: torch.Tensor, q: torch.Tensor, n_experts: int = 1,
                         offsets: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.float32,
                         out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """[E,M,N] = per expert p^T q over its rows.  Given ``out`` (float32), the products are added to it."""
-    if p.dim() != 2 or q.dim() != 2 or p.shape[0] != q.shape[0] or p.dtype != q.dtype:
-        _fail("ffn_weight_gradient: p and q must be [T, M] and [T, N] of one type")
-    (T, M), N = p.shape, q.shape[1]
-    _offsets(offsets, n_experts)
-    _same_device(p, q, offsets, out)
+    what = "ffn_weight_gradient"
+    if p.dim() != 2 or q.dim() != 2 or p.dtype not in _HALF:
+        _fail(f"{what}: p and q must be [T, M] and [T, N] of torch.bfloat16 or torch.float16")
+    dev, (T, M), N = _device(p, what), p.shape, q.shape[1]
+    pp, pq = _check(p, dev, p.dtype, (T, M), what), _check(q, dev, p.dtype, (T, N), what)
+    off = _offsets(offsets, dev, n_experts, what)
     if dtype not in (torch.float32, torch.bfloat16):
-        _fail(f"ffn_weight_gradient: dtype {dtype}, expected torch.float32 or torch.bfloat16")
+        _fail(f"{what}: dtype {dtype}, expected torch.float32 or torch.bfloat16")
     if out is None:
-        dw = p.new_empty(n_experts, M, N, dtype=dtype)
+        dw = p.new_empty((n_experts, M, N), dtype=dtype)
     else:
         dw = out
-        if tuple(dw.shape) != (n_experts, M, N) or dw.dtype != torch.float32:
-            _fail(f"ffn_weight_gradient: out must be float32 {(n_experts, M, N)}")
-    need = L.fp8z1_ffn_wgrad_workspace_bytes(T, n_experts, M, N)
-    ws = p.new_empty(need, dtype=torch.uint8) if need else None
-    L.fp8z1_ffn_wgrad(T, n_experts, M, N, _code(p, "ffn_weight_gradient"), p, q, offsets, _CODE[dw.dtype], dw,
-                      accumulate=out is not None, workspace=ws)
+        _check(dw, dev, torch.float32, (n_experts, M, N), f"{what} out")
+    n = L.fp8z1_ffn_wgrad_workspace_bytes(T, n_experts, M, N)
+    ws = _scratch(p, n)
+    L._check(L.lib.fp8z1_ffn_wgrad(T, n_experts, M, N, _CODE[p.dtype], pp, pq, off, _CODE[dw.dtype], dw.data_ptr(),
+                                   int(out is not None), L._ptr(ws), n, L._current_stream(dev)), what)
     return dw
 
 
@@ -161,13 +175,18 @@ def _gate_kind(gate: Optional[torch.Tensor], T: int, C: int) -> int:
     return L.GATE_CHANNEL
 
 
-def _norm(rows: torch.Tensor, res: torch.Tensor, gate, eps, res_scale, block_scale, weight_offset, what) -> L.Norm:
-    if rows.dim() != 2 or res.shape != rows.shape:
-        _fail(f"{what}: rows must be [T, C], all of one shape")
-    T, C = rows.shape
-    dt = _code(rows, what, (torch.float32, torch.bfloat16, torch.float16))
-    rt = _code(res, what, (torch.float32, rows.dtype))
-    return L.Norm(T, C, dt, rt, _gate_kind(gate, T, C), eps, res_scale, block_scale, weight_offset, 0)
+def _norm(rows_dtype: torch.dtype, res: torch.Tensor, w_post, gate, w_pre, settings, what: str):
+    """Device, sizes, description, and the addresses of the weights and the gate."""
+    if res.dim() != 2:
+        _fail(f"{what}: rows must be [T, C]")
+    if rows_dtype not in _CODE or res.dtype not in (rows_dtype, torch.float32):
+        _fail(f"{what}: rows of {rows_dtype} with a residual of {res.dtype}")
+    T, C = res.shape
+    dev, kind = _device(res, what), _gate_kind(gate, T, C)
+    wpost, wpre = (None if w is None else _check(w, dev, torch.float32, (C,), f"{what} weight") for w in (w_post, w_pre))
+    pg = None if gate is None else _check(gate, dev, rows_dtype if kind == L.GATE_FULL else torch.float32, gate.shape,
+                                          f"{what} gate")
+    return dev, T, C, L.Norm(T, C, _CODE[rows_dtype], _CODE[res.dtype], kind, *settings, 0), wpost, pg, wpre
 
 
 def norm_join(y: Optional[torch.Tensor], res: torch.Tensor, w_post: Optional[torch.Tensor] = None,
@@ -177,12 +196,14 @@ def norm_join(y: Optional[torch.Tensor], res: torch.Tensor, w_post: Optional[tor
     """(z, n): z = res_scale res + block_scale gate norm(y), n = norm(z) (see fp8z1_norm_join).
     The gate is [C] (per channel), [T,1] (per token) or [T,C].
     ``dtype``: type of n where there is no block output y (default: that of res)."""
-    n = torch.empty_like(y, memory_format=torch.contiguous_format) if y is not None else torch.empty_like(
-        res, dtype=dtype or res.dtype, memory_format=torch.contiguous_format)
-    z = torch.empty_like(res, memory_format=torch.contiguous_format)
-    f = _norm(n, res, gate, eps, res_scale, block_scale, weight_offset, "norm_join")
-    _same_device(res, y, w_post, gate, w_pre)
-    L.fp8z1_norm_join(f, y, res, w_post, gate, w_pre, z, n)
+    what = "norm_join"
+    rows = y.dtype if y is not None else dtype or res.dtype
+    dev, T, C, f, wpost, pg, wpre = _norm(rows, res, w_post, gate, w_pre, (eps, res_scale, block_scale, weight_offset),
+                                          what)
+    py = None if y is None else _check(y, dev, rows, (T, C), what)
+    pr = _check(res, dev, res.dtype, (T, C), what)
+    z, n = res.new_empty((T, C)), res.new_empty((T, C), dtype=rows)
+    L._check(L.lib.fp8z1_norm_join(f, py, pr, wpost, pg, wpre, z.data_ptr(), n.data_ptr(), L._current_stream(dev)), what)
     return z, n
 
 
@@ -191,16 +212,22 @@ def norm_join_backward(dz: Optional[torch.Tensor], dn: Optional[torch.Tensor], y
                        w_pre: Optional[torch.Tensor] = None, eps: float = 1e-6, res_scale: float = 1.0,
                        block_scale: float = 1.0, weight_offset: float = 0.0) -> Dict[str, Optional[torch.Tensor]]:
     """{"dy", "dres", "dw_post", "dgate", "dw_pre"} (None where the forward call had no such input)."""
-    rows = y if y is not None else dn if dn is not None else z
-    f = _norm(rows, z, gate, eps, res_scale, block_scale, weight_offset, "norm_join_backward")
-    _same_device(z, dz, dn, y, w_post, gate, w_pre)
-    contiguous = dict(memory_format=torch.contiguous_format)
+    what = "norm_join_backward"
+    rows = y.dtype if y is not None else dn.dtype if dn is not None else z.dtype
+    dev, T, C, f, wpost, pg, wpre = _norm(rows, z, w_post, gate, w_pre, (eps, res_scale, block_scale, weight_offset),
+                                          what)
+    pdz = None if dz is None else _check(dz, dev, z.dtype, (T, C), f"{what} dz")
+    pdn = None if dn is None else _check(dn, dev, rows, (T, C), f"{what} dn")
+    py = None if y is None else _check(y, dev, rows, (T, C), f"{what} y")
+    pz = _check(z, dev, z.dtype, (T, C), f"{what} z")
     out: Dict[str, Optional[torch.Tensor]] = {
-        "dy": torch.empty_like(y, **contiguous) if y is not None else None,
-        "dres": torch.empty_like(z, **contiguous),
-        "dw_post": torch.empty_like(w_post, **contiguous) if w_post is not None else None,
-        "dgate": torch.empty_like(gate, **contiguous) if gate is not None else None,
-        "dw_pre": torch.empty_like(w_pre, **contiguous) if w_pre is not None else None}
-    ws = z.new_empty(L.fp8z1_norm_join_bwd_workspace_bytes(f), dtype=torch.uint8)
-    L.fp8z1_norm_join_bwd(f, dz, dn, y, z, w_post, gate, w_pre, *out.values(), workspace=ws)
+        "dy": None if y is None else y.new_empty((T, C)),
+        "dres": z.new_empty((T, C)),
+        "dw_post": None if w_post is None else w_post.new_empty((C,)),
+        "dgate": None if gate is None else gate.new_empty(gate.shape),
+        "dw_pre": None if w_pre is None else w_pre.new_empty((C,))}
+    n = L.fp8z1_norm_join_bwd_workspace_bytes(f)
+    ws = _scratch(z, n)
+    L._check(L.lib.fp8z1_norm_join_bwd(f, pdz, pdn, py, pz, wpost, pg, wpre, *(L._ptr(v) for v in out.values()),
+                                       L._ptr(ws), n, L._current_stream(dev)), what)
     return out

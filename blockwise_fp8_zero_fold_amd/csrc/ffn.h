@@ -25,6 +25,7 @@ struct FfnArgs {
   const int32_t* offsets;  // [E + 1], or NULL: one expert, all rows
   const uint16_t *h, *u;   // [T, N] inputs of kFfnDownBwd
   uint16_t *o0, *o1, *o2;  // outputs [T, N]
+  float* part;             // partial sums of split tiles, or NULL: no tile is split
   int32_t T, E, N, K, act;
 };
 
@@ -45,49 +46,79 @@ __device__ __forceinline__ int32_t wave_isum(int32_t v) {
   return v;
 }
 
-// The tile (expert, its rows lo..hi, first row m0, tile column) of workgroup b, or
-// false if there is none: the number of row tiles depends on the offsets, which only
-// the device knows, so the grid holds the most there can be.  Consecutive workgroups
-// go to the XCDs in turn; each XCD gets a contiguous run of tiles, ordered in groups
-// of kGroup row tiles by all columns, so that the tiles running on one XCD at a time
-// share rows and weights in its L2.
-constexpr int kGroup = 8;
+// Work items of a launch.  The tiles (row tiles of all experts by tile columns) are counted on
+// the device, which alone knows the offsets; the grid holds the most there can be.
+// The card runs kSlots workgroups at once (two on each compute unit).  Where the tiles
+// past the last full round would leave most of it idle, they are split along k instead
+// (`splits` parts each, at least 8 scale blocks of k per part), the parts' float32 sums
+// go to the workspace and a second kernel adds them in order and finishes the tiles.
+constexpr int32_t kSlots = 512;
+
+struct Plan {
+  int32_t tiles;   // all tiles
+  int32_t whole;   // tiles done by one workgroup; the others by `splits`
+  int32_t splits;
+  __device__ int64_t items() const { return whole + static_cast<int64_t>(tiles - whole) * splits; }
+};
+
 template <int ROWS>
-__device__ __forceinline__ bool find_tile(const int32_t* offsets, int32_t T, int32_t E, int32_t ncols, int32_t b,
-                                          int32_t& e, int32_t& lo, int32_t& hi, int32_t& m0, int32_t& col) {
+__device__ __forceinline__ int32_t row_tiles(const int32_t* offsets, int32_t T, int32_t e) {
+  int32_t lo, hi;
+  expert_rows(offsets, T, e, lo, hi);
+  return (hi - lo + ROWS - 1) / ROWS;
+}
+
+template <int ROWS>
+__device__ __forceinline__ Plan plan_tiles(const int32_t* offsets, int32_t T, int32_t E, int32_t ncols,
+                                           int32_t blocks, bool may_split, int32_t& rowtiles) {
   const int lane = threadIdx.x & 63;
   int32_t total = 0;
   if (offsets) {
-    for (int32_t e0 = 0; e0 < E; e0 += 64) {
-      int32_t n = 0;
-      if (e0 + lane < E) {
-        int32_t l, h;
-        expert_rows(offsets, T, e0 + lane, l, h);
-        n = (h - l + ROWS - 1) / ROWS;
-      }
-      total += wave_isum(n);
-    }
+    for (int32_t e0 = 0; e0 < E; e0 += 64) total += wave_isum(e0 + lane < E ? row_tiles<ROWS>(offsets, T, e0 + lane) : 0);
   } else {
     total = (T + ROWS - 1) / ROWS;
   }
-  total = __builtin_amdgcn_readfirstlane(total);
-  const int64_t all = static_cast<int64_t>(total) * ncols;
-  if (b >= all) return false;
-  const int32_t g = static_cast<int32_t>(all), x = b % kXcds, per = g / kXcds, rem = g % kXcds;
-  const int32_t id = x * per + min(x, rem) + b / kXcds;
+  rowtiles = __builtin_amdgcn_readfirstlane(total);
+  Plan p;
+  // (offsets out of order can count rows twice: no more tiles than an int can number)
+  p.tiles = static_cast<int32_t>(min(static_cast<int64_t>(rowtiles) * ncols, static_cast<int64_t>(0x7fffffff)));
+  p.whole = p.tiles;
+  p.splits = 1;
+  const int32_t rest = p.tiles % kSlots;
+  if (may_split && rest) {
+    const int32_t s = min(kSlots / rest, blocks / 8);
+    if (s > 1) {
+      p.whole = p.tiles - rest;
+      p.splits = s;
+    }
+  }
+  return p;
+}
+
+// Consecutive workgroups go to the XCDs in turn; item b of n becomes a tile so that each
+// XCD gets a contiguous run of them.
+__device__ __forceinline__ int32_t xcd_run(int32_t b, int32_t n) {
+  const int32_t x = b % kXcds;
+  return x * (n / kXcds) + min(x, n % kXcds) + b / kXcds;
+}
+
+// Tile id -> expert, its rows lo..hi, first row m0 and tile column.  Tiles are ordered in
+// groups of kGroup row tiles by all columns, so that the tiles running on one XCD at a
+// time share rows and weights in its L2.
+constexpr int kGroup = 8;
+template <int ROWS>
+__device__ __forceinline__ bool find_tile(const int32_t* offsets, int32_t T, int32_t E, int32_t ncols, int32_t rowtiles,
+                                          int32_t id, int32_t& e, int32_t& lo, int32_t& hi, int32_t& m0,
+                                          int32_t& col) {
+  const int lane = threadIdx.x & 63;
   const int32_t grp = id / (kGroup * ncols), in = id - grp * kGroup * ncols;
-  const int32_t rows = min(kGroup, total - grp * kGroup);
+  const int32_t rows = min(kGroup, rowtiles - grp * kGroup);
   col = in / rows;
   int32_t mt = grp * kGroup + in - col * rows;
   e = 0;
   if (offsets) {
     for (int32_t e0 = 0; e0 < E; e0 += 64) {
-      int32_t n = 0;
-      if (e0 + lane < E) {
-        int32_t l, h;
-        expert_rows(offsets, T, e0 + lane, l, h);
-        n = (h - l + ROWS - 1) / ROWS;
-      }
+      const int32_t n = e0 + lane < E ? row_tiles<ROWS>(offsets, T, e0 + lane) : 0;
       int32_t upto = n;  // tiles of this chunk's experts up to and with this lane's
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) {

@@ -5,7 +5,7 @@ using namespace fp8z1;
 
 extern "C" int fp8z1_ffn_down_bwd(const fp8z1_ffn* f, const void* dy, const uint8_t* down_codes,
                                   const float* down_scales, const void* h, const void* u, const int32_t* offsets,
-                                  void* dh, void* du, void* a, void* stream) {
+                                  void* dh, void* du, void* a, void* d_workspace, size_t workspace_bytes, void* stream) {
   const char* what = "ffn_down_bwd";
   int rc = check_cfg(f, offsets, what);
   if (!rc && f->T) rc = check_rows({dy, h, u, dh, du}, what);
@@ -21,5 +21,6 @@ extern "C" int fp8z1_ffn_down_bwd(const fp8z1_ffn* f, const void* dy, const uint
   p.o0 = static_cast<uint16_t*>(dh);
   p.o1 = static_cast<uint16_t*>(du);
   p.o2 = static_cast<uint16_t*>(a);
-  return launch<kFfnDownBwd>(p, f->dtype, static_cast<hipStream_t>(stream), what);
+  return launch<kFfnDownBwd>(p, f->dtype, d_workspace, workspace_bytes, static_cast<hipStream_t>(stream),
+                       what);
 }

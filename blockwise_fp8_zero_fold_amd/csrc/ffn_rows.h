@@ -144,16 +144,16 @@ void launch_rows_as(const FfnArgs& p, bool aligned, dim3 g, hipStream_t s) {
     hipLaunchKernelGGL((ffn_rows_kernel<H, KIND, WAVES, TT, false>), g, dim3(WAVES * 64), 0, s, p);
 }
 
-// Few workgroups: 16 waves each, so that all of k is on its way at once; else 4.  Up to 16
+// Few workgroups: 8 waves each; else 4.  Up to 16
 // rows per expert on average: one matrix tile of rows at a time; else two.
 template <class H, int KIND>
 void launch_rows(const FfnArgs& p, bool aligned, hipStream_t s) {
   const dim3 g(static_cast<unsigned>((p.N + 15) / 16), static_cast<unsigned>(p.E));
   const bool deep = static_cast<int64_t>(g.x) * g.y < 512, two = static_cast<int64_t>(p.T) > 8ll * p.E;
   if (deep && two)
-    launch_rows_as<H, KIND, 16, 2>(p, aligned, g, s);
+    launch_rows_as<H, KIND, 8, 2>(p, aligned, g, s);
   else if (deep)
-    launch_rows_as<H, KIND, 16, 1>(p, aligned, g, s);
+    launch_rows_as<H, KIND, 8, 1>(p, aligned, g, s);
   else if (two)
     launch_rows_as<H, KIND, 4, 2>(p, aligned, g, s);
   else

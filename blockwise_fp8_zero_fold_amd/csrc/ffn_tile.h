@@ -24,6 +24,45 @@ constexpr int kRows = 128;  // tile rows
 constexpr int kStep = 64;   // k per LDS stage
 constexpr int kABytes = kRows * kStep * 2;
 
+// The results of 32 x 32 tile (i, j) of a wave: lane l holds column l % 32.
+template <class H, int KIND, int NT>
+__device__ __forceinline__ void store_tile(const FfnArgs& p, const f32x16& x, const f32x16& v, int32_t hi, int32_t m0,
+                                           int32_t n0, int i, int j) {
+  constexpr bool kUp = KIND == kFfnUp;
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, wm = w >> 1, wn = w & 1;
+  const int32_t n = n0 + (wn * (kUp ? NT / 2 : NT) + j) * 32 + (lane & 31);
+  if (n >= p.N) return;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    const int32_t m = m0 + wm * 64 + i * 32 + (r >> 2) * 8 + (lane >> 5) * 4 + (r & 3);
+    if (m >= hi) continue;
+    const int64_t at = static_cast<int64_t>(m) * p.N + n;
+    if (kUp) {
+      p.o0[at] = H::from_f32(act_value(p.act, x[r]) * v[r]);
+      if (p.o1) {
+        p.o1[at] = H::from_f32(x[r]);
+        p.o2[at] = H::from_f32(v[r]);
+      }
+    } else if (KIND == kFfnDownBwd) {
+      const float h = H::to_f32(p.h[at]), u = H::to_f32(p.u[at]);
+      float f, slope;
+      act_both(p.act, h, f, slope);
+      p.o0[at] = H::from_f32(x[r] * u * slope);
+      p.o1[at] = H::from_f32(x[r] * f);
+      if (p.o2) p.o2[at] = H::from_f32(f * u);
+    } else {
+      p.o0[at] = H::from_f32(x[r]);
+    }
+  }
+}
+
+// Part `at` of the split tiles in the workspace: the accumulators of all threads, float4 by
+// float4, so that each store of a wave is 1 KB in a row.
+template <int NT>
+__device__ __forceinline__ f32x4* part_at(float* part, int32_t at) {
+  return reinterpret_cast<f32x4*>(part) + static_cast<int64_t>(at) * (2 * NT * 4 * kThreads);
+}
+
 // Whether the block scales that a tile multiplies by are positive, finite and within a
 // factor 2^40 of each other.  Every wave looks at all of them, so all agree.
 __device__ __forceinline__ bool scales_close(const float* s, int32_t count, int32_t stride, float& lo, float& hi) {
@@ -76,12 +115,21 @@ __global__ __launch_bounds__(kThreads, 2) void ffn_tile_kernel(FfnArgs p, int32_
   __shared__ __attribute__((aligned(16))) uint8_t sa1[kABytes];
   __shared__ __attribute__((aligned(16))) uint8_t sb1[kBBytes];
 
-  int32_t e, lo, hi, m0, col;
-  if (!find_tile<kRows>(p.offsets, p.T, p.E, ncols, static_cast<int32_t>(blockIdx.x), e, lo, hi, m0, col)) return;
+  const int32_t kb = (p.K + kB - 1) / kB, blocks = kSeg * kb;  // scale blocks of k, each two stages
+  int32_t rowtiles, e, lo, hi, m0, col;
+  const int32_t item = static_cast<int32_t>(blockIdx.x);
+  const Plan plan = plan_tiles<kRows>(p.offsets, p.T, p.E, ncols, blocks, p.part != nullptr, rowtiles);
+  if (item >= plan.items()) return;
+  const bool split = item >= plan.whole;
+  const int32_t rest = plan.tiles - plan.whole;
+  const int32_t id = split ? plan.whole + (item - plan.whole) % rest : xcd_run(item, plan.whole);
+  const int32_t sp = split ? (item - plan.whole) / rest : 0, parts = split ? plan.splits : 1;
+  const int32_t q0 = blocks * sp / parts, q1 = blocks * (sp + 1) / parts;
+  if (!find_tile<kRows>(p.offsets, p.T, p.E, ncols, rowtiles, id, e, lo, hi, m0, col)) return;
   const int32_t n0 = col * kCols;
   const int t = threadIdx.x, lane = t & 63, w = t >> 6, wm = w >> 1, wn = w & 1;
   const int32_t N = p.N, K = p.K;
-  const int32_t nb = (N + kB - 1) / kB, kb = (K + kB - 1) / kB;
+  const int32_t nb = (N + kB - 1) / kB;
 
   // This thread's 16-byte chunks of a stage, positions id = t + 256 j of the LDS tile.
   // Their addresses are a base that is the same for the workgroup and moves with k,
@@ -201,17 +249,16 @@ __global__ __launch_bounds__(kThreads, 2) void ffn_tile_kernel(FfnArgs p, int32_
   const int64_t sat = kTrans ? static_cast<int64_t>(e) * kb * nb + nblk : (static_cast<int64_t>(e) * nb + nblk) * kb;
   const float* const sp0 = p.s0 + sat;
   const float* const sp1 = KIND == kFfnUpBwd || kUp ? p.s1 + sat : nullptr;
-  const int32_t blocks = kSeg * kb;  // scale blocks of k, each two stages
   auto scale = [&](int32_t q, int which) {
     const bool second = kSeg == 2 ? q >= kb : which == 1;
     return (second ? sp1 : sp0)[static_cast<int64_t>(kSeg == 2 && second ? q - kb : q) * sstride];
   };
 
-  // One pass over k; `block(q)` runs after the two stages of scale block q.
+  // One pass over this item's k; `after(q)` runs after the two stages of scale block q.
   auto sweep = [&](auto& d, auto j0_, auto nj_, auto before, auto after) {
-    fetch(0, 0, sa0, sb0);
+    fetch(kSeg == 2 && q0 >= kb ? 1 : 0, (kSeg == 2 && q0 >= kb ? q0 - kb : q0) * kB, sa0, sb0);
     put(sa0, sb0);
-    for (int32_t q = 0; q < blocks; ++q) {
+    for (int32_t q = q0; q < q1; ++q) {
       before(q);
       __syncthreads();
       const int32_t kn = (kSeg == 2 && q >= kb ? q - kb : q) * kB + kStep;
@@ -221,38 +268,26 @@ __global__ __launch_bounds__(kThreads, 2) void ffn_tile_kernel(FfnArgs p, int32_
       if (both) put(sa1, sb1);
       __syncthreads();
       const int32_t qn = q + 1;
-      if (qn < blocks) fetch(kSeg == 2 && qn >= kb ? 1 : 0, (kSeg == 2 && qn >= kb ? qn - kb : qn) * kB, sa0, sb0);
+      if (qn < q1) fetch(kSeg == 2 && qn >= kb ? 1 : 0, (kSeg == 2 && qn >= kb ? qn - kb : qn) * kB, sa0, sb0);
       if (both) compute(sa1, sb1, d, j0_, nj_);
-      if (qn < blocks) put(sa0, sb0);
+      if (qn < q1) put(sa0, sb0);
       after(q);
     }
     __syncthreads();  // the stages are written again by the next pass
   };
 
-  // results of tile column j (for kFfnUp: gate columns x, up columns v)
+  // a tile's results (for kFfnUp: gate columns x, up columns v), or a part's sums
   auto emit = [&](const f32x16& x, const f32x16& v, int i, int j) {
+    if (split) {
+      f32x4* const to = part_at<NT>(p.part, item - plan.whole);
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const int32_t m = m0 + wm * 64 + i * 32 + (r >> 2) * 8 + half * 4 + (r & 3);
-      const int32_t n = n0 + (wn * (kUp ? NT / 2 : NT) + j) * 32 + l32;
-      if (m >= hi || n >= N) continue;
-      const int64_t at = static_cast<int64_t>(m) * N + n;
-      if (kUp) {
-        p.o0[at] = H::from_f32(act_value(p.act, x[r]) * v[r]);
-        if (p.o1) {
-          p.o1[at] = H::from_f32(x[r]);
-          p.o2[at] = H::from_f32(v[r]);
-        }
-      } else if (KIND == kFfnDownBwd) {
-        const float h = H::to_f32(p.h[at]), u = H::to_f32(p.u[at]);
-        float f, slope;
-        act_both(p.act, h, f, slope);
-        p.o0[at] = H::from_f32(x[r] * u * slope);
-        p.o1[at] = H::from_f32(x[r] * f);
-        if (p.o2) p.o2[at] = H::from_f32(f * u);
-      } else {
-        p.o0[at] = H::from_f32(x[r]);
+      for (int r = 0; r < 4; ++r) {
+        to[((i * NT + j) * 4 + r) * kThreads + t] = f32x4{x[4 * r], x[4 * r + 1], x[4 * r + 2], x[4 * r + 3]};
+        if (kUp)
+          to[((i * NT + j + NT / 2) * 4 + r) * kThreads + t] = f32x4{v[4 * r], v[4 * r + 1], v[4 * r + 2], v[4 * r + 3]};
       }
+    } else {
+      store_tile<H, KIND, NT>(p, x, v, hi, m0, n0, i, j);
     }
   };
 
@@ -278,11 +313,11 @@ __global__ __launch_bounds__(kThreads, 2) void ffn_tile_kernel(FfnArgs p, int32_
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int j = 0; j < NT; ++j) acc[i][j] = zero;
-    float was[2] = {scale(0, 0), kUp ? scale(0, 1) : 1.0f};
+    float was[2] = {scale(q0, 0), kUp ? scale(q0, 1) : 1.0f};
     sweep(
         acc, Int<0>{}, Int<NT>{}, [&](int32_t) {},
         [&](int32_t q) {
-          if (q + 1 == blocks) return;
+          if (q + 1 == q1) return;
           float ratio[2];
 #pragma unroll
           for (int k = 0; k < (kUp ? 2 : 1); ++k) {
@@ -340,25 +375,63 @@ __global__ __launch_bounds__(kThreads, 2) void ffn_tile_kernel(FfnArgs p, int32_
   }
 }
 
+// The split tiles: their parts' sums added in order, one 32 x 32 tile of each wave per
+// workgroup, and the results as above.
+template <class H, int KIND, int NT>
+__global__ __launch_bounds__(kThreads) void ffn_join_kernel(FfnArgs p, int32_t ncols) {
+  constexpr bool kUp = KIND == kFfnUp;
+  constexpr int kCols = (kUp ? 32 : 64) * NT, kJ = kUp ? NT / 2 : NT;
+  const int32_t blocks = (KIND == kFfnUpBwd ? 2 : 1) * ((p.K + kB - 1) / kB);
+  int32_t rowtiles, e, lo, hi, m0, col;
+  const Plan plan = plan_tiles<kRows>(p.offsets, p.T, p.E, ncols, blocks, true, rowtiles);
+  const int32_t rest = plan.tiles - plan.whole, tile = static_cast<int32_t>(blockIdx.x) / (2 * kJ);
+  if (tile >= rest) return;
+  const int ij = static_cast<int>(blockIdx.x) % (2 * kJ), i = ij / kJ, j = ij % kJ, t = threadIdx.x;
+  if (!find_tile<kRows>(p.offsets, p.T, p.E, ncols, rowtiles, plan.whole + tile, e, lo, hi, m0, col)) return;
+  f32x16 v[2] = {};
+  for (int32_t s = 0; s < plan.splits; ++s) {
+    const f32x4* from = part_at<NT>(p.part, s * rest + tile);
+#pragma unroll
+    for (int k = 0; k < (kUp ? 2 : 1); ++k)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const f32x4 x = from[((i * NT + j + k * (NT / 2)) * 4 + r) * kThreads + t];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[k][4 * r + c] += x[c];
+      }
+  }
+  store_tile<H, KIND, NT>(p, v[0], v[1], hi, m0, col * kCols, i, j);
+}
+
 // The most row tiles that T rows in E runs can make: every run may end in a partial tile.
 int64_t most_row_tiles(int64_t T, int64_t E) { return T / kRows + (T < E ? T : E); }
 
+// Whether k is long enough to be split (two parts of 8 scale blocks), and the bytes of a round
+// of parts.
+bool split_pays(const FfnArgs& p, int products) { return products * ((p.K + kB - 1) / kB) >= 16; }
+size_t part_bytes(int nt) { return sizeof(float) * kSlots * kRows * 64 * nt; }
+
 template <class H, int KIND, int NT>
-void launch_tiles(const FfnArgs& p, bool direct, dim3 g, int32_t ncols, hipStream_t s) {
+void launch_tiles(const FfnArgs& p, bool direct, int64_t tiles, int32_t ncols, hipStream_t s) {
+  // a grid with room for the most parts: the rest of a round becomes at most a round of parts
+  const dim3 g(static_cast<unsigned>(tiles + (p.part ? kSlots : 0))), b(kThreads);
   if (direct)
-    hipLaunchKernelGGL((ffn_tile_kernel<H, KIND, NT, true>), g, dim3(kThreads), 0, s, p, ncols);
+    hipLaunchKernelGGL((ffn_tile_kernel<H, KIND, NT, true>), g, b, 0, s, p, ncols);
   else
-    hipLaunchKernelGGL((ffn_tile_kernel<H, KIND, NT, false>), g, dim3(kThreads), 0, s, p, ncols);
+    hipLaunchKernelGGL((ffn_tile_kernel<H, KIND, NT, false>), g, b, 0, s, p, ncols);
+  if (!p.part) return;
+  const int64_t rest = tiles < kSlots ? tiles : kSlots - 1;
+  const dim3 gj(static_cast<unsigned>(rest * 2 * (KIND == kFfnUp ? NT / 2 : NT)));
+  hipLaunchKernelGGL((ffn_join_kernel<H, KIND, NT>), gj, b, 0, s, p, ncols);
 }
 
 bool misaligned(const void* p, size_t a);
 
 template <int KIND>
-int launch(const FfnArgs& p, int32_t dtype, hipStream_t s, const char* what) {
+int launch(FfnArgs p, int32_t dtype, void* workspace, size_t workspace_bytes, hipStream_t s, const char* what) {
   if (p.T == 0) return FP8Z1_OK;
+  if (misaligned(workspace, 16)) return set_error(FP8Z1_EINVAL, std::string(what) + ": misaligned workspace");
   constexpr bool kTrans = KIND == kFfnDownBwd || KIND == kFfnUpBwd;
-  const bool direct = !misaligned(p.x0, 16) && !misaligned(p.x1, 16) && !misaligned(p.w0, 16) &&
-                      !misaligned(p.w1, 16) && p.K % kStep == 0 && (!kTrans || p.N % 16 == 0);
   // Few rows per expert: the weights' read is what counts
   if constexpr (!kTrans)
     if (static_cast<int64_t>(p.T) <= 32ll * p.E) {
@@ -369,21 +442,24 @@ int launch(const FfnArgs& p, int32_t dtype, hipStream_t s, const char* what) {
         launch_rows<F16, KIND>(p, aligned, s);
       return check_hip(hipGetLastError(), what);
     }
+  const bool direct = !misaligned(p.x0, 16) && !misaligned(p.x1, 16) && !misaligned(p.w0, 16) &&
+                      !misaligned(p.w1, 16) && p.K % kStep == 0 && (!kTrans || p.N % 16 == 0);
   const int64_t rows = most_row_tiles(p.T, p.E);
   const int32_t per = KIND == kFfnUp ? 32 : 64;  // columns per NT
-  const bool wide = rows * ((p.N + 4 * per - 1) / (4 * per)) >= 512;
+  const bool wide = rows * ((p.N + 4 * per - 1) / (4 * per)) >= kSlots;
   const int32_t cols = per * (wide ? 4 : 2), ncols = (p.N + cols - 1) / cols;
-  const int64_t grid = rows * ncols;
-  if (grid > 0x7fffffff) return set_error(FP8Z1_ESHAPE, std::string(what) + ": too many tiles");
-  const dim3 g(static_cast<unsigned>(grid));
+  const int64_t tiles = rows * ncols;
+  if (tiles > 0x7fffffff - kSlots) return set_error(FP8Z1_ESHAPE, std::string(what) + ": too many tiles");
+  if (split_pays(p, KIND == kFfnUpBwd ? 2 : 1) && workspace_bytes >= part_bytes(wide ? 4 : 2))
+    p.part = static_cast<float*>(workspace);
   if (dtype == FP8Z1_BF16 && wide)
-    launch_tiles<Bf16, KIND, 4>(p, direct, g, ncols, s);
+    launch_tiles<Bf16, KIND, 4>(p, direct, tiles, ncols, s);
   else if (dtype == FP8Z1_BF16)
-    launch_tiles<Bf16, KIND, 2>(p, direct, g, ncols, s);
+    launch_tiles<Bf16, KIND, 2>(p, direct, tiles, ncols, s);
   else if (wide)
-    launch_tiles<F16, KIND, 4>(p, direct, g, ncols, s);
+    launch_tiles<F16, KIND, 4>(p, direct, tiles, ncols, s);
   else
-    launch_tiles<F16, KIND, 2>(p, direct, g, ncols, s);
+    launch_tiles<F16, KIND, 2>(p, direct, tiles, ncols, s);
   return check_hip(hipGetLastError(), what);
 }
 

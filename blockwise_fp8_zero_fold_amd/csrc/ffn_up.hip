@@ -5,7 +5,7 @@ using namespace fp8z1;
 
 extern "C" int fp8z1_ffn_up(const fp8z1_ffn* f, const void* x, const uint8_t* gate_codes, const float* gate_scales,
                             const uint8_t* up_codes, const float* up_scales, const int32_t* offsets, void* h, void* u,
-                            void* a, void* stream) {
+                            void* a, void* d_workspace, size_t workspace_bytes, void* stream) {
   const char* what = "ffn_up";
   int rc = check_cfg(f, offsets, what);
   if (!rc && f->T) rc = check_rows({x, a}, what);
@@ -22,5 +22,6 @@ extern "C" int fp8z1_ffn_up(const fp8z1_ffn* f, const void* x, const uint8_t* ga
   p.o0 = static_cast<uint16_t*>(a);
   p.o1 = static_cast<uint16_t*>(h);
   p.o2 = static_cast<uint16_t*>(u);
-  return launch<kFfnUp>(p, f->dtype, static_cast<hipStream_t>(stream), what);
+  return launch<kFfnUp>(p, f->dtype, d_workspace, workspace_bytes, static_cast<hipStream_t>(stream),
+                       what);
 }

@@ -5,7 +5,7 @@ using namespace fp8z1;
 
 extern "C" int fp8z1_ffn_up_bwd(const fp8z1_ffn* f, const void* dh, const void* du, const uint8_t* gate_codes,
                                 const float* gate_scales, const uint8_t* up_codes, const float* up_scales,
-                                const int32_t* offsets, void* dx, void* stream) {
+                                const int32_t* offsets, void* dx, void* d_workspace, size_t workspace_bytes, void* stream) {
   const char* what = "ffn_up_bwd";
   int rc = check_cfg(f, offsets, what);
   if (!rc && f->T) rc = check_rows({dh, du, dx}, what);
@@ -20,5 +20,6 @@ extern "C" int fp8z1_ffn_up_bwd(const fp8z1_ffn* f, const void* dh, const void* 
   p.s0 = gate_scales;
   p.s1 = up_scales;
   p.o0 = static_cast<uint16_t*>(dx);
-  return launch<kFfnUpBwd>(p, f->dtype, static_cast<hipStream_t>(stream), what);
+  return launch<kFfnUpBwd>(p, f->dtype, d_workspace, workspace_bytes, static_cast<hipStream_t>(stream),
+                       what);
 }

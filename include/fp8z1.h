@@ -344,26 +344,31 @@ typedef struct {
   int32_t act;   /* FP8Z1_ACT_* */
 } fp8z1_ffn;
 
+/* Bytes of device workspace (16-byte aligned) with which the four calls below can split the
+ * tiles that do not fill a round of the card along k; calls one after another may share it.
+ * With less (or NULL) they do not split. */
+int fp8z1_ffn_workspace_bytes(const fp8z1_ffn* f, size_t* bytes);
+
 /* a [T,F] = act(x Wg^T) * (x Wu^T) in one kernel; gate and up codes [E,F,D].  h and u
  * [T,F] (both or neither NULL) keep the projections for the backward pass. */
 int fp8z1_ffn_up(const fp8z1_ffn* f, const void* x, const uint8_t* gate_codes, const float* gate_scales,
                  const uint8_t* up_codes, const float* up_scales, const int32_t* offsets, void* h, void* u, void* a,
-                 void* stream);
+                 void* d_workspace, size_t workspace_bytes, void* stream);
 
 /* y [T,D] = a Wd^T; down codes [E,D,F]. */
 int fp8z1_ffn_down(const fp8z1_ffn* f, const void* a, const uint8_t* down_codes, const float* down_scales,
-                   const int32_t* offsets, void* y, void* stream);
+                   const int32_t* offsets, void* y, void* d_workspace, size_t workspace_bytes, void* stream);
 
 /* From dy [T,D] and the kept h, u: da = dy Wd (never written), dh = da * u * act'(h),
  * du = da * act(h), and, unless a is NULL, a = act(h) * u again for the weight gradient. */
 int fp8z1_ffn_down_bwd(const fp8z1_ffn* f, const void* dy, const uint8_t* down_codes, const float* down_scales,
                        const void* h, const void* u, const int32_t* offsets, void* dh, void* du, void* a,
-                       void* stream);
+                       void* d_workspace, size_t workspace_bytes, void* stream);
 
 /* dx [T,D] = dh Wg + du Wu, both products in one sum. */
 int fp8z1_ffn_up_bwd(const fp8z1_ffn* f, const void* dh, const void* du, const uint8_t* gate_codes,
                      const float* gate_scales, const uint8_t* up_codes, const float* up_scales, const int32_t* offsets,
-                     void* dx, void* stream);
+                     void* dx, void* d_workspace, size_t workspace_bytes, void* stream);
 
 /* Weight gradient dw [E,M,N] = per expert sum over its rows t of p[t,m] q[t,n], with p
  * [T,M] and q [T,N] of `dtype` (FP8Z1_BF16 or FP8Z1_F16): dWg = (dh, x), dWu = (du, x),

@@ -18,10 +18,10 @@ def ffn(**kw):
 def calls(f, offsets=P, codes=P, scales=P, rows=P):
     lib = fz.lib
     return {
-        "up": lib.fp8z1_ffn_up(f, rows, codes, scales, codes, scales, offsets, None, None, rows, None),
-        "down": lib.fp8z1_ffn_down(f, rows, codes, scales, offsets, rows, None),
-        "down_bwd": lib.fp8z1_ffn_down_bwd(f, rows, codes, scales, rows, rows, offsets, rows, rows, None, None),
-        "up_bwd": lib.fp8z1_ffn_up_bwd(f, rows, rows, codes, scales, codes, scales, offsets, rows, None),
+        "up": lib.fp8z1_ffn_up(f, rows, codes, scales, codes, scales, offsets, None, None, rows, None, 0, None),
+        "down": lib.fp8z1_ffn_down(f, rows, codes, scales, offsets, rows, None, 0, None),
+        "down_bwd": lib.fp8z1_ffn_down_bwd(f, rows, codes, scales, rows, rows, offsets, rows, rows, None, None, 0, None),
+        "up_bwd": lib.fp8z1_ffn_up_bwd(f, rows, rows, codes, scales, codes, scales, offsets, rows, None, 0, None),
     }
 
 
@@ -42,13 +42,23 @@ def test_ffn_pointers(bad):
 
 
 def test_ffn_up_keeps_both_projections_or_none():
-    assert fz.lib.fp8z1_ffn_up(ffn(), P, P, P, P, P, P, P, None, P, None) == EINVAL
-    assert fz.lib.fp8z1_ffn_up(ffn(), P, P, P, P, P, P, None, P, P, None) == EINVAL
+    assert fz.lib.fp8z1_ffn_up(ffn(), P, P, P, P, P, P, P, None, P, None, 0, None) == EINVAL
+    assert fz.lib.fp8z1_ffn_up(ffn(), P, P, P, P, P, P, None, P, P, None, 0, None) == EINVAL
 
 
 def test_no_rows_is_no_work():
     f = ffn(T=0)
     assert set(calls(f, rows=None).values()) == {0}
+
+
+def test_ffn_workspace():
+    n = C.c_size_t()
+    q = fz.lib.fp8z1_ffn_workspace_bytes
+    assert q(None, C.byref(n)) == EINVAL and q(ffn(), None) == EINVAL and q(ffn(D=0), C.byref(n)) == ESHAPE
+    assert q(ffn(), C.byref(n)) == 0 and n.value == 0  # sums of 64: nothing to split
+    assert q(ffn(D=7168), C.byref(n)) == 0 and n.value > 0
+    lib = fz.lib
+    assert lib.fp8z1_ffn_down(ffn(), P, P, P, P, P, P + 4, 1 << 30, None) == EINVAL  # misaligned workspace
 
 
 def wgrad(T=8, E=1, M=16, N=16, dtype=fz.BF16, p=P, q=P, offsets=P, out=fz.F32, dw=P, acc=0, ws=None, n=0):

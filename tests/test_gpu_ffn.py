@@ -120,6 +120,28 @@ def test_one_expert_without_offsets(T):
     c.check_down(y, f"{T} rows")
 
 
+@pytest.mark.parametrize("T,E,D,F", [(150, 2, 2176, 130), (300, 1, 130, 2300), (100, 2, 2053, 1111), (200, 1, 4096, 1088)])
+@pytest.mark.parametrize("far", [False, True])
+def test_long_sums_split_over_workgroups(T, E, D, F, far):
+    """Few tiles and long sums: with a workspace each call splits its tiles along k."""
+    c = Case(T, E, D, F, "bf16", "gelu", lo=-40.0 if far else -3.0, hi=30.0 if far else 3.0)
+    what = f"{T} rows, {E} experts, {D} x {F}"
+    print("#", what, flush=True)
+    ws = torch.empty(fz.fp8z1_ffn_workspace_bytes(c.cfg), dtype=torch.uint8, device="cuda")
+    assert ws.numel()
+    h, u, a, dh, du, a2 = (c.out(F) for _ in range(6))
+    y, dx = c.out(D), c.out(D)
+    off = c.dev("offsets")
+    fz.fp8z1_ffn_up(c.cfg, c.dev("x"), *c.dev("gate"), *c.dev("up"), off, h, u, a, workspace=ws)
+    c.check_up((h, u, a), what)
+    fz.fp8z1_ffn_down(c.cfg, c.dev("a"), *c.dev("down"), off, y, workspace=ws)
+    c.check_down(y, what)
+    fz.fp8z1_ffn_down_bwd(c.cfg, c.dev("dy"), *c.dev("down"), c.dev("h"), c.dev("u"), off, dh, du, a2, workspace=ws)
+    c.check_down_bwd((dh, du, a2), what)
+    fz.fp8z1_ffn_up_bwd(c.cfg, c.dev("dh"), c.dev("du"), *c.dev("gate"), *c.dev("up"), off, dx, workspace=ws)
+    c.check_up_bwd(dx, what)
+
+
 def wgrad_check(p, q, E, offsets, got, dtype, what, start=None):
     T = p.shape[0]
     exact = torch.zeros(E, p.shape[1], q.shape[1], dtype=torch.float64)
@@ -292,9 +314,9 @@ def _layer(c):
     return run
 
 
-@pytest.mark.parametrize("T", [6, 400])
-def test_graph_replays_equal_eager(T):
-    c = Case(T, 3, 264, 160)
+@pytest.mark.parametrize("T,F", [(6, 160), (400, 160), (200, 1200)])
+def test_graph_replays_equal_eager(T, F):
+    c = Case(T, 3, 264, F)
     run = _layer(c)
     x, dy = c.dev("x"), c.dev("dy")
     run(x, dy)
