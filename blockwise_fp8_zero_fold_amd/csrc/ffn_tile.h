@@ -127,7 +127,7 @@ __global__ __launch_bounds__(kThreads, 2) void ffn_tile_kernel(FfnArgs p, int32_
   const int32_t q0 = blocks * sp / parts, q1 = blocks * (sp + 1) / parts;
   if (!find_tile<kRows>(p.offsets, p.T, p.E, ncols, rowtiles, id, e, lo, hi, m0, col)) return;
   const int32_t n0 = col * kCols;
-  const int t = threadIdx.x, lane = t & 63, w = t >> 6, wm = w >> 1, wn = w & 1;
+  const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6), wm = w >> 1, wn = w & 1;
   const int32_t N = p.N, K = p.K;
   const int32_t nb = (N + kB - 1) / kB;
 
@@ -195,42 +195,47 @@ __global__ __launch_bounds__(kThreads, 2) void ffn_tile_kernel(FfnArgs p, int32_
 
   const f32x16 zero = {};
   const int half = lane >> 5, l32 = lane & 31, l16 = lane & 15, grp = lane >> 4;
-  // d[i][j - j0] += A tile i times B tile j, over one stage.  All LDS reads of the stage
-  // are issued before its matrix instructions, which then wait for them one by one.
-  auto compute = [&](const uint8_t* sa, const uint8_t* sb, auto& d, auto j0_, auto nj_) {
+  // d[i][j - j0] += A tile i times B tile j, over one stage: LDS reads of half a stage, the
+  // copies of the next stage (`next`), and the matrix instructions among the other
+  // half's reads.
+  auto compute = [&](const uint8_t* sa, const uint8_t* sb, auto& d, auto j0_, auto nj_, auto next) {
     constexpr int j0 = decltype(j0_)::value, nj = decltype(nj_)::value;
     uint4 a[4][2];
     uint2 b[4][nj];
+    auto read = [&](int ks0) {
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
+      for (int ks = ks0; ks < ks0 + 2; ++ks) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = wm * 64 + i * 32 + l32;
-        // k of this lane: plain order where B is read transposed; otherwise the lane's
-        // 16 consecutive k of a 32-wide group, 8 per step, as B's 16-byte chunk holds them
-        const int c = kTrans ? ks * 2 + half : (ks >> 1) * 4 + half * 2 + (ks & 1);
-        a[ks][i] = *reinterpret_cast<const uint4*>(sa + r * 128 + ((c ^ swizzle_a(r)) << 4));
-      }
+        for (int i = 0; i < 2; ++i) {
+          const int r = wm * 64 + i * 32 + l32;
+          // k of this lane: plain order where B is read transposed; otherwise the lane's
+          // 16 consecutive k of a 32-wide group, 8 per step, as B's 16-byte chunk holds them
+          const int c = kTrans ? ks * 2 + half : (ks >> 1) * 4 + half * 2 + (ks & 1);
+          a[ks][i] = *reinterpret_cast<const uint4*>(sa + r * 128 + ((c ^ swizzle_a(r)) << 4));
+        }
 #pragma unroll
-      for (int jj = 0; jj < nj; ++jj) {
-        const int j = j0 + jj;
-        if (kTrans) {
-          const int r = ks * 16 + (grp >> 1) * 8 + (l16 >> 1);
-          const int c = (wn * NT + j) * 2 + (grp & 1);
-          const i32x2 q = read_tr8(sb + r * kB2 + ((c ^ swizzle_t<kB2>(r)) << 4) + (l16 & 1) * 8);
-          b[ks][jj] = make_uint2(q.x, q.y);
-        } else if (ks % 2 == 0) {
-          // gate tiles first, then the up tiles of the same columns
-          const int r = kUp ? (j / (NT / 2)) * (kB2 / 2) + (wn * (NT / 2) + j % (NT / 2)) * 32 + l32
-                            : (wn * NT + j) * 32 + l32;
-          const int c = ks + half;
-          const uint4 q = *reinterpret_cast<const uint4*>(sb + r * 64 + ((c ^ swizzle_b(r)) << 4));
-          b[ks][jj] = make_uint2(q.x, q.y);
-          b[ks + 1][jj] = make_uint2(q.z, q.w);
+        for (int jj = 0; jj < nj; ++jj) {
+          const int j = j0 + jj;
+          if (kTrans) {
+            const int r = ks * 16 + (grp >> 1) * 8 + (l16 >> 1);
+            const int c = (wn * NT + j) * 2 + (grp & 1);
+            const i32x2 q = read_tr8(sb + r * kB2 + ((c ^ swizzle_t<kB2>(r)) << 4) + (l16 & 1) * 8);
+            b[ks][jj] = make_uint2(q.x, q.y);
+          } else if (ks % 2 == 0) {
+            // gate tiles first, then the up tiles of the same columns
+            const int r = kUp ? (j / (NT / 2)) * (kB2 / 2) + (wn * (NT / 2) + j % (NT / 2)) * 32 + l32
+                              : (wn * NT + j) * 32 + l32;
+            const int c = ks + half;
+            const uint4 q = *reinterpret_cast<const uint4*>(sb + r * 64 + ((c ^ swizzle_b(r)) << 4));
+            b[ks][jj] = make_uint2(q.x, q.y);
+            b[ks + 1][jj] = make_uint2(q.z, q.w);
+          }
         }
       }
-    }
-    __builtin_amdgcn_sched_barrier(0);
+    };
+    read(0);
+    next();
+    read(2);
     v8 bw = widen8<H>(b[0][0].x, b[0][0].y);
 #pragma unroll
     for (int s = 0; s < 4 * nj; ++s) {
@@ -251,28 +256,33 @@ __global__ __launch_bounds__(kThreads, 2) void ffn_tile_kernel(FfnArgs p, int32_
   const float* const sp1 = KIND == kFfnUpBwd || kUp ? p.s1 + sat : nullptr;
   auto scale = [&](int32_t q, int which) {
     const bool second = kSeg == 2 ? q >= kb : which == 1;
-    return (second ? sp1 : sp0)[static_cast<int64_t>(kSeg == 2 && second ? q - kb : q) * sstride];
+    // (through the scalar cache: the scales do not change while the kernel runs)
+    typedef const __attribute__((address_space(4))) float* scalar_t;
+    return ((scalar_t)(second ? sp1 : sp0))[static_cast<int64_t>(kSeg == 2 && second ? q - kb : q) * sstride];
   };
 
   // One pass over this item's k; `after(q)` runs after the two stages of scale block q.
   auto sweep = [&](auto& d, auto j0_, auto nj_, auto before, auto after) {
-    fetch(kSeg == 2 && q0 >= kb ? 1 : 0, (kSeg == 2 && q0 >= kb ? q0 - kb : q0) * kB, sa0, sb0);
+    auto stage = [&](int32_t q, int32_t second, uint8_t* sa, uint8_t* sb) {
+      const bool seg = kSeg == 2 && q >= kb;
+      fetch(seg ? 1 : 0, (seg ? q - kb : q) * kB + second, sa, sb);
+    };
+    stage(q0, 0, sa0, sb0);
     put(sa0, sb0);
     for (int32_t q = q0; q < q1; ++q) {
       before(q);
+      if (DIRECT) wait_copies();
       __syncthreads();
-      const int32_t kn = (kSeg == 2 && q >= kb ? q - kb : q) * kB + kStep;
-      const bool both = kn < K;  // the last block may end with its first stage
-      if (both) fetch(kSeg == 2 && q >= kb ? 1 : 0, kn, sa1, sb1);
-      compute(sa0, sb0, d, j0_, nj_);
-      if (both) put(sa1, sb1);
+      compute(sa0, sb0, d, j0_, nj_, [&] { stage(q, kStep, sa1, sb1); });
+      put(sa1, sb1);
+      if (DIRECT) wait_copies();
       __syncthreads();
-      const int32_t qn = q + 1;
-      if (qn < q1) fetch(kSeg == 2 && qn >= kb ? 1 : 0, (kSeg == 2 && qn >= kb ? qn - kb : qn) * kB, sa0, sb0);
-      if (both) compute(sa1, sb1, d, j0_, nj_);
-      if (qn < q1) put(sa0, sb0);
+      // (the last block's turn fetches it again rather than branch)
+      compute(sa1, sb1, d, j0_, nj_, [&] { stage(min(q + 1, q1 - 1), 0, sa0, sb0); });
+      put(sa0, sb0);
       after(q);
     }
+    if (DIRECT) wait_copies();
     __syncthreads();  // the stages are written again by the next pass
   };
 
@@ -417,8 +427,8 @@ void launch_tiles(const FfnArgs& p, bool direct, int64_t tiles, int32_t ncols, h
   const dim3 g(static_cast<unsigned>(tiles + (p.part ? kSlots : 0))), b(kThreads);
   if (direct)
     hipLaunchKernelGGL((ffn_tile_kernel<H, KIND, NT, true>), g, b, 0, s, p, ncols);
-  else
-    hipLaunchKernelGGL((ffn_tile_kernel<H, KIND, NT, false>), g, b, 0, s, p, ncols);
+  else if constexpr (NT == 2)
+    hipLaunchKernelGGL((ffn_tile_kernel<H, KIND, 2, false>), g, b, 0, s, p, ncols);
   if (!p.part) return;
   const int64_t rest = tiles < kSlots ? tiles : kSlots - 1;
   const dim3 gj(static_cast<unsigned>(rest * 2 * (KIND == kFfnUp ? NT / 2 : NT)));
@@ -443,10 +453,11 @@ int launch(FfnArgs p, int32_t dtype, void* workspace, size_t workspace_bytes, hi
       return check_hip(hipGetLastError(), what);
     }
   const bool direct = !misaligned(p.x0, 16) && !misaligned(p.x1, 16) && !misaligned(p.w0, 16) &&
-                      !misaligned(p.w1, 16) && p.K % kStep == 0 && (!kTrans || p.N % 16 == 0);
+                      !misaligned(p.w1, 16) && p.K % kB == 0 && (!kTrans || p.N % 16 == 0);
   const int64_t rows = most_row_tiles(p.T, p.E);
   const int32_t per = KIND == kFfnUp ? 32 : 64;  // columns per NT
-  const bool wide = rows * ((p.N + 4 * per - 1) / (4 * per)) >= kSlots;
+  // 256 columns a tile where they fill the card; what goes through registers takes too many for it
+  const bool wide = direct && rows * ((p.N + 4 * per - 1) / (4 * per)) >= kSlots;
   const int32_t cols = per * (wide ? 4 : 2), ncols = (p.N + cols - 1) / cols;
   const int64_t tiles = rows * ncols;
   if (tiles > 0x7fffffff - kSlots) return set_error(FP8Z1_ESHAPE, std::string(what) + ": too many tiles");

@@ -103,15 +103,25 @@ __device__ __forceinline__ uint4 ld16_part(const uint8_t* p, int n) {
 // at `off` bytes (16-byte aligned, its own for each lane) behind the buffer's base,
 // land at dst + 16 l.  The buffer is `size` bytes long at most; base and size are the
 // same for the wave, so the only vector register that an address takes is the offset.
-typedef __amdgpu_buffer_rsrc_t buffer_t;
+// Written as assembly so that the compiler does not make every later LDS read wait for the
+// copy (it cannot tell that a read is of another stage); it has no register output.
+// The caller waits with wait_copies() before the barrier that hands the stage over.
+typedef int buffer_t __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ buffer_t make_buffer(const uint8_t* base, int64_t size) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0,
-                                           static_cast<int>(size < 0x7fffffff ? size : 0x7fffffff), 0x00027000);
+  const uint64_t at = reinterpret_cast<uint64_t>(base);
+  return buffer_t{__builtin_amdgcn_readfirstlane(static_cast<int>(at)),
+                  __builtin_amdgcn_readfirstlane(static_cast<int>(at >> 32) & 0xffff),
+                  __builtin_amdgcn_readfirstlane(static_cast<int>(size < 0x7fffffff ? size : 0x7fffffff)), 0x00027000};
 }
 __device__ __forceinline__ void copy16_to_lds(buffer_t b, uint32_t off, uint8_t* dst) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (__attribute__((address_space(3))) void*)(dst), 16,
-                                           static_cast<int>(off), 0, 0, 0);
+  const uint32_t at = static_cast<uint32_t>(
+      reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)(dst)));
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :
+               : "s"(__builtin_amdgcn_readfirstlane(static_cast<int>(at))), "v"(off), "s"(b)
+               : "memory");
 }
+__device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // Transposing reads, per group of 16 lanes.  16-bit: lane 4r + c names the 8 bytes
 // of row r, columns 4c..4c+3, and lane i receives column i of the four rows.
