@@ -49,7 +49,7 @@ __global__ __launch_bounds__(WAVES * 64) void ffn_rows_kernel(FfnArgs p) {
           if (ALIGNED)
             b.c[m][i] = 16 * i < left ? *reinterpret_cast<const uint4*>(src) : make_uint4(0u, 0u, 0u, 0u);
           else
-            b.c[m][i] = ld16_part(src, left - 16 * i);
+            b.c[m][i] = ld16_part(src, left - 16 * i, K - left + 16 * i);
         }
       }
 #pragma unroll
@@ -60,7 +60,7 @@ __global__ __launch_bounds__(WAVES * 64) void ffn_rows_kernel(FfnArgs p) {
           if (ALIGNED)
             b.x[t][i] = 8 * i < left ? *reinterpret_cast<const uint4*>(src) : make_uint4(0u, 0u, 0u, 0u);
           else
-            b.x[t][i] = ld16_part(src, 2 * left - 16 * i);
+            b.x[t][i] = ld16_part(src, 2 * left - 16 * i, 2 * (K - left) + 16 * i);
         }
     };
     f32x4 acc[kM][TT];

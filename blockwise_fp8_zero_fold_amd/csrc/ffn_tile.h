@@ -180,10 +180,11 @@ __global__ __launch_bounds__(kThreads, 2) void ffn_tile_kernel(FfnArgs p, int32_
       return;
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) ra[j] = ld16_part(x + aoff[j], (K - k0) * 2 - ac[j]);
+    for (int j = 0; j < 4; ++j) ra[j] = ld16_part(x + aoff[j], (K - k0) * 2 - ac[j], k0 * 2 + ac[j]);
 #pragma unroll
     for (int j = 0; j < kBC; ++j)
-      rb[j] = ld16_part((j < kBC / 2 ? wa : wb) + boff[j], kTrans ? (k0 + br[j] < K ? bn[j] : 0) : K - k0 - bn[j]);
+      rb[j] = kTrans ? ld16_part(wa + boff[j], k0 + br[j] < K ? bn[j] : 0, N - bn[j])
+                     : ld16_part((j < kBC / 2 ? wa : wb) + boff[j], K - k0 - bn[j], k0 + bn[j]);
   };
   auto put = [&](uint8_t* sa, uint8_t* sb) {
     if (DIRECT) return;

@@ -2,9 +2,9 @@
 // tokens t of p[t][m] q[t][n], written as the row-major [E, M, N] gradient that the
 // shard step reads.
 //
-// A workgroup of 4 waves computes 128 x 128 of one expert's dW, each wave 64 x 64 as
-// 2 x 2 matrix tiles of 32 x 32.  Both operands run along the columns while the sum
-// runs down the rows, so a stage of 64 tokens is kept in LDS as it lies in memory and
+// A workgroup of 4 waves computes 128 x 64 NT of one expert's dW, each wave 64 x 32 NT as
+// 2 x NT matrix tiles of 32 x 32.  Both operands run along the columns while the sum
+// runs down the rows, so a stage of 32 tokens is kept in LDS as it lies in memory and
 // the matrix operands are gathered by the transposing LDS reads.
 #include <hip/hip_runtime.h>
 
@@ -14,9 +14,9 @@ namespace fp8z1 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTile = 128;  // rows and columns of a tile
-constexpr int kStep = 64;   // tokens per stage
-constexpr int kBytes = kTile * kStep * 2;
+constexpr int kTile = 128;  // tile rows
+constexpr int kStep = 32;   // tokens per stage
+constexpr int kPBytes = kTile * kStep * 2;
 
 struct WgradArgs {
   const uint8_t *p, *q;  // [T, M], [T, N]
@@ -26,96 +26,139 @@ struct WgradArgs {
   int32_t T, E, M, N, mt, nt, splits, accumulate;
 };
 
-template <class H, bool F32OUT>
+// Chunk c (16 bytes) of row r of a stage sits at position c ^ swizzle(r): a transposing read
+// takes 4 rows of 4 neighbouring chunks at a time, which then lie in 16 different places.
+__device__ __forceinline__ int swizzle(int r) { return (r & 3) << 2; }
+
+// DIRECT: rows are 16-byte aligned, so a stage goes from memory to LDS by direct copies;
+// otherwise through registers, with the bytes outside a row left out.
+template <class H, bool F32OUT, int NT, bool DIRECT>
 __global__ __launch_bounds__(kThreads, 2) void ffn_wgrad_kernel(WgradArgs g) {
   typedef typename H::v8 v8;
-  __shared__ __attribute__((aligned(16))) uint8_t sp[2][kBytes];
-  __shared__ __attribute__((aligned(16))) uint8_t sq[2][kBytes];
-  const int t = threadIdx.x, lane = t & 63, w = t >> 6, wm = w >> 1, wn = w & 1;
+  constexpr int kCols = NT * 64, kQBytes = kCols * kStep * 2, kStage = kPBytes + kQBytes;
+  constexpr int kPC = kPBytes / 16 / kThreads, kQC = kQBytes / 16 / kThreads;  // chunks per thread
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kStage];
+  const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6), wm = w >> 1, wn = w & 1;
 
-  // tiles in contiguous runs per XCD, in groups of 8 tile rows by all tile columns
-  const int32_t all = static_cast<int32_t>(gridDim.x), x = blockIdx.x % kXcds;
-  int32_t id = x * (all / kXcds) + min(x, all % kXcds) + static_cast<int32_t>(blockIdx.x) / kXcds;
+  // tiles in contiguous runs per XCD, in groups of kGroup tile rows by all tile columns
+  int32_t id = xcd_run(static_cast<int32_t>(blockIdx.x), static_cast<int32_t>(gridDim.x));
   const int32_t per = g.mt * g.nt, split = id / (per * g.E);
   id -= split * per * g.E;
   const int32_t e = id / per;
   id -= e * per;
   const int32_t gr = id / (kGroup * g.nt), in = id - gr * kGroup * g.nt, rows = min(kGroup, g.mt - gr * kGroup);
-  const int32_t m0 = (gr * kGroup + in % rows) * kTile, n0 = in / rows * kTile;
+  const int32_t m0 = (gr * kGroup + in % rows) * kTile, n0 = in / rows * kCols;
 
   int32_t lo, hi;
   expert_rows(g.offsets, g.T, e, lo, hi);
+  lo = __builtin_amdgcn_readfirstlane(lo);
+  hi = __builtin_amdgcn_readfirstlane(hi);
   const int32_t stages = (hi - lo + kStep - 1) / kStep;
   const int32_t s0 = static_cast<int32_t>(static_cast<int64_t>(stages) * split / g.splits);
   const int32_t s1 = static_cast<int32_t>(static_cast<int64_t>(stages) * (split + 1) / g.splits);
 
-  int64_t poff[4], qoff[4];
-  int32_t pn[4], qn[4], row[4];
+  uint32_t poff[kPC], qoff[kQC];
+  int32_t pc[kPC], qc[kQC];  // byte column of the chunk
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int ch = t + kThreads * j, r = ch >> 4, c = ((ch & 15) ^ ((r & 3) << 2)) * 8;
-    row[j] = r;
-    poff[j] = (static_cast<int64_t>(lo + r) * g.M + m0 + c) * 2;
-    qoff[j] = (static_cast<int64_t>(lo + r) * g.N + n0 + c) * 2;
-    pn[j] = (g.M - m0 - c) * 2;
-    qn[j] = (g.N - n0 - c) * 2;
+  for (int j = 0; j < kPC; ++j) {
+    const int ch = t + kThreads * j, r = ch / (kTile / 8);
+    pc[j] = ((ch % (kTile / 8)) ^ swizzle(r)) * 16;
+    poff[j] = static_cast<uint32_t>(r) * static_cast<uint32_t>(g.M) * 2 + pc[j];
   }
-  uint4 rp[4], rq[4];
-  auto load = [&](int32_t s) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const bool in_run = lo + s * kStep + row[j] < hi;
-      rp[j] = ld16_part(g.p + poff[j] + static_cast<int64_t>(s) * kStep * g.M * 2, in_run ? pn[j] : 0);
-      rq[j] = ld16_part(g.q + qoff[j] + static_cast<int64_t>(s) * kStep * g.N * 2, in_run ? qn[j] : 0);
+  for (int j = 0; j < kQC; ++j) {
+    const int ch = t + kThreads * j, r = ch / (kCols / 8);
+    qc[j] = ((ch % (kCols / 8)) ^ swizzle(r)) * 16;
+    qoff[j] = static_cast<uint32_t>(r) * static_cast<uint32_t>(g.N) * 2 + qc[j];
+  }
+  uint4 rp[kPC], rq[kQC];
+  auto fetch = [&](int32_t s, uint8_t* to) {
+    const int32_t t0 = lo + s * kStep;
+    const uint8_t* const pb = g.p + (static_cast<int64_t>(t0) * g.M + m0) * 2;
+    const uint8_t* const qb = g.q + (static_cast<int64_t>(t0) * g.N + n0) * 2;
+    if (DIRECT) {
+      // The buffers end with the run: chunks of later rows are not read.  A chunk past the
+      // end of a row is the next row's; its columns are not stored.
+      const buffer_t ba = make_buffer(pb, (static_cast<int64_t>(hi - t0) * g.M - m0) * 2);
+      const buffer_t bb = make_buffer(qb, (static_cast<int64_t>(hi - t0) * g.N - n0) * 2);
+#pragma unroll
+      for (int j = 0; j < kPC; ++j) copy16_to_lds(ba, poff[j], to + (w * 64 + kThreads * j) * 16);
+#pragma unroll
+      for (int j = 0; j < kQC; ++j) copy16_to_lds(bb, qoff[j], to + kPBytes + (w * 64 + kThreads * j) * 16);
+      return;
+    }
+#pragma unroll
+    for (int j = 0; j < kPC; ++j) {
+      const int r = (t + kThreads * j) / (kTile / 8);
+      rp[j] = ld16_part(pb + poff[j], t0 + r < hi ? (g.M - m0) * 2 - pc[j] : 0, m0 * 2 + pc[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < kQC; ++j) {
+      const int r = (t + kThreads * j) / (kCols / 8);
+      rq[j] = ld16_part(qb + qoff[j], t0 + r < hi ? (g.N - n0) * 2 - qc[j] : 0, n0 * 2 + qc[j]);
     }
   };
-  auto store = [&](int buf) {
+  auto put = [&](uint8_t* to) {
+    if (DIRECT) return;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      *reinterpret_cast<uint4*>(&sp[buf][(t + kThreads * j) * 16]) = rp[j];
-      *reinterpret_cast<uint4*>(&sq[buf][(t + kThreads * j) * 16]) = rq[j];
-    }
+    for (int j = 0; j < kPC; ++j) *reinterpret_cast<uint4*>(to + (t + kThreads * j) * 16) = rp[j];
+#pragma unroll
+    for (int j = 0; j < kQC; ++j) *reinterpret_cast<uint4*>(to + kPBytes + (t + kThreads * j) * 16) = rq[j];
   };
   const int l16 = lane & 15, grp = lane >> 4;
   // 8 tokens of one column per lane: two reads of 4
-  auto operand = [&](const uint8_t* s, int col0, int ks) {
+  auto operand = [&](const uint8_t* s, int stride, int col0, int ks) {
     const int r = ks * 16 + (grp >> 1) * 8 + (l16 >> 2);
     const int c = col0 / 8 + (grp & 1) * 2 + ((l16 & 3) >> 1);
-    const uint8_t* at = s + r * 256 + ((c ^ ((r & 3) << 2)) << 4) + (l16 & 1) * 8;
-    const i32x2 a = read_tr16(at), b = read_tr16(at + 4 * 256);
+    const uint8_t* at = s + r * stride + ((c ^ swizzle(r)) << 4) + (l16 & 1) * 8;
+    const i32x2 a = read_tr16(at), b = read_tr16(at + 4 * stride);
     return as_v8<H>(make_uint4(a.x, a.y, b.x, b.y));
   };
 
-  f32x16 acc[2][2];
+  f32x16 acc[2][NT];
   const f32x16 zero = {};
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j) acc[i][j] = zero;
+    for (int j = 0; j < NT; ++j) acc[i][j] = zero;
 
   if (s0 < s1) {
-    load(s0);
-    store(0);
+    fetch(s0, lds);
+    put(lds);
   }
-  __syncthreads();
   for (int32_t s = s0; s < s1; ++s) {
     const int buf = (s - s0) & 1;
-    if (s + 1 < s1) load(s + 1);
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      v8 a[2], b[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        a[i] = operand(sp[buf], wm * 64 + i * 32, ks);
-        b[i] = operand(sq[buf], wn * 64 + i * 32, ks);
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = H::mma32(a[i], b[j], acc[i][j]);
-    }
-    if (s + 1 < s1) store(buf ^ 1);
+    uint8_t* const here = lds + buf * kStage;
+    uint8_t* const there = lds + (buf ^ 1) * kStage;
+    if (DIRECT) wait_copies();
     __syncthreads();
+    const int32_t left = hi - lo - s * kStep;
+    if (DIRECT && left < kStep) {  // the run ends inside the stage: rows past it count nothing
+      const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+      for (int at = left * (kTile / 8) + t; at < kStep * (kTile / 8); at += kThreads)
+        *reinterpret_cast<uint4*>(here + at * 16) = z;
+      for (int at = left * (kCols / 8) + t; at < kStep * (kCols / 8); at += kThreads)
+        *reinterpret_cast<uint4*>(here + kPBytes + at * 16) = z;
+      __syncthreads();
+    }
+    v8 a[2][2], b[2][NT];
+    auto read = [&](int ks) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) a[ks][i] = operand(here, kTile * 2, wm * 64 + i * 32, ks);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) b[ks][j] = operand(here + kPBytes, kCols * 2, (wn * NT + j) * 32, ks);
+    };
+    read(0);
+    if (s + 1 < s1) fetch(s + 1, there);
+    read(1);
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) acc[i][j] = H::mma32(a[ks][i], b[ks][j], acc[i][j]);
+    __builtin_amdgcn_sched_barrier(0);
+    if (s + 1 < s1) put(there);
   }
 
   const int64_t size = static_cast<int64_t>(g.E) * g.M * g.N;
@@ -126,8 +169,8 @@ __global__ __launch_bounds__(kThreads, 2) void ffn_wgrad_kernel(WgradArgs g) {
       const int32_t m = m0 + wm * 64 + i * 32 + (r >> 2) * 8 + (lane >> 5) * 4 + (r & 3);
       if (m >= g.M) continue;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int32_t n = n0 + wn * 64 + j * 32 + (lane & 31);
+      for (int j = 0; j < NT; ++j) {
+        const int32_t n = n0 + (wn * NT + j) * 32 + (lane & 31);
         if (n >= g.N) continue;
         const int64_t at = (static_cast<int64_t>(e) * g.M + m) * g.N + n;
         if (g.part)
@@ -155,12 +198,18 @@ __global__ __launch_bounds__(256) void ffn_wgrad_join_kernel(const float* __rest
   }
 }
 
-// Splits of the tokens: where the output has fewer tiles than the card runs at once
-// (two workgroups on each of 256 compute units), the tokens are cut so that about that
-// many run, each with at least 4 stages of an even share.
+// Columns of a tile: 256 where such tiles fill the card twice over (as many workgroups as run
+// at once, two on each of 256 compute units), else 128.
+int wgrad_nt(int64_t E, int64_t M, int64_t N, bool direct) {
+  return direct && E * ((M + kTile - 1) / kTile) * ((N + 255) / 256) >= 2 * kSlots ? 4 : 2;
+}
+
+// Splits of the tokens: where the output has fewer tiles (of 128 columns) than the card runs at
+// once, the tokens are cut so that about that many run, each with at least 8 stages of
+// an even share.
 int32_t wgrad_splits(int64_t T, int64_t E, int64_t M, int64_t N) {
   const int64_t tiles = E * ((M + kTile - 1) / kTile) * ((N + kTile - 1) / kTile);
-  const int64_t want = 512 / (tiles < 1 ? 1 : tiles), most = T / E / (4 * kStep);
+  const int64_t want = kSlots / (tiles < 1 ? 1 : tiles), most = T / E / (8 * kStep);
   const int64_t s = want < most ? want : most;
   return static_cast<int32_t>(s < 1 ? 1 : s);
 }
@@ -173,6 +222,24 @@ int check_wgrad(int64_t T, int64_t E, int64_t M, int64_t N) {
   const int64_t tiles = E * ((M + kTile - 1) / kTile) * ((N + kTile - 1) / kTile);
   if (tiles > 0x7fffffff) return set_error(FP8Z1_ESHAPE, "ffn_wgrad: too many tiles");
   return FP8Z1_OK;
+}
+
+template <class H, bool F32OUT>
+void launch_wgrad_as(const WgradArgs& g, int nt, bool direct, dim3 grid, hipStream_t s) {
+  if (nt == 4)
+    hipLaunchKernelGGL((ffn_wgrad_kernel<H, F32OUT, 4, true>), grid, dim3(kThreads), 0, s, g);
+  else if (direct)
+    hipLaunchKernelGGL((ffn_wgrad_kernel<H, F32OUT, 2, true>), grid, dim3(kThreads), 0, s, g);
+  else
+    hipLaunchKernelGGL((ffn_wgrad_kernel<H, F32OUT, 2, false>), grid, dim3(kThreads), 0, s, g);
+}
+
+template <class H>
+void launch_wgrad(const WgradArgs& g, bool f32out, int nt, bool direct, dim3 grid, hipStream_t s) {
+  if (f32out)
+    launch_wgrad_as<H, true>(g, nt, direct, grid, s);
+  else
+    launch_wgrad_as<H, false>(g, nt, direct, grid, s);
 }
 
 bool misaligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
@@ -216,8 +283,10 @@ extern "C" int fp8z1_ffn_wgrad(int64_t T, int64_t E, int64_t M, int64_t N, int32
   g.E = static_cast<int32_t>(E);
   g.M = static_cast<int32_t>(M);
   g.N = static_cast<int32_t>(N);
+  const bool direct = M % 8 == 0 && N % 8 == 0 && !misaligned(p, 16) && !misaligned(q, 16);
+  const int nt = wgrad_nt(E, M, N, direct);
   g.mt = static_cast<int32_t>((M + kTile - 1) / kTile);
-  g.nt = static_cast<int32_t>((N + kTile - 1) / kTile);
+  g.nt = static_cast<int32_t>((N + nt * 64 - 1) / (nt * 64));
   g.accumulate = accumulate;
   g.splits = 1;
   const int32_t splits = wgrad_splits(T, E, M, N);
@@ -227,15 +296,11 @@ extern "C" int fp8z1_ffn_wgrad(int64_t T, int64_t E, int64_t M, int64_t N, int32
     g.part = static_cast<float*>(workspace);
   }
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const dim3 grid(static_cast<unsigned>(g.E * g.mt * g.nt * g.splits)), block(kThreads);
-  if (dtype == FP8Z1_BF16 && dw_dtype == FP8Z1_F32)
-    hipLaunchKernelGGL((ffn_wgrad_kernel<Bf16, true>), grid, block, 0, s, g);
-  else if (dtype == FP8Z1_BF16)
-    hipLaunchKernelGGL((ffn_wgrad_kernel<Bf16, false>), grid, block, 0, s, g);
-  else if (dw_dtype == FP8Z1_F32)
-    hipLaunchKernelGGL((ffn_wgrad_kernel<F16, true>), grid, block, 0, s, g);
+  const dim3 grid(static_cast<unsigned>(g.E * g.mt * g.nt * g.splits));
+  if (dtype == FP8Z1_BF16)
+    launch_wgrad<Bf16>(g, dw_dtype == FP8Z1_F32, nt, direct, grid, s);
   else
-    hipLaunchKernelGGL((ffn_wgrad_kernel<F16, false>), grid, block, 0, s, g);
+    launch_wgrad<F16>(g, dw_dtype == FP8Z1_F32, nt, direct, grid, s);
   rc = check_hip(hipGetLastError(), "ffn_wgrad: launch");
   if (rc || !g.part) return rc;
   const int64_t want = (size + 255) / 256;

@@ -88,14 +88,41 @@ __device__ __forceinline__ uint4 ld16(const uint8_t* p) {
   return make_uint4(r.x, r.y, r.z, r.w);
 }
 
-// The first `n` of 16 bytes, zeros after them (n may be <= 0 or >= 16); only those n
-// bytes are touched.
-__device__ __forceinline__ uint4 ld16_part(const uint8_t* p, int n) {
-  if (n >= 16) return ld16(p);
+// The first `n` of the 16 bytes at p, zeros after them (n may be <= 0 or >= 16), for a p that
+// lies `before` bytes behind the start of its row: the 16 bytes that end with the n-th are
+// read and shifted down, so that only bytes of the row are touched; rows of less than
+// 16 bytes are read byte by byte.
+__device__ __forceinline__ uint4 ld16_part(const uint8_t* p, int n, int before) {
+  uint4 r = make_uint4(0u, 0u, 0u, 0u);
+  if (n <= 0) return r;
+  const int back = n < 16 ? 16 - n : 0;
+  if (back <= before) {
+    r = ld16(p - back);
+    if (back) {
+      uint64_t lo = r.x | static_cast<uint64_t>(r.y) << 32, hi = r.z | static_cast<uint64_t>(r.w) << 32;
+      const int bits = 8 * (back & 7);
+      if (back >= 8) {
+        lo = hi;
+        hi = 0;
+      }
+      if (bits) {
+        lo = lo >> bits | hi << (64 - bits);
+        hi >>= bits;
+      }
+      r = make_uint4(static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32), static_cast<uint32_t>(hi),
+                     static_cast<uint32_t>(hi >> 32));
+    }
+    return r;
+  }
   uint32_t w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-  for (int i = 0; i < 16; ++i)
-    if (i < n) w[i / 4] |= static_cast<uint32_t>(p[i]) << (8 * (i % 4));
+#pragma unroll 1
+  for (int i = 0; i < n; ++i) {
+    const uint32_t b = static_cast<uint32_t>(p[i]) << (8 * (i & 3));
+    w[0] |= i < 4 ? b : 0u;
+    w[1] |= i >= 4 && i < 8 ? b : 0u;
+    w[2] |= i >= 8 && i < 12 ? b : 0u;
+    w[3] |= i >= 12 ? b : 0u;
+  }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 

@@ -41,55 +41,81 @@ struct Elem<F32> {
   typedef float type;
 };
 
-// 8 elements of chunk `ch` of a row.  VEC: 8 consecutive ones by 16-byte accesses.
-// Otherwise (odd widths, unaligned rows) 8 elements a workgroup's width apart, so that
-// neighbouring threads still touch neighbouring elements.
-template <class H, bool VEC>
-__device__ __forceinline__ void load8(const void* row, int32_t C, int ch, float (&v)[8]) {
+// 8 consecutive elements of a row: chunk `ch` of this thread, in 16-byte accesses at any
+// alignment of the elements (gfx950 runs in unaligned-access mode); those past the end
+// are 0 and not stored.
+typedef uint32_t v4u_a2_global_t __attribute__((ext_vector_type(4), aligned(2), address_space(1)));
+
+// the elements as they lie in memory (so that a row can be on its way while the row before it
+// is computed), and their values
+template <class H>
+struct Raw8 {
+  v4u_v_t x[sizeof(typename Elem<H>::type) * 8 / 16];
+};
+
+template <class H>
+__device__ __forceinline__ Raw8<H> fetch8(const void* row, int32_t C, int ch) {
   typedef typename Elem<H>::type E;
-  const E* p = static_cast<const E*>(row);
-  if (VEC) {
-    const int32_t c = (ch * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * 8;
-    if (c < C) {
-      E x[8];
+  constexpr int kVecs = sizeof(E) * 8 / 16;
+  const int32_t c = (ch * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * 8;
+  const E* p = static_cast<const E*>(row) + c;
+  Raw8<H> r;
 #pragma unroll
-      for (size_t i = 0; i < sizeof(x) / 16; ++i)
-        reinterpret_cast<uint4*>(x)[i] = reinterpret_cast<const uint4*>(p + c)[i];
+  for (int i = 0; i < kVecs; ++i) r.x[i] = v4u_v_t{0u, 0u, 0u, 0u};
+  if (c + 8 <= C) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = H::to_f32(x[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-    }
+    for (int i = 0; i < kVecs; ++i) r.x[i] = ((const v4u_a2_global_t*)(p))[i];
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int32_t c = (ch * 8 + i) * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x);
-      v[i] = c < C ? H::to_f32(p[c]) : 0.0f;
-    }
+    for (int i = 0; i < 8; ++i)
+      if (c + i < C) {
+        if constexpr (sizeof(E) == 2)
+          r.x[0][i / 2] |= static_cast<uint32_t>(p[i]) << (16 * (i % 2));
+        else
+          r.x[i / 4][i % 4] = __float_as_uint(p[i]);
+      }
+  }
+  return r;
+}
+
+template <class H>
+__device__ __forceinline__ void widen8f(const Raw8<H>& r, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (sizeof(typename Elem<H>::type) == 2)
+      v[i] = H::to_f32(static_cast<uint16_t>(r.x[0][i / 2] >> (16 * (i % 2))));
+    else
+      v[i] = __uint_as_float(r.x[i / 4][i % 4]);
   }
 }
 
-template <class H, bool VEC>
+template <class H>
+__device__ __forceinline__ void load8(const void* row, int32_t C, int ch, float (&v)[8]) {
+  widen8f<H>(fetch8<H>(row, C, ch), v);
+}
+
+template <class H>
 __device__ __forceinline__ void store8(void* row, int32_t C, int ch, const float (&v)[8]) {
   typedef typename Elem<H>::type E;
-  E* p = static_cast<E*>(row);
-  if (VEC) {
-    const int32_t c = (ch * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * 8;
-    if (c < C) {
-      E x[8];
+  constexpr int kVecs = sizeof(E) * 8 / 16;
+  const int32_t c = (ch * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * 8;
+  E* p = static_cast<E*>(row) + c;
+  if (c + 8 <= C) {
+    v4u_v_t x[kVecs];
+    if (sizeof(E) == 2) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = H::from_f32(v[i]);
+      for (int i = 0; i < 4; ++i)
+        x[0][i] = static_cast<uint32_t>(H::from_f32(v[2 * i])) | static_cast<uint32_t>(H::from_f32(v[2 * i + 1])) << 16;
+    } else {
 #pragma unroll
-      for (size_t i = 0; i < sizeof(x) / 16; ++i)
-        reinterpret_cast<uint4*>(p + c)[i] = reinterpret_cast<const uint4*>(x)[i];
+      for (int i = 0; i < 8; ++i) x[(i / 4) % kVecs][i % 4] = __float_as_uint(v[i]);
     }
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) ((v4u_a2_global_t*)(p))[i] = x[i];
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int32_t c = (ch * 8 + i) * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x);
-      if (c < C) p[c] = H::from_f32(v[i]);
-    }
+    for (int i = 0; i < 8; ++i)
+      if (c + i < C) p[i] = H::from_f32(v[i]);
   }
 }
 
@@ -102,15 +128,29 @@ __device__ __forceinline__ void* row_of(void* p, int64_t row, int32_t C) {
   return static_cast<typename Elem<H>::type*>(p) + row * C;
 }
 
+// Sum over the wave, the same in every lane: pairs, fours, eights and sixteens by lane
+// permutations within the vector unit, the last two steps through LDS.
+template <int CTRL>
+__device__ __forceinline__ float permuted(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float wave_fsum(float v) {
+  v += permuted<0xb1>(v);   // lanes 1 0 3 2 of each four
+  v += permuted<0x4e>(v);   // lanes 2 3 0 1 of each four
+  v += permuted<0x141>(v);  // each eight mirrored
+  v += permuted<0x140>(v);  // each sixteen mirrored
+  v += __shfl_xor(v, 16);
+  v += __shfl_xor(v, 32);
+  return v;
+}
+
 // Sums of N values over the workgroup, in a fixed order; every thread gets them.  `lds`
 // holds 16 N floats; calls in a row use different ones, so one barrier each is enough
 // (a set is written again only after the next set's barrier).
 template <int N>
 __device__ __forceinline__ void row_sums(float (&v)[N], float* lds) {
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1)
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += __shfl_xor(v[i], o);
+  for (int i = 0; i < N; ++i) v[i] = wave_fsum(v[i]);
   const int waves = blockDim.x >> 6, w = threadIdx.x >> 6;
   if (waves == 1) return;
   if ((threadIdx.x & 63) == 0)
@@ -129,10 +169,9 @@ __device__ __forceinline__ float rstd_of(float sum, int32_t C, float eps) {
 }
 
 // o + w, or 1 where there is no weight
-template <bool VEC>
 __device__ __forceinline__ void load_weight(const float* w, int32_t C, int ch, float offset, float (&v)[8]) {
   if (w) {
-    load8<F32, VEC>(w, C, ch, v);
+    load8<F32>(w, C, ch, v);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] += offset;
   } else {
@@ -142,12 +181,12 @@ __device__ __forceinline__ void load_weight(const float* w, int32_t C, int ch, f
 }
 
 // the gate's values of a row, times block_scale
-template <class H, bool VEC>
+template <class H>
 __device__ __forceinline__ void load_gate(const NormArgs& a, int64_t row, int ch, float (&g)[8]) {
   if (a.gate_kind == FP8Z1_GATE_CHANNEL) {
-    load8<F32, VEC>(a.gate, a.C, ch, g);
+    load8<F32>(a.gate, a.C, ch, g);
   } else if (a.gate_kind == FP8Z1_GATE_FULL) {
-    load8<H, VEC>(row_of<H>(a.gate, row, a.C), a.C, ch, g);
+    load8<H>(row_of<H>(a.gate, row, a.C), a.C, ch, g);
   } else {
     const float x = a.gate_kind == FP8Z1_GATE_TOKEN ? static_cast<const float*>(a.gate)[row] : 1.0f;
 #pragma unroll
@@ -157,7 +196,7 @@ __device__ __forceinline__ void load_gate(const NormArgs& a, int64_t row, int ch
   for (int i = 0; i < 8; ++i) g[i] *= a.block_scale;
 }
 
-template <class H, class R, bool VEC, int CH>
+template <class H, class R, int CH>
 __global__ __launch_bounds__(1024) void norm_join_kernel(NormArgs a) {
   __shared__ float lds[2][16];
   constexpr bool kHold = CH == 1;  // weights kept in registers over the rows
@@ -165,22 +204,22 @@ __global__ __launch_bounds__(1024) void norm_join_kernel(NormArgs a) {
 #pragma unroll
   for (int ch = 0; ch < CH; ++ch)
     if (kHold) {
-      load_weight<VEC>(a.w_post, a.C, ch, a.offset, wpost[ch]);
-      load_weight<VEC>(a.w_pre, a.C, ch, a.offset, wpre[ch]);
-      if (a.gate_kind == FP8Z1_GATE_CHANNEL) load_gate<H, VEC>(a, 0, ch, gate[ch]);
+      load_weight(a.w_post, a.C, ch, a.offset, wpost[ch]);
+      load_weight(a.w_pre, a.C, ch, a.offset, wpre[ch]);
+      if (a.gate_kind == FP8Z1_GATE_CHANNEL) load_gate<H>(a, 0, ch, gate[ch]);
     }
   for (int32_t row = blockIdx.x; row < a.T; row += gridDim.x) {
     float y[CH][8], z[CH][8];
     float sum[1] = {0.0f};
 #pragma unroll
     for (int ch = 0; ch < CH; ++ch) {
-      if (a.y) load8<H, VEC>(row_of<H>(a.y, row, a.C), a.C, ch, y[ch]);
-      load8<R, VEC>(row_of<R>(a.res, row, a.C), a.C, ch, z[ch]);
+      if (a.y) load8<H>(row_of<H>(a.y, row, a.C), a.C, ch, y[ch]);
+      load8<R>(row_of<R>(a.res, row, a.C), a.C, ch, z[ch]);
       if (!kHold) {
-        load_weight<VEC>(a.w_post, a.C, ch, a.offset, wpost[ch]);
-        load_weight<VEC>(a.w_pre, a.C, ch, a.offset, wpre[ch]);
+        load_weight(a.w_post, a.C, ch, a.offset, wpost[ch]);
+        load_weight(a.w_pre, a.C, ch, a.offset, wpre[ch]);
       }
-      if (a.y && (!kHold || a.gate_kind != FP8Z1_GATE_CHANNEL)) load_gate<H, VEC>(a, row, ch, gate[ch]);
+      if (a.y && (!kHold || a.gate_kind != FP8Z1_GATE_CHANNEL)) load_gate<H>(a, row, ch, gate[ch]);
       if (a.y)
 #pragma unroll
         for (int i = 0; i < 8; ++i) sum[0] = fmaf(y[ch][i], y[ch][i], sum[0]);
@@ -199,7 +238,7 @@ __global__ __launch_bounds__(1024) void norm_join_kernel(NormArgs a) {
         if (a.y) z[ch][i] = fmaf(gate[ch][i], y[ch][i] * r * wpost[ch][i], z[ch][i]);
         sum[0] = fmaf(z[ch][i], z[ch][i], sum[0]);
       }
-      if (a.z) store8<R, VEC>(row_of<R>(a.z, row, a.C), a.C, ch, z[ch]);
+      if (a.z) store8<R>(row_of<R>(a.z, row, a.C), a.C, ch, z[ch]);
     }
     if (a.n) {
       row_sums<1>(sum, lds[1]);
@@ -208,7 +247,7 @@ __global__ __launch_bounds__(1024) void norm_join_kernel(NormArgs a) {
       for (int ch = 0; ch < CH; ++ch) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) z[ch][i] = z[ch][i] * r * wpre[ch][i];
-        store8<H, VEC>(row_of<H>(a.n, row, a.C), a.C, ch, z[ch]);
+        store8<H>(row_of<H>(a.n, row, a.C), a.C, ch, z[ch]);
       }
     }
     if (!(a.w_post && a.n)) __syncthreads();  // only one of the two LDS sets is used per row
@@ -223,43 +262,88 @@ __global__ __launch_bounds__(1024) void norm_join_kernel(NormArgs a) {
 // Two rounds of row sums; the sums over rows are kept per thread (each owns its
 // columns), written per workgroup and added in order by the kernel below, so no
 // atomics decide their order.
-template <class H, class R, bool VEC, int CH>
+//
+// AHEAD (16-byte aligned rows of at most 8192): while a row is computed the next one is copied
+// to LDS, where each thread finds its own elements, so the loads overlap the row sums;
+// the registers are full with the weights and the column sums.
+template <class H, class R, int CH, bool AHEAD>
 __global__ __launch_bounds__(1024) void norm_join_bwd_kernel(NormArgs a) {
   __shared__ float lds[2][48];
+  extern __shared__ __attribute__((aligned(16))) uint8_t ahead[];
   constexpr bool kHold = CH == 1;
+  constexpr int kR = sizeof(typename Elem<R>::type) / 2, kH = sizeof(typename Elem<H>::type) / 2;  // KB of a wave's 512
   float wpost[CH][8], wpre[CH][8], gate[CH][8], spost[CH][8], spre[CH][8], sgate[CH][8];
 #pragma unroll
   for (int ch = 0; ch < CH; ++ch) {
     if (kHold) {
-      load_weight<VEC>(a.w_post, a.C, ch, a.offset, wpost[ch]);
-      load_weight<VEC>(a.w_pre, a.C, ch, a.offset, wpre[ch]);
-      if (a.gate_kind == FP8Z1_GATE_CHANNEL) load_gate<H, VEC>(a, 0, ch, gate[ch]);
+      load_weight(a.w_post, a.C, ch, a.offset, wpost[ch]);
+      load_weight(a.w_pre, a.C, ch, a.offset, wpre[ch]);
+      if (a.gate_kind == FP8Z1_GATE_CHANNEL) load_gate<H>(a, 0, ch, gate[ch]);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) spost[ch][i] = spre[ch][i] = sgate[ch][i] = 0.0f;
   }
   const float inv = 1.0f / static_cast<float>(a.C);
+
+  // a wave's part of LDS: y, dn, z, dz of its 512 columns; 16 bytes per lane and copy
+  const int lane = threadIdx.x & 63;
+  const int32_t c = static_cast<int32_t>(threadIdx.x) * 8, cin = min(c, a.C - 8);  // (lanes past the row copy its end)
+  uint8_t* const mine = ahead + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * ((2 * kH + 2 * kR) * 1024);
+  auto copy_row = [&](int32_t row) {
+    auto one = [&](const void* p, int per, int at) {  // per: 2-byte units of an element
+      const int64_t bytes = static_cast<int64_t>(a.C) * 2 * per;
+      const buffer_t b = make_buffer(static_cast<const uint8_t*>(p) + row * bytes, bytes);
+      for (int i = 0; i < per; ++i) copy16_to_lds(b, static_cast<uint32_t>(cin * 2 * per + 16 * i), mine + (at + i) * 1024);
+    };
+    if (a.y) one(a.y, kH, 0);
+    if (a.dn) {
+      one(a.dn, kH, kH);
+      one(a.res, kR, 2 * kH);
+    }
+    if (a.dz) one(a.dz, kR, 2 * kH + kR);
+  };
+  auto take = [&](auto tag, int at, float(&v)[8]) {
+    typedef decltype(tag) T;
+    Raw8<T> r;
+#pragma unroll
+    for (size_t i = 0; i < sizeof(r) / 16; ++i)
+      r.x[i] = *reinterpret_cast<const v4u_v_t*>(mine + (at + i) * 1024 + lane * 16);
+    widen8f<T>(r, v);
+    if (c >= a.C)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+  };
+  if (AHEAD && static_cast<int32_t>(blockIdx.x) < a.T) copy_row(blockIdx.x);
+
   for (int32_t row = blockIdx.x; row < a.T; row += gridDim.x) {
     float y[CH][8], z[CH][8], d[CH][8], dn[CH][8];
     float s1[3] = {0.0f, 0.0f, 0.0f};
+    if (AHEAD) wait_copies();
 #pragma unroll
     for (int ch = 0; ch < CH; ++ch) {
-      if (a.y) load8<H, VEC>(row_of<H>(a.y, row, a.C), a.C, ch, y[ch]);
-      if (a.dn) {
-        load8<H, VEC>(row_of<H>(a.dn, row, a.C), a.C, ch, dn[ch]);
-        load8<R, VEC>(row_of<R>(a.res, row, a.C), a.C, ch, z[ch]);
-      }
-      if (a.dz) {
-        load8<R, VEC>(row_of<R>(a.dz, row, a.C), a.C, ch, d[ch]);
+      if (AHEAD) {
+        if (a.y) take(H{}, 0, y[ch]);
+        if (a.dn) {
+          take(H{}, kH, dn[ch]);
+          take(R{}, 2 * kH, z[ch]);
+        }
+        if (a.dz) take(R{}, 2 * kH + kR, d[ch]);
       } else {
+        if (a.y) load8<H>(row_of<H>(a.y, row, a.C), a.C, ch, y[ch]);
+        if (a.dn) {
+          load8<H>(row_of<H>(a.dn, row, a.C), a.C, ch, dn[ch]);
+          load8<R>(row_of<R>(a.res, row, a.C), a.C, ch, z[ch]);
+        }
+        if (a.dz) load8<R>(row_of<R>(a.dz, row, a.C), a.C, ch, d[ch]);
+      }
+      if (!a.dz)
 #pragma unroll
         for (int i = 0; i < 8; ++i) d[ch][i] = 0.0f;
-      }
       if (!kHold) {
-        load_weight<VEC>(a.w_post, a.C, ch, a.offset, wpost[ch]);
-        load_weight<VEC>(a.w_pre, a.C, ch, a.offset, wpre[ch]);
+        load_weight(a.w_post, a.C, ch, a.offset, wpost[ch]);
+        load_weight(a.w_pre, a.C, ch, a.offset, wpre[ch]);
       }
-      if (a.y && (!kHold || a.gate_kind != FP8Z1_GATE_CHANNEL)) load_gate<H, VEC>(a, row, ch, gate[ch]);
+      if (a.y && (!kHold || a.gate_kind != FP8Z1_GATE_CHANNEL)) load_gate<H>(a, row, ch, gate[ch]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         if (a.y) s1[0] = fmaf(y[ch][i], y[ch][i], s1[0]);
@@ -269,13 +353,17 @@ __global__ __launch_bounds__(1024) void norm_join_bwd_kernel(NormArgs a) {
         }
       }
     }
+    if (AHEAD && row + static_cast<int32_t>(gridDim.x) < a.T) {
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // this row's elements have left LDS
+      copy_row(row + gridDim.x);
+    }
     row_sums<3>(s1, lds[0]);
     const float ry = a.w_post ? rstd_of(s1[0], a.C, a.eps) : 1.0f;
     const float rz = rstd_of(s1[1], a.C, a.eps);
     const float mz = s1[2] * rz * rz * inv;  // mean(v z^) rstd(z)
     float s2[2] = {0.0f, 0.0f};
 #pragma unroll
-    for (int ch = 0; ch < CH; ++ch)
+    for (int ch = 0; ch < CH; ++ch) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         if (a.dn) {
@@ -283,7 +371,7 @@ __global__ __launch_bounds__(1024) void norm_join_bwd_kernel(NormArgs a) {
           spre[ch][i] = fmaf(dn[ch][i], z[ch][i] * rz, spre[ch][i]);
         }
         if (a.y) {
-          y[ch][i] *= ry;                               // y^ (or y)
+          y[ch][i] *= ry;  // y^ (or y)
           const float p = y[ch][i] * wpost[ch][i];
           const float dp = gate[ch][i] * d[ch][i];
           spost[ch][i] = fmaf(dp, y[ch][i], spost[ch][i]);
@@ -292,62 +380,72 @@ __global__ __launch_bounds__(1024) void norm_join_bwd_kernel(NormArgs a) {
           s2[1] = fmaf(d[ch][i], p, s2[1]);
         }
       }
+      if (a.dres) {
+        float o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = a.res_scale * d[ch][i];
+        store8<R>(row_of<R>(a.dres, row, a.C), a.C, ch, o);
+      }
+    }
     row_sums<2>(s2, lds[1]);
     const float my = s2[0] * inv;  // mean(dp (o + w_post) y^)
+    if (a.y)
 #pragma unroll
-    for (int ch = 0; ch < CH; ++ch) {
-      if (a.y) {
+      for (int ch = 0; ch < CH; ++ch) {
         float o[8];
         if (a.gate_kind == FP8Z1_GATE_FULL && a.dgate) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) o[i] = a.block_scale * d[ch][i] * (y[ch][i] * wpost[ch][i]);
-          store8<H, VEC>(row_of<H>(a.dgate, row, a.C), a.C, ch, o);
+          store8<H>(row_of<H>(a.dgate, row, a.C), a.C, ch, o);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           o[i] = gate[ch][i] * d[ch][i];
           if (a.w_post) o[i] = ry * fmaf(-y[ch][i], my, o[i] * wpost[ch][i]);
         }
-        if (a.dy) store8<H, VEC>(row_of<H>(a.dy, row, a.C), a.C, ch, o);
+        if (a.dy) store8<H>(row_of<H>(a.dy, row, a.C), a.C, ch, o);
       }
-      if (a.dres) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) d[ch][i] *= a.res_scale;
-        store8<R, VEC>(row_of<R>(a.dres, row, a.C), a.C, ch, d[ch]);
-      }
-    }
     if (a.gate_kind == FP8Z1_GATE_TOKEN && a.dgate && threadIdx.x == 0)
       static_cast<float*>(a.dgate)[row] = a.block_scale * s2[1];
   }
   const int64_t set = static_cast<int64_t>(gridDim.x) * a.C;
 #pragma unroll
   for (int ch = 0; ch < CH; ++ch) {
-    if (a.want_post) store8<F32, VEC>(a.part + blockIdx.x * static_cast<int64_t>(a.C), a.C, ch, spost[ch]);
-    if (a.want_pre) store8<F32, VEC>(a.part + set + blockIdx.x * static_cast<int64_t>(a.C), a.C, ch, spre[ch]);
+    if (a.want_post) store8<F32>(a.part + blockIdx.x * static_cast<int64_t>(a.C), a.C, ch, spost[ch]);
+    if (a.want_pre) store8<F32>(a.part + set + blockIdx.x * static_cast<int64_t>(a.C), a.C, ch, spre[ch]);
     if (a.want_gate) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) sgate[ch][i] *= a.block_scale;
-      store8<F32, VEC>(a.part + 2 * set + blockIdx.x * static_cast<int64_t>(a.C), a.C, ch, sgate[ch]);
+      store8<F32>(a.part + 2 * set + blockIdx.x * static_cast<int64_t>(a.C), a.C, ch, sgate[ch]);
     }
   }
 }
 
 // Column sums of the workgroups' partial sums (blockIdx.y: which gradient), in a fixed
-// order: 4 waves take every fourth workgroup's row, then their sums are added in order.
-__global__ __launch_bounds__(256) void norm_columns_kernel(const float* __restrict__ part, int32_t groups, int32_t C,
-                                                           float* o0, float* o1, float* o2) {
-  __shared__ float lds[4][64];
+// order: wave w of 16 takes rows w, w + 16, ... (four at a time, so that several loads are on
+// their way), then the waves' sums are added in order.
+__global__ __launch_bounds__(1024) void norm_columns_kernel(const float* __restrict__ part, int32_t groups, int32_t C,
+                                                            float* o0, float* o1, float* o2) {
+  __shared__ float lds[16][64];
   float* out = blockIdx.y == 0 ? o0 : blockIdx.y == 1 ? o1 : o2;
   if (!out) return;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int32_t c = static_cast<int32_t>(blockIdx.x) * 64 + lane;
   const float* p = part + static_cast<int64_t>(blockIdx.y) * groups * C;
-  float v = 0.0f;
+  float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   if (c < C)
-    for (int32_t g = w; g < groups; g += 4) v += p[static_cast<int64_t>(g) * C + c];
-  lds[w][lane] = v;
+    for (int32_t g = w; g < groups; g += 64)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (g + 16 * i < groups) v[i] += p[static_cast<int64_t>(g + 16 * i) * C + c];
+  lds[w][lane] = (v[0] + v[1]) + (v[2] + v[3]);
   __syncthreads();
-  if (w == 0 && c < C) out[c] = lds[0][lane] + lds[1][lane] + lds[2][lane] + lds[3][lane];
+  if (w == 0 && c < C) {
+    float sum = lds[0][lane];
+#pragma unroll
+    for (int k = 1; k < 16; ++k) sum += lds[k][lane];
+    out[c] = sum;
+  }
 }
 
 constexpr int64_t kMaxC = FP8Z1_NORM_MAX_WIDTH;
@@ -403,56 +501,53 @@ NormArgs base_args(const fp8z1_norm* f, const void* y, const void* res, const fl
   return a;
 }
 
+bool rows_aligned(const NormArgs& a) {
+  return !misaligned(a.y, 16) && !misaligned(a.res, 16) && !misaligned(a.dz, 16) && !misaligned(a.dn, 16);
+}
+
 template <class H, class R, bool BWD>
-void launch_typed(const NormArgs& a, bool vec, dim3 g, dim3 b, hipStream_t s) {
+void launch_typed(const NormArgs& a, dim3 g, dim3 b, hipStream_t s) {
   const bool one = a.C <= 8192;
-#define FP8Z1_NORM_GO(V, N)                                                        \
-  if (BWD)                                                                         \
-    hipLaunchKernelGGL((norm_join_bwd_kernel<H, R, V, N>), g, b, 0, s, a);         \
-  else                                                                             \
-    hipLaunchKernelGGL((norm_join_kernel<H, R, V, N>), g, b, 0, s, a)
-  if (vec && one) {
-    FP8Z1_NORM_GO(true, 1);
-  } else if (vec) {
-    FP8Z1_NORM_GO(true, 2);
-  } else if (one) {
-    FP8Z1_NORM_GO(false, 1);
-  } else {
-    FP8Z1_NORM_GO(false, 2);
-  }
-#undef FP8Z1_NORM_GO
+  constexpr size_t kBytes = 2 * (sizeof(typename Elem<H>::type) + sizeof(typename Elem<R>::type)) * 8;  // per thread
+  if (BWD && one && a.C % 8 == 0 && rows_aligned(a))
+    hipLaunchKernelGGL((norm_join_bwd_kernel<H, R, 1, true>), g, b, kBytes * b.x, s, a);
+  else if (BWD && one)
+    hipLaunchKernelGGL((norm_join_bwd_kernel<H, R, 1, false>), g, b, 0, s, a);
+  else if (BWD)
+    hipLaunchKernelGGL((norm_join_bwd_kernel<H, R, 2, false>), g, b, 0, s, a);
+  else if (one)
+    hipLaunchKernelGGL((norm_join_kernel<H, R, 1>), g, b, 0, s, a);
+  else
+    hipLaunchKernelGGL((norm_join_kernel<H, R, 2>), g, b, 0, s, a);
 }
 
 template <bool BWD>
-void launch(const fp8z1_norm* f, const NormArgs& a, bool vec, int64_t groups, hipStream_t s) {
+void launch(const fp8z1_norm* f, const NormArgs& a, int64_t groups, hipStream_t s) {
   const dim3 g(static_cast<unsigned>(groups)), b(static_cast<unsigned>(threads_for(f->C)));
   const bool wide = f->res_dtype == FP8Z1_F32;
   if (f->dtype == FP8Z1_F32)
-    launch_typed<F32, F32, BWD>(a, vec, g, b, s);
+    launch_typed<F32, F32, BWD>(a, g, b, s);
   else if (f->dtype == FP8Z1_BF16 && wide)
-    launch_typed<Bf16, F32, BWD>(a, vec, g, b, s);
+    launch_typed<Bf16, F32, BWD>(a, g, b, s);
   else if (f->dtype == FP8Z1_BF16)
-    launch_typed<Bf16, Bf16, BWD>(a, vec, g, b, s);
+    launch_typed<Bf16, Bf16, BWD>(a, g, b, s);
   else if (wide)
-    launch_typed<F16, F32, BWD>(a, vec, g, b, s);
+    launch_typed<F16, F32, BWD>(a, g, b, s);
   else
-    launch_typed<F16, F16, BWD>(a, vec, g, b, s);
+    launch_typed<F16, F16, BWD>(a, g, b, s);
 }
 
 size_t elem_size(int32_t dtype) { return dtype == FP8Z1_F32 ? 4 : 2; }
 
-// Every pointer aligned to its elements (else an error), and whether 16-byte accesses fit.
+// Every pointer aligned to its elements
 int check_alignment(const fp8z1_norm* f, std::initializer_list<const void*> act, std::initializer_list<const void*> res,
-                    std::initializer_list<const void*> f32, const void* gate_any, bool& vec, const char* what) {
-  vec = f->C % 8 == 0;
+                    std::initializer_list<const void*> f32, std::initializer_list<const void*> gates,
+                    const char* what) {
   bool bad = false;
-  for (const void* p : act) bad |= misaligned(p, elem_size(f->dtype)), vec &= !misaligned(p, 16);
-  for (const void* p : res) bad |= misaligned(p, elem_size(f->res_dtype)), vec &= !misaligned(p, 16);
-  for (const void* p : f32) bad |= misaligned(p, 4), vec &= !misaligned(p, 16);
-  if (f->gate != FP8Z1_GATE_NONE) {
-    bad |= misaligned(gate_any, f->gate == FP8Z1_GATE_FULL ? elem_size(f->dtype) : 4);
-    vec &= f->gate == FP8Z1_GATE_TOKEN || !misaligned(gate_any, 16);
-  }
+  for (const void* p : act) bad |= misaligned(p, elem_size(f->dtype));
+  for (const void* p : res) bad |= misaligned(p, elem_size(f->res_dtype));
+  for (const void* p : f32) bad |= misaligned(p, 4);
+  for (const void* p : gates) bad |= misaligned(p, f->gate == FP8Z1_GATE_FULL ? elem_size(f->dtype) : 4);
   return bad ? set_error(FP8Z1_EINVAL, std::string(what) + ": misaligned argument") : FP8Z1_OK;
 }
 
@@ -468,13 +563,12 @@ extern "C" int fp8z1_norm_join(const fp8z1_norm* f, const void* y, const void* r
   if (rc) return rc;
   if (f->T == 0) return FP8Z1_OK;
   if (!res || (!z && !n)) return set_error(FP8Z1_EINVAL, "norm_join: NULL argument");
-  bool vec = false;
-  rc = check_alignment(f, {y, n}, {res, z}, {w_post, w_pre}, gate, vec, what);
+  rc = check_alignment(f, {y, n}, {res, z}, {w_post, w_pre}, {gate}, what);
   if (rc) return rc;
   NormArgs a = base_args(f, y, res, w_post, gate, w_pre);
   a.z = z;
   a.n = n;
-  launch<false>(f, a, vec, groups_for(f->T, f->C, kFwdWaves), static_cast<hipStream_t>(stream));
+  launch<false>(f, a, groups_for(f->T, f->C, kFwdWaves), static_cast<hipStream_t>(stream));
   return check_hip(hipGetLastError(), "norm_join: launch");
 }
 
@@ -499,13 +593,7 @@ extern "C" int fp8z1_norm_join_bwd(const fp8z1_norm* f, const void* dz, const vo
   if (f->T && dy && !y) return set_error(FP8Z1_EINVAL, "norm_join_bwd: dy needs y");
   if ((dw_post && !w_post) || (dw_pre && !w_pre)) return set_error(FP8Z1_EINVAL, "norm_join_bwd: gradient of no weight");
   if (dgate && f->gate == FP8Z1_GATE_NONE) return set_error(FP8Z1_EINVAL, "norm_join_bwd: gradient of no gate");
-  bool vec = false;
-  rc = check_alignment(f, {y, dn, dy}, {z, dz, dres}, {w_post, w_pre, dw_post, dw_pre}, gate, vec, what);
-  if (!rc && dgate) {
-    bool v2 = false;
-    rc = check_alignment(f, {}, {}, {}, dgate, v2, what);
-    vec &= v2;
-  }
+  rc = check_alignment(f, {y, dn, dy}, {z, dz, dres}, {w_post, w_pre, dw_post, dw_pre}, {gate, dgate}, what);
   if (rc) return rc;
   float* gate_cols = f->gate == FP8Z1_GATE_CHANNEL ? static_cast<float*>(dgate) : nullptr;
   const bool sums = dw_post || dw_pre || gate_cols;
@@ -529,12 +617,12 @@ extern "C" int fp8z1_norm_join_bwd(const fp8z1_norm* f, const void* dz, const vo
     a.want_post = dw_post != nullptr;
     a.want_pre = dw_pre != nullptr;
     a.want_gate = gate_cols != nullptr;
-    launch<true>(f, a, vec, groups, s);
+    launch<true>(f, a, groups, s);
     rc = check_hip(hipGetLastError(), "norm_join_bwd: launch");
     if (rc) return rc;
   }
   if (sums) {
-    hipLaunchKernelGGL(norm_columns_kernel, dim3(static_cast<unsigned>((f->C + 63) / 64), 3), dim3(256), 0, s,
+    hipLaunchKernelGGL(norm_columns_kernel, dim3(static_cast<unsigned>((f->C + 63) / 64), 3), dim3(1024), 0, s,
                        static_cast<const float*>(workspace), static_cast<int32_t>(groups), static_cast<int32_t>(f->C),
                        dw_post, dw_pre, gate_cols);
     rc = check_hip(hipGetLastError(), "norm_join_bwd: sums launch");
