@@ -37,7 +37,7 @@ __global__ __launch_bounds__(kThreads, 2) void ffn_wgrad_kernel(WgradArgs g) {
   typedef typename H::v8 v8;
   constexpr int kCols = NT * 64, kQBytes = kCols * kStep * 2, kStage = kPBytes + kQBytes;
   constexpr int kPC = kPBytes / 16 / kThreads, kQC = kQBytes / 16 / kThreads;  // chunks per thread
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kStage];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[3 * kStage];
   const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6), wm = w >> 1, wn = w & 1;
 
   // tiles in contiguous runs per XCD, in groups of kGroup tile rows by all tile columns
@@ -122,23 +122,33 @@ __global__ __launch_bounds__(kThreads, 2) void ffn_wgrad_kernel(WgradArgs g) {
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[i][j] = zero;
 
+  // Three stages: direct copies run two stages ahead (one stage's matrix instructions take
+  // less time than a copy), loads through registers one.
+  int at = 0;  // stage in use
   if (s0 < s1) {
     fetch(s0, lds);
     put(lds);
+    if (DIRECT && s0 + 1 < s1) fetch(s0 + 1, lds + kStage);
   }
   for (int32_t s = s0; s < s1; ++s) {
-    const int buf = (s - s0) & 1;
-    uint8_t* const here = lds + buf * kStage;
-    uint8_t* const there = lds + (buf ^ 1) * kStage;
-    if (DIRECT) wait_copies();
+    uint8_t* const here = lds + at * kStage;
+    const int32_t ahead = s + (DIRECT ? 2 : 1);
+    uint8_t* const there = lds + (at + (DIRECT ? 2 : 1)) % 3 * kStage;
+    at = at == 2 ? 0 : at + 1;
+    if (DIRECT) {
+      if (s + 1 < s1)
+        wait_copies<kPC + kQC>();
+      else
+        wait_copies<0>();
+    }
     __syncthreads();
     const int32_t left = hi - lo - s * kStep;
     if (DIRECT && left < kStep) {  // the run ends inside the stage: rows past it count nothing
       const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-      for (int at = left * (kTile / 8) + t; at < kStep * (kTile / 8); at += kThreads)
-        *reinterpret_cast<uint4*>(here + at * 16) = z;
-      for (int at = left * (kCols / 8) + t; at < kStep * (kCols / 8); at += kThreads)
-        *reinterpret_cast<uint4*>(here + kPBytes + at * 16) = z;
+      for (int c = left * (kTile / 8) + t; c < kStep * (kTile / 8); c += kThreads)
+        *reinterpret_cast<uint4*>(here + c * 16) = z;
+      for (int c = left * (kCols / 8) + t; c < kStep * (kCols / 8); c += kThreads)
+        *reinterpret_cast<uint4*>(here + kPBytes + c * 16) = z;
       __syncthreads();
     }
     v8 a[2][2], b[2][NT];
@@ -149,7 +159,7 @@ __global__ __launch_bounds__(kThreads, 2) void ffn_wgrad_kernel(WgradArgs g) {
       for (int j = 0; j < NT; ++j) b[ks][j] = operand(here + kPBytes, kCols * 2, (wn * NT + j) * 32, ks);
     };
     read(0);
-    if (s + 1 < s1) fetch(s + 1, there);
+    if (ahead < s1) fetch(ahead, there);
     read(1);
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks)
@@ -158,7 +168,7 @@ __global__ __launch_bounds__(kThreads, 2) void ffn_wgrad_kernel(WgradArgs g) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) acc[i][j] = H::mma32(a[ks][i], b[ks][j], acc[i][j]);
     __builtin_amdgcn_sched_barrier(0);
-    if (s + 1 < s1) put(there);
+    if (ahead < s1) put(there);
   }
 
   const int64_t size = static_cast<int64_t>(g.E) * g.M * g.N;
