@@ -18,6 +18,7 @@ A training step over one block (see ``examples/train_ffn_layer.py``):
 """
 from __future__ import annotations
 
+import functools
 from typing import Dict, Optional, Sequence, Tuple
 
 import torch
@@ -43,15 +44,25 @@ def _device(x: torch.Tensor, what: str) -> int:
     return dev
 
 
-def _check(x: torch.Tensor, dev: int, dtype: torch.dtype, shape: Sequence[int], what: str) -> int:
+def _check(x: torch.Tensor, dev: int, dtype: torch.dtype, shape: Tuple[int, ...], what: str) -> int:
     """The address of a contiguous tensor of this type and shape on this device."""
-    if x.shape != shape:
-        _fail(f"{what}: shape {tuple(x.shape)}, expected {tuple(shape)}")
-    if x.dtype != dtype:
-        _fail(f"{what}: dtype {x.dtype}, expected {dtype}")
-    if x.get_device() != dev or not x.is_contiguous():
-        _fail(f"{what}: must be a contiguous tensor on device {dev}")
+    if x.shape != shape or x.dtype != dtype or x.get_device() != dev or not x.is_contiguous():
+        _fail(f"{what}: {x.dtype} {tuple(x.shape)} on {x.device}{'' if x.is_contiguous() else ', not contiguous'}; "
+              f"expected a contiguous {dtype} {tuple(shape)} on device {dev}")
     return x.data_ptr()
+
+
+@functools.lru_cache(maxsize=256)
+def _ffn_workspace(T: int, E: int, D: int, F: int) -> int:
+    return L.fp8z1_ffn_workspace_bytes(L.Ffn(T, E, D, F, L.BF16, L.ACT_SILU))
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_workspace(T: int, C: int) -> int:
+    return L.fp8z1_norm_join_bwd_workspace_bytes(L.Norm(T, C, L.F32, L.F32, L.GATE_NONE, 0.0, 1.0, 1.0, 0.0, 0))
+
+
+_wgrad_workspace = functools.lru_cache(maxsize=256)(L.fp8z1_ffn_wgrad_workspace_bytes)
 
 
 def _weight(w: Weight, dev: int, e: int, r: int, c: int, what: str) -> Tuple[int, int]:
@@ -99,7 +110,7 @@ def ffn_forward(x: torch.Tensor, w_gate: Weight, w_up: Weight, w_down: Weight,
     off = _offsets(offsets, dev, E, what)
     a, y = _empty(x, T, F), _empty(x, T, D)
     h, u = (_empty(x, T, F), _empty(x, T, F)) if save else (None, None)
-    n = L.fp8z1_ffn_workspace_bytes(f)
+    n = _ffn_workspace(T, E, D, F)
     ws = _scratch(x, n)
     pw, pa, stream = L._ptr(ws), a.data_ptr(), L._current_stream(dev)
     L._check(L.lib.fp8z1_ffn_up(f, px, *gate, *up, off, L._ptr(h), L._ptr(u), pa, pw, n, stream), what)
@@ -119,7 +130,7 @@ def ffn_backward_data(dy: torch.Tensor, h: torch.Tensor, u: torch.Tensor, w_gate
                       _weight(w_down, dev, E, D, F, f"{what} down"))
     off = _offsets(offsets, dev, E, what)
     dh, du, a, dx = _empty(dy, T, F), _empty(dy, T, F), _empty(dy, T, F), _empty(dy, T, D)
-    n = L.fp8z1_ffn_workspace_bytes(f)
+    n = _ffn_workspace(T, E, D, F)
     ws = _scratch(dy, n)
     pw, pdh, pdu, stream = L._ptr(ws), dh.data_ptr(), du.data_ptr(), L._current_stream(dev)
     L._check(L.lib.fp8z1_ffn_down_bwd(f, py, *down, ph, pu, off, pdh, pdu, a.data_ptr(), pw, n, stream), what)
@@ -144,7 +155,7 @@ def ffn_weight_gradient(p: torch.Tensor, q: torch.Tensor, n_experts: int = 1,
     else:
         dw = out
         _check(dw, dev, torch.float32, (n_experts, M, N), f"{what} out")
-    n = L.fp8z1_ffn_wgrad_workspace_bytes(T, n_experts, M, N)
+    n = _wgrad_workspace(T, n_experts, M, N)
     ws = _scratch(p, n)
     L._check(L.lib.fp8z1_ffn_wgrad(T, n_experts, M, N, _CODE[p.dtype], pp, pq, off, _CODE[dw.dtype], dw.data_ptr(),
                                    int(out is not None), L._ptr(ws), n, L._current_stream(dev)), what)
@@ -226,7 +237,7 @@ def norm_join_backward(dz: Optional[torch.Tensor], dn: Optional[torch.Tensor], y
         "dw_post": None if w_post is None else w_post.new_empty((C,)),
         "dgate": None if gate is None else gate.new_empty(gate.shape),
         "dw_pre": None if w_pre is None else w_pre.new_empty((C,))}
-    n = L.fp8z1_norm_join_bwd_workspace_bytes(f)
+    n = _norm_workspace(T, C)
     ws = _scratch(z, n)
     L._check(L.lib.fp8z1_norm_join_bwd(f, pdz, pdn, py, pz, wpost, pg, wpre, *(L._ptr(v) for v in out.values()),
                                        L._ptr(ws), n, L._current_stream(dev)), what)

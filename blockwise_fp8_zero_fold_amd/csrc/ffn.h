@@ -49,10 +49,18 @@ __device__ __forceinline__ int32_t wave_isum(int32_t v) {
 // Work items of a launch.  The tiles (row tiles of all experts by tile columns) are counted on
 // the device, which alone knows the offsets; the grid holds the most there can be.
 // The card runs kSlots workgroups at once (two on each compute unit).  Where the tiles
-// past the last full round would leave most of it idle, they are split along k instead
-// (`splits` parts each, at least 8 scale blocks of k per part), the parts' float32 sums
-// go to the workspace and a second kernel adds them in order and finishes the tiles.
+// past the last full round would leave most of it idle, they are split along k instead into
+// `splits` parts each, the parts' float32 sums go to the workspace and a second kernel
+// (some 5 us) adds them in order and finishes the tiles.  A part is at least 8 scale
+// blocks of k behind full rounds, and 2 where there is no full round.
 constexpr int32_t kSlots = 512;
+
+__host__ __device__ __forceinline__ int32_t tile_splits(int64_t tiles, int32_t blocks) {
+  const int32_t rest = static_cast<int32_t>(tiles % kSlots);
+  if (!rest) return 1;
+  const int32_t s = kSlots / rest, most = blocks / (tiles < kSlots ? 2 : 8);
+  return s < most ? s : most;
+}
 
 struct Plan {
   int32_t tiles;   // all tiles
@@ -70,11 +78,14 @@ __device__ __forceinline__ int32_t row_tiles(const int32_t* offsets, int32_t T, 
 
 template <int ROWS>
 __device__ __forceinline__ Plan plan_tiles(const int32_t* offsets, int32_t T, int32_t E, int32_t ncols,
-                                           int32_t blocks, bool may_split, int32_t& rowtiles) {
+                                           int32_t blocks, bool may_split, int32_t& rowtiles, int32_t& first) {
   const int lane = threadIdx.x & 63;
   int32_t total = 0;
+  first = 0;  // row tiles of expert `lane`
   if (offsets) {
-    for (int32_t e0 = 0; e0 < E; e0 += 64) total += wave_isum(e0 + lane < E ? row_tiles<ROWS>(offsets, T, e0 + lane) : 0);
+    first = lane < E ? row_tiles<ROWS>(offsets, T, lane) : 0;
+    total = wave_isum(first);
+    for (int32_t e0 = 64; e0 < E; e0 += 64) total += wave_isum(e0 + lane < E ? row_tiles<ROWS>(offsets, T, e0 + lane) : 0);
   } else {
     total = (T + ROWS - 1) / ROWS;
   }
@@ -85,12 +96,10 @@ __device__ __forceinline__ Plan plan_tiles(const int32_t* offsets, int32_t T, in
   p.whole = p.tiles;
   p.splits = 1;
   const int32_t rest = p.tiles % kSlots;
-  if (may_split && rest) {
-    const int32_t s = min(kSlots / rest, blocks / 8);
-    if (s > 1) {
-      p.whole = p.tiles - rest;
-      p.splits = s;
-    }
+  const int32_t s = tile_splits(p.tiles, blocks);
+  if (may_split && s > 1) {
+    p.whole = p.tiles - rest;
+    p.splits = s;
   }
   return p;
 }
@@ -108,7 +117,7 @@ __device__ __forceinline__ int32_t xcd_run(int32_t b, int32_t n) {
 constexpr int kGroup = 8;
 template <int ROWS>
 __device__ __forceinline__ bool find_tile(const int32_t* offsets, int32_t T, int32_t E, int32_t ncols, int32_t rowtiles,
-                                          int32_t id, int32_t& e, int32_t& lo, int32_t& hi, int32_t& m0,
+                                          int32_t first, int32_t id, int32_t& e, int32_t& lo, int32_t& hi, int32_t& m0,
                                           int32_t& col) {
   const int lane = threadIdx.x & 63;
   const int32_t grp = id / (kGroup * ncols), in = id - grp * kGroup * ncols;
@@ -118,7 +127,7 @@ __device__ __forceinline__ bool find_tile(const int32_t* offsets, int32_t T, int
   e = 0;
   if (offsets) {
     for (int32_t e0 = 0; e0 < E; e0 += 64) {
-      const int32_t n = e0 + lane < E ? row_tiles<ROWS>(offsets, T, e0 + lane) : 0;
+      const int32_t n = e0 == 0 ? first : e0 + lane < E ? row_tiles<ROWS>(offsets, T, e0 + lane) : 0;
       int32_t upto = n;  // tiles of this chunk's experts up to and with this lane's
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) {

@@ -12,22 +12,26 @@
 namespace fp8z1 {
 namespace {
 
-template <class H, int KIND, int WAVES, int TT, bool ALIGNED>
+//
+// PAIR (kFfnUp where workgroups are few): the 16 rows of the matrix tile are 8 of gate and the
+// same 8 of up, which makes twice as many workgroups.
+template <class H, int KIND, int WAVES, int TT, bool ALIGNED, bool PAIR>
 __global__ __launch_bounds__(WAVES * 64) void ffn_rows_kernel(FfnArgs p) {
   constexpr bool kUp = KIND == kFfnUp;
-  constexpr int kM = kUp ? 2 : 1;  // matrices
+  constexpr int kM = kUp && !PAIR ? 2 : 1;  // matrix tiles
+  constexpr int kRowsN = PAIR ? 8 : 16;     // columns of the result per workgroup
   typedef typename H::v8 v8;
   __shared__ f32x4 sums[WAVES][kM * TT][64];
   const int32_t e = blockIdx.y;
   int32_t lo, hi;
   expert_rows(p.offsets, p.T, e, lo, hi);
-  const int32_t N = p.N, K = p.K, n0 = static_cast<int32_t>(blockIdx.x) * 16;
+  const int32_t N = p.N, K = p.K, n0 = static_cast<int32_t>(blockIdx.x) * kRowsN;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
   const int32_t kb = (K + kB - 1) / kB, nb = (N + kB - 1) / kB;
-  const int64_t row = (static_cast<int64_t>(e) * N + min(n0 + r, N - 1)) * K + g * 32;
-  const uint8_t* const wt[2] = {p.w0 + row, kUp ? p.w1 + row : nullptr};
+  const int64_t row = (static_cast<int64_t>(e) * N + min(n0 + r % kRowsN, N - 1)) * K + g * 32;
+  const uint8_t* const wt[2] = {(PAIR && r >= 8 ? p.w1 : p.w0) + row, kM == 2 ? p.w1 + row : nullptr};
   const int64_t sat = (static_cast<int64_t>(e) * nb + n0 / kB) * kb;
-  const float* const sc[2] = {p.s0 + sat, kUp ? p.s1 + sat : nullptr};
+  const float* const sc[2] = {(PAIR && g >= 2 ? p.s1 : p.s0) + sat, kM == 2 ? p.s1 + sat : nullptr};  // of this lane's results
 
   struct Block {
     uint4 c[kM][2];
@@ -105,7 +109,7 @@ __global__ __launch_bounds__(WAVES * 64) void ffn_rows_kernel(FfnArgs p) {
       for (int t = 0; t < TT; ++t) sums[w][m * TT + t][lane] = acc[m][t];
     __syncthreads();
     if (w < TT) {
-      f32x4 v[kM];
+      f32x4 v[2];
 #pragma unroll
       for (int m = 0; m < kM; ++m) {
         v[m] = sums[0][m * TT + w][lane];
@@ -113,18 +117,21 @@ __global__ __launch_bounds__(WAVES * 64) void ffn_rows_kernel(FfnArgs p) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) v[m][i] += sums[k][m * TT + w][lane][i];
       }
+      if (PAIR)  // the up results of a column are in the upper lanes
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[1][i] = __shfl_xor(v[0][i], 32);
       const int32_t t = t0 + 16 * w + r;
-      if (t < hi) {
+      if (t < hi && (!PAIR || g < 2)) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int32_t n = n0 + 4 * g + i;
           if (n >= N) continue;
           const int64_t at = static_cast<int64_t>(t) * N + n;
           if (kUp) {
-            p.o0[at] = H::from_f32(act_value(p.act, v[0][i]) * v[kM - 1][i]);
+            p.o0[at] = H::from_f32(act_value(p.act, v[0][i]) * v[1][i]);
             if (p.o1) {
               p.o1[at] = H::from_f32(v[0][i]);
-              p.o2[at] = H::from_f32(v[kM - 1][i]);
+              p.o2[at] = H::from_f32(v[1][i]);
             }
           } else {
             p.o0[at] = H::from_f32(v[0][i]);
@@ -136,28 +143,30 @@ __global__ __launch_bounds__(WAVES * 64) void ffn_rows_kernel(FfnArgs p) {
   }
 }
 
-template <class H, int KIND, int WAVES, int TT>
-void launch_rows_as(const FfnArgs& p, bool aligned, dim3 g, hipStream_t s) {
+template <class H, int KIND, int WAVES, int TT, bool PAIR>
+void launch_rows_as(const FfnArgs& p, bool aligned, hipStream_t s) {
+  constexpr int kRowsN = PAIR ? 8 : 16;
+  const dim3 g(static_cast<unsigned>((p.N + kRowsN - 1) / kRowsN), static_cast<unsigned>(p.E));
   if (aligned)
-    hipLaunchKernelGGL((ffn_rows_kernel<H, KIND, WAVES, TT, true>), g, dim3(WAVES * 64), 0, s, p);
+    hipLaunchKernelGGL((ffn_rows_kernel<H, KIND, WAVES, TT, true, PAIR>), g, dim3(WAVES * 64), 0, s, p);
   else
-    hipLaunchKernelGGL((ffn_rows_kernel<H, KIND, WAVES, TT, false>), g, dim3(WAVES * 64), 0, s, p);
+    hipLaunchKernelGGL((ffn_rows_kernel<H, KIND, WAVES, TT, false, PAIR>), g, dim3(WAVES * 64), 0, s, p);
 }
 
-// Few workgroups: 8 waves each; else 4.  Up to 16
-// rows per expert on average: one matrix tile of rows at a time; else two.
+// Workgroups that do not fill the card twice: 8 waves each (and gate and up in one tile);
+// else 4.  Up to 8 rows per expert on average: one matrix tile of rows at a time; else two.
 template <class H, int KIND>
 void launch_rows(const FfnArgs& p, bool aligned, hipStream_t s) {
-  const dim3 g(static_cast<unsigned>((p.N + 15) / 16), static_cast<unsigned>(p.E));
-  const bool deep = static_cast<int64_t>(g.x) * g.y < 512, two = static_cast<int64_t>(p.T) > 8ll * p.E;
+  constexpr bool kUp = KIND == kFfnUp;
+  const bool deep = static_cast<int64_t>((p.N + 15) / 16) * p.E < 512, two = static_cast<int64_t>(p.T) > 8ll * p.E;
   if (deep && two)
-    launch_rows_as<H, KIND, 8, 2>(p, aligned, g, s);
+    launch_rows_as<H, KIND, 8, 2, kUp>(p, aligned, s);
   else if (deep)
-    launch_rows_as<H, KIND, 8, 1>(p, aligned, g, s);
+    launch_rows_as<H, KIND, 8, 1, kUp>(p, aligned, s);
   else if (two)
-    launch_rows_as<H, KIND, 4, 2>(p, aligned, g, s);
+    launch_rows_as<H, KIND, 4, 2, false>(p, aligned, s);
   else
-    launch_rows_as<H, KIND, 4, 1>(p, aligned, g, s);
+    launch_rows_as<H, KIND, 4, 1, false>(p, aligned, s);
 }
 
 }  // namespace

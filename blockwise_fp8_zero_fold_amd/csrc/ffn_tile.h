@@ -177,16 +177,16 @@ __global__ __launch_bounds__(kThreads, 2) void ffn_tile_kernel(FfnArgs p, int32_
   __shared__ __attribute__((aligned(16))) uint8_t sb1[kBBytes];
 
   const int32_t kb = (p.K + kB - 1) / kB, blocks = kSeg * kb;  // scale blocks of k, each two stages
-  int32_t rowtiles, e, lo, hi, m0, col;
+  int32_t rowtiles, first, e, lo, hi, m0, col;
   const int32_t item = static_cast<int32_t>(blockIdx.x);
-  const Plan plan = plan_tiles<kRows>(p.offsets, p.T, p.E, ncols, blocks, p.part != nullptr, rowtiles);
+  const Plan plan = plan_tiles<kRows>(p.offsets, p.T, p.E, ncols, blocks, p.part != nullptr, rowtiles, first);
   if (item >= plan.items()) return;
   const bool split = item >= plan.whole;
   const int32_t rest = plan.tiles - plan.whole;
   const int32_t id = split ? plan.whole + (item - plan.whole) % rest : xcd_run(item, plan.whole);
   const int32_t sp = split ? (item - plan.whole) / rest : 0, parts = split ? plan.splits : 1;
   const int32_t q0 = blocks * sp / parts, q1 = blocks * (sp + 1) / parts;
-  if (!find_tile<kRows>(p.offsets, p.T, p.E, ncols, rowtiles, id, e, lo, hi, m0, col)) return;
+  if (!find_tile<kRows>(p.offsets, p.T, p.E, ncols, rowtiles, first, id, e, lo, hi, m0, col)) return;
   const int32_t n0 = col * kCols;
   const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6), wm = w >> 1, wn = w & 1;
   const int32_t N = p.N, K = p.K;
@@ -229,7 +229,7 @@ __global__ __launch_bounds__(kThreads, 2) void ffn_tile_kernel(FfnArgs p, int32_
     const int64_t kw = kTrans ? static_cast<int64_t>(k0) * N : k0;
     const uint8_t* const wa = (seg ? p.w1 : p.w0) + bbase + kw;
     const uint8_t* const wb = kUp ? p.w1 + bbase + kw : wa;  // upper half of the stage's rows
-    if (DIRECT) {  // k ends with a stage
+    if (DIRECT) {  // (the buffers end with the tensors: what lies behind is not read)
       const buffer_t xb = make_buffer(x, static_cast<int64_t>(p.T - m0) * K * 2 - 2 * static_cast<int64_t>(k0));
       const int64_t left = static_cast<int64_t>(p.E) * N * K - bbase - kw;
       const buffer_t ba = make_buffer(wa, left), bb = make_buffer(wb, left);
@@ -253,6 +253,30 @@ __global__ __launch_bounds__(kThreads, 2) void ffn_tile_kernel(FfnArgs p, int32_
     for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(sa + (t + kThreads * j) * 16) = ra[j];
 #pragma unroll
     for (int j = 0; j < kBC; ++j) *reinterpret_cast<uint4*>(sb + (t + kThreads * j) * 16) = rb[j];
+  };
+
+  // Clears what a stage holds past the end of k: `v` of its 64 k are there.
+  auto clear_past = [&](int32_t v, uint8_t* sa, uint8_t* sb) {
+    auto keep = [](uint8_t* at, int n) {  // the first n of 16 bytes
+      if (n >= 16) return;
+      uint4 x = *reinterpret_cast<uint4*>(at);
+      uint32_t* const o[4] = {&x.x, &x.y, &x.z, &x.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int in = n - 4 * i;
+        *o[i] = in >= 4 ? *o[i] : in > 0 ? *o[i] & (0xffffffffu >> (32 - 8 * in)) : 0u;
+      }
+      *reinterpret_cast<uint4*>(at) = x;
+    };
+    for (int id = t; id < kABytes / 16; id += kThreads) {
+      const int r = id >> 3;
+      keep(sa + id * 16, 2 * v - ((id & 7) ^ swizzle_a(r)) * 16);
+    }
+    for (int id = t; id < kBBytes / 16; id += kThreads) {
+      const int r = id / kBPer;
+      keep(sb + id * 16, kTrans ? (r < v ? 16 : 0) : v - ((id & 3) ^ swizzle_b(r)) * 16);
+    }
+    __syncthreads();
   };
 
   const f32x16 zero = {};
@@ -335,10 +359,13 @@ __global__ __launch_bounds__(kThreads, 2) void ffn_tile_kernel(FfnArgs p, int32_
       before(q);
       if (DIRECT) wait_copies();
       __syncthreads();
+      const int32_t left = K - (kSeg == 2 && q >= kb ? q - kb : q) * kB;
+      if (DIRECT && left < kStep) clear_past(left, sa0, sb0);
       compute(sa0, sb0, d, j0_, nj_, [&] { stage(q, kStep, sa1, sb1); });
       put(sa1, sb1);
       if (DIRECT) wait_copies();
       __syncthreads();
+      if (DIRECT && left < kB) clear_past(left - kStep, sa1, sb1);
       // (the last block's turn fetches it again rather than branch)
       compute(sa1, sb1, d, j0_, nj_, [&] { stage(min(q + 1, q1 - 1), 0, sa0, sb0); });
       put(sa0, sb0);
@@ -454,12 +481,12 @@ __global__ __launch_bounds__(kThreads) void ffn_join_kernel(FfnArgs p, int32_t n
   constexpr bool kUp = KIND == kFfnUp;
   constexpr int kCols = (kUp ? 32 : 64) * NT, kJ = kUp ? NT / 2 : NT;
   const int32_t blocks = (KIND == kFfnUpBwd ? 2 : 1) * ((p.K + kB - 1) / kB);
-  int32_t rowtiles, e, lo, hi, m0, col;
-  const Plan plan = plan_tiles<kRows>(p.offsets, p.T, p.E, ncols, blocks, true, rowtiles);
+  int32_t rowtiles, first, e, lo, hi, m0, col;
+  const Plan plan = plan_tiles<kRows>(p.offsets, p.T, p.E, ncols, blocks, true, rowtiles, first);
   const int32_t rest = plan.tiles - plan.whole, tile = static_cast<int32_t>(blockIdx.x) / (2 * kJ);
   if (tile >= rest) return;
   const int ij = static_cast<int>(blockIdx.x) % (2 * kJ), i = ij / kJ, j = ij % kJ, t = threadIdx.x;
-  if (!find_tile<kRows>(p.offsets, p.T, p.E, ncols, rowtiles, plan.whole + tile, e, lo, hi, m0, col)) return;
+  if (!find_tile<kRows>(p.offsets, p.T, p.E, ncols, rowtiles, first, plan.whole + tile, e, lo, hi, m0, col)) return;
   f32x16 v[2] = {};
   for (int32_t s = 0; s < plan.splits; ++s) {
     const f32x4* from = part_at<NT>(p.part, s * rest + tile);
@@ -478,9 +505,13 @@ __global__ __launch_bounds__(kThreads) void ffn_join_kernel(FfnArgs p, int32_t n
 // The most row tiles that T rows in E runs can make: every run may end in a partial tile.
 int64_t most_row_tiles(int64_t T, int64_t E) { return T / kRows + (T < E ? T : E); }
 
-// Whether k is long enough to be split (two parts of 8 scale blocks), and the bytes of a round
-// of parts.
-bool split_pays(const FfnArgs& p, int products) { return products * ((p.K + kB - 1) / kB) >= 16; }
+// Whether tiles may be split: k is long enough, and if the host knows the tiles (no offsets), there
+// are some to split.
+bool split_pays(const FfnArgs& p, int products, int64_t tiles) {
+  const int32_t blocks = products * ((p.K + kB - 1) / kB);
+  return p.offsets ? blocks >= 4 : tile_splits(tiles, blocks) > 1;
+}
+// bytes of a round of parts
 size_t part_bytes(int nt) { return sizeof(float) * kSlots * kRows * 64 * nt; }
 
 template <class H, int KIND, int NT>
@@ -514,8 +545,8 @@ int launch(FfnArgs p, int32_t dtype, void* workspace, size_t workspace_bytes, hi
         launch_rows<F16, KIND>(p, aligned, s);
       return check_hip(hipGetLastError(), what);
     }
-  const bool direct = !misaligned(p.x0, 16) && !misaligned(p.x1, 16) && !misaligned(p.w0, 16) &&
-                      !misaligned(p.w1, 16) && p.K % kB == 0 && (!kTrans || p.N % 16 == 0);
+  const bool direct = !misaligned(p.x0, 4) && !misaligned(p.x1, 4) && !misaligned(p.w0, 4) && !misaligned(p.w1, 4) &&
+                      (kTrans ? p.K % 2 == 0 && p.N % 4 == 0 : p.K % 4 == 0);
   const int64_t rows = most_row_tiles(p.T, p.E);
   const int32_t per = KIND == kFfnUp ? 32 : 64;  // columns per NT
   // 256 columns a tile where they fill the card; what goes through registers takes too many for it
@@ -523,7 +554,8 @@ int launch(FfnArgs p, int32_t dtype, void* workspace, size_t workspace_bytes, hi
   const int32_t cols = per * (wide ? 4 : 2), ncols = (p.N + cols - 1) / cols;
   const int64_t tiles = rows * ncols;
   if (tiles > 0x7fffffff - kSlots) return set_error(FP8Z1_ESHAPE, std::string(what) + ": too many tiles");
-  if (split_pays(p, KIND == kFfnUpBwd ? 2 : 1) && workspace_bytes >= part_bytes(wide ? 4 : 2))
+  const int64_t known = p.offsets ? tiles : static_cast<int64_t>((p.T + kRows - 1) / kRows) * ncols;
+  if (split_pays(p, KIND == kFfnUpBwd ? 2 : 1, known) && workspace_bytes >= part_bytes(wide ? 4 : 2))
     p.part = static_cast<float*>(workspace);
   if (dtype == FP8Z1_BF16 && wide)
     launch_tiles<Bf16, KIND, 4>(p, direct, tiles, ncols, s);

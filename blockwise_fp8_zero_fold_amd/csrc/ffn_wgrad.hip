@@ -30,7 +30,7 @@ struct WgradArgs {
 // takes 4 rows of 4 neighbouring chunks at a time, which then lie in 16 different places.
 __device__ __forceinline__ int swizzle(int r) { return (r & 3) << 2; }
 
-// DIRECT: rows are 16-byte aligned, so a stage goes from memory to LDS by direct copies;
+// DIRECT: rows are 4-byte aligned, so a stage goes from memory to LDS by direct copies;
 // otherwise through registers, with the bytes outside a row left out.
 template <class H, bool F32OUT, int NT, bool DIRECT>
 __global__ __launch_bounds__(kThreads, 2) void ffn_wgrad_kernel(WgradArgs g) {
@@ -293,7 +293,7 @@ extern "C" int fp8z1_ffn_wgrad(int64_t T, int64_t E, int64_t M, int64_t N, int32
   g.E = static_cast<int32_t>(E);
   g.M = static_cast<int32_t>(M);
   g.N = static_cast<int32_t>(N);
-  const bool direct = M % 8 == 0 && N % 8 == 0 && !misaligned(p, 16) && !misaligned(q, 16);
+  const bool direct = M % 2 == 0 && N % 2 == 0 && !misaligned(p, 4) && !misaligned(q, 4);
   const int nt = wgrad_nt(E, M, N, direct);
   g.mt = static_cast<int32_t>((M + kTile - 1) / kTile);
   g.nt = static_cast<int32_t>((N + nt * 64 - 1) / (nt * 64));

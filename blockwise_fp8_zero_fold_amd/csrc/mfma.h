@@ -127,7 +127,7 @@ __device__ __forceinline__ uint4 ld16_part(const uint8_t* p, int n, int before) 
 }
 
 // A wave's direct copy of 64 x 16 bytes from global memory to 1 KB of LDS: lane l's bytes,
-// at `off` bytes (16-byte aligned, its own for each lane) behind the buffer's base,
+// at `off` bytes (4-byte aligned, its own for each lane) behind the buffer's base,
 // land at dst + 16 l.  The buffer is `size` bytes long at most; base and size are the
 // same for the wave, so the only vector register that an address takes is the offset.
 // Written as assembly so that the compiler does not make every later LDS read wait for the
@@ -136,6 +136,7 @@ __device__ __forceinline__ uint4 ld16_part(const uint8_t* p, int n, int before) 
 typedef int buffer_t __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ buffer_t make_buffer(const uint8_t* base, int64_t size) {
   const uint64_t at = reinterpret_cast<uint64_t>(base);
+  if (size < 0) size = 0;  // a base past the tensor: nothing is read
   return buffer_t{__builtin_amdgcn_readfirstlane(static_cast<int>(at)),
                   __builtin_amdgcn_readfirstlane(static_cast<int>(at >> 32) & 0xffff),
                   __builtin_amdgcn_readfirstlane(static_cast<int>(size < 0x7fffffff ? size : 0x7fffffff)), 0x00027000};

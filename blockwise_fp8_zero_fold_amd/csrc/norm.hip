@@ -455,13 +455,18 @@ int threads_for(int64_t C) {
   return static_cast<int>((C + 64 * per - 1) / (64 * per) * 64);
 }
 
-// Workgroups: enough waves for the card (16 per compute unit), each walking over rows.
-int64_t groups_for(int64_t T, int64_t C, int waves_per_cu) {
+// Workgroups, each walking over rows: as many waves as fit the card at a time.  Backward, each also
+// writes its column sums, so it takes at least 4 rows where that leaves a workgroup per
+// compute unit.
+int64_t groups_for(int64_t T, int64_t C, int waves_per_cu, int64_t rows = 1) {
   const int64_t waves = threads_for(C) / 64;
-  const int64_t most = (256 * waves_per_cu + waves - 1) / waves;
+  int64_t most = (256 * waves_per_cu + waves - 1) / waves;
+  const int64_t few = T / rows > 256 ? T / rows : 256;
+  if (most > few) most = few;
   return T < most ? T : most;
 }
 constexpr int kFwdWaves = 28, kBwdWaves = 14;
+int64_t bwd_groups(int64_t T, int64_t C) { return groups_for(T, C, kBwdWaves, 4); }
 
 bool misaligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
 
@@ -577,7 +582,7 @@ extern "C" int fp8z1_norm_join_bwd_workspace_bytes(const fp8z1_norm* f, size_t* 
   if (!f) return set_error(FP8Z1_EINVAL, "norm_join_bwd_workspace_bytes: NULL description");
   if (f->T < 0 || f->T > FP8Z1_FFN_MAX_ROWS || f->C < 1 || f->C > kMaxC)
     return set_error(FP8Z1_ESHAPE, "norm_join_bwd_workspace_bytes: T or C out of range");
-  *bytes = sizeof(float) * 3 * static_cast<size_t>(groups_for(f->T, f->C, kBwdWaves)) * static_cast<size_t>(f->C);
+  *bytes = sizeof(float) * 3 * static_cast<size_t>(bwd_groups(f->T, f->C)) * static_cast<size_t>(f->C);
   return FP8Z1_OK;
 }
 
@@ -597,7 +602,7 @@ extern "C" int fp8z1_norm_join_bwd(const fp8z1_norm* f, const void* dz, const vo
   if (rc) return rc;
   float* gate_cols = f->gate == FP8Z1_GATE_CHANNEL ? static_cast<float*>(dgate) : nullptr;
   const bool sums = dw_post || dw_pre || gate_cols;
-  const int64_t groups = groups_for(f->T, f->C, kBwdWaves);
+  const int64_t groups = bwd_groups(f->T, f->C);
   if (sums && f->T) {
     size_t need = 0;
     rc = fp8z1_norm_join_bwd_workspace_bytes(f, &need);

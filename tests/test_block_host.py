@@ -55,7 +55,7 @@ def test_ffn_workspace():
     n = C.c_size_t()
     q = fz.lib.fp8z1_ffn_workspace_bytes
     assert q(None, C.byref(n)) == EINVAL and q(ffn(), None) == EINVAL and q(ffn(D=0), C.byref(n)) == ESHAPE
-    assert q(ffn(), C.byref(n)) == 0 and n.value == 0  # sums of 64: nothing to split
+    assert q(ffn(), C.byref(n)) == 0 and n.value == 0  # sums of 64 and 2 x 32: nothing to split
     assert q(ffn(D=7168), C.byref(n)) == 0 and n.value > 0
     lib = fz.lib
     assert lib.fp8z1_ffn_down(ffn(), P, P, P, P, P, P + 4, 1 << 30, None) == EINVAL  # misaligned workspace

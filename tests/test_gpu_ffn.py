@@ -85,6 +85,7 @@ class Case:
 SIZES = [  # T, E, D, F
     (1, 1, 128, 128), (1, 1, 7, 3), (2, 3, 130, 65), (17, 1, 256, 192), (33, 2, 64, 64), (128, 1, 128, 64),
     (129, 4, 100, 300), (300, 5, 521, 257), (257, 3, 384, 640), (1000, 9, 144, 48), (70, 70, 136, 72),
+    (150, 2, 132, 260), (140, 1, 252, 68), (200, 3, 196, 324), (90, 2, 70, 134),
 ]
 
 
@@ -219,13 +220,13 @@ def test_scales_far_apart(T):
     c.check_up_bwd(dx, "far scales")
 
 
-@pytest.mark.parametrize("T", [4, 200])
-def test_special_values_stay_in_their_row(T):
+@pytest.mark.parametrize("T,D,F", [(4, 200, 100), (200, 200, 100), (200, 201, 101), (200, 256, 128)])
+def test_special_values_stay_in_their_row(T, D, F):
     """A NaN code reaches only its column, an infinite activation only its row, whatever the
     tile edges: neighbours across a row's end and past the last k stay out of the sums."""
-    c = Case(T, 2, 200, 100, one_run=False)
+    c = Case(T, 2, D, F)
     c.offsets = torch.tensor([0, T // 2, T], dtype=torch.int32)
-    for w, row in ((c.gate, 3), (c.up, 99), (c.down, 199)):
+    for w, row in ((c.gate, 3), (c.up, F - 1), (c.down, D - 1)):
         w[0][0, row, 0] = 0x7F  # first element of a row: right behind the row before it
         w[0][1, row - 1, -1] = 0xFF
     c.x[1, 0] = float("inf")
