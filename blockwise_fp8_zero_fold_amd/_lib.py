@@ -132,6 +132,9 @@ _sig = {
     "fp8z1_ffn_wgrad_workspace_bytes": (C.c_int, [*[C.c_int64] * 4, C.POINTER(C.c_size_t)]),
     "fp8z1_ffn_wgrad": (C.c_int, [*[C.c_int64] * 4, C.c_int32, _vp, _vp, _vp, C.c_int32, _vp, C.c_int32, _vp,
                                   C.c_size_t, _vp]),
+    "fp8z1_ffn_bwd_weights_workspace_bytes": (C.c_int, [C.POINTER(Ffn), C.POINTER(C.c_size_t)]),
+    "fp8z1_ffn_bwd_weights": (C.c_int, [C.POINTER(Ffn), *[_vp] * 6, C.c_int32, _vp, _vp, _vp, C.c_int32, _vp, C.c_size_t,
+                                        _vp]),
     "fp8z1_norm_join": (C.c_int, [C.POINTER(Norm), *[_vp] * 8]),
     "fp8z1_norm_join_bwd_workspace_bytes": (C.c_int, [C.POINTER(Norm), C.POINTER(C.c_size_t)]),
     "fp8z1_norm_join_bwd": (C.c_int, [C.POINTER(Norm), *[_vp] * 13, C.c_size_t, _vp]),
@@ -503,6 +506,25 @@ def fp8z1_ffn_wgrad(T: int, E: int, M: int, N: int, dtype: int, p, q, offsets, d
     _check(lib.fp8z1_ffn_wgrad(T, E, M, N, dtype, _ptr(p), _ptr(q), _ptr(offsets), dw_dtype, _ptr(dw),
                                int(bool(accumulate)), _ptr(workspace), workspace_bytes, _stream(stream)),
            "fp8z1_ffn_wgrad")
+
+
+def fp8z1_ffn_bwd_weights_workspace_bytes(f: Ffn) -> int:
+    n = C.c_size_t()
+    _check(lib.fp8z1_ffn_bwd_weights_workspace_bytes(C.byref(f), C.byref(n)), "fp8z1_ffn_bwd_weights_workspace_bytes")
+    return n.value
+
+
+def fp8z1_ffn_bwd_weights(f: Ffn, x, a, dy, dh, du, offsets, dw_dtype: int, dw_gate, dw_up, dw_down,
+                          accumulate: bool = False, workspace=None, workspace_bytes: int = 0, stream=None) -> None:
+    """The three weight gradients in one launch (added to the outputs with accumulate)."""
+    workspace_bytes = _workspace(workspace, workspace_bytes, "ffn_bwd_weights")
+    _need_rows(f, "ffn_bwd_weights", x=(x, f.D), a=(a, f.F), dy=(dy, f.D), dh=(dh, f.F), du=(du, f.F))
+    for w in (dw_gate, dw_up, dw_down):
+        _need(w, f.E * f.D * f.F * (4 if dw_dtype == F32 else 2), "ffn_bwd_weights gradient", _torch_dtype(dw_dtype))
+    _need_offsets(offsets, f.E, "ffn_bwd_weights")
+    _check(lib.fp8z1_ffn_bwd_weights(C.byref(f), _ptr(x), _ptr(a), _ptr(dy), _ptr(dh), _ptr(du), _ptr(offsets), dw_dtype,
+                                     _ptr(dw_gate), _ptr(dw_up), _ptr(dw_down), int(bool(accumulate)), _ptr(workspace),
+                                     workspace_bytes, _stream(stream)), "fp8z1_ffn_bwd_weights")
 
 
 def _need_norm(f: Norm, what: str, act=(), res=(), weights=(), gates=()) -> None:

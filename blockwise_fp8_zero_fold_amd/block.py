@@ -62,6 +62,11 @@ def _norm_workspace(T: int, C: int) -> int:
     return L.fp8z1_norm_join_bwd_workspace_bytes(L.Norm(T, C, L.F32, L.F32, L.GATE_NONE, 0.0, 1.0, 1.0, 0.0, 0))
 
 
+@functools.lru_cache(maxsize=256)
+def _weights_workspace(T: int, E: int, D: int, F: int) -> int:
+    return L.fp8z1_ffn_bwd_weights_workspace_bytes(L.Ffn(T, E, D, F, L.BF16, L.ACT_SILU))
+
+
 _wgrad_workspace = functools.lru_cache(maxsize=256)(L.fp8z1_ffn_wgrad_workspace_bytes)
 
 
@@ -167,10 +172,29 @@ def ffn_backward_weights(x: torch.Tensor, a: torch.Tensor, dy: torch.Tensor, dh:
                          dtype: torch.dtype = torch.float32, out: Optional[Sequence[torch.Tensor]] = None):
     """(dWg [E,F,D], dWu [E,F,D], dWd [E,D,F]), row-major as the shard step reads its gradients.
     Given ``out`` (three float32 tensors), the products are added to them."""
-    og, ou, od = out if out is not None else (None, None, None)
-    return (ffn_weight_gradient(dh, x, n_experts, offsets, dtype, og),
-            ffn_weight_gradient(du, x, n_experts, offsets, dtype, ou),
-            ffn_weight_gradient(dy, a, n_experts, offsets, dtype, od))
+    what = "ffn_backward_weights"
+    if x.dim() != 2 or a.dim() != 2 or x.dtype not in _HALF:
+        _fail(f"{what}: rows must be [T, D] and [T, F] of torch.bfloat16 or torch.float16")
+    dev, (T, D), F, E = _device(x, what), x.shape, a.shape[1], n_experts
+    if dtype not in (torch.float32, torch.bfloat16):
+        _fail(f"{what}: dtype {dtype}, expected torch.float32 or torch.bfloat16")
+    wide = [_check(v, dev, x.dtype, (T, D), f"{what} {n}") for v, n in ((x, "x"), (dy, "dy"))]
+    inner = [_check(v, dev, x.dtype, (T, F), f"{what} {n}") for v, n in ((a, "a"), (dh, "dh"), (du, "du"))]
+    off = _offsets(offsets, dev, E, what)
+    shapes = ((E, F, D), (E, F, D), (E, D, F))
+    if out is None:
+        dw = tuple(x.new_empty(s, dtype=dtype) for s in shapes)
+    else:
+        dtype, dw = torch.float32, tuple(out)
+        for w, s in zip(dw, shapes):
+            _check(w, dev, dtype, s, f"{what} out")
+    n = _weights_workspace(T, E, D, F)
+    ws = _scratch(x, n)
+    f = L.Ffn(T, E, D, F, _CODE[x.dtype], L.ACT_SILU)
+    L._check(L.lib.fp8z1_ffn_bwd_weights(f, wide[0], inner[0], wide[1], inner[1], inner[2], off, _CODE[dtype],
+                                         dw[0].data_ptr(), dw[1].data_ptr(), dw[2].data_ptr(), int(out is not None),
+                                         L._ptr(ws), n, L._current_stream(dev)), what)
+    return dw
 
 
 def _gate_kind(gate: Optional[torch.Tensor], T: int, C: int) -> int:

@@ -8,6 +8,8 @@
 // the matrix operands are gathered by the transposing LDS reads.
 #include <hip/hip_runtime.h>
 
+#include <initializer_list>
+
 #include "ffn.h"
 
 namespace fp8z1 {
@@ -18,12 +20,23 @@ constexpr int kTile = 128;  // tile rows
 constexpr int kStep = 32;   // tokens per stage
 constexpr int kPBytes = kTile * kStep * 2;
 
-struct WgradArgs {
-  const uint8_t *p, *q;  // [T, M], [T, N]
-  const int32_t* offsets;
-  float* part;  // [splits, E, M, N] partial sums, or NULL
+// One gradient dw [E, M, N] of rows p [T, M] and q [T, N]
+struct Wgrad {
+  const uint8_t *p, *q;
   void* dw;
-  int32_t T, E, M, N, mt, nt, splits, accumulate;
+  int64_t part;  // of its partial sums within a split's
+  int32_t M, N, mt, nt;
+};
+
+// Up to three gradients over the same tokens in one launch (the block's own three: each alone
+// may have too few tiles to fill the card, and a launch takes as long as a small gradient)
+constexpr int kMost = 3;
+struct WgradArgs {
+  Wgrad g[kMost];
+  const int32_t* offsets;
+  float* part;  // partial sums of each split: all gradients [E, M, N] in turn; or NULL
+  int64_t size;  // elements of all gradients
+  int32_t T, E, count, tiles, splits, accumulate;
 };
 
 // Chunk c (16 bytes) of row r of a stage sits at position c ^ swizzle(r): a transposing read
@@ -33,7 +46,7 @@ __device__ __forceinline__ int swizzle(int r) { return (r & 3) << 2; }
 // DIRECT: rows are 4-byte aligned, so a stage goes from memory to LDS by direct copies;
 // otherwise through registers, with the bytes outside a row left out.
 template <class H, bool F32OUT, int NT, bool DIRECT>
-__global__ __launch_bounds__(kThreads, 2) void ffn_wgrad_kernel(WgradArgs g) {
+__global__ __launch_bounds__(kThreads, 2) void ffn_wgrad_kernel(WgradArgs all) {
   typedef typename H::v8 v8;
   constexpr int kCols = NT * 64, kQBytes = kCols * kStep * 2, kStage = kPBytes + kQBytes;
   constexpr int kPC = kPBytes / 16 / kThreads, kQC = kQBytes / 16 / kThreads;  // chunks per thread
@@ -42,20 +55,27 @@ __global__ __launch_bounds__(kThreads, 2) void ffn_wgrad_kernel(WgradArgs g) {
 
   // tiles in contiguous runs per XCD, in groups of kGroup tile rows by all tile columns
   int32_t id = xcd_run(static_cast<int32_t>(blockIdx.x), static_cast<int32_t>(gridDim.x));
-  const int32_t per = g.mt * g.nt, split = id / (per * g.E);
-  id -= split * per * g.E;
-  const int32_t e = id / per;
+  const int32_t split = id / all.tiles;
+  id -= split * all.tiles;
+  int which = 0;
+  for (; which + 1 < all.count; ++which) {
+    const int32_t n = all.E * all.g[which].mt * all.g[which].nt;
+    if (id < n) break;
+    id -= n;
+  }
+  const Wgrad g = all.g[which];
+  const int32_t per = g.mt * g.nt, e = id / per;
   id -= e * per;
   const int32_t gr = id / (kGroup * g.nt), in = id - gr * kGroup * g.nt, rows = min(kGroup, g.mt - gr * kGroup);
   const int32_t m0 = (gr * kGroup + in % rows) * kTile, n0 = in / rows * kCols;
 
   int32_t lo, hi;
-  expert_rows(g.offsets, g.T, e, lo, hi);
+  expert_rows(all.offsets, all.T, e, lo, hi);
   lo = __builtin_amdgcn_readfirstlane(lo);
   hi = __builtin_amdgcn_readfirstlane(hi);
   const int32_t stages = (hi - lo + kStep - 1) / kStep;
-  const int32_t s0 = static_cast<int32_t>(static_cast<int64_t>(stages) * split / g.splits);
-  const int32_t s1 = static_cast<int32_t>(static_cast<int64_t>(stages) * (split + 1) / g.splits);
+  const int32_t s0 = static_cast<int32_t>(static_cast<int64_t>(stages) * split / all.splits);
+  const int32_t s1 = static_cast<int32_t>(static_cast<int64_t>(stages) * (split + 1) / all.splits);
 
   uint32_t poff[kPC], qoff[kQC];
   int32_t pc[kPC], qc[kQC];  // byte column of the chunk
@@ -171,7 +191,7 @@ __global__ __launch_bounds__(kThreads, 2) void ffn_wgrad_kernel(WgradArgs g) {
     if (ahead < s1) put(there);
   }
 
-  const int64_t size = static_cast<int64_t>(g.E) * g.M * g.N;
+  float* const part = all.part ? all.part + split * all.size + g.part : nullptr;
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -183,76 +203,171 @@ __global__ __launch_bounds__(kThreads, 2) void ffn_wgrad_kernel(WgradArgs g) {
         const int32_t n = n0 + (wn * NT + j) * 32 + (lane & 31);
         if (n >= g.N) continue;
         const int64_t at = (static_cast<int64_t>(e) * g.M + m) * g.N + n;
-        if (g.part)
-          g.part[split * size + at] = acc[i][j][r];
+        if (part)
+          part[at] = acc[i][j][r];
         else if (F32OUT)
-          static_cast<float*>(g.dw)[at] = g.accumulate ? static_cast<float*>(g.dw)[at] + acc[i][j][r] : acc[i][j][r];
+          static_cast<float*>(g.dw)[at] = all.accumulate ? static_cast<float*>(g.dw)[at] + acc[i][j][r] : acc[i][j][r];
         else
           static_cast<uint16_t*>(g.dw)[at] = Bf16::from_f32(acc[i][j][r]);
       }
     }
 }
 
-// The splits' partial sums added in order, one element per thread.
+// The splits' partial sums added in order, one element per thread and turn (blockIdx.y: which
+// gradient), four splits' loads on their way at a time.
 template <bool F32OUT>
-__global__ __launch_bounds__(256) void ffn_wgrad_join_kernel(const float* __restrict__ part, int32_t splits,
-                                                             int64_t size, void* dw, int32_t accumulate) {
+__global__ __launch_bounds__(256) void ffn_wgrad_join_kernel(WgradArgs all) {
+  const Wgrad g = all.g[blockIdx.y];
+  const int64_t size = static_cast<int64_t>(all.E) * g.M * g.N;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < size;
        i += static_cast<int64_t>(gridDim.x) * 256) {
-    float v = part[i];
-    for (int32_t s = 1; s < splits; ++s) v += part[s * size + i];
+    const float* from = all.part + g.part + i;
+    float v = 0.0f;
+    int32_t s = 0;
+    for (; s + 4 <= all.splits; s += 4, from += 4 * all.size) {
+      const float x0 = from[0], x1 = from[all.size], x2 = from[2 * all.size], x3 = from[3 * all.size];
+      v = (((v + x0) + x1) + x2) + x3;
+    }
+    for (; s < all.splits; ++s, from += all.size) v += *from;
     if (F32OUT)
-      static_cast<float*>(dw)[i] = accumulate ? static_cast<float*>(dw)[i] + v : v;
+      static_cast<float*>(g.dw)[i] = all.accumulate ? static_cast<float*>(g.dw)[i] + v : v;
     else
-      static_cast<uint16_t*>(dw)[i] = Bf16::from_f32(v);
+      static_cast<uint16_t*>(g.dw)[i] = Bf16::from_f32(v);
   }
 }
 
 // Columns of a tile: 256 where such tiles fill the card twice over (as many workgroups as run
 // at once, two on each of 256 compute units), else 128.
-int wgrad_nt(int64_t E, int64_t M, int64_t N, bool direct) {
-  return direct && E * ((M + kTile - 1) / kTile) * ((N + 255) / 256) >= 2 * kSlots ? 4 : 2;
+int64_t tiles_of(int64_t E, int64_t M, int64_t N, int64_t cols) {
+  return E * ((M + kTile - 1) / kTile) * ((N + cols - 1) / cols);
 }
 
-// Splits of the tokens: where the output has fewer tiles (of 128 columns) than the card runs at
+// Splits of the tokens: where the outputs have fewer tiles (of 128 columns) than the card runs at
 // once, the tokens are cut so that about that many run, each with at least 8 stages of
 // an even share.
-int32_t wgrad_splits(int64_t T, int64_t E, int64_t M, int64_t N) {
-  const int64_t tiles = E * ((M + kTile - 1) / kTile) * ((N + kTile - 1) / kTile);
+int32_t wgrad_splits(int64_t T, int64_t E, int64_t tiles) {
   const int64_t want = kSlots / (tiles < 1 ? 1 : tiles), most = T / E / (8 * kStep);
   const int64_t s = want < most ? want : most;
   return static_cast<int32_t>(s < 1 ? 1 : s);
 }
 
-int check_wgrad(int64_t T, int64_t E, int64_t M, int64_t N) {
-  if (T < 0 || T > FP8Z1_FFN_MAX_ROWS) return set_error(FP8Z1_ESHAPE, "ffn_wgrad: T outside 0 .. 2^30");
-  if (E < 1 || E > FP8Z1_FFN_MAX_EXPERTS) return set_error(FP8Z1_ESHAPE, "ffn_wgrad: E outside 1 .. 65535");
-  if (M < 1 || M > FP8Z1_FFN_MAX_WIDTH || N < 1 || N > FP8Z1_FFN_MAX_WIDTH)
-    return set_error(FP8Z1_ESHAPE, "ffn_wgrad: M and N must be 1 .. 2^20");
-  const int64_t tiles = E * ((M + kTile - 1) / kTile) * ((N + kTile - 1) / kTile);
-  if (tiles > 0x7fffffff) return set_error(FP8Z1_ESHAPE, "ffn_wgrad: too many tiles");
+struct Shape {
+  int64_t M, N;
+};
+
+int check_wgrad(int64_t T, int64_t E, std::initializer_list<Shape> shapes, const char* what) {
+  const std::string w(what);
+  if (T < 0 || T > FP8Z1_FFN_MAX_ROWS) return set_error(FP8Z1_ESHAPE, w + ": T outside 0 .. 2^30");
+  if (E < 1 || E > FP8Z1_FFN_MAX_EXPERTS) return set_error(FP8Z1_ESHAPE, w + ": E outside 1 .. 65535");
+  int64_t tiles = 0;
+  for (const Shape& s : shapes) {
+    if (s.M < 1 || s.M > FP8Z1_FFN_MAX_WIDTH || s.N < 1 || s.N > FP8Z1_FFN_MAX_WIDTH)
+      return set_error(FP8Z1_ESHAPE, w + ": widths must be 1 .. 2^20");
+    tiles += tiles_of(E, s.M, s.N, kTile);
+  }
+  if (tiles > 0x7fffffff) return set_error(FP8Z1_ESHAPE, w + ": too many tiles");
   return FP8Z1_OK;
 }
 
-template <class H, bool F32OUT>
-void launch_wgrad_as(const WgradArgs& g, int nt, bool direct, dim3 grid, hipStream_t s) {
-  if (nt == 4)
-    hipLaunchKernelGGL((ffn_wgrad_kernel<H, F32OUT, 4, true>), grid, dim3(kThreads), 0, s, g);
-  else if (direct)
-    hipLaunchKernelGGL((ffn_wgrad_kernel<H, F32OUT, 2, true>), grid, dim3(kThreads), 0, s, g);
-  else
-    hipLaunchKernelGGL((ffn_wgrad_kernel<H, F32OUT, 2, false>), grid, dim3(kThreads), 0, s, g);
-}
-
-template <class H>
-void launch_wgrad(const WgradArgs& g, bool f32out, int nt, bool direct, dim3 grid, hipStream_t s) {
-  if (f32out)
-    launch_wgrad_as<H, true>(g, nt, direct, grid, s);
-  else
-    launch_wgrad_as<H, false>(g, nt, direct, grid, s);
+size_t workspace_for(int64_t T, int64_t E, std::initializer_list<Shape> shapes) {
+  int64_t tiles = 0, size = 0;
+  for (const Shape& s : shapes) {
+    tiles += tiles_of(E, s.M, s.N, kTile);
+    size += E * s.M * s.N;
+  }
+  const int32_t s = wgrad_splits(T, E, tiles);
+  return s > 1 ? sizeof(float) * static_cast<size_t>(s) * size : 0;
 }
 
 bool misaligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
+
+template <class H, bool F32OUT>
+void launch_kernels(const WgradArgs& w, int nt, bool direct, hipStream_t s) {
+  const dim3 grid(static_cast<unsigned>(w.tiles * w.splits)), block(kThreads);
+  if (nt == 4)
+    hipLaunchKernelGGL((ffn_wgrad_kernel<H, F32OUT, 4, true>), grid, block, 0, s, w);
+  else if (direct)
+    hipLaunchKernelGGL((ffn_wgrad_kernel<H, F32OUT, 2, true>), grid, block, 0, s, w);
+  else
+    hipLaunchKernelGGL((ffn_wgrad_kernel<H, F32OUT, 2, false>), grid, block, 0, s, w);
+  if (!w.part) return;
+  int64_t most = 0;
+  for (int i = 0; i < w.count; ++i) {
+    const int64_t n = static_cast<int64_t>(w.E) * w.g[i].M * w.g[i].N;
+    most = most > n ? most : n;
+  }
+  const int64_t want = (most + 255) / 256;
+  hipLaunchKernelGGL(ffn_wgrad_join_kernel<F32OUT>,
+                     dim3(static_cast<unsigned>(want < 4096 ? want : 4096), static_cast<unsigned>(w.count)), block, 0, s,
+                     w);
+}
+
+int launch_wgrad(int64_t T, int64_t E, int32_t dtype, const int32_t* offsets, int32_t dw_dtype, int32_t accumulate,
+                 std::initializer_list<Wgrad> gs, void* workspace, size_t workspace_bytes, void* stream,
+                 const char* what) {
+  const std::string name(what);
+  if (dtype != FP8Z1_BF16 && dtype != FP8Z1_F16)
+    return set_error(FP8Z1_EINVAL, name + ": dtype must be FP8Z1_BF16 or FP8Z1_F16");
+  if (dw_dtype != FP8Z1_F32 && dw_dtype != FP8Z1_BF16)
+    return set_error(FP8Z1_EINVAL, name + ": dw_dtype must be FP8Z1_F32 or FP8Z1_BF16");
+  if (accumulate && dw_dtype != FP8Z1_F32)
+    return set_error(FP8Z1_EINVAL, name + ": only FP8Z1_F32 gradients can be accumulated");
+  if (!offsets && E != 1) return set_error(FP8Z1_EINVAL, name + ": offsets may be NULL for one expert only");
+  if (misaligned(offsets, 4) || misaligned(workspace, 4))
+    return set_error(FP8Z1_EINVAL, name + ": misaligned argument");
+  bool direct = true;
+  int64_t wide = 0, narrow = 0, size = 0;
+  for (const Wgrad& g : gs) {
+    if (!g.dw || (T && (!g.p || !g.q))) return set_error(FP8Z1_EINVAL, name + ": NULL argument");
+    if (misaligned(g.p, 2) || misaligned(g.q, 2) || misaligned(g.dw, dw_dtype == FP8Z1_F32 ? 4 : 2))
+      return set_error(FP8Z1_EINVAL, name + ": misaligned argument");
+    direct = direct && g.M % 2 == 0 && g.N % 2 == 0 && !misaligned(g.p, 4) && !misaligned(g.q, 4);
+    wide += tiles_of(E, g.M, g.N, 256);
+    narrow += tiles_of(E, g.M, g.N, kTile);
+    size += E * g.M * g.N;
+  }
+  const int nt = direct && wide >= 2 * kSlots ? 4 : 2;
+  WgradArgs w{};
+  for (const Wgrad& g : gs) {
+    Wgrad& to = w.g[w.count++];
+    to = g;
+    to.mt = (g.M + kTile - 1) / kTile;
+    to.nt = (g.N + nt * 64 - 1) / (nt * 64);
+    to.part = w.size;
+    w.size += E * g.M * g.N;
+  }
+  w.offsets = offsets;
+  w.T = static_cast<int32_t>(T);
+  w.E = static_cast<int32_t>(E);
+  w.tiles = static_cast<int32_t>(nt == 4 ? wide : narrow);
+  w.accumulate = accumulate;
+  w.splits = 1;
+  const int32_t splits = wgrad_splits(T, E, narrow);
+  if (splits > 1 && workspace && workspace_bytes >= sizeof(float) * static_cast<size_t>(splits) * size) {
+    w.splits = splits;
+    w.part = static_cast<float*>(workspace);
+  }
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (dtype == FP8Z1_BF16 && dw_dtype == FP8Z1_F32)
+    launch_kernels<Bf16, true>(w, nt, direct, s);
+  else if (dtype == FP8Z1_BF16)
+    launch_kernels<Bf16, false>(w, nt, direct, s);
+  else if (dw_dtype == FP8Z1_F32)
+    launch_kernels<F16, true>(w, nt, direct, s);
+  else
+    launch_kernels<F16, false>(w, nt, direct, s);
+  return check_hip(hipGetLastError(), what);
+}
+
+Wgrad gradient(const void* p, const void* q, void* dw, int64_t M, int64_t N) {
+  Wgrad g{};
+  g.p = static_cast<const uint8_t*>(p);
+  g.q = static_cast<const uint8_t*>(q);
+  g.dw = dw;
+  g.M = static_cast<int32_t>(M);
+  g.N = static_cast<int32_t>(N);
+  return g;
+}
 
 }  // namespace
 }  // namespace fp8z1
@@ -261,63 +376,38 @@ using namespace fp8z1;
 
 extern "C" int fp8z1_ffn_wgrad_workspace_bytes(int64_t T, int64_t E, int64_t M, int64_t N, size_t* bytes) {
   if (!bytes) return set_error(FP8Z1_EINVAL, "ffn_wgrad_workspace_bytes: NULL argument");
-  const int rc = check_wgrad(T, E, M, N);
+  const int rc = check_wgrad(T, E, {{M, N}}, "ffn_wgrad_workspace_bytes");
   if (rc) return rc;
-  const int32_t s = wgrad_splits(T, E, M, N);
-  *bytes = s > 1 ? sizeof(float) * static_cast<size_t>(s) * E * M * N : 0;
+  *bytes = workspace_for(T, E, {{M, N}});
   return FP8Z1_OK;
 }
 
 extern "C" int fp8z1_ffn_wgrad(int64_t T, int64_t E, int64_t M, int64_t N, int32_t dtype, const void* p, const void* q,
-                               const int32_t* offsets, int32_t dw_dtype, void* dw, int32_t accumulate, void* workspace,
-                               size_t workspace_bytes, void* stream) {
-  int rc = check_wgrad(T, E, M, N);
+                               const int32_t* offsets, int32_t dw_dtype, void* dw, int32_t accumulate,
+                               void* d_workspace, size_t workspace_bytes, void* stream) {
+  const int rc = check_wgrad(T, E, {{M, N}}, "ffn_wgrad");
   if (rc) return rc;
-  if (dtype != FP8Z1_BF16 && dtype != FP8Z1_F16)
-    return set_error(FP8Z1_EINVAL, "ffn_wgrad: dtype must be FP8Z1_BF16 or FP8Z1_F16");
-  if (dw_dtype != FP8Z1_F32 && dw_dtype != FP8Z1_BF16)
-    return set_error(FP8Z1_EINVAL, "ffn_wgrad: dw_dtype must be FP8Z1_F32 or FP8Z1_BF16");
-  if (accumulate && dw_dtype != FP8Z1_F32)
-    return set_error(FP8Z1_EINVAL, "ffn_wgrad: only FP8Z1_F32 gradients can be accumulated");
-  if (!dw || (T && (!p || !q))) return set_error(FP8Z1_EINVAL, "ffn_wgrad: NULL argument");
-  if (!offsets && E != 1) return set_error(FP8Z1_EINVAL, "ffn_wgrad: offsets may be NULL for one expert only");
-  if (misaligned(p, 2) || misaligned(q, 2) || misaligned(offsets, 4) || misaligned(workspace, 4) ||
-      misaligned(dw, dw_dtype == FP8Z1_F32 ? 4 : 2))
-    return set_error(FP8Z1_EINVAL, "ffn_wgrad: misaligned argument");
-  WgradArgs g{};
-  g.p = static_cast<const uint8_t*>(p);
-  g.q = static_cast<const uint8_t*>(q);
-  g.offsets = offsets;
-  g.dw = dw;
-  g.T = static_cast<int32_t>(T);
-  g.E = static_cast<int32_t>(E);
-  g.M = static_cast<int32_t>(M);
-  g.N = static_cast<int32_t>(N);
-  const bool direct = M % 2 == 0 && N % 2 == 0 && !misaligned(p, 4) && !misaligned(q, 4);
-  const int nt = wgrad_nt(E, M, N, direct);
-  g.mt = static_cast<int32_t>((M + kTile - 1) / kTile);
-  g.nt = static_cast<int32_t>((N + nt * 64 - 1) / (nt * 64));
-  g.accumulate = accumulate;
-  g.splits = 1;
-  const int32_t splits = wgrad_splits(T, E, M, N);
-  const int64_t size = E * M * N;
-  if (splits > 1 && workspace && workspace_bytes >= sizeof(float) * static_cast<size_t>(splits) * size) {
-    g.splits = splits;
-    g.part = static_cast<float*>(workspace);
-  }
-  hipStream_t s = static_cast<hipStream_t>(stream);
-  const dim3 grid(static_cast<unsigned>(g.E * g.mt * g.nt * g.splits));
-  if (dtype == FP8Z1_BF16)
-    launch_wgrad<Bf16>(g, dw_dtype == FP8Z1_F32, nt, direct, grid, s);
-  else
-    launch_wgrad<F16>(g, dw_dtype == FP8Z1_F32, nt, direct, grid, s);
-  rc = check_hip(hipGetLastError(), "ffn_wgrad: launch");
-  if (rc || !g.part) return rc;
-  const int64_t want = (size + 255) / 256;
-  const dim3 jgrid(static_cast<unsigned>(want < 4096 ? want : 4096));
-  if (dw_dtype == FP8Z1_F32)
-    hipLaunchKernelGGL(ffn_wgrad_join_kernel<true>, jgrid, dim3(256), 0, s, g.part, g.splits, size, dw, accumulate);
-  else
-    hipLaunchKernelGGL(ffn_wgrad_join_kernel<false>, jgrid, dim3(256), 0, s, g.part, g.splits, size, dw, accumulate);
-  return check_hip(hipGetLastError(), "ffn_wgrad: join launch");
+  return launch_wgrad(T, E, dtype, offsets, dw_dtype, accumulate, {gradient(p, q, dw, M, N)}, d_workspace,
+                      workspace_bytes, stream, "ffn_wgrad");
+}
+
+extern "C" int fp8z1_ffn_bwd_weights_workspace_bytes(const fp8z1_ffn* f, size_t* bytes) {
+  if (!f || !bytes) return set_error(FP8Z1_EINVAL, "ffn_bwd_weights_workspace_bytes: NULL argument");
+  const int rc = check_wgrad(f->T, f->E, {{f->F, f->D}, {f->F, f->D}, {f->D, f->F}}, "ffn_bwd_weights_workspace_bytes");
+  if (rc) return rc;
+  *bytes = workspace_for(f->T, f->E, {{f->F, f->D}, {f->F, f->D}, {f->D, f->F}});
+  return FP8Z1_OK;
+}
+
+extern "C" int fp8z1_ffn_bwd_weights(const fp8z1_ffn* f, const void* x, const void* a, const void* dy, const void* dh,
+                                     const void* du, const int32_t* offsets, int32_t dw_dtype, void* dw_gate,
+                                     void* dw_up, void* dw_down, int32_t accumulate, void* d_workspace,
+                                     size_t workspace_bytes, void* stream) {
+  if (!f) return set_error(FP8Z1_EINVAL, "ffn_bwd_weights: NULL description");
+  const int rc = check_wgrad(f->T, f->E, {{f->F, f->D}, {f->F, f->D}, {f->D, f->F}}, "ffn_bwd_weights");
+  if (rc) return rc;
+  return launch_wgrad(f->T, f->E, f->dtype, offsets, dw_dtype, accumulate,
+                      {gradient(dh, x, dw_gate, f->F, f->D), gradient(du, x, dw_up, f->F, f->D),
+                       gradient(dy, a, dw_down, f->D, f->F)},
+                      d_workspace, workspace_bytes, stream, "ffn_bwd_weights");
 }

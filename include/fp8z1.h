@@ -383,6 +383,13 @@ int fp8z1_ffn_wgrad(int64_t T, int64_t E, int64_t M, int64_t N, int32_t dtype, c
                     const int32_t* offsets, int32_t dw_dtype, void* dw, int32_t accumulate, void* d_workspace,
                     size_t workspace_bytes, void* stream);
 
+/* The block's three weight gradients in one launch: dw_gate and dw_up [E,F,D] (from dh, du and
+ * x), dw_down [E,D,F] (from dy and a); the rest as for fp8z1_ffn_wgrad. */
+int fp8z1_ffn_bwd_weights_workspace_bytes(const fp8z1_ffn* f, size_t* bytes);
+int fp8z1_ffn_bwd_weights(const fp8z1_ffn* f, const void* x, const void* a, const void* dy, const void* dh,
+                          const void* du, const int32_t* offsets, int32_t dw_dtype, void* dw_gate, void* dw_up,
+                          void* dw_down, int32_t accumulate, void* d_workspace, size_t workspace_bytes, void* stream);
+
 /* gates of the join: the block's output is multiplied by */
 #define FP8Z1_GATE_NONE 0    /* nothing */
 #define FP8Z1_GATE_CHANNEL 1 /* float32 [C], the same for all rows */

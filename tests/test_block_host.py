@@ -75,6 +75,23 @@ def test_wgrad_arguments(bad, status):
     assert wgrad(**bad) == status
 
 
+def test_three_gradients_arguments():
+    def call(f, x=P, offsets=P, out=fz.F32, dw=P, acc=0, ws=None):
+        return fz.lib.fp8z1_ffn_bwd_weights(f, x, P, P, P, P, offsets, out, dw, P, P, acc, ws, 0, None)
+
+    assert call(None) == EINVAL
+    for bad in (dict(x=None), dict(x=P + 1), dict(offsets=None), dict(offsets=P + 1), dict(out=fz.F16), dict(dw=None),
+                dict(dw=P + 2), dict(out=fz.BF16, acc=1), dict(ws=P + 2)):
+        assert call(ffn(), **bad) == EINVAL, bad
+    for bad in (dict(T=-1), dict(E=0), dict(D=0), dict(F=2 ** 20 + 1), dict(E=65535, D=2 ** 20, F=2 ** 20)):
+        assert call(ffn(**bad)) == ESHAPE, bad
+    assert call(ffn(dtype=fz.F32)) == EINVAL
+    n = C.c_size_t()
+    q = fz.lib.fp8z1_ffn_bwd_weights_workspace_bytes
+    assert q(None, C.byref(n)) == EINVAL and q(ffn(), None) == EINVAL and q(ffn(D=0), C.byref(n)) == ESHAPE
+    assert q(ffn(E=1, T=100000), C.byref(n)) == 0 and n.value and n.value % (3 * 4 * 64 * 32) == 0
+
+
 def test_wgrad_workspace():
     n = C.c_size_t(7)
     q = fz.lib.fp8z1_ffn_wgrad_workspace_bytes

@@ -183,6 +183,25 @@ def test_weight_gradient(T, E, M, N, dtype):
         wgrad_check(p, q, E, offsets, dw, torch.float32, "accumulated dw", start)
 
 
+@pytest.mark.parametrize("T,E,D,F", [(0, 2, 40, 24), (1, 1, 130, 66), (150, 3, 200, 136), (4000, 1, 72, 264),
+                                     (3000, 2, 133, 65)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_three_weight_gradients_at_once(T, E, D, F, dtype):
+    c = Case(T, E, D, F, dtype)
+    dev = [c.dev(n) for n in ("x", "a", "dy", "dh", "du")]
+    want = ((c.dh, c.x), (c.du, c.x), (c.dy, c.a))
+    for t in (torch.float32, torch.bfloat16):
+        dw = block.ffn_backward_weights(*dev, n_experts=E, offsets=c.dev("offsets"), dtype=t)
+        for (p, q), got in zip(want, dw):
+            wgrad_check(p, q, E, c.offsets, got, t, f"{t}")
+    start = [torch.randn(w.shape, generator=torch.Generator().manual_seed(5)) for w in dw]
+    out = [s.cuda() for s in start]
+    got = block.ffn_backward_weights(*dev, n_experts=E, offsets=c.dev("offsets"), out=out)
+    for (p, q), g, s, o in zip(want, got, start, out):
+        assert g is o
+        wgrad_check(p, q, E, c.offsets, g, torch.float32, "added", s)
+
+
 def test_rows_and_codes_at_any_alignment():
     """Every buffer one element past a 16-byte boundary, codes at odd addresses."""
     c = Case(150, 2, 192, 160)
