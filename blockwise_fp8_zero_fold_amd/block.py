@@ -255,14 +255,14 @@ def norm_join_backward(dz: Optional[torch.Tensor], dn: Optional[torch.Tensor], y
     pdn = None if dn is None else _check(dn, dev, rows, (T, C), f"{what} dn")
     py = None if y is None else _check(y, dev, rows, (T, C), f"{what} y")
     pz = _check(z, dev, z.dtype, (T, C), f"{what} z")
-    out: Dict[str, Optional[torch.Tensor]] = {
-        "dy": None if y is None else y.new_empty((T, C)),
-        "dres": z.new_empty((T, C)),
-        "dw_post": None if w_post is None else w_post.new_empty((C,)),
-        "dgate": None if gate is None else gate.new_empty(gate.shape),
-        "dw_pre": None if w_pre is None else w_pre.new_empty((C,))}
+    dy, dres = None if y is None else y.new_empty((T, C)), z.new_empty((T, C))
+    # the gradients summed over rows share one buffer
+    cols = z.new_empty((3, C), dtype=torch.float32).unbind(0)
+    dgate = None if gate is None else cols[2] if gate.dim() == 1 else gate.new_empty(gate.shape)
+    dw_post, dw_pre = None if w_post is None else cols[0], None if w_pre is None else cols[1]
     n = _norm_workspace(T, C)
     ws = _scratch(z, n)
-    L._check(L.lib.fp8z1_norm_join_bwd(f, pdz, pdn, py, pz, wpost, pg, wpre, *(L._ptr(v) for v in out.values()),
-                                       L._ptr(ws), n, L._current_stream(dev)), what)
-    return out
+    L._check(L.lib.fp8z1_norm_join_bwd(f, pdz, pdn, py, pz, wpost, pg, wpre, L._ptr(dy), dres.data_ptr(),
+                                       L._ptr(dw_post), L._ptr(dgate), L._ptr(dw_pre), L._ptr(ws), n,
+                                       L._current_stream(dev)), what)
+    return {"dy": dy, "dres": dres, "dw_post": dw_post, "dgate": dgate, "dw_pre": dw_pre}

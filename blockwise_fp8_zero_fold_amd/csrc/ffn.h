@@ -52,12 +52,13 @@ __device__ __forceinline__ int32_t wave_isum(int32_t v) {
 // past the last full round would leave most of it idle, they are split along k instead into
 // `splits` parts each, the parts' float32 sums go to the workspace and a second kernel
 // (some 5 us) adds them in order and finishes the tiles.  A part is at least 8 scale
-// blocks of k behind full rounds, and 2 where there is no full round.
+// blocks of k behind full rounds, and 2 where there is no full round; sums of less than 8
+// blocks are not split (a block takes about 1 us).
 constexpr int32_t kSlots = 512;
 
 __host__ __device__ __forceinline__ int32_t tile_splits(int64_t tiles, int32_t blocks) {
   const int32_t rest = static_cast<int32_t>(tiles % kSlots);
-  if (!rest) return 1;
+  if (!rest || blocks < 8) return 1;
   const int32_t s = kSlots / rest, most = blocks / (tiles < kSlots ? 2 : 8);
   return s < most ? s : most;
 }

@@ -170,11 +170,15 @@ __global__ __launch_bounds__(kThreads, 2) void ffn_tile_kernel(FfnArgs p, int32_
   constexpr int kBC = kBBytes / 16 / kThreads;  // 16-byte chunks per thread and stage: 2 or 4
   constexpr int kBPer = kTrans ? kB2 / 16 : 4;  // chunks per row of B's stage
   typedef typename H::v8 v8;
-  // two stages, as separate arrays: copies into one are then known not to touch the other
-  __shared__ __attribute__((aligned(16))) uint8_t sa0[kABytes];
-  __shared__ __attribute__((aligned(16))) uint8_t sb0[kBBytes];
-  __shared__ __attribute__((aligned(16))) uint8_t sa1[kABytes];
-  __shared__ __attribute__((aligned(16))) uint8_t sb1[kBBytes];
+  // Stages in LDS: two, each copied while the other is computed.  The narrow tiles of small
+  // problems, whose matrix instructions take less time than a copy, have three, copied two ahead.
+  constexpr bool kRing = DIRECT && NT == 2;
+  constexpr int kStageBytes = kABytes + kBBytes;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[(kRing ? 3 : 2) * kStageBytes];
+  uint8_t* const sa0 = lds;
+  uint8_t* const sb0 = lds + kABytes;
+  uint8_t* const sa1 = sa0 + kStageBytes;
+  uint8_t* const sb1 = sb0 + kStageBytes;
 
   const int32_t kb = (p.K + kB - 1) / kB, blocks = kSeg * kb;  // scale blocks of k, each two stages
   int32_t rowtiles, first, e, lo, hi, m0, col;
@@ -353,6 +357,34 @@ __global__ __launch_bounds__(kThreads, 2) void ffn_tile_kernel(FfnArgs p, int32_
       const bool seg = kSeg == 2 && q >= kb;
       fetch(seg ? 1 : 0, (seg ? q - kb : q) * kB + second, sa, sb);
     };
+    if constexpr (kRing) {
+      const int32_t count = 2 * (q1 - q0);
+      auto ring = [&](int32_t s, int at) {
+        stage(q0 + (s >> 1), (s & 1) * kStep, lds + at * kStageBytes, lds + at * kStageBytes + kABytes);
+      };
+      ring(0, 0);
+      ring(1, 1);
+      int at = 0;
+      for (int32_t s = 0; s < count; ++s) {
+        const int32_t q = q0 + (s >> 1);
+        if (!(s & 1)) before(q);
+        if (s + 1 < count)
+          wait_copies<4 + kBC>();
+        else
+          wait_copies<0>();
+        __syncthreads();
+        uint8_t* const sa = lds + at * kStageBytes;
+        const int32_t left = K - (kSeg == 2 && q >= kb ? q - kb : q) * kB - (s & 1) * kStep;
+        if (left < kStep) clear_past(left, sa, sa + kABytes);
+        compute(sa, sa + kABytes, d, j0_, nj_, [&] {
+          if (s + 2 < count) ring(s + 2, at == 0 ? 2 : at - 1);
+        });
+        at = at == 2 ? 0 : at + 1;
+        if (s & 1) after(q);
+      }
+      __syncthreads();  // the stages are written again by the next pass
+      return;
+    }
     stage(q0, 0, sa0, sb0);
     put(sa0, sb0);
     for (int32_t q = q0; q < q1; ++q) {
@@ -509,7 +541,7 @@ int64_t most_row_tiles(int64_t T, int64_t E) { return T / kRows + (T < E ? T : E
 // are some to split.
 bool split_pays(const FfnArgs& p, int products, int64_t tiles) {
   const int32_t blocks = products * ((p.K + kB - 1) / kB);
-  return p.offsets ? blocks >= 4 : tile_splits(tiles, blocks) > 1;
+  return p.offsets ? blocks >= 8 : tile_splits(tiles, blocks) > 1;
 }
 // bytes of a round of parts
 size_t part_bytes(int nt) { return sizeof(float) * kSlots * kRows * 64 * nt; }

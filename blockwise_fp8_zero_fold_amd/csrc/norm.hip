@@ -25,6 +25,7 @@ struct NormArgs {
   void *dy, *dres, *dgate;
   float* part;  // [3][gridDim.x][C]: dw_post, dw_pre, dgate
   int32_t T, C, gate_kind, want_post, want_pre, want_gate;
+  int32_t waves;  // per row (backward)
   float eps, res_scale, block_scale, offset;
 };
 
@@ -41,7 +42,7 @@ struct Elem<F32> {
   typedef float type;
 };
 
-// 8 consecutive elements of a row: chunk `ch` of this thread, in 16-byte accesses at any
+// 8 consecutive elements of a row from column c, in 16-byte accesses at any
 // alignment of the elements (gfx950 runs in unaligned-access mode); those past the end
 // are 0 and not stored.
 typedef uint32_t v4u_a2_global_t __attribute__((ext_vector_type(4), aligned(2), address_space(1)));
@@ -54,10 +55,9 @@ struct Raw8 {
 };
 
 template <class H>
-__device__ __forceinline__ Raw8<H> fetch8(const void* row, int32_t C, int ch) {
+__device__ __forceinline__ Raw8<H> fetch8(const void* row, int32_t C, int32_t c) {
   typedef typename Elem<H>::type E;
   constexpr int kVecs = sizeof(E) * 8 / 16;
-  const int32_t c = (ch * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * 8;
   const E* p = static_cast<const E*>(row) + c;
   Raw8<H> r;
 #pragma unroll
@@ -90,15 +90,14 @@ __device__ __forceinline__ void widen8f(const Raw8<H>& r, float (&v)[8]) {
 }
 
 template <class H>
-__device__ __forceinline__ void load8(const void* row, int32_t C, int ch, float (&v)[8]) {
-  widen8f<H>(fetch8<H>(row, C, ch), v);
+__device__ __forceinline__ void load8(const void* row, int32_t C, int32_t c, float (&v)[8]) {
+  widen8f<H>(fetch8<H>(row, C, c), v);
 }
 
 template <class H>
-__device__ __forceinline__ void store8(void* row, int32_t C, int ch, const float (&v)[8]) {
+__device__ __forceinline__ void store8(void* row, int32_t C, int32_t c, const float (&v)[8]) {
   typedef typename Elem<H>::type E;
   constexpr int kVecs = sizeof(E) * 8 / 16;
-  const int32_t c = (ch * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * 8;
   E* p = static_cast<E*>(row) + c;
   if (c + 8 <= C) {
     v4u_v_t x[kVecs];
@@ -144,24 +143,25 @@ __device__ __forceinline__ float wave_fsum(float v) {
   return v;
 }
 
-// Sums of N values over the workgroup, in a fixed order; every thread gets them.  `lds`
-// holds 16 N floats; calls in a row use different ones, so one barrier each is enough
-// (a set is written again only after the next set's barrier).
+// Sums of N values over the `waves` waves of a row, in a fixed order; every thread of the row
+// gets them.  A workgroup may hold several rows, each with its own consecutive waves.
+// `lds` holds 16 N floats; calls in a row use different ones, so one barrier each is
+// enough (a set is written again only after the next set's barrier).
 template <int N>
-__device__ __forceinline__ void row_sums(float (&v)[N], float* lds) {
+__device__ __forceinline__ void row_sums(float (&v)[N], float* lds, int waves) {
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = wave_fsum(v[i]);
-  const int waves = blockDim.x >> 6, w = threadIdx.x >> 6;
   if (waves == 1) return;
+  const int w = threadIdx.x >> 6, w0 = w / waves * waves;
   if ((threadIdx.x & 63) == 0)
 #pragma unroll
     for (int i = 0; i < N; ++i) lds[w * N + i] = v[i];
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = lds[i];
+  for (int i = 0; i < N; ++i) v[i] = lds[w0 * N + i];
   for (int k = 1; k < waves; ++k)
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += lds[k * N + i];
+    for (int i = 0; i < N; ++i) v[i] += lds[(w0 + k) * N + i];
 }
 
 __device__ __forceinline__ float rstd_of(float sum, int32_t C, float eps) {
@@ -169,9 +169,9 @@ __device__ __forceinline__ float rstd_of(float sum, int32_t C, float eps) {
 }
 
 // o + w, or 1 where there is no weight
-__device__ __forceinline__ void load_weight(const float* w, int32_t C, int ch, float offset, float (&v)[8]) {
+__device__ __forceinline__ void load_weight(const float* w, int32_t C, int32_t c, float offset, float (&v)[8]) {
   if (w) {
-    load8<F32>(w, C, ch, v);
+    load8<F32>(w, C, c, v);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] += offset;
   } else {
@@ -182,11 +182,11 @@ __device__ __forceinline__ void load_weight(const float* w, int32_t C, int ch, f
 
 // the gate's values of a row, times block_scale
 template <class H>
-__device__ __forceinline__ void load_gate(const NormArgs& a, int64_t row, int ch, float (&g)[8]) {
+__device__ __forceinline__ void load_gate(const NormArgs& a, int64_t row, int32_t c, float (&g)[8]) {
   if (a.gate_kind == FP8Z1_GATE_CHANNEL) {
-    load8<F32>(a.gate, a.C, ch, g);
+    load8<F32>(a.gate, a.C, c, g);
   } else if (a.gate_kind == FP8Z1_GATE_FULL) {
-    load8<H>(row_of<H>(a.gate, row, a.C), a.C, ch, g);
+    load8<H>(row_of<H>(a.gate, row, a.C), a.C, c, g);
   } else {
     const float x = a.gate_kind == FP8Z1_GATE_TOKEN ? static_cast<const float*>(a.gate)[row] : 1.0f;
 #pragma unroll
@@ -200,33 +200,35 @@ template <class H, class R, int CH>
 __global__ __launch_bounds__(1024) void norm_join_kernel(NormArgs a) {
   __shared__ float lds[2][16];
   constexpr bool kHold = CH == 1;  // weights kept in registers over the rows
+  const int waves = blockDim.x >> 6;
+  auto col = [&](int ch) { return static_cast<int32_t>(ch * blockDim.x + threadIdx.x) * 8; };
   float wpost[CH][8], wpre[CH][8], gate[CH][8];
 #pragma unroll
   for (int ch = 0; ch < CH; ++ch)
     if (kHold) {
-      load_weight(a.w_post, a.C, ch, a.offset, wpost[ch]);
-      load_weight(a.w_pre, a.C, ch, a.offset, wpre[ch]);
-      if (a.gate_kind == FP8Z1_GATE_CHANNEL) load_gate<H>(a, 0, ch, gate[ch]);
+      load_weight(a.w_post, a.C, col(ch), a.offset, wpost[ch]);
+      load_weight(a.w_pre, a.C, col(ch), a.offset, wpre[ch]);
+      if (a.gate_kind == FP8Z1_GATE_CHANNEL) load_gate<H>(a, 0, col(ch), gate[ch]);
     }
   for (int32_t row = blockIdx.x; row < a.T; row += gridDim.x) {
     float y[CH][8], z[CH][8];
     float sum[1] = {0.0f};
 #pragma unroll
     for (int ch = 0; ch < CH; ++ch) {
-      if (a.y) load8<H>(row_of<H>(a.y, row, a.C), a.C, ch, y[ch]);
-      load8<R>(row_of<R>(a.res, row, a.C), a.C, ch, z[ch]);
+      if (a.y) load8<H>(row_of<H>(a.y, row, a.C), a.C, col(ch), y[ch]);
+      load8<R>(row_of<R>(a.res, row, a.C), a.C, col(ch), z[ch]);
       if (!kHold) {
-        load_weight(a.w_post, a.C, ch, a.offset, wpost[ch]);
-        load_weight(a.w_pre, a.C, ch, a.offset, wpre[ch]);
+        load_weight(a.w_post, a.C, col(ch), a.offset, wpost[ch]);
+        load_weight(a.w_pre, a.C, col(ch), a.offset, wpre[ch]);
       }
-      if (a.y && (!kHold || a.gate_kind != FP8Z1_GATE_CHANNEL)) load_gate<H>(a, row, ch, gate[ch]);
+      if (a.y && (!kHold || a.gate_kind != FP8Z1_GATE_CHANNEL)) load_gate<H>(a, row, col(ch), gate[ch]);
       if (a.y)
 #pragma unroll
         for (int i = 0; i < 8; ++i) sum[0] = fmaf(y[ch][i], y[ch][i], sum[0]);
     }
     float r = 1.0f;
     if (a.w_post) {
-      row_sums<1>(sum, lds[0]);
+      row_sums<1>(sum, lds[0], waves);
       r = rstd_of(sum[0], a.C, a.eps);
     }
     sum[0] = 0.0f;
@@ -238,16 +240,16 @@ __global__ __launch_bounds__(1024) void norm_join_kernel(NormArgs a) {
         if (a.y) z[ch][i] = fmaf(gate[ch][i], y[ch][i] * r * wpost[ch][i], z[ch][i]);
         sum[0] = fmaf(z[ch][i], z[ch][i], sum[0]);
       }
-      if (a.z) store8<R>(row_of<R>(a.z, row, a.C), a.C, ch, z[ch]);
+      if (a.z) store8<R>(row_of<R>(a.z, row, a.C), a.C, col(ch), z[ch]);
     }
     if (a.n) {
-      row_sums<1>(sum, lds[1]);
+      row_sums<1>(sum, lds[1], waves);
       r = rstd_of(sum[0], a.C, a.eps);
 #pragma unroll
       for (int ch = 0; ch < CH; ++ch) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) z[ch][i] = z[ch][i] * r * wpre[ch][i];
-        store8<H>(row_of<H>(a.n, row, a.C), a.C, ch, z[ch]);
+        store8<H>(row_of<H>(a.n, row, a.C), a.C, col(ch), z[ch]);
       }
     }
     if (!(a.w_post && a.n)) __syncthreads();  // only one of the two LDS sets is used per row
@@ -272,23 +274,28 @@ __global__ __launch_bounds__(1024) void norm_join_bwd_kernel(NormArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t ahead[];
   constexpr bool kHold = CH == 1;
   constexpr int kR = sizeof(typename Elem<R>::type) / 2, kH = sizeof(typename Elem<H>::type) / 2;  // KB of a wave's 512
+  const int rt = a.waves * 64, sub = static_cast<int>(threadIdx.x) / rt, t = static_cast<int>(threadIdx.x) - sub * rt;
+  const int rows = blockDim.x / rt;  // rows at a time
+  auto col = [&](int ch) { return static_cast<int32_t>(ch * rt + t) * 8; };
   float wpost[CH][8], wpre[CH][8], gate[CH][8], spost[CH][8], spre[CH][8], sgate[CH][8];
 #pragma unroll
   for (int ch = 0; ch < CH; ++ch) {
     if (kHold) {
-      load_weight(a.w_post, a.C, ch, a.offset, wpost[ch]);
-      load_weight(a.w_pre, a.C, ch, a.offset, wpre[ch]);
-      if (a.gate_kind == FP8Z1_GATE_CHANNEL) load_gate<H>(a, 0, ch, gate[ch]);
+      load_weight(a.w_post, a.C, col(ch), a.offset, wpost[ch]);
+      load_weight(a.w_pre, a.C, col(ch), a.offset, wpre[ch]);
+      if (a.gate_kind == FP8Z1_GATE_CHANNEL) load_gate<H>(a, 0, col(ch), gate[ch]);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) spost[ch][i] = spre[ch][i] = sgate[ch][i] = 0.0f;
   }
   const float inv = 1.0f / static_cast<float>(a.C);
 
-  // a wave's part of LDS: y, dn, z, dz of its 512 columns; 16 bytes per lane and copy
+  // a wave's part of LDS: y, dn, z, dz and a full gate of its 512 columns; 16 bytes per lane and copy
   const int lane = threadIdx.x & 63;
-  const int32_t c = static_cast<int32_t>(threadIdx.x) * 8, cin = min(c, a.C - 8);  // (lanes past the row copy its end)
-  uint8_t* const mine = ahead + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * ((2 * kH + 2 * kR) * 1024);
+  const int32_t c = t * 8, cin = min(c, a.C - 8);  // (lanes past the row copy its end)
+  const bool full = a.gate_kind == FP8Z1_GATE_FULL;
+  uint8_t* const mine =
+      ahead + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * ((2 * kH + 2 * kR + (full ? kH : 0)) * 1024);
   auto copy_row = [&](int32_t row) {
     auto one = [&](const void* p, int per, int at) {  // per: 2-byte units of an element
       const int64_t bytes = static_cast<int64_t>(a.C) * 2 * per;
@@ -301,6 +308,7 @@ __global__ __launch_bounds__(1024) void norm_join_bwd_kernel(NormArgs a) {
       one(a.res, kR, 2 * kH);
     }
     if (a.dz) one(a.dz, kR, 2 * kH + kR);
+    if (full) one(a.gate, kH, 2 * kH + 2 * kR);
   };
   auto take = [&](auto tag, int at, float(&v)[8]) {
     typedef decltype(tag) T;
@@ -313,9 +321,16 @@ __global__ __launch_bounds__(1024) void norm_join_bwd_kernel(NormArgs a) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = 0.0f;
   };
-  if (AHEAD && static_cast<int32_t>(blockIdx.x) < a.T) copy_row(blockIdx.x);
+  const int32_t step = static_cast<int32_t>(gridDim.x) * rows, last = a.T - 1;
+  const int32_t usub = __builtin_amdgcn_readfirstlane(sub);
+  int32_t base = static_cast<int32_t>(blockIdx.x) * rows;
+  if (AHEAD && base < a.T) copy_row(min(base + usub, last));
 
-  for (int32_t row = blockIdx.x; row < a.T; row += gridDim.x) {
+  // (all rows of a workgroup take the same number of turns: the barriers are shared; a turn
+  // past the end repeats the last row and adds and writes nothing)
+  for (; base < a.T; base += step) {
+    const bool live = base + usub < a.T;
+    const int32_t row = min(base + usub, last);
     float y[CH][8], z[CH][8], d[CH][8], dn[CH][8];
     float s1[3] = {0.0f, 0.0f, 0.0f};
     if (AHEAD) wait_copies();
@@ -329,21 +344,29 @@ __global__ __launch_bounds__(1024) void norm_join_bwd_kernel(NormArgs a) {
         }
         if (a.dz) take(R{}, 2 * kH + kR, d[ch]);
       } else {
-        if (a.y) load8<H>(row_of<H>(a.y, row, a.C), a.C, ch, y[ch]);
+        if (a.y) load8<H>(row_of<H>(a.y, row, a.C), a.C, col(ch), y[ch]);
         if (a.dn) {
-          load8<H>(row_of<H>(a.dn, row, a.C), a.C, ch, dn[ch]);
-          load8<R>(row_of<R>(a.res, row, a.C), a.C, ch, z[ch]);
+          load8<H>(row_of<H>(a.dn, row, a.C), a.C, col(ch), dn[ch]);
+          load8<R>(row_of<R>(a.res, row, a.C), a.C, col(ch), z[ch]);
         }
-        if (a.dz) load8<R>(row_of<R>(a.dz, row, a.C), a.C, ch, d[ch]);
+        if (a.dz) load8<R>(row_of<R>(a.dz, row, a.C), a.C, col(ch), d[ch]);
       }
       if (!a.dz)
 #pragma unroll
         for (int i = 0; i < 8; ++i) d[ch][i] = 0.0f;
       if (!kHold) {
-        load_weight(a.w_post, a.C, ch, a.offset, wpost[ch]);
-        load_weight(a.w_pre, a.C, ch, a.offset, wpre[ch]);
+        load_weight(a.w_post, a.C, col(ch), a.offset, wpost[ch]);
+        load_weight(a.w_pre, a.C, col(ch), a.offset, wpre[ch]);
       }
-      if (a.y && (!kHold || a.gate_kind != FP8Z1_GATE_CHANNEL)) load_gate<H>(a, row, ch, gate[ch]);
+      if (a.y && (!kHold || a.gate_kind != FP8Z1_GATE_CHANNEL)) {
+        if (AHEAD && full) {
+          take(H{}, 2 * kH + 2 * kR, gate[ch]);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) gate[ch][i] *= a.block_scale;
+        } else {
+          load_gate<H>(a, row, col(ch), gate[ch]);
+        }
+      }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         if (a.y) s1[0] = fmaf(y[ch][i], y[ch][i], s1[0]);
@@ -353,11 +376,11 @@ __global__ __launch_bounds__(1024) void norm_join_bwd_kernel(NormArgs a) {
         }
       }
     }
-    if (AHEAD && row + static_cast<int32_t>(gridDim.x) < a.T) {
+    if (AHEAD && base + step < a.T) {
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // this row's elements have left LDS
-      copy_row(row + gridDim.x);
+      copy_row(min(base + step + usub, last));
     }
-    row_sums<3>(s1, lds[0]);
+    row_sums<3>(s1, lds[0], a.waves);
     const float ry = a.w_post ? rstd_of(s1[0], a.C, a.eps) : 1.0f;
     const float rz = rstd_of(s1[1], a.C, a.eps);
     const float mz = s1[2] * rz * rz * inv;  // mean(v z^) rstd(z)
@@ -368,57 +391,74 @@ __global__ __launch_bounds__(1024) void norm_join_bwd_kernel(NormArgs a) {
       for (int i = 0; i < 8; ++i) {
         if (a.dn) {
           d[ch][i] = fmaf(rz, fmaf(-z[ch][i], mz, dn[ch][i] * wpre[ch][i]), d[ch][i]);
-          spre[ch][i] = fmaf(dn[ch][i], z[ch][i] * rz, spre[ch][i]);
+          if (live) spre[ch][i] = fmaf(dn[ch][i], z[ch][i] * rz, spre[ch][i]);
         }
         if (a.y) {
           y[ch][i] *= ry;  // y^ (or y)
           const float p = y[ch][i] * wpost[ch][i];
           const float dp = gate[ch][i] * d[ch][i];
-          spost[ch][i] = fmaf(dp, y[ch][i], spost[ch][i]);
-          sgate[ch][i] = fmaf(d[ch][i], p, sgate[ch][i]);
+          if (live) {
+            spost[ch][i] = fmaf(dp, y[ch][i], spost[ch][i]);
+            sgate[ch][i] = fmaf(d[ch][i], p, sgate[ch][i]);
+          }
           s2[0] = fmaf(dp, p, s2[0]);
           s2[1] = fmaf(d[ch][i], p, s2[1]);
         }
       }
-      if (a.dres) {
+      if (live && a.dres) {
         float o[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i] = a.res_scale * d[ch][i];
-        store8<R>(row_of<R>(a.dres, row, a.C), a.C, ch, o);
+        store8<R>(row_of<R>(a.dres, row, a.C), a.C, col(ch), o);
       }
     }
-    row_sums<2>(s2, lds[1]);
+    row_sums<2>(s2, lds[1], a.waves);
     const float my = s2[0] * inv;  // mean(dp (o + w_post) y^)
-    if (a.y)
+    if (live && a.y)
 #pragma unroll
       for (int ch = 0; ch < CH; ++ch) {
         float o[8];
         if (a.gate_kind == FP8Z1_GATE_FULL && a.dgate) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) o[i] = a.block_scale * d[ch][i] * (y[ch][i] * wpost[ch][i]);
-          store8<H>(row_of<H>(a.dgate, row, a.C), a.C, ch, o);
+          store8<H>(row_of<H>(a.dgate, row, a.C), a.C, col(ch), o);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           o[i] = gate[ch][i] * d[ch][i];
           if (a.w_post) o[i] = ry * fmaf(-y[ch][i], my, o[i] * wpost[ch][i]);
         }
-        if (a.dy) store8<H>(row_of<H>(a.dy, row, a.C), a.C, ch, o);
+        if (a.dy) store8<H>(row_of<H>(a.dy, row, a.C), a.C, col(ch), o);
       }
-    if (a.gate_kind == FP8Z1_GATE_TOKEN && a.dgate && threadIdx.x == 0)
+    if (a.gate_kind == FP8Z1_GATE_TOKEN && a.dgate && live && t == 0)
       static_cast<float*>(a.dgate)[row] = a.block_scale * s2[1];
   }
+  // the rows' column sums: added in order through LDS, then one set per workgroup
   const int64_t set = static_cast<int64_t>(gridDim.x) * a.C;
+  auto finish = [&](float(&v)[CH][8], int which, float scale) {
+    if constexpr (CH == 1)
+      if (rows > 1) {
+        float* const all = reinterpret_cast<float*>(ahead);
+        __syncthreads();
 #pragma unroll
-  for (int ch = 0; ch < CH; ++ch) {
-    if (a.want_post) store8<F32>(a.part + blockIdx.x * static_cast<int64_t>(a.C), a.C, ch, spost[ch]);
-    if (a.want_pre) store8<F32>(a.part + set + blockIdx.x * static_cast<int64_t>(a.C), a.C, ch, spre[ch]);
-    if (a.want_gate) {
+        for (int i = 0; i < 8; ++i) all[i * blockDim.x + threadIdx.x] = v[0][i];
+        __syncthreads();
+        if (sub == 0)
+          for (int k = 1; k < rows; ++k)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sgate[ch][i] *= a.block_scale;
-      store8<F32>(a.part + 2 * set + blockIdx.x * static_cast<int64_t>(a.C), a.C, ch, sgate[ch]);
+            for (int i = 0; i < 8; ++i) v[0][i] += all[i * blockDim.x + k * rt + t];
+      }
+    if (sub != 0) return;
+#pragma unroll
+    for (int ch = 0; ch < CH; ++ch) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[ch][i] *= scale;
+      store8<F32>(a.part + which * set + blockIdx.x * static_cast<int64_t>(a.C), a.C, col(ch), v[ch]);
     }
-  }
+  };
+  if (a.want_post) finish(spost, 0, 1.0f);
+  if (a.want_pre) finish(spre, 1, 1.0f);
+  if (a.want_gate) finish(sgate, 2, a.block_scale);
 }
 
 // Column sums of the workgroups' partial sums (blockIdx.y: which gradient), in a fixed
@@ -448,6 +488,8 @@ __global__ __launch_bounds__(1024) void norm_columns_kernel(const float* __restr
   }
 }
 
+bool misaligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
+
 constexpr int64_t kMaxC = FP8Z1_NORM_MAX_WIDTH;
 
 int threads_for(int64_t C) {
@@ -455,20 +497,25 @@ int threads_for(int64_t C) {
   return static_cast<int>((C + 64 * per - 1) / (64 * per) * 64);
 }
 
-// Workgroups, each walking over rows: as many waves as fit the card at a time.  Backward, each also
-// writes its column sums, so it takes at least 4 rows where that leaves a workgroup per
-// compute unit.
-int64_t groups_for(int64_t T, int64_t C, int waves_per_cu, int64_t rows = 1) {
-  const int64_t waves = threads_for(C) / 64;
-  int64_t most = (256 * waves_per_cu + waves - 1) / waves;
-  const int64_t few = T / rows > 256 ? T / rows : 256;
-  if (most > few) most = few;
+// Forward: a row per workgroup, as many waves as fit the card at a time, each walking over rows.
+int64_t fwd_groups(int64_t T, int64_t C) {
+  const int64_t waves = threads_for(C) / 64, most = (256 * 28 + waves - 1) / waves;
   return T < most ? T : most;
 }
-constexpr int kFwdWaves = 28, kBwdWaves = 14;
-int64_t bwd_groups(int64_t T, int64_t C) { return groups_for(T, C, kBwdWaves, 4); }
 
-bool misaligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
+// Backward: up to 16 waves per workgroup (a compute unit holds 16 of them, by their registers),
+// for several short rows at a time, since every workgroup also writes its column sums.
+struct Groups {
+  int64_t rows, count;  // rows at a time per workgroup, workgroups
+};
+Groups bwd_groups(int64_t T, int64_t C) {
+  const int64_t waves = threads_for(C) / 64;
+  int64_t rows = C <= 8192 ? 16 / waves : 1;
+  if (rows > (T + 255) / 256) rows = (T + 255) / 256;
+  if (rows < 1) rows = 1;
+  const int64_t most = 256 * (16 / (waves * rows)), want = (T + rows - 1) / rows;
+  return {rows, want < most ? want : most};
+}
 
 int check_norm(const fp8z1_norm* f, const void* y, const float* w_post, const void* gate, const char* what) {
   const std::string w(what);
@@ -507,17 +554,20 @@ NormArgs base_args(const fp8z1_norm* f, const void* y, const void* res, const fl
 }
 
 bool rows_aligned(const NormArgs& a) {
-  return !misaligned(a.y, 16) && !misaligned(a.res, 16) && !misaligned(a.dz, 16) && !misaligned(a.dn, 16);
+  return !misaligned(a.y, 16) && !misaligned(a.res, 16) && !misaligned(a.dz, 16) && !misaligned(a.dn, 16) &&
+         (a.gate_kind != FP8Z1_GATE_FULL || !misaligned(a.gate, 16));
 }
 
 template <class H, class R, bool BWD>
 void launch_typed(const NormArgs& a, dim3 g, dim3 b, hipStream_t s) {
   const bool one = a.C <= 8192;
-  constexpr size_t kBytes = 2 * (sizeof(typename Elem<H>::type) + sizeof(typename Elem<R>::type)) * 8;  // per thread
-  if (BWD && one && a.C % 8 == 0 && rows_aligned(a))
-    hipLaunchKernelGGL((norm_join_bwd_kernel<H, R, 1, true>), g, b, kBytes * b.x, s, a);
+  // LDS: the next row's elements, or the sums of several rows (32 bytes per thread, no more)
+  const size_t h = sizeof(typename Elem<H>::type), r = sizeof(typename Elem<R>::type);
+  const size_t bytes = (2 * h + 2 * r + (a.gate_kind == FP8Z1_GATE_FULL ? h : 0)) * 8 * b.x;
+  if (BWD && one && a.C % 8 == 0 && rows_aligned(a) && bytes <= 159 * 1024)  // of 160 KB
+    hipLaunchKernelGGL((norm_join_bwd_kernel<H, R, 1, true>), g, b, bytes, s, a);
   else if (BWD && one)
-    hipLaunchKernelGGL((norm_join_bwd_kernel<H, R, 1, false>), g, b, 0, s, a);
+    hipLaunchKernelGGL((norm_join_bwd_kernel<H, R, 1, false>), g, b, 32 * b.x, s, a);
   else if (BWD)
     hipLaunchKernelGGL((norm_join_bwd_kernel<H, R, 2, false>), g, b, 0, s, a);
   else if (one)
@@ -527,8 +577,8 @@ void launch_typed(const NormArgs& a, dim3 g, dim3 b, hipStream_t s) {
 }
 
 template <bool BWD>
-void launch(const fp8z1_norm* f, const NormArgs& a, int64_t groups, hipStream_t s) {
-  const dim3 g(static_cast<unsigned>(groups)), b(static_cast<unsigned>(threads_for(f->C)));
+void launch(const fp8z1_norm* f, const NormArgs& a, int64_t groups, int64_t rows, hipStream_t s) {
+  const dim3 g(static_cast<unsigned>(groups)), b(static_cast<unsigned>(rows * threads_for(f->C)));
   const bool wide = f->res_dtype == FP8Z1_F32;
   if (f->dtype == FP8Z1_F32)
     launch_typed<F32, F32, BWD>(a, g, b, s);
@@ -573,7 +623,7 @@ extern "C" int fp8z1_norm_join(const fp8z1_norm* f, const void* y, const void* r
   NormArgs a = base_args(f, y, res, w_post, gate, w_pre);
   a.z = z;
   a.n = n;
-  launch<false>(f, a, groups_for(f->T, f->C, kFwdWaves), static_cast<hipStream_t>(stream));
+  launch<false>(f, a, fwd_groups(f->T, f->C), 1, static_cast<hipStream_t>(stream));
   return check_hip(hipGetLastError(), "norm_join: launch");
 }
 
@@ -582,7 +632,7 @@ extern "C" int fp8z1_norm_join_bwd_workspace_bytes(const fp8z1_norm* f, size_t* 
   if (!f) return set_error(FP8Z1_EINVAL, "norm_join_bwd_workspace_bytes: NULL description");
   if (f->T < 0 || f->T > FP8Z1_FFN_MAX_ROWS || f->C < 1 || f->C > kMaxC)
     return set_error(FP8Z1_ESHAPE, "norm_join_bwd_workspace_bytes: T or C out of range");
-  *bytes = sizeof(float) * 3 * static_cast<size_t>(bwd_groups(f->T, f->C)) * static_cast<size_t>(f->C);
+  *bytes = sizeof(float) * 3 * static_cast<size_t>(bwd_groups(f->T, f->C).count) * static_cast<size_t>(f->C);
   return FP8Z1_OK;
 }
 
@@ -602,7 +652,7 @@ extern "C" int fp8z1_norm_join_bwd(const fp8z1_norm* f, const void* dz, const vo
   if (rc) return rc;
   float* gate_cols = f->gate == FP8Z1_GATE_CHANNEL ? static_cast<float*>(dgate) : nullptr;
   const bool sums = dw_post || dw_pre || gate_cols;
-  const int64_t groups = bwd_groups(f->T, f->C);
+  const Groups groups = bwd_groups(f->T, f->C);
   if (sums && f->T) {
     size_t need = 0;
     rc = fp8z1_norm_join_bwd_workspace_bytes(f, &need);
@@ -622,13 +672,14 @@ extern "C" int fp8z1_norm_join_bwd(const fp8z1_norm* f, const void* dz, const vo
     a.want_post = dw_post != nullptr;
     a.want_pre = dw_pre != nullptr;
     a.want_gate = gate_cols != nullptr;
-    launch<true>(f, a, groups, s);
+    a.waves = threads_for(f->C) / 64;
+    launch<true>(f, a, groups.count, groups.rows, s);
     rc = check_hip(hipGetLastError(), "norm_join_bwd: launch");
     if (rc) return rc;
   }
   if (sums) {
     hipLaunchKernelGGL(norm_columns_kernel, dim3(static_cast<unsigned>((f->C + 63) / 64), 3), dim3(1024), 0, s,
-                       static_cast<const float*>(workspace), static_cast<int32_t>(groups), static_cast<int32_t>(f->C),
+                       static_cast<const float*>(workspace), static_cast<int32_t>(groups.count), static_cast<int32_t>(f->C),
                        dw_post, dw_pre, gate_cols);
     rc = check_hip(hipGetLastError(), "norm_join_bwd: sums launch");
   }
