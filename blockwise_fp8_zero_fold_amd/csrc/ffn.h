@@ -27,6 +27,8 @@ struct FfnArgs {
   uint16_t *o0, *o1, *o2;  // outputs [T, N]
   float* part;             // partial sums of split tiles, or NULL: no tile is split
   int32_t T, E, N, K, act;
+  int32_t stages;      // LDS stages
+  int32_t split_from;  // sums of at least so many scale blocks may be split
 };
 
 // Rows of expert e, kept inside [0, T] whatever the offsets hold, so a wrong
@@ -52,13 +54,14 @@ __device__ __forceinline__ int32_t wave_isum(int32_t v) {
 // past the last full round would leave most of it idle, they are split along k instead into
 // `splits` parts each, the parts' float32 sums go to the workspace and a second kernel
 // (some 5 us) adds them in order and finishes the tiles.  A part is at least 8 scale
-// blocks of k behind full rounds, and 2 where there is no full round; sums of less than 8
-// blocks are not split (a block takes about 1 us).
+// blocks of k behind full rounds, and 2 where there is no full round; sums of less than
+// split_from blocks are not split: 8 with direct copies (a block takes about 1 us), 4
+// through registers (twice that).
 constexpr int32_t kSlots = 512;
 
-__host__ __device__ __forceinline__ int32_t tile_splits(int64_t tiles, int32_t blocks) {
+__host__ __device__ __forceinline__ int32_t tile_splits(int64_t tiles, int32_t blocks, int32_t from) {
   const int32_t rest = static_cast<int32_t>(tiles % kSlots);
-  if (!rest || blocks < 8) return 1;
+  if (!rest || !from || blocks < from) return 1;
   const int32_t s = kSlots / rest, most = blocks / (tiles < kSlots ? 2 : 8);
   return s < most ? s : most;
 }
@@ -79,7 +82,7 @@ __device__ __forceinline__ int32_t row_tiles(const int32_t* offsets, int32_t T, 
 
 template <int ROWS>
 __device__ __forceinline__ Plan plan_tiles(const int32_t* offsets, int32_t T, int32_t E, int32_t ncols,
-                                           int32_t blocks, bool may_split, int32_t& rowtiles, int32_t& first) {
+                                           int32_t blocks, int32_t split_from, int32_t& rowtiles, int32_t& first) {
   const int lane = threadIdx.x & 63;
   int32_t total = 0;
   first = 0;  // row tiles of expert `lane`
@@ -97,8 +100,8 @@ __device__ __forceinline__ Plan plan_tiles(const int32_t* offsets, int32_t T, in
   p.whole = p.tiles;
   p.splits = 1;
   const int32_t rest = p.tiles % kSlots;
-  const int32_t s = tile_splits(p.tiles, blocks);
-  if (may_split && s > 1) {
+  const int32_t s = tile_splits(p.tiles, blocks, split_from);
+  if (s > 1) {
     p.whole = p.tiles - rest;
     p.splits = s;
   }

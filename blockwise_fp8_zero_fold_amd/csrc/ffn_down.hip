@@ -25,6 +25,6 @@ extern "C" int fp8z1_ffn_workspace_bytes(const fp8z1_ffn* f, size_t* bytes) {
   const int rc = check_cfg(f, &some_offsets, "ffn_workspace_bytes");
   if (rc) return rc;
   const int64_t most = f->D > 2 * f->F ? f->D : 2 * f->F;  // longest sum of the four calls
-  *bytes = f->T && most > 6 * kB ? part_bytes(4) : 0;
+  *bytes = f->T && most > 2 * kB ? part_bytes(4) : 0;
   return FP8Z1_OK;
 }

@@ -47,22 +47,49 @@ __device__ __forceinline__ void load_row8(const uint16_t* from, uint32_t (&x)[4]
   }
 }
 
-// The results of 32 x 32 tile (i, j) of a wave (for kFfnUp x: gate, v: up): lane l holds of row
-// l % 32 the columns 8 q + 4 (l / 32) + 0..3, and exchanges them with the other half wave
-// for 8 columns in a row, so that rows are read and written 16 bytes at a time (2 bytes
-// at a time the results took a quarter of the kernel's time).
-template <class H, int KIND, int NT>
-__device__ __forceinline__ void store_tile(const FfnArgs& p, const f32x16& x, const f32x16& v, int32_t hi, int32_t m0,
-                                           int32_t n0, int i, int j) {
-  constexpr bool kUp = KIND == kFfnUp;
+// Where the lane's 8 columns g of tile (i, j) of its wave lie: lane l holds of row l % 32 the
+// columns 8 q + 4 (l / 32) + 0..3, and exchanges them with the other half wave for 8
+// columns in a row, so that rows are read and written 16 bytes at a time (2 bytes at
+// a time the results took a quarter of the kernel's time).
+template <int KIND, int NT>
+__device__ __forceinline__ int64_t place8(const FfnArgs& p, int32_t hi, int32_t m0, int32_t n0, int i, int j, int g,
+                                          int& count) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, wm = w >> 1, wn = w & 1;
   const int32_t m = m0 + wm * 64 + i * 32 + (lane & 31);
-  const bool row = m < hi;
+  const int32_t n = n0 + (wn * (KIND == kFfnUp ? NT / 2 : NT) + j) * 32 + g * 16 + (lane >> 5) * 8;
+  count = m < hi ? min(p.N - n, 8) : 0;
+  return static_cast<int64_t>(m) * p.N + n;
+}
+
+// h and u of a tile, for kFfnDownBwd; loaded for several tiles before the first is used
+struct Kept {
+  uint32_t h[2][4], u[2][4];
+};
+template <int KIND, int NT>
+__device__ __forceinline__ Kept load_kept(const FfnArgs& p, int32_t hi, int32_t m0, int32_t n0, int i, int j) {
+  Kept k = {};
+  if constexpr (KIND == kFfnDownBwd) {
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      int count;
+      const int64_t at = place8<KIND, NT>(p, hi, m0, n0, i, j, g, count);
+      if (count > 0) {
+        load_row8(p.h + at, k.h[g], count);
+        load_row8(p.u + at, k.u[g], count);
+      }
+    }
+  }
+  return k;
+}
+
+// The results of tile (i, j) of a wave (for kFfnUp x: gate, v: up).
+template <class H, int KIND, int NT>
+__device__ __forceinline__ void store_tile(const FfnArgs& p, const f32x16& x, const f32x16& v, Kept kept, int32_t hi,
+                                           int32_t m0, int32_t n0, int i, int j) {
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
-    const int32_t n = n0 + (wn * (kUp ? NT / 2 : NT) + j) * 32 + g * 16 + (lane >> 5) * 8;
-    const int count = row ? min(p.N - n, 8) : 0;
-    const int64_t at = static_cast<int64_t>(m) * p.N + n;
+    int count;
+    const int64_t at = place8<KIND, NT>(p, hi, m0, n0, i, j, g, count);
     // (x, y) pairs to exchange: words 0, 1 of group 2g and words 0, 1 of group 2g + 1
     auto pack = [&](const float (&f)[8], uint16_t* to) {
       uint32_t o[4];
@@ -74,7 +101,7 @@ __device__ __forceinline__ void store_tile(const FfnArgs& p, const f32x16& x, co
       if (count > 0) store_row8(to + at, o, count);
     };
     float f0[8], f1[8], f2[8];
-    if (kUp) {
+    if (KIND == kFfnUp) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         f1[k] = x[8 * g + k];
@@ -87,11 +114,8 @@ __device__ __forceinline__ void store_tile(const FfnArgs& p, const f32x16& x, co
         pack(f2, p.o2);
       }
     } else if (KIND == kFfnDownBwd) {
-      uint32_t h[4] = {0u, 0u, 0u, 0u}, u[4] = {0u, 0u, 0u, 0u};
-      if (count > 0) {
-        load_row8(p.h + at, h, count);
-        load_row8(p.u + at, u, count);
-      }
+      uint32_t(&h)[4] = kept.h[g];
+      uint32_t(&u)[4] = kept.u[g];
       exchange(h[0], h[2]);
       exchange(h[1], h[3]);
       exchange(u[0], u[2]);
@@ -171,10 +195,11 @@ __global__ __launch_bounds__(kThreads, 2) void ffn_tile_kernel(FfnArgs p, int32_
   constexpr int kBPer = kTrans ? kB2 / 16 : 4;  // chunks per row of B's stage
   typedef typename H::v8 v8;
   // Stages in LDS: two, each copied while the other is computed.  The narrow tiles of small
-  // problems, whose matrix instructions take less time than a copy, have three, copied two ahead.
+  // problems, whose matrix instructions take less time than a copy, have three, copied two
+  // ahead (two workgroups per compute unit), or five (where there is one at most).
   constexpr bool kRing = DIRECT && NT == 2;
   constexpr int kStageBytes = kABytes + kBBytes;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[(kRing ? 3 : 2) * kStageBytes];
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   uint8_t* const sa0 = lds;
   uint8_t* const sb0 = lds + kABytes;
   uint8_t* const sa1 = sa0 + kStageBytes;
@@ -183,7 +208,7 @@ __global__ __launch_bounds__(kThreads, 2) void ffn_tile_kernel(FfnArgs p, int32_
   const int32_t kb = (p.K + kB - 1) / kB, blocks = kSeg * kb;  // scale blocks of k, each two stages
   int32_t rowtiles, first, e, lo, hi, m0, col;
   const int32_t item = static_cast<int32_t>(blockIdx.x);
-  const Plan plan = plan_tiles<kRows>(p.offsets, p.T, p.E, ncols, blocks, p.part != nullptr, rowtiles, first);
+  const Plan plan = plan_tiles<kRows>(p.offsets, p.T, p.E, ncols, blocks, p.part ? p.split_from : 0, rowtiles, first);
   if (item >= plan.items()) return;
   const bool split = item >= plan.whole;
   const int32_t rest = plan.tiles - plan.whole;
@@ -242,6 +267,13 @@ __global__ __launch_bounds__(kThreads, 2) void ffn_tile_kernel(FfnArgs p, int32_
 #pragma unroll
       for (int j = 0; j < kBC; ++j)
         copy16_to_lds(j < kBC / 2 ? ba : bb, boff[j], sb + (w * 64 + kThreads * j) * 16);
+      return;
+    }
+    if (k0 + kStep <= K && (!kTrans || n0 + kB2 <= N)) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) ra[j] = ld16(x + aoff[j]);
+#pragma unroll
+      for (int j = 0; j < kBC; ++j) rb[j] = ld16((j < kBC / 2 ? wa : wb) + boff[j]);
       return;
     }
 #pragma unroll
@@ -362,24 +394,27 @@ __global__ __launch_bounds__(kThreads, 2) void ffn_tile_kernel(FfnArgs p, int32_
       auto ring = [&](int32_t s, int at) {
         stage(q0 + (s >> 1), (s & 1) * kStep, lds + at * kStageBytes, lds + at * kStageBytes + kABytes);
       };
-      ring(0, 0);
-      ring(1, 1);
+      const int32_t depth = p.stages;
+      for (int32_t s = 0; s < depth - 1 && s < count; ++s) ring(s, s);
       int at = 0;
       for (int32_t s = 0; s < count; ++s) {
         const int32_t q = q0 + (s >> 1);
         if (!(s & 1)) before(q);
-        if (s + 1 < count)
-          wait_copies<4 + kBC>();
-        else
-          wait_copies<0>();
+        constexpr int kCopies = 4 + kBC;  // of a stage
+        switch (min(depth - 2, count - 1 - s)) {  // stages that may still be on their way
+          case 0: wait_copies<0>(); break;
+          case 1: wait_copies<kCopies>(); break;
+          case 2: wait_copies<2 * kCopies>(); break;
+          default: wait_copies<3 * kCopies>(); break;
+        }
         __syncthreads();
         uint8_t* const sa = lds + at * kStageBytes;
         const int32_t left = K - (kSeg == 2 && q >= kb ? q - kb : q) * kB - (s & 1) * kStep;
         if (left < kStep) clear_past(left, sa, sa + kABytes);
         compute(sa, sa + kABytes, d, j0_, nj_, [&] {
-          if (s + 2 < count) ring(s + 2, at == 0 ? 2 : at - 1);
+          if (s + depth - 1 < count) ring(s + depth - 1, at == 0 ? depth - 1 : at - 1);
         });
-        at = at == 2 ? 0 : at + 1;
+        at = at == depth - 1 ? 0 : at + 1;
         if (s & 1) after(q);
       }
       __syncthreads();  // the stages are written again by the next pass
@@ -408,7 +443,7 @@ __global__ __launch_bounds__(kThreads, 2) void ffn_tile_kernel(FfnArgs p, int32_
   };
 
   // a tile's results (for kFfnUp: gate columns x, up columns v), or a part's sums
-  auto emit = [&](const f32x16& x, const f32x16& v, int i, int j) {
+  auto emit = [&](const f32x16& x, const f32x16& v, const Kept& kept, int i, int j) {
     if (split) {
       f32x4* const to = part_at<NT>(p.part, item - plan.whole);
 #pragma unroll
@@ -418,9 +453,10 @@ __global__ __launch_bounds__(kThreads, 2) void ffn_tile_kernel(FfnArgs p, int32_
           to[((i * NT + j + NT / 2) * 4 + r) * kThreads + t] = f32x4{v[4 * r], v[4 * r + 1], v[4 * r + 2], v[4 * r + 3]};
       }
     } else {
-      store_tile<H, KIND, NT>(p, x, v, hi, m0, n0, i, j);
+      store_tile<H, KIND, NT>(p, x, v, kept, hi, m0, n0, i, j);
     }
   };
+  auto keep = [&](int i, int j) { return split ? Kept{} : load_kept<KIND, NT>(p, hi, m0, n0, i, j); };
 
   // all waves decide alike: the barriers are shared
   float slo = 3e38f, shi = 0.0f;
@@ -469,10 +505,15 @@ __global__ __launch_bounds__(kThreads, 2) void ffn_tile_kernel(FfnArgs p, int32_
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[i][j][r] *= was[kUp && j >= NT / 2 ? 1 : 0];
+    constexpr int kJ = kUp ? NT / 2 : NT;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 2; ++i) {
+      Kept kept[kJ];
 #pragma unroll
-      for (int j = 0; j < (kUp ? NT / 2 : NT); ++j) emit(acc[i][j], acc[i][kUp ? j + NT / 2 : j], i, j);
+      for (int j = 0; j < kJ; ++j) kept[j] = keep(i, j);
+#pragma unroll
+      for (int j = 0; j < kJ; ++j) emit(acc[i][j], acc[i][kUp ? j + NT / 2 : j], kept[j], i, j);
+    }
   } else {
     auto pass = [&](auto j_) {
       constexpr int j = decltype(j_)::value;
@@ -495,7 +536,7 @@ __global__ __launch_bounds__(kThreads, 2) void ffn_tile_kernel(FfnArgs p, int32_
           sweep(part, Int<j>{}, Int<1>{}, clear, add);
       }
 #pragma unroll
-      for (int i = 0; i < 2; ++i) emit(sum[i][0], up[i][0], i, j);
+      for (int i = 0; i < 2; ++i) emit(sum[i][0], up[i][0], keep(i, j), i, j);
     };
     pass(Int<0>{});
     if constexpr (!kUp || NT == 4) pass(Int<1>{});
@@ -514,11 +555,12 @@ __global__ __launch_bounds__(kThreads) void ffn_join_kernel(FfnArgs p, int32_t n
   constexpr int kCols = (kUp ? 32 : 64) * NT, kJ = kUp ? NT / 2 : NT;
   const int32_t blocks = (KIND == kFfnUpBwd ? 2 : 1) * ((p.K + kB - 1) / kB);
   int32_t rowtiles, first, e, lo, hi, m0, col;
-  const Plan plan = plan_tiles<kRows>(p.offsets, p.T, p.E, ncols, blocks, true, rowtiles, first);
+  const Plan plan = plan_tiles<kRows>(p.offsets, p.T, p.E, ncols, blocks, p.split_from, rowtiles, first);
   const int32_t rest = plan.tiles - plan.whole, tile = static_cast<int32_t>(blockIdx.x) / (2 * kJ);
   if (tile >= rest) return;
   const int ij = static_cast<int>(blockIdx.x) % (2 * kJ), i = ij / kJ, j = ij % kJ, t = threadIdx.x;
   if (!find_tile<kRows>(p.offsets, p.T, p.E, ncols, rowtiles, first, plan.whole + tile, e, lo, hi, m0, col)) return;
+  const Kept kept = load_kept<KIND, NT>(p, hi, m0, col * kCols, i, j);
   f32x16 v[2] = {};
   for (int32_t s = 0; s < plan.splits; ++s) {
     const f32x4* from = part_at<NT>(p.part, s * rest + tile);
@@ -531,7 +573,7 @@ __global__ __launch_bounds__(kThreads) void ffn_join_kernel(FfnArgs p, int32_t n
         for (int c = 0; c < 4; ++c) v[k][4 * r + c] += x[c];
       }
   }
-  store_tile<H, KIND, NT>(p, v[0], v[1], hi, m0, col * kCols, i, j);
+  store_tile<H, KIND, NT>(p, v[0], v[1], kept, hi, m0, col * kCols, i, j);
 }
 
 // The most row tiles that T rows in E runs can make: every run may end in a partial tile.
@@ -541,7 +583,7 @@ int64_t most_row_tiles(int64_t T, int64_t E) { return T / kRows + (T < E ? T : E
 // are some to split.
 bool split_pays(const FfnArgs& p, int products, int64_t tiles) {
   const int32_t blocks = products * ((p.K + kB - 1) / kB);
-  return p.offsets ? blocks >= 8 : tile_splits(tiles, blocks) > 1;
+  return p.offsets ? blocks >= p.split_from : tile_splits(tiles, blocks, p.split_from) > 1;
 }
 // bytes of a round of parts
 size_t part_bytes(int nt) { return sizeof(float) * kSlots * kRows * 64 * nt; }
@@ -550,10 +592,11 @@ template <class H, int KIND, int NT>
 void launch_tiles(const FfnArgs& p, bool direct, int64_t tiles, int32_t ncols, hipStream_t s) {
   // a grid with room for the most parts: the rest of a round becomes at most a round of parts
   const dim3 g(static_cast<unsigned>(tiles + (p.part ? kSlots : 0))), b(kThreads);
+  const size_t lds = p.stages * (kABytes + NT * 64 * kStep);
   if (direct)
-    hipLaunchKernelGGL((ffn_tile_kernel<H, KIND, NT, true>), g, b, 0, s, p, ncols);
+    hipLaunchKernelGGL((ffn_tile_kernel<H, KIND, NT, true>), g, b, lds, s, p, ncols);
   else if constexpr (NT == 2)
-    hipLaunchKernelGGL((ffn_tile_kernel<H, KIND, 2, false>), g, b, 0, s, p, ncols);
+    hipLaunchKernelGGL((ffn_tile_kernel<H, KIND, 2, false>), g, b, lds, s, p, ncols);
   if (!p.part) return;
   const int64_t rest = tiles < kSlots ? tiles : kSlots - 1;
   const dim3 gj(static_cast<unsigned>(rest * 2 * (KIND == kFfnUp ? NT / 2 : NT)));
@@ -586,9 +629,11 @@ int launch(FfnArgs p, int32_t dtype, void* workspace, size_t workspace_bytes, hi
   const int32_t cols = per * (wide ? 4 : 2), ncols = (p.N + cols - 1) / cols;
   const int64_t tiles = rows * ncols;
   if (tiles > 0x7fffffff - kSlots) return set_error(FP8Z1_ESHAPE, std::string(what) + ": too many tiles");
+  p.split_from = direct ? 8 : 4;
   const int64_t known = p.offsets ? tiles : static_cast<int64_t>((p.T + kRows - 1) / kRows) * ncols;
   if (split_pays(p, KIND == kFfnUpBwd ? 2 : 1, known) && workspace_bytes >= part_bytes(wide ? 4 : 2))
     p.part = static_cast<float*>(workspace);
+  p.stages = !direct || wide ? 2 : tiles + (p.part ? kSlots : 0) > 256 ? 3 : 5;
   if (dtype == FP8Z1_BF16 && wide)
     launch_tiles<Bf16, KIND, 4>(p, direct, tiles, ncols, s);
   else if (dtype == FP8Z1_BF16)
