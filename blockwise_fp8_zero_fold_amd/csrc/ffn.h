@@ -27,7 +27,6 @@ struct FfnArgs {
   uint16_t *o0, *o1, *o2;  // outputs [T, N]
   float* part;             // partial sums of split tiles, or NULL: no tile is split
   int32_t T, E, N, K, act;
-  int32_t stages;      // LDS stages
   int32_t split_from;  // sums of at least so many scale blocks may be split
 };
 

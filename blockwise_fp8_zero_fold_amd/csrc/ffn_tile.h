@@ -47,97 +47,115 @@ __device__ __forceinline__ void load_row8(const uint16_t* from, uint32_t (&x)[4]
   }
 }
 
-// Where the lane's 8 columns g of tile (i, j) of its wave lie: lane l holds of row l % 32 the
-// columns 8 q + 4 (l / 32) + 0..3, and exchanges them with the other half wave for 8
-// columns in a row, so that rows are read and written 16 bytes at a time (2 bytes at
-// a time the results took a quarter of the kernel's time).
-template <int KIND, int NT>
-__device__ __forceinline__ int64_t place8(const FfnArgs& p, int32_t hi, int32_t m0, int32_t n0, int i, int j, int g,
-                                          int& count) {
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, wm = w >> 1, wn = w & 1;
-  const int32_t m = m0 + wm * 64 + i * 32 + (lane & 31);
-  const int32_t n = n0 + (wn * (KIND == kFfnUp ? NT / 2 : NT) + j) * 32 + g * 16 + (lane >> 5) * 8;
-  count = m < hi ? min(p.N - n, 8) : 0;
-  return static_cast<int64_t>(m) * p.N + n;
-}
-
-// h and u of a tile, for kFfnDownBwd; loaded for several tiles before the first is used
+// h and u of 8 columns of a row, for kFfnDownBwd
 struct Kept {
-  uint32_t h[2][4], u[2][4];
+  uint32_t h[4], u[4];
 };
-template <int KIND, int NT>
-__device__ __forceinline__ Kept load_kept(const FfnArgs& p, int32_t hi, int32_t m0, int32_t n0, int i, int j) {
+template <int KIND>
+__device__ __forceinline__ Kept load_kept(const FfnArgs& p, int64_t at, int count) {
   Kept k = {};
-  if constexpr (KIND == kFfnDownBwd) {
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      int count;
-      const int64_t at = place8<KIND, NT>(p, hi, m0, n0, i, j, g, count);
-      if (count > 0) {
-        load_row8(p.h + at, k.h[g], count);
-        load_row8(p.u + at, k.u[g], count);
-      }
+  if constexpr (KIND == kFfnDownBwd)
+    if (count > 0) {
+      load_row8(p.h + at, k.h, count);
+      load_row8(p.u + at, k.u, count);
     }
-  }
   return k;
 }
 
-// The results of tile (i, j) of a wave (for kFfnUp x: gate, v: up).
-template <class H, int KIND, int NT>
-__device__ __forceinline__ void store_tile(const FfnArgs& p, const f32x16& x, const f32x16& v, Kept kept, int32_t hi,
-                                           int32_t m0, int32_t n0, int i, int j) {
+// The results of 8 columns of a row, of which `count` are there (for kFfnUp x: gate, v: up).
+template <class H, int KIND>
+__device__ __forceinline__ void finish8(const FfnArgs& p, int64_t at, int count, const float (&x)[8],
+                                        const float (&v)[8], const Kept& kept) {
+  auto put = [&](const float (&f)[8], uint16_t* to) {
+    uint32_t o[4];
 #pragma unroll
-  for (int g = 0; g < 2; ++g) {
-    int count;
-    const int64_t at = place8<KIND, NT>(p, hi, m0, n0, i, j, g, count);
-    // (x, y) pairs to exchange: words 0, 1 of group 2g and words 0, 1 of group 2g + 1
-    auto pack = [&](const float (&f)[8], uint16_t* to) {
-      uint32_t o[4];
+    for (int k = 0; k < 4; ++k)
+      o[k] = static_cast<uint32_t>(H::from_f32(f[2 * k])) | static_cast<uint32_t>(H::from_f32(f[2 * k + 1])) << 16;
+    store_row8(to + at, o, count);
+  };
+  if (count <= 0) return;
+  if (KIND == kFfnUp) {
+    float a[8];
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        o[k] = static_cast<uint32_t>(H::from_f32(f[2 * k])) | static_cast<uint32_t>(H::from_f32(f[2 * k + 1])) << 16;
-      exchange(o[0], o[2]);
-      exchange(o[1], o[3]);
-      if (count > 0) store_row8(to + at, o, count);
-    };
-    float f0[8], f1[8], f2[8];
-    if (KIND == kFfnUp) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        f1[k] = x[8 * g + k];
-        f2[k] = v[8 * g + k];
-        f0[k] = act_value(p.act, f1[k]) * f2[k];
-      }
-      pack(f0, p.o0);
-      if (p.o1) {
-        pack(f1, p.o1);
-        pack(f2, p.o2);
-      }
-    } else if (KIND == kFfnDownBwd) {
-      uint32_t(&h)[4] = kept.h[g];
-      uint32_t(&u)[4] = kept.u[g];
-      exchange(h[0], h[2]);
-      exchange(h[1], h[3]);
-      exchange(u[0], u[2]);
-      exchange(u[1], u[3]);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float hk = H::to_f32(static_cast<uint16_t>(h[k / 2] >> (16 * (k % 2))));
-        const float uk = H::to_f32(static_cast<uint16_t>(u[k / 2] >> (16 * (k % 2))));
-        float value, slope;
-        act_both(p.act, hk, value, slope);
-        f0[k] = x[8 * g + k] * uk * slope;
-        f1[k] = x[8 * g + k] * value;
-        f2[k] = value * uk;
-      }
-      pack(f0, p.o0);
-      pack(f1, p.o1);
-      if (p.o2) pack(f2, p.o2);
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) f0[k] = x[8 * g + k];
-      pack(f0, p.o0);
+    for (int k = 0; k < 8; ++k) a[k] = act_value(p.act, x[k]) * v[k];
+    put(a, p.o0);
+    if (p.o1) {
+      put(x, p.o1);
+      put(v, p.o2);
     }
+  } else if (KIND == kFfnDownBwd) {
+    float dh[8], du[8], a[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float h = H::to_f32(static_cast<uint16_t>(kept.h[k / 2] >> (16 * (k % 2))));
+      const float u = H::to_f32(static_cast<uint16_t>(kept.u[k / 2] >> (16 * (k % 2))));
+      float value, slope;
+      act_both(p.act, h, value, slope);
+      dh[k] = x[k] * u * slope;
+      du[k] = x[k] * value;
+      a[k] = value * u;
+    }
+    put(dh, p.o0);
+    put(du, p.o1);
+    if (p.o2) put(a, p.o2);
+  } else {
+    put(x, p.o0);
+  }
+}
+
+// A wave's results on their way to memory: 64 rows of 64 float32 in LDS (for kFfnUp 32 gate
+// and 32 up columns), so that the rows leave 16 bytes per lane and 128 bytes in a row, by a
+// loop of little code: from the accumulators directly, 2 bytes at a time, the results took
+// a quarter of a large problem's time, and their unrolled code, read once, most of a
+// small one's.  Chunk c (16 bytes) of row r sits at c ^ (r mod 16).
+constexpr int kResultBytes = 4 * 64 * 64 * 4;
+__device__ __forceinline__ int result_at(int r, int c) { return r * 256 + ((c ^ (r & 15)) << 4); }
+
+// 32 x 32 tile (i, j): lane l holds of row l % 32 the columns 8 q + 4 (l / 32) + 0..3.
+__device__ __forceinline__ void lay_tile(const f32x16& x, uint8_t* to, int i, int j) {
+  const int lane = threadIdx.x & 63, r = i * 32 + (lane & 31);
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    *reinterpret_cast<f32x4*>(to + result_at(r, j * 8 + q * 2 + (lane >> 5))) =
+        f32x4{x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]};
+}
+
+__device__ __forceinline__ void read8(const uint8_t* from, int r, int c, float (&x)[8]) {
+  const f32x4 a = *reinterpret_cast<const f32x4*>(from + result_at(r, c));
+  const f32x4 b = *reinterpret_cast<const f32x4*>(from + result_at(r, c + 1));
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    x[k] = a[k];
+    x[4 + k] = b[k];
+  }
+}
+
+// The 64 rows laid out, from row m and column n of the results on.
+template <class H, int KIND>
+__device__ __forceinline__ void store_rows(const FfnArgs& p, const uint8_t* from, int32_t m, int32_t hi, int32_t n) {
+  constexpr int kPer = KIND == kFfnUp ? 4 : 8;  // 8-column groups per row
+  const int lane = threadIdx.x & 63, c = lane % kPer;
+  auto place = [&](int turn, int& r, int& count) {
+    r = turn * (64 / kPer) + lane / kPer;
+    count = m + r < hi ? min(p.N - n - 8 * c, 8) : 0;
+    return static_cast<int64_t>(m + r) * p.N + n + 8 * c;
+  };
+  int r, count;
+  int64_t at = place(0, r, count);
+  Kept kept = load_kept<KIND>(p, at, count);
+#pragma unroll 1
+  for (int turn = 0; turn < kPer; ++turn) {
+    int rn, cn;
+    const int64_t an = place(turn + 1, rn, cn);
+    const Kept next = load_kept<KIND>(p, an, turn + 1 < kPer ? cn : 0);
+    float x[8], v[8] = {};
+    read8(from, r, 2 * c, x);
+    if (KIND == kFfnUp) read8(from, r, 8 + 2 * c, v);
+    finish8<H, KIND>(p, at, count, x, v, kept);
+    r = rn;
+    count = cn;
+    at = an;
+    kept = next;
   }
 }
 
@@ -194,12 +212,9 @@ __global__ __launch_bounds__(kThreads, 2) void ffn_tile_kernel(FfnArgs p, int32_
   constexpr int kBC = kBBytes / 16 / kThreads;  // 16-byte chunks per thread and stage: 2 or 4
   constexpr int kBPer = kTrans ? kB2 / 16 : 4;  // chunks per row of B's stage
   typedef typename H::v8 v8;
-  // Stages in LDS: two, each copied while the other is computed.  The narrow tiles of small
-  // problems, whose matrix instructions take less time than a copy, have three, copied two
-  // ahead (two workgroups per compute unit), or five (where there is one at most).
-  constexpr bool kRing = DIRECT && NT == 2;
+  // two stages in LDS, each copied while the other is computed; then the waves' results
   constexpr int kStageBytes = kABytes + kBBytes;
-  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kStageBytes > kResultBytes ? 2 * kStageBytes : kResultBytes];
   uint8_t* const sa0 = lds;
   uint8_t* const sb0 = lds + kABytes;
   uint8_t* const sa1 = sa0 + kStageBytes;
@@ -389,37 +404,6 @@ __global__ __launch_bounds__(kThreads, 2) void ffn_tile_kernel(FfnArgs p, int32_
       const bool seg = kSeg == 2 && q >= kb;
       fetch(seg ? 1 : 0, (seg ? q - kb : q) * kB + second, sa, sb);
     };
-    if constexpr (kRing) {
-      const int32_t count = 2 * (q1 - q0);
-      auto ring = [&](int32_t s, int at) {
-        stage(q0 + (s >> 1), (s & 1) * kStep, lds + at * kStageBytes, lds + at * kStageBytes + kABytes);
-      };
-      const int32_t depth = p.stages;
-      for (int32_t s = 0; s < depth - 1 && s < count; ++s) ring(s, s);
-      int at = 0;
-      for (int32_t s = 0; s < count; ++s) {
-        const int32_t q = q0 + (s >> 1);
-        if (!(s & 1)) before(q);
-        constexpr int kCopies = 4 + kBC;  // of a stage
-        switch (min(depth - 2, count - 1 - s)) {  // stages that may still be on their way
-          case 0: wait_copies<0>(); break;
-          case 1: wait_copies<kCopies>(); break;
-          case 2: wait_copies<2 * kCopies>(); break;
-          default: wait_copies<3 * kCopies>(); break;
-        }
-        __syncthreads();
-        uint8_t* const sa = lds + at * kStageBytes;
-        const int32_t left = K - (kSeg == 2 && q >= kb ? q - kb : q) * kB - (s & 1) * kStep;
-        if (left < kStep) clear_past(left, sa, sa + kABytes);
-        compute(sa, sa + kABytes, d, j0_, nj_, [&] {
-          if (s + depth - 1 < count) ring(s + depth - 1, at == 0 ? depth - 1 : at - 1);
-        });
-        at = at == depth - 1 ? 0 : at + 1;
-        if (s & 1) after(q);
-      }
-      __syncthreads();  // the stages are written again by the next pass
-      return;
-    }
     stage(q0, 0, sa0, sb0);
     put(sa0, sb0);
     for (int32_t q = q0; q < q1; ++q) {
@@ -442,21 +426,40 @@ __global__ __launch_bounds__(kThreads, 2) void ffn_tile_kernel(FfnArgs p, int32_
     __syncthreads();  // the stages are written again by the next pass
   };
 
-  // a tile's results (for kFfnUp: gate columns x, up columns v), or a part's sums
-  auto emit = [&](const f32x16& x, const f32x16& v, const Kept& kept, int i, int j) {
+  // The accumulators as results, or as a part's sums.  Tile columns from j0 on are in d, two at a
+  // time (for kFfnUp one of gate and the one of up that belongs to it, NT / 2 further on).
+  uint8_t* const mine = lds + w * (kResultBytes / 4);
+  auto emit = [&](const auto& d, auto nj_) {
+    constexpr int nj = decltype(nj_)::value;  // tile columns in d, the first of them j0
     if (split) {
       f32x4* const to = part_at<NT>(p.part, item - plan.whole);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        to[((i * NT + j) * 4 + r) * kThreads + t] = f32x4{x[4 * r], x[4 * r + 1], x[4 * r + 2], x[4 * r + 3]};
-        if (kUp)
-          to[((i * NT + j + NT / 2) * 4 + r) * kThreads + t] = f32x4{v[4 * r], v[4 * r + 1], v[4 * r + 2], v[4 * r + 3]};
-      }
-    } else {
-      store_tile<H, KIND, NT>(p, x, v, kept, hi, m0, n0, i, j);
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < nj; ++j)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            to[((i * NT + j) * 4 + r) * kThreads + t] =
+                f32x4{d[i][j][4 * r], d[i][j][4 * r + 1], d[i][j][4 * r + 2], d[i][j][4 * r + 3]};
+      return;
+    }
+#pragma unroll 1
+    for (int turn = 0; turn < NT / 2; ++turn) {
+      auto lay = [&](auto first_) {
+        constexpr int first = decltype(first_)::value;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          lay_tile(d[i][first], mine, i, 0);
+          lay_tile(d[i][first + (kUp ? NT / 2 : 1)], mine, i, 1);
+        }
+      };
+      if (turn == 0)
+        lay(Int<0>{});
+      else
+        lay(Int<NT == 2 ? 0 : kUp ? 1 : 2>{});
+      store_rows<H, KIND>(p, mine, m0 + wm * 64, hi, n0 + wn * (NT / 2) * (kUp ? 32 : 64) + turn * (kUp ? 32 : 64));
     }
   };
-  auto keep = [&](int i, int j) { return split ? Kept{} : load_kept<KIND, NT>(p, hi, m0, n0, i, j); };
 
   // all waves decide alike: the barriers are shared
   float slo = 3e38f, shi = 0.0f;
@@ -505,45 +508,32 @@ __global__ __launch_bounds__(kThreads, 2) void ffn_tile_kernel(FfnArgs p, int32_
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[i][j][r] *= was[kUp && j >= NT / 2 ? 1 : 0];
-    constexpr int kJ = kUp ? NT / 2 : NT;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      Kept kept[kJ];
-#pragma unroll
-      for (int j = 0; j < kJ; ++j) kept[j] = keep(i, j);
-#pragma unroll
-      for (int j = 0; j < kJ; ++j) emit(acc[i][j], acc[i][kUp ? j + NT / 2 : j], kept[j], i, j);
-    }
+    emit(acc, Int<NT>{});
   } else {
+    // sums by blocks, one tile column at a time, in a pass each; the results wait in `sum`
+    f32x16 sum[2][NT];
     auto pass = [&](auto j_) {
       constexpr int j = decltype(j_)::value;
-      f32x16 sum[2][1], part[2][1], up[2][1];
+      f32x16 part[2][1];
 #pragma unroll
-      for (int k = 0; k < (kUp ? 2 : 1); ++k) {
-        auto& d = k ? up : sum;
-        d[0][0] = d[1][0] = zero;
-        auto add = [&](int32_t q) {
-          const float s = scale(q, k);
+      for (int i = 0; i < 2; ++i) sum[i][j] = zero;
+      sweep(
+          part, Int<j>{}, Int<1>{}, [&](int32_t) { part[0][0] = part[1][0] = zero; },
+          [&](int32_t q) {
+            const float s = scale(q, kUp && j >= NT / 2 ? 1 : 0);
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) d[i][0][r] = fmaf(s, part[i][0][r], d[i][0][r]);
-        };
-        auto clear = [&](int32_t) { part[0][0] = part[1][0] = zero; };
-        if (k)
-          sweep(part, Int<kUp ? j + NT / 2 : j>{}, Int<1>{}, clear, add);
-        else
-          sweep(part, Int<j>{}, Int<1>{}, clear, add);
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) emit(sum[i][0], up[i][0], keep(i, j), i, j);
+              for (int r = 0; r < 16; ++r) sum[i][j][r] = fmaf(s, part[i][0][r], sum[i][j][r]);
+          });
     };
     pass(Int<0>{});
-    if constexpr (!kUp || NT == 4) pass(Int<1>{});
-    if constexpr (!kUp && NT == 4) {
+    pass(Int<1>{});
+    if constexpr (NT == 4) {
       pass(Int<2>{});
       pass(Int<3>{});
     }
+    emit(sum, Int<NT>{});
   }
 }
 
@@ -560,20 +550,48 @@ __global__ __launch_bounds__(kThreads) void ffn_join_kernel(FfnArgs p, int32_t n
   if (tile >= rest) return;
   const int ij = static_cast<int>(blockIdx.x) % (2 * kJ), i = ij / kJ, j = ij % kJ, t = threadIdx.x;
   if (!find_tile<kRows>(p.offsets, p.T, p.E, ncols, rowtiles, first, plan.whole + tile, e, lo, hi, m0, col)) return;
-  const Kept kept = load_kept<KIND, NT>(p, hi, m0, col * kCols, i, j);
-  f32x16 v[2] = {};
+  const int lane = t & 63, w = t >> 6;
+  const int32_t m = m0 + (w >> 1) * 64 + i * 32 + (lane & 31);
+  const int32_t n = col * kCols + ((w & 1) * kJ + j) * 32 + (lane >> 5) * 8;
+  int count[2];
+  Kept kept[2];
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    count[g] = m < hi ? min(p.N - n - 16 * g, 8) : 0;
+    kept[g] = load_kept<KIND>(p, static_cast<int64_t>(m) * p.N + n + 16 * g, count[g]);
+  }
+  float x[16] = {}, v[16] = {};
+#pragma unroll 2
   for (int32_t s = 0; s < plan.splits; ++s) {
     const f32x4* from = part_at<NT>(p.part, s * rest + tile);
 #pragma unroll
-    for (int k = 0; k < (kUp ? 2 : 1); ++k)
+    for (int r = 0; r < 4; ++r) {
+      const f32x4 a = from[((i * NT + j) * 4 + r) * kThreads + t];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const f32x4 x = from[((i * NT + j + k * (NT / 2)) * 4 + r) * kThreads + t];
+      for (int c = 0; c < 4; ++c) x[4 * r + c] += a[c];
+      if (kUp) {
+        const f32x4 b = from[((i * NT + j + NT / 2) * 4 + r) * kThreads + t];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) v[k][4 * r + c] += x[c];
+        for (int c = 0; c < 4; ++c) v[4 * r + c] += b[c];
       }
+    }
   }
-  store_tile<H, KIND, NT>(p, v[0], v[1], kept, hi, m0, col * kCols, i, j);
+  // 8 columns in a row: the half waves exchange theirs
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    float xg[8], vg[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      exchange(x[8 * g + k], x[8 * g + 4 + k]);
+      if (kUp) exchange(v[8 * g + k], v[8 * g + 4 + k]);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      xg[k] = x[8 * g + k];
+      vg[k] = v[8 * g + k];
+    }
+    finish8<H, KIND>(p, static_cast<int64_t>(m) * p.N + n + 16 * g, count[g], xg, vg, kept[g]);
+  }
 }
 
 // The most row tiles that T rows in E runs can make: every run may end in a partial tile.
@@ -592,11 +610,10 @@ template <class H, int KIND, int NT>
 void launch_tiles(const FfnArgs& p, bool direct, int64_t tiles, int32_t ncols, hipStream_t s) {
   // a grid with room for the most parts: the rest of a round becomes at most a round of parts
   const dim3 g(static_cast<unsigned>(tiles + (p.part ? kSlots : 0))), b(kThreads);
-  const size_t lds = p.stages * (kABytes + NT * 64 * kStep);
   if (direct)
-    hipLaunchKernelGGL((ffn_tile_kernel<H, KIND, NT, true>), g, b, lds, s, p, ncols);
+    hipLaunchKernelGGL((ffn_tile_kernel<H, KIND, NT, true>), g, b, 0, s, p, ncols);
   else if constexpr (NT == 2)
-    hipLaunchKernelGGL((ffn_tile_kernel<H, KIND, 2, false>), g, b, lds, s, p, ncols);
+    hipLaunchKernelGGL((ffn_tile_kernel<H, KIND, 2, false>), g, b, 0, s, p, ncols);
   if (!p.part) return;
   const int64_t rest = tiles < kSlots ? tiles : kSlots - 1;
   const dim3 gj(static_cast<unsigned>(rest * 2 * (KIND == kFfnUp ? NT / 2 : NT)));
@@ -633,7 +650,6 @@ int launch(FfnArgs p, int32_t dtype, void* workspace, size_t workspace_bytes, hi
   const int64_t known = p.offsets ? tiles : static_cast<int64_t>((p.T + kRows - 1) / kRows) * ncols;
   if (split_pays(p, KIND == kFfnUpBwd ? 2 : 1, known) && workspace_bytes >= part_bytes(wide ? 4 : 2))
     p.part = static_cast<float*>(workspace);
-  p.stages = !direct || wide ? 2 : tiles + (p.part ? kSlots : 0) > 256 ? 3 : 5;
   if (dtype == FP8Z1_BF16 && wide)
     launch_tiles<Bf16, KIND, 4>(p, direct, tiles, ncols, s);
   else if (dtype == FP8Z1_BF16)

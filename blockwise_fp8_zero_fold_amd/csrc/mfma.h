@@ -150,13 +150,13 @@ __device__ __forceinline__ void copy16_to_lds(buffer_t b, uint32_t off, uint8_t*
                : "memory");
 }
 // 32 x 32 results with rows n and columns m: lane l holds, of column m = l % 32, rows
-// 8 q + 4 (l / 32) + 0..3 as its value group q = 0..3.  exchange(x, y) of what two
-// neighbouring groups 2g and 2g + 1 pack to leaves (x, y) of the lower lanes rows 16 g + 0..7 and of
-// the upper lanes rows 16 g + 8..15, in order; done again it undoes itself.
-__device__ __forceinline__ void exchange(uint32_t& x, uint32_t& y) {
-  const auto r = __builtin_amdgcn_permlane32_swap(x, y, false, false);
-  x = r[0];
-  y = r[1];
+// 8 q + 4 (l / 32) + 0..3 as its value group q = 0..3.  exchange(x, y) of the k-th values of two
+// neighbouring groups 2g and 2g + 1, k = 0..3, leaves the x then y of the lower lanes rows
+// 16 g + 0..7 and of the upper lanes rows 16 g + 8..15, in order.
+__device__ __forceinline__ void exchange(float& x, float& y) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(y), false, false);
+  x = __uint_as_float(r[0]);
+  y = __uint_as_float(r[1]);
 }
 
 // until at most LEFT of the copies (and other memory operations) last issued are on their way
