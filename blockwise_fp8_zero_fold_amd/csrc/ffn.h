@@ -72,23 +72,30 @@ struct Plan {
   __device__ int64_t items() const { return whole + static_cast<int64_t>(tiles - whole) * splits; }
 };
 
+// Rows and row tiles of an expert
+struct Run {
+  int32_t lo, hi, tiles;
+};
 template <int ROWS>
-__device__ __forceinline__ int32_t row_tiles(const int32_t* offsets, int32_t T, int32_t e) {
-  int32_t lo, hi;
-  expert_rows(offsets, T, e, lo, hi);
-  return (hi - lo + ROWS - 1) / ROWS;
+__device__ __forceinline__ Run run_of(const int32_t* offsets, int32_t T, int32_t E, int32_t e) {
+  Run r = {0, 0, 0};
+  if (e < E) {
+    expert_rows(offsets, T, e, r.lo, r.hi);
+    r.tiles = (r.hi - r.lo + ROWS - 1) / ROWS;
+  }
+  return r;
 }
 
+// `first`: the run of expert `lane`, for find_tile
 template <int ROWS>
-__device__ __forceinline__ Plan plan_tiles(const int32_t* offsets, int32_t T, int32_t E, int32_t ncols,
-                                           int32_t blocks, int32_t split_from, int32_t& rowtiles, int32_t& first) {
+__device__ __forceinline__ Plan plan_tiles(const int32_t* offsets, int32_t T, int32_t E, int32_t ncols, int32_t blocks,
+                                           int32_t split_from, int32_t& rowtiles, Run& first) {
   const int lane = threadIdx.x & 63;
-  int32_t total = 0;
-  first = 0;  // row tiles of expert `lane`
+  first = run_of<ROWS>(offsets, T, E, lane);
+  int32_t total;
   if (offsets) {
-    first = lane < E ? row_tiles<ROWS>(offsets, T, lane) : 0;
-    total = wave_isum(first);
-    for (int32_t e0 = 64; e0 < E; e0 += 64) total += wave_isum(e0 + lane < E ? row_tiles<ROWS>(offsets, T, e0 + lane) : 0);
+    total = wave_isum(first.tiles);
+    for (int32_t e0 = 64; e0 < E; e0 += 64) total += wave_isum(run_of<ROWS>(offsets, T, E, e0 + lane).tiles);
   } else {
     total = (T + ROWS - 1) / ROWS;
   }
@@ -120,7 +127,7 @@ __device__ __forceinline__ int32_t xcd_run(int32_t b, int32_t n) {
 constexpr int kGroup = 8;
 template <int ROWS>
 __device__ __forceinline__ bool find_tile(const int32_t* offsets, int32_t T, int32_t E, int32_t ncols, int32_t rowtiles,
-                                          int32_t first, int32_t id, int32_t& e, int32_t& lo, int32_t& hi, int32_t& m0,
+                                          const Run& first, int32_t id, int32_t& e, int32_t& lo, int32_t& hi, int32_t& m0,
                                           int32_t& col) {
   const int lane = threadIdx.x & 63;
   const int32_t grp = id / (kGroup * ncols), in = id - grp * kGroup * ncols;
@@ -128,10 +135,12 @@ __device__ __forceinline__ bool find_tile(const int32_t* offsets, int32_t T, int
   col = in / rows;
   int32_t mt = grp * kGroup + in - col * rows;
   e = 0;
+  lo = 0;
+  hi = T;
   if (offsets) {
     for (int32_t e0 = 0; e0 < E; e0 += 64) {
-      const int32_t n = e0 == 0 ? first : e0 + lane < E ? row_tiles<ROWS>(offsets, T, e0 + lane) : 0;
-      int32_t upto = n;  // tiles of this chunk's experts up to and with this lane's
+      const Run run = e0 == 0 ? first : run_of<ROWS>(offsets, T, E, e0 + lane);
+      int32_t upto = run.tiles;  // tiles of this chunk's experts up to and with this lane's
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) {
         const int32_t v = __shfl_up(upto, o);
@@ -141,7 +150,9 @@ __device__ __forceinline__ bool find_tile(const int32_t* offsets, int32_t T, int
       if (past) {
         const int at = __builtin_ctzll(past);
         e = e0 + at;
-        mt -= __shfl(upto - n, at);
+        mt -= __shfl(upto - run.tiles, at);
+        lo = __shfl(run.lo, at);
+        hi = __shfl(run.hi, at);
         break;
       }
       mt -= __shfl(upto, 63);
@@ -149,7 +160,6 @@ __device__ __forceinline__ bool find_tile(const int32_t* offsets, int32_t T, int
   }
   e = __builtin_amdgcn_readfirstlane(e);
   mt = __builtin_amdgcn_readfirstlane(mt);
-  expert_rows(offsets, T, e, lo, hi);
   lo = __builtin_amdgcn_readfirstlane(lo);
   hi = __builtin_amdgcn_readfirstlane(hi);
   m0 = lo + mt * ROWS;

@@ -221,7 +221,8 @@ __global__ __launch_bounds__(kThreads, 2) void ffn_tile_kernel(FfnArgs p, int32_
   uint8_t* const sb1 = sb0 + kStageBytes;
 
   const int32_t kb = (p.K + kB - 1) / kB, blocks = kSeg * kb;  // scale blocks of k, each two stages
-  int32_t rowtiles, first, e, lo, hi, m0, col;
+  int32_t rowtiles, e, lo, hi, m0, col;
+  Run first;
   const int32_t item = static_cast<int32_t>(blockIdx.x);
   const Plan plan = plan_tiles<kRows>(p.offsets, p.T, p.E, ncols, blocks, p.part ? p.split_from : 0, rowtiles, first);
   if (item >= plan.items()) return;
@@ -537,61 +538,49 @@ __global__ __launch_bounds__(kThreads, 2) void ffn_tile_kernel(FfnArgs p, int32_
   }
 }
 
-// The split tiles: their parts' sums added in order, one 32 x 32 tile of each wave per
-// workgroup, and the results as above.
+// The split tiles: their parts' sums added in order, and the results as above.  A workgroup takes
+// half of a 32 x 32 tile of each wave: 8 columns of 32 rows per half wave, after an exchange.
 template <class H, int KIND, int NT>
 __global__ __launch_bounds__(kThreads) void ffn_join_kernel(FfnArgs p, int32_t ncols) {
   constexpr bool kUp = KIND == kFfnUp;
   constexpr int kCols = (kUp ? 32 : 64) * NT, kJ = kUp ? NT / 2 : NT;
   const int32_t blocks = (KIND == kFfnUpBwd ? 2 : 1) * ((p.K + kB - 1) / kB);
-  int32_t rowtiles, first, e, lo, hi, m0, col;
+  int32_t rowtiles, e, lo, hi, m0, col;
+  Run first;
   const Plan plan = plan_tiles<kRows>(p.offsets, p.T, p.E, ncols, blocks, p.split_from, rowtiles, first);
-  const int32_t rest = plan.tiles - plan.whole, tile = static_cast<int32_t>(blockIdx.x) / (2 * kJ);
+  const int32_t rest = plan.tiles - plan.whole, tile = static_cast<int32_t>(blockIdx.x) / (4 * kJ);
   if (tile >= rest) return;
-  const int ij = static_cast<int>(blockIdx.x) % (2 * kJ), i = ij / kJ, j = ij % kJ, t = threadIdx.x;
-  if (!find_tile<kRows>(p.offsets, p.T, p.E, ncols, rowtiles, first, plan.whole + tile, e, lo, hi, m0, col)) return;
-  const int lane = t & 63, w = t >> 6;
-  const int32_t m = m0 + (w >> 1) * 64 + i * 32 + (lane & 31);
-  const int32_t n = col * kCols + ((w & 1) * kJ + j) * 32 + (lane >> 5) * 8;
-  int count[2];
-  Kept kept[2];
+  const int g = blockIdx.x & 1, i = (blockIdx.x >> 1) & 1, j = static_cast<int>(blockIdx.x >> 2) % kJ;
+  const int t = threadIdx.x, lane = t & 63, w = t >> 6;
+  const f32x4* const from = part_at<NT>(p.part, tile) + ((i * NT + j) * 4 + 2 * g) * kThreads + t;
+  const int64_t step = part_at<NT>(p.part, rest) - part_at<NT>(p.part, 0);
+  constexpr int kV = (NT / 2) * 4 * kThreads;  // from gate to up
+  float x[8] = {}, v[8] = {};
+#pragma unroll 4
+  for (int32_t s = 0; s < plan.splits; ++s)
 #pragma unroll
-  for (int g = 0; g < 2; ++g) {
-    count[g] = m < hi ? min(p.N - n - 16 * g, 8) : 0;
-    kept[g] = load_kept<KIND>(p, static_cast<int64_t>(m) * p.N + n + 16 * g, count[g]);
-  }
-  float x[16] = {}, v[16] = {};
-#pragma unroll 2
-  for (int32_t s = 0; s < plan.splits; ++s) {
-    const f32x4* from = part_at<NT>(p.part, s * rest + tile);
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const f32x4 a = from[((i * NT + j) * 4 + r) * kThreads + t];
+    for (int r = 0; r < 2; ++r) {
+      const f32x4 a = from[s * step + r * kThreads];
 #pragma unroll
       for (int c = 0; c < 4; ++c) x[4 * r + c] += a[c];
       if (kUp) {
-        const f32x4 b = from[((i * NT + j + NT / 2) * 4 + r) * kThreads + t];
+        const f32x4 b = from[s * step + r * kThreads + kV];
 #pragma unroll
         for (int c = 0; c < 4; ++c) v[4 * r + c] += b[c];
       }
     }
+  if (!find_tile<kRows>(p.offsets, p.T, p.E, ncols, rowtiles, first, plan.whole + tile, e, lo, hi, m0, col)) return;
+  const int32_t m = m0 + (w >> 1) * 64 + i * 32 + (lane & 31);
+  const int32_t n = col * kCols + ((w & 1) * kJ + j) * 32 + g * 16 + (lane >> 5) * 8;
+  const int count = m < hi ? min(p.N - n, 8) : 0;
+  const int64_t at = static_cast<int64_t>(m) * p.N + n;
+  const Kept kept = load_kept<KIND>(p, at, count);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    exchange(x[k], x[4 + k]);
+    if (kUp) exchange(v[k], v[4 + k]);
   }
-  // 8 columns in a row: the half waves exchange theirs
-#pragma unroll
-  for (int g = 0; g < 2; ++g) {
-    float xg[8], vg[8];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      exchange(x[8 * g + k], x[8 * g + 4 + k]);
-      if (kUp) exchange(v[8 * g + k], v[8 * g + 4 + k]);
-    }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      xg[k] = x[8 * g + k];
-      vg[k] = v[8 * g + k];
-    }
-    finish8<H, KIND>(p, static_cast<int64_t>(m) * p.N + n + 16 * g, count[g], xg, vg, kept[g]);
-  }
+  finish8<H, KIND>(p, at, count, x, v, kept);
 }
 
 // The most row tiles that T rows in E runs can make: every run may end in a partial tile.
@@ -616,7 +605,7 @@ void launch_tiles(const FfnArgs& p, bool direct, int64_t tiles, int32_t ncols, h
     hipLaunchKernelGGL((ffn_tile_kernel<H, KIND, 2, false>), g, b, 0, s, p, ncols);
   if (!p.part) return;
   const int64_t rest = tiles < kSlots ? tiles : kSlots - 1;
-  const dim3 gj(static_cast<unsigned>(rest * 2 * (KIND == kFfnUp ? NT / 2 : NT)));
+  const dim3 gj(static_cast<unsigned>(rest * 4 * (KIND == kFfnUp ? NT / 2 : NT)));
   hipLaunchKernelGGL((ffn_join_kernel<H, KIND, NT>), gj, b, 0, s, p, ncols);
 }
 
