@@ -416,3 +416,81 @@ def test_block_refuses_what_does_not_fit():
         block.ffn_weight_gradient(x, x, n_experts=2)
     with pytest.raises(E):
         block.ffn_weight_gradient(x, x, dtype=torch.float16)
+
+
+@pytest.mark.parametrize("dtype,value", [("f16", 2.0 ** -20), ("bf16", 2.0 ** -130)])
+@pytest.mark.parametrize("T", [3, 150])
+def test_subnormal_activations_count(T, dtype, value):
+    """Activations below the type's normal range: D equal ones times codes of 1 give D times the value."""
+    c = Case(T, 1, 256, 64, dtype, one_run=True)
+    c.x = torch.full_like(c.x, value)
+    c.gate = (torch.full_like(c.gate[0], 0x38), torch.ones_like(c.gate[1]))
+    h, _, _ = c.run_up()
+    assert torch.equal(h.cpu(), torch.full((T, c.F), 256 * value, dtype=c.dtype))
+    c.du, c.dh = torch.zeros_like(c.du), torch.full_like(c.dh, value)
+    dx = c.out(c.D)
+    fz.fp8z1_ffn_up_bwd(c.cfg, c.dev("dh"), c.dev("du"), *c.dev("gate"), *c.dev("up"), None, dx)
+    assert torch.equal(dx.cpu(), torch.full((T, c.D), 64 * value, dtype=c.dtype))
+    dw = torch.empty(1, c.F, c.D, device="cuda")
+    ones = torch.ones(T, c.D, dtype=c.dtype, device="cuda")
+    fz.fp8z1_ffn_wgrad(T, 1, c.F, c.D, c.cfg.dtype, c.dev("dh"), ones, None, fz.F32, dw)
+    assert torch.equal(dw.cpu(), torch.full((1, c.F, c.D), T * value))
+
+
+def test_no_rows():
+    c = Case(0, 2, 64, 32)
+    gate, up, down, off = c.dev("gate"), c.dev("up"), c.dev("down"), c.dev("offsets")
+    y, (h, u, a) = block.ffn_forward(c.dev("x"), gate, up, down, off, save=True)
+    assert y.shape == (0, 64) and h.shape == u.shape == a.shape == (0, 32)
+    out = block.ffn_backward_data(c.dev("dy"), h, u, gate, up, down, off)
+    assert [tuple(t.shape) for t in out] == [(0, 64), (0, 32), (0, 32), (0, 32)]
+
+
+@pytest.mark.parametrize("bad", [0.0, -2.0, float("nan"), float("inf"), 2.0 ** -140])
+def test_any_scale(bad):
+    """One block with a scale that is zero, negative, not finite or subnormal: it counts as it is."""
+    for T in (5, 140):
+        c = Case(T, 1, 384, 256, one_run=True)
+        c.gate[1][0, 0, 1] = bad
+        c.down[1][0, 1, 0] = bad
+        h, u, _ = c.run_up()
+        exact, mag = ref.grouped(c.x, ref.dequantize(*c.gate), None, False)
+        err = ref.sum_error(mag, c.D)
+        if bad == float("inf"):  # sums of infinities of both signs: no number
+            assert not torch.isfinite(h[:, :128]).any() and torch.isfinite(h[:, 128:]).all()
+        else:
+            ref.check(h, exact, ref.rounded(exact, err, c.dtype), f"h, scale {bad}")
+        dh, du, a = (c.out(c.F) for _ in range(3))
+        fz.fp8z1_ffn_down_bwd(c.cfg, c.dev("dy"), *c.dev("down"), c.dev("h"), c.dev("u"), None, dh, du, a)
+        if bad == bad and abs(bad) != float("inf"):
+            c.check_down_bwd((dh, du, a), f"scale {bad}")
+        else:
+            assert not torch.isfinite(du[:, :128]).any() and torch.isfinite(du[:, 128:]).all()
+
+
+def test_rows_past_four_gigabytes():
+    """Rows whose byte offsets need more than 32 bits, forward and backward."""
+    T, D, F = 310000, 7168, 24
+    g = torch.Generator().manual_seed(1)
+    gate, up, down = (tuple(t.cuda() for t in ref.make_weight(g, 2, *s)) for s in ((F, D), (F, D), (D, F)))
+    offsets = torch.tensor([0, 200, T], dtype=torch.int32, device="cuda")
+    x = torch.zeros(T, D, dtype=torch.bfloat16, device="cuda")
+    tail = torch.randn(150, D, generator=g).bfloat16()
+    x[-150:] = tail.cuda()
+    y, (h, u, a) = block.ffn_forward(x, gate, up, down, offsets, save=True)
+    w = [ref.dequantize(c.cpu()[1:], s.cpu()[1:]) for c, s in (gate, up, down)]
+    hd, mag = ref.grouped(tail, w[0], None, False)
+    ref.check(h[-150:], hd, ref.rounded(hd, ref.sum_error(mag, D), torch.bfloat16), "far h")
+    yd, mag = ref.grouped(a[-150:].cpu(), w[2], None, False)
+    ref.check(y[-150:], yd, ref.rounded(yd, ref.sum_error(mag, F), torch.bfloat16), "far y")
+    assert not y[:-150].any() and not h[:-150].any()
+    dx, dh, du, _ = block.ffn_backward_data(x, h, u, gate, up, down, offsets)
+    exact = [ref.grouped(d[-150:].cpu(), m, None, True) for d, m in ((dh, w[0]), (du, w[1]))]
+    total, mag = exact[0][0] + exact[1][0], exact[0][1] + exact[1][1]
+    ref.check(dx[-150:], total, ref.rounded(total, ref.sum_error(mag, 2 * F), torch.bfloat16), "far dx")
+    dw = block.ffn_weight_gradient(dh, x, 2, offsets)
+    want = dh[-150:].cpu().double().t() @ tail.double()
+    mag = dh[-150:].cpu().double().abs().t() @ tail.double().abs()
+    # (rows of zeros add nothing: the sum has 150 terms)
+    ref.check(dw[1], want, ref.rounded(want, ref.sum_error(mag, 150), torch.float32), "far dw")
+    assert not dw[0].any()

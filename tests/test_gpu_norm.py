@@ -323,3 +323,21 @@ def test_refusals():
     wide_rows = torch.zeros(1, 16385, device="cuda")
     with pytest.raises(E):
         block.norm_join(None, wide_rows)
+
+
+def test_rows_past_four_gigabytes():
+    T, C = 310000, 7168
+    d = make(60, C, BF, BF, "channel")
+    g = dev(d)
+    y, res = torch.zeros(T, C, dtype=BF, device="cuda"), torch.zeros(T, C, dtype=BF, device="cuda")
+    y[-60:], res[-60:] = g["y"], g["res"]
+    z, n = block.norm_join(y, res, g["w_post"], g["gate"], g["w_pre"], **OPT)
+    check_forward(d, z[-60:], n[-60:], "far rows")
+    assert not z[:-60].any() and not n[:-60].any()
+    del z, n
+    zero = torch.zeros_like(y)
+    dn, dz = zero.clone(), zero.clone()
+    dn[-60:], dz[-60:] = g["dn"], g["dz"]
+    got = block.norm_join_backward(dz, dn, y, res, g["w_post"], g["gate"], g["w_pre"], **OPT)
+    assert not got["dres"][:-60].any() and not got["dy"][:-60].any()
+    check_backward(d, d["res"], {k: v[-60:] if v.shape[0] == T else v for k, v in got.items()}, "far rows")
