@@ -5,6 +5,10 @@
 // each of its weight rows' 128 bytes straight into registers, 32 bytes per lane, widens
 // them and multiplies by 16 TT rows of x on the matrix cores; the next block's bytes are
 // on their way meanwhile.  The waves' sums are added in order through LDS.
+//
+// 128 tokens on 32 experts of widths 7168 and 2048: up 158 us (6.0 TB/s), down 97 us (4.9 TB/s; 2048 is 4
+// blocks for each wave, little to have on its way); with 1, 2 or 8 waves a workgroup up takes
+// 183, 175 or 188 us.  One token on one expert: 8.9 and 5.3 us, the latency of a few reads.
 #pragma once
 
 #include "ffn.h"

@@ -6,6 +6,11 @@
 // 2 x NT matrix tiles of 32 x 32.  Both operands run along the columns while the sum
 // runs down the rows, so a stage of 32 tokens is kept in LDS as it lies in memory and
 // the matrix operands are gathered by the transposing LDS reads.
+//
+// 8192 tokens of 8 experts, widths 7168 and 2048, float32 gradients: 390 us for one gradient, 1.15 ms
+// for the three (600 to 650 TFLOP/s).  A gradient's 470 MB of output take 100 us by themselves (4.6
+// TB/s), which 32 stages of a tile do not hide; with four times the tokens it runs at 810 TFLOP/s, 940
+// for the tokens added.  2-byte results and gradients of one small tile are bound by latency.
 #include <hip/hip_runtime.h>
 
 #include <initializer_list>

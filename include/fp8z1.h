@@ -323,7 +323,8 @@ int fp8z1_dequantize(const uint8_t* codes, const float* scales, int64_t E, int64
  * their element (16-byte aligned rows run faster), codes at any alignment.
  * Products are summed in float32 on the matrix cores: codes are widened exactly and
  * each block's scale multiplies the float32 partial sum of its 128 products, so
- * the only roundings to 16 bits are those of the tensors that a call writes.
+ * the only roundings to 16 bits are those of the tensors that a call writes.  (The float32
+ * sums hold x * code before the scale: keep the activations' magnitude below 2^56.)
  * Outputs must not overlap inputs.  T may be 0 (pointers to rows may then be NULL).
  * No call allocates or waits; all of them may be captured into a HIP graph. */
 
