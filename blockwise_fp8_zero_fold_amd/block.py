@@ -39,7 +39,7 @@ def _fail(msg: str):
 def _device(x: torch.Tensor, what: str) -> int:
     """The current device's index; the library launches there, on torch's current stream."""
     dev = x.get_device()
-    if dev < 0 or dev != torch.cuda.current_device():
+    if dev < 0 or dev != torch._C._cuda_getDevice():
         _fail(f"{what}: tensors must be on the current device, not {x.device}")
     return dev
 

@@ -132,7 +132,8 @@ __device__ __forceinline__ uint4 ld16_part(const uint8_t* p, int n, int before) 
 // same for the wave, so the only vector register that an address takes is the offset.
 // Written as assembly so that the compiler does not make every later LDS read wait for the
 // copy (it cannot tell that a read is of another stage); it has no register output.
-// The caller waits with wait_copies() before the barrier that hands the stage over.
+// The caller waits with wait_copies() before the barrier that hands the stage over.  (m0, the copy's
+// LDS address, is not a register that the compiler keeps values in, and nothing else here uses it.)
 typedef int buffer_t __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ buffer_t make_buffer(const uint8_t* base, int64_t size) {
   const uint64_t at = reinterpret_cast<uint64_t>(base);

@@ -25,7 +25,8 @@ struct NormArgs {
   // backward
   const void *dz, *dn;
   void *dy, *dres, *dgate;
-  float* part;  // [3][gridDim.x][C]: dw_post, dw_pre, dgate
+  float* part;       // [3][gridDim.x][C]: dw_post, dw_pre, dgate; or NULL with one workgroup:
+  float* direct[3];  // the gradients themselves
   int32_t T, C, gate_kind, want_post, want_pre, want_gate;
   int32_t waves;  // per row (backward)
   float eps, res_scale, block_scale, offset;
@@ -462,7 +463,8 @@ __global__ __launch_bounds__(1024) void norm_join_bwd_kernel(NormArgs a) {
     for (int ch = 0; ch < CH; ++ch) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[ch][i] *= scale;
-      store8<F32>(a.part + which * set + blockIdx.x * static_cast<int64_t>(a.C), a.C, col(ch), v[ch]);
+      store8<F32>(a.part ? a.part + which * set + blockIdx.x * static_cast<int64_t>(a.C) : a.direct[which], a.C, col(ch),
+                  v[ch]);
     }
   };
   if (a.want_post) finish(spost, 0, 1.0f);
@@ -515,7 +517,9 @@ int64_t fwd_groups(int64_t T, int64_t C) {
 }
 
 // Backward: up to 16 waves per workgroup (a compute unit holds 16 of them, by their registers),
-// for several short rows at a time, since every workgroup also writes its column sums.
+// for several short rows at a time, since every workgroup also writes its column sums.  Rows for
+// at most four turns of one workgroup go to one, which writes the gradients itself (a turn
+// takes about 2 us, the second launch and its kernel 7).
 struct Groups {
   int64_t rows, count;  // rows at a time per workgroup, workgroups
 };
@@ -524,6 +528,8 @@ Groups bwd_groups(int64_t T, int64_t C) {
   int64_t rows = C <= 8192 ? 16 / waves : 1;
   if (rows > (T + 255) / 256) rows = (T + 255) / 256;
   if (rows < 1) rows = 1;
+  const int64_t all = C <= 8192 ? 16 / waves : 1;
+  if (T <= 4 * all) return {T < all ? T : all, 1};
   const int64_t most = 256 * (16 / (waves * rows)), want = (T + rows - 1) / rows;
   return {rows, want < most ? want : most};
 }
@@ -679,7 +685,10 @@ extern "C" int fp8z1_norm_join_bwd(const fp8z1_norm* f, const void* dz, const vo
     a.dy = dy;
     a.dres = dres;
     a.dgate = dgate;
-    a.part = static_cast<float*>(workspace);
+    a.part = groups.count > 1 ? static_cast<float*>(workspace) : nullptr;
+    a.direct[0] = dw_post;
+    a.direct[1] = dw_pre;
+    a.direct[2] = gate_cols;
     a.want_post = dw_post != nullptr;
     a.want_pre = dw_pre != nullptr;
     a.want_gate = gate_cols != nullptr;
@@ -688,9 +697,9 @@ extern "C" int fp8z1_norm_join_bwd(const fp8z1_norm* f, const void* dz, const vo
     rc = check_hip(hipGetLastError(), "norm_join_bwd: launch");
     if (rc) return rc;
   }
-  if (sums) {
+  if (sums && (f->T == 0 || groups.count > 1)) {
     hipLaunchKernelGGL(norm_columns_kernel, dim3(static_cast<unsigned>((f->C + 63) / 64), 3), dim3(1024), 0, s,
-                       static_cast<const float*>(workspace), static_cast<int32_t>(groups.count), static_cast<int32_t>(f->C),
+                       static_cast<const float*>(workspace), static_cast<int32_t>(f->T ? groups.count : 0), static_cast<int32_t>(f->C),
                        dw_post, dw_pre, gate_cols);
     rc = check_hip(hipGetLastError(), "norm_join_bwd: sums launch");
   }
