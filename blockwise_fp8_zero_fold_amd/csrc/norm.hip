@@ -473,8 +473,8 @@ __global__ __launch_bounds__(1024) void norm_join_bwd_kernel(NormArgs a) {
 }
 
 // Column sums of the workgroups' partial sums (blockIdx.y: which gradient), in a fixed
-// order: wave w of 16 takes rows w, w + 16, ... (four at a time, so that several loads are on
-// their way), then the waves' sums are added in order.
+// order: wave w of 16 takes rows w, w + 16, ... (16 at a time, all of a usual call's 256, so
+// that their loads are on their way together), then the waves' sums are added in order.
 __global__ __launch_bounds__(1024) void norm_columns_kernel(const float* __restrict__ part, int32_t groups, int32_t C,
                                                             float* o0, float* o1, float* o2) {
   __shared__ float lds[16][64];
@@ -485,10 +485,13 @@ __global__ __launch_bounds__(1024) void norm_columns_kernel(const float* __restr
   const float* p = part + static_cast<int64_t>(blockIdx.y) * groups * C;
   float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   if (c < C)
-    for (int32_t g = w; g < groups; g += 64)
+    for (int32_t g = w; g < groups; g += 256) {
+      float x[16];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (g + 16 * i < groups) v[i] += p[static_cast<int64_t>(g + 16 * i) * C + c];
+      for (int i = 0; i < 16; ++i) x[i] = p[static_cast<int64_t>(min(g + 16 * i, groups - 1)) * C + c];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i & 3] += g + 16 * i < groups ? x[i] : 0.0f;
+    }
   lds[w][lane] = (v[0] + v[1]) + (v[2] + v[3]);
   __syncthreads();
   if (w == 0 && c < C) {
@@ -518,18 +521,17 @@ int64_t fwd_groups(int64_t T, int64_t C) {
 
 // Backward: up to 16 waves per workgroup (a compute unit holds 16 of them, by their registers),
 // for several short rows at a time, since every workgroup also writes its column sums.  Rows for
-// at most four turns of one workgroup go to one, which writes the gradients itself (a turn
-// takes about 2 us, the second launch and its kernel 7).
+// one turn of one workgroup go to one, which writes the gradients itself: no second launch (3 us
+// on the host).  Not for more: a turn takes 4.3 us, the second launch and its kernel 4 (captured,
+// 2 rows of 7168: one workgroup 13.2 us, two and the second launch 11.5; 32 rows of 1024: 20.9 and 8.2).
 struct Groups {
   int64_t rows, count;  // rows at a time per workgroup, workgroups
 };
 Groups bwd_groups(int64_t T, int64_t C) {
-  const int64_t waves = threads_for(C) / 64;
-  int64_t rows = C <= 8192 ? 16 / waves : 1;
-  if (rows > (T + 255) / 256) rows = (T + 255) / 256;
-  if (rows < 1) rows = 1;
-  const int64_t all = C <= 8192 ? 16 / waves : 1;
-  if (T <= 4 * all) return {T < all ? T : all, 1};
+  const int64_t waves = threads_for(C) / 64, all = C <= 8192 ? 16 / waves : 1;
+  if (T <= all) return {T, 1};
+  int64_t rows = (T + 255) / 256;
+  if (rows > all) rows = all;
   const int64_t most = 256 * (16 / (waves * rows)), want = (T + rows - 1) / rows;
   return {rows, want < most ? want : most};
 }
