@@ -256,10 +256,7 @@ def norm_join_backward(dz: Optional[torch.Tensor], dn: Optional[torch.Tensor], y
     py = None if y is None else _check(y, dev, rows, (T, C), f"{what} y")
     pz = _check(z, dev, z.dtype, (T, C), f"{what} z")
     dy, dres = None if y is None else y.new_empty((T, C)), z.new_empty((T, C))
-    # the gradients summed over rows share one buffer
-    cols = z.new_empty((3, C), dtype=torch.float32).unbind(0)
-    dgate = None if gate is None else cols[2] if gate.dim() == 1 else gate.new_empty(gate.shape)
-    dw_post, dw_pre = None if w_post is None else cols[0], None if w_pre is None else cols[1]
+    dw_post, dgate, dw_pre = (None if v is None else v.new_empty(v.shape) for v in (w_post, gate, w_pre))
     n = _norm_workspace(T, C)
     ws = _scratch(z, n)
     L._check(L.lib.fp8z1_norm_join_bwd(f, pdz, pdn, py, pz, wpost, pg, wpre, L._ptr(dy), dres.data_ptr(),
