@@ -445,13 +445,15 @@ __global__ __launch_bounds__(kThreads, 2) void ffn_tile_kernel(FfnArgs p, int32_
     if (split) {
       f32x4* const to = part_at<NT>(p.part, item - plan.whole);
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < 2; ++i) {
+        if (m0 + wm * 64 + i * 32 >= hi) break;  // (rows past the run are not joined either)
 #pragma unroll
         for (int j = 0; j < nj; ++j)
 #pragma unroll
           for (int r = 0; r < 4; ++r)
             to[((i * NT + j) * 4 + r) * kThreads + t] =
                 f32x4{d[i][j][4 * r], d[i][j][4 * r + 1], d[i][j][4 * r + 2], d[i][j][4 * r + 3]};
+      }
       return;
     }
 #pragma unroll 1
@@ -562,6 +564,9 @@ __global__ __launch_bounds__(kThreads) void ffn_join_kernel(FfnArgs p, int32_t n
   if (tile >= rest) return;
   const int g = blockIdx.x & 1, i = (blockIdx.x >> 1) & 1, j = static_cast<int>(blockIdx.x >> 2) % kJ;
   const int t = threadIdx.x, lane = t & 63, w = t >> 6;
+  if (!find_tile<kRows>(p.offsets, p.T, p.E, ncols, rowtiles, first, plan.whole + tile, e, lo, hi, m0, col)) return;
+  const int32_t mw = m0 + (w >> 1) * 64 + i * 32;
+  if (mw >= hi) return;  // (the parts of rows past the run were not written)
   const f32x4* const from = part_at<NT>(p.part, tile) + ((i * NT + j) * 4 + 2 * g) * kThreads + t;
   const int64_t step = part_at<NT>(p.part, rest) - part_at<NT>(p.part, 0);
   constexpr int kV = (NT / 2) * 4 * kThreads;  // from gate to up
@@ -579,8 +584,7 @@ __global__ __launch_bounds__(kThreads) void ffn_join_kernel(FfnArgs p, int32_t n
         for (int c = 0; c < 4; ++c) v[4 * r + c] += b[c];
       }
     }
-  if (!find_tile<kRows>(p.offsets, p.T, p.E, ncols, rowtiles, first, plan.whole + tile, e, lo, hi, m0, col)) return;
-  const int32_t m = m0 + (w >> 1) * 64 + i * 32 + (lane & 31);
+  const int32_t m = mw + (lane & 31);
   const int32_t n = col * kCols + ((w & 1) * kJ + j) * 32 + g * 16 + (lane >> 5) * 8;
   const int count = m < hi ? min(p.N - n, 8) : 0;
   const int64_t at = static_cast<int64_t>(m) * p.N + n;
