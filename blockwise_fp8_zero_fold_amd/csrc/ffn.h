@@ -55,14 +55,24 @@ __device__ __forceinline__ int32_t wave_isum(int32_t v) {
 // (some 5 us) adds them in order and finishes the tiles.  A part is at least 8 scale
 // blocks of k behind full rounds, and 2 where there is no full round; sums of less than
 // split_from blocks are not split: 8 with direct copies (a block takes about 1 us), 4
-// through registers (twice that).
+// through registers (twice that).  A part also writes and reads 64 KB, so that s parts of each
+// of n tiles cost about blocks / s + n s / 80 us: with direct copies no more than the s where
+// that is least, sqrt(80 blocks / n).  (512 tokens, 1024 x 4096, forward: 48 us without this
+// bound, 36 with it; 1024 tokens on 8 experts, 2048 x 1024: 52 and 48; 1024 tokens, 7168 x 2048:
+// 129 and 126; through registers, where a block takes longer, it cost up to 9 %.)
 constexpr int32_t kSlots = 512;
+constexpr int32_t kDirectFrom = 8, kRegisterFrom = 4;  // split_from
 
 __host__ __device__ __forceinline__ int32_t tile_splits(int64_t tiles, int32_t blocks, int32_t from) {
   const int32_t rest = static_cast<int32_t>(tiles % kSlots);
   if (!rest || !from || blocks < from) return 1;
-  const int32_t s = kSlots / rest, most = blocks / (tiles < kSlots ? 2 : 8);
-  return s < most ? s : most;
+  int32_t s = kSlots / rest, most = blocks / (tiles < kSlots ? 2 : 8);
+  if (tiles < kSlots && from == kDirectFrom) {
+    const int32_t least = static_cast<int32_t>(sqrtf(80.0f * static_cast<float>(blocks) / static_cast<float>(rest)));
+    most = least < most ? least : most;
+  }
+  if (s > most) s = most;
+  return s > 1 ? s : 1;
 }
 
 struct Plan {

@@ -650,7 +650,7 @@ int launch(FfnArgs p, int32_t dtype, void* workspace, size_t workspace_bytes, hi
   const int32_t cols = per * (wide ? 4 : 2), ncols = (p.N + cols - 1) / cols;
   const int64_t tiles = rows * ncols;
   if (tiles > 0x7fffffff - kSlots) return set_error(FP8Z1_ESHAPE, std::string(what) + ": too many tiles");
-  p.split_from = direct ? 8 : 4;
+  p.split_from = direct ? kDirectFrom : kRegisterFrom;
   const int64_t known = p.offsets ? tiles : static_cast<int64_t>((p.T + kRows - 1) / kRows) * ncols;
   if (split_pays(p, KIND == kFfnUpBwd ? 2 : 1, known) && workspace_bytes >= part_bytes(wide ? 4 : 2))
     p.part = static_cast<float*>(workspace);
