@@ -630,10 +630,17 @@ int launch(FfnArgs p, int32_t dtype, void* workspace, size_t workspace_bytes, hi
   if (p.T == 0) return FP8Z1_OK;
   if (misaligned(workspace, 16)) return set_error(FP8Z1_EINVAL, std::string(what) + ": misaligned workspace");
   constexpr bool kTrans = KIND == kFfnDownBwd || KIND == kFfnUpBwd;
+  const bool direct = !misaligned(p.x0, 4) && !misaligned(p.x1, 4) && !misaligned(p.w0, 4) && !misaligned(p.w1, 4) &&
+                      (kTrans ? p.K % 2 == 0 && p.N % 4 == 0 : p.K % 4 == 0);
   // Few rows per expert (32 on average at most): the weights' read is what counts, and a tile of 128
-  // rows would be mostly empty (128 tokens on 32 experts: 425 us by tiles, 250 by rows)
-  if constexpr (!kTrans)
-    if (static_cast<int64_t>(p.T) <= 32ll * p.E) {
+  // rows would be mostly empty (128 tokens on 32 experts: 425 us by tiles, 250 by rows).  Above 12
+  // rows the row kernel reads them slower, at 2.2 TB/s for 32 rows where tiles with direct
+  // copies reach 3.5 after some 7 us more of latency: tiles from about 10^9 bytes x rows above 12.
+  // (7168 x 2048, forward, rows and tiles: 1024 tokens on 32 experts 654 and 405 us, 256 on 8 169 and
+  // 134, 128 on 8 122 and 138, 32 on 1 33 and 37.)
+  if constexpr (!kTrans) {
+    const double weights = static_cast<double>(KIND == kFfnUp ? 2 : 1) * p.E * p.N * p.K;
+    if (static_cast<int64_t>(p.T) <= 32ll * p.E && (!direct || weights * (p.T - 12.0 * p.E) <= 1e9 * p.E)) {
       const bool aligned = !misaligned(p.x0, 16) && !misaligned(p.w0, 16) && !misaligned(p.w1, 16) && p.K % 16 == 0;
       if (dtype == FP8Z1_BF16)
         launch_rows<Bf16, KIND>(p, aligned, s);
@@ -641,8 +648,7 @@ int launch(FfnArgs p, int32_t dtype, void* workspace, size_t workspace_bytes, hi
         launch_rows<F16, KIND>(p, aligned, s);
       return check_hip(hipGetLastError(), what);
     }
-  const bool direct = !misaligned(p.x0, 4) && !misaligned(p.x1, 4) && !misaligned(p.w0, 4) && !misaligned(p.w1, 4) &&
-                      (kTrans ? p.K % 2 == 0 && p.N % 4 == 0 : p.K % 4 == 0);
+  }
   const int64_t rows = most_row_tiles(p.T, p.E);
   const int32_t per = KIND == kFfnUp ? 32 : 64;  // columns per NT
   // 256 columns a tile where they fill the card; what goes through registers takes too many for it

@@ -494,3 +494,37 @@ def test_rows_past_four_gigabytes():
     # (rows of zeros add nothing: the sum has 150 terms)
     ref.check(dw[1], want, ref.rounded(want, ref.sum_error(mag, 150), torch.float32), "far dw")
     assert not dw[0].any()
+
+
+@pytest.mark.parametrize("T,E,D,F", [(40, 1, 2176, 132), (33, 1, 260, 2304), (70, 2, 2176, 132), (129, 1, 2176, 132)])
+def test_split_tiles_of_few_rows(T, E, D, F):
+    """What the workspace held before is not read: rows past a run have no partial sums."""
+    c = Case(T, E, D, F)
+    what = f"{T} rows, {E} experts, {D} x {F}"
+    print("#", what, flush=True)
+    off = c.dev("offsets")
+
+    def ws():
+        return torch.full((fz.fp8z1_ffn_workspace_bytes(c.cfg),), 0xFF, dtype=torch.uint8, device="cuda")  # NaN
+
+    h, u, a, dh, du, a2 = (c.out(F) for _ in range(6))
+    y, dx = c.out(D), c.out(D)
+    fz.fp8z1_ffn_up(c.cfg, c.dev("x"), *c.dev("gate"), *c.dev("up"), off, h, u, a, workspace=ws())
+    c.check_up((h, u, a), what)
+    fz.fp8z1_ffn_down(c.cfg, c.dev("a"), *c.dev("down"), off, y, workspace=ws())
+    c.check_down(y, what)
+    fz.fp8z1_ffn_down_bwd(c.cfg, c.dev("dy"), *c.dev("down"), c.dev("h"), c.dev("u"), off, dh, du, a2, workspace=ws())
+    c.check_down_bwd((dh, du, a2), what)
+    fz.fp8z1_ffn_up_bwd(c.cfg, c.dev("dh"), c.dev("du"), *c.dev("gate"), *c.dev("up"), off, dx, workspace=ws())
+    c.check_up_bwd(dx, what)
+
+
+@pytest.mark.parametrize("T", [31, 32])
+def test_few_rows_of_large_weights(T):
+    """Either side of where the projections' 52 million codes go from the row kernel to tiles."""
+    c = Case(T, 1, 5120, 5120)
+    print("#", T, "rows", flush=True)
+    ws = torch.full((fz.fp8z1_ffn_workspace_bytes(c.cfg),), 0xFF, dtype=torch.uint8, device="cuda")
+    h, u, a = (c.out(c.F) for _ in range(3))
+    fz.fp8z1_ffn_up(c.cfg, c.dev("x"), *c.dev("gate"), *c.dev("up"), c.dev("offsets"), h, u, a, workspace=ws)
+    c.check_up((h, u, a), f"{T} rows")
