@@ -51,7 +51,7 @@ __device__ __forceinline__ int swizzle(int r) { return (r & 3) << 2; }
 // DIRECT: rows are 4-byte aligned, so a stage goes from memory to LDS by direct copies;
 // otherwise through registers, with the bytes outside a row left out.
 template <class H, bool F32OUT, int NT, bool DIRECT>
-__global__ __launch_bounds__(kThreads, 2) void ffn_wgrad_kernel(WgradArgs all) {
+__global__ __launch_bounds__(kThreads, NT == 2 ? 3 : 2) void ffn_wgrad_kernel(WgradArgs all) {
   typedef typename H::v8 v8;
   constexpr int kCols = NT * 64, kQBytes = kCols * kStep * 2, kStage = kPBytes + kQBytes;
   constexpr int kPC = kPBytes / 16 / kThreads, kQC = kQBytes / 16 / kThreads;  // chunks per thread
@@ -248,12 +248,24 @@ int64_t tiles_of(int64_t E, int64_t M, int64_t N, int64_t cols) {
 }
 
 // Splits of the tokens: where the outputs have fewer tiles (of 128 columns) than the card runs at
-// once, the tokens are cut so that about that many run, each with at least 8 stages of
-// an even share.
+// once (three workgroups on each of 256 compute units), the tokens are cut so that more run, each
+// with at least 8 stages of an even share.  A part writes and reads 64 KB, about 1/12 of a stage's
+// time for each tile, so s parts of each of n tiles are least dear at s = sqrt(12 stages / n); no
+// more are made, and up to a quarter less where that leaves the compute units more evenly filled.
+// (Three weight gradients, against two workgroups a unit and no such bound: 8192 tokens, 1024 x 1024
+// 106 -> 85 us; 1024 tokens, 1024 x 1024 34 -> 26; 65,536 tokens, 512 x 512 179 -> 165.)
+constexpr int64_t kUnits = 256, kParts = 3 * kUnits;
 int32_t wgrad_splits(int64_t T, int64_t E, int64_t tiles) {
-  const int64_t want = kSlots / (tiles < 1 ? 1 : tiles), most = T / E / (8 * kStep);
-  const int64_t s = want < most ? want : most;
-  return static_cast<int32_t>(s < 1 ? 1 : s);
+  if (tiles < 1) tiles = 1;
+  const int64_t stages = T / E / kStep;
+  int64_t s = kParts / tiles;
+  if (s > stages / 8) s = stages / 8;
+  while (s > 1 && s * s * tiles > 12 * stages) --s;
+  auto filled = [&](int64_t n) { return n * tiles * 100 / ((n * tiles + kUnits - 1) / kUnits * kUnits); };  // %
+  int64_t best = s;
+  for (int64_t n = s - 1; n >= 1 && 4 * n >= 3 * s; --n)
+    if (filled(n) > filled(best)) best = n;
+  return static_cast<int32_t>(best < 1 ? 1 : best);
 }
 
 struct Shape {
