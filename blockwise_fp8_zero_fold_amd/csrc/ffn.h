@@ -41,9 +41,15 @@ __device__ __forceinline__ void expert_rows(const int32_t* offsets, int32_t T, i
   }
 }
 
-__device__ __forceinline__ int32_t wave_isum(int32_t v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+// Sums over this lane and those before it, by lane moves within rows of 16 and from a row's last
+// lane on (through LDS, as shuffles go, the sum's six steps take 0.3 us of a launch)
+__device__ __forceinline__ int32_t wave_upto(int32_t v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);  // 1, 2, 4, 8 lanes up the row
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // lane 15 of rows 0 and 2 to the next row
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // lane 31 to rows 2 and 3
   return v;
 }
 
@@ -82,17 +88,18 @@ struct Plan {
   __device__ int64_t items() const { return whole + static_cast<int64_t>(tiles - whole) * splits; }
 };
 
-// Rows and row tiles of an expert
+// Rows and row tiles of an expert, and the tiles of the 64 that lanes hold up to and with its own
 struct Run {
-  int32_t lo, hi, tiles;
+  int32_t lo, hi, tiles, upto;
 };
 template <int ROWS>
 __device__ __forceinline__ Run run_of(const int32_t* offsets, int32_t T, int32_t E, int32_t e) {
-  Run r = {0, 0, 0};
+  Run r = {0, 0, 0, 0};
   if (e < E) {
     expert_rows(offsets, T, e, r.lo, r.hi);
     r.tiles = (r.hi - r.lo + ROWS - 1) / ROWS;
   }
+  r.upto = wave_upto(r.tiles);
   return r;
 }
 
@@ -104,8 +111,9 @@ __device__ __forceinline__ Plan plan_tiles(const int32_t* offsets, int32_t T, in
   first = run_of<ROWS>(offsets, T, E, lane);
   int32_t total;
   if (offsets) {
-    total = wave_isum(first.tiles);
-    for (int32_t e0 = 64; e0 < E; e0 += 64) total += wave_isum(run_of<ROWS>(offsets, T, E, e0 + lane).tiles);
+    total = __builtin_amdgcn_readlane(first.upto, 63);
+    for (int32_t e0 = 64; e0 < E; e0 += 64)
+      total += __builtin_amdgcn_readlane(run_of<ROWS>(offsets, T, E, e0 + lane).upto, 63);
   } else {
     total = (T + ROWS - 1) / ROWS;
   }
@@ -150,22 +158,17 @@ __device__ __forceinline__ bool find_tile(const int32_t* offsets, int32_t T, int
   if (offsets) {
     for (int32_t e0 = 0; e0 < E; e0 += 64) {
       const Run run = e0 == 0 ? first : run_of<ROWS>(offsets, T, E, e0 + lane);
-      int32_t upto = run.tiles;  // tiles of this chunk's experts up to and with this lane's
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const int32_t v = __shfl_up(upto, o);
-        if (lane >= o) upto += v;
-      }
+      const int32_t upto = run.upto;
       const uint64_t past = __ballot(upto > mt);
       if (past) {
         const int at = __builtin_ctzll(past);
         e = e0 + at;
-        mt -= __shfl(upto - run.tiles, at);
-        lo = __shfl(run.lo, at);
-        hi = __shfl(run.hi, at);
+        mt -= __builtin_amdgcn_readlane(upto - run.tiles, at);
+        lo = __builtin_amdgcn_readlane(run.lo, at);
+        hi = __builtin_amdgcn_readlane(run.hi, at);
         break;
       }
-      mt -= __shfl(upto, 63);
+      mt -= __builtin_amdgcn_readlane(upto, 63);
     }
   }
   e = __builtin_amdgcn_readfirstlane(e);
