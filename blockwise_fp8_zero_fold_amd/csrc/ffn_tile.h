@@ -409,13 +409,18 @@ __global__ __launch_bounds__(kThreads, 2) void ffn_tile_kernel(FfnArgs p, int32_
     return ((scalar_t)(second ? sp1 : sp0))[static_cast<int64_t>(kSeg == 2 && second ? q - kb : q) * sstride];
   };
 
+  auto stage = [&](int32_t q, int32_t second, uint8_t* sa, uint8_t* sb) {
+    const bool seg = kSeg == 2 && q >= kb;
+    fetch(seg ? 1 : 0, (seg ? q - kb : q) * kB + second, sa, sb);
+  };
+  // The first stage is on its way while the scales are looked at
+  stage(q0, 0, sa0, sb0);
+  bool first_pass = true;
+
   // One pass over this item's k; `after(q)` runs after the two stages of scale block q.
   auto sweep = [&](auto& d, auto j0_, auto nj_, auto before, auto after) {
-    auto stage = [&](int32_t q, int32_t second, uint8_t* sa, uint8_t* sb) {
-      const bool seg = kSeg == 2 && q >= kb;
-      fetch(seg ? 1 : 0, (seg ? q - kb : q) * kB + second, sa, sb);
-    };
-    stage(q0, 0, sa0, sb0);
+    if (!first_pass) stage(q0, 0, sa0, sb0);
+    first_pass = false;
     put(sa0, sb0);
     for (int32_t q = q0; q < q1; ++q) {
       before(q);
