@@ -186,6 +186,8 @@ def ffn_backward_weights(x: torch.Tensor, a: torch.Tensor, dy: torch.Tensor, dh:
         dw = tuple(x.new_empty(s, dtype=dtype) for s in shapes)
     else:
         dtype, dw = torch.float32, tuple(out)
+        if len(dw) != len(shapes):
+            _fail(f"{what}: out holds {len(dw)} tensors, expected {len(shapes)}")
         for w, s in zip(dw, shapes):
             _check(w, dev, dtype, s, f"{what} out")
     n = _weights_workspace(T, E, D, F)

@@ -528,3 +528,12 @@ def test_few_rows_of_large_weights(T):
     h, u, a = (c.out(c.F) for _ in range(3))
     fz.fp8z1_ffn_up(c.cfg, c.dev("x"), *c.dev("gate"), *c.dev("up"), c.dev("offsets"), h, u, a, workspace=ws)
     c.check_up((h, u, a), f"{T} rows")
+
+
+@pytest.mark.parametrize("count", [2, 4])
+def test_weight_gradients_refuse_another_count_of_outputs(count):
+    x, a = (torch.zeros(3, n, dtype=torch.bfloat16, device="cuda") for n in (16, 8))
+    out = [torch.zeros(1, 8, 16, device="cuda"), torch.zeros(1, 8, 16, device="cuda"),
+           torch.zeros(1, 16, 8, device="cuda"), torch.zeros(1, 16, 8, device="cuda")][:count]
+    with pytest.raises(fz.Fp8z1Error, match="expected 3"):
+        block.ffn_backward_weights(x, a, x, a, a, out=out)
