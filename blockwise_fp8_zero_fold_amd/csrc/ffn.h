@@ -2,6 +2,7 @@
 #pragma once
 
 #include "device_util.h"
+#include "ffn_refuse.h"
 #include "mfma.h"
 
 namespace fp8z1 {

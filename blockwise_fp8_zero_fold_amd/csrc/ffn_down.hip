@@ -20,7 +20,7 @@ extern "C" int fp8z1_ffn_down(const fp8z1_ffn* f, const void* a, const uint8_t* 
 }
 
 extern "C" int fp8z1_ffn_workspace_bytes(const fp8z1_ffn* f, size_t* bytes) {
-  if (!f || !bytes) return set_error(FP8Z1_EINVAL, "ffn_workspace_bytes: NULL argument");
+  if (!f || !bytes) return refuse(FP8Z1_EINVAL, "ffn_workspace_bytes", "NULL argument");
   static const int32_t some_offsets = 0;
   const int rc = check_cfg(f, &some_offsets, "ffn_workspace_bytes");
   if (rc) return rc;

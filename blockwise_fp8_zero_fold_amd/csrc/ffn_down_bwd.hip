@@ -9,7 +9,7 @@ extern "C" int fp8z1_ffn_down_bwd(const fp8z1_ffn* f, const void* dy, const uint
   const char* what = "ffn_down_bwd";
   int rc = check_cfg(f, offsets, what);
   if (!rc && f->T) rc = check_rows({dy, h, u, dh, du}, what);
-  if (!rc && misaligned(a, 2)) rc = set_error(FP8Z1_EINVAL, "ffn_down_bwd: misaligned rows");
+  if (!rc && misaligned(a, 2)) rc = refuse(FP8Z1_EINVAL, "ffn_down_bwd", "misaligned rows");
   if (!rc) rc = check_weights(down_codes, down_scales, what);
   if (rc) return rc;
   FfnArgs p = base_args(f, offsets, true);

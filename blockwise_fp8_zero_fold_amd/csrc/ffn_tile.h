@@ -633,7 +633,7 @@ bool misaligned(const void* p, size_t a);
 template <int KIND>
 int launch(FfnArgs p, int32_t dtype, void* workspace, size_t workspace_bytes, hipStream_t s, const char* what) {
   if (p.T == 0) return FP8Z1_OK;
-  if (misaligned(workspace, 16)) return set_error(FP8Z1_EINVAL, std::string(what) + ": misaligned workspace");
+  if (misaligned(workspace, 16)) return refuse(FP8Z1_EINVAL, what, "misaligned workspace");
   constexpr bool kTrans = KIND == kFfnDownBwd || KIND == kFfnUpBwd;
   const bool direct = !misaligned(p.x0, 4) && !misaligned(p.x1, 4) && !misaligned(p.w0, 4) && !misaligned(p.w1, 4) &&
                       (kTrans ? p.K % 2 == 0 && p.N % 4 == 0 : p.K % 4 == 0);
@@ -651,7 +651,7 @@ int launch(FfnArgs p, int32_t dtype, void* workspace, size_t workspace_bytes, hi
         launch_rows<Bf16, KIND>(p, aligned, s);
       else
         launch_rows<F16, KIND>(p, aligned, s);
-      return check_hip(hipGetLastError(), what);
+      return launched(what);
     }
   }
   const int64_t rows = most_row_tiles(p.T, p.E);
@@ -660,7 +660,7 @@ int launch(FfnArgs p, int32_t dtype, void* workspace, size_t workspace_bytes, hi
   const bool wide = direct && rows * ((p.N + 4 * per - 1) / (4 * per)) >= kSlots;
   const int32_t cols = per * (wide ? 4 : 2), ncols = (p.N + cols - 1) / cols;
   const int64_t tiles = rows * ncols;
-  if (tiles > 0x7fffffff - kSlots) return set_error(FP8Z1_ESHAPE, std::string(what) + ": too many tiles");
+  if (tiles > 0x7fffffff - kSlots) return refuse(FP8Z1_ESHAPE, what, "too many tiles");
   p.split_from = direct ? kDirectFrom : kRegisterFrom;
   const int64_t known = p.offsets ? tiles : static_cast<int64_t>((p.T + kRows - 1) / kRows) * ncols;
   if (split_pays(p, KIND == kFfnUpBwd ? 2 : 1, known) && workspace_bytes >= part_bytes(wide ? 4 : 2))
@@ -673,38 +673,37 @@ int launch(FfnArgs p, int32_t dtype, void* workspace, size_t workspace_bytes, hi
     launch_tiles<F16, KIND, 4>(p, direct, tiles, ncols, s);
   else
     launch_tiles<F16, KIND, 2>(p, direct, tiles, ncols, s);
-  return check_hip(hipGetLastError(), what);
+  return launched(what);
 }
 
 bool misaligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
 
 int check_cfg(const fp8z1_ffn* f, const int32_t* offsets, const char* what) {
-  const std::string w(what);
-  if (!f) return set_error(FP8Z1_EINVAL, w + ": NULL description");
+  if (!f) return refuse(FP8Z1_EINVAL, what, "NULL description");
   if (f->dtype != FP8Z1_BF16 && f->dtype != FP8Z1_F16)
-    return set_error(FP8Z1_EINVAL, w + ": dtype must be FP8Z1_BF16 or FP8Z1_F16");
+    return refuse(FP8Z1_EINVAL, what, "dtype must be FP8Z1_BF16 or FP8Z1_F16");
   if (f->act != FP8Z1_ACT_SILU && f->act != FP8Z1_ACT_GELU)
-    return set_error(FP8Z1_EINVAL, w + ": act must be FP8Z1_ACT_SILU or FP8Z1_ACT_GELU");
-  if (f->T < 0 || f->T > FP8Z1_FFN_MAX_ROWS) return set_error(FP8Z1_ESHAPE, w + ": T outside 0 .. 2^30");
-  if (f->E < 1 || f->E > FP8Z1_FFN_MAX_EXPERTS) return set_error(FP8Z1_ESHAPE, w + ": E outside 1 .. 65535");
+    return refuse(FP8Z1_EINVAL, what, "act must be FP8Z1_ACT_SILU or FP8Z1_ACT_GELU");
+  if (f->T < 0 || f->T > FP8Z1_FFN_MAX_ROWS) return refuse(FP8Z1_ESHAPE, what, "T outside 0 .. 2^30");
+  if (f->E < 1 || f->E > FP8Z1_FFN_MAX_EXPERTS) return refuse(FP8Z1_ESHAPE, what, "E outside 1 .. 65535");
   if (f->D < 1 || f->D > FP8Z1_FFN_MAX_WIDTH || f->F < 1 || f->F > FP8Z1_FFN_MAX_WIDTH)
-    return set_error(FP8Z1_ESHAPE, w + ": D and F must be 1 .. 2^20");
-  if (!offsets && f->E != 1) return set_error(FP8Z1_EINVAL, w + ": offsets may be NULL for one expert only");
-  if (misaligned(offsets, 4)) return set_error(FP8Z1_EINVAL, w + ": misaligned offsets");
+    return refuse(FP8Z1_ESHAPE, what, "D and F must be 1 .. 2^20");
+  if (!offsets && f->E != 1) return refuse(FP8Z1_EINVAL, what, "offsets may be NULL for one expert only");
+  if (misaligned(offsets, 4)) return refuse(FP8Z1_EINVAL, what, "misaligned offsets");
   return FP8Z1_OK;
 }
 
 int check_rows(std::initializer_list<const void*> xs, const char* what) {
   for (const void* x : xs) {
-    if (!x) return set_error(FP8Z1_EINVAL, std::string(what) + ": NULL argument");
-    if (misaligned(x, 2)) return set_error(FP8Z1_EINVAL, std::string(what) + ": misaligned rows");
+    if (!x) return refuse(FP8Z1_EINVAL, what, "NULL argument");
+    if (misaligned(x, 2)) return refuse(FP8Z1_EINVAL, what, "misaligned rows");
   }
   return FP8Z1_OK;
 }
 
 int check_weights(const uint8_t* codes, const float* scales, const char* what) {
-  if (!codes || !scales) return set_error(FP8Z1_EINVAL, std::string(what) + ": NULL weights");
-  if (misaligned(scales, 4)) return set_error(FP8Z1_EINVAL, std::string(what) + ": misaligned scales");
+  if (!codes || !scales) return refuse(FP8Z1_EINVAL, what, "NULL weights");
+  if (misaligned(scales, 4)) return refuse(FP8Z1_EINVAL, what, "misaligned scales");
   return FP8Z1_OK;
 }
 

@@ -273,16 +273,15 @@ struct Shape {
 };
 
 int check_wgrad(int64_t T, int64_t E, std::initializer_list<Shape> shapes, const char* what) {
-  const std::string w(what);
-  if (T < 0 || T > FP8Z1_FFN_MAX_ROWS) return set_error(FP8Z1_ESHAPE, w + ": T outside 0 .. 2^30");
-  if (E < 1 || E > FP8Z1_FFN_MAX_EXPERTS) return set_error(FP8Z1_ESHAPE, w + ": E outside 1 .. 65535");
+  if (T < 0 || T > FP8Z1_FFN_MAX_ROWS) return refuse(FP8Z1_ESHAPE, what, "T outside 0 .. 2^30");
+  if (E < 1 || E > FP8Z1_FFN_MAX_EXPERTS) return refuse(FP8Z1_ESHAPE, what, "E outside 1 .. 65535");
   int64_t tiles = 0;
   for (const Shape& s : shapes) {
     if (s.M < 1 || s.M > FP8Z1_FFN_MAX_WIDTH || s.N < 1 || s.N > FP8Z1_FFN_MAX_WIDTH)
-      return set_error(FP8Z1_ESHAPE, w + ": widths must be 1 .. 2^20");
+      return refuse(FP8Z1_ESHAPE, what, "widths must be 1 .. 2^20");
     tiles += tiles_of(E, s.M, s.N, kTile);
   }
-  if (tiles > 0x7fffffff) return set_error(FP8Z1_ESHAPE, w + ": too many tiles");
+  if (tiles > 0x7fffffff) return refuse(FP8Z1_ESHAPE, what, "too many tiles");
   return FP8Z1_OK;
 }
 
@@ -322,22 +321,21 @@ void launch_kernels(const WgradArgs& w, int nt, bool direct, hipStream_t s) {
 int launch_wgrad(int64_t T, int64_t E, int32_t dtype, const int32_t* offsets, int32_t dw_dtype, int32_t accumulate,
                  std::initializer_list<Wgrad> gs, void* workspace, size_t workspace_bytes, void* stream,
                  const char* what) {
-  const std::string name(what);
   if (dtype != FP8Z1_BF16 && dtype != FP8Z1_F16)
-    return set_error(FP8Z1_EINVAL, name + ": dtype must be FP8Z1_BF16 or FP8Z1_F16");
+    return refuse(FP8Z1_EINVAL, what, "dtype must be FP8Z1_BF16 or FP8Z1_F16");
   if (dw_dtype != FP8Z1_F32 && dw_dtype != FP8Z1_BF16)
-    return set_error(FP8Z1_EINVAL, name + ": dw_dtype must be FP8Z1_F32 or FP8Z1_BF16");
+    return refuse(FP8Z1_EINVAL, what, "dw_dtype must be FP8Z1_F32 or FP8Z1_BF16");
   if (accumulate && dw_dtype != FP8Z1_F32)
-    return set_error(FP8Z1_EINVAL, name + ": only FP8Z1_F32 gradients can be accumulated");
-  if (!offsets && E != 1) return set_error(FP8Z1_EINVAL, name + ": offsets may be NULL for one expert only");
+    return refuse(FP8Z1_EINVAL, what, "only FP8Z1_F32 gradients can be accumulated");
+  if (!offsets && E != 1) return refuse(FP8Z1_EINVAL, what, "offsets may be NULL for one expert only");
   if (misaligned(offsets, 4) || misaligned(workspace, 4))
-    return set_error(FP8Z1_EINVAL, name + ": misaligned argument");
+    return refuse(FP8Z1_EINVAL, what, "misaligned argument");
   bool direct = true;
   int64_t wide = 0, narrow = 0, size = 0;
   for (const Wgrad& g : gs) {
-    if (!g.dw || (T && (!g.p || !g.q))) return set_error(FP8Z1_EINVAL, name + ": NULL argument");
+    if (!g.dw || (T && (!g.p || !g.q))) return refuse(FP8Z1_EINVAL, what, "NULL argument");
     if (misaligned(g.p, 2) || misaligned(g.q, 2) || misaligned(g.dw, dw_dtype == FP8Z1_F32 ? 4 : 2))
-      return set_error(FP8Z1_EINVAL, name + ": misaligned argument");
+      return refuse(FP8Z1_EINVAL, what, "misaligned argument");
     direct = direct && g.M % 2 == 0 && g.N % 2 == 0 && !misaligned(g.p, 4) && !misaligned(g.q, 4);
     wide += tiles_of(E, g.M, g.N, 256);
     narrow += tiles_of(E, g.M, g.N, kTile);
@@ -373,7 +371,7 @@ int launch_wgrad(int64_t T, int64_t E, int32_t dtype, const int32_t* offsets, in
     launch_kernels<F16, true>(w, nt, direct, s);
   else
     launch_kernels<F16, false>(w, nt, direct, s);
-  return check_hip(hipGetLastError(), what);
+  return launched(what);
 }
 
 Wgrad gradient(const void* p, const void* q, void* dw, int64_t M, int64_t N) {
@@ -392,7 +390,7 @@ Wgrad gradient(const void* p, const void* q, void* dw, int64_t M, int64_t N) {
 using namespace fp8z1;
 
 extern "C" int fp8z1_ffn_wgrad_workspace_bytes(int64_t T, int64_t E, int64_t M, int64_t N, size_t* bytes) {
-  if (!bytes) return set_error(FP8Z1_EINVAL, "ffn_wgrad_workspace_bytes: NULL argument");
+  if (!bytes) return refuse(FP8Z1_EINVAL, "ffn_wgrad_workspace_bytes", "NULL argument");
   const int rc = check_wgrad(T, E, {{M, N}}, "ffn_wgrad_workspace_bytes");
   if (rc) return rc;
   *bytes = workspace_for(T, E, {{M, N}});
@@ -409,7 +407,7 @@ extern "C" int fp8z1_ffn_wgrad(int64_t T, int64_t E, int64_t M, int64_t N, int32
 }
 
 extern "C" int fp8z1_ffn_bwd_weights_workspace_bytes(const fp8z1_ffn* f, size_t* bytes) {
-  if (!f || !bytes) return set_error(FP8Z1_EINVAL, "ffn_bwd_weights_workspace_bytes: NULL argument");
+  if (!f || !bytes) return refuse(FP8Z1_EINVAL, "ffn_bwd_weights_workspace_bytes", "NULL argument");
   const int rc = check_wgrad(f->T, f->E, {{f->F, f->D}, {f->F, f->D}, {f->D, f->F}}, "ffn_bwd_weights_workspace_bytes");
   if (rc) return rc;
   *bytes = workspace_for(f->T, f->E, {{f->F, f->D}, {f->F, f->D}, {f->D, f->F}});
@@ -420,7 +418,7 @@ extern "C" int fp8z1_ffn_bwd_weights(const fp8z1_ffn* f, const void* x, const vo
                                      const void* du, const int32_t* offsets, int32_t dw_dtype, void* dw_gate,
                                      void* dw_up, void* dw_down, int32_t accumulate, void* d_workspace,
                                      size_t workspace_bytes, void* stream) {
-  if (!f) return set_error(FP8Z1_EINVAL, "ffn_bwd_weights: NULL description");
+  if (!f) return refuse(FP8Z1_EINVAL, "ffn_bwd_weights", "NULL description");
   const int rc = check_wgrad(f->T, f->E, {{f->F, f->D}, {f->F, f->D}, {f->D, f->F}}, "ffn_bwd_weights");
   if (rc) return rc;
   return launch_wgrad(f->T, f->E, f->dtype, offsets, dw_dtype, accumulate,

@@ -13,6 +13,7 @@
 #include <hip/hip_runtime.h>
 
 #include "device_util.h"
+#include "ffn_refuse.h"
 #include "mfma.h"
 
 namespace fp8z1 {
@@ -537,20 +538,19 @@ Groups bwd_groups(int64_t T, int64_t C) {
 }
 
 int check_norm(const fp8z1_norm* f, const void* y, const float* w_post, const void* gate, const char* what) {
-  const std::string w(what);
-  if (!f) return set_error(FP8Z1_EINVAL, w + ": NULL description");
+  if (!f) return refuse(FP8Z1_EINVAL, what, "NULL description");
   if (f->dtype != FP8Z1_BF16 && f->dtype != FP8Z1_F16 && f->dtype != FP8Z1_F32)
-    return set_error(FP8Z1_EINVAL, w + ": dtype must be FP8Z1_F32, FP8Z1_BF16 or FP8Z1_F16");
+    return refuse(FP8Z1_EINVAL, what, "dtype must be FP8Z1_F32, FP8Z1_BF16 or FP8Z1_F16");
   if (f->res_dtype != f->dtype && f->res_dtype != FP8Z1_F32)
-    return set_error(FP8Z1_EINVAL, w + ": res_dtype must be dtype or FP8Z1_F32");
-  if (f->gate < FP8Z1_GATE_NONE || f->gate > FP8Z1_GATE_FULL) return set_error(FP8Z1_EINVAL, w + ": unknown gate kind");
-  if (f->T < 0 || f->T > FP8Z1_FFN_MAX_ROWS) return set_error(FP8Z1_ESHAPE, w + ": T outside 0 .. 2^30");
-  if (f->C < 1 || f->C > kMaxC) return set_error(FP8Z1_ESHAPE, w + ": C outside 1 .. 16384");
-  if (!(f->eps >= 0.0f)) return set_error(FP8Z1_EINVAL, w + ": eps must be >= 0");
+    return refuse(FP8Z1_EINVAL, what, "res_dtype must be dtype or FP8Z1_F32");
+  if (f->gate < FP8Z1_GATE_NONE || f->gate > FP8Z1_GATE_FULL) return refuse(FP8Z1_EINVAL, what, "unknown gate kind");
+  if (f->T < 0 || f->T > FP8Z1_FFN_MAX_ROWS) return refuse(FP8Z1_ESHAPE, what, "T outside 0 .. 2^30");
+  if (f->C < 1 || f->C > kMaxC) return refuse(FP8Z1_ESHAPE, what, "C outside 1 .. 16384");
+  if (!(f->eps >= 0.0f)) return refuse(FP8Z1_EINVAL, what, "eps must be >= 0");
   if (!y && f->T && (w_post || f->gate != FP8Z1_GATE_NONE))
-    return set_error(FP8Z1_EINVAL, w + ": a norm after the block or a gate needs y");
+    return refuse(FP8Z1_EINVAL, what, "a norm after the block or a gate needs y");
   if ((f->gate != FP8Z1_GATE_NONE) != (gate != nullptr) && f->T)
-    return set_error(FP8Z1_EINVAL, w + ": gate pointer and gate kind disagree");
+    return refuse(FP8Z1_EINVAL, what, "gate pointer and gate kind disagree");
   return FP8Z1_OK;
 }
 
@@ -622,7 +622,7 @@ int check_alignment(const fp8z1_norm* f, std::initializer_list<const void*> act,
   for (const void* p : res) bad |= misaligned(p, elem_size(f->res_dtype));
   for (const void* p : f32) bad |= misaligned(p, 4);
   for (const void* p : gates) bad |= misaligned(p, f->gate == FP8Z1_GATE_FULL ? elem_size(f->dtype) : 4);
-  return bad ? set_error(FP8Z1_EINVAL, std::string(what) + ": misaligned argument") : FP8Z1_OK;
+  return bad ? refuse(FP8Z1_EINVAL, what, "misaligned argument") : FP8Z1_OK;
 }
 
 }  // namespace
@@ -636,21 +636,21 @@ extern "C" int fp8z1_norm_join(const fp8z1_norm* f, const void* y, const void* r
   int rc = check_norm(f, y, w_post, gate, what);
   if (rc) return rc;
   if (f->T == 0) return FP8Z1_OK;
-  if (!res || (!z && !n)) return set_error(FP8Z1_EINVAL, "norm_join: NULL argument");
+  if (!res || (!z && !n)) return refuse(FP8Z1_EINVAL, "norm_join", "NULL argument");
   rc = check_alignment(f, {y, n}, {res, z}, {w_post, w_pre}, {gate}, what);
   if (rc) return rc;
   NormArgs a = base_args(f, y, res, w_post, gate, w_pre);
   a.z = z;
   a.n = n;
   launch<false>(f, a, fwd_groups(f->T, f->C), 1, static_cast<hipStream_t>(stream));
-  return check_hip(hipGetLastError(), "norm_join: launch");
+  return launched("norm_join");
 }
 
 extern "C" int fp8z1_norm_join_bwd_workspace_bytes(const fp8z1_norm* f, size_t* bytes) {
-  if (!bytes) return set_error(FP8Z1_EINVAL, "norm_join_bwd_workspace_bytes: NULL argument");
-  if (!f) return set_error(FP8Z1_EINVAL, "norm_join_bwd_workspace_bytes: NULL description");
+  if (!bytes) return refuse(FP8Z1_EINVAL, "norm_join_bwd_workspace_bytes", "NULL argument");
+  if (!f) return refuse(FP8Z1_EINVAL, "norm_join_bwd_workspace_bytes", "NULL description");
   if (f->T < 0 || f->T > FP8Z1_FFN_MAX_ROWS || f->C < 1 || f->C > kMaxC)
-    return set_error(FP8Z1_ESHAPE, "norm_join_bwd_workspace_bytes: T or C out of range");
+    return refuse(FP8Z1_ESHAPE, "norm_join_bwd_workspace_bytes", "T or C out of range");
   *bytes = sizeof(float) * 3 * static_cast<size_t>(bwd_groups(f->T, f->C).count) * static_cast<size_t>(f->C);
   return FP8Z1_OK;
 }
@@ -662,11 +662,11 @@ extern "C" int fp8z1_norm_join_bwd(const fp8z1_norm* f, const void* dz, const vo
   const char* what = "norm_join_bwd";
   int rc = check_norm(f, y, w_post, gate, what);
   if (rc) return rc;
-  if (f->T && !dz && !dn) return set_error(FP8Z1_EINVAL, "norm_join_bwd: dz and dn are both NULL");
-  if (f->T && dn && !z) return set_error(FP8Z1_EINVAL, "norm_join_bwd: dn needs z");
-  if (f->T && dy && !y) return set_error(FP8Z1_EINVAL, "norm_join_bwd: dy needs y");
-  if ((dw_post && !w_post) || (dw_pre && !w_pre)) return set_error(FP8Z1_EINVAL, "norm_join_bwd: gradient of no weight");
-  if (dgate && f->gate == FP8Z1_GATE_NONE) return set_error(FP8Z1_EINVAL, "norm_join_bwd: gradient of no gate");
+  if (f->T && !dz && !dn) return refuse(FP8Z1_EINVAL, "norm_join_bwd", "dz and dn are both NULL");
+  if (f->T && dn && !z) return refuse(FP8Z1_EINVAL, "norm_join_bwd", "dn needs z");
+  if (f->T && dy && !y) return refuse(FP8Z1_EINVAL, "norm_join_bwd", "dy needs y");
+  if ((dw_post && !w_post) || (dw_pre && !w_pre)) return refuse(FP8Z1_EINVAL, "norm_join_bwd", "gradient of no weight");
+  if (dgate && f->gate == FP8Z1_GATE_NONE) return refuse(FP8Z1_EINVAL, "norm_join_bwd", "gradient of no gate");
   rc = check_alignment(f, {y, dn, dy}, {z, dz, dres}, {w_post, w_pre, dw_post, dw_pre}, {gate, dgate}, what);
   if (rc) return rc;
   float* gate_cols = f->gate == FP8Z1_GATE_CHANNEL ? static_cast<float*>(dgate) : nullptr;
@@ -676,8 +676,8 @@ extern "C" int fp8z1_norm_join_bwd(const fp8z1_norm* f, const void* dz, const vo
     size_t need = 0;
     rc = fp8z1_norm_join_bwd_workspace_bytes(f, &need);
     if (rc) return rc;
-    if (!workspace || workspace_bytes < need) return set_error(FP8Z1_EINVAL, "norm_join_bwd: workspace too small");
-    if (misaligned(workspace, 16)) return set_error(FP8Z1_EINVAL, "norm_join_bwd: misaligned workspace");
+    if (!workspace || workspace_bytes < need) return refuse(FP8Z1_EINVAL, "norm_join_bwd", "workspace too small");
+    if (misaligned(workspace, 16)) return refuse(FP8Z1_EINVAL, "norm_join_bwd", "misaligned workspace");
   }
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (f->T) {
@@ -696,14 +696,14 @@ extern "C" int fp8z1_norm_join_bwd(const fp8z1_norm* f, const void* dz, const vo
     a.want_gate = gate_cols != nullptr;
     a.waves = threads_for(f->C) / 64;
     launch<true>(f, a, groups.count, groups.rows, s);
-    rc = check_hip(hipGetLastError(), "norm_join_bwd: launch");
+    rc = launched("norm_join_bwd");
     if (rc) return rc;
   }
   if (sums && (f->T == 0 || groups.count > 1)) {
     hipLaunchKernelGGL(norm_columns_kernel, dim3(static_cast<unsigned>((f->C + 63) / 64), 3), dim3(1024), 0, s,
                        static_cast<const float*>(workspace), static_cast<int32_t>(f->T ? groups.count : 0), static_cast<int32_t>(f->C),
                        dw_post, dw_pre, gate_cols);
-    rc = check_hip(hipGetLastError(), "norm_join_bwd: sums launch");
+    rc = launched("norm_join_bwd");
   }
   return rc;
 }
