@@ -117,7 +117,8 @@ __device__ __forceinline__ void finish8(const FfnArgs& p, int64_t at, int count,
 // and 32 up columns), so that the rows leave 16 bytes per lane and 128 bytes in a row, by a
 // loop of little code: from the accumulators directly, 2 bytes at a time, the results took
 // a quarter of a large problem's time, and their unrolled code, read once, most of a
-// small one's.  Chunk c (16 bytes) of row r sits at c ^ (r mod 16).
+// small one's.  Chunk c (16 bytes) of row r sits at c ^ (r mod 16).  What a lane writes there another
+// lane of its wave reads, and the next turn's results go over it: handed_over() stands between.
 constexpr int kResultBytes = 4 * 64 * 64 * 4;
 __device__ __forceinline__ int result_at(int r, int c) { return r * 256 + ((c ^ (r & 15)) << 4); }
 
@@ -128,6 +129,14 @@ __device__ __forceinline__ void lay_tile(const f32x16& x, uint8_t* to, int i, in
   for (int q = 0; q < 4; ++q)
     *reinterpret_cast<f32x4*>(to + result_at(r, j * 8 + q * 2 + (lane >> 5))) =
         f32x4{x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]};
+}
+
+// LDS accesses of the wave's lanes stay on their side of this.  The hardware runs a wave's LDS
+// accesses in order, so it costs no instruction: it keeps the compiler, which sees a lane's own
+// addresses only, from moving a read of another lane's values over their write.
+__device__ __forceinline__ void handed_over() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
 }
 
 __device__ __forceinline__ void read8(const uint8_t* from, int r, int c, float (&x)[8]) {
@@ -475,7 +484,9 @@ __global__ __launch_bounds__(kThreads, 2) void ffn_tile_kernel(FfnArgs p, int32_
         lay(Int<0>{});
       else
         lay(Int<NT == 2 ? 0 : kUp ? 1 : 2>{});
+      handed_over();
       store_rows<H, KIND>(p, mine, m0 + wm * 64, hi, n0 + wn * (NT / 2) * (kUp ? 32 : 64) + turn * (kUp ? 32 : 64));
+      handed_over();
     }
   };
 
