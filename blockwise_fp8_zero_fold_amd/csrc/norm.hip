@@ -15,6 +15,7 @@
 #include "device_util.h"
 #include "ffn_refuse.h"
 #include "mfma.h"
+#include "norm_plan.h"
 
 namespace fp8z1 {
 namespace {
@@ -507,36 +508,6 @@ bool misaligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p)
 
 constexpr int64_t kMaxC = FP8Z1_NORM_MAX_WIDTH;
 
-int threads_for(int64_t C) {
-  const int64_t per = C <= 8192 ? 8 : 16;  // elements a thread holds
-  return static_cast<int>((C + 64 * per - 1) / (64 * per) * 64);
-}
-
-// Forward: a row per workgroup, 14 waves per compute unit (twice as many are 2 % slower, a
-// workgroup for every row 20 %), the workgroups walking over the rows side by side (each
-// over rows of its own in a row: 20 % slower).
-int64_t fwd_groups(int64_t T, int64_t C) {
-  const int64_t waves = threads_for(C) / 64, most = (256 * 14 + waves - 1) / waves;
-  return T < most ? T : most;
-}
-
-// Backward: up to 16 waves per workgroup (a compute unit holds 16 of them, by their registers),
-// for several short rows at a time, since every workgroup also writes its column sums.  Rows for
-// one turn of one workgroup go to one, which writes the gradients itself: no second launch (3 us
-// on the host).  Not for more: a turn takes 4.3 us, the second launch and its kernel 4 (captured,
-// 2 rows of 7168: one workgroup 13.2 us, two and the second launch 11.5; 32 rows of 1024: 20.9 and 8.2).
-struct Groups {
-  int64_t rows, count;  // rows at a time per workgroup, workgroups
-};
-Groups bwd_groups(int64_t T, int64_t C) {
-  const int64_t waves = threads_for(C) / 64, all = C <= 8192 ? 16 / waves : 1;
-  if (T <= all) return {T, 1};
-  int64_t rows = (T + 255) / 256;
-  if (rows > all) rows = all;
-  const int64_t most = 256 * (16 / (waves * rows)), want = (T + rows - 1) / rows;
-  return {rows, want < most ? want : most};
-}
-
 int check_norm(const fp8z1_norm* f, const void* y, const float* w_post, const void* gate, const char* what) {
   if (!f) return refuse(FP8Z1_EINVAL, what, "NULL description");
   if (f->dtype != FP8Z1_BF16 && f->dtype != FP8Z1_F16 && f->dtype != FP8Z1_F32)
@@ -597,7 +568,7 @@ void launch_typed(const NormArgs& a, dim3 g, dim3 b, hipStream_t s) {
 
 template <bool BWD>
 void launch(const fp8z1_norm* f, const NormArgs& a, int64_t groups, int64_t rows, hipStream_t s) {
-  const dim3 g(static_cast<unsigned>(groups)), b(static_cast<unsigned>(rows * threads_for(f->C)));
+  const dim3 g(static_cast<unsigned>(groups)), b(static_cast<unsigned>(rows * norm_threads(f->C)));
   const bool wide = f->res_dtype == FP8Z1_F32;
   if (f->dtype == FP8Z1_F32)
     launch_typed<F32, F32, BWD>(a, g, b, s);
@@ -642,7 +613,7 @@ extern "C" int fp8z1_norm_join(const fp8z1_norm* f, const void* y, const void* r
   NormArgs a = base_args(f, y, res, w_post, gate, w_pre);
   a.z = z;
   a.n = n;
-  launch<false>(f, a, fwd_groups(f->T, f->C), 1, static_cast<hipStream_t>(stream));
+  launch<false>(f, a, norm_fwd_groups(f->T, f->C), 1, static_cast<hipStream_t>(stream));
   return launched("norm_join");
 }
 
@@ -651,7 +622,7 @@ extern "C" int fp8z1_norm_join_bwd_workspace_bytes(const fp8z1_norm* f, size_t* 
   if (!f) return refuse(FP8Z1_EINVAL, "norm_join_bwd_workspace_bytes", "NULL description");
   if (f->T < 0 || f->T > FP8Z1_FFN_MAX_ROWS || f->C < 1 || f->C > kMaxC)
     return refuse(FP8Z1_ESHAPE, "norm_join_bwd_workspace_bytes", "T or C out of range");
-  *bytes = sizeof(float) * 3 * static_cast<size_t>(bwd_groups(f->T, f->C).count) * static_cast<size_t>(f->C);
+  *bytes = sizeof(float) * 3 * static_cast<size_t>(norm_bwd_groups(f->T, f->C).count) * static_cast<size_t>(f->C);
   return FP8Z1_OK;
 }
 
@@ -671,7 +642,7 @@ extern "C" int fp8z1_norm_join_bwd(const fp8z1_norm* f, const void* dz, const vo
   if (rc) return rc;
   float* gate_cols = f->gate == FP8Z1_GATE_CHANNEL ? static_cast<float*>(dgate) : nullptr;
   const bool sums = dw_post || dw_pre || gate_cols;
-  const Groups groups = bwd_groups(f->T, f->C);
+  const NormGroups groups = norm_bwd_groups(f->T, f->C);
   if (sums && f->T) {
     size_t need = 0;
     rc = fp8z1_norm_join_bwd_workspace_bytes(f, &need);
@@ -694,7 +665,7 @@ extern "C" int fp8z1_norm_join_bwd(const fp8z1_norm* f, const void* dz, const vo
     a.want_post = dw_post != nullptr;
     a.want_pre = dw_pre != nullptr;
     a.want_gate = gate_cols != nullptr;
-    a.waves = threads_for(f->C) / 64;
+    a.waves = norm_threads(f->C) / 64;
     launch<true>(f, a, groups.count, groups.rows, s);
     rc = launched("norm_join_bwd");
     if (rc) return rc;
