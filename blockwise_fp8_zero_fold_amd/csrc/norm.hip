@@ -99,8 +99,7 @@ __device__ __forceinline__ void load8(const void* row, int32_t C, int32_t c, flo
   widen8f<H>(fetch8<H>(row, C, c), v);
 }
 
-// STREAM: with the non-temporal hint, which the forward pass gains 3 % from and the backward
-// pass loses 4 % with
+// STREAM: with the non-temporal hint (where: see launch_join)
 template <class H, bool STREAM = false>
 __device__ __forceinline__ void store8(void* row, int32_t C, int32_t c, const float (&v)[8]) {
   typedef typename Elem<H>::type E;
@@ -208,7 +207,7 @@ __device__ __forceinline__ void load_gate(const NormArgs& a, int64_t row, int32_
   for (int i = 0; i < 8; ++i) g[i] *= a.block_scale;
 }
 
-template <class H, class R, int CH>
+template <class H, class R, int CH, bool STREAM>
 __global__ __launch_bounds__(1024) void norm_join_kernel(NormArgs a) {
   __shared__ float lds[2][16];
   constexpr bool kHold = CH == 1;  // weights kept in registers over the rows
@@ -252,7 +251,7 @@ __global__ __launch_bounds__(1024) void norm_join_kernel(NormArgs a) {
         if (a.y) z[ch][i] = fmaf(gate[ch][i], y[ch][i] * r * wpost[ch][i], z[ch][i]);
         sum[0] = fmaf(z[ch][i], z[ch][i], sum[0]);
       }
-      if (a.z) store8<R, true>(row_of<R>(a.z, row, a.C), a.C, col(ch), z[ch]);
+      if (a.z) store8<R, STREAM>(row_of<R>(a.z, row, a.C), a.C, col(ch), z[ch]);
     }
     if (a.n) {
       row_sums<1>(sum, lds[1], waves);
@@ -261,7 +260,7 @@ __global__ __launch_bounds__(1024) void norm_join_kernel(NormArgs a) {
       for (int ch = 0; ch < CH; ++ch) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) z[ch][i] = z[ch][i] * r * wpre[ch][i];
-        store8<H, true>(row_of<H>(a.n, row, a.C), a.C, col(ch), z[ch]);
+        store8<H, STREAM>(row_of<H>(a.n, row, a.C), a.C, col(ch), z[ch]);
       }
     }
     if (!(a.w_post && a.n)) __syncthreads();  // only one of the two LDS sets is used per row
@@ -548,6 +547,29 @@ bool rows_aligned(const NormArgs& a) {
          (a.gate_kind != FP8Z1_GATE_FULL || !misaligned(a.gate, 16));
 }
 
+// The forward pass stores z and n with the non-temporal hint while they take no more than half of the
+// L2 caches, and without it above, where it would push them out of the caches that the next calls
+// read them from.  A join, an up projection of n and a join of z, with and without the hint (bfloat16,
+// float32 residual): 256 x 7168 31.8 and 33.1 us, 2048 x 1024 30.1 and 31.4, 512 x 7168 47.0 and 45.6, 4096 x
+// 1024 41.5 and 38.2, 2048 x 7168 110 and 105, 3000 x 5120 127 and 116.  (The join alone, which leaves
+// its stores to others: 512 x 7168 11.1 and 12.7, 8192 x 7168 121 and 120, x 8192 144 and 137.)  The backward
+// pass stores without (221 and 211).
+constexpr int64_t kHalfOfL2 = kXcds * (4LL << 20) / 2;
+template <class H, class R>
+void launch_join(const NormArgs& a, dim3 g, dim3 b, hipStream_t s) {
+  const int64_t bytes =
+      static_cast<int64_t>(a.T) * a.C * (sizeof(typename Elem<H>::type) + sizeof(typename Elem<R>::type));
+  const bool one = a.C <= 8192, hint = bytes <= kHalfOfL2;
+  if (one && hint)
+    hipLaunchKernelGGL((norm_join_kernel<H, R, 1, true>), g, b, 0, s, a);
+  else if (one)
+    hipLaunchKernelGGL((norm_join_kernel<H, R, 1, false>), g, b, 0, s, a);
+  else if (hint)
+    hipLaunchKernelGGL((norm_join_kernel<H, R, 2, true>), g, b, 0, s, a);
+  else
+    hipLaunchKernelGGL((norm_join_kernel<H, R, 2, false>), g, b, 0, s, a);
+}
+
 template <class H, class R, bool BWD>
 void launch_typed(const NormArgs& a, dim3 g, dim3 b, hipStream_t s) {
   const bool one = a.C <= 8192;
@@ -560,10 +582,8 @@ void launch_typed(const NormArgs& a, dim3 g, dim3 b, hipStream_t s) {
     hipLaunchKernelGGL((norm_join_bwd_kernel<H, R, 1, false>), g, b, 32 * b.x, s, a);
   else if (BWD)
     hipLaunchKernelGGL((norm_join_bwd_kernel<H, R, 2, false>), g, b, 0, s, a);
-  else if (one)
-    hipLaunchKernelGGL((norm_join_kernel<H, R, 1>), g, b, 0, s, a);
   else
-    hipLaunchKernelGGL((norm_join_kernel<H, R, 2>), g, b, 0, s, a);
+    launch_join<H, R>(a, g, b, s);
 }
 
 template <bool BWD>
