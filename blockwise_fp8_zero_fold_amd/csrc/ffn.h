@@ -42,6 +42,45 @@ __device__ __forceinline__ void expert_rows(const int32_t* offsets, int32_t T, i
   }
 }
 
+// Rows in groups of ROWS for launches that give each group a workgroup of its own.  Group e < E is the
+// first of expert e, as one would number them if no expert had more.  The others follow: expert e
+// has the numbers E + rows_before / ROWS and on, as many as its rows can need (one may be over), so that a
+// group's expert is the last whose first number is not above it, and E + T / ROWS groups are enough.
+// A wave looks for it 64 experts at a time (a step per power of 64).  False: the group has no rows;
+// also for offsets out of order, which give wrong rows but no access out of bounds.
+template <int ROWS>
+__device__ __forceinline__ bool find_group(const int32_t* offsets, int32_t T, int32_t E, int32_t group, int32_t& e,
+                                           int32_t& lo, int32_t& hi, int32_t& t0) {
+  if (group < E) {
+    e = group;
+    expert_rows(offsets, T, e, lo, hi);
+    t0 = lo;
+    return t0 < hi;
+  }
+  group -= E;
+  e = 0;
+  lo = 0;
+  hi = T;
+  if (offsets) {
+    const int lane = threadIdx.x & 63;
+    int32_t stride = 1;
+    while (static_cast<int64_t>(stride) * 64 < E) stride *= 64;
+    for (; stride > 0; stride /= 64) {
+      const int32_t at = min(e + lane * stride, E - 1);
+      int32_t from, to;
+      expert_rows(offsets, T, at, from, to);
+      const uint64_t upto = __ballot(e + lane * stride < E && from / ROWS <= group);
+      const int last = upto ? 63 - __builtin_clzll(upto) : 0;
+      e = __builtin_amdgcn_readfirstlane(e + last * stride);
+      lo = __builtin_amdgcn_readlane(from, last);  // (of expert e once the stride is 1)
+      hi = __builtin_amdgcn_readlane(to, last);
+    }
+  }
+  const int32_t past = group - lo / ROWS + 1;  // groups of this expert before it
+  t0 = lo + past * ROWS;
+  return past >= 1 && past <= (hi - lo) / ROWS && t0 < hi;
+}
+
 // Sums over this lane and those before it, by lane moves within rows of 16 and from a row's last
 // lane on (through LDS, as shuffles go, the sum's six steps take 0.3 us of a launch)
 __device__ __forceinline__ int32_t wave_upto(int32_t v) {

@@ -1,5 +1,6 @@
 """GPU: the feed-forward calls where one of many experts takes nearly all rows, and in several threads and
 streams at once."""
+import copy
 import threading
 
 import pytest
@@ -63,3 +64,68 @@ def test_streams_and_threads_at_once():
         t.join()
     torch.cuda.synchronize()
     assert not wrong
+
+
+@pytest.mark.parametrize("T,E,D,F", [(300, 5000, 16, 24), (70000, 65535, 8, 16)])
+def test_thousands_of_experts(T, E, D, F):
+    """More experts than one or two looks of a wave find, and more groups of rows than a grid has in y."""
+    c = small.Case(T, E, D, F)
+    what = f"{T} rows, {E} experts"
+    print("#", what, flush=True)
+    s, rows = large.sampled(c)
+    outs = c.run_up()
+    s.check_up([t[rows.cuda()] for t in outs], what)
+    y = c.out(D)
+    small.fz.fp8z1_ffn_down(c.cfg, c.dev("a"), *c.dev("down"), c.dev("offsets"), y)
+    s.check_down(y[rows.cuda()], what)
+    assert all(bool(torch.isfinite(t).all()) for t in (*outs, y))
+
+
+def test_rows_of_few_experts_without_cover():
+    """Few rows (the row kernel): rows that no expert covers are left alone, offsets out of range and out
+    of order write within the tensor."""
+    c = small.Case(90, 5, 136, 72)
+    c.offsets = torch.tensor([20, 40, 40, 41, 75, 75], dtype=torch.int32)
+    outs = c.run_up()
+    s = copy.copy(c)
+    rows = torch.arange(20, 75)
+    for k in ("x", "dy", "a", "h", "u", "dh", "du"):
+        setattr(s, k, getattr(c, k)[rows])
+    s.T, s.offsets = rows.numel(), c.offsets - 20
+    s.check_up([t[rows.cuda()] for t in outs], "covered rows")
+    for t in outs:
+        assert bool((t[:20] == 7.0).all()) and bool((t[75:] == 7.0).all())
+    for bad in ([-50, 20, 10, 100000, 3, 90], [90, 80, 60, 40, 20, 0], [2 ** 31 - 1] * 6, [-2 ** 31] * 6):
+        c.offsets = torch.tensor(bad, dtype=torch.int64).to(torch.int32)
+        assert all(bool(torch.isfinite(t).all()) for t in c.run_up()), bad
+
+
+def test_a_load_on_one_expert_takes_no_longer_than_an_even_one():
+    """All of 8192 rows on one of 256 experts, and evenly on all: the groups of rows run side by side either
+    way (one after another they took 7 times as long; 3 are allowed)."""
+    T, E, D, F = 8192, 256, 510, 510
+
+    def weight(r, c):
+        return (torch.full((E, r, c), 0x30, dtype=torch.uint8, device="cuda"),
+                torch.full((E, -(-r // 128), -(-c // 128)), 1e-3, device="cuda"))
+
+    gate, up, down = weight(F, D), weight(F, D), weight(D, F)
+    x = torch.ones(T, D, dtype=torch.bfloat16, device="cuda")
+    even = (torch.arange(E + 1, device="cuda") * T // E).to(torch.int32)
+    one = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    one[E // 2 + 1:] = T
+
+    def least(offsets):
+        times = []
+        for _ in range(12):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            for _ in range(5):
+                small.block.ffn_forward(x, gate, up, down, offsets)
+            b.record()
+            b.synchronize()
+            times.append(a.elapsed_time(b))
+        return min(times)
+
+    t_even, t_one = least(even), least(one)
+    assert t_one <= 3 * t_even, (t_one, t_even)
