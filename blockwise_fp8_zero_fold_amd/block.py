@@ -4,7 +4,12 @@ allocation of outputs and call order only; all arithmetic runs in libfp8z1.
 A weight is a pair ``(codes [E,R,C] uint8, scales [E,ceil(R/128),ceil(C/128)] float32)`` as
 ``Shard.unfold`` writes it.  Gate and up weights are [E,F,D], the down weight [E,D,F].
 Rows (tokens) are sorted by expert: ``offsets`` [E+1] int32 on the device holds each
-expert's first row; None means one expert.  Everything runs on torch's current stream.
+expert's first row, from 0 to T; None means one expert.  Outputs' rows that no expert covers hold whatever
+their memory held.  Everything runs on torch's current stream.
+
+Products are summed in float32; the results, the inner ones too (``a`` between up and down,
+``dh`` and ``du`` before ``dx``), are rounded to the activations' 16 bits.  The sums hold
+activation * code before the block's scale: magnitudes of activations and gradients stay below 2^56.
 
 A training step over one block (see ``examples/train_ffn_layer.py``):
 
@@ -125,8 +130,8 @@ def ffn_forward(x: torch.Tensor, w_gate: Weight, w_up: Weight, w_down: Weight,
 
 def ffn_backward_data(dy: torch.Tensor, h: torch.Tensor, u: torch.Tensor, w_gate: Weight, w_up: Weight,
                       w_down: Weight, offsets: Optional[torch.Tensor] = None, act: str = "silu"):
-    """(dx, dh, du, a): the gradients at the block's input and its projections, and a again
-    (what the weight gradients need)."""
+    """(dx, dh, du, a): the gradients at the block's input and its projections, and a again, from the kept
+    (rounded) h and u (what the weight gradients need)."""
     what = "ffn_backward_data"
     dev, T, D, E, F, f = _ffn(dy, w_gate, act, what)
     py = _check(dy, dev, dy.dtype, (T, D), what)

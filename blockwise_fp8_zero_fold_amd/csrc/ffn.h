@@ -223,6 +223,7 @@ __device__ __forceinline__ bool find_tile(const int32_t* offsets, int32_t T, int
 // with v = sqrt(2/pi) (h + 0.044715 h^3); s is the logistic function, so one exponential
 // serves both.  Beyond |h| = 10^4, where s(1 - s) is 0 in float32, the derivative's second
 // term is taken at the border, which keeps h^3 from overflowing against that zero.
+// Where the exponential overflows, below -88.7, the logistic is 0 (it is less than 3e-39 there).
 // (the hardware's exponential and reciprocal, 1 ulp each, a third of the instructions of the
 // exact division; a reciprocal that would be subnormal is taken of a scaled argument)
 __device__ __forceinline__ float logistic(float x) {

@@ -13,7 +13,8 @@
 //
 // 128 tokens, evenly on 32 experts of widths 7168 and 2048: up 158 us (6.0 TB/s), down 97 us (4.9 TB/s; 2048 is 4
 // blocks for each wave, little to have on its way); with 1, 2 or 8 waves a workgroup up takes
-// 183, 175 or 188 us.  One token on one expert: 8.9 and 5.3 us, the latency of a few reads.
+// 183, 175 or 188 us.  One token on one expert: 9.4 and 5.4 us, the latency of a few reads
+// after one another.
 #pragma once
 
 #include "ffn.h"

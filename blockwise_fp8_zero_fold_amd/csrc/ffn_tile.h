@@ -11,11 +11,14 @@
 // rounded.  Two workgroups share a compute unit, one computing while the other waits.
 //
 // What bounds it: on 8192 tokens of 8 experts with widths 7168 and 2048 the four products run at
-// 870 to 980 TFLOP/s (up 0.50-0.55 ms, down 0.26, backward 0.28 and 0.50) and at 840 to 1090 on one dense
-// 4096 x 4096 expert, where a plain bfloat16 library product reaches 1340 to 1400.  The matrix
-// cores are then busy for 48 to 55 % of the cycles, and the clock is at 1.6 to 1.9 GHz of 2.4: the
-// card's power is what ends.  So bytes moved per product count: a wave of 128 x 64, which reads a
-// quarter more from LDS and widens half as many codes, needs 4 to 7 % fewer cycles and 4 to 7 % more time.
+// 830 to 960 TFLOP/s over many launches (up 0.51 ms, down 0.29, backward 0.28 and 0.54), single ones at
+// up to 1100, and at 840 to 1090 on one dense 4096 x 4096 expert, where a plain bfloat16 library
+// product reaches 1340 to 1400.  No one thing ends it.  The matrix cores are busy for 45 to 56 % of
+// the cycles; the waves wait for 35 to 41 % of theirs until an instruction can issue (matrix
+// instructions, the codes' widening, which both row halves of a tile do, and the rescaling between blocks)
+// and for 20 to 29 % on data and barriers; the clock is at 1.7 to 2.0 GHz of 2.4, so power has its share: a
+// wave of 128 x 64, which reads a quarter more from LDS and widens half as many codes, needs 4 to 7 % fewer
+// cycles and 4 to 7 % more time.  Up reads 980 MB of HBM for 350 MB of operands.
 // Small problems are bound by the chain of one tile: about 5 us and 1.5 us per scale block.
 #pragma once
 
@@ -73,6 +76,9 @@ __device__ __forceinline__ Kept load_kept(const FfnArgs& p, int64_t at, int coun
 }
 
 // The results of 8 columns of a row, of which `count` are there (for kFfnUp x: gate, v: up).
+// Each is rounded once, from float32 to the activations' 16 bits, which is what the matrix instructions
+// of the next product take and what a training step keeps: a between up and down, dh and du before dx
+// (so y and dx lie 1.4 times as far from the 64-bit result as after a single rounding at their end).
 template <class H, int KIND>
 __device__ __forceinline__ void finish8(const FfnArgs& p, int64_t at, int count, const float (&x)[8],
                                         const float (&v)[8], const Kept& kept) {
@@ -652,6 +658,7 @@ int launch(FfnArgs p, int32_t dtype, void* workspace, size_t workspace_bytes, hi
   // rows would be mostly empty (128 tokens on 32 experts: 425 us by tiles, 250 by rows).  Above 12
   // rows the row kernel reads them slower, at 2.2 TB/s for 32 rows where tiles with direct
   // copies reach 3.5 after some 7 us more of latency: tiles from about 10^9 bytes x rows above 12.
+  // (The average is all that the host knows; the row kernel keeps to it with any load, see there.)
   // (7168 x 2048, forward, rows and tiles: 1024 tokens on 32 experts 654 and 405 us, 256 on 8 169 and
   // 134, 128 on 8 122 and 138, 32 on 1 33 and 37.)
   if constexpr (!kTrans) {

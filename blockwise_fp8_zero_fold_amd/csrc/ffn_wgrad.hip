@@ -7,10 +7,15 @@
 // runs down the rows, so a stage of 32 tokens is kept in LDS as it lies in memory and
 // the matrix operands are gathered by the transposing LDS reads.
 //
-// 8192 tokens of 8 experts, widths 7168 and 2048, float32 gradients: 390 us for one gradient, 1.15 ms
-// for the three (600 to 650 TFLOP/s).  A gradient's 470 MB of output take 100 us by themselves (4.6
+// 8192 tokens of 8 experts, widths 7168 and 2048, float32 gradients: 390 us for one gradient, 1.10 to 1.16
+// ms for the three (620 to 660 TFLOP/s).  A gradient's 470 MB of output take 100 us by themselves (4.6
 // TB/s), which 32 stages of a tile do not hide; with four times the tokens it runs at 810 TFLOP/s, 940
-// for the tokens added.  2-byte results and gradients of one small tile are bound by latency.
+// for the tokens added.  The matrix cores are busy for 27 % of the cycles, at 2.2 GHz of 2.4 (power is not
+// what ends), the waves wait for 28 % of theirs on data and barriers (16 matrix instructions a wave between
+// two) and for 37 % until an instruction can issue.  Added to what is there (`accumulate`) the three take
+// 2.0 ms, 1.7 where 2048 tokens' take 0.57: each result's load waits behind the loop.
+// 20,000 tokens on widths 520 and 300 (few tiles, 11 parts each): 51 us; matrix cores 22 %, waves on data 27
+// %, at issue 31 %; 98 MB of HBM read, 5.7 million L2 requests of which 84 % hit: neither memory ends it.
 #include <hip/hip_runtime.h>
 
 #include <initializer_list>
@@ -241,8 +246,6 @@ __global__ __launch_bounds__(256) void ffn_wgrad_join_kernel(WgradArgs all) {
   }
 }
 
-// Columns of a tile: 256 where such tiles fill the card twice over (as many workgroups as run
-// at once, two on each of 256 compute units), else 128.
 int64_t tiles_of(int64_t E, int64_t M, int64_t N, int64_t cols) {
   return E * ((M + kTile - 1) / kTile) * ((N + cols - 1) / cols);
 }
@@ -341,6 +344,9 @@ int launch_wgrad(int64_t T, int64_t E, int32_t dtype, const int32_t* offsets, in
     narrow += tiles_of(E, g.M, g.N, kTile);
     size += E * g.M * g.N;
   }
+  // Columns of a tile: 256 where such tiles fill the card twice over (twice as many as the workgroups that
+  // run at once, two on each of 256 compute units), else 128.  Rows of odd width go through registers, in
+  // tiles of 128 (wider ones have not been tried).
   const int nt = direct && wide >= 2 * kSlots ? 4 : 2;
   WgradArgs w{};
   for (const Wgrad& g : gs) {

@@ -8,8 +8,12 @@
 // A workgroup keeps a whole row in registers, 8 elements per thread and chunk, and walks
 // over rows with the weights held in registers, so each tensor is read or written
 // once and the weights once per workgroup.  The kernels are bound by HBM bandwidth: 8192 rows of
-// 7168, bfloat16 with a float32 residual and a channel gate, take 125 us forward (5.6 TB/s) and 208 us
-// backward (5.1 TB/s, with the column sums' 7 us).  Two rows take 4.6 us.
+// 7168, bfloat16 with a float32 residual and a channel gate, take 120 to 126 us forward (5.6 to 5.9
+// TB/s) and 200 to 208 us backward (5.1 to 5.3 TB/s, with the column sums' 7 us).  Two rows take 4.6 us.
+// Other widths, forward and backward, 8192 rows: 1024 22 and 40 us, 4096 75 and 125, 5120 93 and 149, 8192 139
+// and 235, 16,384 353 and 1590.  Backward, rows that are no multiple of 8 wide are loaded when they are needed
+// instead of a row ahead (7001: 290 us), and above 8192, where a thread holds two chunks, 143 to 238
+// registers spill (8200: 1150 us); up to 8192 2 to 11 do.  The forward pass spills none.
 #include <hip/hip_runtime.h>
 
 #include "device_util.h"
