@@ -24,6 +24,8 @@ NOALLOC_MAX_SLOTS = 262144  # largest table fp8z1_step_rowmajor_noalloc takes
 ALL_RANKS = -1
 ACT_SILU, ACT_GELU = 0, 1
 GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL = 0, 1, 2, 3
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+ROUTE_MAX_EXPERTS, ROUTE_MAX_CHOICES = 1024, 32
 
 BLOCK_ENTRY_DTYPE = np.dtype([
     ("param", "<i4"), ("expert", "<i4"), ("brow", "<u2"), ("bcol", "<u2"),
@@ -98,8 +100,19 @@ class Norm(C.Structure):
                 ("weight_offset", C.c_float), ("reserved", C.c_int32)]
 
 
+class Router(C.Structure):
+    """The router's sizes and settings."""
+    _fields_ = [("T", C.c_int64), ("E", C.c_int32), ("k", C.c_int32), ("dtype", C.c_int32), ("score", C.c_int32),
+                ("normalize", C.c_int32), ("scale", C.c_float)]
+
+
+class Routed(C.Structure):
+    """Sizes of tokens [T,D] and their sorted rows [R,D], k rows of each token."""
+    _fields_ = [("T", C.c_int64), ("D", C.c_int64), ("R", C.c_int64), ("k", C.c_int32), ("dtype", C.c_int32)]
+
+
 assert C.sizeof(Block) == 16 and C.sizeof(State) == 64 and C.sizeof(Hparams) == 72
-assert C.sizeof(Ffn) == 40 and C.sizeof(Norm) == 48
+assert C.sizeof(Ffn) == 40 and C.sizeof(Norm) == 48 and C.sizeof(Router) == 32 and C.sizeof(Routed) == 32
 
 _vp = C.c_void_p
 _sig = {
@@ -138,6 +151,14 @@ _sig = {
     "fp8z1_norm_join": (C.c_int, [C.POINTER(Norm), *[_vp] * 8]),
     "fp8z1_norm_join_bwd_workspace_bytes": (C.c_int, [C.POINTER(Norm), C.POINTER(C.c_size_t)]),
     "fp8z1_norm_join_bwd": (C.c_int, [C.POINTER(Norm), *[_vp] * 13, C.c_size_t, _vp]),
+    "fp8z1_norm_join8": (C.c_int, [C.POINTER(Norm), *[_vp] * 9, C.c_int32, _vp]),
+    "fp8z1_route": (C.c_int, [C.POINTER(Router), *[_vp] * 5]),
+    "fp8z1_route_bwd": (C.c_int, [C.POINTER(Router), *[_vp] * 5]),
+    "fp8z1_sort_tokens_workspace_bytes": (C.c_int, [C.c_int64, C.c_int32, C.c_int32, C.POINTER(C.c_size_t)]),
+    "fp8z1_sort_tokens": (C.c_int, [C.c_int64, C.c_int32, C.c_int32, *[_vp] * 4, C.c_size_t, _vp]),
+    "fp8z1_dispatch": (C.c_int, [C.POINTER(Routed), *[_vp] * 6]),
+    "fp8z1_combine": (C.c_int, [C.POINTER(Routed), *[_vp] * 6]),
+    "fp8z1_combine_bwd": (C.c_int, [C.POINTER(Routed), *[_vp] * 7]),
     "fp8z1_probe_copy": (C.c_int, [_vp, _vp, C.c_int64, C.c_int64, _vp]),
     "fp8z1_probe_update_pattern": (C.c_int, [_vp, _vp, _vp, _vp, _vp, C.c_int64, C.c_int32, _vp]),
 }
@@ -566,6 +587,101 @@ def fp8z1_norm_join_bwd(f: Norm, dz, dn, y, z, w_post, gate, w_pre, dy, dres, dw
     _check(lib.fp8z1_norm_join_bwd(C.byref(f), _ptr(dz), _ptr(dn), _ptr(y), _ptr(z), _ptr(w_post), _ptr(gate),
                                    _ptr(w_pre), _ptr(dy), _ptr(dres), _ptr(dw_post), _ptr(dgate), _ptr(dw_pre),
                                    _ptr(workspace), workspace_bytes, _stream(stream)), "fp8z1_norm_join_bwd")
+
+
+def fp8z1_norm_join8(f: Norm, y, res, w_post, gate, w_pre, z, n, codes, scales, scale_rule: int = SCALE_AMAX,
+                     stream=None) -> None:
+    """The join with n in 8 bits: codes [T,C] and scales [T, ceil(C/128)]."""
+    _need_norm(f, "norm_join8", (y, n), (res, z), (w_post, w_pre), (gate,))
+    _need_rows8(f.T, f.C, "norm_join8", codes, scales)
+    _check(lib.fp8z1_norm_join8(C.byref(f), _ptr(y), _ptr(res), _ptr(w_post), _ptr(gate), _ptr(w_pre), _ptr(z), _ptr(n),
+                                _ptr(codes), _ptr(scales), scale_rule, _stream(stream)), "fp8z1_norm_join8")
+
+
+def _need_rows8(rows: int, width: int, what: str, codes, scales) -> None:
+    if codes is not None:
+        _need(codes, rows * width, f"{what} codes", torch.uint8)
+    if scales is not None:
+        _need(scales, rows * (-(-width // 128)) * 4, f"{what} scales", torch.float32)
+
+
+def _need_router(f: Router, what: str, logits=(), bias=None, choices=(), weights=()) -> None:
+    for x in logits:
+        _need(x, f.T * f.E * (4 if f.dtype == F32 else 2), f"{what} logits", _torch_dtype(f.dtype))
+    if bias is not None:
+        _need(bias, 4 * f.E, f"{what} bias", torch.float32)
+    for x in choices:
+        _need(x, 4 * f.T * f.k, f"{what} experts", torch.int32)
+    for x in weights:
+        _need(x, 4 * f.T * f.k, f"{what} weights", torch.float32)
+
+
+def fp8z1_route(f: Router, logits, bias, experts, weights, stream=None) -> None:
+    """experts and weights [T,k] of the k best scores (plus bias) of each row of logits [T,E]."""
+    _need_router(f, "route", (logits,), bias, (experts,), (weights,))
+    _check(lib.fp8z1_route(C.byref(f), _ptr(logits), _ptr(bias), _ptr(experts), _ptr(weights), _stream(stream)),
+           "fp8z1_route")
+
+
+def fp8z1_route_bwd(f: Router, logits, experts, dweights, dlogits, stream=None) -> None:
+    """The logits' gradient from that of the weights."""
+    _need_router(f, "route_bwd", (logits, dlogits), None, (experts,), (dweights,))
+    _check(lib.fp8z1_route_bwd(C.byref(f), _ptr(logits), _ptr(experts), _ptr(dweights), _ptr(dlogits), _stream(stream)),
+           "fp8z1_route_bwd")
+
+
+def fp8z1_sort_tokens_workspace_bytes(T: int, k: int, E: int) -> int:
+    n = C.c_size_t()
+    _check(lib.fp8z1_sort_tokens_workspace_bytes(T, k, E, C.byref(n)), "fp8z1_sort_tokens_workspace_bytes")
+    return n.value
+
+
+def fp8z1_sort_tokens(T: int, k: int, E: int, experts, offsets, row_of, workspace=None, workspace_bytes: int = 0,
+                      stream=None) -> None:
+    """offsets [E+1] and row_of [T,k] of experts [T,k]."""
+    workspace_bytes = _workspace(workspace, workspace_bytes, "sort_tokens")
+    for x in (experts, row_of):
+        if x is not None:
+            _need(x, 4 * T * k, "sort_tokens choices", torch.int32)
+    _need_offsets(offsets, E, "sort_tokens")
+    _check(lib.fp8z1_sort_tokens(T, k, E, _ptr(experts), _ptr(offsets), _ptr(row_of), _ptr(workspace), workspace_bytes,
+                                 _stream(stream)), "fp8z1_sort_tokens")
+
+
+def _need_routed(f: Routed, what: str, row_of, tokens=(), rows=(), weights=()) -> None:
+    el, dt = {F32: 4, E4M3: 1}.get(f.dtype, 2), _torch_dtype(f.dtype)
+    if row_of is not None:
+        _need(row_of, 4 * f.T * f.k, f"{what} row_of", torch.int32)
+    for xs, n in ((tokens, f.T), (rows, f.R)):
+        for x in xs:
+            if x is not None:
+                _need(x, n * f.D * el, what, dt)
+    for x in weights:
+        if x is not None:
+            _need(x, 4 * f.T * f.k, f"{what} weights", torch.float32)
+
+
+def fp8z1_dispatch(f: Routed, row_of, x, scales, rows, row_scales, stream=None) -> None:
+    """rows[row_of[t][j]] = x[t], and the scales of 8-bit rows with them."""
+    _need_routed(f, "dispatch", row_of, (x,), (rows,))
+    _need_rows8(f.T, f.D, "dispatch", None, scales)
+    _need_rows8(f.R, f.D, "dispatch", None, row_scales)
+    _check(lib.fp8z1_dispatch(C.byref(f), _ptr(row_of), _ptr(x), _ptr(scales), _ptr(rows), _ptr(row_scales),
+                              _stream(stream)), "fp8z1_dispatch")
+
+
+def fp8z1_combine(f: Routed, row_of, rows, weights, base, y, stream=None) -> None:
+    """y[t] = base[t] + sum over j of weights[t][j] rows[row_of[t][j]]."""
+    _need_routed(f, "combine", row_of, (base, y), (rows,), (weights,))
+    _check(lib.fp8z1_combine(C.byref(f), _ptr(row_of), _ptr(rows), _ptr(weights), _ptr(base), _ptr(y), _stream(stream)),
+           "fp8z1_combine")
+
+
+def fp8z1_combine_bwd(f: Routed, row_of, dy, rows, weights, drows, dweights, stream=None) -> None:
+    """The gradients of the rows and of the weights; one that is None is not computed."""
+    _need_routed(f, "combine_bwd", row_of, (dy,), (rows, drows), (weights, dweights))
+    _check(lib.fp8z1_combine_bwd(C.byref(f), _ptr(row_of), _ptr(dy), _ptr(rows), _ptr(weights), _ptr(drows),
+                                 _ptr(dweights), _stream(stream)), "fp8z1_combine_bwd")
 
 
 def fp8z1_probe_copy(src, dst, spread: int = 1, stream=None) -> None:

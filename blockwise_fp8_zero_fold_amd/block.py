@@ -31,10 +31,12 @@ import torch
 from . import _lib as L
 
 Weight = Tuple[torch.Tensor, torch.Tensor]
+Rows8 = Tuple[torch.Tensor, torch.Tensor]  # codes [T,C] uint8, scales [T,ceil(C/128)] float32
 
 _ACT = {"silu": L.ACT_SILU, "gelu": L.ACT_GELU}
 _CODE = {torch.float32: L.F32, torch.bfloat16: L.BF16, torch.float16: L.F16}
 _HALF = (torch.bfloat16, torch.float16)
+_SCALE = {"amax": L.SCALE_AMAX, "pow2": L.SCALE_POW2}
 
 
 def _fail(msg: str):
@@ -107,6 +109,16 @@ def _empty(like: torch.Tensor, *shape: int) -> torch.Tensor:
 
 def _scratch(like: torch.Tensor, nbytes: int) -> Optional[torch.Tensor]:
     return like.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
+
+
+def _empty8(like: torch.Tensor, T: int, C: int) -> Rows8:
+    return like.new_empty((T, C), dtype=torch.uint8), like.new_empty((T, -(-C // 128)), dtype=torch.float32)
+
+
+def _scale_rule(name: str, what: str) -> int:
+    if name not in _SCALE:
+        _fail(f"{what}: scale_rule {name!r}, expected one of {', '.join(_SCALE)}")
+    return _SCALE[name]
 
 
 def ffn_forward(x: torch.Tensor, w_gate: Weight, w_up: Weight, w_down: Weight,
@@ -247,6 +259,25 @@ def norm_join(y: Optional[torch.Tensor], res: torch.Tensor, w_post: Optional[tor
     z, n = res.new_empty((T, C)), res.new_empty((T, C), dtype=rows)
     L._check(L.lib.fp8z1_norm_join(f, py, pr, wpost, pg, wpre, z.data_ptr(), n.data_ptr(), L._current_stream(dev)), what)
     return z, n
+
+
+def norm_join8(y: Optional[torch.Tensor], res: torch.Tensor, w_post: Optional[torch.Tensor] = None,
+               gate: Optional[torch.Tensor] = None, w_pre: Optional[torch.Tensor] = None, eps: float = 1e-6,
+               res_scale: float = 1.0, block_scale: float = 1.0, weight_offset: float = 0.0,
+               dtype: Optional[torch.dtype] = None, keep: bool = False, scale_rule: str = "amax"):
+    """(z, n, (codes, scales)): norm_join with n in 8 bits, a scale for every 128 columns of a row; n itself
+    (for a weight gradient) with ``keep``, else None.  Its gradients are norm_join_backward's."""
+    what = "norm_join8"
+    rows = y.dtype if y is not None else dtype or res.dtype
+    dev, T, C, f, wpost, pg, wpre = _norm(rows, res, w_post, gate, w_pre, (eps, res_scale, block_scale, weight_offset),
+                                          what)
+    py = None if y is None else _check(y, dev, rows, (T, C), what)
+    pr = _check(res, dev, res.dtype, (T, C), what)
+    z, n = res.new_empty((T, C)), res.new_empty((T, C), dtype=rows) if keep else None
+    codes, scales = _empty8(res, T, C)
+    L._check(L.lib.fp8z1_norm_join8(f, py, pr, wpost, pg, wpre, z.data_ptr(), L._ptr(n), codes.data_ptr(),
+                                    scales.data_ptr(), _scale_rule(scale_rule, what), L._current_stream(dev)), what)
+    return z, n, (codes, scales)
 
 
 def norm_join_backward(dz: Optional[torch.Tensor], dn: Optional[torch.Tensor], y: Optional[torch.Tensor],

@@ -20,6 +20,8 @@
 #include "ffn_refuse.h"
 #include "mfma.h"
 #include "norm_plan.h"
+#include "rows.h"
+#include "rows8.h"
 
 namespace fp8z1 {
 namespace {
@@ -28,6 +30,9 @@ struct NormArgs {
   const void *y, *res, *gate;  // backward: res is the kept z
   const float *w_post, *w_pre;
   void *z, *n;  // forward outputs
+  uint8_t* codes;  // n in 8 bits, and its scales [T][groups of 128]
+  float* scales;
+  int32_t pow2;
   // backward
   const void *dz, *dn;
   void *dy, *dres, *dgate;
@@ -37,126 +42,6 @@ struct NormArgs {
   int32_t waves;  // per row (backward)
   float eps, res_scale, block_scale, offset;
 };
-
-struct F32 {
-  static __device__ __forceinline__ float to_f32(float x) { return x; }
-  static __device__ __forceinline__ float from_f32(float x) { return x; }
-};
-template <class H>
-struct Elem {
-  typedef uint16_t type;
-};
-template <>
-struct Elem<F32> {
-  typedef float type;
-};
-
-// 8 consecutive elements of a row from column c, in 16-byte accesses at any
-// alignment of the elements (gfx950 runs in unaligned-access mode); those past the end
-// are 0 and not stored.
-typedef uint32_t v4u_a2_global_t __attribute__((ext_vector_type(4), aligned(2), address_space(1)));
-
-// the elements as they lie in memory (so that a row can be on its way while the row before it
-// is computed), and their values
-template <class H>
-struct Raw8 {
-  v4u_v_t x[sizeof(typename Elem<H>::type) * 8 / 16];
-};
-
-template <class H>
-__device__ __forceinline__ Raw8<H> fetch8(const void* row, int32_t C, int32_t c) {
-  typedef typename Elem<H>::type E;
-  constexpr int kVecs = sizeof(E) * 8 / 16;
-  const E* p = static_cast<const E*>(row) + c;
-  Raw8<H> r;
-#pragma unroll
-  for (int i = 0; i < kVecs; ++i) r.x[i] = v4u_v_t{0u, 0u, 0u, 0u};
-  if (c + 8 <= C) {
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) r.x[i] = ((const v4u_a2_global_t*)(p))[i];
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c + i < C) {
-        if constexpr (sizeof(E) == 2)
-          r.x[0][i / 2] |= static_cast<uint32_t>(p[i]) << (16 * (i % 2));
-        else
-          r.x[i / 4][i % 4] = __float_as_uint(p[i]);
-      }
-  }
-  return r;
-}
-
-template <class H>
-__device__ __forceinline__ void widen8f(const Raw8<H>& r, float (&v)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if constexpr (sizeof(typename Elem<H>::type) == 2)
-      v[i] = H::to_f32(static_cast<uint16_t>(r.x[0][i / 2] >> (16 * (i % 2))));
-    else
-      v[i] = __uint_as_float(r.x[i / 4][i % 4]);
-  }
-}
-
-template <class H>
-__device__ __forceinline__ void load8(const void* row, int32_t C, int32_t c, float (&v)[8]) {
-  widen8f<H>(fetch8<H>(row, C, c), v);
-}
-
-// STREAM: with the non-temporal hint (where: see launch_join)
-template <class H, bool STREAM = false>
-__device__ __forceinline__ void store8(void* row, int32_t C, int32_t c, const float (&v)[8]) {
-  typedef typename Elem<H>::type E;
-  constexpr int kVecs = sizeof(E) * 8 / 16;
-  E* p = static_cast<E*>(row) + c;
-  if (c + 8 <= C) {
-    v4u_v_t x[kVecs];
-    if (sizeof(E) == 2) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        x[0][i] = static_cast<uint32_t>(H::from_f32(v[2 * i])) | static_cast<uint32_t>(H::from_f32(v[2 * i + 1])) << 16;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[(i / 4) % kVecs][i % 4] = __float_as_uint(v[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      if (STREAM)
-        __builtin_nontemporal_store(x[i], (v4u_a2_global_t*)(p) + i);
-      else
-        ((v4u_a2_global_t*)(p))[i] = x[i];
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c + i < C) p[i] = H::from_f32(v[i]);
-  }
-}
-
-template <class H>
-__device__ __forceinline__ const void* row_of(const void* p, int64_t row, int32_t C) {
-  return static_cast<const typename Elem<H>::type*>(p) + row * C;
-}
-template <class H>
-__device__ __forceinline__ void* row_of(void* p, int64_t row, int32_t C) {
-  return static_cast<typename Elem<H>::type*>(p) + row * C;
-}
-
-// Sum over the wave, the same in every lane: pairs, fours, eights and sixteens by lane
-// permutations within the vector unit, the last two steps through LDS.
-template <int CTRL>
-__device__ __forceinline__ float permuted(float v) {
-  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
-}
-__device__ __forceinline__ float wave_fsum(float v) {
-  v += permuted<0xb1>(v);   // lanes 1 0 3 2 of each four
-  v += permuted<0x4e>(v);   // lanes 2 3 0 1 of each four
-  v += permuted<0x141>(v);  // each eight mirrored
-  v += permuted<0x140>(v);  // each sixteen mirrored
-  v += __shfl_xor(v, 16);
-  v += __shfl_xor(v, 32);
-  return v;
-}
 
 // Sums of N values over the `waves` waves of a row, in a fixed order; every thread of the row
 // gets them.  A workgroup may hold several rows, each with its own consecutive waves.
@@ -211,7 +96,31 @@ __device__ __forceinline__ void load_gate(const NormArgs& a, int64_t row, int32_
   for (int i = 0; i < 8; ++i) g[i] *= a.block_scale;
 }
 
-template <class H, class R, int CH, bool STREAM>
+// n in 8 bits: 16 neighbouring threads hold a group of 128 columns, whose largest magnitude they find by
+// lane permutations (NaN are passed over: they are NaN as codes).
+typedef uint32_t v2u_a1_global_t __attribute__((ext_vector_type(2), aligned(1), address_space(1)));
+__device__ __forceinline__ void store_codes(const NormArgs& a, int64_t row, int32_t c, const float (&n)[8]) {
+  float top = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = fmaxf(top, c + i < a.C ? fabsf(n[i]) : 0.0f);
+  top = fmaxf(top, permuted<0xb1>(top));
+  top = fmaxf(top, permuted<0x4e>(top));
+  top = fmaxf(top, permuted<0x141>(top));
+  top = fmaxf(top, permuted<0x140>(top));
+  if (c >= a.C) return;
+  const float scale = row8_scale(top, a.pow2 != 0);
+  if (c % kB == 0) a.scales[row * ((a.C + kB - 1) / kB) + c / kB] = scale;
+  const uint32_t lo = codes4(n[0], n[1], n[2], n[3], scale), hi = codes4(n[4], n[5], n[6], n[7], scale);
+  uint8_t* const to = a.codes + row * a.C + c;
+  if (c + 8 <= a.C) {
+    *(v2u_a1_global_t*)(to) = v2u_t{lo, hi};
+  } else {
+    for (int i = 0; i < 8; ++i)
+      if (c + i < a.C) to[i] = static_cast<uint8_t>((i < 4 ? lo : hi) >> (8 * (i & 3)));
+  }
+}
+
+template <class H, class R, int CH, bool STREAM, bool EIGHT>
 __global__ __launch_bounds__(1024) void norm_join_kernel(NormArgs a) {
   __shared__ float lds[2][16];
   constexpr bool kHold = CH == 1;  // weights kept in registers over the rows
@@ -257,17 +166,18 @@ __global__ __launch_bounds__(1024) void norm_join_kernel(NormArgs a) {
       }
       if (a.z) store8<R, STREAM>(row_of<R>(a.z, row, a.C), a.C, col(ch), z[ch]);
     }
-    if (a.n) {
+    if (a.n || EIGHT) {
       row_sums<1>(sum, lds[1], waves);
       r = rstd_of(sum[0], a.C, a.eps);
 #pragma unroll
       for (int ch = 0; ch < CH; ++ch) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) z[ch][i] = z[ch][i] * r * wpre[ch][i];
-        store8<H, STREAM>(row_of<H>(a.n, row, a.C), a.C, col(ch), z[ch]);
+        if (!EIGHT || a.n) store8<H, STREAM>(row_of<H>(a.n, row, a.C), a.C, col(ch), z[ch]);
+        if (EIGHT) store_codes(a, row, col(ch), z[ch]);
       }
     }
-    if (!(a.w_post && a.n)) __syncthreads();  // only one of the two LDS sets is used per row
+    if (!(a.w_post && (a.n || EIGHT))) __syncthreads();  // only one of the two LDS sets is used per row
   }
 }
 
@@ -559,19 +469,19 @@ bool rows_aligned(const NormArgs& a) {
 // its stores to others: 512 x 7168 11.1 and 12.7, 8192 x 7168 121 and 120, x 8192 144 and 137.)  The backward
 // pass stores without (221 and 211).
 constexpr int64_t kHalfOfL2 = kXcds * (4LL << 20) / 2;
-template <class H, class R>
+template <class H, class R, bool EIGHT>
 void launch_join(const NormArgs& a, dim3 g, dim3 b, hipStream_t s) {
-  const int64_t bytes =
-      static_cast<int64_t>(a.T) * a.C * (sizeof(typename Elem<H>::type) + sizeof(typename Elem<R>::type));
+  const int64_t n = EIGHT && !a.n ? 0 : sizeof(typename Elem<H>::type);
+  const int64_t bytes = static_cast<int64_t>(a.T) * a.C * (n + EIGHT + sizeof(typename Elem<R>::type));
   const bool one = a.C <= 8192, hint = bytes <= kHalfOfL2;
   if (one && hint)
-    hipLaunchKernelGGL((norm_join_kernel<H, R, 1, true>), g, b, 0, s, a);
+    hipLaunchKernelGGL((norm_join_kernel<H, R, 1, true, EIGHT>), g, b, 0, s, a);
   else if (one)
-    hipLaunchKernelGGL((norm_join_kernel<H, R, 1, false>), g, b, 0, s, a);
+    hipLaunchKernelGGL((norm_join_kernel<H, R, 1, false, EIGHT>), g, b, 0, s, a);
   else if (hint)
-    hipLaunchKernelGGL((norm_join_kernel<H, R, 2, true>), g, b, 0, s, a);
+    hipLaunchKernelGGL((norm_join_kernel<H, R, 2, true, EIGHT>), g, b, 0, s, a);
   else
-    hipLaunchKernelGGL((norm_join_kernel<H, R, 2, false>), g, b, 0, s, a);
+    hipLaunchKernelGGL((norm_join_kernel<H, R, 2, false, EIGHT>), g, b, 0, s, a);
 }
 
 template <class H, class R, bool BWD>
@@ -586,8 +496,10 @@ void launch_typed(const NormArgs& a, dim3 g, dim3 b, hipStream_t s) {
     hipLaunchKernelGGL((norm_join_bwd_kernel<H, R, 1, false>), g, b, 32 * b.x, s, a);
   else if (BWD)
     hipLaunchKernelGGL((norm_join_bwd_kernel<H, R, 2, false>), g, b, 0, s, a);
+  else if (a.codes)
+    launch_join<H, R, true>(a, g, b, s);
   else
-    launch_join<H, R>(a, g, b, s);
+    launch_join<H, R, false>(a, g, b, s);
 }
 
 template <bool BWD>
@@ -639,6 +551,28 @@ extern "C" int fp8z1_norm_join(const fp8z1_norm* f, const void* y, const void* r
   a.n = n;
   launch<false>(f, a, norm_fwd_groups(f->T, f->C), 1, static_cast<hipStream_t>(stream));
   return launched("norm_join");
+}
+
+extern "C" int fp8z1_norm_join8(const fp8z1_norm* f, const void* y, const void* res, const float* w_post,
+                                const void* gate, const float* w_pre, void* z, void* n, uint8_t* codes, float* scales,
+                                int32_t scale_rule, void* stream) {
+  const char* what = "norm_join8";
+  int rc = check_norm(f, y, w_post, gate, what);
+  if (rc) return rc;
+  if (scale_rule != FP8Z1_SCALE_AMAX && scale_rule != FP8Z1_SCALE_POW2)
+    return refuse(FP8Z1_EINVAL, what, "scale_rule must be FP8Z1_SCALE_AMAX or FP8Z1_SCALE_POW2");
+  if (f->T == 0) return FP8Z1_OK;
+  if (!res || !codes || !scales) return refuse(FP8Z1_EINVAL, what, "NULL argument");
+  rc = check_alignment(f, {y, n}, {res, z}, {w_post, w_pre, scales}, {gate}, what);
+  if (rc) return rc;
+  NormArgs a = base_args(f, y, res, w_post, gate, w_pre);
+  a.z = z;
+  a.n = n;
+  a.codes = codes;
+  a.scales = scales;
+  a.pow2 = scale_rule == FP8Z1_SCALE_POW2;
+  launch<false>(f, a, norm_fwd_groups(f->T, f->C), 1, static_cast<hipStream_t>(stream));
+  return launched(what);
 }
 
 extern "C" int fp8z1_norm_join_bwd_workspace_bytes(const fp8z1_norm* f, size_t* bytes) {

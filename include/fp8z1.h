@@ -432,6 +432,82 @@ int fp8z1_norm_join_bwd(const fp8z1_norm* f, const void* dz, const void* dn, con
                         float* dw_post, void* dgate, float* dw_pre, void* d_workspace, size_t workspace_bytes,
                         void* stream);
 
+/* fp8z1_norm_join with n in 8 bits: codes [T,C] (at any alignment) and scales [T, ceil(C/128)] float32, one scale for
+ * every 128 columns of a row, by `scale_rule` (FP8Z1_SCALE_*) from the group's largest magnitude as for the blocks
+ * of the weights, but not below 2^-126.  A code is the float32 n over its scale, rounded once (n is not rounded to 16 bits
+ * before).  NaN stay NaN; the group of an infinite n gets an infinite scale, with which all it stands for is NaN.
+ * z or n (in dtype, for a weight gradient) may be NULL if it is not wanted.  Its gradient is that of
+ * fp8z1_norm_join: the rounding to 8 bits passes dn through. */
+int fp8z1_norm_join8(const fp8z1_norm* f, const void* y, const void* res, const float* w_post, const void* gate,
+                     const float* w_pre, void* z, void* n, uint8_t* codes, float* scales, int32_t scale_rule, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The router, and tokens sorted by expert and back.  No call allocates or waits; all may be captured into a HIP
+ * graph.  Results do not depend on the order in which anything runs. */
+
+#define FP8Z1_SCORE_SOFTMAX 0 /* p_e = exp(l_e) / sum over all experts of exp(l) */
+#define FP8Z1_SCORE_SIGMOID 1 /* p_e = 1 / (1 + exp(-l_e)) */
+
+#define FP8Z1_ROUTE_MAX_EXPERTS 1024
+#define FP8Z1_ROUTE_MAX_CHOICES 32
+
+typedef struct {
+  int64_t T;         /* tokens */
+  int32_t E, k;      /* experts; choices of a token, at most E */
+  int32_t dtype;     /* logits and their gradient: FP8Z1_BF16, FP8Z1_F16 or FP8Z1_F32 */
+  int32_t score;     /* FP8Z1_SCORE_* */
+  int32_t normalize; /* nonzero: the chosen scores are divided by their sum */
+  float scale;       /* multiplies the weights */
+} fp8z1_router;
+
+/* From logits [T,E]: experts [T,k] int32, the k experts of the largest p_e + bias_e (bias float32 [E]; NULL: of
+ * the largest logits), largest first, the lowest index among equals, and their weights [T,k] float32, scale p_e or scale p_e / (sum of
+ * the chosen p).  The bias decides the choice only.  Ranks are compared in 64 bits.
+ * An expert with a logit of -inf or NaN is not chosen; where fewer than k are left, the other choices are expert -1
+ * with weight 0.  A row of softmax logits that holds a NaN or +inf has NaN weights.  No logit's size makes
+ * normalized weights overflow or vanish. */
+int fp8z1_route(const fp8z1_router* f, const void* logits, const float* bias, int32_t* experts, float* weights,
+                void* stream);
+
+/* The logits' gradient [T,E] (dtype) from that of the weights, dweights [T,k] float32; experts as fp8z1_route
+ * wrote them (choices outside 0..E-1 have no gradient). */
+int fp8z1_route_bwd(const fp8z1_router* f, const void* logits, const int32_t* experts, const float* dweights,
+                    void* dlogits, void* stream);
+
+/* The plan of the sorted rows, from experts [T,k] (T k at most 2^30): offsets [E+1], each expert's first row and at the end
+ * their number, and row_of [T,k], the row of each choice; an expert's rows are in the order of
+ * the choices.  A choice outside 0..E-1 gets row -1 and no place.  All int32.  Needs
+ * fp8z1_sort_tokens_workspace_bytes() bytes of device workspace (16-byte aligned; 0 for few choices). */
+int fp8z1_sort_tokens_workspace_bytes(int64_t T, int32_t k, int32_t E, size_t* bytes);
+int fp8z1_sort_tokens(int64_t T, int32_t k, int32_t E, const int32_t* experts, int32_t* offsets, int32_t* row_of,
+                      void* d_workspace, size_t workspace_bytes, void* stream);
+
+typedef struct {
+  int64_t T;     /* tokens */
+  int64_t D;     /* width */
+  int64_t R;     /* rows that the buffer of sorted rows has */
+  int32_t k;     /* choices of a token */
+  int32_t dtype; /* of tokens and rows: FP8Z1_BF16, FP8Z1_F16 or FP8Z1_F32; dispatch also FP8Z1_E4M3 */
+} fp8z1_routed;
+
+/* rows [R,D]: row row_of[t][j] = x[t], for x [T,D].  Choices whose row is not among 0..R-1 are left out, here and
+ * below, and rows that no choice has stay as they were; no row may be that of two choices.
+ * FP8Z1_E4M3: x and rows are codes, and scales [T, ceil(D/128)] go to row_scales [R, ceil(D/128)] with them;
+ * otherwise both are NULL. */
+int fp8z1_dispatch(const fp8z1_routed* f, const int32_t* row_of, const void* x, const float* scales, void* rows,
+                   float* row_scales, void* stream);
+
+/* y [T,D] = base + sum over j of weights[t][j] rows[row_of[t][j]], summed in float32 in the order of j and
+ * rounded once.  weights float32 [T,k], or NULL: 1 (the gradient of fp8z1_dispatch).  base [T,D] or NULL: 0; y may be
+ * base itself. */
+int fp8z1_combine(const fp8z1_routed* f, const int32_t* row_of, const void* rows, const float* weights, const void* base,
+                  void* y, void* stream);
+
+/* Its gradients from dy [T,D]: drows, row row_of[t][j] = weights[t][j] dy[t] (other rows stay as they were), and dweights
+ * [T,k] float32 = <dy[t], rows[row_of[t][j]]> (0 where there is no row); one of them may be NULL.  (base has dy.) */
+int fp8z1_combine_bwd(const fp8z1_routed* f, const int32_t* row_of, const void* dy, const void* rows,
+                      const float* weights, void* drows, float* dweights, void* stream);
+
 /* Copy the device state to the host (synchronizes the stream) / from the host
  * (resume from a checkpoint). */
 int fp8z1_state_read(const fp8z1_state* d_state, fp8z1_state* out, void* stream);
