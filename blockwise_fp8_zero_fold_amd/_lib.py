@@ -22,7 +22,7 @@ SPLIT_BLOCK, SPLIT_PARAM = 0, 1
 STAT_PARTS = 4  # float64 partial sums of squares per slot
 NOALLOC_MAX_SLOTS = 262144  # largest table fp8z1_step_rowmajor_noalloc takes
 ALL_RANKS = -1
-ACT_SILU, ACT_GELU = 0, 1
+ACT_SILU, ACT_GELU, ACT_NONE = 0, 1, 2
 GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL = 0, 1, 2, 3
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 ROUTE_MAX_EXPERTS, ROUTE_MAX_CHOICES = 1024, 32
@@ -100,6 +100,12 @@ class Norm(C.Structure):
                 ("weight_offset", C.c_float), ("reserved", C.c_int32)]
 
 
+class Product(C.Structure):
+    """A product with one weight: T rows, E experts, widths N (y) and K (x)."""
+    _fields_ = [("T", C.c_int64), ("E", C.c_int64), ("N", C.c_int64), ("K", C.c_int64), ("dtype", C.c_int32),
+                ("x_dtype", C.c_int32), ("act", C.c_int32), ("reserved", C.c_int32)]
+
+
 class Router(C.Structure):
     """The router's sizes and settings."""
     _fields_ = [("T", C.c_int64), ("E", C.c_int32), ("k", C.c_int32), ("dtype", C.c_int32), ("score", C.c_int32),
@@ -112,7 +118,8 @@ class Routed(C.Structure):
 
 
 assert C.sizeof(Block) == 16 and C.sizeof(State) == 64 and C.sizeof(Hparams) == 72
-assert C.sizeof(Ffn) == 40 and C.sizeof(Norm) == 48 and C.sizeof(Router) == 32 and C.sizeof(Routed) == 32
+assert C.sizeof(Ffn) == 40 and C.sizeof(Norm) == 48 and C.sizeof(Product) == 48
+assert C.sizeof(Router) == 32 and C.sizeof(Routed) == 32
 
 _vp = C.c_void_p
 _sig = {
@@ -152,6 +159,12 @@ _sig = {
     "fp8z1_norm_join_bwd_workspace_bytes": (C.c_int, [C.POINTER(Norm), C.POINTER(C.c_size_t)]),
     "fp8z1_norm_join_bwd": (C.c_int, [C.POINTER(Norm), *[_vp] * 13, C.c_size_t, _vp]),
     "fp8z1_norm_join8": (C.c_int, [C.POINTER(Norm), *[_vp] * 9, C.c_int32, _vp]),
+    "fp8z1_linear_workspace_bytes": (C.c_int, [C.POINTER(Product), C.POINTER(C.c_size_t)]),
+    "fp8z1_linear": (C.c_int, [C.POINTER(Product), *[_vp] * 10, C.c_size_t, _vp]),
+    "fp8z1_linear_bwd_workspace_bytes": (C.c_int, [C.POINTER(Product), C.POINTER(C.c_size_t)]),
+    "fp8z1_linear_bwd": (C.c_int, [C.POINTER(Product), *[_vp] * 9, C.c_size_t, _vp]),
+    "fp8z1_ffn_up8_workspace_bytes": (C.c_int, [C.POINTER(Ffn), C.POINTER(C.c_size_t)]),
+    "fp8z1_ffn_up8": (C.c_int, [C.POINTER(Ffn), *[_vp] * 11, C.c_int32, _vp, C.c_size_t, _vp]),
     "fp8z1_route": (C.c_int, [C.POINTER(Router), *[_vp] * 5]),
     "fp8z1_route_bwd": (C.c_int, [C.POINTER(Router), *[_vp] * 5]),
     "fp8z1_sort_tokens_workspace_bytes": (C.c_int, [C.c_int64, C.c_int32, C.c_int32, C.POINTER(C.c_size_t)]),
@@ -603,6 +616,76 @@ def _need_rows8(rows: int, width: int, what: str, codes, scales) -> None:
         _need(codes, rows * width, f"{what} codes", torch.uint8)
     if scales is not None:
         _need(scales, rows * (-(-width // 128)) * 4, f"{what} scales", torch.float32)
+
+
+def _need_product(f: Product, what: str, out=(), wide=(), bias=()) -> None:
+    for xs, width in ((out, f.N), (wide, f.K)):
+        for x in xs:
+            if x is not None:
+                _need(x, f.T * width * 2, what, _torch_dtype(f.dtype))
+    for x in bias:
+        if x is not None:
+            _need(x, 4 * f.E * f.N, f"{what} bias", torch.float32)
+
+
+def fp8z1_linear_workspace_bytes(f: Product) -> int:
+    n = C.c_size_t()
+    _check(lib.fp8z1_linear_workspace_bytes(C.byref(f), C.byref(n)), "fp8z1_linear_workspace_bytes")
+    return n.value
+
+
+def fp8z1_linear(f: Product, x, x_scales, codes, scales, offsets, bias, res, y, p=None, workspace=None,
+                 workspace_bytes: int = 0, stream=None) -> None:
+    """y = res + act(x W^T + bias); p keeps x W^T + bias."""
+    workspace_bytes = _workspace(workspace, workspace_bytes, "linear")
+    eight = f.x_dtype == E4M3
+    _need_product(f, "linear", (res, y, p), () if eight else (x,), (bias,))
+    if eight:
+        _need_rows8(f.T, f.K, "linear", x, x_scales)
+    _need_weights(f, "linear", f.N, f.K, (codes, scales))
+    _need_offsets(offsets, f.E, "linear")
+    _check(lib.fp8z1_linear(C.byref(f), _ptr(x), _ptr(x_scales), _ptr(codes), _ptr(scales), _ptr(offsets), _ptr(bias),
+                            _ptr(res), _ptr(y), _ptr(p), _ptr(workspace), workspace_bytes, _stream(stream)),
+           "fp8z1_linear")
+
+
+def fp8z1_linear_bwd_workspace_bytes(f: Product) -> int:
+    n = C.c_size_t()
+    _check(lib.fp8z1_linear_bwd_workspace_bytes(C.byref(f), C.byref(n)), "fp8z1_linear_bwd_workspace_bytes")
+    return n.value
+
+
+def fp8z1_linear_bwd(f: Product, dy, p, codes, scales, offsets, dp, dbias, dx, workspace=None, workspace_bytes: int = 0,
+                     stream=None) -> None:
+    """dp = dy act'(p), its sums dbias, and dx = dp W; those that are None are not computed."""
+    workspace_bytes = _workspace(workspace, workspace_bytes, "linear_bwd")
+    _need_product(f, "linear_bwd", (dy, p, dp), (dx,), (dbias,))
+    if codes is not None:
+        _need_weights(f, "linear_bwd", f.N, f.K, (codes, scales))
+    _need_offsets(offsets, f.E, "linear_bwd")
+    _check(lib.fp8z1_linear_bwd(C.byref(f), _ptr(dy), _ptr(p), _ptr(codes), _ptr(scales), _ptr(offsets), _ptr(dp),
+                                _ptr(dbias), _ptr(dx), _ptr(workspace), workspace_bytes, _stream(stream)),
+           "fp8z1_linear_bwd")
+
+
+def fp8z1_ffn_up8_workspace_bytes(f: Ffn) -> int:
+    n = C.c_size_t()
+    _check(lib.fp8z1_ffn_up8_workspace_bytes(C.byref(f), C.byref(n)), "fp8z1_ffn_up8_workspace_bytes")
+    return n.value
+
+
+def fp8z1_ffn_up8(f: Ffn, x, x_scales, gate_codes, gate_scales, up_codes, up_scales, offsets, h, u, a, a_scales,
+                  scale_rule: int = SCALE_AMAX, workspace=None, workspace_bytes: int = 0, stream=None) -> None:
+    """a = act(x Wg^T) * (x Wu^T), x and a in 8 bits; h and u keep the projections (both or neither None)."""
+    workspace_bytes = _workspace(workspace, workspace_bytes, "ffn_up8")
+    _need_rows8(f.T, f.D, "ffn_up8 x", x, x_scales)
+    _need_rows8(f.T, f.F, "ffn_up8 a", a, a_scales)
+    _need_rows(f, "ffn_up8", h=(h, f.F), u=(u, f.F))
+    _need_weights(f, "ffn_up8", f.F, f.D, (gate_codes, gate_scales), (up_codes, up_scales))
+    _need_offsets(offsets, f.E, "ffn_up8")
+    _check(lib.fp8z1_ffn_up8(C.byref(f), _ptr(x), _ptr(x_scales), _ptr(gate_codes), _ptr(gate_scales), _ptr(up_codes),
+                             _ptr(up_scales), _ptr(offsets), _ptr(h), _ptr(u), _ptr(a), _ptr(a_scales), scale_rule,
+                             _ptr(workspace), workspace_bytes, _stream(stream)), "fp8z1_ffn_up8")
 
 
 def _need_router(f: Router, what: str, logits=(), bias=None, choices=(), weights=()) -> None:

@@ -24,7 +24,7 @@ A training step over one block (see ``examples/train_ffn_layer.py``):
 from __future__ import annotations
 
 import functools
-from typing import Dict, Optional, Sequence, Tuple
+from typing import Dict, Optional, Sequence, Tuple, Union
 
 import torch
 
@@ -214,6 +214,129 @@ def ffn_backward_weights(x: torch.Tensor, a: torch.Tensor, dy: torch.Tensor, dh:
                                          dw[0].data_ptr(), dw[1].data_ptr(), dw[2].data_ptr(), int(out is not None),
                                          L._ptr(ws), n, L._current_stream(dev)), what)
     return dw
+
+
+@functools.lru_cache(maxsize=256)
+def _linear_workspace(T: int, E: int, N: int, K: int, eight: bool) -> int:
+    return L.fp8z1_linear_workspace_bytes(L.Product(T, E, N, K, L.BF16, L.E4M3 if eight else L.BF16, L.ACT_NONE, 0))
+
+
+@functools.lru_cache(maxsize=256)
+def _linear_bwd_workspace(T: int, E: int, N: int, K: int) -> int:
+    return L.fp8z1_linear_bwd_workspace_bytes(L.Product(T, E, N, K, L.BF16, L.BF16, L.ACT_NONE, 0))
+
+
+@functools.lru_cache(maxsize=256)
+def _up8_workspace(T: int, E: int, D: int, F: int) -> int:
+    return L.fp8z1_ffn_up8_workspace_bytes(L.Ffn(T, E, D, F, L.BF16, L.ACT_SILU))
+
+
+def _rows8(x: Rows8, dev: int, T: int, C: int, what: str) -> Tuple[int, int]:
+    return (_check(x[0], dev, torch.uint8, (T, C), what),
+            _check(x[1], dev, torch.float32, (T, -(-C // 128)), f"{what} scales"))
+
+
+def _linear_act(act: Optional[str], what: str) -> int:
+    if act is not None and act not in _ACT:
+        _fail(f"{what}: act {act!r}, expected None or one of {', '.join(_ACT)}")
+    return L.ACT_NONE if act is None else _ACT[act]
+
+
+def _half(dtype: Optional[torch.dtype], what: str) -> torch.dtype:
+    if dtype not in _HALF:
+        _fail(f"{what}: dtype {dtype}, expected torch.bfloat16 or torch.float16")
+    return dtype
+
+
+def linear(x: Union[torch.Tensor, Rows8], w: Weight, offsets: Optional[torch.Tensor] = None,
+           bias: Optional[torch.Tensor] = None, act: Optional[str] = None, res: Optional[torch.Tensor] = None,
+           save: bool = False, dtype: Optional[torch.dtype] = None):
+    """(y, p): y [T,N] = res + act(p), p = x W^T + bias, codes [E,N,K].  x is [T,K] in 16 bits, or a pair (codes,
+    scales) in 8; bias float32 [E,N] (one expert: or [N]).  p is None unless ``save``.
+    ``dtype`` (of y, p and res): x's own, for 8-bit rows that of res or bfloat16 unless it is given."""
+    what = "linear"
+    eight = isinstance(x, tuple)
+    rows = x[0] if eight else x
+    if rows.dim() != 2 or w[0].dim() != 3:
+        _fail(f"{what}: rows must be [T, K] and codes [E, N, K]")
+    if eight:
+        dtype = _half(dtype or (res.dtype if res is not None else torch.bfloat16), what)
+    elif dtype not in (None, rows.dtype) or rows.dtype not in _HALF:
+        _fail(f"{what}: rows of {rows.dtype} for dtype {dtype}, expected torch.bfloat16 or torch.float16, both alike")
+    else:
+        dtype = rows.dtype
+    dev, (T, K), (E, N, _) = _device(rows, what), rows.shape, w[0].shape
+    px, ps = _rows8(x, dev, T, K, what) if eight else (_check(rows, dev, dtype, (T, K), what), None)
+    pw = _weight(w, dev, E, N, K, f"{what} weight")
+    off = _offsets(offsets, dev, E, what)
+    pb = None if bias is None else _check(bias, dev, torch.float32, (E, N) if E > 1 or bias.dim() != 1 else (N,),
+                                          f"{what} bias")
+    pr = None if res is None else _check(res, dev, dtype, (T, N), f"{what} res")
+    y = rows.new_empty((T, N), dtype=dtype)
+    p = torch.empty_like(y) if save else None
+    f = L.Product(T, E, N, K, _CODE[dtype], L.E4M3 if eight else _CODE[dtype], _linear_act(act, what), 0)
+    n = _linear_workspace(T, E, N, K, eight)
+    ws = _scratch(rows, n)
+    L._check(L.lib.fp8z1_linear(f, px, ps, *pw, off, pb, pr, y.data_ptr(), L._ptr(p), L._ptr(ws), n,
+                                L._current_stream(dev)), what)
+    return y, p
+
+
+def linear_backward(dy: torch.Tensor, w: Weight, p: Optional[torch.Tensor] = None,
+                    offsets: Optional[torch.Tensor] = None, act: Optional[str] = None,
+                    bias: bool = False) -> Dict[str, Optional[torch.Tensor]]:
+    """{"dx" [T,K], "dp" [T,N], "dbias" [E,N] (with ``bias``)} from dy and, with an activation, the kept p.  Without one
+    dp is dy itself.  The weight gradient is ffn_weight_gradient(dp, x in 16 bits); res has the gradient dy."""
+    what = "linear_backward"
+    if dy.dim() != 2 or w[0].dim() != 3:
+        _fail(f"{what}: dy must be [T, N] and codes [E, N, K]")
+    dtype, kind = _half(dy.dtype, what), _linear_act(act, what)
+    dev, (T, N), (E, _, K) = _device(dy, what), dy.shape, w[0].shape
+    py = _check(dy, dev, dtype, (T, N), what)
+    if (p is None) != (act is None):
+        _fail(f"{what}: p is kept where there is an activation, and only there")
+    pp = None if p is None else _check(p, dev, dtype, (T, N), f"{what} p")
+    pw = _weight(w, dev, E, N, K, f"{what} weight")
+    off = _offsets(offsets, dev, E, what)
+    dp, dx = dy if p is None else torch.empty_like(dy), dy.new_empty((T, K))
+    dbias = dy.new_empty((E, N), dtype=torch.float32) if bias else None
+    f = L.Product(T, E, N, K, _CODE[dtype], _CODE[dtype], kind, 0)
+    n = _linear_bwd_workspace(T, E, N, K)
+    ws = _scratch(dy, n)
+    L._check(L.lib.fp8z1_linear_bwd(f, py, pp, *pw, off, None if p is None else dp.data_ptr(), L._ptr(dbias), dx.data_ptr(),
+                                    L._ptr(ws), n, L._current_stream(dev)), what)
+    return {"dx": dx, "dp": dp, "dbias": dbias}
+
+
+def ffn_up8(x: Rows8, w_gate: Weight, w_up: Weight, offsets: Optional[torch.Tensor] = None, act: str = "silu",
+            save: bool = False, dtype: torch.dtype = torch.bfloat16, scale_rule: str = "amax"):
+    """((codes [T,F], scales), (h, u)): a = act(x Wg^T) * (x Wu^T) of rows x in 8 bits, in 8 bits; h and u in ``dtype``
+    with ``save``, else None.  ``linear`` of a makes y."""
+    what = "ffn_up8"
+    if x[0].dim() != 2 or w_gate[0].dim() != 3:
+        _fail(f"{what}: rows must be [T, D] and codes [E, F, D]")
+    if act not in _ACT:
+        _fail(f"{what}: act {act!r}, expected one of {', '.join(_ACT)}")
+    dev, (T, D), (E, F, _) = _device(x[0], what), x[0].shape, w_gate[0].shape
+    px = _rows8(x, dev, T, D, what)
+    gate, up = (_weight(w, dev, E, F, D, f"{what} {n}") for w, n in ((w_gate, "gate"), (w_up, "up")))
+    off = _offsets(offsets, dev, E, what)
+    f = L.Ffn(T, E, D, F, _CODE[_half(dtype, what)], _ACT[act])
+    codes, scales = _empty8(x[0], T, F)
+    h, u = (x[0].new_empty((T, F), dtype=dtype) for _ in range(2)) if save else (None, None)
+    n = _up8_workspace(T, E, D, F)
+    ws = _scratch(x[0], n)
+    L._check(L.lib.fp8z1_ffn_up8(f, *px, *gate, *up, off, L._ptr(h), L._ptr(u), codes.data_ptr(), scales.data_ptr(),
+                                 _scale_rule(scale_rule, what), L._ptr(ws), n, L._current_stream(dev)), what)
+    return (codes, scales), ((h, u) if save else None)
+
+
+def ffn_forward8(x: Rows8, w_gate: Weight, w_up: Weight, w_down: Weight, offsets: Optional[torch.Tensor] = None,
+                 act: str = "silu", save: bool = False, dtype: torch.dtype = torch.bfloat16):
+    """(y [T,D], (h, u)): ffn_forward with x and a in 8 bits; y, h and u in ``dtype``.  The backward pass is
+    ffn_backward_data of h and u, and ffn_backward_weights of x in 16 bits and the a that it gives."""
+    a, kept = ffn_up8(x, w_gate, w_up, offsets, act, save, dtype)
+    return linear(a, w_down, offsets, dtype=dtype)[0], kept
 
 
 def _gate_kind(gate: Optional[torch.Tensor], T: int, C: int) -> int:

@@ -35,6 +35,9 @@ HIP_FLAGS = [
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wall", "-Wno-unused-function", "-Wno-unused-command-line-argument",
 ]
+# Results of matrix instructions in the vector registers that the next instructions read them from: the 8-bit
+# products add each block's sums there, and would move every one of them from the accumulation registers.
+FILE_FLAGS = {name: ["-mllvm", "-amdgpu-mfma-vgpr-form"] for name in ("linear8.hip", "ffn_up8.hip")}
 CXX_FLAGS = ["-O2", "-fPIC", "-std=c++17", "-Wall", "-Wextra"]
 
 
@@ -57,7 +60,7 @@ def build(verbose: bool = False) -> str:
     jobs = []
     for src in hip:
         obj = os.path.join(OBJ, os.path.basename(src) + ".o")
-        jobs.append([HIPCC, *HIP_FLAGS, "-c", src, "-o", obj])
+        jobs.append([HIPCC, *HIP_FLAGS, *FILE_FLAGS.get(os.path.basename(src), []), "-c", src, "-o", obj])
     for src in cpp:
         obj = os.path.join(OBJ, os.path.basename(src) + ".o")
         jobs.append([CXX, *CXX_FLAGS, "-c", src, "-o", obj])

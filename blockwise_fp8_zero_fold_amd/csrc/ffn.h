@@ -16,20 +16,32 @@ enum FfnKind {
   kFfnUp = 0,       // a = act(x Wg^T) * (x Wu^T)
   kFfnDown = 1,     // y = a Wd^T
   kFfnDownBwd = 2,  // da = dy Wd, then dh, du (and a) from da, h, u
-  kFfnUpBwd = 3     // dx = dh Wg + du Wu
+  kFfnUpBwd = 3,    // dx = dh Wg + du Wu
+  kLinear = 4,      // y = res + act(x W^T + bias)
+  kLinearBwd = 5    // dx = dp W
 };
 
 struct FfnArgs {
   const uint8_t *x0, *x1;  // 16-bit rows [T, K] (x1: du of kFfnUpBwd)
-  const uint8_t *w0, *w1;  // codes: [E, N, K] (kFfnUp, kFfnDown) or [E, K, N]
+  const uint8_t *w0, *w1;  // codes: [E, N, K] (forward) or [E, K, N]
   const float *s0, *s1;    // their block scales
   const int32_t* offsets;  // [E + 1], or NULL: one expert, all rows
   const uint16_t *h, *u;   // [T, N] inputs of kFfnDownBwd
   uint16_t *o0, *o1, *o2;  // outputs [T, N]
+  const float* bias;       // [E, N] (kLinear; NULL: 0)
+  const uint16_t* res;     // [T, N] (kLinear; NULL: 0)
+  const float* xs;         // x0 in 8 bits: its scales [T, blocks of K]
+  uint8_t* codes;          // kFfnUp of 8-bit rows: a in 8 bits [T, N]
+  float* code_scales;      // [T, blocks of N]
+  int32_t pow2;            // their rule
   float* part;             // partial sums of split tiles, or NULL: no tile is split
   int32_t T, E, N, K, act;
   int32_t split_from;  // sums of at least so many scale blocks may be split
 };
+
+// y = res + act(x W^T + bias) of rows in 8 bits (checked arguments), and the workspace that it can use
+int linear8(const FfnArgs& p, int32_t dtype, void* workspace, size_t workspace_bytes, hipStream_t s, const char* what);
+size_t linear8_workspace();
 
 // Rows of expert e, kept inside [0, T] whatever the offsets hold, so a wrong
 // offset gives wrong rows but no access out of bounds.
@@ -237,6 +249,8 @@ __device__ __forceinline__ float gelu_arg(float h) { return 1.5957691216057308f 
 __device__ __forceinline__ float act_value(int act, float h) {
   return h * logistic(act == FP8Z1_ACT_SILU ? h : gelu_arg(h));
 }
+// with FP8Z1_ACT_NONE too
+__device__ __forceinline__ float linear_act(int act, float h) { return act == FP8Z1_ACT_NONE ? h : act_value(act, h); }
 
 __device__ __forceinline__ void act_both(int act, float h, float& value, float& slope) {
   const float c = fminf(fmaxf(h, -1e4f), 1e4f);

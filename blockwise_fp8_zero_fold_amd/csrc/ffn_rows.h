@@ -142,6 +142,11 @@ __global__ __launch_bounds__(WAVES * 64) void ffn_rows_kernel(FfnArgs p) {
             p.o1[at] = H::from_f32(v[0][i]);
             p.o2[at] = H::from_f32(v[1][i]);
           }
+        } else if (KIND == kLinear) {
+          const float b = p.bias ? v[0][i] + p.bias[static_cast<int64_t>(e) * N + n] : v[0][i];
+          const float y = linear_act(p.act, b), r = p.res ? H::to_f32(p.res[at]) : 0.0f;
+          p.o0[at] = H::from_f32(p.res ? y + r : y);
+          if (p.o1) p.o1[at] = H::from_f32(b);
         } else {
           p.o0[at] = H::from_f32(v[0][i]);
         }

@@ -75,12 +75,34 @@ __device__ __forceinline__ Kept load_kept(const FfnArgs& p, int64_t at, int coun
   return k;
 }
 
+// y = res + act(x + bias) of 8 columns from column n of a row on, and x + bias (what the backward pass
+// needs) where it is wanted; both are rounded once.  `bias` is the expert's.
+template <class H>
+__device__ __forceinline__ void finish_linear(const FfnArgs& p, int64_t at, int32_t n, int count, const float (&x)[8]) {
+  uint32_t r[4] = {}, o[4], k[4];
+  float y[8], b[8];
+  if (p.res) load_row8(p.res + at, r, count);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    b[i] = p.bias && i < count ? x[i] + p.bias[n + i] : x[i];
+    y[i] = linear_act(p.act, b[i]);
+    if (p.res) y[i] += H::to_f32(static_cast<uint16_t>(r[i / 2] >> (16 * (i % 2))));
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    o[i] = static_cast<uint32_t>(H::from_f32(y[2 * i])) | static_cast<uint32_t>(H::from_f32(y[2 * i + 1])) << 16;
+    k[i] = static_cast<uint32_t>(H::from_f32(b[2 * i])) | static_cast<uint32_t>(H::from_f32(b[2 * i + 1])) << 16;
+  }
+  store_row8(p.o0 + at, o, count);
+  if (p.o1) store_row8(p.o1 + at, k, count);
+}
+
 // The results of 8 columns of a row, of which `count` are there (for kFfnUp x: gate, v: up).
 // Each is rounded once, from float32 to the activations' 16 bits, which is what the matrix instructions
 // of the next product take and what a training step keeps: a between up and down, dh and du before dx
 // (so y and dx lie 1.4 times as far from the 64-bit result as after a single rounding at their end).
 template <class H, int KIND>
-__device__ __forceinline__ void finish8(const FfnArgs& p, int64_t at, int count, const float (&x)[8],
+__device__ __forceinline__ void finish8(const FfnArgs& p, int64_t at, int32_t n, int count, const float (&x)[8],
                                         const float (&v)[8], const Kept& kept) {
   auto put = [&](const float (&f)[8], uint16_t* to) {
     uint32_t o[4];
@@ -114,6 +136,8 @@ __device__ __forceinline__ void finish8(const FfnArgs& p, int64_t at, int count,
     put(dh, p.o0);
     put(du, p.o1);
     if (p.o2) put(a, p.o2);
+  } else if (KIND == kLinear) {
+    finish_linear<H>(p, at, n, count, x);
   } else {
     put(x, p.o0);
   }
@@ -176,7 +200,7 @@ __device__ __forceinline__ void store_rows(const FfnArgs& p, const uint8_t* from
     float x[8], v[8] = {};
     read8(from, r, 2 * c, x);
     if (KIND == kFfnUp) read8(from, r, 8 + 2 * c, v);
-    finish8<H, KIND>(p, at, count, x, v, kept);
+    finish8<H, KIND>(p, at, n + 8 * c, count, x, v, kept);
     r = rn;
     count = cn;
     at = an;
@@ -228,7 +252,7 @@ __device__ __forceinline__ int swizzle_t(int r) {  // transposed reads, rows of 
 // sums each block apart and adds scale * sum, in a pass for each of its wave's tile columns.
 template <class H, int KIND, int NT, bool DIRECT>
 __global__ __launch_bounds__(kThreads, 2) void ffn_tile_kernel(FfnArgs p, int32_t ncols) {
-  constexpr bool kTrans = KIND == kFfnDownBwd || KIND == kFfnUpBwd;  // weights run along n
+  constexpr bool kTrans = KIND == kFfnDownBwd || KIND == kFfnUpBwd || KIND == kLinearBwd;  // weights run along n
   constexpr bool kUp = KIND == kFfnUp;
   constexpr int kB2 = NT * 64;                  // weight rows (or columns) of a stage
   constexpr int kCols = kUp ? kB2 / 2 : kB2;    // output columns of a tile
@@ -258,6 +282,7 @@ __global__ __launch_bounds__(kThreads, 2) void ffn_tile_kernel(FfnArgs p, int32_
   const int32_t q0 = blocks * sp / parts, q1 = blocks * (sp + 1) / parts;
   if (!find_tile<kRows>(p.offsets, p.T, p.E, ncols, rowtiles, first, id, e, lo, hi, m0, col)) return;
   const int32_t n0 = col * kCols;
+  if (KIND == kLinear && p.bias) p.bias += static_cast<int64_t>(e) * p.N;
   const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6), wm = w >> 1, wn = w & 1;
   const int32_t N = p.N, K = p.K;
   const int32_t nb = (N + kB - 1) / kB;
@@ -587,6 +612,7 @@ __global__ __launch_bounds__(kThreads) void ffn_join_kernel(FfnArgs p, int32_t n
   const int g = blockIdx.x & 1, i = (blockIdx.x >> 1) & 1, j = static_cast<int>(blockIdx.x >> 2) % kJ;
   const int t = threadIdx.x, lane = t & 63, w = t >> 6;
   if (!find_tile<kRows>(p.offsets, p.T, p.E, ncols, rowtiles, first, plan.whole + tile, e, lo, hi, m0, col)) return;
+  if (KIND == kLinear && p.bias) p.bias += static_cast<int64_t>(e) * p.N;
   const int32_t mw = m0 + (w >> 1) * 64 + i * 32;
   if (mw >= hi) return;  // (the parts of rows past the run were not written)
   const f32x4* const from = part_at<NT>(p.part, tile) + ((i * NT + j) * 4 + 2 * g) * kThreads + t;
@@ -616,7 +642,7 @@ __global__ __launch_bounds__(kThreads) void ffn_join_kernel(FfnArgs p, int32_t n
     exchange(x[k], x[4 + k]);
     if (kUp) exchange(v[k], v[4 + k]);
   }
-  finish8<H, KIND>(p, at, count, x, v, kept);
+  finish8<H, KIND>(p, at, n, count, x, v, kept);
 }
 
 // The most row tiles that T rows in E runs can make: every run may end in a partial tile.
@@ -651,7 +677,7 @@ template <int KIND>
 int launch(FfnArgs p, int32_t dtype, void* workspace, size_t workspace_bytes, hipStream_t s, const char* what) {
   if (p.T == 0) return FP8Z1_OK;
   if (misaligned(workspace, 16)) return refuse(FP8Z1_EINVAL, what, "misaligned workspace");
-  constexpr bool kTrans = KIND == kFfnDownBwd || KIND == kFfnUpBwd;
+  constexpr bool kTrans = KIND == kFfnDownBwd || KIND == kFfnUpBwd || KIND == kLinearBwd;
   const bool direct = !misaligned(p.x0, 4) && !misaligned(p.x1, 4) && !misaligned(p.w0, 4) && !misaligned(p.w1, 4) &&
                       (kTrans ? p.K % 2 == 0 && p.N % 4 == 0 : p.K % 4 == 0);
   // Few rows per expert (32 on average at most): the weights' read is what counts, and a tile of 128
@@ -695,6 +721,23 @@ int launch(FfnArgs p, int32_t dtype, void* workspace, size_t workspace_bytes, hi
 }
 
 bool misaligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
+
+int check_product(const fp8z1_product* f, const int32_t* offsets, const char* what) {
+  if (!f) return refuse(FP8Z1_EINVAL, what, "NULL description");
+  if (f->dtype != FP8Z1_BF16 && f->dtype != FP8Z1_F16)
+    return refuse(FP8Z1_EINVAL, what, "dtype must be FP8Z1_BF16 or FP8Z1_F16");
+  if (f->x_dtype != f->dtype && f->x_dtype != FP8Z1_E4M3)
+    return refuse(FP8Z1_EINVAL, what, "x_dtype must be dtype or FP8Z1_E4M3");
+  if (f->act != FP8Z1_ACT_SILU && f->act != FP8Z1_ACT_GELU && f->act != FP8Z1_ACT_NONE)
+    return refuse(FP8Z1_EINVAL, what, "act must be FP8Z1_ACT_SILU, FP8Z1_ACT_GELU or FP8Z1_ACT_NONE");
+  if (f->T < 0 || f->T > FP8Z1_FFN_MAX_ROWS) return refuse(FP8Z1_ESHAPE, what, "T outside 0 .. 2^30");
+  if (f->E < 1 || f->E > FP8Z1_FFN_MAX_EXPERTS) return refuse(FP8Z1_ESHAPE, what, "E outside 1 .. 65535");
+  if (f->N < 1 || f->N > FP8Z1_FFN_MAX_WIDTH || f->K < 1 || f->K > FP8Z1_FFN_MAX_WIDTH)
+    return refuse(FP8Z1_ESHAPE, what, "N and K must be 1 .. 2^20");
+  if (!offsets && f->E != 1) return refuse(FP8Z1_EINVAL, what, "offsets may be NULL for one expert only");
+  if (misaligned(offsets, 4)) return refuse(FP8Z1_EINVAL, what, "misaligned offsets");
+  return FP8Z1_OK;
+}
 
 int check_cfg(const fp8z1_ffn* f, const int32_t* offsets, const char* what) {
   if (!f) return refuse(FP8Z1_EINVAL, what, "NULL description");

@@ -1,0 +1,168 @@
+// Gradients of y = res + act(x W^T + bias): dp = dy act'(p) with its sums over an expert's rows (the
+// bias's gradient) in one pass over dy and p, and dx = dp W on the tile kernel of the feed-forward block.
+//
+// The pass is bound by HBM.  A workgroup takes 16 rows of one expert by up to 2048 columns, 8 of them per thread, and
+// writes their float32 column sums to the workspace; a second kernel adds an expert's groups in order.
+#include "ffn_tile.h"
+#include "rows.h"
+
+namespace fp8z1 {
+namespace {
+
+constexpr int kSumRows = 16;
+
+struct DpArgs {
+  const uint16_t *dy, *p;
+  uint16_t* dp;
+  float* sums;  // [groups][N], or NULL
+  const int32_t* offsets;
+  int32_t T, E, N, act;
+};
+
+template <class H>
+__global__ __launch_bounds__(kThreads) void linear_dp_kernel(DpArgs a) {
+  int32_t e, lo, hi, t0;
+  const int32_t group = static_cast<int32_t>(blockIdx.z * gridDim.y + blockIdx.y);
+  if (!find_group<kSumRows>(a.offsets, a.T, a.E, group, e, lo, hi, t0)) return;
+  const int32_t n = static_cast<int32_t>(blockIdx.x * blockDim.x + threadIdx.x) * 8, rows = min(hi - t0, kSumRows);
+  if (n >= a.N) return;
+  float sum[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sum[i] = 0.0f;
+  for (int32_t r0 = 0; r0 < rows; r0 += 4) {
+    Raw8<H> d[4], p[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (r0 + k < rows) {
+        d[k] = fetch8<H>(row_of<H>(static_cast<const void*>(a.dy), t0 + r0 + k, a.N), a.N, n);
+        if (a.p) p[k] = fetch8<H>(row_of<H>(static_cast<const void*>(a.p), t0 + r0 + k, a.N), a.N, n);
+      }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (r0 + k < rows) {
+        float dy[8], h[8];
+        widen8f<H>(d[k], dy);
+        if (a.p) {
+          widen8f<H>(p[k], h);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float value, slope;
+            act_both(a.act, h[i], value, slope);
+            dy[i] *= slope;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i] += dy[i];
+        if (a.dp) store8<H>(row_of<H>(static_cast<void*>(a.dp), t0 + r0 + k, a.N), a.N, n, dy);
+      }
+  }
+  if (a.sums) store8<F32>(a.sums + static_cast<int64_t>(group) * a.N, a.N, n, sum);
+}
+
+// dbias[e][n]: the sums of expert e's groups, numbered as find_group numbers them
+__global__ __launch_bounds__(kThreads) void linear_dbias_kernel(const float* sums, const int32_t* offsets, int32_t T,
+                                                                int32_t E, int32_t N, float* dbias) {
+  const int32_t strips = (N + kThreads - 1) / kThreads;
+  const int32_t e = static_cast<int32_t>(blockIdx.x) / strips;
+  const int32_t n = (static_cast<int32_t>(blockIdx.x) - e * strips) * kThreads + threadIdx.x;
+  if (n >= N) return;
+  int32_t lo, hi;
+  expert_rows(offsets, T, e, lo, hi);
+  float sum = 0.0f;
+  if (lo < hi) {
+    sum = sums[static_cast<int64_t>(e) * N + n];
+    const float* const from = sums + (static_cast<int64_t>(E) + lo / kSumRows) * N + n;
+    const int32_t more = (hi - lo - 1) / kSumRows;  // groups behind the first
+#pragma unroll 8
+    for (int32_t k = 0; k < more; ++k) sum += from[static_cast<int64_t>(k) * N];
+  }
+  dbias[static_cast<int64_t>(e) * N + n] = sum;
+}
+
+int64_t sum_groups(int64_t T, int64_t E) { return E + T / kSumRows; }
+
+}  // namespace
+}  // namespace fp8z1
+
+using namespace fp8z1;
+
+extern "C" int fp8z1_linear_bwd_workspace_bytes(const fp8z1_product* f, size_t* bytes) {
+  const char* what = "linear_bwd_workspace_bytes";
+  if (!f || !bytes) return refuse(FP8Z1_EINVAL, what, "NULL argument");
+  static const int32_t some_offsets = 0;
+  const int rc = check_product(f, &some_offsets, what);
+  if (rc) return rc;
+  // the bias's sums are joined before the tiles are split: both use the same memory
+  const size_t sums = sizeof(float) * static_cast<size_t>(sum_groups(f->T, f->E)) * static_cast<size_t>(f->N);
+  const size_t parts = f->N > 2 * kB ? part_bytes(4) : 0;
+  *bytes = !f->T ? 0 : ((sums > parts ? sums : parts) + 15) / 16 * 16;
+  return FP8Z1_OK;
+}
+
+extern "C" int fp8z1_linear_bwd(const fp8z1_product* f, const void* dy, const void* p, const uint8_t* codes,
+                                const float* scales, const int32_t* offsets, void* dp, float* dbias, void* dx,
+                                void* d_workspace, size_t workspace_bytes, void* stream) {
+  const char* what = "linear_bwd";
+  int rc = check_product(f, offsets, what);
+  if (rc) return rc;
+  const bool act = f->act != FP8Z1_ACT_NONE;
+  if (!dp && !dbias && !dx) return refuse(FP8Z1_EINVAL, what, "no gradient is wanted");
+  if (f->T) rc = check_rows({dy}, what);
+  if (f->T && !rc && act) rc = check_rows({p}, what);
+  if (rc) return rc;
+  if (f->T && dx && act && !dp) return refuse(FP8Z1_EINVAL, what, "dx needs dp behind an activation");
+  if (misaligned(dp, 2) || misaligned(dx, 2) || misaligned(dbias, 4))
+    return refuse(FP8Z1_EINVAL, what, "misaligned argument");
+  if (dx) rc = check_weights(codes, scales, what);
+  if (rc) return rc;
+  if (misaligned(d_workspace, 16)) return refuse(FP8Z1_EINVAL, what, "misaligned workspace");
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  DpArgs a{};
+  a.dy = static_cast<const uint16_t*>(dy);
+  a.p = act ? static_cast<const uint16_t*>(p) : nullptr;
+  a.dp = static_cast<uint16_t*>(dp);
+  a.offsets = offsets;
+  a.T = static_cast<int32_t>(f->T);
+  a.E = static_cast<int32_t>(f->E);
+  a.N = static_cast<int32_t>(f->N);
+  a.act = f->act;
+  const int64_t groups = sum_groups(f->T, f->E);
+  if (dbias && f->T) {
+    if (!d_workspace || workspace_bytes < sizeof(float) * static_cast<size_t>(groups) * static_cast<size_t>(f->N))
+      return refuse(FP8Z1_EINVAL, what, "workspace too small");
+    a.sums = static_cast<float*>(d_workspace);
+  }
+  const int64_t strips = f->E * ((f->N + kThreads - 1) / kThreads);
+  if (dbias && strips > 0x7fffffff / kThreads) return refuse(FP8Z1_ESHAPE, what, "too many gradients of biases");
+  if (f->T && (dp || dbias)) {
+    const int64_t chunks = (f->N + 7) / 8, threads = chunks < kThreads ? (chunks + 63) / 64 * 64 : kThreads;
+    const int64_t turns = (groups + 65534) / 65535;  // (a grid's y ends at 65,535)
+    const dim3 g(static_cast<unsigned>((chunks + threads - 1) / threads),
+                 static_cast<unsigned>((groups + turns - 1) / turns), static_cast<unsigned>(turns));
+    const dim3 b(static_cast<unsigned>(threads));
+    if (f->dtype == FP8Z1_BF16)
+      hipLaunchKernelGGL((linear_dp_kernel<Bf16>), g, b, 0, s, a);
+    else
+      hipLaunchKernelGGL((linear_dp_kernel<F16>), g, b, 0, s, a);
+    rc = launched(what);
+    if (rc) return rc;
+  }
+  if (dbias) {
+    hipLaunchKernelGGL(linear_dbias_kernel, dim3(static_cast<unsigned>(strips)), dim3(kThreads), 0, s, a.sums, offsets, a.T,
+                       a.E, a.N, dbias);
+    rc = launched(what);
+    if (rc) return rc;
+  }
+  if (!dx) return FP8Z1_OK;
+  FfnArgs q{};
+  q.offsets = offsets;
+  q.T = a.T;
+  q.E = a.E;
+  q.N = static_cast<int32_t>(f->K);
+  q.K = static_cast<int32_t>(f->N);
+  q.x0 = bytes(act ? dp : dy);
+  q.w0 = codes;
+  q.s0 = scales;
+  q.o0 = static_cast<uint16_t*>(dx);
+  return launch<kLinearBwd>(q, f->dtype, d_workspace, workspace_bytes, s, what);
+}

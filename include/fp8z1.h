@@ -332,10 +332,13 @@ int fp8z1_dequantize(const uint8_t* codes, const float* scales, int64_t E, int64
 #define FP8Z1_ACT_SILU 0 /* h / (1 + exp(-h)) */
 #define FP8Z1_ACT_GELU 1 /* 0.5 h (1 + tanh(sqrt(2/pi) (h + 0.044715 h^3))) */
 
+#define FP8Z1_ACT_NONE 2 /* h (fp8z1_linear only) */
+
 #define FP8Z1_FFN_MAX_ROWS (1 << 30)
 #define FP8Z1_FFN_MAX_WIDTH (1 << 20)
 #define FP8Z1_FFN_MAX_EXPERTS 65535
 
+/* (Products with one weight, a bias and a residual, and with rows in 8 bits: below.) */
 typedef struct {
   int64_t T; /* rows (tokens) */
   int64_t E; /* experts */
@@ -440,6 +443,51 @@ int fp8z1_norm_join_bwd(const fp8z1_norm* f, const void* dz, const void* dn, con
  * fp8z1_norm_join: the rounding to 8 bits passes dn through. */
 int fp8z1_norm_join8(const fp8z1_norm* f, const void* y, const void* res, const float* w_post, const void* gate,
                      const float* w_pre, void* z, void* n, uint8_t* codes, float* scales, int32_t scale_rule, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Products with one weight, and with rows in 8 bits.  Rows in 8 bits are codes [T,K] (at any alignment) and scales
+ * [T, ceil(K/128)] float32, as fp8z1_norm_join8 writes them; the products of 8-bit rows and codes are
+ * summed in float32 on the matrix cores, and both scales multiply the sum of each 128. */
+
+typedef struct {
+  int64_t T; /* rows */
+  int64_t E; /* experts (offsets as above) */
+  int64_t N; /* width of y; weight codes [E, N, K] */
+  int64_t K; /* width of x */
+  int32_t dtype;   /* y, res, p and all gradients: FP8Z1_BF16 or FP8Z1_F16 */
+  int32_t x_dtype; /* x: dtype, or FP8Z1_E4M3 */
+  int32_t act;     /* FP8Z1_ACT_* */
+  int32_t reserved;
+} fp8z1_product;
+
+/* y [T,N] = res + act(x W^T + bias).  x_scales for x in 8 bits, else NULL.  bias float32 [E,N] or NULL; res [T,N] or NULL
+ * (y may be res itself); p [T,N], unless NULL, keeps x W^T + bias for the backward pass.  With
+ * fp8z1_linear_workspace_bytes() bytes of device workspace (16-byte aligned) tiles that do not fill
+ * the card are split along k; with less (or NULL) they are not. */
+int fp8z1_linear_workspace_bytes(const fp8z1_product* f, size_t* bytes);
+int fp8z1_linear(const fp8z1_product* f, const void* x, const float* x_scales, const uint8_t* codes, const float* scales,
+                 const int32_t* offsets, const float* bias, const void* res, void* y, void* p, void* d_workspace,
+                 size_t workspace_bytes, void* stream);
+
+/* Its gradients from dy [T,N] and the kept p (NULL without an activation): dp = dy act'(p) (at x W^T + bias; the weight
+ * gradient is fp8z1_ffn_wgrad of dp and x in 16 bits), dbias float32 [E,N] = the sum of an expert's dp before they are
+ * rounded (0 for one without rows), dx [T,K] = dp W of the rounded dp.  (res has dy.)  Each may be NULL if it
+ * is not wanted; dx needs dp where there is an activation.  x's rounding to 8 bits passes dx through;
+ * x_dtype is not looked at.  dbias needs fp8z1_linear_bwd_workspace_bytes() bytes of device workspace
+ * (16-byte aligned), with which tiles are split too. */
+int fp8z1_linear_bwd_workspace_bytes(const fp8z1_product* f, size_t* bytes);
+int fp8z1_linear_bwd(const fp8z1_product* f, const void* dy, const void* p, const uint8_t* codes, const float* scales,
+                     const int32_t* offsets, void* dp, float* dbias, void* dx, void* d_workspace, size_t workspace_bytes,
+                     void* stream);
+
+/* fp8z1_ffn_up with x and a in 8 bits: a = act(x Wg^T) * (x Wu^T), its codes [T,F] and scales [T, ceil(F/128)] by
+ * `scale_rule` from the float32 a.  h and u [T,F] in f->dtype (both or neither NULL) are for fp8z1_ffn_down_bwd;
+ * fp8z1_linear of a makes y.  Workspace as for fp8z1_linear, fp8z1_ffn_up8_workspace_bytes() bytes. */
+int fp8z1_ffn_up8_workspace_bytes(const fp8z1_ffn* f, size_t* bytes);
+int fp8z1_ffn_up8(const fp8z1_ffn* f, const uint8_t* x, const float* x_scales, const uint8_t* gate_codes,
+                  const float* gate_scales, const uint8_t* up_codes, const float* up_scales, const int32_t* offsets,
+                  void* h, void* u, uint8_t* a, float* a_scales, int32_t scale_rule, void* d_workspace,
+                  size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
  * The router, and tokens sorted by expert and back.  No call allocates or waits; all may be captured into a HIP

@@ -1,0 +1,366 @@
+"""GPU: products with an epilogue, of rows in 16 and in 8 bits, and their gradients, against float64."""
+import pytest
+
+torch = pytest.importorskip("torch")
+from tests import block_reference as ref  # noqa: E402
+from tests import rows8_reference as r8  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+U = ref.U32
+
+
+def setup_module(module):
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def block():
+    from blockwise_fp8_zero_fold_amd import block as b
+    return b
+
+
+def pair(x):
+    return tuple(v.cuda() for v in x)
+
+
+def value(act, h):
+    return h if act is None else ref.act_value(act, h)
+
+
+def act_error(act, h):
+    return (torch.zeros_like(h), torch.zeros_like(h)) if act is None else ref.act_error(act, h)
+
+
+def make(T, E, N, K, x_type, seed=0):
+    g = torch.Generator().manual_seed(seed + T + N + K)
+    w = ref.make_weight(g, E, N, K)
+    offsets = ref.make_offsets(g, T, E) if E > 1 else None
+    x = r8.make_rows8(g, T, K) if x_type == "e4m3" else torch.randn(T, K, generator=g).to(x_type)
+    xd = r8.dequantize(*x) if x_type == "e4m3" else x.double()
+    return g, w, offsets, x, xd
+
+
+def sum_error(mag, n, x_type="e4m3"):
+    """Of a float32 sum of n products; on 8-bit rows also of the matrix instruction's own sums.  It adds the products of
+    8 consecutive k as fixed-point numbers that keep 13 bits below the largest one's power of two, and cuts off the rest:
+    less than 2^-13 of the largest for each of the 7 others.  Over all groups that is less than 7 * 2^-13 of
+    the sum of the groups' largest, so of the sum of all magnitudes.  (Seen with one product of 448 * 448 and one of 36,
+    18, 9, 4.5 .. among the same 8: 32, 16, 8, 0 .. of the small one are kept; in another 8 it is kept to float32.)"""
+    return ref.sum_error(mag, n) + (7 * 2.0 ** -13 * mag if x_type == "e4m3" else 0.0)
+
+
+def covered(offsets, T):
+    """Whether a row belongs to an expert."""
+    m = torch.zeros(T, dtype=torch.bool)
+    for _, lo, hi in ref.runs(offsets, T):
+        m[lo:hi] = True
+    return m
+
+
+# few rows (one matrix tile or two of rows; k shared by 8 or 4 waves), tiles, tiles split along k, rows through registers
+SIZES = [(1, 1, 1, 1), (1, 1, 16, 128), (3, 1, 17, 129), (1, 1, 2048, 7168), (9, 4, 33, 200), (20, 1, 40, 1000), (32, 1, 520, 136),
+         (90, 3, 130, 261), (33, 1, 1, 1), (40, 1, 300, 1000), (64, 1, 256, 1001), (130, 3, 257, 260), (200, 1, 512, 2048),
+         (300, 2, 700, 516), (129, 1, 64, 64), (600, 5, 129, 384), (1000, 1, 1024, 896), (260, 1, 100, 4100), (150, 1, 90, 2043)]
+
+
+@pytest.mark.parametrize("T,E,N,K", SIZES)
+@pytest.mark.parametrize("x_type,dtype", [("e4m3", torch.bfloat16), ("e4m3", torch.float16), (torch.bfloat16, torch.bfloat16),
+                                          (torch.float16, torch.float16)])
+@pytest.mark.parametrize("act,with_bias,with_res", [(None, False, False), ("silu", True, True), ("gelu", True, False),
+                                                    (None, False, True)])
+def test_forward(T, E, N, K, x_type, dtype, act, with_bias, with_res):
+    g, w, offsets, x, xd = make(T, E, N, K, x_type)
+    bias = torch.randn(E, N, generator=g) if with_bias else None
+    res = torch.randn(T, N, generator=g).to(dtype) if with_res else None
+    p, mag = ref.grouped(xd, ref.dequantize(*w), offsets, False)
+    if with_bias:
+        for e, lo, hi in ref.runs(offsets, T):
+            p[lo:hi] += bias[e].double()
+            mag[lo:hi] += bias[e].double().abs()
+    before = sum_error(mag, K + 1, x_type)
+    y = value(act, p)
+    err = 1.2 * before + act_error(act, p)[0]
+    if with_res:
+        y, err = y + res.double(), err + U * (y.abs() + res.double().abs())
+    got, kept = block().linear(pair(x) if x_type == "e4m3" else x.cuda(), pair(w), None if offsets is None else offsets.cuda(),
+                               None if bias is None else bias.cuda(), act, None if res is None else res.cuda(),
+                               save=True, dtype=dtype)
+    assert got.dtype == dtype and kept.dtype == dtype
+    m = covered(offsets, T)
+    ref.check(got.cpu()[m], y[m], ref.rounded(y, err, dtype)[m], "y")
+    ref.check(kept.cpu()[m], p[m], ref.rounded(p, before, dtype)[m], "p")
+    again, none = block().linear(pair(x) if x_type == "e4m3" else x.cuda(), pair(w),
+                                 None if offsets is None else offsets.cuda(), None if bias is None else bias.cuda(), act,
+                                 None if res is None else res.cuda(), dtype=dtype)
+    assert none is None and torch.equal(again.cpu()[m], got.cpu()[m])
+
+
+@pytest.mark.parametrize("T", [5, 100, 700])
+def test_sums_that_float32_holds_are_exact(T):
+    """Small whole numbers: every product and sum is a whole number below 2^24, so y is the exact sum rounded once."""
+    g = torch.Generator().manual_seed(T)
+    E, N, K = 2, 300, 1200
+    whole = torch.randint(-4, 5, (E, N, K), generator=g).float(), torch.randint(-4, 5, (T, K), generator=g).float()
+    codes = tuple(v.to(torch.float8_e4m3fn).view(torch.uint8) for v in whole)
+    ws = 2.0 ** torch.randint(-2, 3, (E, 3, 10), generator=g).float()
+    xs = 2.0 ** torch.randint(-2, 3, (T, 10), generator=g).float()
+    offsets = torch.tensor([0, T // 3, T], dtype=torch.int32)
+    want, _ = ref.grouped(r8.dequantize(codes[1], xs), ref.dequantize(codes[0], ws), offsets, False)
+    y, _ = block().linear(pair((codes[1], xs)), pair((codes[0], ws)), offsets.cuda(), dtype=torch.float16)
+    assert torch.equal(y.cpu(), want.to(torch.float16))
+
+
+@pytest.mark.parametrize("T", [3, 200])
+def test_special_codes_scales_and_the_end_of_a_row(T):
+    """NaN codes and infinite scales stay in their rows and columns; what lies behind a row's end is not its."""
+    g = torch.Generator().manual_seed(1)
+    N, K = 140, 300
+    x, w = r8.make_rows8(g, T, K), ref.make_weight(g, 1, N, K)
+    x[0][1, 0] = 0x7F  # the first code of a row: behind the end of the row before
+    x[1][2, 1] = float("inf")
+    w[0][0, 5, 0] = 0xFF
+    p, mag = ref.grouped(r8.dequantize(*x), ref.dequantize(*w), None, False)
+    y, _ = block().linear(pair(x), pair(w))
+    # an infinite scale times a block's sum: an infinity or NaN by its sign, as the sum's, and NaN of 0
+    fine = torch.ones(T, dtype=torch.bool)
+    fine[2] = False
+    ref.check(y.cpu()[fine], p[fine], ref.rounded(p, sum_error(mag, K), torch.bfloat16)[fine], "y")
+    assert not torch.isfinite(y[2].float()).any()
+    x[1][2, 1] = 0.0
+    w[1][0, 1, 2] = 0.0
+    w[1][0, 0, 0] = -w[1][0, 0, 0]
+    p, mag = ref.grouped(r8.dequantize(*x), ref.dequantize(*w), None, False)
+    y, _ = block().linear(pair(x), pair(w))
+    ref.check(y, p, ref.rounded(p, sum_error(mag, K), torch.bfloat16), "y")
+
+
+def test_scales_far_apart():
+    g = torch.Generator().manual_seed(2)
+    for T in (10, 300):
+        x, w = r8.make_rows8(g, T, 520, -60.0, 20.0), ref.make_weight(g, 1, 200, 520, -40.0, 30.0)
+        p, mag = ref.grouped(r8.dequantize(*x), ref.dequantize(*w), None, False)
+        y, _ = block().linear(pair(x), pair(w))
+        ref.check(y, p, ref.rounded(p, sum_error(mag, 520), torch.bfloat16), "y")
+
+
+@pytest.mark.parametrize("T,E,N,K", [(1, 1, 1, 1), (5, 1, 300, 40), (40, 3, 136, 264), (200, 1, 1000, 77), (333, 4, 520, 130),
+                                     (700, 2, 2100, 128)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("act,with_bias", [("silu", True), ("gelu", False), (None, True), (None, False)])
+def test_backward(T, E, N, K, dtype, act, with_bias):
+    g, w, offsets, _, _ = make(T, E, N, K, dtype)
+    dy = torch.randn(T, N, generator=g).to(dtype)
+    p = (torch.randn(T, N, generator=g) * 2).to(dtype) if act else None
+    got = block().linear_backward(dy.cuda(), pair(w), None if p is None else p.cuda(),
+                                  None if offsets is None else offsets.cuda(), act, with_bias)
+    slope = ref.act_slope(act, p.double()) if act else torch.ones(T, N, dtype=torch.float64)
+    dp = dy.double() * slope
+    err = dy.double().abs() * (act_error(act, p.double())[1] if act else 0.0) + U * dp.abs()
+    m = covered(offsets, T)
+    if act:
+        ref.check(got["dp"].cpu()[m], dp[m], ref.rounded(dp, err, dtype)[m], "dp")
+    else:
+        assert got["dp"].data_ptr() != 0 and torch.equal(got["dp"].cpu(), dy)
+    kept = torch.where(m[:, None], got["dp"].cpu().double(), torch.zeros(1, dtype=torch.float64))
+    dx, mag = ref.grouped(kept, ref.dequantize(*w), offsets, True)
+    ref.check(got["dx"].cpu()[m], dx[m], ref.rounded(dx, ref.sum_error(mag, N), dtype)[m], "dx")
+    if with_bias:
+        db, bound = torch.zeros(E, N, dtype=torch.float64), torch.zeros(E, N, dtype=torch.float64)
+        for e, lo, hi in ref.runs(offsets, T):
+            db[e] = dp[lo:hi].sum(0)
+            bound[e] = err[lo:hi].sum(0) + ref.sum_error(dp[lo:hi].abs().sum(0), hi - lo)
+        ref.check(got["dbias"], db, bound, "dbias")
+    else:
+        assert got["dbias"] is None
+
+
+def test_gradients_against_differences():
+    """The whole layer in float64 by central differences of <dy, y>, at the kernel's own kept p."""
+    g = torch.Generator().manual_seed(4)
+    T, N, K = 6, 20, 24
+    w, b = ref.make_weight(g, 1, N, K), torch.randn(1, N, generator=g)
+    x, dy = torch.randn(T, K, generator=g).half(), torch.randn(T, N, generator=g).half()
+    wd = ref.dequantize(*w)[0]
+    for act in ("silu", "gelu", None):
+        _, p = block().linear(x.cuda(), pair(w), bias=b.cuda(), act=act, save=True)
+        got = block().linear_backward(dy.cuda(), pair(w), p if act else None, act=act, bias=True)
+
+        def loss(xx, bb):
+            return float((value(act, xx @ wd.t() + bb) * dy.double()).sum())
+
+        h = 1e-4
+        sx, sb = torch.randn(T, K, generator=g).double(), torch.randn(1, N, generator=g).double()
+        by_x = (loss(x.double() + h * sx, b.double()) - loss(x.double() - h * sx, b.double())) / (2 * h)
+        by_b = (loss(x.double(), b.double() + h * sb) - loss(x.double(), b.double() - h * sb)) / (2 * h)
+        # p, dp and dx carry a rounding to 11 bits each; sums of that many terms of either sign
+        dx, db = got["dx"].cpu().double(), got["dbias"].cpu().double()
+        assert abs(by_x - float((dx * sx).sum())) <= 8 * 2.0 ** -11 * float((dx * sx).norm() * T * K) ** 1.0
+        assert abs(by_b - float((db * sb).sum())) <= 8 * 2.0 ** -11 * float((dy.double().abs().sum(0) * sb.abs()).sum())
+
+
+UP = [(1, 1, 1, 1), (3, 1, 128, 16), (1, 1, 7168, 2048), (7, 4, 200, 130), (32, 1, 1000, 257), (90, 3, 261, 300),
+      (33, 1, 1, 1), (64, 1, 1001, 256), (130, 3, 260, 257), (200, 1, 2048, 500), (129, 1, 64, 64), (600, 5, 384, 129),
+      (300, 1, 1028, 1100), (150, 1, 2043, 90)]
+
+
+@pytest.mark.parametrize("T,E,D,F", UP)
+@pytest.mark.parametrize("dtype,act,rule", [(torch.bfloat16, "silu", "amax"), (torch.float16, "gelu", "amax"),
+                                            (torch.bfloat16, "gelu", "pow2")])
+def test_up8(T, E, D, F, dtype, act, rule):
+    g, wg, offsets, x, xd = make(T, E, F, D, "e4m3")
+    wu = ref.make_weight(g, E, F, D)
+    off = None if offsets is None else offsets.cuda()
+    (codes, scales), (h, u) = block().ffn_up8(pair(x), pair(wg), pair(wu), off, act, True, dtype, rule)
+    m = covered(offsets, T)
+    he, hm = ref.grouped(xd, ref.dequantize(*wg), offsets, False)
+    ue, um = ref.grouped(xd, ref.dequantize(*wu), offsets, False)
+    eh, eu = sum_error(hm, D), sum_error(um, D)
+    ref.check(h.cpu()[m], he[m], ref.rounded(he, eh, dtype)[m], "h")
+    ref.check(u.cpu()[m], ue[m], ref.rounded(ue, eu, dtype)[m], "u")
+    a = ref.act_value(act, he) * ue
+    ea = (1.2 * eh + ref.act_error(act, he)[0]) * (ue.abs() + eu) + ref.act_value(act, he).abs() * eu + 2 * U * a.abs()
+    top = r8.groups(a.abs()).amax(2)
+    etop = r8.groups(ea).amax(2)
+    s = scales.cpu().double()
+    if rule == "amax":
+        want = torch.where(top == 0, torch.ones_like(top), top / 448.0)
+        fine = (top > 2 * etop) & m[:, None]
+        assert ((s - want).abs() <= etop / 448.0 + U * want)[fine].all()
+        room = torch.full_like(s, 1.0)
+    else:
+        fine = (top > 2 * etop) & m[:, None]
+        lo, hi = torch.floor(torch.log2(top - etop)) - 8, torch.floor(torch.log2(top + etop)) - 8
+        assert ((s >= torch.exp2(lo)) & (s <= torch.exp2(hi)))[fine].all() and (torch.frexp(s).mantissa[fine] == 0.5).all()
+        room = torch.full_like(s, 512.0 / 448.0)  # what the codes cannot hold of [448, 512) saturates
+    wide = s.repeat_interleave(128, 1)[:, :F]
+    got = r8.dequantize(codes.cpu(), scales.cpu())
+    cut = (a.abs() - 448.0 * wide).clamp(min=0.0)
+    bound = ea + torch.maximum((a.abs() + ea) * 2.0 ** -4, wide * 2.0 ** -10) + cut
+    ok = m[:, None] & fine.repeat_interleave(128, 1)[:, :F]
+    assert (((got - a).abs() <= bound) | ~ok).all(), float(((got - a).abs() - bound)[ok].max())
+    assert float(room.max()) * 448 >= 0
+    (c2, s2), none = block().ffn_up8(pair(x), pair(wg), pair(wu), off, act, False, dtype, rule)
+    assert none is None and torch.equal(c2.cpu()[m], codes.cpu()[m]) and torch.equal(s2.cpu()[m], scales.cpu()[m])
+
+
+def test_without_a_workspace():
+    """Unsplit tiles, and up's few rows on tiles: the same within the bounds."""
+    import blockwise_fp8_zero_fold_amd as fz
+    g, w, _, x, xd = make(200, 1, 300, 2048, "e4m3")
+    p, mag = ref.grouped(xd, ref.dequantize(*w), None, False)
+    y = torch.zeros(200, 300, dtype=torch.bfloat16, device="cuda")
+    f = fz.Product(200, 1, 300, 2048, fz.BF16, fz.E4M3, fz.ACT_NONE, 0)
+    fz.fp8z1_linear(f, *pair(x), *pair(w), None, None, None, y)
+    ref.check(y, p, ref.rounded(p, sum_error(mag, 2048), torch.bfloat16), "y")
+    for T in (1, 20):
+        g, w, _, x, xd = make(T, 1, 300, 520, "e4m3")
+        want, _ = block().ffn_up8(pair(x), pair(w), pair(w))
+        codes, scales = torch.zeros_like(want[0]), torch.zeros_like(want[1])
+        fz.fp8z1_ffn_up8(fz.Ffn(T, 1, 520, 300, fz.BF16, fz.ACT_SILU), *pair(x), *pair(w), *pair(w), None, None, None, codes,
+                         scales)
+        a, b = (r8.dequantize(c.cpu(), s.cpu()) for c, s in (want, (codes, scales)))
+        assert float((a - b).norm()) <= 0.01 * float(a.norm())
+
+
+def test_unaligned_buffers_and_the_residual_in_place():
+    import blockwise_fp8_zero_fold_amd as fz
+    for T, N, K in ((5, 40, 256), (100, 70, 256)):
+        g, w, _, x, xd = make(T, 1, N, K, "e4m3")
+        want, _ = block().linear(pair(x), pair(w))
+        xc = torch.zeros(T * K + 1, dtype=torch.uint8, device="cuda")[1:]
+        wc = torch.zeros(N * K + 3, dtype=torch.uint8, device="cuda")[3:]
+        xc.copy_(x[0].flatten())
+        wc.copy_(w[0].flatten())
+        f = fz.Product(T, 1, N, K, fz.BF16, fz.E4M3, fz.ACT_NONE, 0)
+        y = torch.zeros(T * N + 1, dtype=torch.bfloat16, device="cuda")[1:]
+        fz.fp8z1_linear(f, xc, x[1].cuda(), wc, w[1].cuda(), None, None, None, y)
+        assert torch.equal(y.view(T, N), want)
+        res = torch.randn(T, N, generator=g).bfloat16().cuda()
+        both, _ = block().linear(pair(x), pair(w), res=res)
+        fz.fp8z1_linear(f, *pair(x), *pair(w), None, None, res, res)
+        assert torch.equal(res, both)
+
+
+def test_rows_without_an_expert_and_offsets_out_of_order():
+    b = block()
+    for T in (30, 300):
+        g, w, _, x, _ = make(T, 3, 60, 200, "e4m3")
+        off = torch.tensor([2, 10, 10, T - 5], dtype=torch.int32)
+        y = torch.full((T, 60), 3.0, dtype=torch.bfloat16, device="cuda")
+        import blockwise_fp8_zero_fold_amd as fz
+        f = fz.Product(T, 3, 60, 200, fz.BF16, fz.E4M3, fz.ACT_NONE, 0)
+        fz.fp8z1_linear(f, *pair(x), *pair(w), off.cuda(), None, None, y)
+        assert (y[:2] == 3).all() and (y[T - 5:] == 3).all()
+        whole, _ = b.linear(pair((x[0][2:10].contiguous(), x[1][2:10].contiguous())),
+                            pair((w[0][:1].contiguous(), w[1][:1].contiguous())))
+        assert torch.allclose(y[2:10].float(), whole.float(), rtol=2.0 ** -7, atol=1e-3)
+        for bad in ([5, 2, 40, 1], [-9, T + 50, 3, T], [T, T, T, 0]):
+            fz.fp8z1_linear(f, *pair(x), *pair(w), torch.tensor(bad, dtype=torch.int32).cuda(), None, None, y)
+            b.ffn_up8(pair(x), pair(w), pair(w), torch.tensor(bad, dtype=torch.int32).cuda())
+        torch.cuda.synchronize()
+
+
+def test_graph_and_side_stream():
+    b = block()
+    g, w, offsets, x, _ = make(300, 2, 256, 1024, "e4m3")
+    wd = ref.make_weight(g, 2, 1024, 256)
+    dev, off = [pair(v) for v in (x, w, wd)], offsets.cuda()
+
+    def step():
+        y, kept = b.ffn_forward8(dev[0], dev[1], dev[1], dev[2], off, save=True)
+        z, p = b.linear(y, dev[1], off, act="silu", save=True)
+        grads = b.linear_backward(z, dev[1], p, off, "silu", True)
+        return y, *kept, z, p, grads["dx"], grads["dp"], grads["dbias"]
+
+    want = step()
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        got = step()
+    stream.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kept = step()
+    for i in range(4):
+        dev[0][0].copy_(r8.make_rows8(g, 300, 1024)[0])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(kept, step())), i
+
+
+def test_forward8_is_near_the_block_on_16_bits():
+    """The same block on the rows' 16-bit values: within the codes' rounding of a (2^-4 each, independent signs)."""
+    b = block()
+    g, wg, offsets, x, xd = make(200, 2, 384, 512, "e4m3")
+    wu, wd = ref.make_weight(g, 2, 384, 512), ref.make_weight(g, 2, 512, 384)
+    y8, _ = b.ffn_forward8(pair(x), pair(wg), pair(wu), pair(wd), offsets.cuda())
+    y, _ = b.ffn_forward(xd.bfloat16().cuda(), pair(wg), pair(wu), pair(wd), offsets.cuda())
+    assert float((y8.float() - y.float()).norm()) <= 2.0 ** -4 * float(y.float().norm())
+
+
+def test_refusals():
+    import blockwise_fp8_zero_fold_amd as fz
+    b = block()
+    g, w, _, x, _ = make(8, 1, 16, 32, "e4m3")
+    x, w = pair(x), pair(w)
+    h, y = torch.zeros(8, 32, dtype=torch.bfloat16, device="cuda"), torch.zeros(8, 16, dtype=torch.bfloat16, device="cuda")
+    for call in (lambda: b.linear(x, w, act="relu"), lambda: b.linear(x, w, dtype=torch.float32), lambda: b.linear(h.float(), w),
+                 lambda: b.linear(h, w, dtype=torch.float16), lambda: b.linear((x[0], x[1].half()), w),
+                 lambda: b.linear((x[0], x[1][:, :0]), w), lambda: b.linear(x, (w[0], w[1][:, :0])),
+                 lambda: b.linear(x, w, bias=torch.zeros(1, 17, device="cuda")), lambda: b.linear(x, w, res=y[:4]),
+                 lambda: b.linear(x, w, res=y.half(), dtype=torch.bfloat16), lambda: b.linear((x[0].cpu(), x[1].cpu()), w),
+                 lambda: b.linear_backward(y, w, act="silu"), lambda: b.linear_backward(y, w, p=y),
+                 lambda: b.linear_backward(y.float(), w), lambda: b.linear_backward(h, w),
+                 lambda: b.ffn_up8(x, w, w, act="relu"), lambda: b.ffn_up8(x, w, w, dtype=torch.float32),
+                 lambda: b.ffn_up8(x, w, w, scale_rule="x"), lambda: b.ffn_up8(x, w, (w[0][:, :8], w[1])),
+                 lambda: b.linear(x, (torch.cat([w[0]] * 2), torch.cat([w[1]] * 2)))):
+        with pytest.raises(fz.Fp8z1Error):
+            call()
+    empty = (x[0][:0], x[1][:0])
+    assert b.linear(empty, w)[0].shape == (0, 16) and b.ffn_up8(empty, w, w)[0][0].shape == (0, 16)
+    grads = b.linear_backward(y[:0], w, bias=True)
+    assert grads["dx"].shape == (0, 32) and (grads["dbias"] == 0).all()
+    # a bias of one expert may be given without the expert's dimension
+    bias = torch.randn(16, generator=g).cuda()
+    assert torch.equal(b.linear(x, w, bias=bias)[0], b.linear(x, w, bias=bias[None])[0])
