@@ -203,44 +203,69 @@ UP = [(1, 1, 1, 1), (3, 1, 128, 16), (1, 1, 7168, 2048), (7, 4, 200, 130), (32, 
       (300, 1, 1028, 1100), (150, 1, 2043, 90)]
 
 
-@pytest.mark.parametrize("T,E,D,F", UP)
-@pytest.mark.parametrize("dtype,act,rule", [(torch.bfloat16, "silu", "amax"), (torch.float16, "gelu", "amax"),
-                                            (torch.bfloat16, "gelu", "pow2")])
-def test_up8(T, E, D, F, dtype, act, rule):
-    g, wg, offsets, x, xd = make(T, E, F, D, "e4m3")
-    wu = ref.make_weight(g, E, F, D)
+def check_up8(x, xd, wg, wu, offsets, T, D, F, dtype, act, rule):
     off = None if offsets is None else offsets.cuda()
     (codes, scales), (h, u) = block().ffn_up8(pair(x), pair(wg), pair(wu), off, act, True, dtype, rule)
     m = covered(offsets, T)
     he, hm = ref.grouped(xd, ref.dequantize(*wg), offsets, False)
     ue, um = ref.grouped(xd, ref.dequantize(*wu), offsets, False)
-    eh, eu = sum_error(hm, D), sum_error(um, D)
+    eh, eu = ref.sum_error(hm, D), ref.sum_error(um, D)  # (float32 sums of exact products)
     ref.check(h.cpu()[m], he[m], ref.rounded(he, eh, dtype)[m], "h")
     ref.check(u.cpu()[m], ue[m], ref.rounded(ue, eu, dtype)[m], "u")
     a = ref.act_value(act, he) * ue
     ea = (1.2 * eh + ref.act_error(act, he)[0]) * (ue.abs() + eu) + ref.act_value(act, he).abs() * eu + 2 * U * a.abs()
-    top = r8.groups(a.abs()).amax(2)
-    etop = r8.groups(ea).amax(2)
+    top, etop = r8.groups(a.abs()).amax(2), r8.groups(ea).amax(2)
     s = scales.cpu().double()
+    # (below 2^-126 a float32 loses bits, and below 2^-149 it is 0, whose scale is 1)
+    fine = (top > 2 * etop) & (top >= 2.0 ** -126) & m[:, None]
     if rule == "amax":
-        want = torch.where(top == 0, torch.ones_like(top), top / 448.0)
-        fine = (top > 2 * etop) & m[:, None]
-        assert ((s - want).abs() <= etop / 448.0 + U * want)[fine].all()
-        room = torch.full_like(s, 1.0)
+        want = (top / 448.0).clamp(min=2.0 ** -126)
+        ref.check(s[fine], want[fine], (etop / 448.0 + U * want)[fine], "scales")
     else:
-        fine = (top > 2 * etop) & m[:, None]
         lo, hi = torch.floor(torch.log2(top - etop)) - 8, torch.floor(torch.log2(top + etop)) - 8
         assert ((s >= torch.exp2(lo)) & (s <= torch.exp2(hi)))[fine].all() and (torch.frexp(s).mantissa[fine] == 0.5).all()
-        room = torch.full_like(s, 512.0 / 448.0)  # what the codes cannot hold of [448, 512) saturates
+    # a code stands for a to half a step of its own, or of the subnormals; what is past 448 scales is cut off
     wide = s.repeat_interleave(128, 1)[:, :F]
     got = r8.dequantize(codes.cpu(), scales.cpu())
-    cut = (a.abs() - 448.0 * wide).clamp(min=0.0)
-    bound = ea + torch.maximum((a.abs() + ea) * 2.0 ** -4, wide * 2.0 ** -10) + cut
+    bound = ea + torch.maximum((a.abs() + ea) * 2.0 ** -4, wide * 2.0 ** -10) + (a.abs() - 448.0 * wide).clamp(min=0.0)
     ok = m[:, None] & fine.repeat_interleave(128, 1)[:, :F]
     assert (((got - a).abs() <= bound) | ~ok).all(), float(((got - a).abs() - bound)[ok].max())
-    assert float(room.max()) * 448 >= 0
     (c2, s2), none = block().ffn_up8(pair(x), pair(wg), pair(wu), off, act, False, dtype, rule)
     assert none is None and torch.equal(c2.cpu()[m], codes.cpu()[m]) and torch.equal(s2.cpu()[m], scales.cpu()[m])
+
+
+@pytest.mark.parametrize("T,E,D,F", UP)
+@pytest.mark.parametrize("dtype,act,rule", [(torch.bfloat16, "silu", "amax"), (torch.float16, "gelu", "amax"),
+                                            (torch.bfloat16, "gelu", "pow2")])
+def test_up8(T, E, D, F, dtype, act, rule):
+    g, wg, offsets, x, xd = make(T, E, F, D, "e4m3")
+    check_up8(x, xd, wg, ref.make_weight(g, E, F, D), offsets, T, D, F, dtype, act, rule)
+
+
+@pytest.mark.parametrize("T,D,F", [(20, 520, 140), (300, 520, 140), (200, 2048, 300), (300, 1001, 130)])
+def test_up8_scales_far_apart(T, D, F):
+    """Scales whose ratios leave float32's range, zero and negative ones: the sums are the same float32 sums."""
+    g = torch.Generator().manual_seed(T + D)
+    x = r8.make_rows8(g, T, D, -100.0, 10.0)
+    wg, wu = ref.make_weight(g, 1, F, D, -20.0, 4.0), ref.make_weight(g, 1, F, D)
+    x[1][3, 0], x[1][4, 1], wg[1][0, 0, 1] = 0.0, -x[1][4, 1], 0.0
+    check_up8(x, r8.dequantize(*x), wg, wu, None, T, D, F, torch.bfloat16, "silu", "amax")
+
+
+@pytest.mark.parametrize("T", [3, 200])
+def test_up8_nan_and_infinities_stay_in_their_rows(T):
+    g = torch.Generator().manual_seed(T)
+    x, w = r8.make_rows8(g, T, 300), ref.make_weight(g, 1, 140, 300)
+    (c0, s0), _ = block().ffn_up8(pair(x), pair(w), pair(w))
+    x[0][1, 7] = 0x7F
+    x[1][2, 1] = float("inf")
+    (c1, s1), (h, u) = block().ffn_up8(pair(x), pair(w), pair(w), save=True)
+    assert torch.isnan(h[1].float()).all() and (c1[1] & 0x7F == 0x7F).all()
+    assert not torch.isfinite(h[2].float()).any()
+    rest = torch.ones(T, dtype=torch.bool)
+    rest[1:3] = False
+    a, b = r8.dequantize(c0.cpu(), s0.cpu())[rest], r8.dequantize(c1.cpu(), s1.cpu())[rest]
+    assert float((a - b).norm()) <= 1e-3 * float(a.norm())  # (another route to the same sums: a code may flip)
 
 
 def test_without_a_workspace():
