@@ -69,11 +69,15 @@ __device__ __forceinline__ void meet() {
 
 // ------------------------------------------------------------------------------------------------ tiles
 
-constexpr int kCols8 = 256;               // weight rows of a tile (up: 128 of gate, 128 of up)
-constexpr int kA8 = kRows * kB, kB8 = kCols8 * kB;
-constexpr int kStage8 = kA8 + kB8 + kRows * 4;  // codes of x, of the weights, and x's scales
-constexpr int kCopies = 13;               // of a wave for a stage
-constexpr int32_t kSlots8 = 256;          // workgroups that the card runs at once: one on each compute unit
+constexpr int kThreads8 = 512;
+constexpr int kRows8 = 256;   // tile rows
+constexpr int kCols8 = 256;   // weight rows of a tile (up: 128 of gate, 128 of up)
+constexpr int kA8 = kRows8 * kB, kB8 = kCols8 * kB;
+// a stage: codes of x, of the weights, x's scales (1 KB), and the weights' two, 64 times each (as a wave copies them)
+constexpr int kScales8 = kA8 + kB8, kStage8 = kScales8 + 2048;
+constexpr int kCopies = 9;                       // of a wave for a stage
+constexpr int kResults8 = 8 * (kResultBytes / 4);  // 64 x 64 float32 of each wave
+constexpr int32_t kSlots8 = 256;                 // workgroups that the card runs at once: one on each compute unit
 
 // Work items: as in ffn.h, for one workgroup per compute unit.
 __host__ __device__ __forceinline__ int32_t tile_splits8(int64_t tiles, int32_t blocks) {
@@ -89,7 +93,7 @@ __host__ __device__ __forceinline__ int32_t tile_splits8(int64_t tiles, int32_t 
 }
 __device__ __forceinline__ Plan plan_tiles8(const FfnArgs& p, int32_t ncols, int32_t blocks, int32_t& rowtiles,
                                             Run& first) {
-  Plan plan = plan_tiles<kRows>(p.offsets, p.T, p.E, ncols, blocks, 0, rowtiles, first);
+  Plan plan = plan_tiles<kRows8>(p.offsets, p.T, p.E, ncols, blocks, 0, rowtiles, first);
   const int32_t rest = plan.tiles % kSlots8, s = p.part ? tile_splits8(plan.tiles, blocks) : 1;
   if (s > 1) {
     plan.whole = plan.tiles - rest;
@@ -98,9 +102,9 @@ __device__ __forceinline__ Plan plan_tiles8(const FfnArgs& p, int32_t ncols, int
   return plan;
 }
 __device__ __forceinline__ float* part8_at(float* part, int32_t at) {
-  return part + static_cast<int64_t>(at) * (kRows * kCols8);
+  return part + static_cast<int64_t>(at) * (kRows8 * kCols8);
 }
-size_t part8_bytes() { return sizeof(float) * kSlots8 * kRows * kCols8; }
+size_t part8_bytes() { return sizeof(float) * kSlots8 * kRows8 * kCols8; }
 
 // a = act(gate) * up of 8 columns from column c of the results on, with 16 neighbouring lanes on the 128
 // columns of a group: h and u where they are wanted, codes and the group's scale.
@@ -121,7 +125,8 @@ __device__ __forceinline__ void finish_up8(const FfnArgs& p, int64_t m, int32_t 
   if (count <= 0) return;
   const float scale = row8_scale(top, p.pow2 != 0);
   if (n % kB == 0) p.code_scales[m * ((p.N + kB - 1) / kB) + n / kB] = scale;
-  const uint32_t lo = codes4(a[0], a[1], a[2], a[3], scale), hi = codes4(a[4], a[5], a[6], a[7], scale);
+  const Over8 over = over8(scale, p.pow2 != 0);
+  const uint32_t lo = codes4(a[0], a[1], a[2], a[3], over), hi = codes4(a[4], a[5], a[6], a[7], over);
   uint8_t* const to = p.codes + m * p.N + n;
   if (count == 8) {
     *(v2u_a1_rw_global_t*)(to) = v2u_t{lo, hi};
@@ -142,15 +147,15 @@ __device__ __forceinline__ void finish_up8(const FfnArgs& p, int64_t m, int32_t 
 
 // DIRECT: rows of x and codes are 4-byte aligned, and a stage is copied to LDS directly.
 //
-// A workgroup of 4 waves computes 128 rows x 256 weight rows, each wave 64 x 128 as 2 x 4 matrix tiles, one wave to a
-// SIMD with all its registers.  While the matrix cores work on block q out of registers, block q + 1 is read from LDS
-// into others and blocks q + 2 and q + 3 are on their way to LDS.
+// A workgroup of 8 waves computes 256 rows x 256 weight rows, each wave 64 x 128 as 2 x 4 matrix tiles; two waves share a
+// SIMD, one's additions and conversions running under the other's products.  A stage of LDS holds a block of k; while
+// it is read, the next one is copied.
 template <class H, int KIND, bool DIRECT>
-__global__ __launch_bounds__(kThreads, 1) void tile8_kernel(FfnArgs p, int32_t ncols) {
+__global__ __launch_bounds__(kThreads8) void tile8_kernel(FfnArgs p, int32_t ncols) {
   constexpr bool kUp = KIND == kFfnUp;
   constexpr int kOut = kUp ? kCols8 / 2 : kCols8;  // output columns of a tile
-  __shared__ __attribute__((aligned(16))) uint8_t lds[3 * kStage8];
-  static_assert(3 * kStage8 >= kResultBytes + 2 * kRows * 4, "results use the stages' LDS");
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kStage8];
+  static_assert(2 * kStage8 >= kResults8 + 2 * kRows8 * 4, "results use the stages' LDS");
 
   const int32_t kb = (p.K + kB - 1) / kB;
   int32_t rowtiles, e, lo, hi, m0, col;
@@ -163,65 +168,68 @@ __global__ __launch_bounds__(kThreads, 1) void tile8_kernel(FfnArgs p, int32_t n
   const int32_t id = split ? plan.whole + (item - plan.whole) % rest : xcd_run(item, plan.whole);
   const int32_t sp = split ? (item - plan.whole) / rest : 0, parts = split ? plan.splits : 1;
   const int32_t q0 = kb * sp / parts, q1 = kb * (sp + 1) / parts;
-  if (!find_tile<kRows>(p.offsets, p.T, p.E, ncols, rowtiles, first, id, e, lo, hi, m0, col)) return;
+  if (!find_tile<kRows8>(p.offsets, p.T, p.E, ncols, rowtiles, first, id, e, lo, hi, m0, col)) return;
   const int32_t n0 = col * kOut, N = p.N, K = p.K;
   if (KIND == kLinear && p.bias) p.bias += static_cast<int64_t>(e) * N;
   const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6), wm = w >> 1, wn = w & 1;
   const int half = lane >> 5, l32 = lane & 31;
   const int32_t nb = (N + kB - 1) / kB;
 
-  // This thread's 16-byte chunks of a stage: chunk c of rows t / 8 + 32 j; rows past the end repeat the last.
-  const int c16 = ((t & 7) ^ swizzle_a(t >> 3)) * 16, r0 = t >> 3;
-  uint32_t aoff[4], boff[8];
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    aoff[j] = static_cast<uint32_t>(min(r0 + 32 * j, hi - 1 - m0)) * static_cast<uint32_t>(K) + c16;
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    boff[j] = static_cast<uint32_t>(min(r0 + 32 * (kUp ? j % 4 : j), N - 1 - n0)) * static_cast<uint32_t>(K) + c16;
-  const uint32_t soff = static_cast<uint32_t>(min(t & (kRows - 1), hi - 1 - m0)) * static_cast<uint32_t>(kb) * 4;
+  // This thread's 16-byte chunks of a stage: chunk c16 of rows t / 8 + 64 j of x and of the weights.  Rows past the
+  // run's or the weight's end are whatever lies there (nothing behind the tensors is read): their results are
+  // not stored, and no other result depends on them.
+  const int r0 = t >> 3, c16 = ((t & 7) ^ swizzle_a(r0)) * 16;
+  const uint32_t roff = static_cast<uint32_t>(r0) * static_cast<uint32_t>(K) + c16, rstep = 64u * static_cast<uint32_t>(K);
   const int64_t abase = static_cast<int64_t>(m0) * K, bbase = (static_cast<int64_t>(e) * N + n0) * K;
-
   const float* const xs = p.xs + static_cast<int64_t>(m0) * kb;
-  // (the buffers end with the tensors: what lies behind is not read)
+  // the weights' scales, one per block of k: of the two blocks of 128 columns, up: of gate and up
+  const float* ws[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    ws[k] = (kUp && k ? p.s1 : p.s0) + (static_cast<int64_t>(e) * nb + min(n0 / kB + (kUp ? 0 : k), nb - 1)) * kb;
   const int64_t wleft = static_cast<int64_t>(p.E) * N * K - bbase;
   const buffer_t xbuf = make_buffer(p.x0 + abase, static_cast<int64_t>(p.T - m0) * K),
                  w0buf = make_buffer(p.w0 + bbase, wleft), w1buf = make_buffer((kUp ? p.w1 : p.w0) + bbase, wleft),
-                 sbuf = make_buffer(reinterpret_cast<const uint8_t*>(xs), static_cast<int64_t>(p.T - m0) * kb * 4);
+                 sbuf = make_buffer(reinterpret_cast<const uint8_t*>(w < 4 ? xs : ws[w & 1]),
+                                    (w < 4 ? static_cast<int64_t>(p.T - m0) * kb : kb) * 4);
+  const uint32_t soff = w < 4 ? static_cast<uint32_t>(t) * static_cast<uint32_t>(kb) * 4 : 0;
   const uint32_t lds0 = lds_address(lds);
-  // copy j of kCopies of the stage at LDS offset `to`
+  // copy j of kCopies of block q to the stage at LDS offset `to`
   auto copy = [&](int j, int32_t q, uint32_t to) {
     const uint32_t at = lds0 + to + w * 1024;
     if (j < 4)
-      copy_to_lds<16>(xbuf, aoff[j], q * kB, at + j * (kThreads * 16));
-    else if (j < 12)
-      copy_to_lds<16>(j < 8 ? w0buf : w1buf, boff[j - 4], q * kB, at + kA8 + (j - 4) * (kThreads * 16));
-    else  // (by two waves each: as many copies of every wave)
-      copy_to_lds<4>(sbuf, soff, q * 4, lds0 + to + kA8 + kB8 + (w & 1) * 256);
+      copy_to_lds<16>(xbuf, roff, q * kB + j * rstep, at + j * (kThreads8 * 16));
+    else if (j < 8)
+      copy_to_lds<16>(j < 6 ? w0buf : w1buf, roff, q * kB + (kUp ? j & 1 : j - 4) * rstep,
+                      at + kA8 + (j - 4) * (kThreads8 * 16));
+    else  // (the weights' by two waves each: as many copies of every wave)
+      copy_to_lds<4>(sbuf, soff, q * 4, lds0 + to + kScales8 + w * 256);
   };
-  // Through registers: batch b of 3, 4 of the 12 chunks, and the scales with the first.
-  uint4 held[4];
-  float scale_held = 0.0f;
-  auto fetch = [&](int batch, int32_t q) {
-    const int32_t k0 = q * kB;
-    const uint8_t* const from = (batch == 0 ? p.x0 + abase : (kUp && batch == 2 ? p.w1 : p.w0) + bbase) + k0;
-    const uint32_t* const off = batch == 0 ? aoff : boff + 4 * (batch - 1);
-    const int n = K - k0 - c16;  // codes of the row from this chunk on
+  // Through registers: half h of the 8 chunks, and the scales with the first.
+  auto fetch = [&](int h, int32_t q, uint8_t* to) {
+    const int32_t k0 = q * kB, n = K - k0 - c16;  // codes of the row from this chunk on
+    uint4 held[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) held[j] = k0 + kB <= K ? ld16(from + off[j]) : ld16_part(from + off[j], n, k0 + c16);
-    if (batch == 0) scale_held = xs[soff / 4 + q];
-  };
-  auto put = [&](int batch, uint8_t* to) {
+    for (int j = 0; j < 4; ++j) {
+      // (a row past the tensor's last one is not there to be read)
+      const int r = r0 + 64 * (kUp && h ? j & 1 : j);
+      const uint8_t* const from = h == 0 ? p.x0 + abase + static_cast<int64_t>(min(r, p.T - 1 - m0)) * K
+                                         : (kUp && j >= 2 ? p.w1 : p.w0) + bbase + static_cast<int64_t>(min(r, N - 1 - n0)) * K;
+      held[j] = k0 + kB <= K ? ld16(from + k0 + c16) : ld16_part(from + k0 + c16, n, k0 + c16);
+    }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(to + (t + kThreads * (4 * batch + j)) * 16) = held[j];
-    if (batch == 0 && t < kRows) *reinterpret_cast<float*>(to + kA8 + kB8 + t * 4) = scale_held;
+    for (int j = 0; j < 4; ++j)
+      *reinterpret_cast<uint4*>(to + h * kA8 + (t + kThreads8 * j) * 16) = held[j];
+    if (h == 0)
+      *reinterpret_cast<float*>(to + kScales8 + t * 4) =
+          t < kRows8 ? xs[static_cast<int64_t>(min(t, p.T - 1 - m0)) * kb + q] : ws[w & 1][q];
   };
   // Clears what the last stage holds past the end of k (both operands: 0 times a NaN is none).
   auto clear_past = [&](uint8_t* at) {
     const int n = K - (kb - 1) * kB - c16;
     if (n >= 16) return;
-    for (int j = 0; j < 12; ++j) {
-      uint4* const x = reinterpret_cast<uint4*>(at + (t + kThreads * j) * 16);
+    for (int j = 0; j < 8; ++j) {
+      uint4* const x = reinterpret_cast<uint4*>(at + (t + kThreads8 * j) * 16);
       uint4 v = *x;
       uint32_t* const o[4] = {&v.x, &v.y, &v.z, &v.w};
 #pragma unroll
@@ -232,13 +240,53 @@ __global__ __launch_bounds__(kThreads, 1) void tile8_kernel(FfnArgs p, int32_t n
       *x = v;
     }
   };
+  const bool tail = DIRECT && K % kB != 0;
+  uint32_t cur = 0, next = kStage8;  // LDS offsets of the stages of blocks q and q + 1
+  // Block q + 1 is in its stage, and all waves have read block q: its stage is free for block q + 2.
+  auto turn_over = [&](int32_t q) {
+    if (DIRECT)
+      meet<0>();
+    else
+      __syncthreads();
+    if (tail && q + 2 == kb) {
+      clear_past(lds + next);
+      __syncthreads();
+    }
+  };
+  auto first_stages = [&] {
+    if (DIRECT) {
+#pragma unroll
+      for (int j = 0; j < kCopies; ++j) copy(j, q0, 0);
+      meet<0>();
+#pragma unroll
+      for (int j = 0; j < kCopies; ++j) copy(j, min(q0 + 1, q1 - 1), kStage8);
+    } else {
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) fetch(h, min(q0 + k, q1 - 1), lds + k * kStage8);
+      __syncthreads();
+    }
+    if (tail && q0 == kb - 1) {
+      clear_past(lds);
+      __syncthreads();
+    }
+  };
 
   const int swz = swizzle_a(l32);  // (that of every row read: they lie 32 apart)
-  // the weights' scales of this wave's columns, one per block of k (two matrices: one each)
-  const int32_t nblk = min((n0 + (kUp ? 0 : wn * 128)) / kB, nb - 1);
-  const int64_t sat = (static_cast<int64_t>(e) * nb + nblk) * kb;
-  typedef const __attribute__((address_space(4))) float* scalar_t;
-  auto wscale = [&](int32_t q, int which) { return ((scalar_t)((which ? p.s1 : p.s0) + sat))[q]; };
+  // chunk c of this lane's half of a row of x, and of a weight's (up: two tile columns of gate, then the same of up)
+  auto chunk_x = [&](uint32_t from, int i, int c) {
+    return *reinterpret_cast<const uint4*>(lds + from + (wm * 64 + i * 32 + l32) * kB + (((half * 4 + c) ^ swz) << 4));
+  };
+  auto chunk_w = [&](uint32_t from, int j, int c) {
+    const int r = kUp ? (j / 2) * 128 + wn * 64 + (j % 2) * 32 : wn * 128 + j * 32;
+    return *reinterpret_cast<const uint4*>(lds + from + kA8 + (r + l32) * kB + (((half * 4 + c) ^ swz) << 4));
+  };
+  auto scale_x = [&](uint32_t from, int i) {
+    return *reinterpret_cast<const float*>(lds + from + kScales8 + (wm * 64 + i * 32 + l32) * 4);
+  };
+  auto scale_w = [&](uint32_t from, int k) {
+    return *reinterpret_cast<const float*>(lds + from + kScales8 + 1024 + k * 256);
+  };
 
   f32x16 acc[2][4];
   const f32x16 zero = {};
@@ -247,49 +295,15 @@ __global__ __launch_bounds__(kThreads, 1) void tile8_kernel(FfnArgs p, int32_t n
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = zero;
 
-  const bool tail = DIRECT && K % kB != 0;
-  uint32_t cur = 0, next = kStage8, last = 2 * kStage8;  // LDS offsets of stages q, q + 1 and q + 2
-  auto rotate = [&] {
-    const uint32_t x = cur;
-    cur = next;
-    next = last;
-    last = x;
-  };
-  if (DIRECT) {
-#pragma unroll 1
-    for (int k = 0; k < 3; ++k)
-#pragma unroll
-      for (int j = 0; j < kCopies; ++j) copy(j, min(q0 + k, q1 - 1), k * kStage8);
-    meet<2 * kCopies>();
-  } else {
-#pragma unroll 1
-    for (int k = 0; k < 3; ++k)
-#pragma unroll
-      for (int b = 0; b < 3; ++b) {
-        fetch(b, min(q0 + k, q1 - 1));
-        put(b, lds + k * kStage8);
-      }
-    __syncthreads();
-  }
-  if (tail && q0 == kb - 1) {
-    clear_past(lds);
-    __syncthreads();
-  }
+  first_stages();
   if constexpr (kUp) {
     // Gate and up: codes widened to bfloat16, which holds them, so that the sums are float32 sums (see the top).
     // A step is 32 k, chunk c of a block's 4 from both halves of the lanes, two matrix instructions for each of the
-    // 8 tiles.  In its 8 slots, a tile's instructions each, the next step's chunks are read from LDS and
-    // widened: a weight's when its two tiles of this step are done, x's into another set.
+    // 8 tiles, in 16 slots of one instruction.  Meanwhile the next step's chunks are read from LDS and widened: a
+    // weight's when its tiles of this step are done, x's into another set.
     typedef Bf16::v8 v8;
     v8 W[4][2], X[2][2][2];
     uint4 rw[4], rx[2];
-    auto read_x = [&](uint32_t from, int c, int i) {
-      rx[i] = *reinterpret_cast<const uint4*>(lds + from + (wm * 64 + i * 32 + l32) * kB + (((half * 4 + c) ^ swz) << 4));
-    };
-    auto read_w = [&](uint32_t from, int c, int j) {  // (two tile columns of gate, then the same of up)
-      rw[j] = *reinterpret_cast<const uint4*>(lds + from + kA8 + ((j / 2) * 128 + wn * 64 + (j % 2) * 32 + l32) * kB +
-                                              (((half * 4 + c) ^ swz) << 4));
-    };
     auto wide_x = [&](int set, int i, int k) {
       X[set][i][k] = k ? widen8<Bf16>(rx[i].z, rx[i].w) : widen8<Bf16>(rx[i].x, rx[i].y);
     };
@@ -299,20 +313,23 @@ __global__ __launch_bounds__(kThreads, 1) void tile8_kernel(FfnArgs p, int32_t n
     // tile is done again, block by block.
     float s[2][2], ratio[2][2];
     bool near = true;
-    auto scales = [&](uint32_t from, const float (&sw)[2], float (&to)[2][2]) {
+    auto scales = [&](uint32_t from, float (&to)[2][2]) {
+      const float sw[2] = {scale_w(from, 0), scale_w(from, 1)};
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float sx = *reinterpret_cast<const float*>(lds + from + kA8 + kB8 + (wm * 64 + i * 32 + l32) * 4);
+        // (rows past the run have no part in this)
+        const float sx = m0 + wm * 64 + i * 32 + l32 < hi ? scale_x(from, i) : 1.0f;
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           to[i][k] = sx * sw[k];
-          near = near && to[i][k] >= 0x1p-70f && to[i][k] <= 0x1p20f;
+          near = near && (m0 + wm * 64 + i * 32 + l32 >= hi || (to[i][k] >= 0x1p-70f && to[i][k] <= 0x1p20f));
         }
       }
     };
-    auto rescale = [&](int u, int r0) {
+    // 4 of a tile's results to the new units; tiles in the order of the slots: (i, j) = (k % 2, k / 2)
+    auto rescale = [&](int k, int r0) {
 #pragma unroll
-      for (int r = r0; r < r0 + 8; ++r) acc[u & 1][u >> 1][r] *= ratio[u & 1][u >> 2];
+      for (int r = r0; r < r0 + 4; ++r) acc[k & 1][k >> 1][r] *= ratio[k & 1][k >> 2];
     };
     auto pin = [&] {  // (the work stays in its step: nothing of it is moved past a barrier behind it)
 #pragma unroll
@@ -324,101 +341,65 @@ __global__ __launch_bounds__(kThreads, 1) void tile8_kernel(FfnArgs p, int32_t n
     };
     // Block q; its first chunk is in X[0] and W (W[3] in rw[3]).  Leaves the next block's so.
     auto turn = [&](int32_t q) {
-      const int32_t far = min(q + 3, q1 - 1), after = min(q + 1, q1 - 1);
-      const float sw[2] = {wscale(after, 0), wscale(after, 1)};
+      const int32_t far = min(q + 2, q1 - 1);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        uint32_t from = cur;
         if (c == 3) {
           pin();
-          if (DIRECT)
-            meet<kCopies>();  // stage q + 1 is there, and all waves have read stage q
-          else
-            __syncthreads();
-          if (tail && q + 2 == kb) {
-            clear_past(lds + next);
-            __syncthreads();
-          }
-          from = next;
+          turn_over(q);
         }
+        const uint32_t from = c == 3 ? next : cur;
         const int set = c & 1, cn = (c + 1) & 3;
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int i = u & 1, j = u >> 1;
-          acc[i][j] = Bf16::mma32(W[j][0], X[set][i][0], acc[i][j]);
+        for (int v = 0; v < 16; ++v) {
+          const int j = v >> 2, i = v & 1, k = (v >> 1) & 1;
+          acc[i][j] = Bf16::mma32(W[j][k], X[set][i][k], acc[i][j]);
           __builtin_amdgcn_sched_barrier(0);
-          if (u == 0) {
-            read_x(from, cn, 0);
-            read_w(from, cn, 0);
-            wide_w(3, 0);
-          } else if (u == 1) {
-            read_x(from, cn, 1);
-            read_w(from, cn, 1);
-          } else if (u == 2) {
-            read_w(from, cn, 2);
-            wide_x(set ^ 1, 0, 0);
-          } else if (u == 3) {
-            wide_x(set ^ 1, 0, 1);
-          } else if (u == 4) {
-            wide_w(0, 1);
-          } else if (u == 5) {
-            read_w(from, cn, 3);
-            wide_x(set ^ 1, 1, 1);
-          } else if (u == 6) {
-            wide_w(1, 1);
-          } else {
-            wide_w(2, 1);
-          }
-          if (c == 0 && u < 7) rescale(u + 1, 0);
-          __builtin_amdgcn_sched_barrier(0);
-          acc[i][j] = Bf16::mma32(W[j][1], X[set][i][1], acc[i][j]);
-          __builtin_amdgcn_sched_barrier(0);
-          if (u == 1) {
-            wide_w(3, 1);
-          } else if (u == 3) {
-            wide_w(0, 0);
-          } else if (u == 4) {
-            wide_x(set ^ 1, 1, 0);
-          } else if (u == 5) {
-            wide_w(1, 0);
-          } else if (u == 6) {
-            wide_w(2, 0);
-          }
-          if (c == 0 && u < 7) rescale(u + 1, 8);
+          if (v == 0) rw[0] = chunk_w(from, 0, cn);
+          if (v == 1) rx[0] = chunk_x(from, 0, cn);
+          if (v == 2) rw[1] = chunk_w(from, 1, cn);
+          if (v == 3) rx[1] = chunk_x(from, 1, cn);
+          if (v == 4) rw[2] = chunk_w(from, 2, cn);
+          if (v == 6) rw[3] = chunk_w(from, 3, cn);
+          if (v < 2) wide_w(3, v);
+          if (v == 5 || v == 6) wide_w(0, v - 5);
+          if (v == 7 || v == 8) wide_x(set ^ 1, 0, v - 7);
+          if (v == 9 || v == 10) wide_w(1, v - 9);
+          if (v == 11 || v == 12) wide_x(set ^ 1, 1, v - 11);
+          if (v == 13 || v == 14) wide_w(2, v - 13);
           if (c == 3) {
-            if (DIRECT) {
-              copy(u, far, cur);
-              if (u + 8 < kCopies) copy(u + 8, far, cur);
-            } else if (u < 3) {
-              fetch(u, far);
-              put(u, lds + cur);
-            }
-            if (u == 3) {
+            if (DIRECT && v < kCopies) copy(v, far, cur);
+            if (!DIRECT && v < 2) fetch(v, far, lds + cur);
+            if (v == 3) {
               float to[2][2];
-              scales(next, sw, to);
+              scales(next, to);
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                ratio[k >> 1][k & 1] = s[k >> 1][k & 1] * __builtin_amdgcn_rcpf(to[k >> 1][k & 1]);
-                s[k >> 1][k & 1] = to[k >> 1][k & 1];
+              for (int h = 0; h < 4; ++h) {
+                ratio[h >> 1][h & 1] = s[h >> 1][h & 1] * __builtin_amdgcn_rcpf(to[h >> 1][h & 1]);
+                s[h >> 1][h & 1] = to[h >> 1][h & 1];
               }
             }
-            if (u == 7) {
-              rescale(0, 0);
-              rescale(0, 8);
-            }
+            // tiles 0 and 1 are done with the block in slot 3, 2 and 3 in slot 7
+            if (v >= 8 && v < 12) rescale(0, 4 * (v - 8));
+            if (v >= 12) rescale(1, 4 * (v - 12));
+          }
+          if (c == 0 && v < 12) {  // tiles 2 to 7, two parts a slot
+            rescale(2 + v / 2, 8 * (v & 1));
+            rescale(2 + v / 2, 8 * (v & 1) + 4);
           }
           __builtin_amdgcn_sched_barrier(0);
         }
       }
-      rotate();
+      const uint32_t x = cur;
+      cur = next;
+      next = x;
     };
-    const float sw0[2] = {wscale(q0, 0), wscale(q0, 1)};
-    scales(0, sw0, s);
+    scales(0, s);
 #pragma unroll
     for (int k = 0; k < 4; ++k) ratio[k >> 1][k & 1] = 1.0f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      read_w(0, 0, j);
+      rw[j] = chunk_w(0, j, 0);
       if (j < 3) {
         wide_w(j, 0);
         wide_w(j, 1);
@@ -426,20 +407,21 @@ __global__ __launch_bounds__(kThreads, 1) void tile8_kernel(FfnArgs p, int32_t n
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      read_x(0, 0, i);
+      rx[i] = chunk_x(0, i, 0);
       wide_x(0, i, 0);
       wide_x(0, i, 1);
     }
     for (int32_t q = q0; q < q1; ++q) turn(q);
     // (the last turn has fetched its own block as the next: its scales are the units still)
     if (DIRECT) wait_copies();
-    int32_t* const far_apart = reinterpret_cast<int32_t*>(lds + kResultBytes);
+    int32_t* const far_apart = reinterpret_cast<int32_t*>(lds + kResults8);
     __syncthreads();
     if (t == 0) *far_apart = 0;
     __syncthreads();
     if (!near) *far_apart = 1;
     __syncthreads();
-    if (!*far_apart) {
+    const bool again = *far_apart != 0;
+    if (!again) {
 #pragma unroll
       for (int u = 0; u < 8; ++u)
 #pragma unroll
@@ -457,10 +439,7 @@ __global__ __launch_bounds__(kThreads, 1) void tile8_kernel(FfnArgs p, int32_t n
             wait_copies();
           } else {
 #pragma unroll
-            for (int b = 0; b < 3; ++b) {
-              fetch(b, q);
-              put(b, lds);
-            }
+            for (int h = 0; h < 2; ++h) fetch(h, q, lds);
           }
           __syncthreads();
           if (tail && q + 1 == kb) {
@@ -470,24 +449,20 @@ __global__ __launch_bounds__(kThreads, 1) void tile8_kernel(FfnArgs p, int32_t n
           f32x16 part[2] = {zero, zero};
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
-            read_w(0, c, j);
+            const uint4 cw = chunk_w(0, j, c);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              read_x(0, c, i);
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const v8 wk = k ? widen8<Bf16>(rw[j].z, rw[j].w) : widen8<Bf16>(rw[j].x, rw[j].y);
-                const v8 xk = k ? widen8<Bf16>(rx[i].z, rx[i].w) : widen8<Bf16>(rx[i].x, rx[i].y);
-                part[i] = Bf16::mma32(wk, xk, part[i]);
-              }
+              const uint4 cx = chunk_x(0, i, c);
+              part[i] = Bf16::mma32(widen8<Bf16>(cw.x, cw.y), widen8<Bf16>(cx.x, cx.y), part[i]);
+              part[i] = Bf16::mma32(widen8<Bf16>(cw.z, cw.w), widen8<Bf16>(cx.z, cx.w), part[i]);
             }
           }
-          const float sw = wscale(q, j / 2);
+          const float sw = scale_w(0, j / 2);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float sx = *reinterpret_cast<const float*>(lds + kA8 + kB8 + (wm * 64 + i * 32 + l32) * 4);
+            const float sq = scale_x(0, i) * sw;
 #pragma unroll
-            for (int r = 0; r < 16; ++r) acc[i][j][r] = fmaf(sx * sw, part[i][r], acc[i][j][r]);
+            for (int r = 0; r < 16; ++r) acc[i][j][r] = fmaf(sq, part[i][r], acc[i][j][r]);
           }
         }
       };
@@ -497,105 +472,82 @@ __global__ __launch_bounds__(kThreads, 1) void tile8_kernel(FfnArgs p, int32_t n
       pass(Int<3>{});
     }
   } else {
-    struct Block {
-      uint4 x[2][4], w[4][4];
-      float s[2];
-    };
-    // part u of 8 of a block's reads: 3 chunks, x first; and its scales
-    auto read = [&](const uint8_t* from, Block& b, int u) {
+    // Tile column j of a block: the weights' 4 chunks are read a column ahead, x's stay.  A tile's two products go to one
+    // of two partial sums, which are added to acc under the next tile's products.
+    uint4 x[2][4], w4[2][4];
+    f32x16 part[2];
+    part[1] = zero;
+    float s[2] = {0.0f, 0.0f}, was = 0.0f;  // `was`: the scale of the tile before the first
+    auto read_x = [&](uint32_t from, int i) {
 #pragma unroll
-      for (int k = 3 * u; k < 3 * u + 3; ++k) {
-        const int c = k & 3, at = ((half * 4 + c) ^ swz) << 4;
-        if (k < 8) {
-          b.x[k >> 2][c] = *reinterpret_cast<const uint4*>(from + (wm * 64 + l32) * kB + at + (k >> 2) * (32 * kB));
-        } else {
-          const int j = (k - 8) >> 2;
-          b.w[j][c] = *reinterpret_cast<const uint4*>(from + kA8 + (wn * 128 + j * 32 + l32) * kB + at);
-        }
-      }
-      if (u == 0)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          b.s[i] = *reinterpret_cast<const float*>(from + kA8 + kB8 + (wm * 64 + i * 32 + l32) * 4);
+      for (int c = 0; c < 4; ++c) x[i][c] = chunk_x(from, i, c);
     };
-
-    // Tile u of a block: column j = u / 2 of the weights, row i = u % 2 of x.  Its two products go to one of four
-    // partial sums, which are added to acc two tiles later: a result may be read some 20 instructions after its
-    // product is issued, and the additions of one tile run under the products of another.
-    f32x16 part[4];
-    part[2] = part[3] = zero;
-    float s[2] = {};  // of the block before: its last two tiles are still to be added
-    auto add = [&](int u, int r0) {
+    auto read_w = [&](uint32_t from, int j) {
 #pragma unroll
-      for (int r = r0; r < r0 + 8; ++r)
-        acc[u & 1][u >> 1][r] = fmaf(s[u & 1], part[u & 3][r], acc[u & 1][u >> 1][r]);
+      for (int c = 0; c < 4; ++c) w4[j & 1][c] = chunk_w(from, j, c);
     };
-
-    // Block q out of registers; block q + 1 from LDS to registers, block q + 3 from memory to LDS.
-    auto turn = [&](int32_t q, const Block& now, Block& then) {
-      if (DIRECT)
-        meet<kCopies>();  // stage q + 1 is there, and all waves have read stage q
-      else
-        __syncthreads();
-      if (tail && q + 2 == kb) {
-        clear_past(lds + next);
-        __syncthreads();
-      }
-      // (the last turns fetch the last block again rather than branch)
-      const int32_t far = min(q + 3, q1 - 1);
-      const float sw = wscale(q, 0);
+    auto add = [&](int u, int r0, float by) {
+#pragma unroll
+      for (int r = r0; r < r0 + 8; ++r) acc[u & 1][u >> 1][r] = fmaf(by, part[u & 1][r], acc[u & 1][u >> 1][r]);
+    };
+    read_x(0, 0);
+    read_w(0, 0);
+    read_x(0, 1);
+    float sx[2] = {scale_x(0, 0), scale_x(0, 1)}, sw = scale_w(0, wn);
+    for (int32_t q = q0; q < q1; ++q) {
+      const int32_t far = min(q + 2, q1 - 1);
+      s[0] = sx[0] * sw;
+      s[1] = sx[1] * sw;
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
-        const int i = u & 1, j = u >> 1, before = (u + 6) & 7;
-        f32x16 d = mma8(code32(now.w[j][0], now.w[j][1]), code32(now.x[i][0], now.x[i][1]), zero);
-        __builtin_amdgcn_sched_barrier(0);
-        read(lds + next, then, u);
-        add(before, 0);
-        __builtin_amdgcn_sched_barrier(0);
-        part[u & 3] = mma8(code32(now.w[j][2], now.w[j][3]), code32(now.x[i][2], now.x[i][3]), d);
-        __builtin_amdgcn_sched_barrier(0);
-        if (DIRECT) {
-          copy(u, far, cur);
-          if (u + 8 < kCopies) copy(u + 8, far, cur);
-        } else {
-          if (u == 2 || u == 4 || u == 7) put(u / 3, lds + cur);
-          if (u == 0 || u == 2 || u == 4) fetch(u / 2, far);
-        }
-        add(before, 8);
-        if (u == 1)
+        const int i = u & 1, j = u >> 1, before = (u + 7) & 7;
+        if (u == 6) {
 #pragma unroll
-          for (int k = 0; k < 2; ++k) s[k] = now.s[k] * sw;
+          for (int k = 0; k < 8; ++k) asm volatile("" : "+v"(acc[k & 1][k >> 1]));
+          asm volatile("" : "+v"(part[1]));
+          turn_over(q);
+        }
+        f32x16 d = mma8(code32(w4[j & 1][0], w4[j & 1][1]), code32(x[i][0], x[i][1]), zero);
+        __builtin_amdgcn_sched_barrier(0);
+        if (i == 0 && j < 3) read_w(cur, j + 1);
+        if (u == 6) read_w(next, 0);
+        add(before, 0, u == 0 ? was : s[before & 1]);
+        __builtin_amdgcn_sched_barrier(0);
+        part[i] = mma8(code32(w4[j & 1][2], w4[j & 1][3]), code32(x[i][2], x[i][3]), d);
+        __builtin_amdgcn_sched_barrier(0);
+        if (u == 6) {
+          read_x(next, 0);
+          sx[0] = scale_x(next, 0);
+          sx[1] = scale_x(next, 1);
+          sw = scale_w(next, wn);
+        }
+        if (u == 7) read_x(next, 1);
+        if (u >= 6) {
+          if (DIRECT) {
+#pragma unroll
+            for (int k = 0; k < 5; ++k)
+              if ((u - 6) * 5 + k < kCopies) copy((u - 6) * 5 + k, far, cur);
+          } else {
+            fetch(u - 6, far, lds + cur);
+          }
+        }
+        add(before, 8, u == 0 ? was : s[before & 1]);
         __builtin_amdgcn_sched_barrier(0);
       }
-      // (the work stays in its turn: nothing of it is moved past the next turn's barrier)
-#pragma unroll
-      for (int u = 0; u < 8; ++u) asm volatile("" : "+v"(acc[u & 1][u >> 1]));
-      asm volatile("" : "+v"(part[2]));
-      asm volatile("" : "+v"(part[3]));
-      rotate();
-    };
-
-    Block b0, b1;
-#pragma unroll
-    for (int u = 0; u < 8; ++u) read(lds, b0, u);
-    int32_t q = q0;
-    for (; q + 1 < q1; q += 2) {
-      turn(q, b0, b1);
-      turn(q + 1, b1, b0);
+      was = s[1];
+      const uint32_t y = cur;
+      cur = next;
+      next = y;
     }
-    if (q < q1) turn(q, b0, b1);
-#pragma unroll
-    for (int u = 6; u < 8; ++u) {
-      add(u, 0);
-      add(u, 8);
-    }
+    add(7, 0, was);
+    add(7, 8, was);
+    if (DIRECT) wait_copies();
+    __syncthreads();  // the results take the stages' place
   }
-  if (DIRECT) wait_copies();
-  __syncthreads();  // the results take the stages' place
 
   uint8_t* const mine = lds + w * (kResultBytes / 4);
   const int32_t mw = m0 + wm * 64;
-  if (split) {  // float32 sums [128][256], up: gate's 128 columns, then up's
+  if (split) {  // float32 sums [256][256], up: gate's 128 columns, then up's
     float* const to = part8_at(p.part, item - plan.whole) + static_cast<int64_t>(wm * 64) * kCols8;
 #pragma unroll 1
     for (int half_ = 0; half_ < 2; ++half_) {
@@ -663,7 +615,7 @@ __global__ __launch_bounds__(kThreads, 1) void tile8_kernel(FfnArgs p, int32_t n
       }
     }
     // a in place of gate; the largest magnitude of a row over this wave's 64 columns, then over both waves'
-    float* const tops = reinterpret_cast<float*>(lds + kResultBytes);  // [2][128]
+    float* const tops = reinterpret_cast<float*>(lds + kResults8);  // [2][256]
     float top[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -677,20 +629,21 @@ __global__ __launch_bounds__(kThreads, 1) void tile8_kernel(FfnArgs p, int32_t n
           top[i] = fmaxf(top[i], n < N ? fabsf(a) : 0.0f);
         }
       top[i] = fmaxf(top[i], __shfl_xor(top[i], 32));
-      if (half == 0) tops[wn * kRows + wm * 64 + i * 32 + l32] = top[i];
+      if (half == 0) tops[wn * kRows8 + wm * 64 + i * 32 + l32] = top[i];
     }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int r = wm * 64 + i * 32 + l32;
-      const float scale = row8_scale(fmaxf(top[i], tops[(1 - wn) * kRows + r]), p.pow2 != 0);
+      const float scale = row8_scale(fmaxf(top[i], tops[(1 - wn) * kRows8 + r]), p.pow2 != 0);
+      const Over8 over = over8(scale, p.pow2 != 0);
       if (wn == 0 && half == 0 && m0 + r < hi) p.code_scales[static_cast<int64_t>(m0 + r) * nb + n0 / kB] = scale;
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int g = 0; g < 4; ++g)
           *reinterpret_cast<uint32_t*>(mine + (i * 32 + l32) * 64 + ((j * 32 + 8 * g + 4 * half) ^ ((l32 & 3) << 4))) =
-              codes4(acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3], scale);
+              codes4(acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3], over);
     }
     handed_over();
     for (int k = 0; k < 4; ++k) {
@@ -716,21 +669,21 @@ __global__ __launch_bounds__(kThreads, 1) void tile8_kernel(FfnArgs p, int32_t n
 template <class H, int KIND>
 __global__ __launch_bounds__(kThreads) void join8_kernel(FfnArgs p, int32_t ncols) {
   constexpr bool kUp = KIND == kFfnUp;
-  constexpr int kOut = kUp ? kCols8 / 2 : kCols8, kLanes = kOut / 8, kTurns = kRows * kLanes / kThreads;
+  constexpr int kOut = kUp ? kCols8 / 2 : kCols8, kLanes = kOut / 8, kTurns = kRows8 * kLanes / kThreads;
   const int32_t kb = (p.K + kB - 1) / kB;
   int32_t rowtiles, e, lo, hi, m0, col;
   Run first;
   const Plan plan = plan_tiles8(p, ncols, kb, rowtiles, first);
   const int32_t rest = plan.tiles - plan.whole, tile = static_cast<int32_t>(blockIdx.x) / kTurns;
   if (tile >= rest) return;
-  if (!find_tile<kRows>(p.offsets, p.T, p.E, ncols, rowtiles, first, plan.whole + tile, e, lo, hi, m0, col)) return;
+  if (!find_tile<kRows8>(p.offsets, p.T, p.E, ncols, rowtiles, first, plan.whole + tile, e, lo, hi, m0, col)) return;
   if (KIND == kLinear && p.bias) p.bias += static_cast<int64_t>(e) * p.N;
   const int r = static_cast<int>(blockIdx.x % kTurns) * (kThreads / kLanes) + threadIdx.x / kLanes, c = threadIdx.x % kLanes;
   const int32_t n = col * kOut + 8 * c, m = m0 + r, count = m < hi ? min(p.N - n, 8) : 0;
   float x[8] = {}, v[8] = {};
   if (m < hi) {  // (the parts of rows past the run were not written)
     const f32x4* from = reinterpret_cast<const f32x4*>(part8_at(p.part, tile) + static_cast<int64_t>(r) * kCols8 + 8 * c);
-    const int64_t step = static_cast<int64_t>(rest) * (kRows * kCols8) / 4;
+    const int64_t step = static_cast<int64_t>(rest) * (kRows8 * kCols8) / 4;
 #pragma unroll 4
     for (int32_t s = 0; s < plan.splits; ++s)
 #pragma unroll
@@ -760,6 +713,7 @@ __global__ __launch_bounds__(kThreads) void join8_kernel(FfnArgs p, int32_t ncol
 template <class H, int KIND, int WAVES, int TT, bool ALIGNED>
 __global__ __launch_bounds__(WAVES * 64) void rows8_kernel(FfnArgs p) {
   constexpr bool kUp = KIND == kFfnUp;
+  constexpr int kDeep = TT == 1 ? 4 : 2;
   __shared__ f32x4 sums[WAVES][TT][64];
   int32_t e, lo, hi, t0;
   const int32_t group = static_cast<int32_t>(blockIdx.z * gridDim.y + blockIdx.y);
@@ -821,16 +775,18 @@ __global__ __launch_bounds__(WAVES * 64) void rows8_kernel(FfnArgs p) {
       for (int i = 0; i < 4; ++i) acc[t][i] = fmaf(s, part[i], acc[t][i]);
     }
   };
-  Block b0, b1;
-  if (w < kb) load(w, b0);
-  if (w + WAVES < kb) load(w + WAVES, b1);
-  for (int32_t q = w; q < kb; q += 2 * WAVES) {
-    add(b0);
-    if (q + 2 * WAVES < kb) load(q + 2 * WAVES, b0);
-    if (q + WAVES < kb) {
-      add(b1);
-      if (q + 3 * WAVES < kb) load(q + 3 * WAVES, b1);
-    }
+  // the blocks w, w + WAVES, .. of k, kDeep of them on their way
+  Block held[kDeep];
+#pragma unroll
+  for (int d = 0; d < kDeep; ++d)
+    if (w + d * WAVES < kb) load(w + d * WAVES, held[d]);
+  for (int32_t q = w; q < kb; q += kDeep * WAVES) {
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d)
+      if (q + d * WAVES < kb) {
+        add(held[d]);
+        if (q + (d + kDeep) * WAVES < kb) load(q + (d + kDeep) * WAVES, held[d]);
+      }
   }
 #pragma unroll
   for (int t = 0; t < TT; ++t) sums[w][t][lane] = acc[t];
@@ -893,9 +849,9 @@ void launch_rows8(const FfnArgs& p, bool aligned, hipStream_t s) {
   const bool deep = static_cast<int64_t>((p.N + 15) / 16) * (KIND == kFfnUp ? 2 : 1) * p.E < 1024;
   const bool two = static_cast<int64_t>(p.T) > 8ll * p.E;
   if (deep && two)
-    launch_rows8_as<H, KIND, 8, 2>(p, aligned, s);
+    launch_rows8_as<H, KIND, 16, 2>(p, aligned, s);
   else if (deep)
-    launch_rows8_as<H, KIND, 8, 1>(p, aligned, s);
+    launch_rows8_as<H, KIND, 16, 1>(p, aligned, s);
   else if (two)
     launch_rows8_as<H, KIND, 4, 2>(p, aligned, s);
   else
@@ -912,15 +868,15 @@ bool few_rows8(int64_t T, int64_t E) { return T <= 32 * E; }
 
 template <class H, int KIND>
 void launch_tiles8(const FfnArgs& p, bool direct, int64_t tiles, int32_t ncols, hipStream_t s) {
-  constexpr int kTurns = KIND == kFfnUp ? 8 : 16;
-  const dim3 g(static_cast<unsigned>(tiles + (p.part ? kSlots8 : 0))), b(kThreads);
+  constexpr int kTurns = KIND == kFfnUp ? 16 : 32;
+  const dim3 g(static_cast<unsigned>(tiles + (p.part ? kSlots8 : 0))), b(kThreads8), bj(kThreads);
   if (direct)
     hipLaunchKernelGGL((tile8_kernel<H, KIND, true>), g, b, 0, s, p, ncols);
   else
     hipLaunchKernelGGL((tile8_kernel<H, KIND, false>), g, b, 0, s, p, ncols);
   if (!p.part) return;
   const int64_t rest = tiles < kSlots8 ? tiles : kSlots8 - 1;
-  hipLaunchKernelGGL((join8_kernel<H, KIND>), dim3(static_cast<unsigned>(rest * kTurns)), b, 0, s, p, ncols);
+  hipLaunchKernelGGL((join8_kernel<H, KIND>), dim3(static_cast<unsigned>(rest * kTurns)), bj, 0, s, p, ncols);
 }
 
 template <int KIND>
@@ -938,10 +894,10 @@ int launch8(FfnArgs p, int32_t dtype, void* workspace, size_t workspace_bytes, h
   }
   const bool direct = !misaligned(p.x0, 4) && !misaligned(p.w0, 4) && !misaligned(p.w1, 4) && p.K % 4 == 0;
   const int32_t per = KIND == kFfnUp ? kCols8 / 2 : kCols8, ncols = (p.N + per - 1) / per;
-  const int64_t tiles = most_row_tiles(p.T, p.E) * ncols;
-  if (tiles > 0x7fffffff / kThreads - kSlots8) return refuse(FP8Z1_ESHAPE, what, "too many tiles");
+  const int64_t tiles = (p.T / kRows8 + (p.T < p.E ? p.T : p.E)) * static_cast<int64_t>(ncols);  // (every run may end in a partial tile)
+  if (tiles > 0x7fffffff / kThreads8 - kSlots8) return refuse(FP8Z1_ESHAPE, what, "too many tiles");
   const int32_t kb = (p.K + kB - 1) / kB;
-  const int64_t known = p.offsets ? tiles : static_cast<int64_t>((p.T + kRows - 1) / kRows) * ncols;
+  const int64_t known = p.offsets ? tiles : static_cast<int64_t>((p.T + kRows8 - 1) / kRows8) * ncols;
   if ((p.offsets ? kb >= 4 : tile_splits8(known, kb) > 1) && workspace_bytes >= part8_bytes())
     p.part = static_cast<float*>(workspace);
   if (dtype == FP8Z1_BF16)

@@ -188,6 +188,7 @@ struct RowsArgs {
   int64_t D, R;
   int32_t T, k;
   int32_t blocks;  // workgroups of a token (dispatch, combine)
+  int32_t chunks;  // 16-byte chunks of a thread (dispatch)
   int64_t items;   // workgroups that all tokens need; where a launch has fewer, they take several each
 };
 
@@ -199,48 +200,58 @@ __device__ __forceinline__ int64_t row_at(const RowsArgs& a, int32_t t, int32_t 
 
 typedef uint32_t v4u_a1_rw_global_t __attribute__((ext_vector_type(4), aligned(1), address_space(1)));
 
-// `bytes` of a token's row to its k places, 16 bytes per thread at any alignment; the last 16 overlap those
-// before them (the same bytes twice).  Rows of less go byte by byte.
-constexpr int kCopyThreads = 256;
+// A token's row of `bytes` to its k places: up to 4 chunks of 16 bytes per thread at any alignment, all loads before
+// the stores; the last chunk overlaps the one before it (the same bytes twice).  Rows of less than 16 go byte by byte.
+// Stores carry no hint: what follows reads the rows.
+constexpr int kCopyThreads = 256, kCopyChunks = 4;
 __device__ __forceinline__ void copy_rows(const RowsArgs& a, int32_t t, const uint8_t* x, uint8_t* rows, int64_t bytes,
-                                          int64_t at) {
+                                          int64_t first, int64_t step) {
   const uint8_t* const from = x + t * bytes;
   if (bytes < 16) {
-    const int64_t i = at / 16;
-    if (i >= bytes) return;
+    if (first >= 16 * bytes) return;
     for (int32_t j = 0; j < a.k; ++j) {
       const int64_t r = row_at(a, t, j);
-      if (r >= 0) rows[r * bytes + i] = from[i];
+      if (r >= 0) rows[r * bytes + first / 16] = from[first / 16];
     }
     return;
   }
-  if (at >= bytes) return;
-  at = min(at, bytes - 16);
-  const uint4 v = ld16(from + at);
+  uint4 v[kCopyChunks];
+  int64_t at[kCopyChunks];
+#pragma unroll
+  for (int i = 0; i < kCopyChunks; ++i) {
+    const int64_t c = first + i * step;
+    at[i] = c < bytes ? min(c, bytes - 16) : -1;
+    if (at[i] >= 0) v[i] = ld16(from + at[i]);
+  }
   for (int32_t j = 0; j < a.k; ++j) {
     const int64_t r = row_at(a, t, j);
-    if (r >= 0) *(v4u_a1_rw_global_t*)(rows + r * bytes + at) = v4u_v_t{v.x, v.y, v.z, v.w};
+    if (r < 0) continue;
+#pragma unroll
+    for (int i = 0; i < kCopyChunks; ++i)
+      if (at[i] >= 0) *(v4u_a1_rw_global_t*)(rows + r * bytes + at[i]) = v4u_v_t{v[i].x, v[i].y, v[i].z, v[i].w};
   }
 }
 
 // ELEM: bytes of an element.  EIGHT: the scales' rows too, by the last workgroup of a token.
 template <int ELEM, bool EIGHT>
 __global__ __launch_bounds__(kCopyThreads) void dispatch_kernel(RowsArgs a) {
+  constexpr int64_t kTurn = kCopyThreads * 16;
   for (int64_t item = blockIdx.x; item < a.items; item += gridDim.x) {
     const int32_t t = static_cast<int32_t>(item / a.blocks), b = static_cast<int32_t>(item % a.blocks);
-    const int64_t at = (static_cast<int64_t>(b) * kCopyThreads + threadIdx.x) * 16;
-    copy_rows(a, t, static_cast<const uint8_t*>(a.x), static_cast<uint8_t*>(a.rows), a.D * ELEM, at);
+    copy_rows(a, t, static_cast<const uint8_t*>(a.x), static_cast<uint8_t*>(a.rows), a.D * ELEM,
+              b * a.chunks * kTurn + threadIdx.x * 16, a.chunks > 1 ? kTurn : kTurn << 32);
     if (EIGHT && b == a.blocks - 1) {
       const int64_t n = (a.D + kB - 1) / kB * 4;
-      for (int64_t i = threadIdx.x * 16; i < max(n, static_cast<int64_t>(256)); i += kCopyThreads * 16)
-        copy_rows(a, t, reinterpret_cast<const uint8_t*>(a.scales), reinterpret_cast<uint8_t*>(a.row_scales), n, i);
+      for (int64_t i = threadIdx.x * 16; i < max(n, static_cast<int64_t>(256)); i += kCopyChunks * kTurn)
+        copy_rows(a, t, reinterpret_cast<const uint8_t*>(a.scales), reinterpret_cast<uint8_t*>(a.row_scales), n, i, kTurn);
     }
   }
 }
 
 // 8 columns per thread; the rows of up to kAhead choices are on their way at once
 constexpr int kAhead = 8;
-template <class H, bool WEIGHTED>
+// KNOWN: the workgroup's threads are all of one token.
+template <class H, bool WEIGHTED, bool KNOWN>
 __device__ __forceinline__ void combine_chunk(const RowsArgs& a, int32_t t, int32_t C, int32_t c) {
   float sum[8];
 #pragma unroll
@@ -249,18 +260,22 @@ __device__ __forceinline__ void combine_chunk(const RowsArgs& a, int32_t t, int3
   for (int32_t j0 = 0; j0 < a.k; j0 += kAhead) {
     Raw8<H> v[kAhead];
     float w[kAhead];
+    int32_t r[kAhead];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      w[j] = 0.0f;
-      v[j] = Raw8<H>{};
-      const int64_t r = j0 + j < a.k ? row_at(a, t, j0 + j) : -1;
-      if (r >= 0) {
-        w[j] = WEIGHTED ? a.weights[static_cast<int64_t>(t) * a.k + j0 + j] : 1.0f;
-        v[j] = fetch8<H>(row_of<H>(static_cast<const void*>(a.rows), r, C), C, c);
+      r[j] = j0 + j < a.k ? static_cast<int32_t>(row_at(a, t, j0 + j)) : -1;
+      w[j] = WEIGHTED && r[j] >= 0 ? a.weights[static_cast<int64_t>(t) * a.k + j0 + j] : 1.0f;
+      if (KNOWN) {
+        r[j] = __builtin_amdgcn_readfirstlane(r[j]);
+        w[j] = __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(w[j])));
       }
     }
 #pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      if (r[j] >= 0) v[j] = fetch8<H>(row_of<H>(static_cast<const void*>(a.rows), r[j], C), C, c);
+#pragma unroll
     for (int j = 0; j < kAhead; ++j) {
+      if (r[j] < 0) continue;
       float x[8];
       widen8f<H>(v[j], x);
 #pragma unroll
@@ -270,17 +285,17 @@ __device__ __forceinline__ void combine_chunk(const RowsArgs& a, int32_t t, int3
   store8<H>(row_of<H>(a.y, t, C), C, c, sum);
 }
 
-template <class H, bool WEIGHTED>
+template <class H, bool WEIGHTED, bool KNOWN>
 __global__ __launch_bounds__(512) void combine_kernel(RowsArgs a, int32_t per) {
   // `per` threads take a token's (part of a) row, so several short rows share a workgroup
-  const int32_t sub = static_cast<int32_t>(threadIdx.x) / per, in = static_cast<int32_t>(threadIdx.x) - sub * per;
-  const int32_t tokens = blockDim.x / per;
+  const int32_t sub = KNOWN ? 0 : static_cast<int32_t>(threadIdx.x) / per;
+  const int32_t in = static_cast<int32_t>(threadIdx.x) - sub * per, tokens = KNOWN ? 1 : blockDim.x / per;
   const int32_t C = static_cast<int32_t>(a.D);
   if (sub >= tokens) return;
   for (int64_t item = blockIdx.x; item < a.items; item += gridDim.x) {
     const int64_t t = item / a.blocks * tokens + sub;
     const int32_t c = (static_cast<int32_t>(item % a.blocks) * per + in) * 8;
-    if (t < a.T && c < C) combine_chunk<H, WEIGHTED>(a, static_cast<int32_t>(t), C, c);
+    if (t < a.T && c < C) combine_chunk<H, WEIGHTED, KNOWN>(a, static_cast<int32_t>(t), C, c);
   }
 }
 
@@ -437,7 +452,10 @@ extern "C" int fp8z1_dispatch(const fp8z1_routed* f, const int32_t* row_of, cons
   a.scales = scales;
   a.rows = rows;
   a.row_scales = row_scales;
-  const int64_t per = kCopyThreads * 16;
+  // many tokens: 4 chunks a thread (8192 tokens of 7168, 8 choices: 200 us, 221 with one); few: a chunk each, on more
+  // compute units
+  a.chunks = f->T >= 512 ? kCopyChunks : 1;
+  const int64_t per = kCopyThreads * 16 * a.chunks;
   a.blocks = static_cast<int32_t>((f->D * elem_size(f->dtype) + per - 1) / per);
   a.items = f->T * a.blocks;
   const dim3 g = groups_of(a), b(kCopyThreads);
@@ -454,12 +472,19 @@ extern "C" int fp8z1_dispatch(const fp8z1_routed* f, const int32_t* row_of, cons
 namespace fp8z1 {
 namespace {
 
+template <class H, bool WEIGHTED>
+void launch_combine_as(const RowsArgs& a, dim3 g, dim3 b, int32_t per, hipStream_t s) {
+  if (static_cast<int32_t>(b.x) == per)
+    hipLaunchKernelGGL((combine_kernel<H, WEIGHTED, true>), g, b, 0, s, a, per);
+  else
+    hipLaunchKernelGGL((combine_kernel<H, WEIGHTED, false>), g, b, 0, s, a, per);
+}
 template <class H>
 void launch_combine(const RowsArgs& a, dim3 g, dim3 b, int32_t per, hipStream_t s) {
   if (a.weights)
-    hipLaunchKernelGGL((combine_kernel<H, true>), g, b, 0, s, a, per);
+    launch_combine_as<H, true>(a, g, b, per, s);
   else
-    hipLaunchKernelGGL((combine_kernel<H, false>), g, b, 0, s, a, per);
+    launch_combine_as<H, false>(a, g, b, per, s);
 }
 
 }  // namespace
