@@ -3,7 +3,8 @@
 
 namespace fp8z1 {
 
-size_t linear8_workspace() { return part8_bytes(); }
+// (few rows are not tiled)
+size_t linear8_workspace(int64_t T, int64_t E) { return few_rows8(T, E) ? 0 : part8_bytes(); }
 
 int linear8(const FfnArgs& p, int32_t dtype, void* workspace, size_t workspace_bytes, hipStream_t s, const char* what) {
   return launch8<kLinear>(p, dtype, workspace, workspace_bytes, s, what);

@@ -59,23 +59,31 @@ __global__ __launch_bounds__(kThreads) void linear_dp_kernel(DpArgs a) {
   if (a.sums) store8<F32>(a.sums + static_cast<int64_t>(group) * a.N, a.N, n, sum);
 }
 
-// dbias[e][n]: the sums of expert e's groups, numbered as find_group numbers them
-__global__ __launch_bounds__(kThreads) void linear_dbias_kernel(const float* sums, const int32_t* offsets, int32_t T,
-                                                                int32_t E, int32_t N, float* dbias) {
-  const int32_t strips = (N + kThreads - 1) / kThreads;
+// dbias[e][n]: the sums of expert e's groups, numbered as find_group numbers them.  64 columns a workgroup, each
+// of its 16 waves adds every 16th group; the waves' sums are added in order.
+constexpr int kBiasWaves = 16, kBiasCols = 64;
+__global__ __launch_bounds__(64 * kBiasWaves) void linear_dbias_kernel(const float* sums, const int32_t* offsets, int32_t T,
+                                                                       int32_t E, int32_t N, float* dbias) {
+  __shared__ float parts[kBiasWaves][kBiasCols];
+  const int32_t strips = (N + kBiasCols - 1) / kBiasCols;
   const int32_t e = static_cast<int32_t>(blockIdx.x) / strips;
-  const int32_t n = (static_cast<int32_t>(blockIdx.x) - e * strips) * kThreads + threadIdx.x;
-  if (n >= N) return;
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int32_t n = min((static_cast<int32_t>(blockIdx.x) - e * strips) * kBiasCols + lane, N - 1);
   int32_t lo, hi;
   expert_rows(offsets, T, e, lo, hi);
   float sum = 0.0f;
   if (lo < hi) {
-    sum = sums[static_cast<int64_t>(e) * N + n];
+    if (w == 0) sum = sums[static_cast<int64_t>(e) * N + n];
     const float* const from = sums + (static_cast<int64_t>(E) + lo / kSumRows) * N + n;
     const int32_t more = (hi - lo - 1) / kSumRows;  // groups behind the first
 #pragma unroll 8
-    for (int32_t k = 0; k < more; ++k) sum += from[static_cast<int64_t>(k) * N];
+    for (int32_t k = w; k < more; k += kBiasWaves) sum += from[static_cast<int64_t>(k) * N];
   }
+  parts[w][lane] = sum;
+  __syncthreads();
+  if (w != 0 || (static_cast<int32_t>(blockIdx.x) - e * strips) * kBiasCols + lane >= N) return;
+#pragma unroll
+  for (int k = 1; k < kBiasWaves; ++k) sum += parts[k][lane];
   dbias[static_cast<int64_t>(e) * N + n] = sum;
 }
 
@@ -132,8 +140,8 @@ extern "C" int fp8z1_linear_bwd(const fp8z1_product* f, const void* dy, const vo
       return refuse(FP8Z1_EINVAL, what, "workspace too small");
     a.sums = static_cast<float*>(d_workspace);
   }
-  const int64_t strips = f->E * ((f->N + kThreads - 1) / kThreads);
-  if (dbias && strips > 0x7fffffff / kThreads) return refuse(FP8Z1_ESHAPE, what, "too many gradients of biases");
+  const int64_t strips = f->E * ((f->N + kBiasCols - 1) / kBiasCols);
+  if (dbias && strips > 0x7fffffff / (64 * kBiasWaves)) return refuse(FP8Z1_ESHAPE, what, "too many gradients of biases");
   if (f->T && (dp || dbias)) {
     const int64_t chunks = (f->N + 7) / 8, threads = chunks < kThreads ? (chunks + 63) / 64 * 64 : kThreads;
     const int64_t turns = (groups + 65534) / 65535;  // (a grid's y ends at 65,535)
@@ -148,7 +156,7 @@ extern "C" int fp8z1_linear_bwd(const fp8z1_product* f, const void* dy, const vo
     if (rc) return rc;
   }
   if (dbias) {
-    hipLaunchKernelGGL(linear_dbias_kernel, dim3(static_cast<unsigned>(strips)), dim3(kThreads), 0, s, a.sums, offsets, a.T,
+    hipLaunchKernelGGL(linear_dbias_kernel, dim3(static_cast<unsigned>(strips)), dim3(64 * kBiasWaves), 0, s, a.sums, offsets, a.T,
                        a.E, a.N, dbias);
     rc = launched(what);
     if (rc) return rc;

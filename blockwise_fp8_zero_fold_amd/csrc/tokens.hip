@@ -250,7 +250,17 @@ __global__ __launch_bounds__(kCopyThreads) void dispatch_kernel(RowsArgs a) {
 
 // 8 columns per thread; the rows of up to kAhead choices are on their way at once
 constexpr int kAhead = 8;
-// KNOWN: the workgroup's threads are all of one token.
+// KNOWN: the workgroup's threads are all of one token, and rows are whole chunks of 8 columns: nothing stands between
+// the loads.
+template <class H>
+__device__ __forceinline__ Raw8<H> fetch_whole8(const void* row, int32_t c) {
+  typedef typename Elem<H>::type E;
+  Raw8<H> r;
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(E)) * 8 / 16; ++i)
+    r.x[i] = ((const v4u_a2_global_t*)(static_cast<const E*>(row) + c))[i];
+  return r;
+}
 template <class H, bool WEIGHTED, bool KNOWN>
 __device__ __forceinline__ void combine_chunk(const RowsArgs& a, int32_t t, int32_t C, int32_t c) {
   float sum[8];
@@ -272,7 +282,10 @@ __device__ __forceinline__ void combine_chunk(const RowsArgs& a, int32_t t, int3
     }
 #pragma unroll
     for (int j = 0; j < kAhead; ++j)
-      if (r[j] >= 0) v[j] = fetch8<H>(row_of<H>(static_cast<const void*>(a.rows), r[j], C), C, c);
+      if (r[j] >= 0) {
+        const void* const row = row_of<H>(static_cast<const void*>(a.rows), r[j], C);
+        v[j] = KNOWN ? fetch_whole8<H>(row, c) : fetch8<H>(row, C, c);
+      }
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       if (r[j] < 0) continue;
@@ -474,7 +487,7 @@ namespace {
 
 template <class H, bool WEIGHTED>
 void launch_combine_as(const RowsArgs& a, dim3 g, dim3 b, int32_t per, hipStream_t s) {
-  if (static_cast<int32_t>(b.x) == per)
+  if (static_cast<int32_t>(b.x) == per && a.D % 8 == 0)
     hipLaunchKernelGGL((combine_kernel<H, WEIGHTED, true>), g, b, 0, s, a, per);
   else
     hipLaunchKernelGGL((combine_kernel<H, WEIGHTED, false>), g, b, 0, s, a, per);

@@ -56,7 +56,8 @@ def test_linear_workspaces():
     for q in (fz.lib.fp8z1_linear_workspace_bytes, fz.lib.fp8z1_linear_bwd_workspace_bytes):
         assert q(None, C.byref(n)) == EINVAL and q(product(), None) == EINVAL
     assert fz.lib.fp8z1_linear_workspace_bytes(product(), C.byref(n)) == 0 and n.value == 0  # nothing to split
-    assert fz.lib.fp8z1_linear_workspace_bytes(product(K=7168), C.byref(n)) == 0 and n.value > 0
+    assert fz.lib.fp8z1_linear_workspace_bytes(product(K=7168), C.byref(n)) == 0 and n.value == 0  # few rows: no tiles
+    assert fz.lib.fp8z1_linear_workspace_bytes(product(T=100, K=7168), C.byref(n)) == 0 and n.value > 0
     assert fz.lib.fp8z1_linear_workspace_bytes(product(K=7168, x_dtype=fz.BF16), C.byref(n)) == 0 and n.value > 0
     # sums of 16 rows each of the bias's gradient
     assert fz.lib.fp8z1_linear_bwd_workspace_bytes(product(), C.byref(n)) == 0 and n.value == 2 * 64 * 4
