@@ -41,7 +41,7 @@ struct FfnArgs {
 
 // y = res + act(x W^T + bias) of rows in 8 bits (checked arguments), and the workspace that it can use
 int linear8(const FfnArgs& p, int32_t dtype, void* workspace, size_t workspace_bytes, hipStream_t s, const char* what);
-size_t linear8_workspace(int64_t T, int64_t E);
+size_t linear8_workspace(int64_t T, int64_t E, int64_t N, int64_t K);
 
 // Rows of expert e, kept inside [0, T] whatever the offsets hold, so a wrong
 // offset gives wrong rows but no access out of bounds.

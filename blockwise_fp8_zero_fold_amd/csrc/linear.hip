@@ -12,7 +12,7 @@ extern "C" int fp8z1_linear_workspace_bytes(const fp8z1_product* f, size_t* byte
   const int rc = check_product(f, &some_offsets, what);
   if (rc) return rc;
   const bool eight = f->x_dtype == FP8Z1_E4M3;
-  *bytes = !f->T || f->K <= 2 * kB ? 0 : eight ? linear8_workspace(f->T, f->E) : part_bytes(4);
+  *bytes = !f->T ? 0 : eight ? linear8_workspace(f->T, f->E, f->N, f->K) : f->K > 2 * kB ? part_bytes(4) : 0;
   return FP8Z1_OK;
 }
 

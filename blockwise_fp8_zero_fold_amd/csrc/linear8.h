@@ -73,9 +73,9 @@ constexpr int kThreads8 = 512;
 constexpr int kRows8 = 256;   // tile rows
 constexpr int kCols8 = 256;   // weight rows of a tile (up: 128 of gate, 128 of up)
 constexpr int kA8 = kRows8 * kB, kB8 = kCols8 * kB;
-// a stage: codes of x, of the weights, x's scales (1 KB), and the weights' two, 64 times each (as a wave copies them)
-constexpr int kScales8 = kA8 + kB8, kStage8 = kScales8 + 2048;
-constexpr int kCopies = 9;                       // of a wave for a stage
+// a stage: codes of x, of the weights, x's scales (1 KB), the weights' two, 64 times each (as a wave copies them), and
+// for shifted rows the 4 bytes behind each row's 128
+constexpr int kScales8 = kA8 + kB8, kBehind8 = kScales8 + 2048, kStage8 = kBehind8 + 4 * (kRows8 + kCols8);
 constexpr int kResults8 = 8 * (kResultBytes / 4);  // 64 x 64 float32 of each wave
 constexpr int32_t kSlots8 = 256;                 // workgroups that the card runs at once: one on each compute unit
 
@@ -145,12 +145,14 @@ __device__ __forceinline__ void finish_up8(const FfnArgs& p, int64_t m, int32_t 
   }
 }
 
-// DIRECT: rows of x and codes are 4-byte aligned, and a stage is copied to LDS directly.
-//
 // A workgroup of 8 waves computes 256 rows x 256 weight rows, each wave 64 x 128 as 2 x 4 matrix tiles; two waves share a
-// SIMD, one's additions and conversions running under the other's products.  A stage of LDS holds a block of k; while
-// it is read, the next one is copied.
-template <class H, int KIND, bool DIRECT>
+// SIMD, one's additions and conversions running under the other's products.  A stage of LDS holds a block of k, copied
+// there directly; while it is read, the next one is on its way.
+//
+// SHIFTED: rows of x or codes are not 4-byte aligned, as the copies want them.  A row's stage then begins with the 4-byte
+// word that its block begins in and has one word more, and a lane shifts what it reads by its row's 0 to 3 bytes.
+// Only where the workspace has no room for packed rows.
+template <class H, int KIND, bool SHIFTED>
 __global__ __launch_bounds__(kThreads8) void tile8_kernel(FfnArgs p, int32_t ncols) {
   constexpr bool kUp = KIND == kFfnUp;
   constexpr int kOut = kUp ? kCols8 / 2 : kCols8;  // output columns of a tile
@@ -176,11 +178,21 @@ __global__ __launch_bounds__(kThreads8) void tile8_kernel(FfnArgs p, int32_t nco
   const int32_t nb = (N + kB - 1) / kB;
 
   // This thread's 16-byte chunks of a stage: chunk c16 of rows t / 8 + 64 j of x and of the weights.  Rows past the
-  // run's or the weight's end are whatever lies there (nothing behind the tensors is read): their results are
-  // not stored, and no other result depends on them.
+  // run's or the weight's end are whatever lies there (nothing behind the tensors' last word is read): their results are
+  // not stored, and no other result depends on them.  The bytes that a row begins behind a word: the same for
+  // rows 4 apart, so for all of a thread's.
+  constexpr int kCopies = SHIFTED ? 10 : 9;  // of a wave for a stage
   const int r0 = t >> 3, c16 = ((t & 7) ^ swizzle_a(r0)) * 16;
-  const uint32_t roff = static_cast<uint32_t>(r0) * static_cast<uint32_t>(K) + c16, rstep = 64u * static_cast<uint32_t>(K);
   const int64_t abase = static_cast<int64_t>(m0) * K, bbase = (static_cast<int64_t>(e) * N + n0) * K;
+  const uint8_t *const x0 = p.x0 + abase, *const w0 = p.w0 + bbase, *const w1 = (kUp ? p.w1 : p.w0) + bbase;
+  auto word = [](const uint8_t* a) {
+    return SHIFTED ? static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(reinterpret_cast<uintptr_t>(a) & 3)))
+                   : 0u;
+  };
+  const uint32_t xw = word(x0), w0w = word(w0), w1w = word(w1);
+  auto row_at = [&](int r, uint32_t in_word) { return static_cast<uint32_t>(r) * static_cast<uint32_t>(K) + in_word; };
+  const uint32_t xoff = (row_at(r0, xw) & ~3u) + c16, w0off = (row_at(r0, w0w) & ~3u) + c16,
+                 w1off = (row_at(r0, w1w) & ~3u) + c16, rstep = 64u * static_cast<uint32_t>(K);
   const float* const xs = p.xs + static_cast<int64_t>(m0) * kb;
   // the weights' scales, one per block of k: of the two blocks of 128 columns, up: of gate and up
   const float* ws[2];
@@ -188,89 +200,69 @@ __global__ __launch_bounds__(kThreads8) void tile8_kernel(FfnArgs p, int32_t nco
   for (int k = 0; k < 2; ++k)
     ws[k] = (kUp && k ? p.s1 : p.s0) + (static_cast<int64_t>(e) * nb + min(n0 / kB + (kUp ? 0 : k), nb - 1)) * kb;
   const int64_t wleft = static_cast<int64_t>(p.E) * N * K - bbase;
-  const buffer_t xbuf = make_buffer(p.x0 + abase, static_cast<int64_t>(p.T - m0) * K),
-                 w0buf = make_buffer(p.w0 + bbase, wleft), w1buf = make_buffer((kUp ? p.w1 : p.w0) + bbase, wleft),
+  auto words = [](int64_t n, uint32_t in_word) { return SHIFTED ? (n + in_word + 3) & ~static_cast<int64_t>(3) : n; };
+  const buffer_t xbuf = make_buffer(x0 - xw, words(static_cast<int64_t>(p.T - m0) * K, xw)),
+                 w0buf = make_buffer(w0 - w0w, words(wleft, w0w)), w1buf = make_buffer(w1 - w1w, words(wleft, w1w)),
                  sbuf = make_buffer(reinterpret_cast<const uint8_t*>(w < 4 ? xs : ws[w & 1]),
                                     (w < 4 ? static_cast<int64_t>(p.T - m0) * kb : kb) * 4);
   const uint32_t soff = w < 4 ? static_cast<uint32_t>(t) * static_cast<uint32_t>(kb) * 4 : 0;
+  // the word behind row t of the stage: rows of x, then of the weights
+  const int brow = w < 4 ? t : kUp ? t & 127 : t & 255;
+  const uint32_t bword = w < 4 ? xw : kUp && w >= 6 ? w1w : w0w, boff = (row_at(brow, bword) & ~3u) + kB;
+  const buffer_t bbuf = make_buffer((w < 4 ? x0 : kUp && w >= 6 ? w1 : w0) - bword,
+                                    words(w < 4 ? static_cast<int64_t>(p.T - m0) * K : wleft, bword));
   const uint32_t lds0 = lds_address(lds);
   // copy j of kCopies of block q to the stage at LDS offset `to`
   auto copy = [&](int j, int32_t q, uint32_t to) {
     const uint32_t at = lds0 + to + w * 1024;
     if (j < 4)
-      copy_to_lds<16>(xbuf, roff, q * kB + j * rstep, at + j * (kThreads8 * 16));
+      copy_to_lds<16>(xbuf, xoff, q * kB + j * rstep, at + j * (kThreads8 * 16));
     else if (j < 8)
-      copy_to_lds<16>(j < 6 ? w0buf : w1buf, roff, q * kB + (kUp ? j & 1 : j - 4) * rstep,
+      copy_to_lds<16>(!kUp || j < 6 ? w0buf : w1buf, !kUp || j < 6 ? w0off : w1off, q * kB + (kUp ? j & 1 : j - 4) * rstep,
                       at + kA8 + (j - 4) * (kThreads8 * 16));
-    else  // (the weights' by two waves each: as many copies of every wave)
+    else if (j == 8)  // (the weights' by two waves each: as many copies of every wave)
       copy_to_lds<4>(sbuf, soff, q * 4, lds0 + to + kScales8 + w * 256);
-  };
-  // Through registers: half h of the 8 chunks, and the scales with the first.
-  auto fetch = [&](int h, int32_t q, uint8_t* to) {
-    const int32_t k0 = q * kB, n = K - k0 - c16;  // codes of the row from this chunk on
-    uint4 held[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      // (a row past the tensor's last one is not there to be read)
-      const int r = r0 + 64 * (kUp && h ? j & 1 : j);
-      const uint8_t* const from = h == 0 ? p.x0 + abase + static_cast<int64_t>(min(r, p.T - 1 - m0)) * K
-                                         : (kUp && j >= 2 ? p.w1 : p.w0) + bbase + static_cast<int64_t>(min(r, N - 1 - n0)) * K;
-      held[j] = k0 + kB <= K ? ld16(from + k0 + c16) : ld16_part(from + k0 + c16, n, k0 + c16);
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      *reinterpret_cast<uint4*>(to + h * kA8 + (t + kThreads8 * j) * 16) = held[j];
-    if (h == 0)
-      *reinterpret_cast<float*>(to + kScales8 + t * 4) =
-          t < kRows8 ? xs[static_cast<int64_t>(min(t, p.T - 1 - m0)) * kb + q] : ws[w & 1][q];
+    else
+      copy_to_lds<4>(bbuf, boff, q * kB, lds0 + to + kBehind8 + w * 256);
   };
   // Clears what the last stage holds past the end of k (both operands: 0 times a NaN is none).
   auto clear_past = [&](uint8_t* at) {
-    const int n = K - (kb - 1) * kB - c16;
-    if (n >= 16) return;
+    const int left = K - (kb - 1) * kB;
+    auto keep = [](uint32_t* x, int n) {  // the first n of 4 bytes
+      *x = n >= 4 ? *x : n > 0 ? *x & (0xffffffffu >> (32 - 8 * n)) : 0u;
+    };
     for (int j = 0; j < 8; ++j) {
+      const uint32_t in_word = j < 4 ? xw : kUp && j >= 6 ? w1w : w0w;
+      const int n = left + (SHIFTED ? row_at(r0, in_word) & 3 : 0) - c16;
       uint4* const x = reinterpret_cast<uint4*>(at + (t + kThreads8 * j) * 16);
       uint4 v = *x;
-      uint32_t* const o[4] = {&v.x, &v.y, &v.z, &v.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int in = n - 4 * i;
-        *o[i] = in >= 4 ? *o[i] : in > 0 ? *o[i] & (0xffffffffu >> (32 - 8 * in)) : 0u;
-      }
+      keep(&v.x, n);
+      keep(&v.y, n - 4);
+      keep(&v.z, n - 8);
+      keep(&v.w, n - 12);
       *x = v;
     }
+    if (SHIFTED) keep(reinterpret_cast<uint32_t*>(at + kBehind8) + t, left + (row_at(brow, bword) & 3) - kB);
   };
-  const bool tail = DIRECT && K % kB != 0;
+  const bool tail = K % kB != 0;
   uint32_t cur = 0, next = kStage8;  // LDS offsets of the stages of blocks q and q + 1
   // Block q + 1 is in its stage, and all waves have read block q: its stage is free for block q + 2.
   auto turn_over = [&](int32_t q) {
-    if (DIRECT)
-      meet<0>();
-    else
-      __syncthreads();
+    meet<0>();
     if (tail && q + 2 == kb) {
       clear_past(lds + next);
       __syncthreads();
     }
   };
-  auto first_stages = [&] {
-    if (DIRECT) {
 #pragma unroll
-      for (int j = 0; j < kCopies; ++j) copy(j, q0, 0);
-      meet<0>();
+  for (int j = 0; j < kCopies; ++j) copy(j, q0, 0);
+  meet<0>();
 #pragma unroll
-      for (int j = 0; j < kCopies; ++j) copy(j, min(q0 + 1, q1 - 1), kStage8);
-    } else {
-      for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) fetch(h, min(q0 + k, q1 - 1), lds + k * kStage8);
-      __syncthreads();
-    }
-    if (tail && q0 == kb - 1) {
-      clear_past(lds);
-      __syncthreads();
-    }
-  };
+  for (int j = 0; j < kCopies; ++j) copy(j, min(q0 + 1, q1 - 1), kStage8);
+  if (tail && q0 == kb - 1) {
+    clear_past(lds);
+    __syncthreads();
+  }
 
   const int swz = swizzle_a(l32);  // (that of every row read: they lie 32 apart)
   // chunk c of this lane's half of a row of x, and of a weight's (up: two tile columns of gate, then the same of up)
@@ -281,6 +273,16 @@ __global__ __launch_bounds__(kThreads8) void tile8_kernel(FfnArgs p, int32_t nco
     const int r = kUp ? (j / 2) * 128 + wn * 64 + (j % 2) * 32 : wn * 128 + j * 32;
     return *reinterpret_cast<const uint4*>(lds + from + kA8 + (r + l32) * kB + (((half * 4 + c) ^ swz) << 4));
   };
+  // the word behind that chunk, and a lane's shift in its rows of x and of either matrix
+  auto behind = [&](uint32_t from, int r, int c) {
+    const uint32_t in_row = r * kB + (((half * 4 + c + 1) ^ swz) << 4);
+    return *reinterpret_cast<const uint32_t*>(lds + from + (c == 3 && half ? kBehind8 + r * 4 : in_row));
+  };
+  auto behind_x = [&](uint32_t from, int i, int c) { return behind(from, wm * 64 + i * 32 + l32, c); };
+  auto behind_w = [&](uint32_t from, int j, int c) {
+    return behind(from, kRows8 + (kUp ? (j / 2) * 128 + wn * 64 + (j % 2) * 32 : wn * 128 + j * 32) + l32, c);
+  };
+  const uint32_t shx = row_at(l32, xw) & 3, shw[2] = {row_at(l32, w0w) & 3, row_at(l32, w1w) & 3};
   auto scale_x = [&](uint32_t from, int i) {
     return *reinterpret_cast<const float*>(lds + from + kScales8 + (wm * 64 + i * 32 + l32) * 4);
   };
@@ -295,7 +297,6 @@ __global__ __launch_bounds__(kThreads8) void tile8_kernel(FfnArgs p, int32_t nco
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = zero;
 
-  first_stages();
   if constexpr (kUp) {
     // Gate and up: codes widened to bfloat16, which holds them, so that the sums are float32 sums (see the top).
     // A step is 32 k, chunk c of a block's 4 from both halves of the lanes, two matrix instructions for each of the
@@ -304,10 +305,23 @@ __global__ __launch_bounds__(kThreads8) void tile8_kernel(FfnArgs p, int32_t nco
     typedef Bf16::v8 v8;
     v8 W[4][2], X[2][2][2];
     uint4 rw[4], rx[2];
-    auto wide_x = [&](int set, int i, int k) {
-      X[set][i][k] = k ? widen8<Bf16>(rx[i].z, rx[i].w) : widen8<Bf16>(rx[i].x, rx[i].y);
+    uint32_t bw[4], bx[2];
+    // half k of a chunk's 16 codes
+    auto wide = [&](const uint4& r, uint32_t b, uint32_t sh, int k) {
+      if (!SHIFTED) return k ? widen8<Bf16>(r.z, r.w) : widen8<Bf16>(r.x, r.y);
+      return k ? widen8<Bf16>(__builtin_amdgcn_alignbyte(r.w, r.z, sh), __builtin_amdgcn_alignbyte(b, r.w, sh))
+               : widen8<Bf16>(__builtin_amdgcn_alignbyte(r.y, r.x, sh), __builtin_amdgcn_alignbyte(r.z, r.y, sh));
     };
-    auto wide_w = [&](int j, int k) { W[j][k] = k ? widen8<Bf16>(rw[j].z, rw[j].w) : widen8<Bf16>(rw[j].x, rw[j].y); };
+    auto wide_x = [&](int set, int i, int k) { X[set][i][k] = wide(rx[i], bx[i], shx, k); };
+    auto wide_w = [&](int j, int k) { W[j][k] = wide(rw[j], bw[j], shw[j / 2], k); };
+    auto read_x = [&](uint32_t from, int i, int c) {
+      rx[i] = chunk_x(from, i, c);
+      bx[i] = SHIFTED ? behind_x(from, i, c) : 0;
+    };
+    auto read_w = [&](uint32_t from, int j, int c) {
+      rw[j] = chunk_w(from, j, c);
+      bw[j] = SHIFTED ? behind_w(from, j, c) : 0;
+    };
     // acc is held in units of the current block's scale: between blocks it is multiplied by scale_before / scale_now.
     // That does no harm while all scales lie between 2^-70 and 2^20, which every wave watches; if one does not, the
     // tile is done again, block by block.
@@ -355,12 +369,12 @@ __global__ __launch_bounds__(kThreads8) void tile8_kernel(FfnArgs p, int32_t nco
           const int j = v >> 2, i = v & 1, k = (v >> 1) & 1;
           acc[i][j] = Bf16::mma32(W[j][k], X[set][i][k], acc[i][j]);
           __builtin_amdgcn_sched_barrier(0);
-          if (v == 0) rw[0] = chunk_w(from, 0, cn);
-          if (v == 1) rx[0] = chunk_x(from, 0, cn);
-          if (v == 2) rw[1] = chunk_w(from, 1, cn);
-          if (v == 3) rx[1] = chunk_x(from, 1, cn);
-          if (v == 4) rw[2] = chunk_w(from, 2, cn);
-          if (v == 6) rw[3] = chunk_w(from, 3, cn);
+          if (v == 0) read_w(from, 0, cn);
+          if (v == 1) read_x(from, 0, cn);
+          if (v == 2) read_w(from, 1, cn);
+          if (v == 3) read_x(from, 1, cn);
+          if (v == 4) read_w(from, 2, cn);
+          if (v == 6) read_w(from, 3, cn);
           if (v < 2) wide_w(3, v);
           if (v == 5 || v == 6) wide_w(0, v - 5);
           if (v == 7 || v == 8) wide_x(set ^ 1, 0, v - 7);
@@ -368,8 +382,7 @@ __global__ __launch_bounds__(kThreads8) void tile8_kernel(FfnArgs p, int32_t nco
           if (v == 11 || v == 12) wide_x(set ^ 1, 1, v - 11);
           if (v == 13 || v == 14) wide_w(2, v - 13);
           if (c == 3) {
-            if (DIRECT && v < kCopies) copy(v, far, cur);
-            if (!DIRECT && v < 2) fetch(v, far, lds + cur);
+            if (v < kCopies) copy(v, far, cur);
             if (v == 3) {
               float to[2][2];
               scales(next, to);
@@ -399,7 +412,7 @@ __global__ __launch_bounds__(kThreads8) void tile8_kernel(FfnArgs p, int32_t nco
     for (int k = 0; k < 4; ++k) ratio[k >> 1][k & 1] = 1.0f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      rw[j] = chunk_w(0, j, 0);
+      read_w(0, j, 0);
       if (j < 3) {
         wide_w(j, 0);
         wide_w(j, 1);
@@ -407,20 +420,20 @@ __global__ __launch_bounds__(kThreads8) void tile8_kernel(FfnArgs p, int32_t nco
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      rx[i] = chunk_x(0, i, 0);
+      read_x(0, i, 0);
       wide_x(0, i, 0);
       wide_x(0, i, 1);
     }
     for (int32_t q = q0; q < q1; ++q) turn(q);
     // (the last turn has fetched its own block as the next: its scales are the units still)
-    if (DIRECT) wait_copies();
+    wait_copies();
     int32_t* const far_apart = reinterpret_cast<int32_t*>(lds + kResults8);
     __syncthreads();
     if (t == 0) *far_apart = 0;
     __syncthreads();
     if (!near) *far_apart = 1;
     __syncthreads();
-    const bool again = *far_apart != 0;
+    const bool again = __builtin_amdgcn_readfirstlane(*far_apart) != 0;
     if (!again) {
 #pragma unroll
       for (int u = 0; u < 8; ++u)
@@ -433,15 +446,9 @@ __global__ __launch_bounds__(kThreads8) void tile8_kernel(FfnArgs p, int32_t nco
         acc[0][j] = acc[1][j] = zero;
         for (int32_t q = q0; q < q1; ++q) {
           __syncthreads();
-          if (DIRECT) {
 #pragma unroll
-            for (int k = 0; k < kCopies; ++k) copy(k, q, 0);
-            wait_copies();
-          } else {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) fetch(h, q, lds);
-          }
-          __syncthreads();
+          for (int k = 0; k < kCopies; ++k) copy(k, q, 0);
+          meet<0>();
           if (tail && q + 1 == kb) {
             clear_past(lds);
             __syncthreads();
@@ -449,12 +456,13 @@ __global__ __launch_bounds__(kThreads8) void tile8_kernel(FfnArgs p, int32_t nco
           f32x16 part[2] = {zero, zero};
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
-            const uint4 cw = chunk_w(0, j, c);
+            read_w(0, j, c);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const uint4 cx = chunk_x(0, i, c);
-              part[i] = Bf16::mma32(widen8<Bf16>(cw.x, cw.y), widen8<Bf16>(cx.x, cx.y), part[i]);
-              part[i] = Bf16::mma32(widen8<Bf16>(cw.z, cw.w), widen8<Bf16>(cx.z, cx.w), part[i]);
+              read_x(0, i, c);
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+                part[i] = Bf16::mma32(wide(rw[j], bw[j], shw[j / 2], k), wide(rx[i], bx[i], shx, k), part[i]);
             }
           }
           const float sw = scale_w(0, j / 2);
@@ -478,13 +486,24 @@ __global__ __launch_bounds__(kThreads8) void tile8_kernel(FfnArgs p, int32_t nco
     f32x16 part[2];
     part[1] = zero;
     float s[2] = {0.0f, 0.0f}, was = 0.0f;  // `was`: the scale of the tile before the first
+    uint32_t bx[2], bw[2];
     auto read_x = [&](uint32_t from, int i) {
 #pragma unroll
       for (int c = 0; c < 4; ++c) x[i][c] = chunk_x(from, i, c);
+      bx[i] = SHIFTED ? behind_x(from, i, 3) : 0;
     };
     auto read_w = [&](uint32_t from, int j) {
 #pragma unroll
       for (int c = 0; c < 4; ++c) w4[j & 1][c] = chunk_w(from, j, c);
+      bw[j & 1] = SHIFTED ? behind_w(from, j, 3) : 0;
+    };
+    auto shift = [&](uint4 (&v)[4], uint32_t b, uint32_t sh) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t after = c < 3 ? v[c + 1].x : b;
+        v[c] = make_uint4(__builtin_amdgcn_alignbyte(v[c].y, v[c].x, sh), __builtin_amdgcn_alignbyte(v[c].z, v[c].y, sh),
+                          __builtin_amdgcn_alignbyte(v[c].w, v[c].z, sh), __builtin_amdgcn_alignbyte(after, v[c].w, sh));
+      }
     };
     auto add = [&](int u, int r0, float by) {
 #pragma unroll
@@ -507,6 +526,8 @@ __global__ __launch_bounds__(kThreads8) void tile8_kernel(FfnArgs p, int32_t nco
           asm volatile("" : "+v"(part[1]));
           turn_over(q);
         }
+        if (SHIFTED && i == 0) shift(w4[j & 1], bw[j & 1], shw[0]);
+        if (SHIFTED && j == 0) shift(x[i], bx[i], shx);
         f32x16 d = mma8(code32(w4[j & 1][0], w4[j & 1][1]), code32(x[i][0], x[i][1]), zero);
         __builtin_amdgcn_sched_barrier(0);
         if (i == 0 && j < 3) read_w(cur, j + 1);
@@ -523,13 +544,9 @@ __global__ __launch_bounds__(kThreads8) void tile8_kernel(FfnArgs p, int32_t nco
         }
         if (u == 7) read_x(next, 1);
         if (u >= 6) {
-          if (DIRECT) {
 #pragma unroll
-            for (int k = 0; k < 5; ++k)
-              if ((u - 6) * 5 + k < kCopies) copy((u - 6) * 5 + k, far, cur);
-          } else {
-            fetch(u - 6, far, lds + cur);
-          }
+          for (int k = 0; k < 5; ++k)
+            if ((u - 6) * 5 + k < kCopies) copy((u - 6) * 5 + k, far, cur);
         }
         add(before, 8, u == 0 ? was : s[before & 1]);
         __builtin_amdgcn_sched_barrier(0);
@@ -541,7 +558,7 @@ __global__ __launch_bounds__(kThreads8) void tile8_kernel(FfnArgs p, int32_t nco
     }
     add(7, 0, was);
     add(7, 8, was);
-    if (DIRECT) wait_copies();
+    wait_copies();
     __syncthreads();  // the results take the stages' place
   }
 
@@ -707,24 +724,31 @@ __global__ __launch_bounds__(kThreads) void join8_kernel(FfnArgs p, int32_t ncol
 // ------------------------------------------------------------------------------------------- few rows
 
 // Few rows per expert: bound by the read of the weights, which go from memory into registers as
-// the matrix instruction's operand.  A workgroup takes 16 weight rows and 16 TT rows of x; its WAVES waves share the
-// blocks of k and their sums are added in order.  Up: gate's or up's 16 rows (blockIdx.x), the float32
-// sums to p.part [T][2][N] for finish_rows8_kernel.
-template <class H, int KIND, int WAVES, int TT, bool ALIGNED>
+// the matrix instruction's operand.  A workgroup takes NS strips of 16 weight rows and 16 TT rows of x; its WAVES waves
+// share the blocks of k and their sums are added in order.  Up: the strips are gate's, then up's (NS 2: one of each), and
+// the float32 sums go to p.part [T][2][N] for finish_rows8_kernel.
+template <class H, int KIND, int WAVES, int TT, int NS, bool ALIGNED>
 __global__ __launch_bounds__(WAVES * 64) void rows8_kernel(FfnArgs p) {
   constexpr bool kUp = KIND == kFfnUp;
-  constexpr int kDeep = TT == 1 ? 4 : 2;
-  __shared__ f32x4 sums[WAVES][TT][64];
+  constexpr int kDeep = TT * NS == 1 ? 4 : 2;
+  __shared__ f32x4 sums[WAVES][NS * TT][64];
   int32_t e, lo, hi, t0;
   const int32_t group = static_cast<int32_t>(blockIdx.z * gridDim.y + blockIdx.y);
   if (!find_group<16 * TT>(p.offsets, p.T, p.E, group, e, lo, hi, t0)) return;
-  const int32_t N = p.N, K = p.K, strips = (N + 15) / 16;
-  const int which = kUp && static_cast<int32_t>(blockIdx.x) >= strips;
-  const int32_t n0 = (static_cast<int32_t>(blockIdx.x) - (which ? strips : 0)) * 16;
+  const int32_t N = p.N, K = p.K, strips = (N + 15) / 16, b = static_cast<int32_t>(blockIdx.x);
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
   const int32_t kb = (K + kB - 1) / kB, nb = (N + kB - 1) / kB;
-  const uint8_t* const wt = (which ? p.w1 : p.w0) + (static_cast<int64_t>(e) * N + min(n0 + r, N - 1)) * K + g * 32;
-  const float* const sc = (which ? p.s1 : p.s0) + (static_cast<int64_t>(e) * nb + n0 / kB) * kb;
+  int32_t n0[NS];
+  int which[NS];
+  const uint8_t* wt[NS];
+  const float* sc[NS];
+#pragma unroll
+  for (int s = 0; s < NS; ++s) {
+    which[s] = kUp && (NS == 2 ? s : b >= strips);
+    n0[s] = (kUp ? b - (NS == 1 && which[s] ? strips : 0) : b * NS + s) * 16;
+    wt[s] = (which[s] ? p.w1 : p.w0) + (static_cast<int64_t>(e) * N + min(n0[s] + r, N - 1)) * K + g * 32;
+    sc[s] = (which[s] ? p.s1 : p.s0) + (static_cast<int64_t>(e) * nb + min(n0[s] / kB, nb - 1)) * kb;
+  }
   const uint8_t* xr[TT];
   const float* xs[TT];
 #pragma unroll
@@ -734,46 +758,53 @@ __global__ __launch_bounds__(WAVES * 64) void rows8_kernel(FfnArgs p) {
     xs[i] = p.xs + row * kb;
   }
   struct Block {
-    uint4 c[2], x[TT][2];
-    float s[TT], sw;
+    uint4 c[NS][2], x[TT][2];
+    float s[TT], sw[NS];
   };
   auto load16 = [&](const uint8_t* from, int32_t left, int32_t before) {
     if (ALIGNED) return left > 0 ? *reinterpret_cast<const uint4*>(from) : make_uint4(0u, 0u, 0u, 0u);
     return ld16_part(from, left, before);
   };
-  auto load = [&](int32_t q, Block& b) {
+  auto load = [&](int32_t q, Block& d) {
     const int32_t at = q * kB, left = K - at - g * 32;  // of this lane's 32 k
-    b.sw = sc[q];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) b.c[i] = load16(wt + at + 16 * i, left - 16 * i, at + g * 32 + 16 * i);
+    for (int s = 0; s < NS; ++s) {
+      d.sw[s] = sc[s][q];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) d.c[s][i] = load16(wt[s] + at + 16 * i, left - 16 * i, at + g * 32 + 16 * i);
+    }
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
-      b.s[t] = xs[t][q];
+      d.s[t] = xs[t][q];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) b.x[t][i] = load16(xr[t] + at + 16 * i, left - 16 * i, at + g * 32 + 16 * i);
+      for (int i = 0; i < 2; ++i) d.x[t][i] = load16(xr[t] + at + 16 * i, left - 16 * i, at + g * 32 + 16 * i);
     }
   };
-  f32x4 acc[TT];
+  f32x4 acc[NS][TT];
   const f32x4 zero = {};
 #pragma unroll
-  for (int t = 0; t < TT; ++t) acc[t] = zero;
-  auto add = [&](const Block& b) {
+  for (int s = 0; s < NS; ++s)
 #pragma unroll
-    for (int t = 0; t < TT; ++t) {
-      f32x4 part = zero;
-      if constexpr (kUp) {  // (float32 sums, as on tiles)
+    for (int t = 0; t < TT; ++t) acc[s][t] = zero;
+  auto add = [&](const Block& d) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          part = Bf16::mma16(widen8<Bf16>(b.c[i].x, b.c[i].y), widen8<Bf16>(b.x[t][i].x, b.x[t][i].y), part);
-          part = Bf16::mma16(widen8<Bf16>(b.c[i].z, b.c[i].w), widen8<Bf16>(b.x[t][i].z, b.x[t][i].w), part);
+    for (int s = 0; s < NS; ++s)
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        f32x4 part = zero;
+        if constexpr (kUp) {  // (float32 sums, as on tiles)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            part = Bf16::mma16(widen8<Bf16>(d.c[s][i].x, d.c[s][i].y), widen8<Bf16>(d.x[t][i].x, d.x[t][i].y), part);
+            part = Bf16::mma16(widen8<Bf16>(d.c[s][i].z, d.c[s][i].w), widen8<Bf16>(d.x[t][i].z, d.x[t][i].w), part);
+          }
+        } else {
+          part = mma8_16(code32(d.c[s][0], d.c[s][1]), code32(d.x[t][0], d.x[t][1]), zero);
         }
-      } else {
-        part = mma8_16(code32(b.c[0], b.c[1]), code32(b.x[t][0], b.x[t][1]), zero);
-      }
-      const float s = b.s[t] * b.sw;
+        const float by = d.s[t] * d.sw[s];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[t][i] = fmaf(s, part[i], acc[t][i]);
-    }
+        for (int i = 0; i < 4; ++i) acc[s][t][i] = fmaf(by, part[i], acc[s][t][i]);
+      }
   };
   // the blocks w, w + WAVES, .. of k, kDeep of them on their way
   Block held[kDeep];
@@ -789,27 +820,33 @@ __global__ __launch_bounds__(WAVES * 64) void rows8_kernel(FfnArgs p) {
       }
   }
 #pragma unroll
-  for (int t = 0; t < TT; ++t) sums[w][t][lane] = acc[t];
+  for (int s = 0; s < NS; ++s)
+#pragma unroll
+    for (int t = 0; t < TT; ++t) sums[w][s * TT + t][lane] = acc[s][t];
   __syncthreads();
-  if (w >= TT) return;
-  f32x4 v = sums[0][w][lane];
-  for (int k = 1; k < WAVES; ++k)
+  // the NS TT tiles of results, one to a wave and turn
+  for (int tile = w; tile < NS * TT; tile += WAVES) {
+    f32x4 v = sums[0][tile][lane];
+    for (int k = 1; k < WAVES; ++k)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] += sums[k][w][lane][i];
-  const int32_t t = t0 + 16 * w + r;
-  if (t >= hi) return;
+      for (int i = 0; i < 4; ++i) v[i] += sums[k][tile][lane][i];
+    const int s = tile / TT;
+    const int32_t t = t0 + 16 * (tile % TT) + r, first = NS == 2 && s ? n0[NS - 1] : n0[0];
+    const int mat = NS == 2 && s ? which[NS - 1] : which[0];
+    if (t >= hi) continue;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int32_t n = n0 + 4 * g + i;
-    if (n >= N) continue;
-    if (kUp) {
-      p.part[(static_cast<int64_t>(t) * 2 + which) * N + n] = v[i];
-    } else {
-      const int64_t at = static_cast<int64_t>(t) * N + n;
-      const float b = p.bias ? v[i] + p.bias[static_cast<int64_t>(e) * N + n] : v[i];
-      const float y = linear_act(p.act, b), res = p.res ? H::to_f32(p.res[at]) : 0.0f;
-      p.o0[at] = H::from_f32(p.res ? y + res : y);
-      if (p.o1) p.o1[at] = H::from_f32(b);
+    for (int i = 0; i < 4; ++i) {
+      const int32_t n = first + 4 * g + i;
+      if (n >= N) continue;
+      if (kUp) {
+        p.part[(static_cast<int64_t>(t) * 2 + mat) * N + n] = v[i];
+      } else {
+        const int64_t at = static_cast<int64_t>(t) * N + n;
+        const float h = p.bias ? v[i] + p.bias[static_cast<int64_t>(e) * N + n] : v[i];
+        const float y = linear_act(p.act, h), res = p.res ? H::to_f32(p.res[at]) : 0.0f;
+        p.o0[at] = H::from_f32(p.res ? y + res : y);
+        if (p.o1) p.o1[at] = H::from_f32(h);
+      }
     }
   }
 }
@@ -832,30 +869,43 @@ __global__ __launch_bounds__(kThreads) void finish_rows8_kernel(FfnArgs p) {
   finish_up8<H>(p, m, n, count, x, v);
 }
 
-template <class H, int KIND, int WAVES, int TT>
+template <class H, int KIND, int WAVES, int TT, int NS>
 void launch_rows8_as(const FfnArgs& p, bool aligned, hipStream_t s) {
   const int64_t groups = static_cast<int64_t>(p.E) + p.T / (16 * TT);
   const int64_t turns = (groups + 65534) / 65535;  // (a grid's y ends at 65,535)
-  const dim3 g(static_cast<unsigned>((p.N + 15) / 16 * (KIND == kFfnUp ? 2 : 1)),
+  const dim3 g(static_cast<unsigned>(((p.N + 15) / 16 * (KIND == kFfnUp ? 2 : 1) + NS - 1) / NS),
                static_cast<unsigned>((groups + turns - 1) / turns), static_cast<unsigned>(turns));
   if (aligned)
-    hipLaunchKernelGGL((rows8_kernel<H, KIND, WAVES, TT, true>), g, dim3(WAVES * 64), 0, s, p);
+    hipLaunchKernelGGL((rows8_kernel<H, KIND, WAVES, TT, NS, true>), g, dim3(WAVES * 64), 0, s, p);
   else
-    hipLaunchKernelGGL((rows8_kernel<H, KIND, WAVES, TT, false>), g, dim3(WAVES * 64), 0, s, p);
+    hipLaunchKernelGGL((rows8_kernel<H, KIND, WAVES, TT, NS, false>), g, dim3(WAVES * 64), 0, s, p);
 }
 
+// Strips of 16 weight rows that do not fill the card
+bool deep8(int64_t E, int64_t N, int matrices) { return (N + 15) / 16 * matrices * E < 1024; }
+// Few rows per expert: 32 on average, and 64 where the strips fill the card.  (4096 x 4096, rows and tiles: 32 tokens 11.5
+// and 21 us, 40 tokens 48 and 21; 300 tokens on 8 experts, gate and up 2048 x 1024: 26 and 37.)
+bool few_rows8(int64_t T, int64_t E, int64_t N, int matrices) { return T <= (deep8(E, N, matrices) ? 32 : 64) * E; }
+
+// Strips that do not fill the card: 16 waves share k.  Otherwise 4, on two strips each, which share x's rows (128
+// tokens on 8 experts of 4096 x 4096: 34 us, 45 with one).  Up to 8, up to 32 and more rows per expert on average: one,
+// two or four matrix tiles of rows.
 template <class H, int KIND>
 void launch_rows8(const FfnArgs& p, bool aligned, hipStream_t s) {
-  const bool deep = static_cast<int64_t>((p.N + 15) / 16) * (KIND == kFfnUp ? 2 : 1) * p.E < 1024;
-  const bool two = static_cast<int64_t>(p.T) > 8ll * p.E;
-  if (deep && two)
-    launch_rows8_as<H, KIND, 16, 2>(p, aligned, s);
-  else if (deep)
-    launch_rows8_as<H, KIND, 16, 1>(p, aligned, s);
-  else if (two)
-    launch_rows8_as<H, KIND, 4, 2>(p, aligned, s);
-  else
-    launch_rows8_as<H, KIND, 4, 1>(p, aligned, s);
+  const int64_t T = p.T, E = p.E;
+  if (deep8(E, p.N, KIND == kFfnUp ? 2 : 1)) {
+    if (T <= 8 * E)
+      launch_rows8_as<H, KIND, 16, 1, 1>(p, aligned, s);
+    else
+      launch_rows8_as<H, KIND, 16, 2, 1>(p, aligned, s);
+  } else {
+    if (T <= 8 * E)
+      launch_rows8_as<H, KIND, 4, 1, 2>(p, aligned, s);
+    else if (T <= 32 * E)
+      launch_rows8_as<H, KIND, 4, 2, 2>(p, aligned, s);
+    else
+      launch_rows8_as<H, KIND, 4, 4, 2>(p, aligned, s);
+  }
   if constexpr (KIND == kFfnUp) {
     const int64_t units = static_cast<int64_t>(p.T) * ((p.N + kB - 1) / kB);
     hipLaunchKernelGGL((finish_rows8_kernel<H>), dim3(static_cast<unsigned>((units + 15) / 16)), dim3(kThreads), 0, s, p);
@@ -864,13 +914,48 @@ void launch_rows8(const FfnArgs& p, bool aligned, hipStream_t s) {
 
 // up's sums of few rows
 size_t rows8_bytes(int64_t T, int64_t N) { return sizeof(float) * 2 * static_cast<size_t>(T) * static_cast<size_t>(N); }
-bool few_rows8(int64_t T, int64_t E) { return T <= 32 * E; }
+
+// Rows that are not 4-byte aligned, packed into the workspace for the tiles: row pitch `wide`, a multiple of 128, zeros
+// behind the row.  x's rows, then each matrix's.
+struct PackArgs {
+  const uint8_t* from[3];
+  int64_t rows[3];
+  uint8_t* to;
+  int32_t K, wide;
+};
+__global__ __launch_bounds__(kThreads) void pack8_kernel(PackArgs a) {
+  const int32_t per = a.wide / 16;
+  const int64_t all = a.rows[0] + a.rows[1] + a.rows[2], step = static_cast<int64_t>(gridDim.x) * kThreads;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; i < all * per; i += step) {
+    const int64_t row = i / per;
+    const int32_t c = static_cast<int32_t>(i - row * per) * 16;
+    int64_t r = row;
+    const uint8_t* from = a.from[0];
+    if (r >= a.rows[0]) {
+      r -= a.rows[0];
+      from = a.from[1];
+      if (r >= a.rows[1]) {
+        r -= a.rows[1];
+        from = a.from[2];
+      }
+    }
+    *reinterpret_cast<uint4*>(a.to + row * a.wide + c) = ld16_part(from + r * a.K + c, a.K - c, c);
+  }
+}
+int32_t packed_width(int64_t K) { return static_cast<int32_t>((K + kB - 1) / kB * kB); }
+size_t packed_bytes(int64_t T, int64_t rows, int64_t K) {
+  return static_cast<size_t>(T + rows) * static_cast<size_t>(packed_width(K));
+}
+// What the tiles can use: partial sums, and rows of a width that leaves them unaligned packed
+size_t tiles8_bytes(int64_t T, int64_t rows, int64_t K) {
+  return (K > 2 * kB ? part8_bytes() : 0) + (K % 4 ? packed_bytes(T, rows, K) : 0);
+}
 
 template <class H, int KIND>
-void launch_tiles8(const FfnArgs& p, bool direct, int64_t tiles, int32_t ncols, hipStream_t s) {
+void launch_tiles8(const FfnArgs& p, bool shifted, int64_t tiles, int32_t ncols, hipStream_t s) {
   constexpr int kTurns = KIND == kFfnUp ? 16 : 32;
   const dim3 g(static_cast<unsigned>(tiles + (p.part ? kSlots8 : 0))), b(kThreads8), bj(kThreads);
-  if (direct)
+  if (shifted)
     hipLaunchKernelGGL((tile8_kernel<H, KIND, true>), g, b, 0, s, p, ncols);
   else
     hipLaunchKernelGGL((tile8_kernel<H, KIND, false>), g, b, 0, s, p, ncols);
@@ -883,7 +968,7 @@ template <int KIND>
 int launch8(FfnArgs p, int32_t dtype, void* workspace, size_t workspace_bytes, hipStream_t s, const char* what) {
   if (p.T == 0) return FP8Z1_OK;
   if (misaligned(workspace, 16)) return refuse(FP8Z1_EINVAL, what, "misaligned workspace");
-  if (few_rows8(p.T, p.E) && (KIND != kFfnUp || workspace_bytes >= rows8_bytes(p.T, p.N))) {
+  if (few_rows8(p.T, p.E, p.N, KIND == kFfnUp ? 2 : 1) && (KIND != kFfnUp || workspace_bytes >= rows8_bytes(p.T, p.N))) {
     const bool aligned = !misaligned(p.x0, 16) && !misaligned(p.w0, 16) && !misaligned(p.w1, 16) && p.K % 16 == 0;
     p.part = static_cast<float*>(workspace);
     if (dtype == FP8Z1_BF16)
@@ -892,7 +977,7 @@ int launch8(FfnArgs p, int32_t dtype, void* workspace, size_t workspace_bytes, h
       launch_rows8<F16, KIND>(p, aligned, s);
     return launched(what);
   }
-  const bool direct = !misaligned(p.x0, 4) && !misaligned(p.w0, 4) && !misaligned(p.w1, 4) && p.K % 4 == 0;
+  bool shifted = misaligned(p.x0, 4) || misaligned(p.w0, 4) || misaligned(p.w1, 4) || p.K % 4 != 0;
   const int32_t per = KIND == kFfnUp ? kCols8 / 2 : kCols8, ncols = (p.N + per - 1) / per;
   const int64_t tiles = (p.T / kRows8 + (p.T < p.E ? p.T : p.E)) * static_cast<int64_t>(ncols);  // (every run may end in a partial tile)
   if (tiles > 0x7fffffff / kThreads8 - kSlots8) return refuse(FP8Z1_ESHAPE, what, "too many tiles");
@@ -900,10 +985,33 @@ int launch8(FfnArgs p, int32_t dtype, void* workspace, size_t workspace_bytes, h
   const int64_t known = p.offsets ? tiles : static_cast<int64_t>((p.T + kRows8 - 1) / kRows8) * ncols;
   if ((p.offsets ? kb >= 4 : tile_splits8(known, kb) > 1) && workspace_bytes >= part8_bytes())
     p.part = static_cast<float*>(workspace);
+  // Unaligned rows are packed where the workspace has room, behind the partial sums: y 8000 x 4001 of width 4001 takes 184
+  // us so, 292 on shifted tiles and 173 at width 4000; 2568 x 1152 of width 822 on 5 experts 45, 51 and 38.
+  const int64_t rows = static_cast<int64_t>(p.E) * p.N, sums = p.K > 2 * kB ? static_cast<int64_t>(part8_bytes()) : 0;
+  if (shifted && workspace_bytes >= sums + packed_bytes(p.T, (KIND == kFfnUp ? 2 : 1) * rows, p.K)) {
+    PackArgs a{};
+    a.from[0] = p.x0;
+    a.from[1] = p.w0;
+    a.from[2] = p.w1;
+    a.rows[0] = p.T;
+    a.rows[1] = rows;
+    a.rows[2] = KIND == kFfnUp ? rows : 0;
+    a.to = static_cast<uint8_t*>(workspace) + sums;
+    a.K = p.K;
+    a.wide = packed_width(p.K);
+    const int64_t groups = ((a.rows[0] + a.rows[1] + a.rows[2]) * (a.wide / 16) + kThreads - 1) / kThreads;
+    hipLaunchKernelGGL(pack8_kernel, dim3(static_cast<unsigned>(groups < (1 << 20) ? groups : 1 << 20)), dim3(kThreads), 0,
+                       s, a);
+    p.x0 = a.to;
+    p.w0 = a.to + a.rows[0] * a.wide;
+    p.w1 = p.w0 + rows * a.wide;
+    p.K = a.wide;
+    shifted = false;
+  }
   if (dtype == FP8Z1_BF16)
-    launch_tiles8<Bf16, KIND>(p, direct, tiles, ncols, s);
+    launch_tiles8<Bf16, KIND>(p, shifted, tiles, ncols, s);
   else
-    launch_tiles8<F16, KIND>(p, direct, tiles, ncols, s);
+    launch_tiles8<F16, KIND>(p, shifted, tiles, ncols, s);
   return launched(what);
 }
 

@@ -287,6 +287,31 @@ def test_without_a_workspace():
         assert float((a - b).norm()) <= 0.01 * float(a.norm())
 
 
+@pytest.mark.parametrize("T,N,K", [(300, 140, 257), (200, 300, 1003), (257, 129, 130), (100, 70, 1), (90, 40, 514)])
+def test_odd_widths_without_room_to_pack(T, N, K):
+    """Rows that are not 4-byte aligned, read shifted where they cannot be packed: as packed, to float32's rounding."""
+    import blockwise_fp8_zero_fold_amd as fz
+    g, w, _, x, xd = make(T, 1, N, K, "e4m3")
+    p, mag = ref.grouped(xd, ref.dequantize(*w), None, False)
+    bound = ref.rounded(p, sum_error(mag, K), torch.bfloat16)
+    f = fz.Product(T, 1, N, K, fz.BF16, fz.E4M3, fz.ACT_NONE, 0)
+    for off in (0, 1, 2):  # rows and codes at every place in a word
+        xc = torch.zeros(T * K + off, dtype=torch.uint8, device="cuda")[off:]
+        wc = torch.zeros(N * K + 2 * off, dtype=torch.uint8, device="cuda")[2 * off:]
+        xc.copy_(x[0].flatten())
+        wc.copy_(w[0].flatten())
+        y = torch.zeros(T, N, dtype=torch.bfloat16, device="cuda")
+        fz.fp8z1_linear(f, xc, x[1].cuda(), wc, w[1].cuda(), None, None, None, y)
+        ref.check(y, p, bound, "y")
+        wu = ref.make_weight(g, 1, N, K)
+        want, _ = block().ffn_up8(pair(x), pair(w), pair(wu))
+        codes, scales = torch.zeros_like(want[0]), torch.zeros_like(want[1])
+        fz.fp8z1_ffn_up8(fz.Ffn(T, 1, K, N, fz.BF16, fz.ACT_SILU), xc, x[1].cuda(), wc, w[1].cuda(), *pair(wu), None, None, None,
+                         codes, scales)
+        a, b = (r8.dequantize(c.cpu(), s.cpu()) for c, s in (want, (codes, scales)))
+        assert float((a - b).norm()) <= 1e-3 * float(a.norm())  # (a code may flip)
+
+
 def test_unaligned_buffers_and_the_residual_in_place():
     import blockwise_fp8_zero_fold_amd as fz
     for T, N, K in ((5, 40, 256), (100, 70, 256)):
