@@ -75,26 +75,50 @@ __device__ __forceinline__ Kept load_kept(const FfnArgs& p, int64_t at, int coun
   return k;
 }
 
+// 8 columns of a row, rounded to the result's type.
+template <class H>
+__device__ __forceinline__ void put8(const float (&f)[8], uint16_t* to, int count) {
+  uint32_t o[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    o[k] = static_cast<uint32_t>(H::from_f32(f[2 * k])) | static_cast<uint32_t>(H::from_f32(f[2 * k + 1])) << 16;
+  store_row8(to, o, count);
+}
+
 // y = res + act(x + bias) of 8 columns from column n of a row on, and x + bias (what the backward pass
 // needs) where it is wanted; both are rounded once.  `bias` is the expert's.
+// The choices are the launch's, each taken once for the 8 columns.
 template <class H>
 __device__ __forceinline__ void finish_linear(const FfnArgs& p, int64_t at, int32_t n, int count, const float (&x)[8]) {
-  uint32_t r[4] = {}, o[4], k[4];
-  float y[8], b[8];
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = x[i];
+  uint32_t r[4] = {};
   if (p.res) load_row8(p.res + at, r, count);
+  if (p.bias) {
+    if (count == 8) {
+      const float4 b0 = ld_global_a4(p.bias + n), b1 = ld_global_a4(p.bias + n + 4);
+      const float b[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    b[i] = p.bias && i < count ? x[i] + p.bias[n + i] : x[i];
-    y[i] = linear_act(p.act, b[i]);
-    if (p.res) y[i] += H::to_f32(static_cast<uint16_t>(r[i / 2] >> (16 * (i % 2))));
-  }
+      for (int i = 0; i < 8; ++i) y[i] += b[i];
+    } else {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    o[i] = static_cast<uint32_t>(H::from_f32(y[2 * i])) | static_cast<uint32_t>(H::from_f32(y[2 * i + 1])) << 16;
-    k[i] = static_cast<uint32_t>(H::from_f32(b[2 * i])) | static_cast<uint32_t>(H::from_f32(b[2 * i + 1])) << 16;
+      for (int i = 0; i < 8; ++i)
+        if (i < count) y[i] += p.bias[n + i];
+    }
   }
-  store_row8(p.o0 + at, o, count);
-  if (p.o1) store_row8(p.o1 + at, k, count);
+  if (p.o1) put8<H>(y, p.o1 + at, count);
+  if (p.act == FP8Z1_ACT_SILU) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = act_value(FP8Z1_ACT_SILU, y[i]);
+  } else if (p.act == FP8Z1_ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = act_value(FP8Z1_ACT_GELU, y[i]);
+  }
+  if (p.res)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] += H::to_f32(static_cast<uint16_t>(r[i / 2] >> (16 * (i % 2))));
+  put8<H>(y, p.o0 + at, count);
 }
 
 // The results of 8 columns of a row, of which `count` are there (for kFfnUp x: gate, v: up).

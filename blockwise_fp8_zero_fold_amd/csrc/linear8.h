@@ -597,7 +597,19 @@ __global__ __launch_bounds__(kThreads8) void tile8_kernel(FfnArgs p, int32_t nco
         lay_tile(half_ ? acc[i][3] : acc[i][1], mine, i, 1);
       }
       handed_over();
-      store_rows<H, kLinear>(p, mine, mw, hi, n0 + wn * 128 + half_ * 64);
+      // 8 lanes a row, the next 8 rows read ahead
+      const int32_t n = n0 + wn * 128 + half_ * 64 + 8 * (lane & 7);
+      const int columns = min(N - n, 8);
+      float x[8], ahead[8];
+      read8(mine, lane >> 3, 2 * (lane & 7), x);
+#pragma unroll 1
+      for (int k = 0; k < 8; ++k) {
+        const int32_t m = mw + k * 8 + (lane >> 3);
+        read8(mine, min(k + 1, 7) * 8 + (lane >> 3), 2 * (lane & 7), ahead);
+        if (m < hi && columns > 0) finish_linear<H>(p, static_cast<int64_t>(m) * N + n, n, columns, x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = ahead[i];
+      }
       handed_over();
     }
   } else {
@@ -631,6 +643,16 @@ __global__ __launch_bounds__(kThreads8) void tile8_kernel(FfnArgs p, int32_t nco
         handed_over();
       }
     }
+    auto activate = [&](auto act_) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[u & 1][u >> 1][r] = act_value(decltype(act_)::value, acc[u & 1][u >> 1][r]);
+    };
+    if (p.act == FP8Z1_ACT_SILU)
+      activate(Int<FP8Z1_ACT_SILU>{});
+    else
+      activate(Int<FP8Z1_ACT_GELU>{});
     // a in place of gate; the largest magnitude of a row over this wave's 64 columns, then over both waves'
     float* const tops = reinterpret_cast<float*>(lds + kResults8);  // [2][256]
     float top[2] = {0.0f, 0.0f};
@@ -641,9 +663,8 @@ __global__ __launch_bounds__(kThreads8) void tile8_kernel(FfnArgs p, int32_t nco
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
           const int32_t n = n0 + wn * 64 + j * 32 + 8 * (r / 4) + 4 * half + r % 4;
-          const float a = act_value(p.act, acc[i][j][r]) * acc[i][j + 2][r];
-          acc[i][j][r] = a;
-          top[i] = fmaxf(top[i], n < N ? fabsf(a) : 0.0f);
+          acc[i][j][r] *= acc[i][j + 2][r];
+          top[i] = fmaxf(top[i], n < N ? fabsf(acc[i][j][r]) : 0.0f);
         }
       top[i] = fmaxf(top[i], __shfl_xor(top[i], 32));
       if (half == 0) tops[wn * kRows8 + wm * 64 + i * 32 + l32] = top[i];
