@@ -108,7 +108,7 @@ size_t part8_bytes() { return sizeof(float) * kSlots8 * kRows8 * kCols8; }
 
 // a = act(gate) * up of 8 columns from column c of the results on, with 16 neighbouring lanes on the 128
 // columns of a group: h and u where they are wanted, codes and the group's scale.
-typedef uint32_t v2u_a1_rw_global_t __attribute__((ext_vector_type(2), aligned(1), address_space(1)));
+typedef uint32_t v2u_a1_wratioglobal_t __attribute__((ext_vector_type(2), aligned(1), address_space(1)));
 template <class H>
 __device__ __forceinline__ void finish_up8(const FfnArgs& p, int64_t m, int32_t n, int count, const float (&x)[8],
                                            const float (&v)[8]) {
@@ -125,11 +125,11 @@ __device__ __forceinline__ void finish_up8(const FfnArgs& p, int64_t m, int32_t 
   if (count <= 0) return;
   const float scale = row8_scale(top, p.pow2 != 0);
   if (n % kB == 0) p.code_scales[m * ((p.N + kB - 1) / kB) + n / kB] = scale;
-  const Over8 over = over8(scale, p.pow2 != 0);
+  const Over8 over = over8(scale);
   const uint32_t lo = codes4(a[0], a[1], a[2], a[3], over), hi = codes4(a[4], a[5], a[6], a[7], over);
   uint8_t* const to = p.codes + m * p.N + n;
   if (count == 8) {
-    *(v2u_a1_rw_global_t*)(to) = v2u_t{lo, hi};
+    *(v2u_a1_wratioglobal_t*)(to) = v2u_t{lo, hi};
   } else {
     for (int i = 0; i < count; ++i) to[i] = static_cast<uint8_t>((i < 4 ? lo : hi) >> (8 * (i & 3)));
   }
@@ -562,6 +562,11 @@ __global__ __launch_bounds__(kThreads8) void tile8_kernel(FfnArgs p, int32_t nco
     __syncthreads();  // the results take the stages' place
   }
 
+  // The lane's place anew from the thread's number, so that nothing derived from it lives through the loop above
+  // only for what follows (its registers are all taken).
+  int after = threadIdx.x;
+  asm volatile("" : "+v"(after));
+  const int lane_ = after & 63, half2 = lane_ >> 5, l2 = lane_ & 31;
   uint8_t* const mine = lds + w * (kResultBytes / 4);
   const int32_t mw = m0 + wm * 64;
   if (split) {  // float32 sums [256][256], up: gate's 128 columns, then up's
@@ -576,7 +581,7 @@ __global__ __launch_bounds__(kThreads8) void tile8_kernel(FfnArgs p, int32_t nco
       handed_over();
       const int32_t c0 = kUp ? half_ * 128 + wn * 64 : wn * 128 + half_ * 64;
       for (int k = 0; k < 8; ++k) {
-        const int r = k * 8 + (lane >> 3), c = lane & 7;
+        const int r = k * 8 + (lane_ >> 3), c = lane_ & 7;
         if (mw + r >= hi) continue;
         float x[8];
         read8(mine, r, 2 * c, x);
@@ -598,14 +603,14 @@ __global__ __launch_bounds__(kThreads8) void tile8_kernel(FfnArgs p, int32_t nco
       }
       handed_over();
       // 8 lanes a row, the next 8 rows read ahead
-      const int32_t n = n0 + wn * 128 + half_ * 64 + 8 * (lane & 7);
+      const int32_t n = n0 + wn * 128 + half_ * 64 + 8 * (lane_ & 7);
       const int columns = min(N - n, 8);
       float x[8], ahead[8];
-      read8(mine, lane >> 3, 2 * (lane & 7), x);
+      read8(mine, lane_ >> 3, 2 * (lane_ & 7), x);
 #pragma unroll 1
       for (int k = 0; k < 8; ++k) {
-        const int32_t m = mw + k * 8 + (lane >> 3);
-        read8(mine, min(k + 1, 7) * 8 + (lane >> 3), 2 * (lane & 7), ahead);
+        const int32_t m = mw + k * 8 + (lane_ >> 3);
+        read8(mine, min(k + 1, 7) * 8 + (lane_ >> 3), 2 * (lane_ & 7), ahead);
         if (m < hi && columns > 0) finish_linear<H>(p, static_cast<int64_t>(m) * N + n, n, columns, x);
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = ahead[i];
@@ -623,7 +628,7 @@ __global__ __launch_bounds__(kThreads8) void tile8_kernel(FfnArgs p, int32_t nco
         }
         handed_over();
         for (int k = 0; k < 4; ++k) {
-          const int r = k * 16 + (lane >> 2), c = lane & 3;
+          const int r = k * 16 + (lane_ >> 2), c = lane_ & 3;
           const int32_t n = n0 + wn * 64 + half_ * 32 + 8 * c;
           const int count = mw + r < hi ? min(N - n, 8) : 0;
           if (count <= 0) continue;
@@ -643,56 +648,56 @@ __global__ __launch_bounds__(kThreads8) void tile8_kernel(FfnArgs p, int32_t nco
         handed_over();
       }
     }
-    auto activate = [&](auto act_) {
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) acc[u & 1][u >> 1][r] = act_value(decltype(act_)::value, acc[u & 1][u >> 1][r]);
-    };
-    if (p.act == FP8Z1_ACT_SILU)
-      activate(Int<FP8Z1_ACT_SILU>{});
-    else
-      activate(Int<FP8Z1_ACT_GELU>{});
     // a in place of gate; the largest magnitude of a row over this wave's 64 columns, then over both waves'
     float* const tops = reinterpret_cast<float*>(lds + kResults8);  // [2][256]
     float top[2] = {0.0f, 0.0f};
+    const bool past = n0 + kCols8 / 2 > N;  // columns past the last count for nothing
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < 2; ++j) {
+        if (p.act == FP8Z1_ACT_SILU) {
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int32_t n = n0 + wn * 64 + j * 32 + 8 * (r / 4) + 4 * half + r % 4;
-          acc[i][j][r] *= acc[i][j + 2][r];
-          top[i] = fmaxf(top[i], n < N ? fabsf(acc[i][j][r]) : 0.0f);
+          for (int r = 0; r < 16; ++r) acc[i][j][r] = act_value(FP8Z1_ACT_SILU, acc[i][j][r]) * acc[i][j + 2][r];
+        } else {
+#pragma unroll
+          for (int r = 0; r < 16; ++r) acc[i][j][r] = act_value(FP8Z1_ACT_GELU, acc[i][j][r]) * acc[i][j + 2][r];
         }
+        if (past) {
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            if (n0 + wn * 64 + j * 32 + 8 * (r / 4) + 4 * half2 + r % 4 >= N) acc[i][j][r] = 0.0f;
+        }
+#pragma unroll
+        for (int r = 0; r < 16; ++r) top[i] = fmaxf(top[i], fabsf(acc[i][j][r]));
+      }
       top[i] = fmaxf(top[i], __shfl_xor(top[i], 32));
-      if (half == 0) tops[wn * kRows8 + wm * 64 + i * 32 + l32] = top[i];
+      if (half2 == 0) tops[wn * kRows8 + wm * 64 + i * 32 + l2] = top[i];
     }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int r = wm * 64 + i * 32 + l32;
+      const int r = wm * 64 + i * 32 + l2;
       const float scale = row8_scale(fmaxf(top[i], tops[(1 - wn) * kRows8 + r]), p.pow2 != 0);
-      const Over8 over = over8(scale, p.pow2 != 0);
-      if (wn == 0 && half == 0 && m0 + r < hi) p.code_scales[static_cast<int64_t>(m0 + r) * nb + n0 / kB] = scale;
+      const Over8 over = over8(scale);
+      if (wn == 0 && half2 == 0 && m0 + r < hi) p.code_scales[static_cast<int64_t>(m0 + r) * nb + n0 / kB] = scale;
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int g = 0; g < 4; ++g)
-          *reinterpret_cast<uint32_t*>(mine + (i * 32 + l32) * 64 + ((j * 32 + 8 * g + 4 * half) ^ ((l32 & 3) << 4))) =
+          *reinterpret_cast<uint32_t*>(mine + (i * 32 + l2) * 64 + ((j * 32 + 8 * g + 4 * half2) ^ ((l2 & 3) << 4))) =
               codes4(acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3], over);
     }
     handed_over();
     for (int k = 0; k < 4; ++k) {
-      const int r = k * 16 + (lane >> 2), c = (lane & 3) * 16;
+      const int r = k * 16 + (lane_ >> 2), c = (lane_ & 3) * 16;
       const int32_t n = n0 + wn * 64 + c, count = mw + r < hi ? min(N - n, 16) : 0;
       if (count <= 0) continue;
       const uint4 v = *reinterpret_cast<const uint4*>(mine + r * 64 + (c ^ ((r & 3) << 4)));
       uint8_t* const to = p.codes + static_cast<int64_t>(mw + r) * N + n;
-      typedef uint32_t v4u_a1_rw_t __attribute__((ext_vector_type(4), aligned(1), address_space(1)));
+      typedef uint32_t v4u_a1_wratiot __attribute__((ext_vector_type(4), aligned(1), address_space(1)));
       if (count == 16) {
-        *(v4u_a1_rw_t*)(to) = v4u_v_t{v.x, v.y, v.z, v.w};
+        *(v4u_a1_wratiot*)(to) = v4u_v_t{v.x, v.y, v.z, v.w};
       } else {
         const uint32_t words[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll

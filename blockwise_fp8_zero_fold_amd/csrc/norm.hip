@@ -110,7 +110,7 @@ __device__ __forceinline__ void store_codes(const NormArgs& a, int64_t row, int3
   if (c >= a.C) return;
   const float scale = row8_scale(top, a.pow2 != 0);
   if (c % kB == 0) a.scales[row * ((a.C + kB - 1) / kB) + c / kB] = scale;
-  const Over8 over = over8(scale, a.pow2 != 0);
+  const Over8 over = over8(scale);
   const uint32_t lo = codes4(n[0], n[1], n[2], n[3], over), hi = codes4(n[4], n[5], n[6], n[7], over);
   uint8_t* const to = a.codes + row * a.C + c;
   if (c + 8 <= a.C) {

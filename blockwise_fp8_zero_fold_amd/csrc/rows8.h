@@ -18,7 +18,7 @@ __device__ __forceinline__ float row8_scale(float amax, bool pow2) {
   if (amax == 0.0f) return 1.0f;
   float s = amax / kTop8;
   if (pow2) {
-    // the exponent's field less 8; (of an infinite amax the largest power there is, of a subnormal the least)
+    // the exponent's field less 8 (of a subnormal amax the least there is; an infinite amax stays so)
     const int32_t e = static_cast<int32_t>(__float_as_uint(amax) >> 23) - 8;
     if (amax < __builtin_huge_valf()) s = __uint_as_float(static_cast<uint32_t>(e < 1 ? 1 : e) << 23);
   }
@@ -26,32 +26,32 @@ __device__ __forceinline__ float row8_scale(float amax, bool pow2) {
 }
 
 // Division by a group's scale.  The steps are those of a correctly rounded division (a reciprocal refined once, a
-// quotient corrected twice by its remainder), with the reciprocal taken once for the group and no scaling of the
-// operands: for scales from 2^-60 to 2^60 nothing in them leaves the normal numbers unless the quotient is below
-// 2^-20, which is code 0 either way.
+// quotient corrected twice by its remainder), with the reciprocal taken once for the group.  For scales from 2^-60 to
+// 2^60 nothing in them leaves the normal numbers unless the quotient is below 2^-20, which is code 0 either way; other
+// scales are brought there by a power of two, and so is what is divided (`times`; what that takes below the normal
+// numbers has a quotient below 2^-120).  Of an infinite scale, times is 0 and the scale 1: 0 of what is finite.
 struct Over8 {
-  float scale, inverse;
-  bool plain;  // scales outside that range: a division each
-  bool cut;    // the power of two rule, whose quotients may pass 448
+  float scale, inverse, times;
 };
-__device__ __forceinline__ Over8 over8(float scale, bool pow2) {
-  const float r = __builtin_amdgcn_rcpf(scale);
-  return Over8{scale, fmaf(fmaf(-scale, r, 1.0f), r, r), !(scale >= 0x1p-60f && scale <= 0x1p60f), pow2};
-}
-__device__ __forceinline__ float quotient8(float x, const Over8& o) {
-  if (o.plain) return x / o.scale;
-  const float q0 = x * o.inverse, q1 = fmaf(fmaf(-q0, o.scale, x), o.inverse, q0);
-  return copysignf(fmaf(fmaf(-q1, o.scale, x), o.inverse, q1), x);  // (a zero's sign is lost in the sums)
+__device__ __forceinline__ Over8 over8(float scale) {
+  float times = 1.0f;
+  if (scale < 0x1p-60f) times = 0x1p66f;
+  if (scale > 0x1p60f) times = 0x1p-66f;
+  float s = scale * times;
+  if (scale == __builtin_huge_valf()) s = 1.0f, times = 0.0f;
+  const float r = __builtin_amdgcn_rcpf(s);
+  return Over8{s, fmaf(fmaf(-s, r, 1.0f), r, r), times};
 }
 
 // 4 values over their group's scale as codes, the first in the lowest byte.  The hardware's conversion rounds to
-// nearest even; what it makes of values past 448 hangs on a mode, so they are cut off before it.
+// nearest even; what it makes of values past 448 (which the rule of powers of two has) hangs on a mode, so they are
+// cut off before it.  The sign is x's own, since a zero loses its sign in the sums.
 __device__ __forceinline__ uint32_t codes4(float x0, float x1, float x2, float x3, const Over8& o) {
-  auto over = [&](float x) {
-    const float q = quotient8(x, o);
-    if (!o.cut) return q;  // (amax / (amax / 448) rounds to 448 or its neighbours, which are code 448)
-    const float c = fminf(fmaxf(q, -kTop8), kTop8);
-    return q != q ? q : c;
+  auto over = [&](float v) {
+    const float x = v * o.times;
+    const float q0 = x * o.inverse, q1 = fmaf(fmaf(-q0, o.scale, x), o.inverse, q0);
+    const float q = fmaf(fmaf(-q1, o.scale, x), o.inverse, q1);
+    return copysignf(fabsf(q) > kTop8 ? kTop8 : q, v);
   };
   int w = __builtin_amdgcn_cvt_pk_fp8_f32(over(x0), over(x1), 0, false);
   w = __builtin_amdgcn_cvt_pk_fp8_f32(over(x2), over(x3), w, true);
