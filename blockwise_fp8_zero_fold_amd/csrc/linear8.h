@@ -108,7 +108,7 @@ size_t part8_bytes() { return sizeof(float) * kSlots8 * kRows8 * kCols8; }
 
 // a = act(gate) * up of 8 columns from column c of the results on, with 16 neighbouring lanes on the 128
 // columns of a group: h and u where they are wanted, codes and the group's scale.
-typedef uint32_t v2u_a1_wratioglobal_t __attribute__((ext_vector_type(2), aligned(1), address_space(1)));
+typedef uint32_t v2u_a1_rw_global_t __attribute__((ext_vector_type(2), aligned(1), address_space(1)));
 template <class H>
 __device__ __forceinline__ void finish_up8(const FfnArgs& p, int64_t m, int32_t n, int count, const float (&x)[8],
                                            const float (&v)[8]) {
@@ -129,7 +129,7 @@ __device__ __forceinline__ void finish_up8(const FfnArgs& p, int64_t m, int32_t 
   const uint32_t lo = codes4(a[0], a[1], a[2], a[3], over), hi = codes4(a[4], a[5], a[6], a[7], over);
   uint8_t* const to = p.codes + m * p.N + n;
   if (count == 8) {
-    *(v2u_a1_wratioglobal_t*)(to) = v2u_t{lo, hi};
+    *(v2u_a1_rw_global_t*)(to) = v2u_t{lo, hi};
   } else {
     for (int i = 0; i < count; ++i) to[i] = static_cast<uint8_t>((i < 4 ? lo : hi) >> (8 * (i & 3)));
   }
@@ -695,9 +695,9 @@ __global__ __launch_bounds__(kThreads8) void tile8_kernel(FfnArgs p, int32_t nco
       if (count <= 0) continue;
       const uint4 v = *reinterpret_cast<const uint4*>(mine + r * 64 + (c ^ ((r & 3) << 4)));
       uint8_t* const to = p.codes + static_cast<int64_t>(mw + r) * N + n;
-      typedef uint32_t v4u_a1_wratiot __attribute__((ext_vector_type(4), aligned(1), address_space(1)));
+      typedef uint32_t v4u_a1_rw_global_t __attribute__((ext_vector_type(4), aligned(1), address_space(1)));
       if (count == 16) {
-        *(v4u_a1_wratiot*)(to) = v4u_v_t{v.x, v.y, v.z, v.w};
+        *(v4u_a1_rw_global_t*)(to) = v4u_v_t{v.x, v.y, v.z, v.w};
       } else {
         const uint32_t words[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll

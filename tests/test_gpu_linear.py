@@ -242,6 +242,26 @@ def test_up8(T, E, D, F, dtype, act, rule):
     check_up8(x, xd, wg, ref.make_weight(g, E, F, D), offsets, T, D, F, dtype, act, rule)
 
 
+@pytest.mark.parametrize("T,E,N,K", [(9000, 7, 2500, 100), (5000, 3, 4200, 128), (8200, 20, 2308, 260), (6000, 1, 2900, 900)])
+@pytest.mark.parametrize("act,with_bias,with_res", [(None, False, False), ("silu", True, True)])
+def test_more_tiles_than_compute_units(T, E, N, K, act, with_bias, with_res):
+    """Whole tiles before split ones: of one block of k, and of blocks that end inside."""
+    test_forward(T, E, N, K, "e4m3", torch.bfloat16, act, with_bias, with_res)
+
+
+@pytest.mark.parametrize("T,E,D,F", [(9000, 6, 100, 1300), (8200, 3, 260, 1152), (6000, 1, 1000, 1700)])
+@pytest.mark.parametrize("apart", [False, True])
+def test_up8_more_tiles_than_compute_units(T, E, D, F, apart):
+    """The same; and tiles among them that are done again, since a row's scales leave the units' range."""
+    g, wg, offsets, x, xd = make(T, E, F, D, "e4m3")
+    if apart:
+        for row in (5, T // 2, T // 2 + 700, T - 3):
+            x[1][row] = 2.0 ** -90
+            x[1][row, -1] = 2.0 ** 25
+        xd = r8.dequantize(*x)
+    check_up8(x, xd, wg, ref.make_weight(g, E, F, D), offsets, T, D, F, torch.bfloat16, "silu", "amax")
+
+
 @pytest.mark.parametrize("T,D,F", [(20, 520, 140), (300, 520, 140), (200, 2048, 300), (300, 1001, 130)])
 def test_up8_scales_far_apart(T, D, F):
     """Scales whose ratios leave float32's range, zero and negative ones: the sums are the same float32 sums."""
