@@ -145,8 +145,8 @@ def combine(rows: torch.Tensor, row_of: torch.Tensor, weights: Optional[torch.Te
 
 def combine_backward(dy: torch.Tensor, rows: torch.Tensor, row_of: torch.Tensor, weights: torch.Tensor,
                      out: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
-    """(drows [R,D], dweights [T,k]) from dy [T,D] (which is base's gradient too).  drows go to ``out`` if it is given;
-    rows that no choice has are not written."""
+    """(drows [R,D], dweights [T,k]) from dy [T,D] (which is base's gradient too).  drows go to ``out`` if it is given
+    (it may be ``rows`` itself); rows that no choice has are not written."""
     what = "combine_backward"
     dev, R, D, px = _rows(rows, what)
     T = row_of.shape[0]

@@ -552,7 +552,8 @@ int fp8z1_combine(const fp8z1_routed* f, const int32_t* row_of, const void* rows
                   void* y, void* stream);
 
 /* Its gradients from dy [T,D]: drows, row row_of[t][j] = weights[t][j] dy[t] (other rows stay as they were), and dweights
- * [T,k] float32 = <dy[t], rows[row_of[t][j]]> (0 where there is no row); one of them may be NULL.  (base has dy.) */
+ * [T,k] float32 = <dy[t], rows[row_of[t][j]]> (0 where there is no row); one of them may be NULL.  drows may be rows
+ * itself.  (base has dy.) */
 int fp8z1_combine_bwd(const fp8z1_routed* f, const int32_t* row_of, const void* dy, const void* rows,
                       const float* weights, void* drows, float* dweights, void* stream);
 

@@ -189,3 +189,37 @@ def test_layer_in_a_graph(T, D, F, E, k):
         eager = {n: to(v, "cpu") for n, v in step(W, {n: v.cuda() for n, v in x.items()}, k, "softmax").items()}
         for (name, a), (_, b) in zip(flat(got), flat(eager)):
             assert torch.equal(a, b), (seed, name)
+
+
+def test_two_threads_on_streams_of_their_own():
+    """Steps of two threads at once give what they give alone."""
+    import threading
+    T, D, F, E, k = SIZES[2]
+    jobs = []
+    for seed in (1, 2):
+        W, x = make(T, D, F, E, torch.bfloat16, seed)
+        jobs.append(({n: to(w, "cuda") for n, w in W.items()}, {n: v.cuda() for n, v in x.items()}))
+    alone = [{n: to(v, "cpu") for n, v in step(W, x, k, "softmax").items()} for W, x in jobs]
+    torch.cuda.synchronize()
+    together, failures = [None, None], []
+
+    def run(i):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                for _ in range(5):
+                    out = step(*jobs[i], k, "softmax")
+                stream.synchronize()
+                together[i] = {n: to(v, "cpu") for n, v in out.items()}
+        except Exception as e:  # (shown by the assertion below)
+            failures.append(e)
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failures
+    for a, b in zip(alone, together):
+        for (name, u), (_, v) in zip(flat(a), flat(b)):
+            assert torch.equal(u, v), name

@@ -173,6 +173,18 @@ def test_gradients_against_differences():
     assert abs(by_w - float((dw.cpu().double() * step_w.double()).sum())) < 1e-3
 
 
+@pytest.mark.parametrize("T,k,D,dtype", [(50, 3, 7168, torch.bfloat16), (9, 20, 1001, torch.float16), (300, 2, 63, torch.float32)])
+def test_gradient_in_place_of_the_rows(T, k, D, dtype):
+    g = torch.Generator().manual_seed(T)
+    _, row_of = routing().sort_tokens(make_experts(g, T, k, 40).cuda(), 40)
+    rows, dy = torch.randn(T * k, D, generator=g).to(dtype).cuda(), torch.randn(T, D, generator=g).to(dtype).cuda()
+    w = torch.rand(T, k, generator=g).cuda()
+    out = rows.clone()  # (rows that no choice has stay)
+    drows, dw = routing().combine_backward(dy, rows, row_of, w, out=out)
+    same, dw2 = routing().combine_backward(dy, rows, row_of, w, out=rows)
+    assert same is rows and torch.equal(rows, drows) and torch.equal(dw, dw2)
+
+
 def test_nan_and_infinite_rows():
     inf, nan = float("inf"), float("nan")
     rows = torch.tensor([[nan], [1.0], [inf]], device="cuda")
