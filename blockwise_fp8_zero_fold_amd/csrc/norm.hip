@@ -14,6 +14,9 @@
 // and 235, 16,384 353 and 1590.  Backward, rows that are no multiple of 8 wide are loaded when they are needed
 // instead of a row ahead (7001: 290 us), and above 8192, where a thread holds two chunks, 143 to 238
 // registers spill (8200: 1150 us); up to 8192 2 to 11 do.  The forward pass spills none.
+//
+// With n in 8 bits (EIGHT) the same pass finds each group's largest magnitude and writes codes and scales, besides n in
+// 16 bits or in its place: 8192 rows of 7168 as above, n kept too, 143 us (0.77 GB, 5.35 TB/s); two rows 5.4.
 #include <hip/hip_runtime.h>
 
 #include "device_util.h"

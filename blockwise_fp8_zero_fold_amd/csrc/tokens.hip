@@ -6,6 +6,13 @@
 //   drows[row_of[t][j]] = w[t][j] dy[t],  dw[t][j] = sum_c dy[t][c] rows[row_of[t][j]][c]
 // All but the plan are bound by HBM: each token's row is read once and its k rows are written (or read)
 // once, by the token's own workgroup, so nothing is added to by two workgroups and no atomics are needed.
+//
+// 8192 tokens of 7168 in bfloat16 with 8 choices of 64 experts (a copy of 0.94 GB moves 4.9 to 5.75 TB/s here):
+//   plan           9 us    two launches: 128 workgroups' counts, then the places (5 + 4)
+//   dispatch     200 us    1.06 GB, 5.2 TB/s
+//   combine      217 us    1.06 GB, 4.9 TB/s
+//   its gradient 387 us    2.0 GB, 5.15 TB/s
+// Copying in the rows' order instead (each row looks its token up, and reads it again) took 217 to 290 us.
 #include <hip/hip_runtime.h>
 
 #include "device_util.h"

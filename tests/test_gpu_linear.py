@@ -370,6 +370,18 @@ def test_rows_without_an_expert_and_offsets_out_of_order():
         torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("T,E,N,K", [(90, 40, 200, 260), (250, 12, 2000, 300), (700, 300, 130, 140)])
+def test_nearly_all_rows_on_one_expert(T, E, N, K):
+    """Few rows on average, many on one expert."""
+    g, w, _, x, xd = make(T, E, N, K, "e4m3")
+    offsets = torch.full((E + 1,), T - 1, dtype=torch.int32)
+    offsets[0], offsets[-1], offsets[1] = 0, T, 1
+    p, mag = ref.grouped(xd, ref.dequantize(*w), offsets, False)
+    y, _ = block().linear(pair(x), pair(w), offsets.cuda())
+    ref.check(y.cpu(), p, ref.rounded(p, sum_error(mag, K), torch.bfloat16), "y")
+    check_up8(x, xd, w, ref.make_weight(g, E, N, K), offsets, T, K, N, torch.bfloat16, "silu", "amax")
+
+
 def test_graph_and_side_stream():
     b = block()
     g, w, offsets, x, _ = make(300, 2, 256, 1024, "e4m3")
