@@ -237,10 +237,9 @@ __device__ __forceinline__ bool find_tile(const int32_t* offsets, int32_t T, int
 // term is taken at the border, which keeps h^3 from overflowing against that zero.
 // Where the exponential overflows, below -88.7, the logistic is 0 (it is less than 3e-39 there).
 // (the hardware's exponential and reciprocal, 1 ulp each, a third of the instructions of the
-// exact division; a reciprocal that would be subnormal is taken of a scaled argument; an exponential
-// that would be is 0 next to the 1)
+// exact division; a reciprocal that would be subnormal is taken of a scaled argument)
 __device__ __forceinline__ float logistic(float x) {
-  const float t = 1.0f + __builtin_amdgcn_exp2f(x * -1.44269504088896340736f);
+  const float t = 1.0f + __expf(-x);
   const bool big = t > 0x1p100f;
   return __builtin_amdgcn_rcpf(big ? t * 0x1p-64f : t) * (big ? 0x1p-64f : 1.0f);
 }

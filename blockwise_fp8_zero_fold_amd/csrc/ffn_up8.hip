@@ -9,7 +9,7 @@ extern "C" int fp8z1_ffn_up8_workspace_bytes(const fp8z1_ffn* f, size_t* bytes) 
   static const int32_t some_offsets = 0;
   const int rc = check_cfg(f, &some_offsets, what);
   if (rc) return rc;
-  *bytes = !f->T ? 0 : few_rows8(f->T, f->E, f->F, 2) ? rows8_bytes(f->T, f->F) : tiles8_bytes(f->T, 2 * f->E * f->F, f->D);
+  *bytes = !f->T ? 0 : few_rows8(f->T, f->E, f->F, f->D, 2) ? rows8_bytes(f->T, f->F) : tiles8_bytes(f->T, 2 * f->E * f->F, f->D);
   return FP8Z1_OK;
 }
 

@@ -76,42 +76,54 @@ __device__ __forceinline__ void meet() {
 
 // ------------------------------------------------------------------------------------------------ tiles
 
-constexpr int kThreads8 = 512;
-constexpr int kRows8 = 256;   // tile rows
-constexpr int kCols8 = 256;   // weight rows of a tile (up: 128 of gate, 128 of up)
-constexpr int kA8 = kRows8 * kB, kB8 = kCols8 * kB;
-// a stage: codes of x, of the weights, x's scales (1 KB), the weights' two, 64 times each (as a wave copies them), and
-// for shifted rows the 4 bytes behind each row's 128
-constexpr int kScales8 = kA8 + kB8, kBehind8 = kScales8 + 2048, kStage8 = kBehind8 + 4 * (kRows8 + kCols8);
-constexpr int kResults8 = 8 * (kResultBytes / 4);  // 64 x 64 float32 of each wave
-constexpr int32_t kSlots8 = 256;                 // workgroups that the card runs at once: one on each compute unit
+// A tile: WM x WN waves of 64 rows x 128 weight rows (up: 64 of gate, 64 of up, WN = 2, a group of 128 results).
+// A stage: codes of x, of the weights, x's scales (1 KB), the weights' two, 64 times each (as a wave copies them), and
+// for shifted rows the 4 bytes behind each row's 128.
+template <int WM, int WN>
+struct Shape8 {
+  static constexpr int kThreads8 = 64 * WM * WN, kRows8 = 64 * WM, kCols8 = 128 * WN;
+  static constexpr int kA8 = kRows8 * kB, kScales8 = kA8 + kCols8 * kB, kBehind8 = kScales8 + 2048,
+                       kStage8 = kBehind8 + 4 * (kRows8 + kCols8);
+  static constexpr int kResults8 = WM * WN * (kResultBytes / 4);  // 64 x 64 float32 of each wave
+  // workgroups to run at once: one on each compute unit, two of the smaller products
+  static constexpr int32_t kSlots8 = WN == 2 ? 256 : 512;
+};
+constexpr int64_t kPart8 = 256 * 256 * 256;  // float32 of all partial sums: as many tiles as run at once
 
 // Work items: as in ffn.h, for one workgroup per compute unit.
+// Splitting pays while the blocks that it saves cost more than the sums' way through memory: the smaller tile's sums are a
+// quarter of the larger one's, and a block of gate and up (WN 2 of the smaller) costs twice that of one product.
+template <class S>
 __host__ __device__ __forceinline__ int32_t tile_splits8(int64_t tiles, int32_t blocks) {
-  const int32_t rest = static_cast<int32_t>(tiles % kSlots8);
+  const int32_t rest = static_cast<int32_t>(tiles % S::kSlots8);
   if (!rest || blocks < 4) return 1;
-  int32_t s = kSlots8 / rest, most = blocks / (tiles < kSlots8 ? 2 : 8);
-  if (tiles < kSlots8) {
-    const int32_t least = static_cast<int32_t>(sqrtf(20.0f * static_cast<float>(blocks) / static_cast<float>(rest)));
+  int32_t s = S::kSlots8 / rest, most = blocks / (tiles < S::kSlots8 ? 2 : 8);
+  if (tiles < S::kSlots8) {
+    const float gain = S::kThreads8 == 512 ? 20.0f : 40.0f;
+    const int32_t least = static_cast<int32_t>(sqrtf(gain * static_cast<float>(blocks) / static_cast<float>(rest)));
     most = least < most ? least : most;
   }
   if (s > most) s = most;
   return s > 1 ? s : 1;
 }
+template <class S>
 __device__ __forceinline__ Plan plan_tiles8(const FfnArgs& p, int32_t ncols, int32_t blocks, int32_t& rowtiles,
                                             Run& first) {
-  Plan plan = plan_tiles<kRows8>(p.offsets, p.T, p.E, ncols, blocks, 0, rowtiles, first);
-  const int32_t rest = plan.tiles % kSlots8, s = p.part ? tile_splits8(plan.tiles, blocks) : 1;
+  Plan plan = plan_tiles<S::kRows8>(p.offsets, p.T, p.E, ncols, blocks, 0, rowtiles, first);
+  const int32_t rest = plan.tiles % S::kSlots8, s = p.part ? tile_splits8<S>(plan.tiles, blocks) : 1;
+  plan.whole = plan.tiles;
+  plan.splits = 1;
   if (s > 1) {
     plan.whole = plan.tiles - rest;
     plan.splits = s;
   }
   return plan;
 }
+template <class S>
 __device__ __forceinline__ float* part8_at(float* part, int32_t at) {
-  return part + static_cast<int64_t>(at) * (kRows8 * kCols8);
+  return part + static_cast<int64_t>(at) * (S::kRows8 * S::kCols8);
 }
-size_t part8_bytes() { return sizeof(float) * kSlots8 * kRows8 * kCols8; }
+size_t part8_bytes() { return sizeof(float) * kPart8; }
 
 // a = act(gate) * up of 8 columns from column c of the results on, with 16 neighbouring lanes on the 128
 // columns of a group: h and u where they are wanted, codes and the group's scale.
@@ -152,7 +164,8 @@ __device__ __forceinline__ void finish_up8(const FfnArgs& p, int64_t m, int32_t 
   }
 }
 
-// A workgroup of 8 waves computes 256 rows x 256 weight rows, each wave 64 x 128 as 2 x 4 matrix tiles; two waves share a
+// A workgroup of 8 waves computes 256 rows x 256 weight rows (the smaller shapes: two waves, 128 x 128 or 64 x 256, where
+// that fills the card better), each wave 64 x 128 as 2 x 4 matrix tiles; two of the 8 waves share a
 // SIMD, one's additions and conversions running under the other's products (one wave a SIMD issues a vector instruction
 // every 5.7 cycles, two together one every 4.3; four waves, one a SIMD, were a tenth to a quarter slower).  A stage of LDS
 // holds a block of k, copied there directly; while it is read, the next one is on its way.  A workgroup has one tile: kept
@@ -162,8 +175,11 @@ __device__ __forceinline__ void finish_up8(const FfnArgs& p, int64_t m, int32_t 
 // SHIFTED: rows of x or codes are not 4-byte aligned, as the copies want them.  A row's stage then begins with the 4-byte
 // word that its block begins in and has one word more, and a lane shifts what it reads by its row's 0 to 3 bytes.
 // Only where the workspace has no room for packed rows.
-template <class H, int KIND, bool SHIFTED>
-__global__ __launch_bounds__(kThreads8) void tile8_kernel(FfnArgs p, int32_t ncols) {
+template <class H, int KIND, bool SHIFTED, int WM, int WN>
+__global__ __launch_bounds__((Shape8<WM, WN>::kThreads8)) void tile8_kernel(FfnArgs p, int32_t ncols) {
+  typedef Shape8<WM, WN> S;
+  constexpr int kThreads8 = S::kThreads8, kRows8 = S::kRows8, kCols8 = S::kCols8, kA8 = S::kA8, kScales8 = S::kScales8,
+                kBehind8 = S::kBehind8, kStage8 = S::kStage8, kResults8 = S::kResults8;
   constexpr bool kUp = KIND == kFfnUp;
   constexpr int kOut = kUp ? kCols8 / 2 : kCols8;  // output columns of a tile
   __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kStage8];
@@ -173,7 +189,7 @@ __global__ __launch_bounds__(kThreads8) void tile8_kernel(FfnArgs p, int32_t nco
   int32_t rowtiles, e, lo, hi, m0, col;
   Run first;
   const int32_t item = static_cast<int32_t>(blockIdx.x);
-  const Plan plan = plan_tiles8(p, ncols, kb, rowtiles, first);
+  const Plan plan = plan_tiles8<S>(p, ncols, kb, rowtiles, first);
   if (item >= plan.items()) return;
   const bool split = item >= plan.whole;
   const int32_t rest = plan.tiles - plan.whole;
@@ -183,7 +199,7 @@ __global__ __launch_bounds__(kThreads8) void tile8_kernel(FfnArgs p, int32_t nco
   if (!find_tile<kRows8>(p.offsets, p.T, p.E, ncols, rowtiles, first, id, e, lo, hi, m0, col)) return;
   const int32_t n0 = col * kOut, N = p.N, K = p.K;
   if (KIND == kLinear && p.bias) p.bias += static_cast<int64_t>(e) * N;
-  const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6), wm = w >> 1, wn = w & 1;
+  const int t = threadIdx.x, lane = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6), wm = w / WN, wn = w % WN;
   const int half = lane >> 5, l32 = lane & 31;
   const int32_t nb = (N + kB - 1) / kB;
 
@@ -191,7 +207,12 @@ __global__ __launch_bounds__(kThreads8) void tile8_kernel(FfnArgs p, int32_t nco
   // run's or the weight's end are whatever lies there (nothing behind the tensors' last word is read): their results are
   // not stored, and no other result depends on them.  The bytes that a row begins behind a word: the same for
   // rows 4 apart, so for all of a thread's.
-  constexpr int kCopies = SHIFTED ? 10 : 9;  // of a wave for a stage
+  // A pass of the workgroup's threads copies kPass rows; a wave makes kCopies copies for a stage.  The scales of 64 rows of
+  // x, or one of the weights' two, are a copy each: of one wave of eight, in the smaller shapes one of either by each wave.
+  constexpr int kPass = kThreads8 / 8, kXs = kRows8 / kPass, kWs = kCols8 / kPass;
+  constexpr bool kBoth = WM * WN < 8;
+  static_assert(!SHIFTED || !kBoth, "the words behind rows are of one wave of eight");
+  constexpr int kCopies = kXs + kWs + (kBoth ? 2 : 1) + (SHIFTED ? 1 : 0);
   const int r0 = t >> 3, c16 = ((t & 7) ^ swizzle_a(r0)) * 16;
   const int64_t abase = static_cast<int64_t>(m0) * K, bbase = (static_cast<int64_t>(e) * N + n0) * K;
   const uint8_t *const x0 = p.x0 + abase, *const w0 = p.w0 + bbase, *const w1 = (kUp ? p.w1 : p.w0) + bbase;
@@ -202,7 +223,7 @@ __global__ __launch_bounds__(kThreads8) void tile8_kernel(FfnArgs p, int32_t nco
   const uint32_t xw = word(x0), w0w = word(w0), w1w = word(w1);
   auto row_at = [&](int r, uint32_t in_word) { return static_cast<uint32_t>(r) * static_cast<uint32_t>(K) + in_word; };
   const uint32_t xoff = (row_at(r0, xw) & ~3u) + c16, w0off = (row_at(r0, w0w) & ~3u) + c16,
-                 w1off = (row_at(r0, w1w) & ~3u) + c16, rstep = 64u * static_cast<uint32_t>(K);
+                 w1off = (row_at(r0, w1w) & ~3u) + c16, rstep = kPass * static_cast<uint32_t>(K);
   const float* const xs = p.xs + static_cast<int64_t>(m0) * kb;
   // the weights' scales, one per block of k: of the two blocks of 128 columns, up: of gate and up
   const float* ws[2];
@@ -213,9 +234,11 @@ __global__ __launch_bounds__(kThreads8) void tile8_kernel(FfnArgs p, int32_t nco
   auto words = [](int64_t n, uint32_t in_word) { return SHIFTED ? (n + in_word + 3) & ~static_cast<int64_t>(3) : n; };
   const buffer_t xbuf = make_buffer(x0 - xw, words(static_cast<int64_t>(p.T - m0) * K, xw)),
                  w0buf = make_buffer(w0 - w0w, words(wleft, w0w)), w1buf = make_buffer(w1 - w1w, words(wleft, w1w)),
-                 sbuf = make_buffer(reinterpret_cast<const uint8_t*>(w < 4 ? xs : ws[w & 1]),
-                                    (w < 4 ? static_cast<int64_t>(p.T - m0) * kb : kb) * 4);
-  const uint32_t soff = w < 4 ? static_cast<uint32_t>(t) * static_cast<uint32_t>(kb) * 4 : 0;
+                 sbuf = make_buffer(reinterpret_cast<const uint8_t*>(kBoth || w < 4 ? xs : ws[w & 1]),
+                                    (kBoth || w < 4 ? static_cast<int64_t>(p.T - m0) * kb : kb) * 4),
+                 wsbuf = make_buffer(reinterpret_cast<const uint8_t*>(ws[w & 1]), static_cast<int64_t>(kb) * 4);
+  const int sw_ = kBoth ? w % WM : w;  // which scales
+  const uint32_t soff = kBoth || w < 4 ? static_cast<uint32_t>(sw_ * 64 + lane) * static_cast<uint32_t>(kb) * 4 : 0;
   // the word behind row t of the stage: rows of x, then of the weights
   const int brow = w < 4 ? t : kUp ? t & 127 : t & 255;
   const uint32_t bword = w < 4 ? xw : kUp && w >= 6 ? w1w : w0w, boff = (row_at(brow, bword) & ~3u) + kB;
@@ -225,13 +248,15 @@ __global__ __launch_bounds__(kThreads8) void tile8_kernel(FfnArgs p, int32_t nco
   // copy j of kCopies of block q to the stage at LDS offset `to`
   auto copy = [&](int j, int32_t q, uint32_t to) {
     const uint32_t at = lds0 + to + w * 1024;
-    if (j < 4)
+    if (j < kXs)
       copy_to_lds<16>(xbuf, xoff, q * kB + j * rstep, at + j * (kThreads8 * 16));
-    else if (j < 8)
-      copy_to_lds<16>(!kUp || j < 6 ? w0buf : w1buf, !kUp || j < 6 ? w0off : w1off, q * kB + (kUp ? j & 1 : j - 4) * rstep,
-                      at + kA8 + (j - 4) * (kThreads8 * 16));
-    else if (j == 8)  // (the weights' by two waves each: as many copies of every wave)
-      copy_to_lds<4>(sbuf, soff, q * 4, lds0 + to + kScales8 + w * 256);
+    else if (j < kXs + kWs)
+      copy_to_lds<16>(!kUp || j < kXs + kWs / 2 ? w0buf : w1buf, !kUp || j < kXs + kWs / 2 ? w0off : w1off,
+                      q * kB + (kUp ? (j - kXs) % (kWs / 2) : j - kXs) * rstep, at + kA8 + (j - kXs) * (kThreads8 * 16));
+    else if (j == kXs + kWs)  // (of eight waves four copy the weights', twice: as many copies of every wave)
+      copy_to_lds<4>(sbuf, soff, q * 4, lds0 + to + kScales8 + sw_ * 256);
+    else if (kBoth)
+      copy_to_lds<4>(wsbuf, 0, q * 4, lds0 + to + kScales8 + 1024 + (w & 1) * 256);
     else
       copy_to_lds<4>(bbuf, boff, q * kB, lds0 + to + kBehind8 + w * 256);
   };
@@ -241,8 +266,8 @@ __global__ __launch_bounds__(kThreads8) void tile8_kernel(FfnArgs p, int32_t nco
     auto keep = [](uint32_t* x, int n) {  // the first n of 4 bytes
       *x = n >= 4 ? *x : n > 0 ? *x & (0xffffffffu >> (32 - 8 * n)) : 0u;
     };
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t in_word = j < 4 ? xw : kUp && j >= 6 ? w1w : w0w;
+    for (int j = 0; j < kXs + kWs; ++j) {
+      const uint32_t in_word = j < kXs ? xw : kUp && j >= kXs + kWs / 2 ? w1w : w0w;
       const int n = left + (SHIFTED ? row_at(r0, in_word) & 3 : 0) - c16;
       uint4* const x = reinterpret_cast<uint4*>(at + (t + kThreads8 * j) * 16);
       uint4 v = *x;
@@ -392,7 +417,8 @@ __global__ __launch_bounds__(kThreads8) void tile8_kernel(FfnArgs p, int32_t nco
           if (v == 11 || v == 12) wide_x(set ^ 1, 1, v - 11);
           if (v == 13 || v == 14) wide_w(2, v - 13);
           if (c == 3) {
-            if (v < kCopies) copy(v, far, cur);
+#pragma unroll
+            for (int k = v; k < kCopies; k += 16) copy(k, far, cur);
             if (v == 3) {
               float to[2][2];
               scales(next, to);
@@ -555,8 +581,7 @@ __global__ __launch_bounds__(kThreads8) void tile8_kernel(FfnArgs p, int32_t nco
         if (u == 7) read_x(next, 1);
         if (u >= 6) {
 #pragma unroll
-          for (int k = 0; k < 5; ++k)
-            if ((u - 6) * 5 + k < kCopies) copy((u - 6) * 5 + k, far, cur);
+          for (int k = u - 6; k < kCopies; k += 2) copy(k, far, cur);
         }
         add(before, 8, u == 0 ? was : s[before & 1]);
         __builtin_amdgcn_sched_barrier(0);
@@ -580,7 +605,7 @@ __global__ __launch_bounds__(kThreads8) void tile8_kernel(FfnArgs p, int32_t nco
   uint8_t* const mine = lds + w * (kResultBytes / 4);
   const int32_t mw = m0 + wm * 64;
   if (split) {  // float32 sums [256][256], up: gate's 128 columns, then up's
-    float* const to = part8_at(p.part, item - plan.whole) + static_cast<int64_t>(wm * 64) * kCols8;
+    float* const to = part8_at<S>(p.part, item - plan.whole) + static_cast<int64_t>(wm * 64) * kCols8;
 #pragma unroll 1
     for (int half_ = 0; half_ < 2; ++half_) {
 #pragma unroll
@@ -719,14 +744,16 @@ __global__ __launch_bounds__(kThreads8) void tile8_kernel(FfnArgs p, int32_t nco
 }
 
 // The split tiles: their parts' sums added in order, and the results.  16 lanes take 128 columns of a row.
-template <class H, int KIND>
+template <class H, int KIND, int WM, int WN>
 __global__ __launch_bounds__(kThreads) void join8_kernel(FfnArgs p, int32_t ncols) {
+  typedef Shape8<WM, WN> S;
+  constexpr int kRows8 = S::kRows8, kCols8 = S::kCols8;
   constexpr bool kUp = KIND == kFfnUp;
   constexpr int kOut = kUp ? kCols8 / 2 : kCols8, kLanes = kOut / 8, kTurns = kRows8 * kLanes / kThreads;
   const int32_t kb = (p.K + kB - 1) / kB;
   int32_t rowtiles, e, lo, hi, m0, col;
   Run first;
-  const Plan plan = plan_tiles8(p, ncols, kb, rowtiles, first);
+  const Plan plan = plan_tiles8<S>(p, ncols, kb, rowtiles, first);
   const int32_t rest = plan.tiles - plan.whole, tile = static_cast<int32_t>(blockIdx.x) / kTurns;
   if (tile >= rest) return;
   if (!find_tile<kRows8>(p.offsets, p.T, p.E, ncols, rowtiles, first, plan.whole + tile, e, lo, hi, m0, col)) return;
@@ -735,7 +762,7 @@ __global__ __launch_bounds__(kThreads) void join8_kernel(FfnArgs p, int32_t ncol
   const int32_t n = col * kOut + 8 * c, m = m0 + r, count = m < hi ? min(p.N - n, 8) : 0;
   float x[8] = {}, v[8] = {};
   if (m < hi) {  // (the parts of rows past the run were not written)
-    const f32x4* from = reinterpret_cast<const f32x4*>(part8_at(p.part, tile) + static_cast<int64_t>(r) * kCols8 + 8 * c);
+    const f32x4* from = reinterpret_cast<const f32x4*>(part8_at<S>(p.part, tile) + static_cast<int64_t>(r) * kCols8 + 8 * c);
     const int64_t step = static_cast<int64_t>(rest) * (kRows8 * kCols8) / 4;
 #pragma unroll 4
     for (int32_t s = 0; s < plan.splits; ++s)
@@ -919,9 +946,15 @@ void launch_rows8_as(const FfnArgs& p, bool aligned, hipStream_t s) {
 
 // Strips of 16 weight rows that do not fill the card
 bool deep8(int64_t E, int64_t N, int matrices) { return (N + 15) / 16 * matrices * E < 1024; }
-// Few rows per expert: 32 on average, and 64 where the strips fill the card.  (4096 x 4096, rows and tiles: 32 tokens 11.5
-// and 21 us, 40 tokens 48 and 21; 300 tokens on 8 experts, gate and up 2048 x 1024: 26 and 37.)
-bool few_rows8(int64_t T, int64_t E, int64_t N, int matrices) { return T <= (deep8(E, N, matrices) ? 32 : 64) * E; }
+// Few rows per expert: 16 on average; while the products are few, 32, and 64 where the strips fill the card.  (4096 x 4096,
+// rows and tiles: 32 tokens 11.8 and 16.6 us; 8 experts of it, 128 tokens 34 and 37, 256 tokens 41 and 38, 400 tokens 58 and
+// 39; 8 experts of 2048 x 1024, 300 tokens 10.8 and 17.1, 500 tokens 13.0 and 18.3; gate and up of 2 x 1024 x 1024 17.0 and
+// 19.2, 20.5 and 21.4.)
+bool few_rows8(int64_t T, int64_t E, int64_t N, int64_t K, int matrices) {
+  if (T <= 16 * E) return true;
+  const double products = static_cast<double>(T) * static_cast<double>(N * matrices) * static_cast<double>(K);
+  return T <= (deep8(E, N, matrices) ? 32 : 64) * E && products <= 0x1p31;
+}
 
 // Strips that do not fill the card: 16 waves share k.  Otherwise 4, on two strips each, which share x's rows (128
 // tokens on 8 experts of 4096 x 4096: 34 us, 45 with one).  Up to 8, up to 32 and more rows per expert on average: one,
@@ -987,24 +1020,56 @@ size_t tiles8_bytes(int64_t T, int64_t rows, int64_t K) {
   return (K > 2 * kB ? part8_bytes() : 0) + (K % 4 ? packed_bytes(T, rows, K) : 0);
 }
 
-template <class H, int KIND>
-void launch_tiles8(const FfnArgs& p, bool shifted, int64_t tiles, int32_t ncols, hipStream_t s) {
-  constexpr int kTurns = KIND == kFfnUp ? 16 : 32;
-  const dim3 g(static_cast<unsigned>(tiles + (p.part ? kSlots8 : 0))), b(kThreads8), bj(kThreads);
-  if (shifted)
-    hipLaunchKernelGGL((tile8_kernel<H, KIND, true>), g, b, 0, s, p, ncols);
-  else
-    hipLaunchKernelGGL((tile8_kernel<H, KIND, false>), g, b, 0, s, p, ncols);
+template <class H, int KIND, int WM, int WN>
+void launch_tiles8_as(const FfnArgs& p, bool shifted, int64_t tiles, int32_t ncols, hipStream_t s) {
+  typedef Shape8<WM, WN> S;
+  constexpr int kTurns = S::kRows8 * ((KIND == kFfnUp ? S::kCols8 / 2 : S::kCols8) / 8) / kThreads;
+  const dim3 g(static_cast<unsigned>(tiles + (p.part ? S::kSlots8 : 0))), b(S::kThreads8), bj(kThreads);
+  if constexpr (WM * WN == 8) {
+    if (shifted) hipLaunchKernelGGL((tile8_kernel<H, KIND, true, WM, WN>), g, b, 0, s, p, ncols);
+  }
+  if (!shifted) hipLaunchKernelGGL((tile8_kernel<H, KIND, false, WM, WN>), g, b, 0, s, p, ncols);
   if (!p.part) return;
-  const int64_t rest = tiles < kSlots8 ? tiles : kSlots8 - 1;
-  hipLaunchKernelGGL((join8_kernel<H, KIND>), dim3(static_cast<unsigned>(rest * kTurns)), bj, 0, s, p, ncols);
+  const int64_t rest = tiles < S::kSlots8 ? tiles : S::kSlots8 - 1;
+  hipLaunchKernelGGL((join8_kernel<H, KIND, WM, WN>), dim3(static_cast<unsigned>(rest * kTurns)), bj, 0, s, p, ncols);
+}
+
+template <class S, int KIND>
+int64_t tiles8(const FfnArgs& p, int32_t& ncols) {
+  constexpr int32_t per = KIND == kFfnUp ? S::kCols8 / 2 : S::kCols8;
+  ncols = (p.N + per - 1) / per;
+  return (p.T / S::kRows8 + (p.T < p.E ? p.T : p.E)) * static_cast<int64_t>(ncols);  // (every run may end in a partial tile)
+}
+template <class H, int KIND, class S, int WM, int WN>
+void launch_tiles8(FfnArgs p, bool shifted, void* workspace, size_t workspace_bytes, hipStream_t s) {
+  int32_t ncols;
+  const int64_t tiles = tiles8<S, KIND>(p, ncols);
+  const int32_t kb = (p.K + kB - 1) / kB;
+  const int64_t known = p.offsets ? tiles : static_cast<int64_t>((p.T + S::kRows8 - 1) / S::kRows8) * ncols;
+  if ((p.offsets ? kb >= 4 : tile_splits8<S>(known, kb) > 1) && workspace_bytes >= part8_bytes())
+    p.part = static_cast<float*>(workspace);
+  launch_tiles8_as<H, KIND, WM, WN>(p, shifted, tiles, ncols, s);
+}
+
+// Tiles of 128 x 128, or 64 x (128 + 128) for gate and up, of two waves, which wait for each other less and split finer:
+// while there are no more than two for each compute unit, of gate and up one (two widen codes no faster than one:
+// 1024 x 2 x 1024 of width 4096 in 384 parts took 56 us, in 256 43, on large tiles 47).  Products 1024 x 2048 of width 1024 18.7 us, on
+// large tiles 28.1; 1024 x 4096 of 2048 28 and 36; 4096 x 4096 of 2048 61 and 46; 600 tokens on 8 experts, 2048 of 2048,
+// 20.5 and 26.7.  Gate and up 1024 x 2 x 1024 of width 1024 24 and 34, 2048 x 2 x 2048 of 512 33 and 26, 600 tokens on 8
+// experts, 2 x 1024 of 2048, 30 and 40.  Of several experts' runs, each ends in half a tile of rows on average.
+template <class S, int KIND>
+bool small_tiles8(const FfnArgs& p) {
+  int32_t ncols;
+  tiles8<S, KIND>(p, ncols);
+  const int64_t halves = 2 * static_cast<int64_t>(p.T) / S::kRows8 + (p.E > 1 ? (p.E < p.T ? p.E : p.T) : 0);
+  return halves * ncols <= 2 * S::kSlots8;
 }
 
 template <int KIND>
 int launch8(FfnArgs p, int32_t dtype, void* workspace, size_t workspace_bytes, hipStream_t s, const char* what) {
   if (p.T == 0) return FP8Z1_OK;
   if (misaligned(workspace, 16)) return refuse(FP8Z1_EINVAL, what, "misaligned workspace");
-  if (few_rows8(p.T, p.E, p.N, KIND == kFfnUp ? 2 : 1) && (KIND != kFfnUp || workspace_bytes >= rows8_bytes(p.T, p.N))) {
+  if (few_rows8(p.T, p.E, p.N, p.K, KIND == kFfnUp ? 2 : 1) && (KIND != kFfnUp || workspace_bytes >= rows8_bytes(p.T, p.N))) {
     const bool aligned = !misaligned(p.x0, 16) && !misaligned(p.w0, 16) && !misaligned(p.w1, 16) && p.K % 16 == 0;
     p.part = static_cast<float*>(workspace);
     if (dtype == FP8Z1_BF16)
@@ -1014,13 +1079,11 @@ int launch8(FfnArgs p, int32_t dtype, void* workspace, size_t workspace_bytes, h
     return launched(what);
   }
   bool shifted = misaligned(p.x0, 4) || misaligned(p.w0, 4) || misaligned(p.w1, 4) || p.K % 4 != 0;
-  const int32_t per = KIND == kFfnUp ? kCols8 / 2 : kCols8, ncols = (p.N + per - 1) / per;
-  const int64_t tiles = (p.T / kRows8 + (p.T < p.E ? p.T : p.E)) * static_cast<int64_t>(ncols);  // (every run may end in a partial tile)
-  if (tiles > 0x7fffffff / kThreads8 - kSlots8) return refuse(FP8Z1_ESHAPE, what, "too many tiles");
-  const int32_t kb = (p.K + kB - 1) / kB;
-  const int64_t known = p.offsets ? tiles : static_cast<int64_t>((p.T + kRows8 - 1) / kRows8) * ncols;
-  if ((p.offsets ? kb >= 4 : tile_splits8(known, kb) > 1) && workspace_bytes >= part8_bytes())
-    p.part = static_cast<float*>(workspace);
+  typedef Shape8<4, 2> Large;
+  constexpr int WM = KIND == kFfnUp ? 1 : 2, WN = KIND == kFfnUp ? 2 : 1;
+  typedef Shape8<WM, WN> Small;
+  int32_t ncols;
+  if (tiles8<Small, KIND>(p, ncols) > 0x7fffffff / 512 - 512) return refuse(FP8Z1_ESHAPE, what, "too many tiles");
   // Unaligned rows are packed where the workspace has room, behind the partial sums: y 8000 x 4001 of width 4001 takes 184
   // us so, 292 on shifted tiles and 173 at width 4000; 2568 x 1152 of width 822 on 5 experts 45, 51 and 38.
   const int64_t rows = static_cast<int64_t>(p.E) * p.N, sums = p.K > 2 * kB ? static_cast<int64_t>(part8_bytes()) : 0;
@@ -1044,10 +1107,13 @@ int launch8(FfnArgs p, int32_t dtype, void* workspace, size_t workspace_bytes, h
     p.K = a.wide;
     shifted = false;
   }
+  const bool small = !shifted && small_tiles8<Small, KIND>(p);
   if (dtype == FP8Z1_BF16)
-    launch_tiles8<Bf16, KIND>(p, shifted, tiles, ncols, s);
+    small ? launch_tiles8<Bf16, KIND, Small, WM, WN>(p, shifted, workspace, workspace_bytes, s)
+          : launch_tiles8<Bf16, KIND, Large, 4, 2>(p, shifted, workspace, workspace_bytes, s);
   else
-    launch_tiles8<F16, KIND>(p, shifted, tiles, ncols, s);
+    small ? launch_tiles8<F16, KIND, Small, WM, WN>(p, shifted, workspace, workspace_bytes, s)
+          : launch_tiles8<F16, KIND, Large, 4, 2>(p, shifted, workspace, workspace_bytes, s);
   return launched(what);
 }
 

@@ -5,7 +5,7 @@ namespace fp8z1 {
 
 // (few rows are not tiled)
 size_t linear8_workspace(int64_t T, int64_t E, int64_t N, int64_t K) {
-  return few_rows8(T, E, N, 1) ? 0 : tiles8_bytes(T, E * N, K);
+  return few_rows8(T, E, N, K, 1) ? 0 : tiles8_bytes(T, E * N, K);
 }
 
 int linear8(const FfnArgs& p, int32_t dtype, void* workspace, size_t workspace_bytes, hipStream_t s, const char* what) {
