@@ -1053,10 +1053,11 @@ void launch_tiles8(FfnArgs p, bool shifted, void* workspace, size_t workspace_by
 
 // Tiles of 128 x 128, or 64 x (128 + 128) for gate and up, of two waves, which wait for each other less and split finer:
 // while there are no more than two for each compute unit, of gate and up one (two widen codes no faster than one:
-// 1024 x 2 x 1024 of width 4096 in 384 parts took 56 us, in 256 43, on large tiles 47).  Products 1024 x 2048 of width 1024 18.7 us, on
-// large tiles 28.1; 1024 x 4096 of 2048 28 and 36; 4096 x 4096 of 2048 61 and 46; 600 tokens on 8 experts, 2048 of 2048,
-// 20.5 and 26.7.  Gate and up 1024 x 2 x 1024 of width 1024 24 and 34, 2048 x 2 x 2048 of 512 33 and 26, 600 tokens on 8
-// experts, 2 x 1024 of 2048, 30 and 40.  Of several experts' runs, each ends in half a tile of rows on average.
+// 1024 x 2 x 1024 of width 4096 in 384 parts took 56 us, in 256 43, on large tiles 47).  Products 1024 x 2048 of width
+// 1024 18.7 us, on large tiles 28.1; 1024 x 4096 of 2048 28 and 36; 4096 x 4096 of 2048 61 and 46; 600 tokens on 8
+// experts, 2048 of 2048, 20.5 and 26.7.  Gate and up 1024 x 2 x 1024 of width 1024 24 and 34, 2048 x 2 x 2048 of 512 33
+// and 26, 600 tokens on 8 experts, 2 x 1024 of 2048, 30 and 40.  Of several experts' runs, each ends in half a tile of
+// rows on average.
 template <class S, int KIND>
 bool small_tiles8(const FfnArgs& p) {
   int32_t ncols;
@@ -1083,7 +1084,9 @@ int launch8(FfnArgs p, int32_t dtype, void* workspace, size_t workspace_bytes, h
   constexpr int WM = KIND == kFfnUp ? 1 : 2, WN = KIND == kFfnUp ? 2 : 1;
   typedef Shape8<WM, WN> Small;
   int32_t ncols;
-  if (tiles8<Small, KIND>(p, ncols) > 0x7fffffff / 512 - 512) return refuse(FP8Z1_ESHAPE, what, "too many tiles");
+  // (the number of a launch's threads has 32 bits; smaller tiles are taken of few only)
+  if (tiles8<Large, KIND>(p, ncols) > 0x7fffffff / Large::kThreads8 - Large::kSlots8)
+    return refuse(FP8Z1_ESHAPE, what, "too many tiles");
   // Unaligned rows are packed where the workspace has room, behind the partial sums: y 8000 x 4001 of width 4001 takes 184
   // us so, 292 on shifted tiles and 173 at width 4000; 2568 x 1152 of width 822 on 5 experts 45, 51 and 38.
   const int64_t rows = static_cast<int64_t>(p.E) * p.N, sums = p.K > 2 * kB ? static_cast<int64_t>(part8_bytes()) : 0;
