@@ -514,6 +514,7 @@ __global__ __launch_bounds__((Shape8<WM, WN>::kThreads8)) void tile8_kernel(FfnA
       pass(Int<1>{});
       pass(Int<2>{});
       pass(Int<3>{});
+      __syncthreads();  // the results take the stage's place, which slower waves may still read
     }
   } else {
     // Tile column j of a block: the weights' 4 chunks are read a column ahead, x's stay.  A tile's two products go to one
