@@ -85,6 +85,9 @@ struct Shape8 {
   static constexpr int kA8 = kRows8 * kB, kScales8 = kA8 + kCols8 * kB, kBehind8 = kScales8 + 2048,
                        kStage8 = kBehind8 + 4 * (kRows8 + kCols8);
   static constexpr int kResults8 = WM * WN * (kResultBytes / 4);  // 64 x 64 float32 of each wave
+  // behind them (up): each row's largest magnitude over 64 columns, of either half, and a word that says whether the tile
+  // is summed again.  No result lies over the word: waves may still read it while others write results and magnitudes.
+  static constexpr int kTops8 = kResults8, kFlag8 = kTops8 + 2 * kRows8 * 4;
   // workgroups to run at once: one on each compute unit, two of the smaller products
   static constexpr int32_t kSlots8 = WN == 2 ? 256 : 512;
 };
@@ -179,11 +182,11 @@ template <class H, int KIND, bool SHIFTED, int WM, int WN>
 __global__ __launch_bounds__((Shape8<WM, WN>::kThreads8)) void tile8_kernel(FfnArgs p, int32_t ncols) {
   typedef Shape8<WM, WN> S;
   constexpr int kThreads8 = S::kThreads8, kRows8 = S::kRows8, kCols8 = S::kCols8, kA8 = S::kA8, kScales8 = S::kScales8,
-                kBehind8 = S::kBehind8, kStage8 = S::kStage8, kResults8 = S::kResults8;
+                kBehind8 = S::kBehind8, kStage8 = S::kStage8;
   constexpr bool kUp = KIND == kFfnUp;
   constexpr int kOut = kUp ? kCols8 / 2 : kCols8;  // output columns of a tile
   __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kStage8];
-  static_assert(2 * kStage8 >= kResults8 + 2 * kRows8 * 4, "results use the stages' LDS");
+  static_assert(2 * kStage8 >= S::kFlag8 + 4, "results use the stages' LDS");
 
   const int32_t kb = (p.K + kB - 1) / kB;
   int32_t rowtiles, e, lo, hi, m0, col;
@@ -463,7 +466,7 @@ __global__ __launch_bounds__((Shape8<WM, WN>::kThreads8)) void tile8_kernel(FfnA
     for (int32_t q = q0; q < q1; ++q) turn(q);
     // (the last turn has fetched its own block as the next: its scales are the units still)
     wait_copies();
-    int32_t* const far_apart = reinterpret_cast<int32_t*>(lds + kResults8);
+    int32_t* const far_apart = reinterpret_cast<int32_t*>(lds + S::kFlag8);
     __syncthreads();
     if (t == 0) *far_apart = 0;
     __syncthreads();
@@ -685,7 +688,7 @@ __global__ __launch_bounds__((Shape8<WM, WN>::kThreads8)) void tile8_kernel(FfnA
       }
     }
     // a in place of gate; the largest magnitude of a row over this wave's 64 columns, then over both waves'
-    float* const tops = reinterpret_cast<float*>(lds + kResults8);  // [2][256]
+    float* const tops = reinterpret_cast<float*>(lds + S::kTops8);  // [2][kRows8]
     float top[2] = {0.0f, 0.0f};
     const bool past = n0 + kCols8 / 2 > N;  // columns past the last count for nothing
 #pragma unroll

@@ -73,3 +73,19 @@ def test_nan_and_infinite_rows_among_sound_ones(T, D, F):
     for got, w in ((h, wg), (u, wu)):
         exact, mag = ref.grouped(xd, ref.dequantize(*w), None, False)
         ref.check(got.cpu()[rest], exact, ref.rounded(exact, ref.sum_error(mag, D), torch.bfloat16), "projection")
+
+
+@pytest.mark.parametrize("T,D,F", [(300, 128, 700), (300, 256, 700), (9000, 100, 1300), (4100, 128, 2100)])
+@pytest.mark.parametrize("far", [False, True])
+def test_whole_tiles_give_the_same_without_kept_projections(T, D, F, far):
+    """Tiles of few blocks, whose waves go straight from the sums to the rows' largest magnitudes where h and u are not kept:
+    whether a tile is summed again is decided alike by all of them, call after call."""
+    g = torch.Generator().manual_seed(T + F)
+    x = r8.make_rows8(g, T, D)
+    if far:
+        x[1][torch.arange(0, T, 130), 0] = 2.0 ** -90
+    x, wg, wu = pair(x), pair(ref.make_weight(g, 1, F, D)), pair(ref.make_weight(g, 1, F, D))
+    (codes, scales), _ = block().ffn_up8(x, wg, wu, save=True)
+    for _ in range(10):
+        (c, s), none = block().ffn_up8(x, wg, wu)
+        assert none is None and torch.equal(c, codes) and torch.equal(s, scales)
