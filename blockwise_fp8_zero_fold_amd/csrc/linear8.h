@@ -479,12 +479,14 @@ __global__ __launch_bounds__((Shape8<WM, WN>::kThreads8)) void tile8_kernel(FfnA
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[u & 1][u >> 1][r] *= s[u & 1][u >> 2];
     } else {
-      // a pass for each tile column: the blocks' sums apart, times their scales
+      __syncthreads();
+      // A pass for each tile column: the blocks' sums apart, times their scales.  A barrier ends every turn, so that
+      // no wave copies the next block, or lays its results, over a stage that a slower one still reads.  (It stands
+      // in the turn: behind the last pass it made the allocator spill in the loop above, 959 us where this takes 461.)
       auto pass = [&](auto j_) {
         constexpr int j = decltype(j_)::value;
         acc[0][j] = acc[1][j] = zero;
         for (int32_t q = q0; q < q1; ++q) {
-          __syncthreads();
 #pragma unroll
           for (int k = 0; k < kCopies; ++k) copy(k, q, 0);
           meet<0>();
@@ -511,13 +513,13 @@ __global__ __launch_bounds__((Shape8<WM, WN>::kThreads8)) void tile8_kernel(FfnA
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[i][j][r] = fmaf(sq, part[i][r], acc[i][j][r]);
           }
+          __syncthreads();
         }
       };
       pass(Int<0>{});
       pass(Int<1>{});
       pass(Int<2>{});
       pass(Int<3>{});
-      __syncthreads();  // the results take the stage's place, which slower waves may still read
     }
   } else {
     // Tile column j of a block: the weights' 4 chunks are read a column ahead, x's stay.  A tile's two products go to one
