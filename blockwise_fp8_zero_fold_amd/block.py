@@ -7,8 +7,8 @@ Rows (tokens) are sorted by expert: ``offsets`` [E+1] int32 on the device holds 
 expert's first row, from 0 to T; None means one expert.  Outputs' rows that no expert covers hold whatever
 their memory held.  Everything runs on torch's current stream.
 
-Products are summed in float32; the results, the inner ones too (``a`` between up and down,
-``dh`` and ``du`` before ``dx``), are rounded to the activations' 16 bits.  The sums hold
+Products are summed in float32 (but ``linear`` of 8-bit rows, see there); the results, the inner ones too (``a`` between
+up and down, ``dh`` and ``du`` before ``dx``), are rounded to the activations' 16 bits.  The sums hold
 activation * code before the block's scale: magnitudes of activations and gradients stay below 2^56.
 
 A training step over one block (see ``examples/train_ffn_layer.py``):
@@ -253,7 +253,9 @@ def linear(x: Union[torch.Tensor, Rows8], w: Weight, offsets: Optional[torch.Ten
            save: bool = False, dtype: Optional[torch.dtype] = None):
     """(y, p): y [T,N] = res + act(p), p = x W^T + bias, codes [E,N,K].  x is [T,K] in 16 bits, or a pair (codes,
     scales) in 8; bias float32 [E,N] (one expert: or [N]).  p is None unless ``save``.
-    ``dtype`` (of y, p and res): x's own, for 8-bit rows that of res or bfloat16 unless it is given."""
+    ``dtype`` (of y, p and res): x's own, for 8-bit rows that of res or bfloat16 unless it is given.
+    Products of 8-bit rows are summed by 8 consecutive ones with 13 bits below the largest, then in float32
+    (see fp8z1.h); those of 16-bit rows in float32 throughout."""
     what = "linear"
     eight = isinstance(x, tuple)
     rows = x[0] if eight else x

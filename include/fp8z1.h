@@ -446,8 +446,13 @@ int fp8z1_norm_join8(const fp8z1_norm* f, const void* y, const void* res, const 
 
 /* ---------------------------------------------------------------------------
  * Products with one weight, and with rows in 8 bits.  Rows in 8 bits are codes [T,K] (at any alignment) and scales
- * [T, ceil(K/128)] float32, as fp8z1_norm_join8 writes them; the products of 8-bit rows and codes are
- * summed in float32 on the matrix cores, and both scales multiply the sum of each 128. */
+ * [T, ceil(K/128)] float32, as fp8z1_norm_join8 writes them; both scales multiply the codes' sum of each 128.
+ *
+ * How the codes' products are summed: by fp8z1_ffn_up8 in float32.  fp8z1_linear of 8-bit rows uses the matrix cores' 8-bit
+ * instruction, which holds fewer bits: it adds the products of 8 consecutive k as fixed-point numbers, with 13 bits
+ * below the power of two of the largest, and cuts off the rest; these sums of 8 are added in float32.  So x W^T is off
+ * by less than 7 * 2^-13 of the sum of the products' magnitudes, besides the float32 sum's roundings.  (Seen, of the norm of
+ * x W^T: 1.3e-5 on rows and weights quantized from normal values, 5e-5 on random codes.)  Rows in 16 bits are summed in float32. */
 
 typedef struct {
   int64_t T; /* rows */
