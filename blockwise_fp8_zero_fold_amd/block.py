@@ -222,8 +222,10 @@ def _linear_workspace(T: int, E: int, N: int, K: int, eight: bool) -> int:
 
 
 @functools.lru_cache(maxsize=256)
-def _linear_bwd_workspace(T: int, E: int, N: int, K: int) -> int:
-    return L.fp8z1_linear_bwd_workspace_bytes(L.Product(T, E, N, K, L.BF16, L.BF16, L.ACT_NONE, 0))
+def _linear_bwd_workspace(T: int, E: int, N: int, K: int, bias: bool) -> int:
+    if bias:
+        return L.fp8z1_linear_bwd_workspace_bytes(L.Product(T, E, N, K, L.BF16, L.BF16, L.ACT_NONE, 0))
+    return L.fp8z1_linear_workspace_bytes(L.Product(T, E, K, N, L.BF16, L.BF16, L.ACT_NONE, 0))  # (dx = dp W alone)
 
 
 @functools.lru_cache(maxsize=256)
@@ -303,7 +305,7 @@ def linear_backward(dy: torch.Tensor, w: Weight, p: Optional[torch.Tensor] = Non
     dp, dx = dy if p is None else torch.empty_like(dy), dy.new_empty((T, K))
     dbias = dy.new_empty((E, N), dtype=torch.float32) if bias else None
     f = L.Product(T, E, N, K, _CODE[dtype], _CODE[dtype], kind, 0)
-    n = _linear_bwd_workspace(T, E, N, K)
+    n = _linear_bwd_workspace(T, E, N, K, bias)
     ws = _scratch(dy, n)
     L._check(L.lib.fp8z1_linear_bwd(f, py, pp, *pw, off, None if p is None else dp.data_ptr(), L._ptr(dbias), dx.data_ptr(),
                                     L._ptr(ws), n, L._current_stream(dev)), what)

@@ -479,7 +479,8 @@ int fp8z1_linear(const fp8z1_product* f, const void* x, const float* x_scales, c
  * rounded (0 for one without rows), dx [T,K] = dp W of the rounded dp.  (res has dy.)  Each may be NULL if it
  * is not wanted; dx needs dp where there is an activation.  x's rounding to 8 bits passes dx through;
  * x_dtype is not looked at.  dbias needs fp8z1_linear_bwd_workspace_bytes() bytes of device workspace
- * (16-byte aligned), with which tiles are split too. */
+ * (16-byte aligned), with which tiles are split too.  Without dbias the tiles' share is enough: what
+ * fp8z1_linear_workspace_bytes() asks for with 16-bit rows and N and K exchanged. */
 int fp8z1_linear_bwd_workspace_bytes(const fp8z1_product* f, size_t* bytes);
 int fp8z1_linear_bwd(const fp8z1_product* f, const void* dy, const void* p, const uint8_t* codes, const float* scales,
                      const int32_t* offsets, void* dp, float* dbias, void* dx, void* d_workspace, size_t workspace_bytes,
