@@ -2,17 +2,21 @@
 // bias's gradient) in one pass over dy and p, and dx = dp W on the tile kernel of the feed-forward block.
 //
 // The pass reads dy and p and writes dp; its arithmetic (the activation's slope, about 30 instructions an element) takes
-// as long as half of the transfers, and runs under other waves'.  A workgroup takes 8 rows of one expert by up to 2048
-// columns, 8 of them per thread, and writes their float32 column sums to the workspace; a second kernel adds an
-// expert's groups in order.  4096 x 4096, GELU: 24 us (4.2 TB/s) and 5.7 for the sums; groups of 16 rows 27 and 4.9, and
-// with the next rows' loads ahead of the arithmetic 29.
+// as long as half of the transfers, and runs under other waves'.  A workgroup takes 8 rows (of many elements more, see sum_rows)
+// of one expert by up to 2048 columns, 8 of them per thread, and writes their float32 column sums to the workspace; a second
+// kernel adds an expert's groups in order.  4096 x 4096, GELU: 24 us (4.2 TB/s) and 5.7 for the sums; groups of 16 rows 27
+// and 4.9, and with the next rows' loads ahead of the arithmetic 29.
 #include "ffn_tile.h"
 #include "rows.h"
 
 namespace fp8z1 {
 namespace {
 
-constexpr int kSumRows = 8;
+// Rows of a group: 8 while there are fewer than 10^8 elements, 64 up to 2^31, then 512, so that the groups' sums take
+// 50 MB, 134 MB or 1/256 of dy (and a row for each expert) at most.  8 and 64 rows, GELU: 8192 x 7168 90 and 105 us, 32,768 x 2048 103
+// and 115, 16,384 x 7168 177 and 172, 65,536 x 2048 212 and 182, 262,144 x 1024 510 and 377, 65,536 x 7168 658 and 608;
+// 64 and 512: 524,288 x 2048 1323 and 1312, 262,144 x 7168 2321 and 2422, 65,536 x 2048 182 and 527.
+int32_t sum_rows(int64_t T, int64_t N) { return T * N < 100000000 ? 8 : T * N < (1ll << 31) ? 64 : 512; }
 
 struct DpArgs {
   const uint16_t *dy, *p;
@@ -22,12 +26,12 @@ struct DpArgs {
   int32_t T, E, N, act;
 };
 
-template <class H>
+template <class H, int ROWS>
 __global__ __launch_bounds__(kThreads) void linear_dp_kernel(DpArgs a) {
   int32_t e, lo, hi, t0;
   const int32_t group = static_cast<int32_t>(blockIdx.z * gridDim.y + blockIdx.y);
-  if (!find_group<kSumRows>(a.offsets, a.T, a.E, group, e, lo, hi, t0)) return;
-  const int32_t n = static_cast<int32_t>(blockIdx.x * blockDim.x + threadIdx.x) * 8, rows = min(hi - t0, kSumRows);
+  if (!find_group<ROWS>(a.offsets, a.T, a.E, group, e, lo, hi, t0)) return;
+  const int32_t n = static_cast<int32_t>(blockIdx.x * blockDim.x + threadIdx.x) * 8, rows = min(hi - t0, ROWS);
   if (n >= a.N) return;
   float sum[8];
 #pragma unroll
@@ -66,7 +70,7 @@ __global__ __launch_bounds__(kThreads) void linear_dp_kernel(DpArgs a) {
 // of its 16 waves adds every 16th group; the waves' sums are added in order.
 constexpr int kBiasWaves = 16, kBiasCols = 64;
 __global__ __launch_bounds__(64 * kBiasWaves) void linear_dbias_kernel(const float* sums, const int32_t* offsets, int32_t T,
-                                                                       int32_t E, int32_t N, float* dbias) {
+                                                                       int32_t E, int32_t N, int32_t rows, float* dbias) {
   __shared__ float parts[kBiasWaves][kBiasCols];
   const int32_t strips = (N + kBiasCols - 1) / kBiasCols;
   const int32_t e = static_cast<int32_t>(blockIdx.x) / strips;
@@ -77,8 +81,8 @@ __global__ __launch_bounds__(64 * kBiasWaves) void linear_dbias_kernel(const flo
   float sum = 0.0f;
   if (lo < hi) {
     if (w == 0) sum = sums[static_cast<int64_t>(e) * N + n];
-    const float* const from = sums + (static_cast<int64_t>(E) + lo / kSumRows) * N + n;
-    const int32_t more = (hi - lo - 1) / kSumRows;  // groups behind the first
+    const float* const from = sums + (static_cast<int64_t>(E) + lo / rows) * N + n;
+    const int32_t more = (hi - lo - 1) / rows;  // groups behind the first
 #pragma unroll 8
     for (int32_t k = w; k < more; k += kBiasWaves) sum += from[static_cast<int64_t>(k) * N];
   }
@@ -90,7 +94,17 @@ __global__ __launch_bounds__(64 * kBiasWaves) void linear_dbias_kernel(const flo
   dbias[static_cast<int64_t>(e) * N + n] = sum;
 }
 
-int64_t sum_groups(int64_t T, int64_t E) { return E + T / kSumRows; }
+int64_t sum_groups(int64_t T, int64_t E, int64_t N) { return E + T / sum_rows(T, N); }
+
+template <class H>
+void launch_dp(const DpArgs& a, int32_t rows, dim3 g, dim3 b, hipStream_t s) {
+  if (rows == 8)
+    hipLaunchKernelGGL((linear_dp_kernel<H, 8>), g, b, 0, s, a);
+  else if (rows == 64)
+    hipLaunchKernelGGL((linear_dp_kernel<H, 64>), g, b, 0, s, a);
+  else
+    hipLaunchKernelGGL((linear_dp_kernel<H, 512>), g, b, 0, s, a);
+}
 
 }  // namespace
 }  // namespace fp8z1
@@ -104,7 +118,7 @@ extern "C" int fp8z1_linear_bwd_workspace_bytes(const fp8z1_product* f, size_t* 
   const int rc = check_product(f, &some_offsets, what);
   if (rc) return rc;
   // the bias's sums are joined before the tiles are split: both use the same memory
-  const size_t sums = sizeof(float) * static_cast<size_t>(sum_groups(f->T, f->E)) * static_cast<size_t>(f->N);
+  const size_t sums = sizeof(float) * static_cast<size_t>(sum_groups(f->T, f->E, f->N)) * static_cast<size_t>(f->N);
   const size_t parts = f->N > 2 * kB ? part_bytes(4) : 0;
   *bytes = !f->T ? 0 : ((sums > parts ? sums : parts) + 15) / 16 * 16;
   return FP8Z1_OK;
@@ -137,7 +151,7 @@ extern "C" int fp8z1_linear_bwd(const fp8z1_product* f, const void* dy, const vo
   a.E = static_cast<int32_t>(f->E);
   a.N = static_cast<int32_t>(f->N);
   a.act = f->act;
-  const int64_t groups = sum_groups(f->T, f->E);
+  const int64_t groups = sum_groups(f->T, f->E, f->N);
   if (dbias && f->T) {
     if (!d_workspace || workspace_bytes < sizeof(float) * static_cast<size_t>(groups) * static_cast<size_t>(f->N))
       return refuse(FP8Z1_EINVAL, what, "workspace too small");
@@ -152,15 +166,15 @@ extern "C" int fp8z1_linear_bwd(const fp8z1_product* f, const void* dy, const vo
                  static_cast<unsigned>((groups + turns - 1) / turns), static_cast<unsigned>(turns));
     const dim3 b(static_cast<unsigned>(threads));
     if (f->dtype == FP8Z1_BF16)
-      hipLaunchKernelGGL((linear_dp_kernel<Bf16>), g, b, 0, s, a);
+      launch_dp<Bf16>(a, sum_rows(f->T, f->N), g, b, s);
     else
-      hipLaunchKernelGGL((linear_dp_kernel<F16>), g, b, 0, s, a);
+      launch_dp<F16>(a, sum_rows(f->T, f->N), g, b, s);
     rc = launched(what);
     if (rc) return rc;
   }
   if (dbias) {
     hipLaunchKernelGGL(linear_dbias_kernel, dim3(static_cast<unsigned>(strips)), dim3(64 * kBiasWaves), 0, s, a.sums, offsets, a.T,
-                       a.E, a.N, dbias);
+                       a.E, a.N, sum_rows(f->T, f->N), dbias);
     rc = launched(what);
     if (rc) return rc;
   }

@@ -20,6 +20,41 @@ def test_without_the_bias_its_sums_take_no_room(T, E, N, K):
     assert block()._linear_bwd_workspace(0, E, N, K, False) == 0
 
 
+@pytest.mark.parametrize("T,E,N,rows", [(100, 2, 64, 8), (37, 1, 40, 8), (4096, 1, 4096, 8), (48828, 3, 2048, 8), (48829, 3, 2048, 64),
+                                        (65536, 8, 7168, 64), (1 << 20, 1, 2047, 64), (1 << 20, 1, 2048, 512),
+                                        (1 << 24, 1, 7168, 512), (1 << 30, 5, 1, 64)])
+def test_the_biass_sums(T, E, N, rows):
+    """A float32 sum of each column for every group of rows; an expert's rows may begin and end inside a group.  They take no more than
+    134 MB, or 1/256 of dy, and a row for each expert."""
+    n, sums = block()._linear_bwd_workspace(T, E, N, 16, True), 4 * (E + T // rows) * N
+    assert n == -(-max(sums, block()._linear_bwd_workspace(T, E, N, 16, False)) // 16) * 16
+    assert sums <= max(2 ** 27, 2 * T * N // 256) + 4 * E * N
+
+
+# groups of 8, 64 and 512 rows; experts that end inside a group, with one row, without one, and all rows with one
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,N,cuts", [(700, 130, (3, 3, 11, 500)), (60000, 2048, (1, 65, 65, 30000)), (400001, 1001, (64, 128, 200, 399999)),
+                                      (1100000, 2047, (513, 514, 1024, 700001))])
+def test_bias_gradient_of_many_rows(T, N, cuts):
+    """dy of small whole numbers, so that every sum is exact in float32."""
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import blockwise_fp8_zero_fold_amd as fz
+    g = torch.Generator(device="cuda").manual_seed(T)
+    dy = torch.randint(-3, 4, (T, N), generator=g, device="cuda", dtype=torch.int8).bfloat16()
+    for off in ((0, *cuts, T), (0, 0, 0, 0, 0, T), (0, T, T, T, T, T)):
+        E, f = 5, fz.Product(T, 5, N, 16, fz.BF16, fz.BF16, fz.ACT_NONE, 0)
+        n = fz.fp8z1_linear_bwd_workspace_bytes(f)
+        db = torch.full((E, N), 7.0, device="cuda")
+        fz.fp8z1_linear_bwd(f, dy, None, None, None, torch.tensor(off, dtype=torch.int32, device="cuda"), None, db, None,
+                            torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda"), n)
+        for e in range(E):
+            want = torch.zeros(N, dtype=torch.float64, device="cuda")
+            for lo in range(off[e], off[e + 1], 1 << 16):
+                want += dy[lo:min(lo + (1 << 16), off[e + 1])].float().sum(0)
+            assert torch.equal(db[e].double(), want), (off, e)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("act", [None, "gelu"])
 def test_memory_of_a_call(act):
