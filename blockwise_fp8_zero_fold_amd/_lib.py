@@ -713,7 +713,15 @@ def fp8z1_route_bwd(f: Router, logits, experts, dweights, dlogits, stream=None) 
            "fp8z1_route_bwd")
 
 
+def _need_counts(what: str, **counts: int) -> None:
+    """(ctypes would cut off what 32 bits do not hold.)"""
+    for name, v in counts.items():
+        if not -2 ** 31 <= v < 2 ** 31:
+            raise Fp8z1Error(f"{what}: {name} = {v}")
+
+
 def fp8z1_sort_tokens_workspace_bytes(T: int, k: int, E: int) -> int:
+    _need_counts("fp8z1_sort_tokens_workspace_bytes", T=T, k=k, E=E)
     n = C.c_size_t()
     _check(lib.fp8z1_sort_tokens_workspace_bytes(T, k, E, C.byref(n)), "fp8z1_sort_tokens_workspace_bytes")
     return n.value
@@ -722,6 +730,7 @@ def fp8z1_sort_tokens_workspace_bytes(T: int, k: int, E: int) -> int:
 def fp8z1_sort_tokens(T: int, k: int, E: int, experts, offsets, row_of, workspace=None, workspace_bytes: int = 0,
                       stream=None) -> None:
     """offsets [E+1] and row_of [T,k] of experts [T,k]."""
+    _need_counts("sort_tokens", T=T, k=k, E=E)
     workspace_bytes = _workspace(workspace, workspace_bytes, "sort_tokens")
     for x in (experts, row_of):
         if x is not None:

@@ -32,11 +32,18 @@ _SCORE = {"softmax": L.SCORE_SOFTMAX, "sigmoid": L.SCORE_SIGMOID}
 _sort_workspace = functools.lru_cache(maxsize=256)(L.fp8z1_sort_tokens_workspace_bytes)
 
 
+def _choices(k: int, what: str) -> None:
+    """(The calls take k in 32 bits, and would see a larger number without its upper ones.)"""
+    if not 1 <= k <= L.ROUTE_MAX_CHOICES:
+        _fail(f"{what}: {k} choices, expected 1 to {L.ROUTE_MAX_CHOICES}")
+
+
 def _router(logits: torch.Tensor, k: int, score: str, normalize: bool, scale: float, what: str):
     if logits.dim() != 2 or logits.dtype not in _CODE:
         _fail(f"{what}: logits must be [T, E] of torch.bfloat16, torch.float16 or torch.float32")
     if score not in _SCORE:
         _fail(f"{what}: score {score!r}, expected one of {', '.join(_SCORE)}")
+    _choices(k, what)
     T, E = logits.shape
     dev = _device(logits, what)
     return dev, T, E, _check(logits, dev, logits.dtype, (T, E), what), L.Router(T, E, k, _CODE[logits.dtype],
@@ -51,7 +58,6 @@ def route(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = None, sco
     what = "route"
     dev, T, E, pl, f = _router(logits, k, score, normalize, scale, what)
     pb = None if bias is None else _check(bias, dev, torch.float32, (E,), f"{what} bias")
-    k = max(k, 0)  # (refused by the call)
     experts, weights = logits.new_empty((T, k), dtype=torch.int32), logits.new_empty((T, k), dtype=torch.float32)
     L._check(L.lib.fp8z1_route(f, pl, pb, experts.data_ptr(), weights.data_ptr(), L._current_stream(dev)), what)
     return experts, weights
@@ -79,6 +85,9 @@ def sort_tokens(experts: torch.Tensor, n_experts: int) -> Tuple[torch.Tensor, to
     if experts.dim() != 2:
         _fail(f"{what}: experts must be [T, k]")
     T, k = experts.shape
+    _choices(k, what)
+    if not 1 <= n_experts <= L.ROUTE_MAX_EXPERTS:
+        _fail(f"{what}: {n_experts} experts, expected 1 to {L.ROUTE_MAX_EXPERTS}")
     dev = _device(experts, what)
     pe = _check(experts, dev, torch.int32, (T, k), what)
     n = _sort_workspace(T, k, n_experts)
@@ -92,6 +101,7 @@ def _plan(row_of: torch.Tensor, T: int, dev: int, what: str) -> Tuple[int, int]:
     if row_of.dim() != 2:
         _fail(f"{what}: row_of must be [T, k]")
     k = row_of.shape[1]
+    _choices(k, what)
     return k, _check(row_of, dev, torch.int32, (T, k), f"{what} row_of")
 
 
