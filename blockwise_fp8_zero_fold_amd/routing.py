@@ -97,12 +97,12 @@ def sort_tokens(experts: torch.Tensor, n_experts: int) -> Tuple[torch.Tensor, to
     return offsets, row_of
 
 
-def _plan(row_of: torch.Tensor, T: int, dev: int, what: str) -> Tuple[int, int]:
+def _plan(row_of: torch.Tensor, dev: int, what: str) -> Tuple[int, int, int]:
     if row_of.dim() != 2:
         _fail(f"{what}: row_of must be [T, k]")
-    k = row_of.shape[1]
+    T, k = row_of.shape
     _choices(k, what)
-    return k, _check(row_of, dev, torch.int32, (T, k), f"{what} row_of")
+    return T, k, _check(row_of, dev, torch.int32, (T, k), f"{what} row_of")
 
 
 def dispatch(x: Union[torch.Tensor, Rows8], row_of: torch.Tensor, out: Union[torch.Tensor, Rows8, None] = None):
@@ -117,7 +117,9 @@ def dispatch(x: Union[torch.Tensor, Rows8], row_of: torch.Tensor, out: Union[tor
     dt = torch.uint8 if eight else codes.dtype
     px = _check(codes, dev, dt, (T, D), what)
     ps = _check(x[1], dev, torch.float32, (T, -(-D // 128)), f"{what} scales") if eight else None
-    k, pr = _plan(row_of, T, dev, what)
+    tokens, k, pr = _plan(row_of, dev, what)
+    if tokens != T:
+        _fail(f"{what}: row_of of {tokens} tokens for {T}")
     if out is None:
         out = _empty8(codes, T * k, D) if eight else codes.new_empty((T * k, D))
     rows = out[0] if eight else out
@@ -143,8 +145,7 @@ def combine(rows: torch.Tensor, row_of: torch.Tensor, weights: Optional[torch.Te
     """y [T,D] = base + sum over j of weights[t,j] rows[row_of[t,j]]; without weights the gradient of dispatch."""
     what = "combine"
     dev, R, D, px = _rows(rows, what)
-    T = row_of.shape[0]
-    k, pr = _plan(row_of, T, dev, what)
+    T, k, pr = _plan(row_of, dev, what)
     pw = None if weights is None else _check(weights, dev, torch.float32, (T, k), f"{what} weights")
     pb = None if base is None else _check(base, dev, rows.dtype, (T, D), f"{what} base")
     y = rows.new_empty((T, D))
@@ -159,8 +160,7 @@ def combine_backward(dy: torch.Tensor, rows: torch.Tensor, row_of: torch.Tensor,
     (it may be ``rows`` itself); rows that no choice has are not written."""
     what = "combine_backward"
     dev, R, D, px = _rows(rows, what)
-    T = row_of.shape[0]
-    k, pr = _plan(row_of, T, dev, what)
+    T, k, pr = _plan(row_of, dev, what)
     py = _check(dy, dev, rows.dtype, (T, D), f"{what} dy")
     pw = _check(weights, dev, torch.float32, (T, k), f"{what} weights")
     drows = torch.empty_like(rows) if out is None else out

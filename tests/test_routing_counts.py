@@ -32,3 +32,16 @@ def test_the_tensor_layer():
                  lambda: r.combine_backward(l, l, wide, wide.float()), lambda: r.route_backward(wide.float(), l, wide)):
         with pytest.raises(fz.Fp8z1Error):
             call()
+
+
+@pytest.mark.gpu
+def test_plans_of_another_shape():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from blockwise_fp8_zero_fold_amd import routing as r
+    x, w = torch.zeros(4, 8, device="cuda"), torch.zeros(4, 2, device="cuda")
+    for shape in ((), (4,), (3, 2), (4, 2, 1), (4, 0)):
+        plan = torch.zeros(shape, dtype=torch.int32, device="cuda")
+        for call in (lambda: r.dispatch(x, plan), lambda: r.combine(x, plan, w), lambda: r.combine_backward(x, x, plan, w)):
+            with pytest.raises(fz.Fp8z1Error):
+                call()
