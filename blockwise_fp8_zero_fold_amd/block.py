@@ -336,10 +336,10 @@ def ffn_up8(x: Rows8, w_gate: Weight, w_up: Weight, offsets: Optional[torch.Tens
 
 
 def ffn_forward8(x: Rows8, w_gate: Weight, w_up: Weight, w_down: Weight, offsets: Optional[torch.Tensor] = None,
-                 act: str = "silu", save: bool = False, dtype: torch.dtype = torch.bfloat16):
-    """(y [T,D], (h, u)): ffn_forward with x and a in 8 bits; y, h and u in ``dtype``.  The backward pass is
-    ffn_backward_data of h and u, and ffn_backward_weights of x in 16 bits and the a that it gives."""
-    a, kept = ffn_up8(x, w_gate, w_up, offsets, act, save, dtype)
+                 act: str = "silu", save: bool = False, dtype: torch.dtype = torch.bfloat16, scale_rule: str = "amax"):
+    """(y [T,D], (h, u)): ffn_forward with x and a in 8 bits, a's scales by ``scale_rule``; y, h and u in ``dtype``.  The
+    backward pass is ffn_backward_data of h and u, and ffn_backward_weights of x in 16 bits and the a that it gives."""
+    a, kept = ffn_up8(x, w_gate, w_up, offsets, act, save, dtype, scale_rule)
     return linear(a, w_down, offsets, dtype=dtype)[0], kept
 
 
