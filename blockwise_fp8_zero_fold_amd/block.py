@@ -288,9 +288,10 @@ def linear(x: Union[torch.Tensor, Rows8], w: Weight, offsets: Optional[torch.Ten
 
 def linear_backward(dy: torch.Tensor, w: Weight, p: Optional[torch.Tensor] = None,
                     offsets: Optional[torch.Tensor] = None, act: Optional[str] = None,
-                    bias: bool = False) -> Dict[str, Optional[torch.Tensor]]:
+                    bias: bool = False, dx: bool = True, dp: bool = True) -> Dict[str, Optional[torch.Tensor]]:
     """{"dx" [T,K], "dp" [T,N], "dbias" [E,N] (with ``bias``)} from dy and, with an activation, the kept p.  Without one
-    dp is dy itself.  The weight gradient is ffn_weight_gradient(dp, x in 16 bits); res has the gradient dy."""
+    dp is dy itself.  The weight gradient is ffn_weight_gradient(dp, x in 16 bits); res has the gradient dy.
+    ``dx`` and ``dp`` False: not wanted, and None (dx needs dp where there is an activation)."""
     what = "linear_backward"
     if dy.dim() != 2 or w[0].dim() != 3:
         _fail(f"{what}: dy must be [T, N] and codes [E, N, K]")
@@ -302,14 +303,15 @@ def linear_backward(dy: torch.Tensor, w: Weight, p: Optional[torch.Tensor] = Non
     pp = None if p is None else _check(p, dev, dtype, (T, N), f"{what} p")
     pw = _weight(w, dev, E, N, K, f"{what} weight")
     off = _offsets(offsets, dev, E, what)
-    dp, dx = dy if p is None else torch.empty_like(dy), dy.new_empty((T, K))
+    dps = None if not dp else dy if p is None else torch.empty_like(dy)
+    dxs = dy.new_empty((T, K)) if dx else None
     dbias = dy.new_empty((E, N), dtype=torch.float32) if bias else None
     f = L.Product(T, E, N, K, _CODE[dtype], _CODE[dtype], kind, 0)
-    n = _linear_bwd_workspace(T, E, N, K, bias)
+    n = _linear_bwd_workspace(T, E, N, K, bias) if bias or dx else 0
     ws = _scratch(dy, n)
-    L._check(L.lib.fp8z1_linear_bwd(f, py, pp, *pw, off, None if p is None else dp.data_ptr(), L._ptr(dbias), dx.data_ptr(),
+    L._check(L.lib.fp8z1_linear_bwd(f, py, pp, *pw, off, None if p is None else L._ptr(dps), L._ptr(dbias), L._ptr(dxs),
                                     L._ptr(ws), n, L._current_stream(dev)), what)
-    return {"dx": dx, "dp": dp, "dbias": dbias}
+    return {"dx": dxs, "dp": dps, "dbias": dbias}
 
 
 def ffn_up8(x: Rows8, w_gate: Weight, w_up: Weight, offsets: Optional[torch.Tensor] = None, act: str = "silu",
