@@ -17,11 +17,12 @@
 // instruction's rows, so that a lane's 16 results are of one row of x: one scale for all of them, and one multiply-add
 // each per 128 products.
 //
-// Measured: y 8192 x 7168 of width 2048 on 8 experts 171 us (1.40 PFLOP/s; the matrix cores busy 38 % of the cycles at
-// 2.05 GHz), gate and up 2 x 2048 of width 7168, kept for the backward pass, 456 to 486 us (0.99 to 1.06 PFLOP/s; busy 57 %
-// at 1.7 to 1.9 GHz).  A block of 128 k costs a lone tile 3270 cycles (gate and up 6100) where the matrix instructions
-// take 2048 (4096): the rest is the waits at its barriers and issue slots that additions, conversions and LDS
-// reads take.  A tile's start and end cost 11.7 us (13.2) with one block.
+// Measured: y 8192 x 7168 of width 2048 on 8 experts 171 to 181 us (1.33 to 1.41 PFLOP/s; the matrix cores busy 38 % of the cycles
+// at 2.05 GHz), gate and up 2 x 2048 of width 7168, kept for the backward pass, 430 to 486 us by box and clock (0.99 to 1.12
+// PFLOP/s; busy 57 % at 1.7 to 1.9 GHz).  A block of 128 k costs a lone tile 3270 cycles (gate and up 6100) where the matrix
+// instructions take 2048 (4096): the rest is the waits at its barriers and issue slots that additions, conversions and LDS
+// reads take.  A tile's start and end cost 11.7 us (13.2) with one block.  Few rows of gate and up, 2 x 2048 of width 7168, in a
+// graph: one token 10.8 us (29 MB of codes, 2.7 TB/s; the second launch 3), 64 tokens on 8 experts 44 us (235 MB, 5.3 TB/s).
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -25,8 +25,9 @@ __device__ __forceinline__ float row8_scale(float amax, bool pow2) {
   return fmaxf(s, 0x1p-126f);
 }
 
-// Division by a group's scale.  The steps are those of a correctly rounded division (a reciprocal refined once, a
-// quotient corrected twice by its remainder), with the reciprocal taken once for the group.  For scales from 2^-60 to
+// Division by a group's scale: Markstein's correctly rounded division (Computation of elementary functions on the IBM RISC
+// System/6000 processor, IBM Journal of Research and Development 34, 1990), a reciprocal refined once and a
+// quotient corrected twice by its remainder, with the reciprocal taken once for the group.  For scales from 2^-60 to
 // 2^60 nothing in them leaves the normal numbers unless the quotient is below 2^-20, which is code 0 either way; other
 // scales are brought there by a power of two, and so is what is divided (`times`; what that takes below the normal
 // numbers has a quotient below 2^-120).  Of an infinite scale, times is 0 and the scale 1: 0 of what is finite.

@@ -468,7 +468,9 @@ typedef struct {
 /* y [T,N] = res + act(x W^T + bias).  x_scales for x in 8 bits, else NULL.  bias float32 [E,N] or NULL; res [T,N] or NULL
  * (y may be res itself); p [T,N], unless NULL, keeps x W^T + bias for the backward pass.  With
  * fp8z1_linear_workspace_bytes() bytes of device workspace (16-byte aligned) tiles that do not fill
- * the card are split along k; with less (or NULL) they are not. */
+ * the card are split along k; with less (or NULL) they are not.  In many 8-bit rows of a width that is no multiple of 4 the
+ * workspace packs them, too.  (Codes whose address is no multiple of 4 at a width that is one have no room there, and
+ * are read shifted, up to 1.6 times slower.) */
 int fp8z1_linear_workspace_bytes(const fp8z1_product* f, size_t* bytes);
 int fp8z1_linear(const fp8z1_product* f, const void* x, const float* x_scales, const uint8_t* codes, const float* scales,
                  const int32_t* offsets, const float* bias, const void* res, void* y, void* p, void* d_workspace,
@@ -516,7 +518,8 @@ typedef struct {
 
 /* From logits [T,E]: experts [T,k] int32, the k experts of the largest p_e + bias_e (bias float32 [E]; NULL: of
  * the largest logits), largest first, the lowest index among equals, and their weights [T,k] float32, scale p_e or scale p_e / (sum of
- * the chosen p).  The bias decides the choice only.  Ranks are compared in 64 bits.
+ * the chosen p).  The bias decides the choice only (NaN and -inf in it rank last).  Ranks are compared in 64 bits, weights
+ * are computed in float32.
  * An expert with a logit of -inf or NaN is not chosen; where fewer than k are left, the other choices are expert -1
  * with weight 0.  A row of softmax logits that holds a NaN or +inf has NaN weights.  No logit's size makes
  * normalized weights overflow or vanish. */
@@ -524,7 +527,8 @@ int fp8z1_route(const fp8z1_router* f, const void* logits, const float* bias, in
                 void* stream);
 
 /* The logits' gradient [T,E] (dtype) from that of the weights, dweights [T,k] float32; experts as fp8z1_route
- * wrote them (choices outside 0..E-1 have no gradient). */
+ * wrote them (choices outside 0..E-1 have no gradient).  Normalized weights depend on the chosen logits alone: NaN in others, which
+ * the forward pass reports, are not looked at. */
 int fp8z1_route_bwd(const fp8z1_router* f, const void* logits, const int32_t* experts, const float* dweights,
                     void* dlogits, void* stream);
 
