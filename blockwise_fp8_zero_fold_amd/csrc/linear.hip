@@ -1,9 +1,10 @@
-// A product with one weight, its epilogue y = res + act(x W^T + bias) where the sums are; x in 16 bits on the tile
-// and row kernels of the feed-forward block, x in 8 bits on those of linear8.h.  One token of width 7168 by 2048 columns,
-// bias and residual, 8-bit rows: 7.8 to 8.2 us in a graph (15 MB of codes, 1.9 TB/s), 10.2 eager.  Latency bounds it: the
-// launch, each wave's 3 or 4 blocks of codes, the sums of 16 waves, and then bias and residual, which are loaded only behind the
-// sums though they do not depend on them (0.4 us).  Rows in 16 bits: one token 8.4 us in a graph; 8192 tokens, 8
-// experts, 7168 of width 2048 266 us (0.91 PFLOP/s), 4096^3 129 to 132 (1.04 to 1.07), on the tiles of ffn_tile.h.
+// A product with one weight, its epilogue y = res + act(x W^T + bias) where the sums are; x in 16 bits on the tile and
+// row kernels of the feed-forward block, x in 8 bits on those of linear8.h.  One token of width 7168 by 2048 columns,
+// bias and residual, 8-bit rows: 7.8 to 8.2 us in a graph (15 MB of codes, 1.9 TB/s), 10.2 eager.  Latency bounds it:
+// the launch, each wave's 3 or 4 blocks of codes, the sums of 16 waves, and then bias and residual, which are loaded
+// only behind the sums though they do not depend on them (0.4 us).  Rows in 16 bits: one token 8.4 us in a graph; 8192
+// tokens, 8 experts, 7168 of width 2048 266 us (0.91 PFLOP/s), 4096^3 129 to 132 (1.04 to 1.07), on the tiles of
+// ffn_tile.h.
 #include "ffn_tile.h"
 
 using namespace fp8z1;

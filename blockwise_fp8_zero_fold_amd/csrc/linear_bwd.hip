@@ -1,11 +1,11 @@
 // Gradients of y = res + act(x W^T + bias): dp = dy act'(p) with its sums over an expert's rows (the
 // bias's gradient) in one pass over dy and p, and dx = dp W on the tile kernel of the feed-forward block.
 //
-// The pass reads dy and p and writes dp; its arithmetic (the activation's slope, about 30 instructions an element) takes
-// as long as half of the transfers, and runs under other waves'.  A workgroup takes 8 rows (of many elements more, see sum_rows)
-// of one expert by up to 2048 columns, 8 of them per thread, and writes their float32 column sums to the workspace; a second
-// kernel adds an expert's groups in order.  4096 x 4096, GELU: 24 us (4.2 TB/s) and 5.7 for the sums; groups of 16 rows 27
-// and 4.9, and with the next rows' loads ahead of the arithmetic 29.
+// The pass reads dy and p and writes dp; its arithmetic (the activation's slope, about 30 instructions an element)
+// takes as long as half of the transfers, and runs under other waves'.  A workgroup takes 8 rows (of many elements
+// more, see sum_rows) of one expert by up to 2048 columns, 8 of them per thread, and writes their float32 column sums
+// to the workspace; a second kernel adds an expert's groups in order.  4096 x 4096, GELU: 24 us (4.2 TB/s) and 5.7 for
+// the sums; groups of 16 rows 27 and 4.9, and with the next rows' loads ahead of the arithmetic 29.
 #include "ffn_tile.h"
 #include "rows.h"
 
@@ -13,9 +13,9 @@ namespace fp8z1 {
 namespace {
 
 // Rows of a group: 8 while there are fewer than 10^8 elements, 64 up to 2^31, then 512, so that the groups' sums take
-// 50 MB, 134 MB or 1/256 of dy (and a row for each expert) at most.  8 and 64 rows, GELU: 8192 x 7168 90 and 105 us, 32,768 x 2048 103
-// and 115, 16,384 x 7168 177 and 172, 65,536 x 2048 212 and 182, 262,144 x 1024 510 and 377, 65,536 x 7168 658 and 608;
-// 64 and 512: 524,288 x 2048 1323 and 1312, 262,144 x 7168 2321 and 2422, 65,536 x 2048 182 and 527.
+// 50 MB, 134 MB or 1/256 of dy (and a row for each expert) at most.  8 and 64 rows, GELU: 8192 x 7168 90 and 105 us,
+// 32,768 x 2048 103 and 115, 16,384 x 7168 177 and 172, 65,536 x 2048 212 and 182, 262,144 x 1024 510 and 377, 65,536 x
+// 7168 658 and 608; 64 and 512: 524,288 x 2048 1323 and 1312, 262,144 x 7168 2321 and 2422, 65,536 x 2048 182 and 527.
 int32_t sum_rows(int64_t T, int64_t N) { return T * N < 100000000 ? 8 : T * N < (1ll << 31) ? 64 : 512; }
 
 struct DpArgs {

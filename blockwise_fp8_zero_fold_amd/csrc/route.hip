@@ -13,11 +13,11 @@
 // 64 bits, since two experts' sums may differ by less than a float32 rounding; logits are ranked as they are.
 //
 // Many tokens: bound by the issue of vector instructions, not by the reads.  8192 tokens of 256 experts in float32, 8
-// choices, take 11 us forward and 6 to 7 backward, where 8.4 MB and twice that cost 2 and 3: 562 vector instructions a wave
-// (255 backward), 8 waves on each SIMD, 4 cycles each are 18,000 (8,200) of the 23,000 (12,600) cycles that the
-// kernel is busy.  With a bias 906, some of them on 64 bits: 15 (logistic) to 16 us.  Few tokens: bound by the latency of the k
-// rounds, which come one after another.  4 tokens of 64 experts with a bias take 4.3 us in a graph, an empty launch 2 to 3;
-// eager calls take 9, the host's time.
+// choices, take 11 us forward and 6 to 7 backward, where 8.4 MB and twice that cost 2 and 3: 562 vector instructions a
+// wave (255 backward), 8 waves on each SIMD, 4 cycles each are 18,000 (8,200) of the 23,000 (12,600) cycles that the
+// kernel is busy.  With a bias 906, some of them on 64 bits: 15 (logistic) to 16 us.  Few tokens: bound by the latency
+// of the k rounds, which come one after another.  4 tokens of 64 experts with a bias take 4.3 us in a graph, an empty
+// launch 2 to 3; eager calls take 9, the host's time.
 #include <hip/hip_runtime.h>
 
 #include "device_util.h"
